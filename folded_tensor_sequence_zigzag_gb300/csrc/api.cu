@@ -11,13 +11,17 @@
 //   MLP ring              -> the W_2 GEMM's K loop runs in ring order per rank;
 //   weight-grad reduction -> the wgrad GEMMs' K loop (tokens) runs over every
 //                            rank's rows into one fp32 accumulator.
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <map>
 #include <mutex>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "common.cuh"
@@ -765,7 +769,9 @@ const char* tsp_strerror(tsp_status s) {
     case TSP_ERR_UNSUPPORTED: return "shape not supported by the selected kernels";
     case TSP_ERR_CUDA: return "CUDA runtime error";
     case TSP_ERR_TIMEOUT: return "device pipeline wait exceeded its time limit";
-    case TSP_ERR_RANGE: return "a value held in fp16 inside the bf16 path was out of fp16 range";
+    case TSP_ERR_RANGE:
+      return "a value held in fp16 inside the bf16 path was out of fp16 range, or a token id was "
+             "past the embedding table";
     case TSP_ERR_BOUNDS: return "a computed index failed its bounds check (checked build)";
   }
   return "unknown status";
@@ -1002,6 +1008,141 @@ int32_t tsp_profile_report(char* buf, int64_t bytes) {
 int64_t tsp_launch_count(void) { return g_launches.load(); }
 
 void tsp_debug_skip_stage(int32_t n) { g_debug_skip.store(n > 0 ? n : 0); }
+
+// ---- around the stack: embedding, sub-layer norms and residual, optimizer ----
+
+static tsp_status check_embed(int64_t S, int32_t D, int64_t V, int32_t d) {
+  if (S <= 0 || D < 1 || D > 64 || V <= 0 || d <= 0) return TSP_ERR_INVALID_ARG;
+  if (D > 1 && S % (2 * (int64_t)D) != 0) return TSP_ERR_INVALID_ARG;
+  if (S > (int64_t)1 << 30 || V > INT32_MAX - 1) return TSP_ERR_UNSUPPORTED;
+  return TSP_OK;
+}
+static bool ids_ok(const void* ids, int32_t id_bytes) {
+  return ids && (id_bytes == 4 || id_bytes == 8) && (uintptr_t)ids % (uintptr_t)id_bytes == 0;
+}
+
+tsp_status tsp_embed_fwd(const void* ids, int32_t id_bytes, const void* table, void* x_z,
+                         int64_t S, int32_t D, int64_t V, int32_t d, float scale, int32_t dtype,
+                         void* stream) {
+  const tsp_status r = check_embed(S, D, V, d);
+  if (r != TSP_OK) return r;
+  if (!ids_ok(ids, id_bytes) || !al16(table) || !al16(x_z) || !std::isfinite(scale) ||
+      (dtype != TSP_F32 && dtype != TSP_BF16))
+    return TSP_ERR_INVALID_ARG;
+  return launch_embed_fwd(ids, id_bytes, table, x_z, S, D, V, d, scale, dtype, S_(stream));
+}
+
+size_t tsp_embed_bwd_workspace_bytes(int64_t S, int64_t V, int32_t d) {
+  return check_embed(S, 1, V, d) == TSP_OK ? embed_bwd_ws_bytes(S, V, d) : 0;
+}
+
+tsp_status tsp_embed_bwd(const void* ids, int32_t id_bytes, const void* dx_z, int32_t dx_dtype,
+                         float* dtable, int64_t S, int32_t D, int64_t V, int32_t d, float scale,
+                         int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+  const tsp_status r = check_embed(S, D, V, d);
+  if (r != TSP_OK) return r;
+  if (!ids_ok(ids, id_bytes) || !al16(dx_z) || !al16(dtable) || !al16(ws) ||
+      !std::isfinite(scale) || (dx_dtype != TSP_F32 && dx_dtype != TSP_BF16) ||
+      ws_bytes < embed_bwd_ws_bytes(S, V, d))
+    return TSP_ERR_INVALID_ARG;
+  return launch_embed_bwd(ids, id_bytes, dx_z, dx_dtype, dtable, S, D, V, d, scale, accumulate != 0,
+                          ws, S_(stream));
+}
+
+// true if p is a 16-byte aligned pointer when `used`, and NULL when not
+static bool used_or_null(const void* p, bool used) { return used ? al16(p) : p == nullptr; }
+
+static tsp_status check_norm_residual(int64_t rows, int32_t n, float scale, int32_t dtype,
+                                      int32_t stream_dtype) {
+  if (rows <= 0 || n <= 0 || !std::isfinite(scale)) return TSP_ERR_INVALID_ARG;
+  if (dtype != TSP_F32 && dtype != TSP_BF16) return TSP_ERR_INVALID_ARG;
+  if (stream_dtype != TSP_F32 && !(stream_dtype == TSP_BF16 && dtype == TSP_BF16))
+    return TSP_ERR_INVALID_ARG;
+  return n > 1 << 24 ? TSP_ERR_UNSUPPORTED : TSP_OK;
+}
+
+tsp_status tsp_norm_residual_fwd(const void* f, const void* x, const void* gate,
+                                 const void* g_post, const void* g_pre, void* h, void* b,
+                                 float* rstd_f, float* rstd_h, int64_t rows, int32_t n,
+                                 float scale, float eps, int32_t dtype, int32_t stream_dtype,
+                                 void* stream) {
+  const tsp_status r = check_norm_residual(rows, n, scale, dtype, stream_dtype);
+  if (r != TSP_OK) return r;
+  if (!al16(f) || !al16(x) || !al16(h) || (gate && !al16(gate)) || (g_post && !al16(g_post)) ||
+      (g_pre && !al16(g_pre)) || !used_or_null(b, g_pre != nullptr) || !(eps >= 0.f) ||
+      (rstd_f && !(g_post && al16(rstd_f))) || (rstd_h && !(g_pre && al16(rstd_h))))
+    return TSP_ERR_INVALID_ARG;
+  return launch_norm_residual_fwd(f, x, gate, g_post, g_pre, h, b, rstd_f, rstd_h, rows, n, scale,
+                                  eps, dtype, stream_dtype, S_(stream));
+}
+
+size_t tsp_norm_residual_bwd_workspace_bytes(int64_t rows, int32_t n) {
+  return check_norm_residual(rows, n, 1.f, TSP_F32, TSP_F32) == TSP_OK
+             ? norm_residual_bwd_ws_bytes(rows, n)
+             : 0;
+}
+
+tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f, const void* gate,
+                                 const void* h, const void* g_post, const void* g_pre,
+                                 const float* rstd_f, const float* rstd_h, float* dx, void* df,
+                                 void* dgate, float* dg_post, float* dg_pre, int64_t rows,
+                                 int32_t n, float scale, int32_t dtype, int32_t stream_dtype,
+                                 void* ws, size_t ws_bytes, void* stream) {
+  const tsp_status r = check_norm_residual(rows, n, scale, dtype, stream_dtype);
+  if (r != TSP_OK) return r;
+  const bool post = g_post != nullptr, pre = g_pre != nullptr;
+  if (!al16(f) || !al16(dx) || !al16(df) || (gate && !al16(gate)) || (post && !al16(g_post)) ||
+      (pre && !al16(g_pre)) || (dh ? !al16(dh) : !pre) || !used_or_null(db, pre) ||
+      !used_or_null(h, pre) || !used_or_null(rstd_h, pre) || !used_or_null(dg_pre, pre) ||
+      !used_or_null(rstd_f, post) || !used_or_null(dg_post, post) ||
+      !used_or_null(dgate, gate != nullptr))
+    return TSP_ERR_INVALID_ARG;
+  if ((post || pre) && (!al16(ws) || ws_bytes < norm_residual_bwd_ws_bytes(rows, n)))
+    return TSP_ERR_INVALID_ARG;
+  return launch_norm_residual_bwd(dh, db, f, gate, h, g_post, g_pre, rstd_f, rstd_h, dx, df, dgate,
+                                  dg_post, dg_pre, rows, n, scale, dtype, stream_dtype, ws,
+                                  S_(stream));
+}
+
+tsp_status tsp_adamw_step(const tsp_adamw_tensor* tensors, int32_t count,
+                          const tsp_adamw_hyper* hyper, int32_t state_bits, int32_t dtype,
+                          void* stream) {
+  if (count < 0 || (count > 0 && !tensors) || !hyper || (state_bits != 32 && state_bits != 8) ||
+      (dtype != TSP_F32 && dtype != TSP_BF16))
+    return TSP_ERR_INVALID_ARG;
+  const bool bf = dtype == TSP_BF16, coded = state_bits == 8;
+  const int64_t e = bf ? 2 : 4;
+  if (!std::isfinite(hyper->lr) || !(hyper->beta1 >= 0.0 && hyper->beta1 < 1.0) ||
+      !(hyper->beta2 >= 0.0 && hyper->beta2 < 1.0) || !(hyper->eps >= 0.0) ||
+      !std::isfinite(hyper->eps) || (!hyper->step_dev && hyper->step < 1) ||
+      (uintptr_t)hyper->lr_dev % 4 || (uintptr_t)hyper->step_dev % 8 ||
+      (uintptr_t)hyper->gscale_dev % 4)
+    return TSP_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < count; ++i) {
+    const tsp_adamw_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    if (t.n < 0 || t.n > (int64_t)1 << 40 || !al16(t.w) || !al16(t.g) || !al16(t.m) ||
+        !al16(t.v) || (t.master && !(bf && al16(t.master))) || (t.prep && !(bf && al16(t.prep))) ||
+        (t.m_scale != nullptr) != coded || (t.v_scale != nullptr) != coded ||
+        (uintptr_t)t.m_scale % 4 || (uintptr_t)t.v_scale % 4 || !std::isfinite(t.weight_decay))
+      return TSP_ERR_INVALID_ARG;
+  }
+  // one call updates a weight once: sorted by address, no weight reaches the next
+  try {
+    std::vector<std::pair<uintptr_t, uintptr_t>> span;
+    span.reserve(count);
+    for (int32_t i = 0; i < count; ++i)
+      if (tensors[i].n > 0)
+        span.emplace_back((uintptr_t)tensors[i].w,
+                          (uintptr_t)tensors[i].w + (uintptr_t)(tensors[i].n * e));
+    std::sort(span.begin(), span.end());
+    for (size_t i = 1; i < span.size(); ++i)
+      if (span[i].first < span[i - 1].second) return TSP_ERR_INVALID_ARG;
+  } catch (const std::exception&) {   // no host memory for the list: nothing was launched
+    return TSP_ERR_INVALID_ARG;
+  }
+  return launch_adamw(tensors, count, hyper, state_bits, dtype, S_(stream));
+}
 
 tsp_status tsp_device_status(void* stream, int32_t reset) {
   int* p = status_word();

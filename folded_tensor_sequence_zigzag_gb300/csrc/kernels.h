@@ -138,6 +138,31 @@ struct DecodeAttn {
 int64_t decode_splits(int64_t S, int D, int64_t n_rows);
 tsp_status launch_decode_attn(const DecodeAttn& a, cudaStream_t st);
 
+// embed.cu (arguments as checked by tsp_embed_fwd / tsp_embed_bwd)
+tsp_status launch_embed_fwd(const void* ids, int id_bytes, const void* table, void* x, int64_t S,
+                            int D, int64_t vocab, int d, float scale, int dtype, cudaStream_t st);
+size_t embed_bwd_ws_bytes(int64_t S, int64_t vocab, int d);
+tsp_status launch_embed_bwd(const void* ids, int id_bytes, const void* dx, int dx_dtype,
+                            float* dtable, int64_t S, int D, int64_t vocab, int d, float scale,
+                            bool accumulate, void* ws, cudaStream_t st);
+
+// norm_residual.cu (null pointers as in tsp_norm_residual_fwd / _bwd)
+tsp_status launch_norm_residual_fwd(const void* f, const void* x, const void* gate,
+                                    const void* g_post, const void* g_pre, void* h, void* b,
+                                    float* rstd_f, float* rstd_h, int64_t rows, int n, float scale,
+                                    float eps, int dtype, int stream_dtype, cudaStream_t st);
+size_t norm_residual_bwd_ws_bytes(int64_t rows, int n);
+tsp_status launch_norm_residual_bwd(const float* dh, const float* db, const void* f,
+                                    const void* gate, const void* h, const void* g_post,
+                                    const void* g_pre, const float* rstd_f, const float* rstd_h,
+                                    float* dx, void* df, void* dgate, float* dg_post, float* dg_pre,
+                                    int64_t rows, int n, float scale, int dtype, int stream_dtype,
+                                    void* ws, cudaStream_t st);
+
+// adamw.cu
+tsp_status launch_adamw(const tsp_adamw_tensor* ts, int count, const tsp_adamw_hyper* h,
+                        int state_bits, int dtype, cudaStream_t st);
+
 // api.cu: TSP_OK if the configuration is valid (the entry points' common check)
 tsp_status cfg_status(const tsp_cfg* cfg);
 

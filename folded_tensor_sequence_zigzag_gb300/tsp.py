@@ -36,7 +36,9 @@ EXPORTED = ("tsp_zigzag_permute", "tsp_rmsnorm_fwd", "tsp_workspace_bytes", "tsp
             "tsp_stack_bwd_prepared", "tsp_pack_mlp_shards", "tsp_rank_workspace_bytes",
             "tsp_rank_attn_project", "tsp_rank_attn_heads", "tsp_rank_mlp_step",
             "tsp_rank_mlp_bwd_step", "tsp_rank_mlp_bwd_finish", "tsp_rank_attn_bwd_heads",
-            "tsp_rank_attn_bwd_weights", "tsp_rank_attn_bwd_finish")
+            "tsp_rank_attn_bwd_weights", "tsp_rank_attn_bwd_finish", "tsp_embed_fwd",
+            "tsp_embed_bwd_workspace_bytes", "tsp_embed_bwd", "tsp_norm_residual_fwd",
+            "tsp_norm_residual_bwd_workspace_bytes", "tsp_norm_residual_bwd", "tsp_adamw_step")
 DECODE_MAX_T = 8   # TSP_DECODE_MAX_T
 
 
@@ -61,6 +63,19 @@ class AttnW(ctypes.Structure):
 class MlpW(ctypes.Structure):
     _fields_ = [("w1", ctypes.c_void_p), ("w3", ctypes.c_void_p), ("w2", ctypes.c_void_p),
                 ("g_mlp", ctypes.c_void_p), ("add_residual", ctypes.c_int32)]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("w", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("g", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("prep", ctypes.c_void_p), ("weight_decay", ctypes.c_float)]
+
+
+class AdamwHyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("lr_dev", ctypes.c_void_p),
+                ("step_dev", ctypes.c_void_p), ("gscale_dev", ctypes.c_void_p)]
 
 
 _lib = None
@@ -121,6 +136,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "tsp_block_prefill": (i32, [P(Cfg), vp, P(AttnW), P(MlpW), vp, vp, i64, vp, sz, vp]),
         "tsp_block_decode": (i32, [P(Cfg), vp, i32, i64, P(AttnW), P(MlpW), vp, vp, i64, vp, sz,
                                    vp]),
+        "tsp_embed_fwd": (i32, [vp, i32, vp, vp, i64, i32, i64, i32, f32, i32, vp]),
+        "tsp_embed_bwd_workspace_bytes": (sz, [i64, i64, i32]),
+        "tsp_embed_bwd": (i32, [vp, i32, vp, i32, vp, i64, i32, i64, i32, f32, i32, vp, sz, vp]),
+        "tsp_norm_residual_fwd": (i32, [vp] * 9 + [i64, i32, f32, f32, i32, i32, vp]),
+        "tsp_norm_residual_bwd_workspace_bytes": (sz, [i64, i32]),
+        "tsp_norm_residual_bwd": (i32, [vp] * 14 + [i64, i32, f32, i32, i32, vp, sz, vp]),
+        "tsp_adamw_step": (i32, [P(AdamwTensor), i32, P(AdamwHyper), i32, i32, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -183,6 +205,11 @@ class BlockWeights:
     def from_dict(cls, d: dict, device="cuda"):
         return cls(**{k: d[k].to(device).contiguous() for k in
                       ("wq", "wk", "wv", "wo", "w1", "w3", "w2", "g_attn", "g_mlp")})
+
+    def params(self) -> list:
+        """The nine tensors in the order of GRAD_NAMES (a layer's gradients)."""
+        return [self.wq, self.wk, self.wv, self.wo, self.w1, self.w3, self.w2, self.g_attn,
+                self.g_mlp]
 
     def attn(self) -> AttnW:
         return AttnW(_ptr(self.wq), _ptr(self.wk), _ptr(self.wv), _ptr(self.wo), _ptr(self.g_attn))
@@ -553,6 +580,307 @@ def rank_attn_bwd_finish(cfg: Cfg, r: int, x_r, g_attn, da_r, dh_r, dx_r, dg_att
                                            _ptr(da_r), _ptr(dh_r), _ptr(dx_r), _ptr(dg_attn),
                                            _ptr(ws), ws.numel(), _stream(stream)),
            "tsp_rank_attn_bwd_finish")
+
+
+# ---- around the stack: embedding, sub-layer norms and residual, optimizer ----
+
+class _On:
+    """Makes ``dev`` and ``stream`` (default: the device's current one) current
+    for a call, so that the buffers it allocates belong to the stream they are
+    used on; gives the stream's handle."""
+    __slots__ = ("dev", "stream", "ctx")
+
+    def __init__(self, dev, stream):
+        if dev.type != "cuda":
+            raise ValueError("tensors must live on the GPU")
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+        self.dev, self.stream, self.ctx = dev, stream, None
+
+    def __enter__(self):
+        st = torch.cuda.current_stream(self.dev) if self.stream is None else self.stream
+        if self.stream is not None or self.dev.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.stream(st)
+            self.ctx.__enter__()
+        return st.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _arg(name, t, shape, dtype, dev):
+    """data_ptr of a dense tensor of this shape, type and device (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} of "
+                         f"shape {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the other tensors are on {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+_ENUM = {torch.bfloat16: TSP_BF16, torch.float32: TSP_F32}
+
+
+def _enum(name, dtype):
+    if dtype not in _ENUM:
+        raise ValueError(f"{name} must be bfloat16 or float32, got {dtype}")
+    return _ENUM[dtype]
+
+
+def _ids_arg(ids):
+    if ids.dim() != 1 or ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"ids: expected int32 or int64 of shape [S], got {ids.dtype} of shape "
+                         f"{tuple(ids.shape)}")
+    return 4 if ids.dtype == torch.int32 else 8
+
+
+def embed_fwd(ids, table, D: int = 1, scale: float = 1.0, out=None, stream=None):
+    """x_z [S, d] = scale * table[ids] in the zigzag order of D ranks (D = 1:
+    global order, any S).  ``ids`` [S] int32 or int64 in global order, < 0 for
+    padding (a zero row)."""
+    id_bytes = _ids_arg(ids)
+    if table.dim() != 2:
+        raise ValueError("table must be [V, d]")
+    S, (V, d), dt, dev = ids.shape[0], table.shape, table.dtype, table.device
+    e = _enum("table", dt)
+    pi, pt = _arg("ids", ids, (S,), ids.dtype, dev), _arg("table", table, (V, d), dt, dev)
+    po = _arg("out", out, (S, d), dt, dev)
+    with _On(dev, stream) as st:
+        if out is None:
+            out = empty((S, d), dt, dev)
+            po = out.data_ptr()
+        _check(load().tsp_embed_fwd(pi, id_bytes, pt, po, S, D, V, d, scale, e, st),
+               "tsp_embed_fwd")
+    return out
+
+
+def embed_bwd_workspace_bytes(S: int, V: int, d: int) -> int:
+    return int(load().tsp_embed_bwd_workspace_bytes(int(S), int(V), int(d)))
+
+
+def embed_bwd(ids, dx_z, V: int, D: int = 1, scale: float = 1.0, out=None,
+              accumulate: bool = False, ws=None, stream=None):
+    """The table's gradient [V, d] fp32 from dx_z [S, d] (fp32 or bf16, zigzag
+    order of D ranks).  ``accumulate`` adds it to ``out`` (a table tied to the
+    output projection) instead of overwriting."""
+    id_bytes = _ids_arg(ids)
+    if dx_z.dim() != 2:
+        raise ValueError("dx_z must be [S, d]")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs the gradient to add to in out")
+    S, d, dt, dev = ids.shape[0], dx_z.shape[1], dx_z.dtype, dx_z.device
+    e = _enum("dx_z", dt)
+    pi, px = _arg("ids", ids, (S,), ids.dtype, dev), _arg("dx_z", dx_z, (S, d), dt, dev)
+    po = _arg("out", out, (V, d), torch.float32, dev)
+    with _On(dev, stream) as st:
+        if out is None:
+            out = empty((V, d), torch.float32, dev)
+            po = out.data_ptr()
+        lib = load()
+        if ws is None:
+            ws = _ws(lib.tsp_embed_bwd_workspace_bytes(S, V, d), dev)
+        _check(lib.tsp_embed_bwd(pi, id_bytes, px, e, po, S, D, V, d, scale,
+                                 1 if accumulate else 0, ws.data_ptr(), ws.numel(), st),
+               "tsp_embed_bwd")
+    return out
+
+
+def norm_residual_fwd(f, x, g_post=None, g_pre=None, gate=None, scale: float = 1.0,
+                      eps: float = 1e-6, h=None, b=None, with_rstd=False, stream=None):
+    """(h, b) of h = x + scale * sigmoid(gate) * rms(f; g_post), b = rms(h; g_pre)
+    (None without g_pre), with_rstd: (h, b, rstd_f, rstd_h).  f, gate [rows, n]
+    and the gains in one type, x and h in fp32 or that type; ``h`` may be x."""
+    if f.dim() != 2:
+        raise ValueError("f must be [rows, n]")
+    shape, dt, dev = f.shape, f.dtype, f.device
+    rows, n = shape
+    e, es = _enum("f", dt), _enum("x", x.dtype)
+    pf, px = _arg("f", f, shape, dt, dev), _arg("x", x, shape, x.dtype, dev)
+    pz = _arg("gate", gate, shape, dt, dev)
+    pp, pq = _arg("g_post", g_post, (n,), dt, dev), _arg("g_pre", g_pre, (n,), dt, dev)
+    ph, pb = _arg("h", h, shape, x.dtype, dev), _arg("b", b, shape, dt, dev)
+    rf = rh = None
+    with _On(dev, stream) as st:
+        if h is None:
+            h = empty(shape, x.dtype, dev)
+            ph = h.data_ptr()
+        if b is None and pq is not None:
+            b = empty(shape, dt, dev)
+            pb = b.data_ptr()
+        if with_rstd:
+            rf = None if pp is None else empty((rows,), torch.float32, dev)
+            rh = None if pq is None else empty((rows,), torch.float32, dev)
+        _check(load().tsp_norm_residual_fwd(pf, px, pz, pp, pq, ph, pb, _addr(rf), _addr(rh), rows,
+                                            n, scale, eps, e, es, st), "tsp_norm_residual_fwd")
+    return (h, b, rf, rh) if with_rstd else (h, b)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def norm_residual_bwd_workspace_bytes(rows: int, n: int) -> int:
+    return int(load().tsp_norm_residual_bwd_workspace_bytes(int(rows), int(n)))
+
+
+def norm_residual_bwd(dh, db, f, h, g_post=None, g_pre=None, rstd_f=None, rstd_h=None, gate=None,
+                      scale: float = 1.0, dx=None, ws=None, stream=None) -> dict:
+    """Gradients of sum(dh * h) + sum(db * b) of norm_residual_fwd: dx (fp32),
+    df and, where they exist, dgate, dg_post, dg_pre (fp32).  dh, db fp32; db, h
+    and rstd_h belong to g_pre, rstd_f to g_post.  ``dx`` may be dh."""
+    if f.dim() != 2:
+        raise ValueError("f must be [rows, n]")
+    shape, dt, dev, f32 = f.shape, f.dtype, f.device, torch.float32
+    rows, n = shape
+    if g_pre is None:
+        h = None                  # only the pre-norm's backward reads it
+    e = _enum("f", dt)
+    hs = f32 if h is None else h.dtype
+    es = _enum("h", hs)
+    pf, ph = _arg("f", f, shape, dt, dev), _arg("h", h, shape, hs, dev)
+    pdh, pdb = _arg("dh", dh, shape, f32, dev), _arg("db", db, shape, f32, dev)
+    pz = _arg("gate", gate, shape, dt, dev)
+    pp, pq = _arg("g_post", g_post, (n,), dt, dev), _arg("g_pre", g_pre, (n,), dt, dev)
+    prf, prh = _arg("rstd_f", rstd_f, (rows,), f32, dev), _arg("rstd_h", rstd_h, (rows,), f32, dev)
+    pdx = _arg("dx", dx, shape, f32, dev)
+    out = {}
+    with _On(dev, stream) as st:
+        lib = load()
+        out["dx"] = empty(shape, f32, dev) if dx is None else dx
+        out["df"] = empty(shape, dt, dev)
+        if gate is not None:
+            out["dgate"] = empty(shape, dt, dev)
+        if g_post is not None:
+            out["dg_post"] = empty((n,), f32, dev)
+        if g_pre is not None:
+            out["dg_pre"] = empty((n,), f32, dev)
+        if ws is None and (g_post is not None or g_pre is not None):
+            ws = _ws(lib.tsp_norm_residual_bwd_workspace_bytes(rows, n), dev)
+        _check(lib.tsp_norm_residual_bwd(pdh, pdb, pf, pz, ph, pp, pq, prf, prh,
+                                         out["dx"].data_ptr(), out["df"].data_ptr(),
+                                         _addr(out.get("dgate")), _addr(out.get("dg_post")),
+                                         _addr(out.get("dg_pre")), rows, n, scale, e, es,
+                                         _addr(ws), 0 if ws is None else ws.numel(), st),
+               "tsp_norm_residual_bwd")
+    return out
+
+
+ADAMW_BLOCK = 128   # TSP_ADAMW_BLOCK
+
+
+def prep_views(cfg: Cfg, prep) -> list:
+    """The fp16 operand copies inside a prepare_weights buffer, in the order of
+    GRAD_NAMES (None for the gains, which have none): what AdamW refreshes."""
+    out, at = [], 0
+    for shape in list(_grad_shapes(cfg).values())[:7]:
+        n = shape[0] * shape[1]
+        out.append(prep[at:at + 2 * n].view(torch.float16))
+        at += (2 * n + 255) // 256 * 256
+    return out + [None, None]
+
+
+class AdamW:
+    """AdamW over a list of tensors of one type (bf16 or fp32) in one launch per
+    128 of them.
+
+    ``weight_decay``: a number, or one per tensor.  ``state_bits``: 32, or 8
+    for e4m3 codes with an fp32 scale per 128 elements (``v`` then holds the
+    square root).  ``master``: True keeps fp32 masters of bf16 tensors (started
+    from them), None updates the tensors themselves, a list gives the masters.
+    ``m``, ``v``, ``m_scale``, ``v_scale``: lists of existing states to go on
+    with (default: zeros).  ``prep``: for each tensor the fp16 operand copy to
+    refresh (prep_views) or None.
+    """
+
+    def __init__(self, params, weight_decay=0.0, state_bits: int = 32, master=True, m=None, v=None,
+                 m_scale=None, v_scale=None, prep=None, betas=(0.9, 0.95), eps: float = 1e-8):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("AdamW needs at least one tensor")
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        n_t, dt, dev = len(self.params), self.params[0].dtype, self.params[0].device
+        self.dtype, self.device, self.state_bits = _enum("params", dt), dev, state_bits
+        self.betas, self.eps, self.t = (float(betas[0]), float(betas[1])), float(eps), 0
+        if isinstance(weight_decay, (int, float)):
+            weight_decay = [weight_decay] * n_t
+        coded, f32 = state_bits == 8, torch.float32
+        code = torch.float8_e4m3fn if coded else f32
+        blocks = [(-(-p.numel() // ADAMW_BLOCK),) for p in self.params]
+
+        def states(given, dtype, shapes, on):
+            if not on:
+                if given is not None:
+                    raise ValueError("block scales belong to 8-bit states")
+                return [None] * n_t
+            if given is not None:
+                return list(given)
+            return [torch.zeros(s, dtype=torch.uint8, device=dev).view(dtype) if dtype != f32
+                    else torch.zeros(s, dtype=f32, device=dev) for s in shapes]
+        shapes = [p.shape for p in self.params]
+        self.m, self.v = states(m, code, shapes, True), states(v, code, shapes, True)
+        self.m_scale = states(m_scale, f32, blocks, coded)
+        self.v_scale = states(v_scale, f32, blocks, coded)
+        if master is True:
+            master = [p.float() for p in self.params] if self.dtype == TSP_BF16 else None
+        self.master = list(master) if master is not None and master is not False else [None] * n_t
+        self.prep = list(prep) if prep is not None else [None] * n_t
+        every = (weight_decay, self.m, self.v, self.m_scale, self.v_scale, self.master, self.prep)
+        if any(len(x) != n_t for x in every):
+            raise ValueError(f"one entry for each of the {n_t} tensors is wanted")
+        self._arr = (AdamwTensor * n_t)()
+        for i, p in enumerate(self.params):
+            t = self._arr[i]
+            t.n, t.w = p.numel(), _arg(f"params[{i}]", p, p.shape, dt, dev)
+            for name, x, dtype in (("m", self.m[i], code), ("v", self.v[i], code),
+                                   ("master", self.master[i], f32),
+                                   ("prep", self.prep[i], torch.float16)):
+                if x is not None and x.numel() != p.numel():
+                    raise ValueError(f"{name}[{i}] has {x.numel()} elements, its tensor {p.numel()}")
+                setattr(t, name, _arg(f"{name}[{i}]", x, None if x is None else x.shape, dtype, dev))
+            t.m_scale = _arg(f"m_scale[{i}]", self.m_scale[i], blocks[i], f32, dev)
+            t.v_scale = _arg(f"v_scale[{i}]", self.v_scale[i], blocks[i], f32, dev)
+            t.weight_decay = float(weight_decay[i])
+        self._sizes = [p.numel() for p in self.params]
+
+    def step(self, grads, lr, step=None, gscale=None, stream=None):
+        """One update from the fp32 ``grads`` (one for each tensor, same sizes).
+        ``lr``: a number, or a one-element fp32 GPU tensor; ``step``: the
+        update's number (1 first; default: counted by this object), or a
+        one-element int64 GPU tensor; ``gscale``: a one-element fp32 GPU tensor
+        that the gradients are multiplied by.  Tensors are read when the kernel
+        runs, so a captured step can be replayed with new values in them."""
+        arr, dev, f32 = self._arr, self.device, torch.float32
+        if len(grads) != len(self._sizes):
+            raise ValueError(f"{len(grads)} gradients for {len(self._sizes)} tensors")
+        index = dev.index
+        for t, g, n in zip(arr, grads, self._sizes):
+            if g.dtype is not f32 or g.numel() != n or g.get_device() != index or \
+                    not g.is_contiguous():
+                raise ValueError("gradients are contiguous fp32 tensors of their tensors' sizes "
+                                 "on their device")
+            t.g = g.data_ptr()
+        hy = AdamwHyper(0.0, self.betas[0], self.betas[1], self.eps, 1)
+        if isinstance(lr, torch.Tensor):
+            hy.lr_dev = _arg("lr", lr.view(-1), (1,), f32, dev)
+        else:
+            hy.lr = lr
+        if isinstance(step, torch.Tensor):
+            hy.step_dev = _arg("step", step.view(-1), (1,), torch.int64, dev)
+        else:
+            hy.step = self.t + 1 if step is None else step
+        if gscale is not None:
+            hy.gscale_dev = _arg("gscale", gscale.view(-1), (1,), f32, dev)
+        with _On(dev, stream) as st:
+            _check(load().tsp_adamw_step(arr, len(arr), ctypes.byref(hy), self.state_bits,
+                                         self.dtype, st), "tsp_adamw_step")
+        if not isinstance(step, torch.Tensor):
+            self.t = int(hy.step)
 
 
 def device_status(reset: bool = True, stream=None) -> int:

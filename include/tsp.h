@@ -81,7 +81,8 @@ typedef enum {
   TSP_ERR_UNSUPPORTED = 2,   /* valid shape that the selected kernels do not take */
   TSP_ERR_CUDA = 3,          /* a CUDA runtime call or launch failed               */
   TSP_ERR_TIMEOUT = 4,       /* a device pipeline wait exceeded its time limit     */
-  TSP_ERR_RANGE = 5,         /* a value the bf16 path holds in fp16 was out of fp16 range */
+  TSP_ERR_RANGE = 5,         /* a value the bf16 path holds in fp16 was out of fp16 range,
+                                or a token id was past the embedding table */
   TSP_ERR_BOUNDS = 6         /* checked build only: a computed index failed its bounds check */
 } tsp_status;
 
@@ -495,6 +496,132 @@ tsp_status tsp_rank_attn_bwd_finish(const tsp_cfg* cfg, int32_t r, const void* x
                                     const void* g_attn, const float* da_r, const float* dh_r,
                                     float* dx_r, float* dg_attn, void* ws, size_t ws_bytes,
                                     void* stream);
+
+/* ---- Around the stack: token embedding --------------------------------------
+ * (not on the pages, whose block starts from x_z: what a model puts before it)
+ *
+ * tsp_embed_fwd: x_z[row(p)] = scale * table[ids[p]] for every global position
+ *   p < S, row(p) its zigzag row: gather, scale and tsp_zigzag_permute in one
+ *   pass.  Scaled in fp32 and rounded once; scale == 1 copies the row's bits.
+ * tsp_embed_bwd: dtable[v] = scale * (sum of dx_z[row(p)] over the p with
+ *   ids[p] == v), fp32; rows of tokens that do not occur are set to zero.
+ *   With accumulate != 0 the sums are added to dtable instead and the other
+ *   rows are left alone (a table tied to the output projection).  dx_z is
+ *   what tsp_stack_bwd leaves (dx_dtype TSP_F32) or bf16 (TSP_BF16).  The
+ *   positions are sorted by token first and each sum runs in the order of the
+ *   positions, in fp32, so equal calls give equal bits; nothing is atomic.
+ *
+ *   ids       [S] global token order, id_bytes 4 (int32) or 8 (int64); needs
+ *             only its own alignment.  id < 0: padding -- a zero row of x_z,
+ *             no gradient.  id >= V: the same, and TSP_ERR_RANGE is recorded
+ *             in the device status word; no row is read or written for it.
+ *   table     [V, d] of dtype;  x_z [S, d] of dtype;  dtable [V, d] fp32
+ *   D         ranks of the zigzag order, 1..64, S a multiple of 2D; D == 1 is
+ *             the global order and takes every S >= 1 (decoded tokens)
+ *   ws        tsp_embed_bwd_workspace_bytes(S, V, d) bytes; nothing in it has
+ *             to survive the call
+ * Errors: TSP_ERR_INVALID_ARG (sizes, NULL or misaligned pointers, a scale
+ *   that is not finite, a short workspace); TSP_ERR_UNSUPPORTED for S > 2^30
+ *   or V > 2^31 - 2.  tsp_embed_bwd_workspace_bytes returns 0 for sizes that
+ *   the call would refuse. */
+tsp_status tsp_embed_fwd(const void* ids, int32_t id_bytes, const void* table, void* x_z,
+                         int64_t S, int32_t D, int64_t V, int32_t d, float scale, int32_t dtype,
+                         void* stream);
+size_t tsp_embed_bwd_workspace_bytes(int64_t S, int64_t V, int32_t d);
+tsp_status tsp_embed_bwd(const void* ids, int32_t id_bytes, const void* dx_z, int32_t dx_dtype,
+                         float* dtable, int64_t S, int32_t D, int64_t V, int32_t d, float scale,
+                         int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Between two sub-layers: post-norm, gate, scaled residual, pre-norm ------
+ * (not on the pages, whose block is pre-norm only.)  For a sub-layer run
+ * without its own norm and residual -- tsp_gated_mlp_fwd with g_mlp NULL and
+ * add_residual 0 -- this is everything between its output f and the next
+ * sub-layer's input b, row by row:
+ *   u = rms(f; g_post)                  (u = f with g_post NULL)
+ *   h = x + scale * sigmoid(gate) * u   (no gate with gate NULL)
+ *   b = rms(h; g_pre)                   (no b with g_pre NULL)
+ * rms(h; .) is that of h as it is stored, so b equals tsp_rmsnorm_fwd of h.
+ * f, gate, b [rows, n] and g_post, g_pre [n] are of dtype; x and h [rows, n]
+ * of stream_dtype (TSP_F32, or TSP_BF16 with dtype TSP_BF16); h may be x.
+ * rstd_f, rstd_h (nullable) [rows] fp32 receive 1/sqrt(mean(.^2) + eps) where
+ * the norm is there: the backward reads them.
+ *
+ * Backward of L = sum(dh * h) + sum(db * b).  dh [rows, n] fp32 (NULL, only
+ * with g_pre: none), db [rows, n] fp32 (with g_pre); h as the forward left it.
+ * Out: dx [rows, n] fp32 (the residual stream's gradient; may be dh), df and
+ * dgate (with gate) [rows, n] of dtype (the sub-layer's upstream gradients),
+ * dg_post, dg_pre [n] fp32, overwritten, summed over the rows in a fixed
+ * order.  ws: tsp_norm_residual_bwd_workspace_bytes(rows, n) bytes (NULL
+ * without gains).
+ * A pointer that the NULLs above leave without a use has to be NULL too.
+ * Errors: TSP_ERR_INVALID_ARG; TSP_ERR_UNSUPPORTED for n > 2^24. */
+tsp_status tsp_norm_residual_fwd(const void* f, const void* x, const void* gate,
+                                 const void* g_post, const void* g_pre, void* h, void* b,
+                                 float* rstd_f, float* rstd_h, int64_t rows, int32_t n,
+                                 float scale, float eps, int32_t dtype, int32_t stream_dtype,
+                                 void* stream);
+size_t tsp_norm_residual_bwd_workspace_bytes(int64_t rows, int32_t n);
+tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f, const void* gate,
+                                 const void* h, const void* g_post, const void* g_pre,
+                                 const float* rstd_f, const float* rstd_h, float* dx, void* df,
+                                 void* dgate, float* dg_post, float* dg_pre, int64_t rows,
+                                 int32_t n, float scale, int32_t dtype, int32_t stream_dtype,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/* ---- After the backward: AdamW over many tensors ------------------------------
+ * (not on the pages: the step that turns the fp32 gradients of tsp_stack_bwd
+ * and tsp_embed_bwd into the next weights.)  For every element of every tensor
+ *   g = g * gscale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   w = w (1 - lr weight_decay)
+ *       - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32, each elementary operation rounded by itself.
+ *
+ * tsp_adamw_tensor (a host array of `count`; the pointers are device pointers):
+ *   n        elements, >= 0 (0: skipped, its pointers may be NULL)
+ *   w        [n] of dtype, updated
+ *   master   [n] fp32 or NULL (TSP_BF16 only): the weight the update is applied
+ *            to; w is then its rounding.  NULL: w itself is updated and
+ *            rounded (in bf16 that loses updates below half a spacing of w)
+ *   g        [n] fp32
+ *   m, v     state_bits 32: [n] fp32.  state_bits 8: [n] e4m3 codes, v holding
+ *            sqrt(v); m_scale, v_scale [ceil(n / TSP_ADAMW_BLOCK)] fp32 (NULL
+ *            with 32; 4-byte aligned), a block's largest magnitude / 448: a code stands for
+ *            code * scale.  A block below 2^-100 is held as zeros; a positive
+ *            sqrt(v) takes at least the smallest code.  Zero bytes are the
+ *            initial state of either.  (Nearest rounding: an 8-bit v that moves
+ *            by less than half a spacing relative to its block stays.)
+ *   prep     [n] fp16 or NULL (TSP_BF16 only): receives the new weight as the
+ *            operand copy tsp_block_weights_prepare would make of it (a weight
+ *            fp16 cannot hold records TSP_ERR_RANGE)
+ * tsp_adamw_hyper: lr, beta1, beta2 in [0, 1), eps >= 0, step t >= 1 (the first
+ *   update is 1).  lr_dev, step_dev, gscale_dev (nullable DEVICE pointers to one
+ *   value, read when the kernel runs): replace lr and step, and scale the
+ *   gradients (clipping by a norm computed on the device).  A captured call
+ *   keeps the host values it was captured with; a graph that is replayed over
+ *   many steps passes step_dev and advances it.
+ * One launch per 128 tensors.  Errors: TSP_ERR_INVALID_ARG (also for two
+ *   tensors whose weights overlap: one call may update a weight once). */
+#define TSP_ADAMW_BLOCK 128
+typedef struct {
+  int64_t n;
+  void* w;
+  float* master;
+  const float* g;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  void* prep;
+  float weight_decay;
+} tsp_adamw_tensor;
+typedef struct {
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  const float* lr_dev;
+  const int64_t* step_dev;
+  const float* gscale_dev;
+} tsp_adamw_hyper;
+tsp_status tsp_adamw_step(const tsp_adamw_tensor* tensors, int32_t count,
+                          const tsp_adamw_hyper* hyper, int32_t state_bits, int32_t dtype,
+                          void* stream);
 
 /* Reads (and with reset != 0 clears) the sticky device status word.  Waits
  * for `stream` to finish.  Returns TSP_OK or the first device error seen
