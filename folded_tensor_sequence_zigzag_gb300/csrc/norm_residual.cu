@@ -14,6 +14,8 @@
 // Sums and statistics are fp32.  rstd_h is the norm of h as it is stored, so b
 // is what tsp_rmsnorm_fwd gives for the h the caller sees, and the backward,
 // which reads that h, differentiates the same function.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -21,60 +23,80 @@ namespace tsp {
 
 namespace {
 
-// N consecutive elements (N = 8: 16-byte accesses; N = 1: any alignment).
+// N consecutive elements as they are stored (N = 4: one 8- or 16-byte access, n
+// a multiple of 4; N = 1: any n).
+template <typename T, int N>
+struct Unit {
+  T e[N];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (N == 1) e[0] = *p;
+    else if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
+    else *reinterpret_cast<float4*>(e) = *reinterpret_cast<const float4*>(p);
+  }
+  __device__ __forceinline__ void get(float (&v)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = to_f<T>(e[i]);
+  }
+} __attribute__((aligned(sizeof(T) * N)));
+
 template <typename T, int N>
 __device__ __forceinline__ void load_n(const T* p, float (&v)[N]) {
-  if constexpr (N == 1) {
-    v[0] = to_f<T>(*p);
-  } else if constexpr (sizeof(T) == 2) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = lo2<T>(w[i]);
-      v[2 * i + 1] = hi2<T>(w[i]);
-    }
-  } else {
-    const float4 a = reinterpret_cast<const float4*>(p)[0];
-    const float4 b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
+  Unit<T, N> u;
+  u.load(p);
+  u.get(v);
 }
 template <typename T, int N>
 __device__ __forceinline__ void store_n(T* p, const float (&v)[N]) {
-  if constexpr (N == 1) {
+  if constexpr (N == 1)
     *p = from_f<T>(v[0]);
-  } else if constexpr (sizeof(T) == 2) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]),
-                                              pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+  else if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+  else
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// sigmoid(z) and its derivative from e = exp(-|z|), which neither overflows nor
+// cancels: sigmoid(|z|) = 1 / (1 + e), sigmoid(-|z|) = e / (1 + e).  e is 2^x of
+// the rounded x = -|z| log2(e): off by |z| + 2 half spacings, which the sigmoid
+// has only where it is e itself, near a closed gate.
+__device__ __forceinline__ float gate_of(float z, float* slope) {
+  const float e = ex2_approx(-1.4426950408889634f * fabsf(z)), r = __fdividef(1.f, 1.f + e);
+  *slope = e * r * r;
+  return z >= 0.f ? r : e * r;   // (a NaN gives NaN: e is one)
+}
+__device__ __forceinline__ float gate_of(float z) {
+  float slope;
+  return gate_of(z, &slope);
+}
+
+// Sum over the TPR threads of a row (TPR <= 32: a part of a warp; 0: the CTA),
+// the same in every one of them.  `part` holds one value a warp and may be
+// reused only after another barrier of the CTA.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* part) {
+  if constexpr (TPR > 0) {
+#pragma unroll
+    for (int o = TPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
   } else {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    v = warp_sum(v);
+    if (lane == 0) part[warp] = v;
+    __syncthreads();
+    return warp_sum(lane < nw ? part[lane] : 0.f);
   }
 }
 
-// sigmoid and its derivative from e = exp(-|z|), which neither overflows nor
-// cancels: sigmoid(|z|) = 1 / (1 + e), sigmoid(-|z|) = e / (1 + e).
-__device__ __forceinline__ float gate_of(float z) {
-  const float e = expf(-fabsf(z)), r = 1.f / (1.f + e);
-  return z >= 0.f ? r : (z < 0.f ? e * r : z);   // a NaN stays one
+// A copy on its way to shared memory.  Every thread copies what it will read
+// itself, so waiting for its own copies is all the synchronisation there is.
+template <typename T, int N>
+__device__ __forceinline__ void copy_ahead(T* dst, const T* src) {
+  constexpr int B = sizeof(T) * N;
+  static_assert(B == 4 || B == 8 || B == 16, "a copy is 4, 8 or 16 bytes");
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(B)
+               : "memory");
 }
-__device__ __forceinline__ float gate_slope(float z) {
-  const float e = expf(-fabsf(z)), r = 1.f / (1.f + e);
-  return e * r * r;
-}
-
-// Sum over the CTA, the same in every thread; `part` holds one value a warp
-// and is reused by the next call only after another barrier.
-__device__ __forceinline__ float cta_sum(float v, float* part) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  v = warp_sum(v);
-  if (nw == 1) return v;
-  if (lane == 0) part[warp] = v;
-  __syncthreads();
-  return warp_sum(lane < nw ? part[lane] : 0.f);
-}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 struct FwdArgs {
   const void *f, *x, *z, *g_post, *g_pre;
@@ -85,72 +107,121 @@ struct FwdArgs {
   float s, eps;
 };
 
-// A CTA a row (grid-stride), the row in registers: UPT units of N elements a
-// thread, unit i of thread t at (i * blockDim + t) * N.
-template <typename T, typename Ts, int N, int UPT>
+// The row in registers: UPT units of N elements a thread, unit i of thread t of
+// the row at (i * threads + t) * N, so that a warp's accesses are contiguous.
+//   TPR > 0: TPR threads a row, 256 / TPR rows a CTA (short rows);
+//   TPR = 0: a CTA a row.
+// AHEAD (TPR = 0): once every thread has its part of a row in registers (the
+// first row sum's barrier), the next row's inputs are sent for, each thread's
+// into the places it has just read, and arrive while this row is worked on.
+// Without that the loads of a row wait for the barriers of the one before.
+template <typename T, typename Ts, int N, int UPT, int TPR, bool AHEAD>
 __global__ void __launch_bounds__(1024) norm_residual_fwd_kernel(const __grid_constant__ FwdArgs a) {
   __shared__ float part[2][32];
-  const int n = a.n, t = threadIdx.x;
+  extern __shared__ __align__(16) uint8_t ahead[];
+  const int n = a.n;
+  const int t = TPR > 0 ? threadIdx.x % (TPR > 0 ? TPR : 1) : threadIdx.x;
+  const int threads = TPR > 0 ? TPR : blockDim.x;
+  const int64_t per = TPR > 0 ? blockDim.x / TPR : 1;
   const float inv_n = 1.f / (float)n;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+  // f, z, x in planes of threads * UPT units
+  const int plane = threads * UPT * N;
+  T* const f_in = (T*)ahead;
+  T* const z_in = f_in + plane;
+  Ts* const x_in = (Ts*)(z_in + plane);
+  auto issue = [&](int64_t row) {
+    if constexpr (AHEAD) {
+      if (row < a.rows) {
+#pragma unroll
+        for (int i = 0; i < UPT; ++i) {
+          const int u = (i * threads + t) * N;
+          if (u < n) {
+            copy_ahead<T, N>(f_in + u, (const T*)a.f + row * n + u);
+            if (a.z) copy_ahead<T, N>(z_in + u, (const T*)a.z + row * n + u);
+            copy_ahead<Ts, N>(x_in + u, (const Ts*)a.x + row * n + u);
+          }
+        }
+      }
+    }
+  };
+  issue(blockIdx.x);
+  for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < a.rows; row0 += (int64_t)gridDim.x * per) {
+    const int64_t row = TPR > 0 ? row0 + threadIdx.x / (TPR > 0 ? TPR : 1) : row0;
+    const bool on = TPR == 0 || row < a.rows;
     const int64_t base = row * n;
+    if constexpr (AHEAD) copies_wait();
+    const T* fp = AHEAD ? f_in : (const T*)a.f + base;
+    const T* zp = AHEAD ? z_in : (const T*)a.z + base;
+    const Ts* xp = AHEAD ? x_in : (const Ts*)a.x + base;
     float v[UPT][N];
+    Unit<Ts, N> q[UPT];
+    Unit<T, N> z[UPT];
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      const int c = (i * blockDim.x + t) * N;
-      if (c < n) {
-        load_n<T, N>((const T*)a.f + base + c, v[i]);
+      const int c = (i * threads + t) * N;
 #pragma unroll
-        for (int e = 0; e < N; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+      for (int e = 0; e < N; ++e) v[i][e] = 0.f;
+      if (c < n && on) {
+        load_n<T, N>(fp + c, v[i]);
+        q[i].load(xp + c);
+        if (a.z) z[i].load(zp + c);
       }
     }
     float r = 1.f;
     if (a.g_post) {
-      r = rsqrtf(cta_sum(ss, part[0]) * inv_n + a.eps);
-      if (t == 0 && a.rstd_f) a.rstd_f[row] = r;
+#pragma unroll
+      for (int i = 0; i < UPT; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) ss = fmaf(v[i][e], v[i][e], ss);
+      r = rsqrtf(row_sum<TPR>(ss, part[0]) * inv_n + a.eps);
+      if (t == 0 && on && a.rstd_f) a.rstd_f[row] = r;
+    } else if (AHEAD) {
+      __syncthreads();
     }
+    issue(row + gridDim.x);
     ss = 0.f;
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      const int c = (i * blockDim.x + t) * N;
-      if (c < n) {
-        float q[N];
+      const int c = (i * threads + t) * N;
+      if (c < n && on) {
+        float w[N];
         if (a.g_post) {
-          load_n<T, N>((const T*)a.g_post + c, q);
+          load_n<T, N>((const T*)a.g_post + c, w);
 #pragma unroll
-          for (int e = 0; e < N; ++e) v[i][e] *= r * q[e];
+          for (int e = 0; e < N; ++e) v[i][e] *= r * w[e];
         }
         if (a.z) {
-          load_n<T, N>((const T*)a.z + base + c, q);
+          z[i].get(w);
 #pragma unroll
-          for (int e = 0; e < N; ++e) v[i][e] *= gate_of(q[e]);
+          for (int e = 0; e < N; ++e) v[i][e] *= gate_of(w[e]);
         }
-        load_n<Ts, N>((const Ts*)a.x + base + c, q);
+        q[i].get(w);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          v[i][e] = to_f<Ts>(from_f<Ts>(fmaf(a.s, v[i][e], q[e])));
+          v[i][e] = to_f<Ts>(from_f<Ts>(fmaf(a.s, v[i][e], w[e])));
           ss = fmaf(v[i][e], v[i][e], ss);
         }
         store_n<Ts, N>((Ts*)a.h + base + c, v[i]);
       }
     }
     if (a.g_pre) {
-      r = rsqrtf(cta_sum(ss, part[1]) * inv_n + a.eps);
-      if (t == 0 && a.rstd_h) a.rstd_h[row] = r;
+      r = rsqrtf(row_sum<TPR>(ss, part[1]) * inv_n + a.eps);
+      if (t == 0 && on && a.rstd_h) a.rstd_h[row] = r;
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
-        const int c = (i * blockDim.x + t) * N;
-        if (c < n) {
-          float q[N];
-          load_n<T, N>((const T*)a.g_pre + c, q);
+        const int c = (i * threads + t) * N;
+        if (c < n && on) {
+          float g[N];
+          load_n<T, N>((const T*)a.g_pre + c, g);
 #pragma unroll
-          for (int e = 0; e < N; ++e) q[e] *= v[i][e] * r;
-          store_n<T, N>((T*)a.b + base + c, q);
+          for (int e = 0; e < N; ++e) g[e] *= v[i][e] * r;
+          store_n<T, N>((T*)a.b + base + c, g);
         }
       }
     }
-    if (!(a.g_post && a.g_pre)) __syncthreads();   // one barrier a row would let `part` be reused early
+    // with one barrier a row, `part` would be written again before all have read it
+    if (TPR == 0 && !(a.g_post && a.g_pre)) __syncthreads();
   }
 }
 
@@ -169,7 +240,7 @@ __global__ void __launch_bounds__(1024) norm_residual_fwd_wide_kernel(const __gr
     float r = 1.f, ss = 0.f;
     if (a.g_post) {
       for (int c = threadIdx.x; c < n; c += blockDim.x) ss = fmaf(to_f<T>(f[c]), to_f<T>(f[c]), ss);
-      r = rsqrtf(cta_sum(ss, part[0]) * inv_n + a.eps);
+      r = rsqrtf(row_sum<0>(ss, part[0]) * inv_n + a.eps);
       if (threadIdx.x == 0 && a.rstd_f) a.rstd_f[row] = r;
     }
     ss = 0.f;
@@ -182,7 +253,7 @@ __global__ void __launch_bounds__(1024) norm_residual_fwd_wide_kernel(const __gr
       ss = fmaf(to_f<Ts>(o), to_f<Ts>(o), ss);
     }
     if (a.g_pre) {
-      r = rsqrtf(cta_sum(ss, part[1]) * inv_n + a.eps);
+      r = rsqrtf(row_sum<0>(ss, part[1]) * inv_n + a.eps);
       if (threadIdx.x == 0 && a.rstd_h) a.rstd_h[row] = r;
       for (int c = threadIdx.x; c < n; c += blockDim.x)
         ((T*)a.b)[row * n + c] = from_f<T>(to_f<Ts>(h[c]) * r * to_f<T>(((const T*)a.g_pre)[c]));
@@ -203,65 +274,117 @@ struct BwdArgs {
   float s;
 };
 
-// The same layout; a thread's columns are the same in every row, so its share
-// of the gain gradients stays in registers until the CTA's last row.
-template <typename T, typename Ts, int N, int UPT>
-__global__ void __launch_bounds__(UPT * N > 8 ? 512 : 1024) norm_residual_bwd_kernel(const __grid_constant__ BwdArgs a) {
+// The same layout and the same copies ahead (dh, db, h, f, z).  A thread's
+// columns are the same in every row, so its share of the gain gradients stays
+// in registers until the CTA's last row; with several rows a CTA the groups'
+// shares are added in shared memory in the order of the groups.
+template <typename T, typename Ts, int N, int UPT, int TPR, bool AHEAD>
+__global__ void __launch_bounds__(512, UPT * N <= 8 ? 2 : 1) norm_residual_bwd_kernel(const __grid_constant__ BwdArgs a) {
   __shared__ float part[2][32];
-  const int n = a.n, t = threadIdx.x;
+  extern __shared__ __align__(16) uint8_t ahead[];
+  const int n = a.n;
+  const int t = TPR > 0 ? threadIdx.x % (TPR > 0 ? TPR : 1) : threadIdx.x;
+  const int threads = TPR > 0 ? TPR : blockDim.x;
+  const int64_t per = TPR > 0 ? blockDim.x / TPR : 1;
   const float inv_n = 1.f / (float)n;
   float dpost[UPT][N], dpre[UPT][N];
 #pragma unroll
   for (int i = 0; i < UPT; ++i)
 #pragma unroll
     for (int e = 0; e < N; ++e) dpost[i][e] = dpre[i][e] = 0.f;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+  // dh, db (fp32), h, f, z in planes of threads * UPT units
+  const int plane = threads * UPT * N;
+  float* const dh_in = (float*)ahead;
+  float* const db_in = dh_in + plane;
+  Ts* const h_in = (Ts*)(db_in + plane);
+  T* const f_in = (T*)(h_in + plane);
+  T* const z_in = f_in + plane;
+  auto issue = [&](int64_t row) {
+    if constexpr (AHEAD) {
+      if (row < a.rows) {
+#pragma unroll
+        for (int i = 0; i < UPT; ++i) {
+          const int u = (i * threads + t) * N;
+          if (u < n) {
+            const int64_t at = row * n + u;
+            if (a.dh) copy_ahead<float, N>(dh_in + u, a.dh + at);
+            if (a.g_pre) {
+              copy_ahead<float, N>(db_in + u, a.db + at);
+              copy_ahead<Ts, N>(h_in + u, (const Ts*)a.h + at);
+            }
+            copy_ahead<T, N>(f_in + u, (const T*)a.f + at);
+            if (a.z) copy_ahead<T, N>(z_in + u, (const T*)a.z + at);
+          }
+        }
+      }
+    }
+  };
+  issue(blockIdx.x);
+  for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < a.rows; row0 += (int64_t)gridDim.x * per) {
+    const int64_t row = TPR > 0 ? row0 + threadIdx.x / (TPR > 0 ? TPR : 1) : row0;
+    const bool on = TPR == 0 || row < a.rows;
     const int64_t base = row * n;
-    float d[UPT][N], q[N];
+    const float rf = a.g_post && on ? a.rstd_f[row] : 1.f;
+    const float rh = a.g_pre && on ? a.rstd_h[row] : 0.f;
+    if constexpr (AHEAD) copies_wait();
+    const float* dhp = AHEAD ? dh_in : a.dh + base;
+    const float* dbp = AHEAD ? db_in : a.db + base;
+    const Ts* hp = AHEAD ? h_in : (const Ts*)a.h + base;
+    const T* fp = AHEAD ? f_in : (const T*)a.f + base;
+    const T* zp = AHEAD ? z_in : (const T*)a.z + base;
+    float d[UPT][N];
+    Unit<T, N> fu[UPT], zu[UPT];
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      const int c = (i * blockDim.x + t) * N;
+      const int c = (i * threads + t) * N;
 #pragma unroll
       for (int e = 0; e < N; ++e) d[i][e] = 0.f;
-      if (c < n && a.dh) load_n<float, N>(a.dh + base + c, d[i]);
+      if (c < n && on) {
+        if (a.dh) load_n<float, N>(dhp + c, d[i]);
+        fu[i].load(fp + c);
+        if (a.z) zu[i].load(zp + c);
+      }
     }
     if (a.g_pre) {
-      const float r = a.rstd_h[row];
       float y[UPT][N], gd[UPT][N], dot = 0.f;
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
-        const int c = (i * blockDim.x + t) * N;
-        if (c < n) {
-          load_n<Ts, N>((const Ts*)a.h + base + c, y[i]);
-          load_n<float, N>(a.db + base + c, gd[i]);
-          load_n<T, N>((const T*)a.g_pre + c, q);
+        const int c = (i * threads + t) * N;
+        if (c < n && on) {
+          float g[N];
+          load_n<Ts, N>(hp + c, y[i]);
+          load_n<float, N>(dbp + c, gd[i]);
+          load_n<T, N>((const T*)a.g_pre + c, g);
 #pragma unroll
           for (int e = 0; e < N; ++e) {
-            y[i][e] *= r;
+            y[i][e] *= rh;
             dpre[i][e] = fmaf(gd[i][e], y[i][e], dpre[i][e]);
-            gd[i][e] *= q[e];
+            gd[i][e] *= g[e];
             dot = fmaf(gd[i][e], y[i][e], dot);
           }
         }
       }
-      dot = cta_sum(dot, part[0]) * inv_n;
+      dot = row_sum<TPR>(dot, part[0]) * inv_n;
+      issue(row + gridDim.x);
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
-        const int c = (i * blockDim.x + t) * N;
-        if (c < n) {
+        const int c = (i * threads + t) * N;
+        if (c < n && on) {
 #pragma unroll
-          for (int e = 0; e < N; ++e) d[i][e] = fmaf(r, gd[i][e] - y[i][e] * dot, d[i][e]);
+          for (int e = 0; e < N; ++e) d[i][e] = fmaf(rh, gd[i][e] - y[i][e] * dot, d[i][e]);
         }
       }
+    } else {
+      if (AHEAD) __syncthreads();
+      issue(row + gridDim.x);
     }
-    const float rf = a.g_post ? a.rstd_f[row] : 1.f;
     float y[UPT][N], dot = 0.f;
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      const int c = (i * blockDim.x + t) * N;
-      if (c < n) {
+      const int c = (i * threads + t) * N;
+      if (c < n && on) {
         store_n<float, N>(a.dx + base + c, d[i]);
-        load_n<T, N>((const T*)a.f + base + c, y[i]);
+        fu[i].get(y[i]);
         float g[N];
 #pragma unroll
         for (int e = 0; e < N; ++e) {
@@ -271,12 +394,13 @@ __global__ void __launch_bounds__(UPT * N > 8 ? 512 : 1024) norm_residual_bwd_ke
         }
         if (a.g_post) load_n<T, N>((const T*)a.g_post + c, g);
         if (a.z) {
-          float dz[N];
-          load_n<T, N>((const T*)a.z + base + c, q);
+          float z[N], dz[N], slope;
+          zu[i].get(z);
 #pragma unroll
           for (int e = 0; e < N; ++e) {
-            dz[e] = d[i][e] * (y[i][e] * g[e]) * gate_slope(q[e]);
-            d[i][e] *= gate_of(q[e]);
+            const float open = gate_of(z[e], &slope);
+            dz[e] = d[i][e] * (y[i][e] * g[e]) * slope;
+            d[i][e] *= open;
           }
           store_n<T, N>((T*)a.dz + base + c, dz);
         }
@@ -290,11 +414,11 @@ __global__ void __launch_bounds__(UPT * N > 8 ? 512 : 1024) norm_residual_bwd_ke
         }
       }
     }
-    if (a.g_post) dot = cta_sum(dot, part[1]) * inv_n;
+    if (a.g_post) dot = row_sum<TPR>(dot, part[1]) * inv_n;
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      const int c = (i * blockDim.x + t) * N;
-      if (c < n) {
+      const int c = (i * threads + t) * N;
+      if (c < n && on) {
         if (a.g_post) {
 #pragma unroll
           for (int e = 0; e < N; ++e) d[i][e] = rf * (d[i][e] - y[i][e] * dot);
@@ -302,14 +426,35 @@ __global__ void __launch_bounds__(UPT * N > 8 ? 512 : 1024) norm_residual_bwd_ke
         store_n<T, N>((T*)a.df + base + c, d[i]);
       }
     }
-    if (!(a.g_post && a.g_pre)) __syncthreads();
+    if (TPR == 0 && !(a.g_post && a.g_pre)) __syncthreads();
   }
+  if constexpr (TPR > 0) {
+    float* sum = reinterpret_cast<float*>(ahead);   // [2][groups][plane]
+    const int groups = (int)per, group = threadIdx.x / (TPR > 0 ? TPR : 1);
 #pragma unroll
-  for (int i = 0; i < UPT; ++i) {
-    const int c = (i * blockDim.x + t) * N;
-    if (c < n) {
-      if (a.g_post) store_n<float, N>(a.part_post + (int64_t)blockIdx.x * n + c, dpost[i]);
-      if (a.g_pre) store_n<float, N>(a.part_pre + (int64_t)blockIdx.x * n + c, dpre[i]);
+    for (int i = 0; i < UPT; ++i) {
+      const int c = (i * threads + t) * N;
+      store_n<float, N>(sum + group * plane + c, dpost[i]);
+      store_n<float, N>(sum + (groups + group) * plane + c, dpre[i]);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < n; c += blockDim.x) {
+      float p = 0.f, q = 0.f;
+      for (int g = 0; g < groups; ++g) {
+        p += sum[g * plane + c];
+        q += sum[(groups + g) * plane + c];
+      }
+      if (a.g_post) a.part_post[(int64_t)blockIdx.x * n + c] = p;
+      if (a.g_pre) a.part_pre[(int64_t)blockIdx.x * n + c] = q;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < UPT; ++i) {
+      const int c = (i * threads + t) * N;
+      if (c < n) {
+        if (a.g_post) store_n<float, N>(a.part_post + (int64_t)blockIdx.x * n + c, dpost[i]);
+        if (a.g_pre) store_n<float, N>(a.part_pre + (int64_t)blockIdx.x * n + c, dpre[i]);
+      }
     }
   }
 }
@@ -339,7 +484,7 @@ __global__ void __launch_bounds__(1024) norm_residual_bwd_wide_kernel(const __gr
         ppre[c] = fmaf(d, y, ppre[c]);
         dot = fmaf(d * to_f<T>(gpre[c]), y, dot);
       }
-      dot = cta_sum(dot, part[0]) * inv_n;
+      dot = row_sum<0>(dot, part[0]) * inv_n;
     }
     const float rf = gpost ? a.rstd_f[row] : 1.f;
     float dot2 = 0.f;
@@ -355,8 +500,10 @@ __global__ void __launch_bounds__(1024) norm_residual_bwd_wide_kernel(const __gr
       const float g = gpost ? to_f<T>(gpost[c]) : 1.f;
       if (a.z) {
         const float z = to_f<T>(((const T*)a.z)[base + c]);
-        ((T*)a.dz)[base + c] = from_f<T>(d * (y * g) * gate_slope(z));
-        d *= gate_of(z);
+        float slope;
+        const float open = gate_of(z, &slope);
+        ((T*)a.dz)[base + c] = from_f<T>(d * (y * g) * slope);
+        d *= open;
       }
       if (gpost) {
         ppost[c] = fmaf(d, y, ppost[c]);
@@ -366,7 +513,7 @@ __global__ void __launch_bounds__(1024) norm_residual_bwd_wide_kernel(const __gr
       }
     }
     if (gpost) {
-      dot2 = cta_sum(dot2, part[1]) * inv_n;
+      dot2 = row_sum<0>(dot2, part[1]) * inv_n;
       for (int c = threadIdx.x; c < n; c += blockDim.x) {
         float d = a.dx[base + c] * a.s;
         if (a.z) d *= gate_of(to_f<T>(((const T*)a.z)[base + c]));
@@ -378,97 +525,167 @@ __global__ void __launch_bounds__(1024) norm_residual_bwd_wide_kernel(const __gr
   }
 }
 
-// dg[i] = the column sums of the CTAs' partials, in a fixed order; blockIdx.y
-// picks the gain.
-__global__ void __launch_bounds__(256) norm_residual_gain_kernel(const float* __restrict__ p0,
-                                                                 float* __restrict__ o0,
-                                                                 const float* __restrict__ p1,
-                                                                 float* __restrict__ o1, int nb,
-                                                                 int n) {
-  __shared__ float acc[8][33];
+// dg[i] = the column sums of the CTAs' partials, in a fixed order: 32 columns a
+// CTA, 32 warps over the partials; blockIdx.y picks the gain.
+__global__ void __launch_bounds__(1024) norm_residual_gain_kernel(const float* __restrict__ p0,
+                                                                  float* __restrict__ o0,
+                                                                  const float* __restrict__ p1,
+                                                                  float* __restrict__ o1, int nb,
+                                                                  int n) {
+  __shared__ float acc[32][33];
   const float* part = blockIdx.y ? p1 : p0;
   float* out = blockIdx.y ? o1 : o0;
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + tx;
   float s = 0.f;
-  if (i < n)
-    for (int b = ty; b < nb; b += 8) s += part[(int64_t)b * n + i];
+  if (i < n) {
+#pragma unroll 4
+    for (int b = ty; b < nb; b += 32) s += part[(int64_t)b * n + i];
+  }
   acc[ty][tx] = s;
   __syncthreads();
-  if (ty == 0 && i < n) {
-    float o = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) o += acc[w][tx];
-    out[i] = o;
-  }
+  s = warp_sum(acc[tx][ty]);   // column ty of this CTA
+  if (tx == 0 && blockIdx.x * 32 + ty < n) out[blockIdx.x * 32 + ty] = s;
 }
 
-// Units a thread and threads a CTA for rows of n elements; upt == 0: wide.
+// How rows of n elements are laid on threads.
 struct Shape {
-  int N, upt, threads;
+  int N, upt;      // units of N elements, units a thread; upt == 0: the wide kernel
+  int tpr;         // threads a row below 32 or of one warp; 0: the CTA
+  int threads;     // of the CTA
 };
 Shape shape_of(int n, int max_threads) {
   Shape s;
-  s.N = n % 8 == 0 ? 8 : 1;
+  s.N = n % 4 == 0 ? 4 : 1;
   const int units = n / s.N;
-  s.upt = s.N == 8 ? 2 : 8;
-  if (units <= 32) s.upt = 1;
-  s.threads = ((units + s.upt - 1) / s.upt + 31) / 32 * 32;
-  if (s.threads > max_threads) {
-    s.upt = 0;
-    s.threads = max_threads;
+  if (units <= 64) {              // up to two units a lane of one warp
+    s.upt = units <= 32 ? 1 : 2;
+    s.tpr = units <= 8 ? 8 : units <= 16 ? 16 : 32;
+    s.threads = 256;
+    return s;
   }
+  s.tpr = 0;
+  s.upt = units <= 512 ? 1 : units <= 1024 ? 2 : 4;
+  if (s.N == 1 && units > 512) s.upt = units <= 2048 ? 4 : 8;
+  s.threads = ((units + s.upt - 1) / s.upt + 31) / 32 * 32;
+  if (s.threads > max_threads) s.upt = 0, s.threads = 1024;
   return s;
 }
-int bwd_blocks(int64_t rows, const Shape& s) {
-  const int per_sm = std::max(1, 512 / s.threads);
-  return (int)std::min<int64_t>(rows, (int64_t)152 * per_sm);
+// CTAs a multiprocessor: what 2048 threads and the copies' shared memory allow.
+// The GB300's 152 multiprocessors are a constant here because the backward's
+// workspace, sized without a device, holds a partial row a CTA.
+constexpr int kSms = 152, kSmemPerSm = 220 * 1024;
+
+struct Plan {
+  Shape s;
+  bool ahead;
+  int smem, grid;
+};
+Plan plan_of(int64_t rows, const Shape& s, int row_bytes_per_el, bool ahead, int threads_per_sm) {
+  Plan p;
+  p.s = s;
+  p.ahead = false;
+  p.smem = 0;
+  const int per = p.s.tpr > 0 ? p.s.threads / p.s.tpr : 1;
+  int per_sm = std::max(1, threads_per_sm / p.s.threads);
+  const int64_t items = (rows + per - 1) / per;
+  const int stage = p.s.threads * p.s.upt * p.s.N * row_bytes_per_el;
+  if (ahead && p.s.tpr == 0 && p.s.upt > 0 && stage <= kSmemPerSm) {
+    p.ahead = true;
+    p.smem = stage;
+    per_sm = std::max(1, std::min(per_sm, kSmemPerSm / (stage + 1024)));
+  }
+  p.grid = (int)std::min<int64_t>(items, (int64_t)kSms * per_sm);
+  return p;
 }
 
 template <typename T, typename Ts>
-tsp_status fwd_t(const FwdArgs& a, cudaStream_t st) {
-  const Shape s = shape_of(a.n, 1024);
-  const int grid = (int)std::min<int64_t>(a.rows, (int64_t)num_sms() * std::max(1, 2048 / s.threads));
-  Prof prof("norm_residual_fwd", st);
-  if (s.upt == 0)
-    norm_residual_fwd_wide_kernel<T, Ts><<<grid, s.threads, 0, st>>>(a);
-  else if (s.N == 8 && s.upt == 1)
-    norm_residual_fwd_kernel<T, Ts, 8, 1><<<grid, s.threads, 0, st>>>(a);
-  else if (s.N == 8)
-    norm_residual_fwd_kernel<T, Ts, 8, 2><<<grid, s.threads, 0, st>>>(a);
-  else if (s.upt == 1)
-    norm_residual_fwd_kernel<T, Ts, 1, 1><<<grid, s.threads, 0, st>>>(a);
-  else
-    norm_residual_fwd_kernel<T, Ts, 1, 8><<<grid, s.threads, 0, st>>>(a);
+Plan fwd_plan(int64_t rows, int n) {
+  const Shape s = shape_of(n, 1024);
+  return plan_of(rows, s, 2 * sizeof(T) + sizeof(Ts), sizeof(T) * s.N >= 4, 2048);
+}
+template <typename T, typename Ts>
+Plan bwd_plan(int64_t rows, int n) {
+  const Shape s = shape_of(n, 512);   // 128 registers a thread: gain sums and a row
+  return plan_of(rows, s, 8 + sizeof(Ts) + 2 * sizeof(T), sizeof(T) * s.N >= 4, 1024);
+}
+
+template <typename K, typename A>
+tsp_status launch(K kernel, const Plan& p, const A& a, cudaStream_t st) {
+  if (p.smem > 47 * 1024)   // (the kernels' static shared memory counts too)
+    TSP_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem));
+  kernel<<<p.grid, p.s.threads, p.smem, st>>>(a);
   TSP_CUDA_TRY(cudaGetLastError());
   return TSP_OK;
 }
 
+template <typename T, typename Ts, int N, int UPT>
+tsp_status fwd_cta(const Plan& p, const FwdArgs& a, cudaStream_t st) {
+  if constexpr (sizeof(T) * N >= 4)
+    if (p.ahead) return launch(norm_residual_fwd_kernel<T, Ts, N, UPT, 0, true>, p, a, st);
+  return launch(norm_residual_fwd_kernel<T, Ts, N, UPT, 0, false>, p, a, st);
+}
+template <typename T, typename Ts, int N>
+tsp_status fwd_n(const Plan& p, const FwdArgs& a, cudaStream_t st) {
+  if (p.s.tpr == 8) return launch(norm_residual_fwd_kernel<T, Ts, N, 1, 8, false>, p, a, st);
+  if (p.s.tpr == 16) return launch(norm_residual_fwd_kernel<T, Ts, N, 1, 16, false>, p, a, st);
+  if (p.s.tpr == 32)
+    return p.s.upt == 1 ? launch(norm_residual_fwd_kernel<T, Ts, N, 1, 32, false>, p, a, st)
+                        : launch(norm_residual_fwd_kernel<T, Ts, N, 2, 32, false>, p, a, st);
+  if (p.s.upt == 1) return fwd_cta<T, Ts, N, 1>(p, a, st);
+  if constexpr (N == 4)
+    if (p.s.upt == 2) return fwd_cta<T, Ts, N, 2>(p, a, st);
+  if (p.s.upt == 4) return fwd_cta<T, Ts, N, 4>(p, a, st);
+  if constexpr (N == 1)
+    if (p.s.upt == 8) return fwd_cta<T, Ts, N, 8>(p, a, st);
+  return launch(norm_residual_fwd_wide_kernel<T, Ts>, p, a, st);
+}
 template <typename T, typename Ts>
-tsp_status bwd_t(const BwdArgs& a, float* dg_post, float* dg_pre, cudaStream_t st) {
-  const Shape s = shape_of(a.n, 512);
-  const int grid = bwd_blocks(a.rows, s);
-  const bool gains = a.g_post || a.g_pre;
-  Prof prof("norm_residual_bwd", st, gains ? 2 : 1);
-  if (s.upt == 0)
-    norm_residual_bwd_wide_kernel<T, Ts><<<grid, s.threads, 0, st>>>(a);
-  else if (s.N == 8 && s.upt == 1)
-    norm_residual_bwd_kernel<T, Ts, 8, 1><<<grid, s.threads, 0, st>>>(a);
-  else if (s.N == 8)
-    norm_residual_bwd_kernel<T, Ts, 8, 2><<<grid, s.threads, 0, st>>>(a);
-  else if (s.upt == 1)
-    norm_residual_bwd_kernel<T, Ts, 1, 1><<<grid, s.threads, 0, st>>>(a);
-  else
-    norm_residual_bwd_kernel<T, Ts, 1, 8><<<grid, s.threads, 0, st>>>(a);
-  TSP_CUDA_TRY(cudaGetLastError());
-  if (gains) {
-    const bool both = a.g_post && a.g_pre;
-    const float* p0 = a.g_post ? a.part_post : a.part_pre;
-    float* o0 = a.g_post ? dg_post : dg_pre;
-    norm_residual_gain_kernel<<<dim3((a.n + 31) / 32, both ? 2 : 1), 256, 0, st>>>(
-        p0, o0, a.part_pre, dg_pre, grid, a.n);
-    TSP_CUDA_TRY(cudaGetLastError());
+tsp_status fwd_t(const FwdArgs& a, cudaStream_t st) {
+  const Plan p = fwd_plan<T, Ts>(a.rows, a.n);
+  Prof prof("norm_residual_fwd", st);
+  return p.s.N == 4 ? fwd_n<T, Ts, 4>(p, a, st) : fwd_n<T, Ts, 1>(p, a, st);
+}
+
+template <typename T, typename Ts, int N, int UPT>
+tsp_status bwd_cta(const Plan& p, const BwdArgs& a, cudaStream_t st) {
+  if constexpr (sizeof(T) * N >= 4)
+    if (p.ahead) return launch(norm_residual_bwd_kernel<T, Ts, N, UPT, 0, true>, p, a, st);
+  return launch(norm_residual_bwd_kernel<T, Ts, N, UPT, 0, false>, p, a, st);
+}
+template <typename T, typename Ts, int N>
+tsp_status bwd_n(Plan p, const BwdArgs& a, cudaStream_t st) {
+  if (p.s.tpr > 0) {
+    p.smem = 2 * p.s.threads * p.s.upt * p.s.N * 4;   // the groups' gain gradients
+    if (p.s.tpr == 8) return launch(norm_residual_bwd_kernel<T, Ts, N, 1, 8, false>, p, a, st);
+    if (p.s.tpr == 16) return launch(norm_residual_bwd_kernel<T, Ts, N, 1, 16, false>, p, a, st);
+    return p.s.upt == 1 ? launch(norm_residual_bwd_kernel<T, Ts, N, 1, 32, false>, p, a, st)
+                        : launch(norm_residual_bwd_kernel<T, Ts, N, 2, 32, false>, p, a, st);
   }
+  if (p.s.upt == 1) return bwd_cta<T, Ts, N, 1>(p, a, st);
+  if constexpr (N == 4)
+    if (p.s.upt == 2) return bwd_cta<T, Ts, N, 2>(p, a, st);
+  if (p.s.upt == 4) return bwd_cta<T, Ts, N, 4>(p, a, st);
+  if constexpr (N == 1)
+    if (p.s.upt == 8) return bwd_cta<T, Ts, N, 8>(p, a, st);
+  return launch(norm_residual_bwd_wide_kernel<T, Ts>, p, a, st);
+}
+
+template <typename T, typename Ts>
+tsp_status bwd_t(BwdArgs a, float* dg_post, float* dg_pre, void* ws, cudaStream_t st) {
+  const Plan p = bwd_plan<T, Ts>(a.rows, a.n);
+  const bool gains = a.g_post || a.g_pre;
+  a.part_post = (float*)ws;
+  a.part_pre = (float*)ws + (int64_t)p.grid * a.n;
+  Prof prof("norm_residual_bwd", st, gains ? 2 : 1);
+  const tsp_status r = p.s.N == 4 ? bwd_n<T, Ts, 4>(p, a, st) : bwd_n<T, Ts, 1>(p, a, st);
+  if (r != TSP_OK || !gains) return r;
+  const bool both = a.g_post && a.g_pre;
+  const float* p0 = a.g_post ? a.part_post : a.part_pre;
+  float* o0 = a.g_post ? dg_post : dg_pre;
+  norm_residual_gain_kernel<<<dim3((a.n + 31) / 32, both ? 2 : 1), 1024, 0, st>>>(
+      p0, o0, a.part_pre, dg_pre, p.grid, a.n);
+  TSP_CUDA_TRY(cudaGetLastError());
   return TSP_OK;
 }
 
@@ -485,7 +702,11 @@ tsp_status launch_norm_residual_fwd(const void* f, const void* x, const void* ga
 }
 
 size_t norm_residual_bwd_ws_bytes(int64_t rows, int n) {
-  return (size_t)bwd_blocks(rows, shape_of(n, 512)) * n * 4 * 2;
+  // the types differ in how many CTAs fit a multiprocessor
+  typedef __nv_bfloat16 bf;
+  const int grid = std::max({bwd_plan<float, float>(rows, n).grid, bwd_plan<bf, float>(rows, n).grid,
+                             bwd_plan<bf, bf>(rows, n).grid});
+  return (size_t)grid * n * 4 * 2;
 }
 
 tsp_status launch_norm_residual_bwd(const float* dh, const float* db, const void* f,
@@ -494,13 +715,12 @@ tsp_status launch_norm_residual_bwd(const float* dh, const float* db, const void
                                     float* dx, void* df, void* dgate, float* dg_post, float* dg_pre,
                                     int64_t rows, int n, float scale, int dtype, int stream_dtype,
                                     void* ws, cudaStream_t st) {
-  float* part = (float*)ws;
-  const int64_t one = (int64_t)bwd_blocks(rows, shape_of(n, 512)) * n;
-  const BwdArgs a = {dh, db, f,  gate,  h,        g_post, g_pre, rstd_f, rstd_h,
-                     dx, df, dgate, part, part + one, rows, n,  scale};
-  if (dtype != TSP_BF16) return bwd_t<float, float>(a, dg_post, dg_pre, st);
-  return stream_dtype == TSP_BF16 ? bwd_t<__nv_bfloat16, __nv_bfloat16>(a, dg_post, dg_pre, st)
-                                  : bwd_t<__nv_bfloat16, float>(a, dg_post, dg_pre, st);
+  const BwdArgs a = {dh, db, f,     gate,    h,       g_post, g_pre, rstd_f, rstd_h,
+                     dx, df, dgate, nullptr, nullptr, rows,   n,     scale};
+  if (dtype != TSP_BF16) return bwd_t<float, float>(a, dg_post, dg_pre, ws, st);
+  return stream_dtype == TSP_BF16
+             ? bwd_t<__nv_bfloat16, __nv_bfloat16>(a, dg_post, dg_pre, ws, st)
+             : bwd_t<__nv_bfloat16, float>(a, dg_post, dg_pre, ws, st);
 }
 
 }  // namespace tsp
