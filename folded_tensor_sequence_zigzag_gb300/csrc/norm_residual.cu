@@ -116,7 +116,8 @@ struct FwdArgs {
 // into the places it has just read, and arrive while this row is worked on.
 // Without that the loads of a row wait for the barriers of the one before.
 template <typename T, typename Ts, int N, int UPT, int TPR, bool AHEAD>
-__global__ void __launch_bounds__(1024) norm_residual_fwd_kernel(const __grid_constant__ FwdArgs a) {
+__global__ void __launch_bounds__(UPT * N < 8 || UPT == 2 ? 512 : 1024, UPT * N < 8 || UPT == 2 ? 3 : 1)
+    norm_residual_fwd_kernel(const __grid_constant__ FwdArgs a) {
   __shared__ float part[2][32];
   extern __shared__ __align__(16) uint8_t ahead[];
   const int n = a.n;
@@ -320,12 +321,22 @@ __global__ void __launch_bounds__(512, UPT * N <= 8 ? 2 : 1) norm_residual_bwd_k
     }
   };
   issue(blockIdx.x);
+  const int64_t row_first = (int64_t)blockIdx.x * per + (TPR > 0 ? threadIdx.x / (TPR > 0 ? TPR : 1) : 0);
+  // a row's inverse norms are loaded with the copies for it, a row ahead
+  float rf_next = 1.f, rh_next = 0.f;
+  auto load_rstd = [&](int64_t row) {
+    if (row < a.rows) {
+      if (a.g_post) rf_next = a.rstd_f[row];
+      if (a.g_pre) rh_next = a.rstd_h[row];
+    }
+  };
+  load_rstd(row_first);
   for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < a.rows; row0 += (int64_t)gridDim.x * per) {
     const int64_t row = TPR > 0 ? row0 + threadIdx.x / (TPR > 0 ? TPR : 1) : row0;
     const bool on = TPR == 0 || row < a.rows;
     const int64_t base = row * n;
-    const float rf = a.g_post && on ? a.rstd_f[row] : 1.f;
-    const float rh = a.g_pre && on ? a.rstd_h[row] : 0.f;
+    const float rf = rf_next, rh = rh_next;
+    load_rstd(row + (int64_t)gridDim.x * per);
     if constexpr (AHEAD) copies_wait();
     const float* dhp = AHEAD ? dh_in : a.dh + base;
     const float* dbp = AHEAD ? db_in : a.db + base;
@@ -602,7 +613,9 @@ Plan plan_of(int64_t rows, const Shape& s, int row_bytes_per_el, bool ahead, int
 template <typename T, typename Ts>
 Plan fwd_plan(int64_t rows, int n) {
   const Shape s = shape_of(n, 1024);
-  return plan_of(rows, s, 2 * sizeof(T) + sizeof(Ts), sizeof(T) * s.N >= 4, 2048);
+  // 40 registers a thread up to 8 elements, 64 above
+  return plan_of(rows, s, 2 * sizeof(T) + sizeof(Ts), sizeof(T) * s.N >= 4,
+                 s.upt * s.N < 8 || s.upt == 2 ? 1536 : 1024);
 }
 template <typename T, typename Ts>
 Plan bwd_plan(int64_t rows, int n) {
