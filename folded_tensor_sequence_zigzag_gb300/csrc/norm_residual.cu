@@ -55,12 +55,75 @@ __device__ __forceinline__ void store_n(T* p, const float (&v)[N]) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
+// Elementwise on N values, two at a time where there are four: the .f32x2 forms
+// round as the scalar ones and take half the issue slots, of which the backward
+// needs most.
+template <int N, typename F2, typename F1>
+__device__ __forceinline__ void pairs(F2 two, F1 one) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) two(e);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e) one(e);
+  }
+}
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\t"
+      "mov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+template <int N>   // a = a * b
+__device__ __forceinline__ void mul_n(float (&a)[N], const float (&b)[N]) {
+  pairs<N>([&](int e) {
+    const float2 r = fmul2(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
+    a[e] = r.x; a[e + 1] = r.y;
+  }, [&](int e) { a[e] *= b[e]; });
+}
+template <int N>   // a = a * s
+__device__ __forceinline__ void mul_n(float (&a)[N], float s) {
+  pairs<N>([&](int e) {
+    const float2 r = fmul2(make_float2(a[e], a[e + 1]), make_float2(s, s));
+    a[e] = r.x; a[e + 1] = r.y;
+  }, [&](int e) { a[e] *= s; });
+}
+template <int N>   // c = a * b + c
+__device__ __forceinline__ void fma_n(float (&c)[N], const float (&a)[N], const float (&b)[N]) {
+  pairs<N>([&](int e) {
+    const float2 r = ffma2(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]),
+                           make_float2(c[e], c[e + 1]));
+    c[e] = r.x; c[e + 1] = r.y;
+  }, [&](int e) { c[e] = fmaf(a[e], b[e], c[e]); });
+}
+template <int N>   // c = a * s + c
+__device__ __forceinline__ void fma_n(float (&c)[N], const float (&a)[N], float s) {
+  pairs<N>([&](int e) {
+    const float2 r = ffma2(make_float2(a[e], a[e + 1]), make_float2(s, s), make_float2(c[e], c[e + 1]));
+    c[e] = r.x; c[e + 1] = r.y;
+  }, [&](int e) { c[e] = fmaf(a[e], s, c[e]); });
+}
+template <int N>
+__device__ __forceinline__ float total(const float (&v)[N]) {
+  float t = v[0];
+#pragma unroll
+  for (int e = 1; e < N; ++e) t += v[e];
+  return t;
+}
+
 // sigmoid(z) and its derivative from e = exp(-|z|), which neither overflows nor
 // cancels: sigmoid(|z|) = 1 / (1 + e), sigmoid(-|z|) = e / (1 + e).  e is 2^x of
 // the rounded x = -|z| log2(e): off by |z| + 2 half spacings, which the sigmoid
 // has only where it is e itself, near a closed gate.
 __device__ __forceinline__ float gate_of(float z, float* slope) {
-  const float e = ex2_approx(-1.4426950408889634f * fabsf(z)), r = __fdividef(1.f, 1.f + e);
+  const float e = ex2_approx(-1.4426950408889634f * fabsf(z));
+  float r;   // 1 / (1 + e): 1 <= 1 + e <= 2, one half spacing off at most
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   *slope = e * r * r;
   return z >= 0.f ? r : e * r;   // (a NaN gives NaN: e is one)
 }
@@ -93,10 +156,27 @@ template <typename T, int N>
 __device__ __forceinline__ void copy_ahead(T* dst, const T* src) {
   constexpr int B = sizeof(T) * N;
   static_assert(B == 4 || B == 8 || B == 16, "a copy is 4, 8 or 16 bytes");
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(B)
-               : "memory");
+  // 16 bytes go past L1, which then keeps the gains (there is no such form for 4 and 8)
+  if constexpr (B == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(B)
+                 : "memory");
 }
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// until at most `LEFT` of the groups committed last are on their way
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// The columns of a thread: UPT units of N, unit i at first + i * 32 * N, those of
+// a warp next to each other.
+template <int N, int UPT, int TPR>
+__device__ __forceinline__ int first_col() {
+  if constexpr (TPR > 0) return (int)(threadIdx.x % TPR) * N;
+  return (int)((threadIdx.x >> 5) * UPT * 32 + (threadIdx.x & 31)) * N;
+}
 
 struct FwdArgs {
   const void *f, *x, *z, *g_post, *g_pre;
@@ -107,8 +187,7 @@ struct FwdArgs {
   float s, eps;
 };
 
-// The row in registers: UPT units of N elements a thread, unit i of thread t of
-// the row at (i * threads + t) * N, so that a warp's accesses are contiguous.
+// The row in registers (first_col).
 //   TPR > 0: TPR threads a row, 256 / TPR rows a CTA (short rows);
 //   TPR = 0: a CTA a row.
 // AHEAD (TPR = 0): once every thread has its part of a row in registers (the
@@ -120,104 +199,108 @@ __global__ void __launch_bounds__(UPT * N < 8 || UPT == 2 ? 512 : 1024, UPT * N 
     norm_residual_fwd_kernel(const __grid_constant__ FwdArgs a) {
   __shared__ float part[2][32];
   extern __shared__ __align__(16) uint8_t ahead[];
-  const int n = a.n;
-  const int t = TPR > 0 ? threadIdx.x % (TPR > 0 ? TPR : 1) : threadIdx.x;
-  const int threads = TPR > 0 ? TPR : blockDim.x;
+  constexpr int kStep = 32 * N;
+  const int n = a.n, c0 = first_col<N, UPT, TPR>();
+  const int group = TPR > 0 ? threadIdx.x / (TPR > 0 ? TPR : 1) : 0;
   const int64_t per = TPR > 0 ? blockDim.x / TPR : 1;
   const float inv_n = 1.f / (float)n;
-  // f, z, x in planes of threads * UPT units
-  const int plane = threads * UPT * N;
-  T* const f_in = (T*)ahead;
-  T* const z_in = f_in + plane;
-  Ts* const x_in = (Ts*)(z_in + plane);
+  // a warp's f, z, x next to each other, at constant distances
+  constexpr int kWarp = UPT * kStep;
+  uint8_t* const mine = ahead + (threadIdx.x >> 5) * kWarp * (2 * sizeof(T) + sizeof(Ts));
+  T* const f_in = (T*)mine + (threadIdx.x & 31) * N;
+  T* const z_in = f_in + kWarp;
+  Ts* const x_in = (Ts*)(mine + 2 * sizeof(T) * kWarp) + (threadIdx.x & 31) * N;
   auto issue = [&](int64_t row) {
     if constexpr (AHEAD) {
       if (row < a.rows) {
+        const int64_t at = row * n + c0;
+        const T *f = (const T*)a.f + at, *z = (const T*)a.z + at;
+        const Ts* x = (const Ts*)a.x + at;
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
-          const int u = (i * threads + t) * N;
-          if (u < n) {
-            copy_ahead<T, N>(f_in + u, (const T*)a.f + row * n + u);
-            if (a.z) copy_ahead<T, N>(z_in + u, (const T*)a.z + row * n + u);
-            copy_ahead<Ts, N>(x_in + u, (const Ts*)a.x + row * n + u);
+          if (c0 + i * kStep < n) {
+            copy_ahead<T, N>(f_in + i * kStep, f + i * kStep);
+            if (a.z) copy_ahead<T, N>(z_in + i * kStep, z + i * kStep);
+            copy_ahead<Ts, N>(x_in + i * kStep, x + i * kStep);
           }
         }
       }
+      copies_commit();
     }
   };
   issue(blockIdx.x);
   for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < a.rows; row0 += (int64_t)gridDim.x * per) {
-    const int64_t row = TPR > 0 ? row0 + threadIdx.x / (TPR > 0 ? TPR : 1) : row0;
-    const bool on = TPR == 0 || row < a.rows;
-    const int64_t base = row * n;
-    if constexpr (AHEAD) copies_wait();
-    const T* fp = AHEAD ? f_in : (const T*)a.f + base;
-    const T* zp = AHEAD ? z_in : (const T*)a.z + base;
-    const Ts* xp = AHEAD ? x_in : (const Ts*)a.x + base;
+    const int64_t row = row0 + group;
+    const int nrow = TPR == 0 || row < a.rows ? n : 0;   // (a group past the last row does nothing)
+    const int64_t at = row * n + c0;
+    if constexpr (AHEAD) copies_wait<0>();
+    const T* fp = AHEAD ? f_in : (const T*)a.f + at;
+    const T* zp = AHEAD ? z_in : (const T*)a.z + at;
+    const Ts* xp = AHEAD ? x_in : (const Ts*)a.x + at;
     float v[UPT][N];
     Unit<Ts, N> q[UPT];
     Unit<T, N> z[UPT];
-    float ss = 0.f;
+    float ss[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) ss[e] = 0.f;
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      const int c = (i * threads + t) * N;
 #pragma unroll
       for (int e = 0; e < N; ++e) v[i][e] = 0.f;
-      if (c < n && on) {
-        load_n<T, N>(fp + c, v[i]);
-        q[i].load(xp + c);
-        if (a.z) z[i].load(zp + c);
+      if (c0 + i * kStep < nrow) {
+        load_n<T, N>(fp + i * kStep, v[i]);
+        q[i].load(xp + i * kStep);
+        if (a.z) z[i].load(zp + i * kStep);
       }
     }
     float r = 1.f;
     if (a.g_post) {
 #pragma unroll
-      for (int i = 0; i < UPT; ++i)
-#pragma unroll
-        for (int e = 0; e < N; ++e) ss = fmaf(v[i][e], v[i][e], ss);
-      r = rsqrtf(row_sum<TPR>(ss, part[0]) * inv_n + a.eps);
-      if (t == 0 && on && a.rstd_f) a.rstd_f[row] = r;
+      for (int i = 0; i < UPT; ++i) fma_n<N>(ss, v[i], v[i]);
+      r = rsqrtf(row_sum<TPR>(total<N>(ss), part[0]) * inv_n + a.eps);
+      if (c0 == 0 && nrow && a.rstd_f) a.rstd_f[row] = r;
     } else if (AHEAD) {
       __syncthreads();
     }
     issue(row + gridDim.x);
-    ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) ss[e] = 0.f;
+    Ts* h = (Ts*)a.h + at;
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      const int c = (i * threads + t) * N;
-      if (c < n && on) {
+      if (c0 + i * kStep < nrow) {
         float w[N];
         if (a.g_post) {
-          load_n<T, N>((const T*)a.g_post + c, w);
-#pragma unroll
-          for (int e = 0; e < N; ++e) v[i][e] *= r * w[e];
+          load_n<T, N>((const T*)a.g_post + c0 + i * kStep, w);
+          mul_n<N>(w, r);
+          mul_n<N>(v[i], w);
         }
         if (a.z) {
           z[i].get(w);
 #pragma unroll
-          for (int e = 0; e < N; ++e) v[i][e] *= gate_of(w[e]);
+          for (int e = 0; e < N; ++e) w[e] = gate_of(w[e]);
+          mul_n<N>(v[i], w);
         }
         q[i].get(w);
+        fma_n<N>(w, v[i], a.s);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          v[i][e] = to_f<Ts>(from_f<Ts>(fmaf(a.s, v[i][e], w[e])));
-          ss = fmaf(v[i][e], v[i][e], ss);
-        }
-        store_n<Ts, N>((Ts*)a.h + base + c, v[i]);
+        for (int e = 0; e < N; ++e) v[i][e] = to_f<Ts>(from_f<Ts>(w[e]));
+        fma_n<N>(ss, v[i], v[i]);
+        store_n<Ts, N>(h + i * kStep, v[i]);
       }
     }
     if (a.g_pre) {
-      r = rsqrtf(row_sum<TPR>(ss, part[1]) * inv_n + a.eps);
-      if (t == 0 && on && a.rstd_h) a.rstd_h[row] = r;
+      r = rsqrtf(row_sum<TPR>(total<N>(ss), part[1]) * inv_n + a.eps);
+      if (c0 == 0 && nrow && a.rstd_h) a.rstd_h[row] = r;
+      T* b = (T*)a.b + at;
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
-        const int c = (i * threads + t) * N;
-        if (c < n && on) {
+        if (c0 + i * kStep < nrow) {
           float g[N];
-          load_n<T, N>((const T*)a.g_pre + c, g);
-#pragma unroll
-          for (int e = 0; e < N; ++e) g[e] *= v[i][e] * r;
-          store_n<T, N>((T*)a.b + base + c, g);
+          load_n<T, N>((const T*)a.g_pre + c0 + i * kStep, g);
+          mul_n<N>(v[i], r);
+          mul_n<N>(g, v[i]);
+          store_n<T, N>(b + i * kStep, g);
         }
       }
     }
@@ -277,51 +360,86 @@ struct BwdArgs {
 
 // The same layout and the same copies ahead (dh, db, h, f, z).  A thread's
 // columns are the same in every row, so its share of the gain gradients stays
-// in registers until the CTA's last row; with several rows a CTA the groups'
-// shares are added in shared memory in the order of the groups.
+// with it until the CTA's last row: in registers, or with AHEAD, where 64
+// registers a thread let two CTAs of 512 run on a multiprocessor, in its own
+// places in shared memory.  With several rows a CTA the groups' shares are added
+// in the order of the groups.
 template <typename T, typename Ts, int N, int UPT, int TPR, bool AHEAD>
 __global__ void __launch_bounds__(512, UPT * N <= 8 ? 2 : 1) norm_residual_bwd_kernel(const __grid_constant__ BwdArgs a) {
   __shared__ float part[2][32];
   extern __shared__ __align__(16) uint8_t ahead[];
-  const int n = a.n;
-  const int t = TPR > 0 ? threadIdx.x % (TPR > 0 ? TPR : 1) : threadIdx.x;
-  const int threads = TPR > 0 ? TPR : blockDim.x;
+  constexpr int kStep = 32 * N;
+  const int n = a.n, c0 = first_col<N, UPT, TPR>();
+  const int group = TPR > 0 ? threadIdx.x / (TPR > 0 ? TPR : 1) : 0;
   const int64_t per = TPR > 0 ? blockDim.x / TPR : 1;
   const float inv_n = 1.f / (float)n;
-  float dpost[UPT][N], dpre[UPT][N];
+  // a warp's dh, db (fp32), h, f, z and its gain sums next to each other, at
+  // constant distances
+  constexpr int kWarp = UPT * kStep;
+  uint8_t* const mine = ahead + (threadIdx.x >> 5) * kWarp * (16 + sizeof(Ts) + 2 * sizeof(T));
+  float* const sum_in = (float*)(mine + (8 + sizeof(Ts) + 2 * sizeof(T)) * kWarp) + (threadIdx.x & 31) * N;
+  float dpost[AHEAD ? 1 : UPT][N], dpre[AHEAD ? 1 : UPT][N];
 #pragma unroll
-  for (int i = 0; i < UPT; ++i)
+  for (int i = 0; i < UPT; ++i) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) dpost[i][e] = dpre[i][e] = 0.f;
-  // dh, db (fp32), h, f, z in planes of threads * UPT units
-  const int plane = threads * UPT * N;
-  float* const dh_in = (float*)ahead;
-  float* const db_in = dh_in + plane;
-  Ts* const h_in = (Ts*)(db_in + plane);
-  T* const f_in = (T*)(h_in + plane);
-  T* const z_in = f_in + plane;
-  auto issue = [&](int64_t row) {
+    for (int e = 0; e < N; ++e) dpost[AHEAD ? 0 : i][e] = dpre[AHEAD ? 0 : i][e] = 0.f;
     if constexpr (AHEAD) {
-      if (row < a.rows) {
+      store_n<float, N>(sum_in + i * kStep, dpost[0]);
+      store_n<float, N>(sum_in + kWarp + i * kStep, dpost[0]);
+    }
+  }
+  // c += a * b, in registers or in the thread's place in shared memory
+  auto add_to = [&](int i, bool post, const float (&x)[N], const float (&y)[N]) {
+    if constexpr (AHEAD) {
+      float* at = sum_in + (post ? kWarp : 0) + i * kStep;
+      float c[N];
+      load_n<float, N>(at, c);
+      fma_n<N>(c, x, y);
+      store_n<float, N>(at, c);
+    } else {
+      fma_n<N>(post ? dpost[i] : dpre[i], x, y);
+    }
+  };
+  float* const dh_in = (float*)mine + (threadIdx.x & 31) * N;
+  float* const db_in = dh_in + kWarp;
+  Ts* const h_in = (Ts*)(mine + 8 * kWarp) + (threadIdx.x & 31) * N;
+  T* const f_in = (T*)(mine + (8 + sizeof(Ts)) * kWarp) + (threadIdx.x & 31) * N;
+  T* const z_in = f_in + kWarp;
+  // The copies of a row go in two groups: db and h, whose places are free after
+  // the first sum's barrier, and dh, f, z, free after the second's.
+  auto issue_pre = [&](int64_t row) {
+    if constexpr (AHEAD) {
+      if (row < a.rows && a.g_pre) {
+        const int64_t at = row * n + c0;
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
-          const int u = (i * threads + t) * N;
-          if (u < n) {
-            const int64_t at = row * n + u;
-            if (a.dh) copy_ahead<float, N>(dh_in + u, a.dh + at);
-            if (a.g_pre) {
-              copy_ahead<float, N>(db_in + u, a.db + at);
-              copy_ahead<Ts, N>(h_in + u, (const Ts*)a.h + at);
-            }
-            copy_ahead<T, N>(f_in + u, (const T*)a.f + at);
-            if (a.z) copy_ahead<T, N>(z_in + u, (const T*)a.z + at);
+          if (c0 + i * kStep < n) {
+            copy_ahead<float, N>(db_in + i * kStep, a.db + at + i * kStep);
+            copy_ahead<Ts, N>(h_in + i * kStep, (const Ts*)a.h + at + i * kStep);
           }
         }
       }
+      copies_commit();
     }
   };
-  issue(blockIdx.x);
-  const int64_t row_first = (int64_t)blockIdx.x * per + (TPR > 0 ? threadIdx.x / (TPR > 0 ? TPR : 1) : 0);
+  auto issue_post = [&](int64_t row) {
+    if constexpr (AHEAD) {
+      if (row < a.rows) {
+        const int64_t at = row * n + c0;
+#pragma unroll
+        for (int i = 0; i < UPT; ++i) {
+          if (c0 + i * kStep < n) {
+            if (a.dh) copy_ahead<float, N>(dh_in + i * kStep, a.dh + at + i * kStep);
+            copy_ahead<T, N>(f_in + i * kStep, (const T*)a.f + at + i * kStep);
+            if (a.z) copy_ahead<T, N>(z_in + i * kStep, (const T*)a.z + at + i * kStep);
+          }
+        }
+      }
+      copies_commit();
+    }
+  };
+  issue_pre(blockIdx.x);
+  issue_post(blockIdx.x);
   // a row's inverse norms are loaded with the copies for it, a row ahead
   float rf_next = 1.f, rh_next = 0.f;
   auto load_rstd = [&](int64_t row) {
@@ -330,130 +448,123 @@ __global__ void __launch_bounds__(512, UPT * N <= 8 ? 2 : 1) norm_residual_bwd_k
       if (a.g_pre) rh_next = a.rstd_h[row];
     }
   };
-  load_rstd(row_first);
+  load_rstd((int64_t)blockIdx.x * per + group);
   for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < a.rows; row0 += (int64_t)gridDim.x * per) {
-    const int64_t row = TPR > 0 ? row0 + threadIdx.x / (TPR > 0 ? TPR : 1) : row0;
-    const bool on = TPR == 0 || row < a.rows;
-    const int64_t base = row * n;
+    const int64_t row = row0 + group;
+    const int nrow = TPR == 0 || row < a.rows ? n : 0;   // (a group past the last row does nothing)
+    const int64_t at = row * n + c0;
     const float rf = rf_next, rh = rh_next;
     load_rstd(row + (int64_t)gridDim.x * per);
-    if constexpr (AHEAD) copies_wait();
-    const float* dhp = AHEAD ? dh_in : a.dh + base;
-    const float* dbp = AHEAD ? db_in : a.db + base;
-    const Ts* hp = AHEAD ? h_in : (const Ts*)a.h + base;
-    const T* fp = AHEAD ? f_in : (const T*)a.f + base;
-    const T* zp = AHEAD ? z_in : (const T*)a.z + base;
+    if constexpr (AHEAD) copies_wait<1>();   // db and h are there
+    const float* dhp = AHEAD ? dh_in : a.dh + at;
+    const float* dbp = AHEAD ? db_in : a.db + at;
+    const Ts* hp = AHEAD ? h_in : (const Ts*)a.h + at;
+    const T* fp = AHEAD ? f_in : (const T*)a.f + at;
+    const T* zp = AHEAD ? z_in : (const T*)a.z + at;
     float d[UPT][N];
-    Unit<T, N> fu[UPT], zu[UPT];
+    float dot[N];
 #pragma unroll
-    for (int i = 0; i < UPT; ++i) {
-      const int c = (i * threads + t) * N;
-#pragma unroll
-      for (int e = 0; e < N; ++e) d[i][e] = 0.f;
-      if (c < n && on) {
-        if (a.dh) load_n<float, N>(dhp + c, d[i]);
-        fu[i].load(fp + c);
-        if (a.z) zu[i].load(zp + c);
-      }
-    }
+    for (int e = 0; e < N; ++e) dot[e] = 0.f;
     if (a.g_pre) {
-      float y[UPT][N], gd[UPT][N], dot = 0.f;
+      float y[UPT][N], gd[UPT][N];
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
-        const int c = (i * threads + t) * N;
-        if (c < n && on) {
+        if (c0 + i * kStep < nrow) {
           float g[N];
-          load_n<Ts, N>(hp + c, y[i]);
-          load_n<float, N>(dbp + c, gd[i]);
-          load_n<T, N>((const T*)a.g_pre + c, g);
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            y[i][e] *= rh;
-            dpre[i][e] = fmaf(gd[i][e], y[i][e], dpre[i][e]);
-            gd[i][e] *= g[e];
-            dot = fmaf(gd[i][e], y[i][e], dot);
-          }
+          load_n<Ts, N>(hp + i * kStep, y[i]);
+          load_n<float, N>(dbp + i * kStep, gd[i]);
+          load_n<T, N>((const T*)a.g_pre + c0 + i * kStep, g);
+          mul_n<N>(y[i], rh);
+          add_to(i, false, gd[i], y[i]);
+          mul_n<N>(gd[i], g);
+          fma_n<N>(dot, gd[i], y[i]);
         }
       }
-      dot = row_sum<TPR>(dot, part[0]) * inv_n;
-      issue(row + gridDim.x);
+      const float mean = row_sum<TPR>(total<N>(dot), part[0]) * inv_n;
+      if constexpr (AHEAD) copies_wait<0>();   // dh, f and z too
+      issue_pre(row + gridDim.x);
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
-        const int c = (i * threads + t) * N;
-        if (c < n && on) {
 #pragma unroll
-          for (int e = 0; e < N; ++e) d[i][e] = fmaf(rh, gd[i][e] - y[i][e] * dot, d[i][e]);
+        for (int e = 0; e < N; ++e) d[i][e] = 0.f;
+        if (c0 + i * kStep < nrow) {
+          if (a.dh) load_n<float, N>(dhp + i * kStep, d[i]);
+          fma_n<N>(gd[i], y[i], -mean);
+          fma_n<N>(d[i], gd[i], rh);
         }
       }
     } else {
-      if (AHEAD) __syncthreads();
-      issue(row + gridDim.x);
+      if constexpr (AHEAD) copies_wait<0>();
+      issue_pre(row + gridDim.x);   // (an empty group)
+#pragma unroll
+      for (int i = 0; i < UPT; ++i)
+        if (c0 + i * kStep < nrow) load_n<float, N>(dhp + i * kStep, d[i]);
     }
-    float y[UPT][N], dot = 0.f;
+    float y[UPT][N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) dot[e] = 0.f;
+    float* dx = a.dx + at;
+    T* dz = (T*)a.dz + at;
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      const int c = (i * threads + t) * N;
-      if (c < n && on) {
-        store_n<float, N>(a.dx + base + c, d[i]);
-        fu[i].get(y[i]);
+      if (c0 + i * kStep < nrow) {
+        store_n<float, N>(dx + i * kStep, d[i]);
+        load_n<T, N>(fp + i * kStep, y[i]);
+        mul_n<N>(y[i], rf);
+        mul_n<N>(d[i], a.s);
         float g[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          y[i][e] *= rf;
-          d[i][e] *= a.s;
-          g[e] = 1.f;
-        }
-        if (a.g_post) load_n<T, N>((const T*)a.g_post + c, g);
+        if (a.g_post) load_n<T, N>((const T*)a.g_post + c0 + i * kStep, g);
         if (a.z) {
-          float z[N], dz[N], slope;
-          zu[i].get(z);
+          float open[N], slope[N];
+          load_n<T, N>(zp + i * kStep, open);
 #pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const float open = gate_of(z[e], &slope);
-            dz[e] = d[i][e] * (y[i][e] * g[e]) * slope;
-            d[i][e] *= open;
-          }
-          store_n<T, N>((T*)a.dz + base + c, dz);
+          for (int e = 0; e < N; ++e) open[e] = gate_of(open[e], &slope[e]);
+          mul_n<N>(slope, d[i]);
+          mul_n<N>(slope, y[i]);
+          if (a.g_post) mul_n<N>(slope, g);
+          store_n<T, N>(dz + i * kStep, slope);
+          mul_n<N>(d[i], open);
         }
         if (a.g_post) {
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            dpost[i][e] = fmaf(d[i][e], y[i][e], dpost[i][e]);
-            d[i][e] *= g[e];
-            dot = fmaf(d[i][e], y[i][e], dot);
-          }
+          add_to(i, true, d[i], y[i]);
+          mul_n<N>(d[i], g);
+          fma_n<N>(dot, d[i], y[i]);
         }
       }
     }
-    if (a.g_post) dot = row_sum<TPR>(dot, part[1]) * inv_n;
+    T* df = (T*)a.df + at;
+    if (a.g_post) {
+      const float mean = row_sum<TPR>(total<N>(dot), part[1]) * inv_n;
+      issue_post(row + gridDim.x);
 #pragma unroll
-    for (int i = 0; i < UPT; ++i) {
-      const int c = (i * threads + t) * N;
-      if (c < n && on) {
-        if (a.g_post) {
-#pragma unroll
-          for (int e = 0; e < N; ++e) d[i][e] = rf * (d[i][e] - y[i][e] * dot);
+      for (int i = 0; i < UPT; ++i) {
+        if (c0 + i * kStep < nrow) {
+          fma_n<N>(d[i], y[i], -mean);
+          mul_n<N>(d[i], rf);
         }
-        store_n<T, N>((T*)a.df + base + c, d[i]);
       }
     }
+#pragma unroll
+    for (int i = 0; i < UPT; ++i)
+      if (c0 + i * kStep < nrow) store_n<T, N>(df + i * kStep, d[i]);
     if (TPR == 0 && !(a.g_post && a.g_pre)) __syncthreads();
+    if (!a.g_post) issue_post(row + gridDim.x);
   }
   if constexpr (TPR > 0) {
-    float* sum = reinterpret_cast<float*>(ahead);   // [2][groups][plane]
-    const int groups = (int)per, group = threadIdx.x / (TPR > 0 ? TPR : 1);
+    constexpr int kPlane = TPR * UPT * N;
+    float* sum = reinterpret_cast<float*>(ahead);   // [2][groups][kPlane]
+    const int groups = (int)per;
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      const int c = (i * threads + t) * N;
-      store_n<float, N>(sum + group * plane + c, dpost[i]);
-      store_n<float, N>(sum + (groups + group) * plane + c, dpre[i]);
+      store_n<float, N>(sum + group * kPlane + c0 + i * kStep, dpost[i]);
+      store_n<float, N>(sum + (groups + group) * kPlane + c0 + i * kStep, dpre[i]);
     }
     __syncthreads();
     for (int c = threadIdx.x; c < n; c += blockDim.x) {
       float p = 0.f, q = 0.f;
       for (int g = 0; g < groups; ++g) {
-        p += sum[g * plane + c];
-        q += sum[(groups + g) * plane + c];
+        p += sum[g * kPlane + c];
+        q += sum[(groups + g) * kPlane + c];
       }
       if (a.g_post) a.part_post[(int64_t)blockIdx.x * n + c] = p;
       if (a.g_pre) a.part_pre[(int64_t)blockIdx.x * n + c] = q;
@@ -461,10 +572,14 @@ __global__ void __launch_bounds__(512, UPT * N <= 8 ? 2 : 1) norm_residual_bwd_k
   } else {
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      const int c = (i * threads + t) * N;
-      if (c < n) {
-        if (a.g_post) store_n<float, N>(a.part_post + (int64_t)blockIdx.x * n + c, dpost[i]);
-        if (a.g_pre) store_n<float, N>(a.part_pre + (int64_t)blockIdx.x * n + c, dpre[i]);
+      if (c0 + i * kStep < n) {
+        const int64_t o = (int64_t)blockIdx.x * n + c0 + i * kStep;
+        if constexpr (AHEAD) {
+          load_n<float, N>(sum_in + kWarp + i * kStep, dpost[0]);
+          load_n<float, N>(sum_in + i * kStep, dpre[0]);
+        }
+        if (a.g_post) store_n<float, N>(a.part_post + o, dpost[AHEAD ? 0 : i]);
+        if (a.g_pre) store_n<float, N>(a.part_pre + o, dpre[AHEAD ? 0 : i]);
       }
     }
   }
@@ -620,7 +735,8 @@ Plan fwd_plan(int64_t rows, int n) {
 template <typename T, typename Ts>
 Plan bwd_plan(int64_t rows, int n) {
   const Shape s = shape_of(n, 512);   // 128 registers a thread: gain sums and a row
-  return plan_of(rows, s, 8 + sizeof(Ts) + 2 * sizeof(T), sizeof(T) * s.N >= 4, 1024);
+  // (the inputs of a row, and two gain sums)
+  return plan_of(rows, s, 16 + sizeof(Ts) + 2 * sizeof(T), sizeof(T) * s.N >= 4, 1024);
 }
 
 template <typename K, typename A>
