@@ -1033,7 +1033,7 @@ tsp_status tsp_embed_fwd(const void* ids, int32_t id_bytes, const void* table, v
 }
 
 size_t tsp_embed_bwd_workspace_bytes(int64_t S, int64_t V, int32_t d) {
-  return check_embed(S, 1, V, d) == TSP_OK ? embed_bwd_ws_bytes(S, V, d) : 0;
+  return check_embed(S, 1, V, d) == TSP_OK ? embed_bwd_ws_bytes(S, d) : 0;
 }
 
 tsp_status tsp_embed_bwd(const void* ids, int32_t id_bytes, const void* dx_z, int32_t dx_dtype,
@@ -1043,7 +1043,7 @@ tsp_status tsp_embed_bwd(const void* ids, int32_t id_bytes, const void* dx_z, in
   if (r != TSP_OK) return r;
   if (!ids_ok(ids, id_bytes) || !al16(dx_z) || !al16(dtable) || !al16(ws) ||
       !std::isfinite(scale) || (dx_dtype != TSP_F32 && dx_dtype != TSP_BF16) ||
-      ws_bytes < embed_bwd_ws_bytes(S, V, d))
+      ws_bytes < embed_bwd_ws_bytes(S, d))
     return TSP_ERR_INVALID_ARG;
   return launch_embed_bwd(ids, id_bytes, dx_z, dx_dtype, dtable, S, D, V, d, scale, accumulate != 0,
                           ws, S_(stream));

@@ -141,7 +141,7 @@ tsp_status launch_decode_attn(const DecodeAttn& a, cudaStream_t st);
 // embed.cu (arguments as checked by tsp_embed_fwd / tsp_embed_bwd)
 tsp_status launch_embed_fwd(const void* ids, int id_bytes, const void* table, void* x, int64_t S,
                             int D, int64_t vocab, int d, float scale, int dtype, cudaStream_t st);
-size_t embed_bwd_ws_bytes(int64_t S, int64_t vocab, int d);
+size_t embed_bwd_ws_bytes(int64_t S, int d);
 tsp_status launch_embed_bwd(const void* ids, int id_bytes, const void* dx, int dx_dtype,
                             float* dtable, int64_t S, int D, int64_t vocab, int d, float scale,
                             bool accumulate, void* ws, cudaStream_t st);

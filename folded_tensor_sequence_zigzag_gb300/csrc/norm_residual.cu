@@ -190,10 +190,10 @@ struct FwdArgs {
 // The row in registers (first_col).
 //   TPR > 0: TPR threads a row, 256 / TPR rows a CTA (short rows);
 //   TPR = 0: a CTA a row.
-// AHEAD (TPR = 0): once every thread has its part of a row in registers (the
-// first row sum's barrier), the next row's inputs are sent for, each thread's
-// into the places it has just read, and arrive while this row is worked on.
-// Without that the loads of a row wait for the barriers of the one before.
+// AHEAD (TPR = 0): past the barrier of a row sum, the next row's inputs are sent
+// for, each thread's into the places it has read before that barrier, and arrive
+// while this row is worked on.  Without that the loads of a row wait for the
+// barriers of the one before.
 template <typename T, typename Ts, int N, int UPT, int TPR, bool AHEAD>
 __global__ void __launch_bounds__(UPT * N < 8 || UPT == 2 ? 512 : 1024, UPT * N < 8 || UPT == 2 ? 3 : 1)
     norm_residual_fwd_kernel(const __grid_constant__ FwdArgs a) {
@@ -210,37 +210,46 @@ __global__ void __launch_bounds__(UPT * N < 8 || UPT == 2 ? 512 : 1024, UPT * N 
   T* const f_in = (T*)mine + (threadIdx.x & 31) * N;
   T* const z_in = f_in + kWarp;
   Ts* const x_in = (Ts*)(mine + 2 * sizeof(T) * kWarp) + (threadIdx.x & 31) * N;
-  auto issue = [&](int64_t row) {
+  // The copies of a row go in two groups: f, whose place is free after the first
+  // sum's barrier, and x and z, free after the second's.
+  auto issue_f = [&](int64_t row) {
     if constexpr (AHEAD) {
       if (row < a.rows) {
         const int64_t at = row * n + c0;
-        const T *f = (const T*)a.f + at, *z = (const T*)a.z + at;
-        const Ts* x = (const Ts*)a.x + at;
+#pragma unroll
+        for (int i = 0; i < UPT; ++i)
+          if (c0 + i * kStep < n) copy_ahead<T, N>(f_in + i * kStep, (const T*)a.f + at + i * kStep);
+      }
+      copies_commit();
+    }
+  };
+  auto issue_x = [&](int64_t row) {
+    if constexpr (AHEAD) {
+      if (row < a.rows) {
+        const int64_t at = row * n + c0;
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
           if (c0 + i * kStep < n) {
-            copy_ahead<T, N>(f_in + i * kStep, f + i * kStep);
-            if (a.z) copy_ahead<T, N>(z_in + i * kStep, z + i * kStep);
-            copy_ahead<Ts, N>(x_in + i * kStep, x + i * kStep);
+            copy_ahead<Ts, N>(x_in + i * kStep, (const Ts*)a.x + at + i * kStep);
+            if (a.z) copy_ahead<T, N>(z_in + i * kStep, (const T*)a.z + at + i * kStep);
           }
         }
       }
       copies_commit();
     }
   };
-  issue(blockIdx.x);
+  issue_f(blockIdx.x);
+  issue_x(blockIdx.x);
   for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < a.rows; row0 += (int64_t)gridDim.x * per) {
     const int64_t row = row0 + group;
     const int nrow = TPR == 0 || row < a.rows ? n : 0;   // (a group past the last row does nothing)
     const int64_t at = row * n + c0;
-    if constexpr (AHEAD) copies_wait<0>();
+    if constexpr (AHEAD) copies_wait<1>();   // f is there
     const T* fp = AHEAD ? f_in : (const T*)a.f + at;
     const T* zp = AHEAD ? z_in : (const T*)a.z + at;
     const Ts* xp = AHEAD ? x_in : (const Ts*)a.x + at;
-    float v[UPT][N];
-    Unit<Ts, N> q[UPT];
-    Unit<T, N> z[UPT];
-    float ss[N];
+    float v[UPT][N], ss[N];
+    float early[AHEAD ? 1 : UPT][N];   // without copies ahead: x, on its way during the first sum
 #pragma unroll
     for (int e = 0; e < N; ++e) ss[e] = 0.f;
 #pragma unroll
@@ -249,8 +258,7 @@ __global__ void __launch_bounds__(UPT * N < 8 || UPT == 2 ? 512 : 1024, UPT * N 
       for (int e = 0; e < N; ++e) v[i][e] = 0.f;
       if (c0 + i * kStep < nrow) {
         load_n<T, N>(fp + i * kStep, v[i]);
-        q[i].load(xp + i * kStep);
-        if (a.z) z[i].load(zp + i * kStep);
+        if constexpr (!AHEAD) load_n<Ts, N>(xp + i * kStep, early[i]);
       }
     }
     float r = 1.f;
@@ -262,7 +270,8 @@ __global__ void __launch_bounds__(UPT * N < 8 || UPT == 2 ? 512 : 1024, UPT * N 
     } else if (AHEAD) {
       __syncthreads();
     }
-    issue(row + gridDim.x);
+    if constexpr (AHEAD) copies_wait<0>();   // x and z too
+    issue_f(row + gridDim.x);
 #pragma unroll
     for (int e = 0; e < N; ++e) ss[e] = 0.f;
     Ts* h = (Ts*)a.h + at;
@@ -276,12 +285,17 @@ __global__ void __launch_bounds__(UPT * N < 8 || UPT == 2 ? 512 : 1024, UPT * N 
           mul_n<N>(v[i], w);
         }
         if (a.z) {
-          z[i].get(w);
+          load_n<T, N>(zp + i * kStep, w);
 #pragma unroll
           for (int e = 0; e < N; ++e) w[e] = gate_of(w[e]);
           mul_n<N>(v[i], w);
         }
-        q[i].get(w);
+        if constexpr (AHEAD) {
+          load_n<Ts, N>(xp + i * kStep, w);
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; ++e) w[e] = early[i][e];
+        }
         fma_n<N>(w, v[i], a.s);
 #pragma unroll
         for (int e = 0; e < N; ++e) v[i][e] = to_f<Ts>(from_f<Ts>(w[e]));
@@ -292,6 +306,7 @@ __global__ void __launch_bounds__(UPT * N < 8 || UPT == 2 ? 512 : 1024, UPT * N 
     if (a.g_pre) {
       r = rsqrtf(row_sum<TPR>(total<N>(ss), part[1]) * inv_n + a.eps);
       if (c0 == 0 && nrow && a.rstd_h) a.rstd_h[row] = r;
+      issue_x(row + gridDim.x);
       T* b = (T*)a.b + at;
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
@@ -306,6 +321,7 @@ __global__ void __launch_bounds__(UPT * N < 8 || UPT == 2 ? 512 : 1024, UPT * N 
     }
     // with one barrier a row, `part` would be written again before all have read it
     if (TPR == 0 && !(a.g_post && a.g_pre)) __syncthreads();
+    if (!a.g_pre) issue_x(row + gridDim.x);
   }
 }
 
