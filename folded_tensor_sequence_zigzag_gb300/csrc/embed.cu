@@ -10,12 +10,8 @@
 // recorded as TSP_ERR_RANGE.  Both directions are bound by HBM: the forward
 // reads the distinct table rows and writes S rows, the backward reads S rows
 // and writes V.
-#include <cooperative_groups.h>
-
 #include "common.cuh"
 #include "kernels.h"
-
-namespace cg = cooperative_groups;
 
 namespace tsp {
 
@@ -37,34 +33,34 @@ __device__ __forceinline__ int row_of(int p, int c, int D) {
 // ---------------------------------------------------------------------------
 
 // One unit of a row scaled in fp32 and rounded once to the table's type.
-template <typename T>
-__device__ __forceinline__ T scaled(T v, float s) {
-  return from_f<T>(to_f<T>(v) * s);
-}
 template <typename T, typename V>
 __device__ __forceinline__ V scale_unit(V u, float s) {
-  constexpr int N = sizeof(V) / sizeof(T);
-  T e[N];
-  memcpy(e, &u, sizeof(V));
+  if constexpr (sizeof(T) == 2 && sizeof(V) > 2) {
+    uint32_t w[sizeof(V) / 4];
+    memcpy(w, &u, sizeof(V));
 #pragma unroll
-  for (int i = 0; i < N; ++i) e[i] = scaled<T>(e[i], s);
-  memcpy(&u, e, sizeof(V));
+    for (int i = 0; i < (int)(sizeof(V) / 4); ++i) w[i] = pack2<T>(lo2<T>(w[i]) * s, hi2<T>(w[i]) * s);
+    memcpy(&u, w, sizeof(V));
+  } else {
+    T e[sizeof(V) / sizeof(T)];
+    memcpy(e, &u, sizeof(V));
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(V) / sizeof(T)); ++i) e[i] = from_f<T>(to_f<T>(e[i]) * s);
+    memcpy(&u, e, sizeof(V));
+  }
   return u;
 }
 
-// One warp per (position, segment of 128 units of V bytes): four loads in
-// flight a lane.
-template <typename T, typename V>
+// A warp a position (grid-stride in x), a segment of 32 * LOADS units of sizeof(V)
+// bytes at a time (stride gridDim.y), LOADS loads in flight a lane.
+template <typename T, typename V, int LOADS>
 __global__ void __launch_bounds__(256) embed_fwd_kernel(const void* __restrict__ ids, int id_bytes,
                                                         const V* __restrict__ table,
                                                         V* __restrict__ x, int S, int c, int D,
-                                                        int64_t vocab, int upr, int nseg,
-                                                        float scale, int* __restrict__ status) {
-  const int lane = threadIdx.x & 31;
-  const int64_t items = (int64_t)S * nseg, stride = (int64_t)gridDim.x * (blockDim.x >> 5);
-  for (int64_t it = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items;
-       it += stride) {
-    const int p = (int)(it / nseg), seg = (int)(it - (int64_t)p * nseg);
+                                                        int64_t vocab, int upr, float scale,
+                                                        int* __restrict__ status) {
+  const int lane = threadIdx.x & 31, stride = gridDim.x * 8;
+  for (int p = blockIdx.x * 8 + (threadIdx.x >> 5); p < S; p += stride) {
     const int64_t id = load_id(ids, id_bytes, p);
     const int row = row_of(p, c, D);
     if (!TSP_INB(row >= 0 && row < S, status)) continue;
@@ -72,17 +68,17 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void* __restrict__
     const bool there = id >= 0 && id < vocab;
     const V* src = table + (there ? id : 0) * upr;
     V* dst = x + (int64_t)row * upr;
-    V v[4];
+    for (int u0 = blockIdx.y * 32 * LOADS + lane; u0 < upr; u0 += gridDim.y * 32 * LOADS) {
+      V v[LOADS];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int u = seg * 128 + k * 32 + lane;
-      v[k] = V{};
-      if (there && u < upr) v[k] = src[u];
-    }
+      for (int k = 0; k < LOADS; ++k) {
+        v[k] = V{};
+        if (there && u0 + k * 32 < upr) v[k] = src[u0 + k * 32];
+      }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int u = seg * 128 + k * 32 + lane;
-      if (u < upr) dst[u] = scale == 1.f ? v[k] : scale_unit<T, V>(v[k], scale);
+      for (int k = 0; k < LOADS; ++k)
+        if (u0 + k * 32 < upr)   // the rows are not read here again: table rows stay in L2
+          __stcs(dst + u0 + k * 32, scale == 1.f ? v[k] : scale_unit<T, V>(v[k], scale));
     }
   }
 }
@@ -91,203 +87,219 @@ template <typename T, typename V>
 tsp_status embed_fwd_t(const void* ids, int id_bytes, const void* table, void* x, int64_t S, int D,
                        int64_t vocab, int d, float scale, cudaStream_t st) {
   const int upr = (int)((int64_t)d * sizeof(T) / sizeof(V));
-  const int nseg = (upr + 127) / 128;
-  const int64_t ctas = (S * nseg + 7) / 8;
-  const int grid = (int)std::min<int64_t>(ctas, (int64_t)num_sms() * 8);
+  const int64_t full = (int64_t)num_sms() * 4;   // CTAs the GPU holds at 64 registers a thread
+  const int64_t gx = std::min<int64_t>((S + 7) / 8, full);
   Prof prof("embed_fwd", st);
-  embed_fwd_kernel<T, V><<<grid, 256, 0, st>>>(ids, id_bytes, (const V*)table, (V*)x, (int)S,
-                                               (int)(S / (2 * D)), D, vocab, upr, nseg, scale,
-                                               status_word());
+  if (gx < full) {   // few positions: short segments, on CTAs of their own
+    const int gy = (int)std::min<int64_t>((upr + 63) / 64, full / gx);
+    embed_fwd_kernel<T, V, 2><<<dim3((unsigned)gx, gy), 256, 0, st>>>(
+        ids, id_bytes, (const V*)table, (V*)x, (int)S, (int)(S / (2 * D)), D, vocab, upr, scale,
+        status_word());
+  } else {
+    embed_fwd_kernel<T, V, 8><<<(unsigned)gx, 256, 0, st>>>(
+        ids, id_bytes, (const V*)table, (V*)x, (int)S, (int)(S / (2 * D)), D, vocab, upr, scale,
+        status_word());
+  }
   TSP_CUDA_TRY(cudaGetLastError());
   return TSP_OK;
 }
 
 // ---------------------------------------------------------------------------
-// Backward, step 1: the positions sorted by token, and the rows of absent tokens
+// Backward, step 1: the positions sorted by token
 // ---------------------------------------------------------------------------
-// The first cluster of the grid sorts (token, zigzag row) by a stable
-// least-significant-digit radix sort: every CTA of it owns a contiguous range of
-// the positions, every warp a contiguous part of that.  A pass counts digits per
-// warp in shared memory, turns the counts into places (over warps, then over the
-// cluster's CTAs through distributed shared memory, then over digits) and
-// scatters.  Equal tokens keep the order of their positions, so the sums of
-// step 2 have one fixed order.  Ids outside the table sort to the end as token
-// `vocab`.  The sort is a few microseconds of latency on eight multiprocessors;
-// meanwhile the CTAs of the other clusters write the zero rows: each owns the
-// tokens v with v % zero_ctas equal to its number, and marks those that occur in
-// a bitmap of its own by reading all ids (from L2).
-constexpr int kBits = 9, kBins = 1 << kBits, kSortWarps = 32, kMaxCluster = 8;
-constexpr int kSortSmem = kSortWarps * kBins * 4;
-constexpr int kBatch = 8;   // positions a lane loads before it uses the first
+// (token, zigzag row) pairs in the order of (token, position), so that the sums
+// of step 2 have one fixed order.  Ids outside the table sort to the end as token
+// `vocab`.  The data are small (8 bytes a position, in L2 throughout): what counts
+// is the number of dependent steps.
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 
 struct SortArgs {
   const void* ids;
   int id_bytes;
-  int S, c, D, vocab, d;
-  int passes, bits;
-  int *key[2], *row[2];   // the last pass writes key[passes & 1], row[passes & 1]
-  float* table;
-  int zero_shift;         // log2 of the CTAs that write zeros, -1: none
+  int S, c, D, vocab;
+  int2* pair[2];          // (token, row): a pass reads one and writes the other
+  int* count;             // [runs][bins] of the pass
+  int run, runs;          // positions of a run, runs
+  int shift, bits;
+  int pass;               // 0: from the ids
   int* status;
 };
 
-template <bool VEC>
-__device__ void zero_absent_rows(const SortArgs& a, int me, int* bitmap) {
-  const int shift = a.zero_shift, t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int mine = (int)(((int64_t)a.vocab - me + (1 << shift) - 1) >> shift);   // my tokens
-  constexpr int kCap = kSortSmem * 8;                                            // marked at a time
-  for (int first = 0; first < mine; first += kCap) {
-    const int count = min(kCap, mine - first);
-    for (int i = t; i < (count + 31) / 32; i += blockDim.x) bitmap[i] = 0;
-    __syncthreads();
-    for (int p = t; p < a.S; p += kBatch * blockDim.x) {
-      int64_t id[kBatch];
+__device__ __forceinline__ int token_of(const SortArgs& a, int p, bool* past) {
+  const int64_t id = load_id(a.ids, a.id_bytes, p);
+  *past |= id >= a.vocab;
+  return id < 0 ? a.vocab : (int)min(id, (int64_t)a.vocab);
+}
+
+// Up to kRankMax positions: the place of each is the number of positions with a
+// smaller (token, position), both in one 32-bit word.  A CTA takes 32 positions, a
+// warp of it a sixteenth of the comparisons (8192 positions: 64 M of them, 5 us).
+constexpr int kRankMax = 8192;
+
+__global__ void __launch_bounds__(kSortThreads) embed_rank_kernel(const __grid_constant__ SortArgs a,
+                                                                  int pos_bits) {
+  __shared__ __align__(16) unsigned word[kRankMax];
+  __shared__ int place[32];
+  constexpr int kBatch = 8;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int padded = (a.S + 63) / 64 * 64;   // each warp's part is whole 4's
+  bool past = false;
+  for (int p = t; p < padded; p += kBatch * kSortThreads) {
+    int key[kBatch];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int q = p + k * (int)blockDim.x;
-        id[k] = q < a.S ? load_id(a.ids, a.id_bytes, q) : -1;
+    for (int k = 0; k < kBatch; ++k) {
+      const int q = p + k * kSortThreads;
+      key[k] = q < a.S ? token_of(a, q, &past) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int q = p + k * kSortThreads;
+      if (q < padded) word[q] = q < a.S ? (unsigned)key[k] << pos_bits | q : 0xffffffffu;
+    }
+  }
+  if (past) report_status(a.status, (int)TSP_ERR_RANGE);
+  if (t < 32) place[t] = 0;
+  __syncthreads();
+  const int i = blockIdx.x * 32 + lane;
+  const unsigned me = i < a.S ? word[i] : 0u;
+  const int part = padded / kSortWarps;
+  const uint4* w4 = reinterpret_cast<const uint4*>(word + warp * part);
+  int below = 0;
+#pragma unroll 4
+  for (int j = 0; j < part / 4; ++j) {
+    const uint4 w = w4[j];
+    below += (w.x < me) + (w.y < me) + (w.z < me) + (w.w < me);
+  }
+  atomicAdd(place + lane, below);   // (integers: the order does not matter)
+  __syncthreads();
+  if (warp == 0 && i < a.S && TSP_INB(place[lane] < a.S, a.status))
+    a.pair[0][place[lane]] = make_int2((int)(me >> pos_bits), row_of(i, a.c, a.D));
+}
+
+// More positions: a stable least-significant-digit radix sort, two launches a
+// pass.  A CTA a run of kTile positions (of several, beyond kMaxRuns of them)
+// counts its digits; then every CTA sums the runs' counts to the places of its
+// own digits and scatters, the positions of a warp in order by votes on the
+// digit's bits.  (One cluster with its counts in distributed shared memory needs
+// one launch but has eight multiprocessors' throughput: 28 us at 16384 positions,
+// 88 at 131072.)
+constexpr int kTile = 1024, kGroups = kTile / kSortThreads;   // groups of 32 a warp
+constexpr int kBits = 9, kBins = 1 << kBits, kMaxRuns = 512;
+
+__global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const __grid_constant__ SortArgs a) {
+  __shared__ int hist[kBins];
+  const int t = threadIdx.x, bins = 1 << a.bits;
+  if (t < bins) hist[t] = 0;
+  __syncthreads();
+  bool past = false;
+  const int end = min(a.S, (int)(blockIdx.x + 1) * a.run);
+#pragma unroll 2
+  for (int p = blockIdx.x * a.run + t; p < end; p += kSortThreads) {
+    const int key = a.pass == 0 ? token_of(a, p, &past) : a.pair[a.pass & 1][p].x;
+    atomicAdd(hist + ((key >> a.shift) & (bins - 1)), 1);
+  }
+  if (past) report_status(a.status, (int)TSP_ERR_RANGE);
+  __syncthreads();
+  if (t < bins) a.count[((int64_t)blockIdx.x << a.bits) + t] = hist[t];
+}
+
+__global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const __grid_constant__ SortArgs a) {
+  __shared__ int hist[kSortWarps][kBins];
+  __shared__ int sum_all[kSortThreads], sum_before[kSortThreads], wsum[kSortWarps];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, bins = 1 << a.bits;
+  // the digits' counts over all runs and over those before this one: thread
+  // (part, digit) sums every parts-th run
+  const int parts = kSortThreads >> a.bits, part = t >> a.bits;
+  int all = 0, before = 0;
+#pragma unroll 8
+  for (int i = part; i < a.runs; i += parts) {
+    const int n = a.count[((int64_t)i << a.bits) + (t & (bins - 1))];
+    all += n;
+    before += i < (int)blockIdx.x ? n : 0;
+  }
+  sum_all[t] = all;
+  sum_before[t] = before;
+  __syncthreads();
+  all = before = 0;
+  if (t < bins) {
+    for (int q = 0; q < parts; ++q) {
+      all += sum_all[q * bins + t];
+      before += sum_before[q * bins + t];
+    }
+  }
+  int inc = all;   // over the digits
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += n;
+  }
+  if (lane == 31) wsum[warp] = inc;
+  __syncthreads();
+  int pre = lane < warp ? wsum[lane < kSortWarps ? lane : 0] : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) pre += __shfl_xor_sync(0xffffffffu, pre, o);
+  int at_digit = inc - all + before + pre;   // where this CTA's next position of digit t goes
+
+  bool past = false;
+  const int end = min(a.S, (int)(blockIdx.x + 1) * a.run);
+  for (int p0 = blockIdx.x * a.run; p0 < end; p0 += kTile) {
+    // this lane's positions: group k of the warp, in position order
+    int2 pair[kGroups];
+    unsigned same[kGroups];
+    int digit[kGroups], was[kGroups];
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const int p = p0 + (warp * kGroups + k) * 32 + lane;
+      pair[k] = make_int2(0, 0);
+      if (p < end)
+        pair[k] = a.pass == 0 ? make_int2(token_of(a, p, &past), row_of(p, a.c, a.D)) : a.pair[a.pass & 1][p];
+      digit[k] = p < end ? (pair[k].x >> a.shift) & (bins - 1) : bins;
+    }
+    for (int i = lane; i < bins; i += 32) hist[warp][i] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      same[k] = 0xffffffffu;   // the lanes with this lane's digit
+#pragma unroll
+      for (int b = 0; b <= kBits; ++b) {
+        const bool one = digit[k] >> b & 1;
+        const unsigned votes = __ballot_sync(0xffffffffu, one);
+        same[k] &= one ? votes : ~votes;
       }
+    }
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        if (id[k] < 0 || id[k] >= a.vocab || ((int)id[k] & ((1 << shift) - 1)) != me) continue;
-        const int i = ((int)id[k] >> shift) - first;
-        if (i >= 0 && i < count) atomicOr(bitmap + (i >> 5), 1 << (i & 31));
+    for (int k = 0; k < kGroups; ++k) {   // was: of the digit in the warp's groups before
+      was[k] = digit[k] < bins ? hist[warp][digit[k]] : 0;
+      __syncwarp();
+      if (digit[k] < bins && lane == __ffs(same[k]) - 1) hist[warp][digit[k]] = was[k] + __popc(same[k]);
+      __syncwarp();
+    }
+    __syncthreads();
+    if (t < bins) {   // places of the warps' digits
+      int n[kSortWarps];
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) n[w] = hist[w][t];
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) {
+        hist[w][t] = at_digit;
+        at_digit += n[w];
       }
     }
     __syncthreads();
-    for (int i = warp; i < count; i += kSortWarps) {
-      if (bitmap[i >> 5] >> (i & 31) & 1) continue;
-      float* row = a.table + (((int64_t)(first + i) << shift) + me) * a.d;
-      if constexpr (VEC) {
-        for (int c = lane * 4; c < a.d; c += 128)
-          *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-      } else {
-        for (int c = lane; c < a.d; c += 32) row[c] = 0.f;
-      }
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      if (digit[k] == bins) continue;
+      const int at = hist[warp][digit[k]] + was[k] + __popc(same[k] & ((1u << lane) - 1));
+      if (TSP_INB(at >= 0 && at < a.S, a.status)) a.pair[(a.pass & 1) ^ 1][at] = pair[k];
     }
-    __syncthreads();
+    __syncwarp();
   }
 }
 
-__global__ void __launch_bounds__(kSortWarps * 32) embed_sort_kernel(const __grid_constant__ SortArgs a) {
-  extern __shared__ int hist[];                   // [kSortWarps][bins]
-  __shared__ int total[kBins], wsum[kSortWarps];
-  cg::cluster_group cl = cg::this_cluster();
-  const int me = (int)cl.block_rank(), nc = (int)cl.num_blocks();
-  if ((int)blockIdx.x >= nc) {
-    const int z = (int)blockIdx.x - nc;
-    if (z >> a.zero_shift) return;   // (the grid is whole clusters)
-    if (a.d % 4 == 0) zero_absent_rows<true>(a, z, hist);
-    else zero_absent_rows<false>(a, z, hist);
-    return;
-  }
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, bins = 1 << a.bits;
-  // this warp's positions, in whole groups of 32
-  const int64_t groups = ((int64_t)a.S + 31) / 32;
-  const int64_t gw = (int64_t)me * kSortWarps + warp, nw = (int64_t)nc * kSortWarps;
-  const int g0 = (int)(groups * gw / nw), g1 = (int)(groups * (gw + 1) / nw);
-  int* const mine = hist + warp * bins;
-
-  for (int pass = 0; pass < a.passes; ++pass) {
-    const int shift = pass * a.bits;
-    const int* key_in = a.key[pass & 1];
-    const int* row_in = a.row[pass & 1];
-    int* key_out = a.key[(pass & 1) ^ 1];
-    int* row_out = a.row[(pass & 1) ^ 1];
-    int key[kBatch], row[kBatch];
-    auto load_keys = [&](int g) {
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int p = (g + u) * 32 + lane;
-        key[u] = 0;
-        if (g + u >= g1 || p >= a.S) continue;
-        if (pass > 0) {
-          key[u] = __ldcg(key_in + p);
-        } else {
-          const int64_t id = load_id(a.ids, a.id_bytes, p);
-          key[u] = id < 0 ? a.vocab : (int)min(id, (int64_t)a.vocab);
-          if (id >= a.vocab) report_status(a.status, (int)TSP_ERR_RANGE);
-        }
-      }
-    };
-    // the digit of batch position u, `bins` where there is none
-    auto digit_of = [&](int g, int u) {
-      return g + u < g1 && (g + u) * 32 + lane < a.S ? (key[u] >> shift) & (bins - 1) : bins;
-    };
-    for (int i = t; i < kSortWarps * bins; i += blockDim.x) hist[i] = 0;
-    __syncthreads();
-    for (int g = g0; g < g1; g += kBatch) {
-      load_keys(g);
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int digit = digit_of(g, u);
-        const unsigned same = __match_any_sync(0xffffffffu, digit);
-        if (digit < bins && lane == __ffs(same) - 1) mine[digit] += __popc(same);
-        __syncwarp();
-      }
-    }
-    __syncthreads();
-    int sum = 0;
-    if (t < bins) {
-#pragma unroll 8
-      for (int w = 0; w < kSortWarps; ++w) {
-        const int n = hist[w * bins + t];
-        hist[w * bins + t] = sum;
-        sum += n;
-      }
-      total[t] = sum;
-    }
-    cl.sync();
-    // this digit's count over the cluster, and over the CTAs before this one
-    int all = 0, before = 0;
-    if (t < bins) {
-      for (int j = 0; j < nc; ++j) {
-        const int n = cl.map_shared_rank(total, j)[t];
-        all += n;
-        if (j < me) before += n;
-      }
-    }
-    int inc = all;   // inclusive scan over the digits
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += n;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    if (t < bins) {
-      int base = inc - all + before;
-      for (int w = 0; w < warp; ++w) base += wsum[w];
-#pragma unroll 8
-      for (int w = 0; w < kSortWarps; ++w) hist[w * bins + t] += base;
-    }
-    __syncthreads();
-    for (int g = g0; g < g1; g += kBatch) {
-      // (one batch a warp: the keys are still there)
-      if (g1 - g0 > kBatch) load_keys(g);
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int p = (g + u) * 32 + lane;
-        row[u] = 0;
-        if (g + u < g1 && p < a.S) row[u] = pass > 0 ? __ldcg(row_in + p) : row_of(p, a.c, a.D);
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int digit = digit_of(g, u);
-        const unsigned same = __match_any_sync(0xffffffffu, digit);
-        int at = -1;
-        if (digit < bins) at = mine[digit] + __popc(same & ((1u << lane) - 1));
-        __syncwarp();
-        if (digit < bins && lane == __ffs(same) - 1) mine[digit] += __popc(same);
-        __syncwarp();
-        if (digit < bins && TSP_INB(at >= 0 && at < a.S, a.status)) {
-          __stcg(key_out + at, key[u]);
-          __stcg(row_out + at, row[u]);
-        }
-      }
-    }
-    cl.sync();   // the pass is written, and no CTA reads `total` any more
-  }
+// Positions of a run.
+int run_of(int64_t S) {
+  const int64_t tiles = (S + kTile - 1) / kTile;
+  return (int)((tiles + kMaxRuns - 1) / kMaxRuns * kTile);
 }
 
 // ---------------------------------------------------------------------------
@@ -298,8 +310,10 @@ __global__ void __launch_bounds__(kSortWarps * 32) embed_sort_kernel(const __gri
 // at a time.  A token whose positions lie inside the chunk is written (or added)
 // to its table row at once; one that came in from the chunk before leaves its
 // part in slot 2*chunk, one that starts here and goes on in slot 2*chunk + 1.
-// Step 3 adds those up.
-constexpr int kSlab = 256;
+// Step 3 adds those up.  The first warps of the grid write the zero rows of absent
+// tokens, eight rows each, which they look up in the sorted tokens: plain stores
+// next to the other warps' loads.
+constexpr int kSlab = 256, kZeroRows = 8;
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_cols(const T* row, int c0, int lane, int d, float (&v)[8]) {
@@ -352,11 +366,11 @@ __device__ __forceinline__ void store_cols(float* row, int c0, int lane, int d, 
 }
 
 struct SumArgs {
-  const int *key, *row;
+  const int2* pair;   // sorted (token, row)
   float *table, *part;
   int S, vocab, d, chunk, nchunks, nslabs;
+  int zero_tasks;   // 0: add to the table rows instead of overwriting them
   float scale;
-  bool add;   // to the table rows instead of overwriting them
   int* status;
 };
 
@@ -364,32 +378,51 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const T* __restrict__ dx,
                                                         const __grid_constant__ SumArgs a) {
   const int lane = threadIdx.x & 31;
-  const int64_t task = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  int64_t task = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const bool add = a.zero_tasks == 0;
+  if (task < a.zero_tasks) {
+    const int v0 = (int)task * kZeroRows, v = v0 + lane % kZeroRows;
+    int lo = 0, hi = a.S;   // the first place with a token >= v
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (a.pair[mid].x < v) lo = mid + 1; else hi = mid;
+    }
+    const bool absent = v < a.vocab && (lo == a.S || a.pair[lo].x != v);
+    const unsigned rows = __ballot_sync(0xffffffffu, absent);
+    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < kZeroRows; ++r) {
+      if (!(rows >> r & 1)) continue;
+      for (int s = 0; s < a.nslabs; ++s)
+        store_cols<VEC>(a.table + (int64_t)(v0 + r) * a.d, s * kSlab, lane, a.d, zero, 1.f, false);
+    }
+    return;
+  }
+  task -= a.zero_tasks;
   if (task >= (int64_t)a.nchunks * a.nslabs) return;
   const int ch = (int)(task / a.nslabs), c0 = (int)(task - (int64_t)ch * a.nslabs) * kSlab;
   const int j0 = ch * a.chunk, j1 = (int)min((int64_t)a.S, (int64_t)j0 + a.chunk);
-  int cur = a.key[j0];
+  int cur = a.pair[j0].x;
   if (cur >= a.vocab) return;
-  bool opened = j0 == 0 || a.key[j0 - 1] != cur;   // the current token's positions start here
-  const bool goes_on = j1 < a.S && a.key[j1] == a.key[j1 - 1];
+  bool opened = j0 == 0 || a.pair[j0 - 1].x != cur;   // the current token's positions start here
+  const bool goes_on = j1 < a.S && a.pair[j1].x == a.pair[j1 - 1].x;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   auto leave = [&](bool on) {
     if (opened && !on)
-      store_cols<VEC>(a.table + (int64_t)cur * a.d, c0, lane, a.d, acc, a.scale, a.add);
+      store_cols<VEC>(a.table + (int64_t)cur * a.d, c0, lane, a.d, acc, a.scale, add);
     else
       store_cols<VEC>(a.part + ((int64_t)2 * ch + (opened ? 1 : 0)) * a.d, c0, lane, a.d, acc, 1.f,
                       false);
   };
   for (int j = j0; j < j1; j += 32) {
     const bool in = j + lane < j1;
-    const int keys = in ? a.key[j + lane] : a.vocab, rows = in ? a.row[j + lane] : 0;
+    const int2 mine = in ? a.pair[j + lane] : make_int2(a.vocab, 0);
     for (int k = 0; k < 32 && j + k < j1; k += 4) {
       float v[4][8];
       int key[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        key[u] = __shfl_sync(0xffffffffu, keys, k + u);
-        const int r = __shfl_sync(0xffffffffu, rows, k + u);
+        key[u] = __shfl_sync(0xffffffffu, mine.x, k + u);
+        const int r = __shfl_sync(0xffffffffu, mine.y, k + u);
         if (key[u] < a.vocab && TSP_INB(r >= 0 && r < a.S, a.status)) {
           load_cols<T, VEC>(dx + (int64_t)r * a.d, c0, lane, a.d, v[u]);
         } else {
@@ -417,46 +450,53 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const T* __restrict__ dx
 }
 
 // Step 3: a token that starts in one chunk and ends in a later one.  A CTA a
-// chunk and slab (nearly all see at once that no token starts there and goes
-// on); the warps add up every eighth part each, then the eight sums in order.
+// chunk (nearly all see at once that no token starts there and goes on); four
+// slabs at a time, eight warps a slab, each of which adds up every eighth part;
+// then the eight sums in order.
 template <bool VEC>
-__global__ void __launch_bounds__(256) embed_join_kernel(const __grid_constant__ SumArgs a) {
-  __shared__ float sums[8][kSlab];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ch = (int)(blockIdx.x / a.nslabs), c0 = (int)(blockIdx.x - ch * a.nslabs) * kSlab;
-  const int end = (ch + 1) * a.chunk;   // < S: there is a chunk after this one
-  const int tok = a.key[end - 1];
-  if (tok >= a.vocab || a.key[end] != tok) return;
-  const int j0 = ch * a.chunk;
-  if (j0 > 0 && a.key[j0] == tok && a.key[j0 - 1] == tok) return;   // it started before this chunk
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (warp == 0) load_cols<float, VEC>(a.part + ((int64_t)2 * ch + 1) * a.d, c0, lane, a.d, acc);
-  for (int k = ch + 1 + warp; k < a.nchunks; k += 32) {
-    float v[4][8];
-    bool in[4];
+__global__ void __launch_bounds__(1024) embed_join_kernel(const __grid_constant__ SumArgs a) {
+  __shared__ float sums[32][kSlab];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp & 7;
+  const int ch = blockIdx.x;
+  const int j0 = ch * a.chunk, end = j0 + a.chunk;   // end < S: there is a chunk after this one
+  const int tok = a.pair[end - 1].x, next = a.pair[end].x, start = a.pair[j0].x;
+  const int prev = j0 > 0 ? a.pair[j0 - 1].x : -1;
+  if (tok >= a.vocab || next != tok || (start == tok && prev == tok)) return;
+  for (int s0 = 0; s0 < a.nslabs; s0 += 4) {
+    const int c0 = (s0 + (warp >> 3)) * kSlab;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (part == 0) load_cols<float, VEC>(a.part + ((int64_t)2 * ch + 1) * a.d, c0, lane, a.d, acc);
+    for (int k = ch + 1 + part; k < a.nchunks; k += 32) {
+      float v[4][8];
+      bool in[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int q = k + u * 8;
-      in[u] = q < a.nchunks && a.key[q * a.chunk] == tok;
-      if (in[u]) load_cols<float, VEC>(a.part + (int64_t)2 * q * a.d, c0, lane, a.d, v[u]);
+      for (int u = 0; u < 4; ++u) {
+        const int q = k + u * 8;
+        in[u] = q < a.nchunks && a.pair[q * a.chunk].x == tok;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (in[u]) load_cols<float, VEC>(a.part + (int64_t)2 * (k + u * 8) * a.d, c0, lane, a.d, v[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (!in[u]) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += v[u][e];
+      }
+      if (!in[3]) break;
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (!in[u]) continue;
+    for (int e = 0; e < 8; ++e) sums[warp][e * 32 + lane] = acc[e];
+    __syncthreads();
+    if (part == 0) {
+      for (int w = 1; w < 8; ++w) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += v[u][e];
+        for (int e = 0; e < 8; ++e) acc[e] += sums[warp + w][e * 32 + lane];
+      }
+      store_cols<VEC>(a.table + (int64_t)tok * a.d, c0, lane, a.d, acc, a.scale, a.zero_tasks == 0);
     }
-    if (!in[3]) break;
+    __syncthreads();
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) sums[warp][e * 32 + lane] = acc[e];
-  __syncthreads();
-  if (warp != 0) return;
-  for (int w = 1; w < 8; ++w) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] += sums[w][e * 32 + lane];
-  }
-  store_cols<VEC>(a.table + (int64_t)tok * a.d, c0, lane, a.d, acc, a.scale, a.add);
 }
 
 // Positions per chunk: the smallest power of two, 16 to 64, with which the
@@ -469,7 +509,8 @@ int chunk_of(int64_t S, int d) {
 }
 
 struct BwdLayout {
-  int *key[2], *row[2];
+  int2* pair[2];
+  int* count;
   float* part;
   size_t bytes;
 };
@@ -481,10 +522,8 @@ BwdLayout bwd_layout(int64_t S, int d, uint8_t* base) {
     off += up256(n);
     return p;
   };
-  for (int k = 0; k < 2; ++k) {
-    L.key[k] = (int*)take((size_t)S * 4);
-    L.row[k] = (int*)take((size_t)S * 4);
-  }
+  for (int k = 0; k < 2; ++k) L.pair[k] = (int2*)take((size_t)S * 8);
+  L.count = (int*)take((size_t)((S + run_of(S) - 1) / run_of(S)) * kBins * 4);
   const int c = chunk_of(S, d);
   L.part = (float*)take((size_t)((S + c - 1) / c) * 2 * d * 4);
   L.bytes = off;
@@ -493,12 +532,12 @@ BwdLayout bwd_layout(int64_t S, int d, uint8_t* base) {
 
 template <typename T, bool VEC>
 tsp_status embed_sum_t(const void* dx, const SumArgs& a, cudaStream_t st) {
-  const int64_t tasks = (int64_t)a.nchunks * a.nslabs;
+  const int64_t tasks = (int64_t)a.nchunks * a.nslabs + a.zero_tasks;
   Prof prof("embed_bwd_sum", st, a.nchunks > 1 ? 2 : 1);
   embed_sum_kernel<T, VEC><<<(unsigned)((tasks + 7) / 8), 256, 0, st>>>((const T*)dx, a);
   TSP_CUDA_TRY(cudaGetLastError());
   if (a.nchunks > 1) {
-    embed_join_kernel<VEC><<<(unsigned)((a.nchunks - 1) * (int64_t)a.nslabs), 256, 0, st>>>(a);
+    embed_join_kernel<VEC><<<(unsigned)(a.nchunks - 1), 1024, 0, st>>>(a);
     TSP_CUDA_TRY(cudaGetLastError());
   }
   return TSP_OK;
@@ -537,52 +576,34 @@ tsp_status launch_embed_bwd(const void* ids, int id_bytes, const void* dx, int d
   s.c = (int)(S / (2 * D));
   s.D = D;
   s.vocab = (int)vocab;
-  int nb = 1;   // bits of the largest key, `vocab` itself
-  while (((int64_t)vocab >> nb) != 0) ++nb;
-  s.passes = (nb + kBits - 1) / kBits;
-  s.bits = (nb + s.passes - 1) / s.passes;
-  for (int k = 0; k < 2; ++k) {
-    s.key[k] = L.key[k];
-    s.row[k] = L.row[k];
-  }
-  s.table = dtable;
-  s.d = d;
+  for (int k = 0; k < 2; ++k) s.pair[k] = L.pair[k];
+  s.count = L.count;
   s.status = status_word();
-  // a CTA for every 256 KB of the table writes its absent rows, 128 at most
-  s.zero_shift = -1;
-  if (!accumulate) {
-    s.zero_shift = 0;
-    while (s.zero_shift < 7 && ((int64_t)vocab * d * 4 >> s.zero_shift) > 256 * 1024) ++s.zero_shift;
-  }
-  {
+  s.pass = s.shift = 0;
+  int nb = 1;   // bits of the largest token, `vocab` itself
+  while ((vocab >> nb) != 0) ++nb;
+  int pos_bits = 1;
+  while ((S - 1) >> pos_bits != 0) ++pos_bits;
+  if (S <= kRankMax && nb + pos_bits <= 32) {
     Prof prof("embed_bwd_sort", st);
-    static bool ready[kMaxDevices] = {false};
-    const int dev = current_device();
-    if (!ready[dev]) {
-      TSP_CUDA_TRY(cudaFuncSetAttribute(embed_sort_kernel,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSortSmem));
-      ready[dev] = true;
+    embed_rank_kernel<<<(unsigned)((S + 31) / 32), kSortThreads, 0, st>>>(s, pos_bits);
+    TSP_CUDA_TRY(cudaGetLastError());
+  } else {
+    const int passes = (nb + kBits - 1) / kBits;
+    s.bits = std::max(5, (nb + passes - 1) / passes);   // whole warps of digits
+    s.run = run_of(S);
+    s.runs = (int)((S + s.run - 1) / s.run);
+    Prof prof("embed_bwd_sort", st, 2 * passes);
+    for (; s.pass < passes; ++s.pass, s.shift += s.bits) {
+      embed_count_kernel<<<s.runs, kSortThreads, 0, st>>>(s);
+      TSP_CUDA_TRY(cudaGetLastError());
+      embed_scatter_kernel<<<s.runs, kSortThreads, 0, st>>>(s);
+      TSP_CUDA_TRY(cudaGetLastError());
     }
-    int nc = 1;   // CTAs of the cluster: 4096 positions each before another joins
-    while (nc < kMaxCluster && (int64_t)nc * 4096 < S) nc *= 2;
-    cudaLaunchConfig_t cfg = {};
-    const int zero = s.zero_shift < 0 ? 0 : 1 << s.zero_shift;
-    cfg.gridDim = dim3(nc + (zero + nc - 1) / nc * nc);
-    cfg.blockDim = dim3(kSortWarps * 32);
-    cfg.dynamicSmemBytes = kSortSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = nc;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    TSP_CUDA_TRY(cudaLaunchKernelEx(&cfg, embed_sort_kernel, s));
   }
   SumArgs a;
-  a.key = L.key[s.passes & 1];
-  a.row = L.row[s.passes & 1];
-  a.add = accumulate;
+  a.pair = L.pair[s.pass & 1];
+  a.zero_tasks = accumulate ? 0 : (int)((vocab + kZeroRows - 1) / kZeroRows);
   a.table = dtable;
   a.part = L.part;
   a.S = (int)S;
