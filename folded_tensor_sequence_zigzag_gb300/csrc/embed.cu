@@ -51,35 +51,36 @@ __device__ __forceinline__ V scale_unit(V u, float s) {
   return u;
 }
 
-// A warp a position (grid-stride in x), a segment of 32 * LOADS units of sizeof(V)
-// bytes at a time (stride gridDim.y), LOADS loads in flight a lane.
+// A warp a position, a segment of 32 * LOADS units of sizeof(V) bytes at a time
+// (stride gridDim.y), LOADS loads in flight a lane.  Not a persistent grid: CTAs
+// started in order keep the rows written at a time next to each other (131072 x
+// 4096 bf16: 232 us with 4 resident CTAs a multiprocessor walking the positions).
 template <typename T, typename V, int LOADS>
 __global__ void __launch_bounds__(256) embed_fwd_kernel(const void* __restrict__ ids, int id_bytes,
                                                         const V* __restrict__ table,
                                                         V* __restrict__ x, int S, int c, int D,
                                                         int64_t vocab, int upr, float scale,
                                                         int* __restrict__ status) {
-  const int lane = threadIdx.x & 31, stride = gridDim.x * 8;
-  for (int p = blockIdx.x * 8 + (threadIdx.x >> 5); p < S; p += stride) {
-    const int64_t id = load_id(ids, id_bytes, p);
-    const int row = row_of(p, c, D);
-    if (!TSP_INB(row >= 0 && row < S, status)) continue;
-    if (id >= vocab && lane == 0) report_status(status, (int)TSP_ERR_RANGE);
-    const bool there = id >= 0 && id < vocab;
-    const V* src = table + (there ? id : 0) * upr;
-    V* dst = x + (int64_t)row * upr;
-    for (int u0 = blockIdx.y * 32 * LOADS + lane; u0 < upr; u0 += gridDim.y * 32 * LOADS) {
-      V v[LOADS];
+  const int lane = threadIdx.x & 31, p = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (p >= S) return;
+  const int64_t id = load_id(ids, id_bytes, p);
+  const int row = row_of(p, c, D);
+  if (!TSP_INB(row >= 0 && row < S, status)) return;
+  if (id >= vocab && lane == 0) report_status(status, (int)TSP_ERR_RANGE);
+  const bool there = id >= 0 && id < vocab;
+  const V* src = table + (there ? id : 0) * upr;
+  V* dst = x + (int64_t)row * upr;
+  for (int u0 = blockIdx.y * 32 * LOADS + lane; u0 < upr; u0 += gridDim.y * 32 * LOADS) {
+    V v[LOADS];
 #pragma unroll
-      for (int k = 0; k < LOADS; ++k) {
-        v[k] = V{};
-        if (there && u0 + k * 32 < upr) v[k] = src[u0 + k * 32];
-      }
-#pragma unroll
-      for (int k = 0; k < LOADS; ++k)
-        if (u0 + k * 32 < upr)   // the rows are not read here again: table rows stay in L2
-          __stcs(dst + u0 + k * 32, scale == 1.f ? v[k] : scale_unit<T, V>(v[k], scale));
+    for (int k = 0; k < LOADS; ++k) {
+      v[k] = V{};
+      if (there && u0 + k * 32 < upr) v[k] = src[u0 + k * 32];
     }
+#pragma unroll
+    for (int k = 0; k < LOADS; ++k)
+      if (u0 + k * 32 < upr)   // the rows are not read here again: table rows stay in L2
+        __stcs(dst + u0 + k * 32, scale == 1.f ? v[k] : scale_unit<T, V>(v[k], scale));
   }
 }
 
@@ -87,16 +88,16 @@ template <typename T, typename V>
 tsp_status embed_fwd_t(const void* ids, int id_bytes, const void* table, void* x, int64_t S, int D,
                        int64_t vocab, int d, float scale, cudaStream_t st) {
   const int upr = (int)((int64_t)d * sizeof(T) / sizeof(V));
+  const unsigned gx = (unsigned)((S + 7) / 8);
   const int64_t full = (int64_t)num_sms() * 4;   // CTAs the GPU holds at 64 registers a thread
-  const int64_t gx = std::min<int64_t>((S + 7) / 8, full);
   Prof prof("embed_fwd", st);
   if (gx < full) {   // few positions: short segments, on CTAs of their own
     const int gy = (int)std::min<int64_t>((upr + 63) / 64, full / gx);
-    embed_fwd_kernel<T, V, 2><<<dim3((unsigned)gx, gy), 256, 0, st>>>(
+    embed_fwd_kernel<T, V, 2><<<dim3(gx, gy), 256, 0, st>>>(
         ids, id_bytes, (const V*)table, (V*)x, (int)S, (int)(S / (2 * D)), D, vocab, upr, scale,
         status_word());
   } else {
-    embed_fwd_kernel<T, V, 8><<<(unsigned)gx, 256, 0, st>>>(
+    embed_fwd_kernel<T, V, 8><<<gx, 256, 0, st>>>(
         ids, id_bytes, (const V*)table, (V*)x, (int)S, (int)(S / (2 * D)), D, vocab, upr, scale,
         status_word());
   }
@@ -122,6 +123,7 @@ struct SortArgs {
   int run, runs;          // positions of a run, runs
   int shift, bits;
   int pass;               // 0: from the ids
+  int* starts;            // [2], set to zero for step 2
   int* status;
 };
 
@@ -159,6 +161,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_rank_kernel(const __grid_c
   }
   if (past) report_status(a.status, (int)TSP_ERR_RANGE);
   if (t < 32) place[t] = 0;
+  if (blockIdx.x == 0 && t < 2) a.starts[t] = 0;
   __syncthreads();
   const int i = blockIdx.x * 32 + lane;
   const unsigned me = i < a.S ? word[i] : 0u;
@@ -190,6 +193,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const __grid_
   __shared__ int hist[kBins];
   const int t = threadIdx.x, bins = 1 << a.bits;
   if (t < bins) hist[t] = 0;
+  if (blockIdx.x == 0 && t < 2) a.starts[t] = 0;
   __syncthreads();
   bool past = false;
   const int end = min(a.S, (int)(blockIdx.x + 1) * a.run);
@@ -313,7 +317,7 @@ int run_of(int64_t S) {
 // Step 3 adds those up.  The first warps of the grid write the zero rows of absent
 // tokens, eight rows each, which they look up in the sorted tokens: plain stores
 // next to the other warps' loads.
-constexpr int kSlab = 256, kZeroRows = 8;
+constexpr int kSlab = 256, kZeroRows = 8, kLong = 12;
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_cols(const T* row, int c0, int lane, int d, float (&v)[8]) {
@@ -340,6 +344,8 @@ __device__ __forceinline__ void load_cols(const T* row, int c0, int lane, int d,
     }
   }
 }
+// row = v * s, or row += v * s.  The addition is the memory's (nothing waits for the
+// old value); it is the only one the element gets in a call, so no order matters.
 template <bool VEC>
 __device__ __forceinline__ void store_cols(float* row, int c0, int lane, int d, const float (&v)[8],
                                            float s, bool add) {
@@ -349,18 +355,17 @@ __device__ __forceinline__ void store_cols(float* row, int c0, int lane, int d, 
       const int c = c0 + h * 128 + lane * 4;
       if (c >= d) continue;
       float4* p = reinterpret_cast<float4*>(row + c);
-      float4 o = make_float4(v[4 * h] * s, v[4 * h + 1] * s, v[4 * h + 2] * s, v[4 * h + 3] * s);
-      if (add) {
-        const float4 q = *p;
-        o = make_float4(q.x + o.x, q.y + o.y, q.z + o.z, q.w + o.w);
-      }
-      *p = o;
+      const float4 o = make_float4(v[4 * h] * s, v[4 * h + 1] * s, v[4 * h + 2] * s, v[4 * h + 3] * s);
+      if (add) atomicAdd(p, o);
+      else *p = o;
     }
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int c = c0 + e * 32 + lane;
-      if (c < d) row[c] = (add ? row[c] : 0.f) + v[e] * s;
+      if (c >= d) continue;
+      if (add) atomicAdd(row + c, v[e] * s);
+      else row[c] = v[e] * s;
     }
   }
 }
@@ -368,6 +373,9 @@ __device__ __forceinline__ void store_cols(float* row, int c0, int lane, int d, 
 struct SumArgs {
   const int2* pair;   // sorted (token, row)
   float *table, *part;
+  // chunks where a token starts that goes on, for at most kLong chunks and for
+  // more: how many [2], which [2][nchunks]
+  int *starts, *start;
   int S, vocab, d, chunk, nchunks, nslabs;
   int zero_tasks;   // 0: add to the table rows instead of overwriting them
   float scale;
@@ -447,55 +455,73 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const T* __restrict__ dx
     }
   }
   leave(goes_on);
+  // (the list's order is that of arrival; its entries are joined each by itself)
+  if (opened && goes_on && c0 == 0 && lane == 0) {
+    const int64_t far = (int64_t)j0 + (int64_t)kLong * a.chunk;
+    const int is_long = far < a.S && a.pair[far].x == cur;
+    a.start[is_long * a.nchunks + atomicAdd(a.starts + is_long, 1)] = ch;
+  }
 }
 
-// Step 3: a token that starts in one chunk and ends in a later one.  A CTA a
-// chunk (nearly all see at once that no token starts there and goes on); four
-// slabs at a time, eight warps a slab, each of which adds up every eighth part;
-// then the eight sums in order.
+// Step 3: a token that starts in one chunk and ends in a later one (step 2 has
+// listed the chunks where one starts): its parts added in chunk order, a warp a
+// token and slab.  The few tokens of more than kLong chunks get a CTA a slab, whose
+// warps add up every eighth part each, then the eight sums in order.
+// acc += the parts of token `tok` in chunks k, k + step, ...
 template <bool VEC>
-__global__ void __launch_bounds__(1024) embed_join_kernel(const __grid_constant__ SumArgs a) {
-  __shared__ float sums[32][kSlab];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp & 7;
-  const int ch = blockIdx.x;
-  const int j0 = ch * a.chunk, end = j0 + a.chunk;   // end < S: there is a chunk after this one
-  const int tok = a.pair[end - 1].x, next = a.pair[end].x, start = a.pair[j0].x;
-  const int prev = j0 > 0 ? a.pair[j0 - 1].x : -1;
-  if (tok >= a.vocab || next != tok || (start == tok && prev == tok)) return;
-  for (int s0 = 0; s0 < a.nslabs; s0 += 4) {
-    const int c0 = (s0 + (warp >> 3)) * kSlab;
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (part == 0) load_cols<float, VEC>(a.part + ((int64_t)2 * ch + 1) * a.d, c0, lane, a.d, acc);
-    for (int k = ch + 1 + part; k < a.nchunks; k += 32) {
-      float v[4][8];
-      bool in[4];
+__device__ __forceinline__ void add_parts(const SumArgs& a, int tok, int k, int step, int c0, int lane,
+                                          float (&acc)[8]) {
+  for (; k < a.nchunks; k += 4 * step) {
+    float v[4][8];
+    bool in[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int q = k + u * 8;
-        in[u] = q < a.nchunks && a.pair[q * a.chunk].x == tok;
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (in[u]) load_cols<float, VEC>(a.part + (int64_t)2 * (k + u * 8) * a.d, c0, lane, a.d, v[u]);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (!in[u]) continue;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += v[u][e];
-      }
-      if (!in[3]) break;
+    for (int u = 0; u < 4; ++u) {
+      const int q = k + u * step;
+      in[u] = q < a.nchunks && a.pair[q * a.chunk].x == tok;
     }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (in[u]) load_cols<float, VEC>(a.part + (int64_t)2 * (k + u * step) * a.d, c0, lane, a.d, v[u]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (!in[u]) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] += v[u][e];
+    }
+    if (!in[3]) return;
+  }
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(256) embed_join_kernel(const __grid_constant__ SumArgs a) {
+  __shared__ float sums[8][kSlab];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t n_short = (int64_t)a.starts[0] * a.nslabs, n_long = (int64_t)a.starts[1] * a.nslabs;
+  for (int64_t task = blockIdx.x; task < n_long; task += gridDim.x) {
+    const int ch = a.start[a.nchunks + task / a.nslabs], c0 = (int)(task % a.nslabs) * kSlab;
+    const int tok = a.pair[(ch + 1) * a.chunk].x;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (warp == 0) load_cols<float, VEC>(a.part + ((int64_t)2 * ch + 1) * a.d, c0, lane, a.d, acc);
+    add_parts<VEC>(a, tok, ch + 1 + warp, 8, c0, lane, acc);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sums[warp][e * 32 + lane] = acc[e];
     __syncthreads();
-    if (part == 0) {
+    if (warp == 0) {
       for (int w = 1; w < 8; ++w) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += sums[warp + w][e * 32 + lane];
+        for (int e = 0; e < 8; ++e) acc[e] += sums[w][e * 32 + lane];
       }
       store_cols<VEC>(a.table + (int64_t)tok * a.d, c0, lane, a.d, acc, a.scale, a.zero_tasks == 0);
     }
     __syncthreads();
+  }
+  for (int64_t task = (int64_t)blockIdx.x * 8 + warp; task < n_short; task += (int64_t)gridDim.x * 8) {
+    const int ch = a.start[task / a.nslabs], c0 = (int)(task % a.nslabs) * kSlab;
+    const int tok = a.pair[(ch + 1) * a.chunk].x;
+    float acc[8];
+    load_cols<float, VEC>(a.part + ((int64_t)2 * ch + 1) * a.d, c0, lane, a.d, acc);
+    add_parts<VEC>(a, tok, ch + 1, 1, c0, lane, acc);
+    store_cols<VEC>(a.table + (int64_t)tok * a.d, c0, lane, a.d, acc, a.scale, a.zero_tasks == 0);
   }
 }
 
@@ -510,7 +536,7 @@ int chunk_of(int64_t S, int d) {
 
 struct BwdLayout {
   int2* pair[2];
-  int* count;
+  int *count, *start;
   float* part;
   size_t bytes;
 };
@@ -524,8 +550,9 @@ BwdLayout bwd_layout(int64_t S, int d, uint8_t* base) {
   };
   for (int k = 0; k < 2; ++k) L.pair[k] = (int2*)take((size_t)S * 8);
   L.count = (int*)take((size_t)((S + run_of(S) - 1) / run_of(S)) * kBins * 4);
-  const int c = chunk_of(S, d);
-  L.part = (float*)take((size_t)((S + c - 1) / c) * 2 * d * 4);
+  const int64_t chunks = (S + chunk_of(S, d) - 1) / chunk_of(S, d);
+  L.start = (int*)take((size_t)(2 + 2 * chunks) * 4);
+  L.part = (float*)take((size_t)chunks * 2 * d * 4);
   L.bytes = off;
   return L;
 }
@@ -537,7 +564,8 @@ tsp_status embed_sum_t(const void* dx, const SumArgs& a, cudaStream_t st) {
   embed_sum_kernel<T, VEC><<<(unsigned)((tasks + 7) / 8), 256, 0, st>>>((const T*)dx, a);
   TSP_CUDA_TRY(cudaGetLastError());
   if (a.nchunks > 1) {
-    embed_join_kernel<VEC><<<(unsigned)(a.nchunks - 1), 1024, 0, st>>>(a);
+    const int64_t most = (int64_t)(a.nchunks - 1) * a.nslabs;   // (a CTA each if all were long)
+    embed_join_kernel<VEC><<<(unsigned)std::min<int64_t>(most, num_sms() * 4), 256, 0, st>>>(a);
     TSP_CUDA_TRY(cudaGetLastError());
   }
   return TSP_OK;
@@ -578,6 +606,7 @@ tsp_status launch_embed_bwd(const void* ids, int id_bytes, const void* dx, int d
   s.vocab = (int)vocab;
   for (int k = 0; k < 2; ++k) s.pair[k] = L.pair[k];
   s.count = L.count;
+  s.starts = L.start;
   s.status = status_word();
   s.pass = s.shift = 0;
   int nb = 1;   // bits of the largest token, `vocab` itself
@@ -606,6 +635,8 @@ tsp_status launch_embed_bwd(const void* ids, int id_bytes, const void* dx, int d
   a.zero_tasks = accumulate ? 0 : (int)((vocab + kZeroRows - 1) / kZeroRows);
   a.table = dtable;
   a.part = L.part;
+  a.starts = L.start;
+  a.start = L.start + 2;
   a.S = (int)S;
   a.vocab = (int)vocab;
   a.d = d;

@@ -509,7 +509,7 @@ tsp_status tsp_rank_attn_bwd_finish(const tsp_cfg* cfg, int32_t r, const void* x
  *   rows are left alone (a table tied to the output projection).  dx_z is
  *   what tsp_stack_bwd leaves (dx_dtype TSP_F32) or bf16 (TSP_BF16).  The
  *   positions are sorted by token first and each sum runs in the order of the
- *   positions, in fp32, so equal calls give equal bits; nothing is atomic.
+ *   positions, in fp32, so equal calls give equal bits.
  *
  *   ids       [S] global token order, id_bytes 4 (int32) or 8 (int64); needs
  *             only its own alignment.  id < 0: padding -- a zero row of x_z,
