@@ -51,7 +51,7 @@ struct Args {
   int64_t end[kTensors];   // chunks of tensors 0..i
   int count;
   float b1, c1, b2, c2;    // beta, 1 - beta
-  float eps;
+  float eps, neg_zero;
   float lr, step_size, fix;   // lr, lr / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
   double dbeta1, dbeta2;
   const float* lr_dev;
@@ -68,33 +68,73 @@ __device__ double power(double x, int64_t n) {
   return r;
 }
 
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, int64_t i, int k, float (&v)[4]) {
-  if (k == 4) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 f = *reinterpret_cast<const float4*>(p + i);
-      v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-    } else {
-      const uint2 u = *reinterpret_cast<const uint2*>(p + i);
-      v[0] = lo2<T>(u.x); v[1] = hi2<T>(u.x); v[2] = lo2<T>(u.y); v[3] = hi2<T>(u.y);
-    }
-  } else {
+// The k (of four) elements at p; ALL: all four, one access.
+template <bool ALL, typename T>
+__device__ __forceinline__ void load4(const T* p, int k, float (&v)[4]) {
+  if constexpr (!ALL) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = e < k ? to_f<T>(p[i + e]) : 0.f;
+    for (int e = 0; e < 4; ++e) v[e] = e < k ? to_f<T>(p[e]) : 0.f;
+  } else if constexpr (sizeof(T) == 4) {
+    const float4 f = *reinterpret_cast<const float4*>(p);
+    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    v[0] = lo2<T>(u.x); v[1] = hi2<T>(u.x); v[2] = lo2<T>(u.y); v[3] = hi2<T>(u.y);
   }
 }
-template <typename T>
-__device__ __forceinline__ void store4(T* p, int64_t i, int k, const float (&v)[4]) {
-  if (k == 4) {
-    if constexpr (sizeof(T) == 4)
-      *reinterpret_cast<float4*>(p + i) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-      *reinterpret_cast<uint2*>(p + i) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
-  } else {
+template <bool ALL, typename T>
+__device__ __forceinline__ void store4(T* p, int k, const float (&v)[4]) {
+  if constexpr (!ALL) {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (e < k) p[i + e] = from_f<T>(v[e]);
+      if (e < k) p[e] = from_f<T>(v[e]);
+  } else if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
   }
+}
+template <bool ALL>
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int k) {
+  if constexpr (ALL) return *reinterpret_cast<const uint32_t*>(p);
+  uint32_t u = 0;
+  for (int e = 0; e < k; ++e) u |= (uint32_t)p[e] << (8 * e);
+  return u;
+}
+template <bool ALL>
+__device__ __forceinline__ void store_codes(uint8_t* p, int k, uint32_t u) {
+  if constexpr (ALL) {
+    *reinterpret_cast<uint32_t*>(p) = u;
+    return;
+  }
+  for (int e = 0; e < k; ++e) p[e] = (uint8_t)(u >> (8 * e));
+}
+
+// Four elements, two an instruction.  The compiler joins a packed product with the
+// sum that follows it into one rounding; a product written as a * b + nz, nz a -0
+// that it cannot see (an argument of the kernel), rounds as the product and stays
+// apart.
+__device__ __forceinline__ void mul4(float (&a)[4], const float (&b)[4], float nz) {
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
+    const float2 r = ffma2(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]), make_float2(nz, nz));
+    a[e] = r.x; a[e + 1] = r.y;
+  }
+}
+__device__ __forceinline__ void mul4(float (&a)[4], float s, float nz) {
+  const float b[4] = {s, s, s, s};
+  mul4(a, b, nz);
+}
+__device__ __forceinline__ void add4(float (&a)[4], const float (&b)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
+    const float2 r = fadd2(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
+    a[e] = r.x; a[e + 1] = r.y;
+  }
+}
+__device__ __forceinline__ void add4(float (&a)[4], float s) {
+  const float b[4] = {s, s, s, s};
+  add4(a, b);
 }
 
 // four e4m3 codes (lowest element in the low byte) and their values
@@ -113,31 +153,15 @@ __device__ __forceinline__ uint32_t f_to_codes(const float (&v)[4]) {
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
 }
-__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int64_t i, int k) {
-  if (k == 4) return *reinterpret_cast<const uint32_t*>(p + i);
-  uint32_t u = 0;
-  for (int e = 0; e < k; ++e) u |= (uint32_t)p[i + e] << (8 * e);
-  return u;
-}
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t i, int k, uint32_t u) {
-  if (k == 4) {
-    *reinterpret_cast<uint32_t*>(p + i) = u;
-    return;
-  }
-  for (int e = 0; e < k; ++e) p[i + e] = (uint8_t)(u >> (8 * e));
-}
-// the larger of a and b; a NaN wins, so that it reaches the block's scale
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-// The warp's 128 values as codes and a scale (written by lane 0).
+// The warp's 128 values as codes and a scale (written by lane 0).  The largest
+// magnitude is found on the bits, whose order is that of non-negative floats with
+// NaN above infinity: one instruction for the warp, and a NaN reaches the scale.
 template <bool ROOT>
 __device__ __forceinline__ uint32_t quantise(const float (&x)[4], float* scale, int lane) {
-  float top = max_nan(max_nan(fabsf(x[0]), fabsf(x[1])), max_nan(fabsf(x[2]), fabsf(x[3])));
+  uint32_t bits = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  for (int e = 0; e < 4; ++e) bits = max(bits, __float_as_uint(x[e]) & 0x7fffffffu);
+  const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, bits));
   const bool live = !(top < kScaleFloor);
   const float inv = live ? __fmul_rn(448.f, __frcp_rn(top)) : 0.f;
   if (lane == 0) *scale = live ? __fmul_rn(top, 1.f / 448.f) : 0.f;
@@ -151,30 +175,135 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[4], float* scale, 
   return f_to_codes(q);
 }
 
-template <typename T, int BITS>
-__global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Args a) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float lr = a.lr, step_size = a.step_size, fix = a.fix;
-  if (a.lr_dev || a.step_dev) {
-    __shared__ float sh[3];
-    if (threadIdx.x == 0) {
-      const double l = a.lr_dev ? (double)*a.lr_dev : (double)a.lr;
-      sh[0] = (float)l;
-      if (a.step_dev) {
-        const int64_t t = *a.step_dev;
-        sh[1] = (float)(l / (1.0 - power(a.dbeta1, t)));
-        sh[2] = (float)(1.0 / sqrt(1.0 - power(a.dbeta2, t)));
-      } else {   // the host folded lr = 1 into step_size
-        sh[1] = (float)(l * (double)a.step_size);
-        sh[2] = a.fix;
+struct Step {
+  float lr, step_size, fix, gscale;
+};
+
+// One warp's 512 elements of a tensor from `first` on, in groups of 128 (four a
+// lane), kBatch groups' loads ahead of their use.  ALL: none is past the end.
+constexpr int kGroups = 4, kBatch = 2;
+
+template <typename T, int BITS, bool ALL>
+__device__ __forceinline__ bool update(const Args& a, const Tensor& t, int64_t first, int lane,
+                                       const Step& s) {
+  const float nz = a.neg_zero;
+  const float keep = __fsub_rn(1.f, __fmul_rn(s.lr, t.wd));
+  const int64_t at = first + lane * 4;
+  const float* gp = t.g + at;
+  T* wp = (T*)t.w + at;
+  float* pp = t.master ? t.master + at : nullptr;
+  __half* hp = t.prep ? t.prep + at : nullptr;
+  float *m32 = (float*)t.m + at, *v32 = (float*)t.v + at;
+  uint8_t *mc = (uint8_t*)t.m + at, *vc = (uint8_t*)t.v + at;
+  float *ms = t.ms + (first >> 7), *vs = t.vs + (first >> 7);
+  bool bad = false;
+#pragma unroll
+  for (int u0 = 0; u0 < kGroups; u0 += kBatch) {
+    float g[kBatch][4], p[kBatch][4], m[kBatch][4], v[kBatch][4], sm[kBatch], sv[kBatch];
+    uint32_t mq[kBatch], vq[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int o = (u0 + u) * 128;
+      const int k = ALL ? 4 : (int)max((int64_t)0, min((int64_t)4, t.n - at - o));
+      load4<ALL>(gp + o, k, g[u]);
+      if (pp) load4<ALL>(pp + o, k, p[u]);
+      else load4<ALL>(wp + o, k, p[u]);
+      if constexpr (BITS == 32) {
+        load4<ALL>(m32 + o, k, m[u]);
+        load4<ALL>(v32 + o, k, v[u]);
+      } else {
+        mq[u] = load_codes<ALL>(mc + o, k);
+        vq[u] = load_codes<ALL>(vc + o, k);
+        const bool there = ALL || first + o < t.n;
+        sm[u] = there ? ms[u0 + u] : 0.f;
+        sv[u] = there ? vs[u0 + u] : 0.f;
       }
     }
-    __syncthreads();
-    lr = sh[0];
-    step_size = sh[1];
-    fix = sh[2];
+    __syncwarp();   // every lane has read the old scales
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int o = (u0 + u) * 128;
+      if (!ALL && first + o >= t.n) break;
+      const int k = ALL ? 4 : (int)max((int64_t)0, min((int64_t)4, t.n - at - o));
+      if constexpr (BITS == 8) {
+        codes_to_f(mq[u], m[u]);
+        codes_to_f(vq[u], v[u]);
+        mul4(m[u], sm[u], nz);
+        mul4(v[u], sv[u], nz);
+        mul4(v[u], v[u], nz);
+      }
+      mul4(g[u], s.gscale, nz);
+      float x[4], root[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = g[u][e];
+      mul4(x, a.c1, nz);
+      mul4(m[u], a.b1, nz);
+      add4(m[u], x);
+      mul4(g[u], g[u], nz);
+      mul4(g[u], a.c2, nz);
+      mul4(v[u], a.b2, nz);
+      add4(v[u], g[u]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = root[e] = __fsqrt_rn(v[u][e]);
+      mul4(x, s.fix, nz);
+      add4(x, a.eps);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = __fdiv_rn(m[u][e], x[e]);
+      mul4(x, -s.step_size, nz);
+      mul4(p[u], keep, nz);
+      add4(p[u], x);
+      if constexpr (BITS == 32) {
+        store4<ALL>(m32 + o, k, m[u]);
+        store4<ALL>(v32 + o, k, v[u]);
+      } else {
+        if constexpr (!ALL) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (e >= k) m[u][e] = root[e] = 0.f;
+        }
+        store_codes<ALL>(mc + o, k, quantise<false>(m[u], ms + u0 + u, lane));
+        store_codes<ALL>(vc + o, k, quantise<true>(root, vs + u0 + u, lane));
+      }
+      if (pp) store4<ALL>(pp + o, k, p[u]);
+      if constexpr (sizeof(T) == 2) {
+        if (hp) {
+          // the operand copy is made of the rounded weight, like the one
+          // tsp_block_weights_prepare makes
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[u][e] = to_f<T>(from_f<T>(p[u][e]));
+            bad |= (ALL || e < k) && f16_bad(p[u][e]);
+          }
+          store4<ALL>(hp + o, k, p[u]);
+        }
+      }
+      store4<ALL>(wp + o, k, p[u]);
+    }
   }
-  const float gs = a.gscale ? *a.gscale : 1.f;
+  return bad;
+}
+
+template <typename T, int BITS>
+__global__ void __launch_bounds__(256, BITS == 8 ? 4 : 3) adamw_kernel(const __grid_constant__ Args a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Step s = {a.lr, a.step_size, a.fix, a.gscale ? *a.gscale : 1.f};
+  if (a.lr_dev || a.step_dev) {
+    __shared__ Step shared;
+    if (threadIdx.x == 0) {
+      const double lr = a.lr_dev ? (double)*a.lr_dev : (double)a.lr;
+      s.lr = (float)lr;
+      if (a.step_dev) {
+        const int64_t t = *a.step_dev;
+        s.step_size = (float)(lr / (1.0 - power(a.dbeta1, t)));
+        s.fix = (float)(1.0 / sqrt(1.0 - power(a.dbeta2, t)));
+      } else {   // the host folded lr = 1 into step_size
+        s.step_size = (float)(lr * (double)a.step_size);
+      }
+      shared = s;
+    }
+    __syncthreads();
+    s = shared;
+  }
   bool bad = false;
   const int64_t chunks = a.end[a.count - 1];
   for (int64_t ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
@@ -185,67 +314,8 @@ __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Args
     }
     const Tensor& t = a.t[lo];
     const int64_t first = (ch - (lo > 0 ? a.end[lo - 1] : 0)) * kChunk + warp * 512;
-    const float keep = __fsub_rn(1.f, __fmul_rn(lr, t.wd));
-    T* w = (T*)t.w;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t b0 = first + u * 128;
-      if (b0 >= t.n) break;
-      const int64_t i = b0 + lane * 4;
-      const int k = (int)max((int64_t)0, min((int64_t)4, t.n - i));
-      float g[4], m[4], v[4], p[4];
-      load4<float>(t.g, i, k, g);
-      if (t.master) load4<float>(t.master, i, k, p);
-      else load4<T>(w, i, k, p);
-      if constexpr (BITS == 32) {
-        load4<float>((const float*)t.m, i, k, m);
-        load4<float>((const float*)t.v, i, k, v);
-      } else {
-        codes_to_f(load_codes((const uint8_t*)t.m, i, k), m);
-        codes_to_f(load_codes((const uint8_t*)t.v, i, k), v);
-        const float sm = t.ms[b0 >> 7], sv = t.vs[b0 >> 7];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          m[e] = __fmul_rn(m[e], sm);
-          v[e] = __fmul_rn(v[e], sv);
-          v[e] = __fmul_rn(v[e], v[e]);
-        }
-      }
-      float root[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        g[e] = __fmul_rn(g[e], gs);
-        m[e] = __fadd_rn(__fmul_rn(m[e], a.b1), __fmul_rn(g[e], a.c1));
-        v[e] = __fadd_rn(__fmul_rn(v[e], a.b2), __fmul_rn(__fmul_rn(g[e], g[e]), a.c2));
-        root[e] = __fsqrt_rn(v[e]);
-        const float q = __fdiv_rn(m[e], __fadd_rn(__fmul_rn(root[e], fix), a.eps));
-        p[e] = __fsub_rn(__fmul_rn(p[e], keep), __fmul_rn(step_size, q));
-      }
-      if constexpr (BITS == 32) {
-        store4<float>((float*)t.m, i, k, m);
-        store4<float>((float*)t.v, i, k, v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e >= k) m[e] = root[e] = 0.f;
-        __syncwarp();   // every lane has read the old scales
-        store_codes((uint8_t*)t.m, i, k, quantise<false>(m, t.ms + (b0 >> 7), lane));
-        store_codes((uint8_t*)t.v, i, k, quantise<true>(root, t.vs + (b0 >> 7), lane));
-      }
-      if (t.master) store4<float>(t.master, i, k, p);
-      if constexpr (sizeof(T) == 2) {
-        // the operand copy is made of the rounded weight, like the one
-        // tsp_block_weights_prepare makes
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = to_f<T>(from_f<T>(p[e]));
-        if (t.prep) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) bad |= e < k && f16_bad(p[e]);
-          store4<__half>(t.prep, i, k, p);
-        }
-      }
-      store4<T>(w, i, k, p);
-    }
+    bad |= first + 512 <= t.n ? update<T, BITS, true>(a, t, first, lane, s)
+                              : update<T, BITS, false>(a, t, first, lane, s);
   }
   if (bad) report_status(a.status, (int)TSP_ERR_RANGE);
 }
@@ -260,6 +330,7 @@ tsp_status launch_adamw(const tsp_adamw_tensor* ts, int count, const tsp_adamw_h
   a.b2 = (float)h->beta2;
   a.c2 = (float)(1.0 - h->beta2);
   a.eps = (float)h->eps;
+  a.neg_zero = -0.f;
   a.lr = (float)h->lr;
   a.dbeta1 = h->beta1;
   a.dbeta2 = h->beta2;

@@ -68,17 +68,6 @@ __device__ __forceinline__ void pairs(F2 two, F1 one) {
     for (int e = 0; e < N; ++e) one(e);
   }
 }
-__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\t"
-      "mov.b64 rb, {%4, %5};\n\t"
-      "mul.rn.f32x2 rd, ra, rb;\n\t"
-      "mov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
 template <int N>   // a = a * b
 __device__ __forceinline__ void mul_n(float (&a)[N], const float (&b)[N]) {
   pairs<N>([&](int e) {
