@@ -574,7 +574,8 @@ tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f
  *   g = g * gscale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
  *   w = w (1 - lr weight_decay)
  *       - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * in fp32, each elementary operation rounded by itself.
+ * in fp32, each elementary operation rounded by itself (with 8-bit states the
+ * quotient by two half spacings at most).
  *
  * tsp_adamw_tensor (a host array of `count`; the pointers are device pointers):
  *   n        elements, >= 0 (0: skipped, its pointers may be NULL)
