@@ -10,6 +10,7 @@ import ctypes
 import os
 from dataclasses import dataclass
 
+import numpy as np
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -584,40 +585,47 @@ def rank_attn_bwd_finish(cfg: Cfg, r: int, x_r, g_attn, da_r, dh_r, dx_r, dg_att
 
 # ---- around the stack: embedding, sub-layer norms and residual, optimizer ----
 
-class _On:
-    """Makes ``dev`` and ``stream`` (default: the device's current one) current
-    for a call, so that the buffers it allocates belong to the stream they are
-    used on; gives the stream's handle."""
-    __slots__ = ("dev", "stream", "ctx")
+# the handle of a device's current stream, without a Stream object (or by one)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    def __init__(self, dev, stream):
-        if dev.type != "cuda":
+
+class _On:
+    """Makes device ``index`` and ``stream`` (default: the device's current one)
+    current for a call, so that the buffers it allocates belong to the stream
+    they are used on; gives the stream's handle."""
+    __slots__ = ("index", "stream", "ctx")
+
+    def __init__(self, index, stream):
+        if index < 0:
             raise ValueError("tensors must live on the GPU")
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
-        self.dev, self.stream, self.ctx = dev, stream, None
+        if stream is not None and stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{index}")
+        self.index, self.stream, self.ctx = index, stream, None
 
     def __enter__(self):
-        st = torch.cuda.current_stream(self.dev) if self.stream is None else self.stream
-        if self.stream is not None or self.dev.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.stream(st)
-            self.ctx.__enter__()
-        return st.cuda_stream
+        if self.stream is None:
+            if self.index == torch.cuda.current_device():
+                return _raw_stream(self.index)
+            self.stream = torch.cuda.current_stream(self.index)
+        self.ctx = torch.cuda.stream(self.stream)
+        self.ctx.__enter__()
+        return self.stream.cuda_stream
 
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
 
 
-def _arg(name, t, shape, dtype, dev):
+def _arg(name, t, shape, dtype, index):
     """data_ptr of a dense tensor of this shape, type and device (None: NULL)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} of "
                          f"shape {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the other tensors are on {dev}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on the device of the other tensors")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -646,13 +654,13 @@ def embed_fwd(ids, table, D: int = 1, scale: float = 1.0, out=None, stream=None)
     id_bytes = _ids_arg(ids)
     if table.dim() != 2:
         raise ValueError("table must be [V, d]")
-    S, (V, d), dt, dev = ids.shape[0], table.shape, table.dtype, table.device
+    (S,), (V, d), dt, index = ids.shape, table.shape, table.dtype, table.get_device()
     e = _enum("table", dt)
-    pi, pt = _arg("ids", ids, (S,), ids.dtype, dev), _arg("table", table, (V, d), dt, dev)
-    po = _arg("out", out, (S, d), dt, dev)
-    with _On(dev, stream) as st:
-        if out is None:
-            out = empty((S, d), dt, dev)
+    pi, pt = _arg("ids", ids, (S,), ids.dtype, index), _arg("table", table, (V, d), dt, index)
+    po = _arg("out", out, (S, d), dt, index)
+    with _On(index, stream) as st:
+        if po is None:
+            out = empty((S, d), dt, table.device)
             po = out.data_ptr()
         _check(load().tsp_embed_fwd(pi, id_bytes, pt, po, S, D, V, d, scale, e, st),
                "tsp_embed_fwd")
@@ -673,12 +681,12 @@ def embed_bwd(ids, dx_z, V: int, D: int = 1, scale: float = 1.0, out=None,
         raise ValueError("dx_z must be [S, d]")
     if accumulate and out is None:
         raise ValueError("accumulate needs the gradient to add to in out")
-    S, d, dt, dev = ids.shape[0], dx_z.shape[1], dx_z.dtype, dx_z.device
-    e = _enum("dx_z", dt)
-    pi, px = _arg("ids", ids, (S,), ids.dtype, dev), _arg("dx_z", dx_z, (S, d), dt, dev)
-    po = _arg("out", out, (V, d), torch.float32, dev)
-    with _On(dev, stream) as st:
-        if out is None:
+    (S,), d, dt, dev = ids.shape, dx_z.shape[1], dx_z.dtype, dx_z.device
+    e, index = _enum("dx_z", dt), dx_z.get_device()
+    pi, px = _arg("ids", ids, (S,), ids.dtype, index), _arg("dx_z", dx_z, (S, d), dt, index)
+    po = _arg("out", out, (V, d), torch.float32, index)
+    with _On(index, stream) as st:
+        if po is None:
             out = empty((V, d), torch.float32, dev)
             po = out.data_ptr()
         lib = load()
@@ -697,31 +705,31 @@ def norm_residual_fwd(f, x, g_post=None, g_pre=None, gate=None, scale: float = 1
     and the gains in one type, x and h in fp32 or that type; ``h`` may be x."""
     if f.dim() != 2:
         raise ValueError("f must be [rows, n]")
-    shape, dt, dev = f.shape, f.dtype, f.device
+    shape, dt, dev, index = f.shape, f.dtype, f.device, f.get_device()
     rows, n = shape
-    e, es = _enum("f", dt), _enum("x", x.dtype)
-    pf, px = _arg("f", f, shape, dt, dev), _arg("x", x, shape, x.dtype, dev)
-    pz = _arg("gate", gate, shape, dt, dev)
-    pp, pq = _arg("g_post", g_post, (n,), dt, dev), _arg("g_pre", g_pre, (n,), dt, dev)
-    ph, pb = _arg("h", h, shape, x.dtype, dev), _arg("b", b, shape, dt, dev)
-    rf = rh = None
-    with _On(dev, stream) as st:
-        if h is None:
-            h = empty(shape, x.dtype, dev)
+    ds = x.dtype
+    e, es = _enum("f", dt), _enum("x", ds)
+    pf, px = _arg("f", f, shape, dt, index), _arg("x", x, shape, ds, index)
+    pz = _arg("gate", gate, shape, dt, index)
+    pp, pq = _arg("g_post", g_post, (n,), dt, index), _arg("g_pre", g_pre, (n,), dt, index)
+    ph, pb = _arg("h", h, shape, ds, index), _arg("b", b, shape, dt, index)
+    rf = rh = prf = prh = None
+    with _On(index, stream) as st:
+        if ph is None:
+            h = empty(shape, ds, dev)
             ph = h.data_ptr()
-        if b is None and pq is not None:
+        if pq is not None and pb is None:
             b = empty(shape, dt, dev)
             pb = b.data_ptr()
-        if with_rstd:
-            rf = None if pp is None else empty((rows,), torch.float32, dev)
-            rh = None if pq is None else empty((rows,), torch.float32, dev)
-        _check(load().tsp_norm_residual_fwd(pf, px, pz, pp, pq, ph, pb, _addr(rf), _addr(rh), rows,
-                                            n, scale, eps, e, es, st), "tsp_norm_residual_fwd")
+        if with_rstd and pp is not None:
+            rf = empty((rows,), torch.float32, dev)
+            prf = rf.data_ptr()
+        if with_rstd and pq is not None:
+            rh = empty((rows,), torch.float32, dev)
+            prh = rh.data_ptr()
+        _check(load().tsp_norm_residual_fwd(pf, px, pz, pp, pq, ph, pb, prf, prh, rows, n, scale,
+                                            eps, e, es, st), "tsp_norm_residual_fwd")
     return (h, b, rf, rh) if with_rstd else (h, b)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
 
 
 def norm_residual_bwd_workspace_bytes(rows: int, n: int) -> int:
@@ -735,37 +743,41 @@ def norm_residual_bwd(dh, db, f, h, g_post=None, g_pre=None, rstd_f=None, rstd_h
     and rstd_h belong to g_pre, rstd_f to g_post.  ``dx`` may be dh."""
     if f.dim() != 2:
         raise ValueError("f must be [rows, n]")
-    shape, dt, dev, f32 = f.shape, f.dtype, f.device, torch.float32
+    shape, dt, dev, index, f32 = f.shape, f.dtype, f.device, f.get_device(), torch.float32
     rows, n = shape
     if g_pre is None:
         h = None                  # only the pre-norm's backward reads it
-    e = _enum("f", dt)
     hs = f32 if h is None else h.dtype
-    es = _enum("h", hs)
-    pf, ph = _arg("f", f, shape, dt, dev), _arg("h", h, shape, hs, dev)
-    pdh, pdb = _arg("dh", dh, shape, f32, dev), _arg("db", db, shape, f32, dev)
-    pz = _arg("gate", gate, shape, dt, dev)
-    pp, pq = _arg("g_post", g_post, (n,), dt, dev), _arg("g_pre", g_pre, (n,), dt, dev)
-    prf, prh = _arg("rstd_f", rstd_f, (rows,), f32, dev), _arg("rstd_h", rstd_h, (rows,), f32, dev)
-    pdx = _arg("dx", dx, shape, f32, dev)
+    e, es = _enum("f", dt), _enum("h", hs)
+    pf, ph = _arg("f", f, shape, dt, index), _arg("h", h, shape, hs, index)
+    pdh, pdb = _arg("dh", dh, shape, f32, index), _arg("db", db, shape, f32, index)
+    pz = _arg("gate", gate, shape, dt, index)
+    pp, pq = _arg("g_post", g_post, (n,), dt, index), _arg("g_pre", g_pre, (n,), dt, index)
+    prf, prh = _arg("rstd_f", rstd_f, (rows,), f32, index), _arg("rstd_h", rstd_h, (rows,), f32, index)
+    pdx = _arg("dx", dx, shape, f32, index)
+    pdz = pdp = pdq = None
     out = {}
-    with _On(dev, stream) as st:
+    with _On(index, stream) as st:
         lib = load()
-        out["dx"] = empty(shape, f32, dev) if dx is None else dx
-        out["df"] = empty(shape, dt, dev)
-        if gate is not None:
+        if pdx is None:
+            dx = empty(shape, f32, dev)
+            pdx = dx.data_ptr()
+        out["dx"], out["df"] = dx, empty(shape, dt, dev)
+        if pz is not None:
             out["dgate"] = empty(shape, dt, dev)
-        if g_post is not None:
+            pdz = out["dgate"].data_ptr()
+        if pp is not None:
             out["dg_post"] = empty((n,), f32, dev)
-        if g_pre is not None:
+            pdp = out["dg_post"].data_ptr()
+        if pq is not None:
             out["dg_pre"] = empty((n,), f32, dev)
-        if ws is None and (g_post is not None or g_pre is not None):
+            pdq = out["dg_pre"].data_ptr()
+        if ws is None and (pp is not None or pq is not None):
             ws = _ws(lib.tsp_norm_residual_bwd_workspace_bytes(rows, n), dev)
-        _check(lib.tsp_norm_residual_bwd(pdh, pdb, pf, pz, ph, pp, pq, prf, prh,
-                                         out["dx"].data_ptr(), out["df"].data_ptr(),
-                                         _addr(out.get("dgate")), _addr(out.get("dg_post")),
-                                         _addr(out.get("dg_pre")), rows, n, scale, e, es,
-                                         _addr(ws), 0 if ws is None else ws.numel(), st),
+        _check(lib.tsp_norm_residual_bwd(pdh, pdb, pf, pz, ph, pp, pq, prf, prh, pdx,
+                                         out["df"].data_ptr(), pdz, pdp, pdq, rows, n, scale, e, es,
+                                         None if ws is None else ws.data_ptr(),
+                                         0 if ws is None else ws.numel(), st),
                "tsp_norm_residual_bwd")
     return out
 
@@ -805,6 +817,7 @@ class AdamW:
         if state_bits not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
         n_t, dt, dev = len(self.params), self.params[0].dtype, self.params[0].device
+        index = self.params[0].get_device()
         self.dtype, self.device, self.state_bits = _enum("params", dt), dev, state_bits
         self.betas, self.eps, self.t = (float(betas[0]), float(betas[1])), float(eps), 0
         if isinstance(weight_decay, (int, float)):
@@ -836,17 +849,20 @@ class AdamW:
         self._arr = (AdamwTensor * n_t)()
         for i, p in enumerate(self.params):
             t = self._arr[i]
-            t.n, t.w = p.numel(), _arg(f"params[{i}]", p, p.shape, dt, dev)
+            t.n, t.w = p.numel(), _arg(f"params[{i}]", p, p.shape, dt, index)
             for name, x, dtype in (("m", self.m[i], code), ("v", self.v[i], code),
                                    ("master", self.master[i], f32),
                                    ("prep", self.prep[i], torch.float16)):
                 if x is not None and x.numel() != p.numel():
                     raise ValueError(f"{name}[{i}] has {x.numel()} elements, its tensor {p.numel()}")
-                setattr(t, name, _arg(f"{name}[{i}]", x, None if x is None else x.shape, dtype, dev))
-            t.m_scale = _arg(f"m_scale[{i}]", self.m_scale[i], blocks[i], f32, dev)
-            t.v_scale = _arg(f"v_scale[{i}]", self.v_scale[i], blocks[i], f32, dev)
+                setattr(t, name, _arg(f"{name}[{i}]", x, None if x is None else x.shape, dtype, index))
+            t.m_scale = _arg(f"m_scale[{i}]", self.m_scale[i], blocks[i], f32, index)
+            t.v_scale = _arg(f"v_scale[{i}]", self.v_scale[i], blocks[i], f32, index)
             t.weight_decay = float(weight_decay[i])
         self._sizes = [p.numel() for p in self.params]
+        # the gradients' addresses in the array, set by every step
+        words = ctypes.sizeof(AdamwTensor) // 8
+        self._g = np.frombuffer(self._arr, np.uint64).reshape(n_t, words)[:, AdamwTensor.g.offset // 8]
 
     def step(self, grads, lr, step=None, gscale=None, stream=None):
         """One update from the fp32 ``grads`` (one for each tensor, same sizes).
@@ -855,29 +871,28 @@ class AdamW:
         one-element int64 GPU tensor; ``gscale``: a one-element fp32 GPU tensor
         that the gradients are multiplied by.  Tensors are read when the kernel
         runs, so a captured step can be replayed with new values in them."""
-        arr, dev, f32 = self._arr, self.device, torch.float32
-        if len(grads) != len(self._sizes):
-            raise ValueError(f"{len(grads)} gradients for {len(self._sizes)} tensors")
-        index = dev.index
-        for t, g, n in zip(arr, grads, self._sizes):
-            if g.dtype is not f32 or g.numel() != n or g.get_device() != index or \
-                    not g.is_contiguous():
-                raise ValueError("gradients are contiguous fp32 tensors of their tensors' sizes "
-                                 "on their device")
-            t.g = g.data_ptr()
+        f32, tensor, index = torch.float32, torch.Tensor, self.params[0].get_device()
+        grads = list(grads)
+        if list(map(tensor.numel, grads)) != self._sizes or \
+                not all(map(tensor.is_contiguous, grads)) or \
+                any([g.dtype is not f32 for g in grads]) or \
+                any([i != index for i in map(tensor.get_device, grads)]):
+            raise ValueError(f"gradients: {len(self._sizes)} contiguous fp32 tensors of the sizes "
+                             "and on the device of the tensors they are for")
+        self._g[:] = list(map(tensor.data_ptr, grads))
         hy = AdamwHyper(0.0, self.betas[0], self.betas[1], self.eps, 1)
         if isinstance(lr, torch.Tensor):
-            hy.lr_dev = _arg("lr", lr.view(-1), (1,), f32, dev)
+            hy.lr_dev = _arg("lr", lr.view(-1), (1,), f32, index)
         else:
             hy.lr = lr
         if isinstance(step, torch.Tensor):
-            hy.step_dev = _arg("step", step.view(-1), (1,), torch.int64, dev)
+            hy.step_dev = _arg("step", step.view(-1), (1,), torch.int64, index)
         else:
             hy.step = self.t + 1 if step is None else step
         if gscale is not None:
-            hy.gscale_dev = _arg("gscale", gscale.view(-1), (1,), f32, dev)
-        with _On(dev, stream) as st:
-            _check(load().tsp_adamw_step(arr, len(arr), ctypes.byref(hy), self.state_bits,
+            hy.gscale_dev = _arg("gscale", gscale.view(-1), (1,), f32, index)
+        with _On(index, stream) as st:
+            _check(load().tsp_adamw_step(self._arr, len(self._arr), ctypes.byref(hy), self.state_bits,
                                          self.dtype, st), "tsp_adamw_step")
         if not isinstance(step, torch.Tensor):
             self.t = int(hy.step)
