@@ -192,6 +192,7 @@ constexpr int kBits = 9, kBins = 1 << kBits, kMaxRuns = 512;
 __global__ void __launch_bounds__(kSortThreads) embed_count_kernel(const __grid_constant__ SortArgs a) {
   __shared__ int hist[kBins];
   const int t = threadIdx.x, bins = 1 << a.bits;
+  after_previous_kernel();   // (pass 0: launched in the ordinary way)
   if (t < bins) hist[t] = 0;
   if (blockIdx.x == 0 && t < 2) a.starts[t] = 0;
   __syncthreads();
@@ -211,6 +212,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_scatter_kernel(const __gri
   __shared__ int hist[kSortWarps][kBins];
   __shared__ int sum_all[kSortThreads], sum_before[kSortThreads], wsum[kSortWarps];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, bins = 1 << a.bits;
+  after_previous_kernel();
   // the digits' counts over all runs and over those before this one: thread
   // (part, digit) sums every parts-th run
   const int parts = kSortThreads >> a.bits, part = t >> a.bits;
@@ -388,6 +390,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const T* __restrict__ dx
   const int lane = threadIdx.x & 31;
   int64_t task = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const bool add = a.zero_tasks == 0;
+  after_previous_kernel();
   if (task < a.zero_tasks) {
     const int v0 = (int)task * kZeroRows, v = v0 + lane % kZeroRows;
     int lo = 0, hi = a.S;   // the first place with a token >= v
@@ -496,6 +499,7 @@ template <bool VEC>
 __global__ void __launch_bounds__(256) embed_join_kernel(const __grid_constant__ SumArgs a) {
   __shared__ float sums[8][kSlab];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  after_previous_kernel();
   const int64_t n_short = (int64_t)a.starts[0] * a.nslabs, n_long = (int64_t)a.starts[1] * a.nslabs;
   for (int64_t task = blockIdx.x; task < n_long; task += gridDim.x) {
     const int ch = a.start[a.nchunks + task / a.nslabs], c0 = (int)(task % a.nslabs) * kSlab;
@@ -561,12 +565,13 @@ template <typename T, bool VEC>
 tsp_status embed_sum_t(const void* dx, const SumArgs& a, cudaStream_t st) {
   const int64_t tasks = (int64_t)a.nchunks * a.nslabs + a.zero_tasks;
   Prof prof("embed_bwd_sum", st, a.nchunks > 1 ? 2 : 1);
-  embed_sum_kernel<T, VEC><<<(unsigned)((tasks + 7) / 8), 256, 0, st>>>((const T*)dx, a);
-  TSP_CUDA_TRY(cudaGetLastError());
+  const tsp_status r =
+      launch_after(embed_sum_kernel<T, VEC>, dim3((unsigned)((tasks + 7) / 8)), 256, 0, st, (const T*)dx, a);
+  if (r != TSP_OK) return r;
   if (a.nchunks > 1) {
     const int64_t most = (int64_t)(a.nchunks - 1) * a.nslabs;   // (a CTA each if all were long)
-    embed_join_kernel<VEC><<<(unsigned)std::min<int64_t>(most, num_sms() * 4), 256, 0, st>>>(a);
-    TSP_CUDA_TRY(cudaGetLastError());
+    return launch_after(embed_join_kernel<VEC>, dim3((unsigned)std::min<int64_t>(most, num_sms() * 4)),
+                        256, 0, st, a);
   }
   return TSP_OK;
 }
@@ -624,10 +629,15 @@ tsp_status launch_embed_bwd(const void* ids, int id_bytes, const void* dx, int d
     s.runs = (int)((S + s.run - 1) / s.run);
     Prof prof("embed_bwd_sort", st, 2 * passes);
     for (; s.pass < passes; ++s.pass, s.shift += s.bits) {
-      embed_count_kernel<<<s.runs, kSortThreads, 0, st>>>(s);
-      TSP_CUDA_TRY(cudaGetLastError());
-      embed_scatter_kernel<<<s.runs, kSortThreads, 0, st>>>(s);
-      TSP_CUDA_TRY(cudaGetLastError());
+      tsp_status r = TSP_OK;
+      if (s.pass == 0) {
+        embed_count_kernel<<<s.runs, kSortThreads, 0, st>>>(s);
+        TSP_CUDA_TRY(cudaGetLastError());
+      } else {
+        r = launch_after(embed_count_kernel, dim3(s.runs), kSortThreads, 0, st, s);
+      }
+      if (r == TSP_OK) r = launch_after(embed_scatter_kernel, dim3(s.runs), kSortThreads, 0, st, s);
+      if (r != TSP_OK) return r;
     }
   }
   SumArgs a;

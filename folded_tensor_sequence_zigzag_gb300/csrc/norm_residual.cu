@@ -23,87 +23,106 @@ namespace tsp {
 
 namespace {
 
-// N consecutive elements as they are stored (N = 4: one 8- or 16-byte access, n
-// a multiple of 4; N = 1: any n).
-template <typename T, int N>
-struct Unit {
-  T e[N];
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (N == 1) e[0] = *p;
-    else if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
-    else *reinterpret_cast<float4*>(e) = *reinterpret_cast<const float4*>(p);
-  }
-  __device__ __forceinline__ void get(float (&v)[N]) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = to_f<T>(e[i]);
-  }
-} __attribute__((aligned(sizeof(T) * N)));
-
-template <typename T, int N>
-__device__ __forceinline__ void load_n(const T* p, float (&v)[N]) {
-  Unit<T, N> u;
-  u.load(p);
-  u.get(v);
+// Rows are worked on in units of four elements, one 8- or 16-byte access.  Where
+// n % 4 != 0 (RAGGED) the units are those of the whole tensor, so that they are
+// aligned all the same: a row starts s = row * n % 4 elements into its first unit,
+// and the units at its two ends hold elements of other rows too, which are left
+// alone.  A thread's rows are a multiple of four apart, so its s is one number and
+// its columns (c .. c + 3, c = 4 * unit - s) are the same in all of them.
+template <bool RAGGED>
+__device__ __forceinline__ bool is_here(int c, int n) {
+  return c < n && (!RAGGED || c + 4 > 0);
 }
-template <typename T, int N>
-__device__ __forceinline__ void store_n(T* p, const float (&v)[N]) {
-  if constexpr (N == 1)
-    *p = from_f<T>(v[0]);
-  else if constexpr (sizeof(T) == 2)
+template <bool RAGGED>
+__device__ __forceinline__ bool is_whole(int c, int n) {
+  return !RAGGED || (c >= 0 && c + 4 <= n);
+}
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, float (&v)[4]) {
+  if constexpr (sizeof(T) == 2) {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    v[0] = lo2<T>(q.x); v[1] = hi2<T>(q.x); v[2] = lo2<T>(q.y); v[3] = hi2<T>(q.y);
+  } else {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+  }
+}
+// the unit at column c of the row at `row`; elements of other rows are 0
+template <bool RAGGED, typename T>
+__device__ __forceinline__ void load_unit(const T* row, int c, int n, float (&v)[4]) {
+  if (is_whole<RAGGED>(c, n)) {
+    load4<T>(row + c, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = c + e >= 0 && c + e < n ? to_f<T>(row[c + e]) : 0.f;
+  }
+}
+// a gain, whose own start is column 0: not aligned to the units of a ragged row
+template <bool RAGGED, typename T>
+__device__ __forceinline__ void load_gain(const T* g, int c, int n, float (&v)[4]) {
+  if constexpr (RAGGED) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = c + e >= 0 && c + e < n ? to_f<T>(g[c + e]) : 0.f;
+  } else {
+    load4<T>(g + c, v);
+  }
+}
+// a unit copied ahead, whole: what is not this row's is masked
+template <bool RAGGED, typename T>
+__device__ __forceinline__ void load_copied(const T* unit, int c, int n, float (&v)[4]) {
+  load4<T>(unit, v);
+  if (!is_whole<RAGGED>(c, n)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < 0 || c + e >= n) v[e] = 0.f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float (&v)[4]) {
+  if constexpr (sizeof(T) == 2)
     *reinterpret_cast<uint2*>(p) = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
   else
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
-
-// Elementwise on N values, two at a time where there are four: the .f32x2 forms
-// round as the scalar ones and take half the issue slots, of which the backward
-// needs most.
-template <int N, typename F2, typename F1>
-__device__ __forceinline__ void pairs(F2 two, F1 one) {
-  if constexpr (N % 2 == 0) {
-#pragma unroll
-    for (int e = 0; e < N; e += 2) two(e);
+template <bool RAGGED, typename T>
+__device__ __forceinline__ void store_unit(T* row, int c, int n, const float (&v)[4]) {
+  if (is_whole<RAGGED>(c, n)) {
+    store4<T>(row + c, v);
   } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) one(e);
+    for (int e = 0; e < 4; ++e)
+      if (c + e >= 0 && c + e < n) row[c + e] = from_f<T>(v[e]);
   }
 }
-template <int N>   // a = a * b
-__device__ __forceinline__ void mul_n(float (&a)[N], const float (&b)[N]) {
-  pairs<N>([&](int e) {
+
+// Elementwise on four values, two an instruction: the .f32x2 forms take half the
+// issue slots, of which the backward needs most.
+__device__ __forceinline__ void mul4(float (&a)[4], const float (&b)[4]) {   // a = a * b
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
     const float2 r = fmul2(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]));
     a[e] = r.x; a[e + 1] = r.y;
-  }, [&](int e) { a[e] *= b[e]; });
+  }
 }
-template <int N>   // a = a * s
-__device__ __forceinline__ void mul_n(float (&a)[N], float s) {
-  pairs<N>([&](int e) {
-    const float2 r = fmul2(make_float2(a[e], a[e + 1]), make_float2(s, s));
-    a[e] = r.x; a[e + 1] = r.y;
-  }, [&](int e) { a[e] *= s; });
+__device__ __forceinline__ void mul4(float (&a)[4], float s) {
+  const float b[4] = {s, s, s, s};
+  mul4(a, b);
 }
-template <int N>   // c = a * b + c
-__device__ __forceinline__ void fma_n(float (&c)[N], const float (&a)[N], const float (&b)[N]) {
-  pairs<N>([&](int e) {
+// c = a * b + c
+__device__ __forceinline__ void fma4(float (&c)[4], const float (&a)[4], const float (&b)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
     const float2 r = ffma2(make_float2(a[e], a[e + 1]), make_float2(b[e], b[e + 1]),
                            make_float2(c[e], c[e + 1]));
     c[e] = r.x; c[e + 1] = r.y;
-  }, [&](int e) { c[e] = fmaf(a[e], b[e], c[e]); });
+  }
 }
-template <int N>   // c = a * s + c
-__device__ __forceinline__ void fma_n(float (&c)[N], const float (&a)[N], float s) {
-  pairs<N>([&](int e) {
-    const float2 r = ffma2(make_float2(a[e], a[e + 1]), make_float2(s, s), make_float2(c[e], c[e + 1]));
-    c[e] = r.x; c[e + 1] = r.y;
-  }, [&](int e) { c[e] = fmaf(a[e], s, c[e]); });
+__device__ __forceinline__ void fma4(float (&c)[4], const float (&a)[4], float s) {
+  const float b[4] = {s, s, s, s};
+  fma4(c, a, b);
 }
-template <int N>
-__device__ __forceinline__ float total(const float (&v)[N]) {
-  float t = v[0];
-#pragma unroll
-  for (int e = 1; e < N; ++e) t += v[e];
-  return t;
-}
+__device__ __forceinline__ void zero4(float (&v)[4]) { v[0] = v[1] = v[2] = v[3] = 0.f; }
+__device__ __forceinline__ float total(const float (&v)[4]) { return (v[0] + v[1]) + (v[2] + v[3]); }
 
 // sigmoid(z) and its derivative from e = exp(-|z|), which neither overflows nor
 // cancels: sigmoid(|z|) = 1 / (1 + e), sigmoid(-|z|) = e / (1 + e).  e is 2^x of
@@ -139,18 +158,34 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   }
 }
 
-// A copy on its way to shared memory.  Every thread copies what it will read
-// itself, so waiting for its own copies is all the synchronisation there is.
-template <typename T, int N>
-__device__ __forceinline__ void copy_ahead(T* dst, const T* src) {
-  constexpr int B = sizeof(T) * N;
-  static_assert(B == 4 || B == 8 || B == 16, "a copy is 4, 8 or 16 bytes");
-  // 16 bytes go past L1, which then keeps the gains (there is no such form for 4 and 8)
+// A unit on its way to shared memory, whole (what it holds of other rows is read
+// past); only the tensor's last one may end beyond it, and is loaded by element.
+// Every thread copies what it will read itself, so waiting for its own copies is
+// all the synchronisation there is.  left: elements from the unit's first to the
+// tensor's end.  copy_own: the same of the row's own elements alone, where the
+// tensor is also the output and other CTAs may be writing its other rows.
+template <bool RAGGED, typename T>
+__device__ __forceinline__ void copy_ahead(T* dst, const T* src, int64_t left) {
+  constexpr int B = sizeof(T) * 4;
+  if (RAGGED && left < 4) {
+    for (int e = 0; e < 4; ++e)
+      if (e < left) dst[e] = src[e];
+    return;
+  }
+  // 16 bytes go past L1, which then keeps the gains (there is no such form for 8)
   if constexpr (B == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(B)
-                 : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+template <bool RAGGED, typename T>
+__device__ __forceinline__ void copy_own(T* dst, const T* src, int c, int n) {
+  if (is_whole<RAGGED>(c, n)) {
+    copy_ahead<false>(dst, src, 4);
+    return;
+  }
+  for (int e = 0; e < 4; ++e)
+    if (c + e >= 0 && c + e < n) dst[e] = src[e];
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // until at most `LEFT` of the groups committed last are on their way
@@ -159,12 +194,17 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
-// The columns of a thread: UPT units of N, unit i at first + i * 32 * N, those of
-// a warp next to each other.
-template <int N, int UPT, int TPR>
-__device__ __forceinline__ int first_col() {
-  if constexpr (TPR > 0) return (int)(threadIdx.x % TPR) * N;
-  return (int)((threadIdx.x >> 5) * UPT * 32 + (threadIdx.x & 31)) * N;
+// A thread's UPT units are kStep elements apart, those of a warp next to each other.
+constexpr int kStep = 128;
+template <int UPT, int TPR>
+__device__ __forceinline__ int first_unit() {
+  if constexpr (TPR > 0) return (int)(threadIdx.x % TPR) * 4;
+  return (int)((threadIdx.x >> 5) * UPT * 32 + (threadIdx.x & 31)) * 4;
+}
+// s of the rows of a thread (see RAGGED)
+template <bool RAGGED>
+__device__ __forceinline__ int start_of(int64_t row, int n) {
+  return RAGGED ? (int)((row * n) & 3) : 0;
 }
 
 struct FwdArgs {
@@ -176,29 +216,30 @@ struct FwdArgs {
   float s, eps;
 };
 
-// The row in registers (first_col).
-//   TPR > 0: TPR threads a row, 256 / TPR rows a CTA (short rows);
+// The row in registers:
+//   TPR > 0: TPR threads a row, 256 / TPR rows a CTA (short rows, no barriers);
 //   TPR = 0: a CTA a row.
 // AHEAD (TPR = 0): past the barrier of a row sum, the next row's inputs are sent
 // for, each thread's into the places it has read before that barrier, and arrive
 // while this row is worked on.  Without that the loads of a row wait for the
 // barriers of the one before.
-template <typename T, typename Ts, int N, int UPT, int TPR, bool AHEAD>
-__global__ void __launch_bounds__(UPT * N < 8 || UPT == 2 ? 512 : 1024, UPT * N < 8 || UPT == 2 ? 3 : 1)
-    norm_residual_fwd_kernel(const __grid_constant__ FwdArgs a) {
+template <typename T, typename Ts, int UPT, int TPR, bool AHEAD, bool RAGGED>
+__global__ void __launch_bounds__(TPR > 0 ? 256 : 1024, TPR > 0 ? 6 : 1) norm_residual_fwd_kernel(const __grid_constant__ FwdArgs a) {
   __shared__ float part[2][32];
   extern __shared__ __align__(16) uint8_t ahead[];
-  constexpr int kStep = 32 * N;
-  const int n = a.n, c0 = first_col<N, UPT, TPR>();
+  const int n = a.n;
   const int group = TPR > 0 ? threadIdx.x / (TPR > 0 ? TPR : 1) : 0;
   const int64_t per = TPR > 0 ? blockDim.x / TPR : 1;
+  const int64_t total_n = a.rows * n;
+  const int unit0 = first_unit<UPT, TPR>();
+  const int c0 = unit0 - start_of<RAGGED>((int64_t)blockIdx.x * per + group, n);
   const float inv_n = 1.f / (float)n;
   // a warp's f, z, x next to each other, at constant distances
   constexpr int kWarp = UPT * kStep;
   uint8_t* const mine = ahead + (threadIdx.x >> 5) * kWarp * (2 * sizeof(T) + sizeof(Ts));
-  T* const f_in = (T*)mine + (threadIdx.x & 31) * N;
+  T* const f_in = (T*)mine + (threadIdx.x & 31) * 4;
   T* const z_in = f_in + kWarp;
-  Ts* const x_in = (Ts*)(mine + 2 * sizeof(T) * kWarp) + (threadIdx.x & 31) * N;
+  Ts* const x_in = (Ts*)(mine + 2 * sizeof(T) * kWarp) + (threadIdx.x & 31) * 4;
   // The copies of a row go in two groups: f, whose place is free after the first
   // sum's barrier, and x and z, free after the second's.
   auto issue_f = [&](int64_t row) {
@@ -207,7 +248,8 @@ __global__ void __launch_bounds__(UPT * N < 8 || UPT == 2 ? 512 : 1024, UPT * N 
         const int64_t at = row * n + c0;
 #pragma unroll
         for (int i = 0; i < UPT; ++i)
-          if (c0 + i * kStep < n) copy_ahead<T, N>(f_in + i * kStep, (const T*)a.f + at + i * kStep);
+          if (is_here<RAGGED>(c0 + i * kStep, n))
+            copy_ahead<RAGGED>(f_in + i * kStep, (const T*)a.f + at + i * kStep, total_n - at - i * kStep);
       }
       copies_commit();
     }
@@ -218,9 +260,12 @@ __global__ void __launch_bounds__(UPT * N < 8 || UPT == 2 ? 512 : 1024, UPT * N 
         const int64_t at = row * n + c0;
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
-          if (c0 + i * kStep < n) {
-            copy_ahead<Ts, N>(x_in + i * kStep, (const Ts*)a.x + at + i * kStep);
-            if (a.z) copy_ahead<T, N>(z_in + i * kStep, (const T*)a.z + at + i * kStep);
+          if (is_here<RAGGED>(c0 + i * kStep, n)) {
+            const int64_t left = total_n - at - i * kStep;
+            const Ts* x = (const Ts*)a.x + at + i * kStep;
+            if (RAGGED && a.x == a.h) copy_own<RAGGED>(x_in + i * kStep, x, c0 + i * kStep, n);
+            else copy_ahead<RAGGED>(x_in + i * kStep, x, left);
+            if (a.z) copy_ahead<RAGGED>(z_in + i * kStep, (const T*)a.z + at + i * kStep, left);
           }
         }
       }
@@ -231,80 +276,81 @@ __global__ void __launch_bounds__(UPT * N < 8 || UPT == 2 ? 512 : 1024, UPT * N 
   issue_x(blockIdx.x);
   for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < a.rows; row0 += (int64_t)gridDim.x * per) {
     const int64_t row = row0 + group;
-    const int nrow = TPR == 0 || row < a.rows ? n : 0;   // (a group past the last row does nothing)
-    const int64_t at = row * n + c0;
+    const int nrow = TPR == 0 || row < a.rows ? n : -4;   // (a group past the last row does nothing)
+    const int64_t base = row * n;
     if constexpr (AHEAD) copies_wait<1>();   // f is there
-    const T* fp = AHEAD ? f_in : (const T*)a.f + at;
-    const T* zp = AHEAD ? z_in : (const T*)a.z + at;
-    const Ts* xp = AHEAD ? x_in : (const Ts*)a.x + at;
-    float v[UPT][N], ss[N];
-    float early[AHEAD ? 1 : UPT][N];   // without copies ahead: x, on its way during the first sum
-#pragma unroll
-    for (int e = 0; e < N; ++e) ss[e] = 0.f;
+    float v[UPT][4], ss[4];
+    // without copies ahead: x and z, on their way during the first sum
+    float early[AHEAD ? 1 : UPT][4], early_z[AHEAD ? 1 : UPT][4];
+    zero4(ss);
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-#pragma unroll
-      for (int e = 0; e < N; ++e) v[i][e] = 0.f;
-      if (c0 + i * kStep < nrow) {
-        load_n<T, N>(fp + i * kStep, v[i]);
-        if constexpr (!AHEAD) load_n<Ts, N>(xp + i * kStep, early[i]);
+      const int c = c0 + i * kStep;
+      zero4(v[i]);
+      if (is_here<RAGGED>(c, nrow)) {
+        if constexpr (AHEAD) {
+          load_copied<RAGGED>(f_in + i * kStep, c, n, v[i]);
+        } else {
+          load_unit<RAGGED>((const T*)a.f + base, c, n, v[i]);
+          load_unit<RAGGED>((const Ts*)a.x + base, c, n, early[i]);
+          if (a.z) load_unit<RAGGED>((const T*)a.z + base, c, n, early_z[i]);
+        }
       }
     }
     float r = 1.f;
     if (a.g_post) {
 #pragma unroll
-      for (int i = 0; i < UPT; ++i) fma_n<N>(ss, v[i], v[i]);
-      r = rsqrtf(row_sum<TPR>(total<N>(ss), part[0]) * inv_n + a.eps);
-      if (c0 == 0 && nrow && a.rstd_f) a.rstd_f[row] = r;
+      for (int i = 0; i < UPT; ++i) fma4(ss, v[i], v[i]);
+      r = rsqrtf(row_sum<TPR>(total(ss), part[0]) * inv_n + a.eps);
+      if (unit0 == 0 && nrow > 0 && a.rstd_f) a.rstd_f[row] = r;
     } else if (AHEAD) {
       __syncthreads();
     }
     if constexpr (AHEAD) copies_wait<0>();   // x and z too
     issue_f(row + gridDim.x);
-#pragma unroll
-    for (int e = 0; e < N; ++e) ss[e] = 0.f;
-    Ts* h = (Ts*)a.h + at;
+    zero4(ss);
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      if (c0 + i * kStep < nrow) {
-        float w[N];
+      const int c = c0 + i * kStep;
+      if (is_here<RAGGED>(c, nrow)) {
+        float w[4];
         if (a.g_post) {
-          load_n<T, N>((const T*)a.g_post + c0 + i * kStep, w);
-          mul_n<N>(w, r);
-          mul_n<N>(v[i], w);
+          load_gain<RAGGED>((const T*)a.g_post, c, n, w);
+          mul4(w, r);
+          mul4(v[i], w);
         }
         if (a.z) {
-          load_n<T, N>(zp + i * kStep, w);
+          if constexpr (AHEAD) load_copied<RAGGED>(z_in + i * kStep, c, n, w);
 #pragma unroll
-          for (int e = 0; e < N; ++e) w[e] = gate_of(w[e]);
-          mul_n<N>(v[i], w);
+          for (int e = 0; e < 4; ++e) w[e] = gate_of(AHEAD ? w[e] : early_z[AHEAD ? 0 : i][e]);
+          mul4(v[i], w);
         }
         if constexpr (AHEAD) {
-          load_n<Ts, N>(xp + i * kStep, w);
+          load_copied<RAGGED>(x_in + i * kStep, c, n, w);
         } else {
 #pragma unroll
-          for (int e = 0; e < N; ++e) w[e] = early[i][e];
+          for (int e = 0; e < 4; ++e) w[e] = early[i][e];
         }
-        fma_n<N>(w, v[i], a.s);
+        fma4(w, v[i], a.s);
 #pragma unroll
-        for (int e = 0; e < N; ++e) v[i][e] = to_f<Ts>(from_f<Ts>(w[e]));
-        fma_n<N>(ss, v[i], v[i]);
-        store_n<Ts, N>(h + i * kStep, v[i]);
+        for (int e = 0; e < 4; ++e) v[i][e] = to_f<Ts>(from_f<Ts>(w[e]));
+        fma4(ss, v[i], v[i]);
+        store_unit<RAGGED>((Ts*)a.h + base, c, n, v[i]);
       }
     }
     if (a.g_pre) {
-      r = rsqrtf(row_sum<TPR>(total<N>(ss), part[1]) * inv_n + a.eps);
-      if (c0 == 0 && nrow && a.rstd_h) a.rstd_h[row] = r;
+      r = rsqrtf(row_sum<TPR>(total(ss), part[1]) * inv_n + a.eps);
+      if (unit0 == 0 && nrow > 0 && a.rstd_h) a.rstd_h[row] = r;
       issue_x(row + gridDim.x);
-      T* b = (T*)a.b + at;
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
-        if (c0 + i * kStep < nrow) {
-          float g[N];
-          load_n<T, N>((const T*)a.g_pre + c0 + i * kStep, g);
-          mul_n<N>(v[i], r);
-          mul_n<N>(g, v[i]);
-          store_n<T, N>(b + i * kStep, g);
+        const int c = c0 + i * kStep;
+        if (is_here<RAGGED>(c, nrow)) {
+          float g[4];
+          load_gain<RAGGED>((const T*)a.g_pre, c, n, g);
+          mul4(v[i], r);
+          mul4(g, v[i]);
+          store_unit<RAGGED>((T*)a.b + base, c, n, g);
         }
       }
     }
@@ -363,53 +409,62 @@ struct BwdArgs {
   float s;
 };
 
+// The gain sums of a CTA-wide row are in shared memory where 64 registers a thread
+// let two CTAs of 512 run on a multiprocessor (two units a thread).
+// (Four units a thread need 128 registers: 512 threads, rows of up to 8192.)
+constexpr int kMaxBwdThreads = 512;
+constexpr bool gain_sums_in_smem(int upt, bool ahead) { return ahead && upt <= 2; }
+
 // The same layout and the same copies ahead (dh, db, h, f, z).  A thread's
 // columns are the same in every row, so its share of the gain gradients stays
-// with it until the CTA's last row: in registers, or with AHEAD, where 64
-// registers a thread let two CTAs of 512 run on a multiprocessor, in its own
-// places in shared memory.  With several rows a CTA the groups' shares are added
-// in the order of the groups.
-template <typename T, typename Ts, int N, int UPT, int TPR, bool AHEAD>
-__global__ void __launch_bounds__(512, UPT * N <= 8 ? 2 : 1) norm_residual_bwd_kernel(const __grid_constant__ BwdArgs a) {
+// with it until the CTA's last row, in registers or in its own places in shared
+// memory.  With several rows a CTA the groups' shares are added in the order of
+// the groups.
+template <typename T, typename Ts, int UPT, int TPR, bool AHEAD, bool RAGGED>
+__global__ void __launch_bounds__(TPR > 0 ? 256 : UPT <= 2 ? 512 : kMaxBwdThreads,
+                                  TPR > 0 ? 3 : UPT <= 2 ? 2 : 1)
+    norm_residual_bwd_kernel(const __grid_constant__ BwdArgs a) {
   __shared__ float part[2][32];
   extern __shared__ __align__(16) uint8_t ahead[];
-  constexpr int kStep = 32 * N;
-  const int n = a.n, c0 = first_col<N, UPT, TPR>();
+  constexpr bool kSums = gain_sums_in_smem(UPT, AHEAD);
+  const int n = a.n;
   const int group = TPR > 0 ? threadIdx.x / (TPR > 0 ? TPR : 1) : 0;
   const int64_t per = TPR > 0 ? blockDim.x / TPR : 1;
+  const int64_t total_n = a.rows * n;
+  const int c0 = first_unit<UPT, TPR>() - start_of<RAGGED>((int64_t)blockIdx.x * per + group, n);
   const float inv_n = 1.f / (float)n;
   // a warp's dh, db (fp32), h, f, z and its gain sums next to each other, at
   // constant distances
   constexpr int kWarp = UPT * kStep;
-  uint8_t* const mine = ahead + (threadIdx.x >> 5) * kWarp * (16 + sizeof(Ts) + 2 * sizeof(T));
-  float* const sum_in = (float*)(mine + (8 + sizeof(Ts) + 2 * sizeof(T)) * kWarp) + (threadIdx.x & 31) * N;
-  float dpost[AHEAD ? 1 : UPT][N], dpre[AHEAD ? 1 : UPT][N];
+  uint8_t* const mine = ahead + (threadIdx.x >> 5) * kWarp * ((kSums ? 16 : 8) + sizeof(Ts) + 2 * sizeof(T));
+  float* const dh_in = (float*)mine + (threadIdx.x & 31) * 4;
+  float* const db_in = dh_in + kWarp;
+  Ts* const h_in = (Ts*)(mine + 8 * kWarp) + (threadIdx.x & 31) * 4;
+  T* const f_in = (T*)(mine + (8 + sizeof(Ts)) * kWarp) + (threadIdx.x & 31) * 4;
+  T* const z_in = f_in + kWarp;
+  float* const sum_in = (float*)(mine + (8 + sizeof(Ts) + 2 * sizeof(T)) * kWarp) + (threadIdx.x & 31) * 4;
+  float dpost[kSums ? 1 : UPT][4], dpre[kSums ? 1 : UPT][4];
 #pragma unroll
   for (int i = 0; i < UPT; ++i) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) dpost[AHEAD ? 0 : i][e] = dpre[AHEAD ? 0 : i][e] = 0.f;
-    if constexpr (AHEAD) {
-      store_n<float, N>(sum_in + i * kStep, dpost[0]);
-      store_n<float, N>(sum_in + kWarp + i * kStep, dpost[0]);
+    zero4(dpost[kSums ? 0 : i]);
+    zero4(dpre[kSums ? 0 : i]);
+    if constexpr (kSums) {
+      store4(sum_in + i * kStep, dpost[0]);
+      store4(sum_in + kWarp + i * kStep, dpost[0]);
     }
   }
-  // c += a * b, in registers or in the thread's place in shared memory
-  auto add_to = [&](int i, bool post, const float (&x)[N], const float (&y)[N]) {
-    if constexpr (AHEAD) {
+  // the gain sum += x * y
+  auto add_to = [&](int i, bool post, const float (&x)[4], const float (&y)[4]) {
+    if constexpr (kSums) {
       float* at = sum_in + (post ? kWarp : 0) + i * kStep;
-      float c[N];
-      load_n<float, N>(at, c);
-      fma_n<N>(c, x, y);
-      store_n<float, N>(at, c);
+      float c[4];
+      load4(at, c);
+      fma4(c, x, y);
+      store4(at, c);
     } else {
-      fma_n<N>(post ? dpost[i] : dpre[i], x, y);
+      fma4(post ? dpost[i] : dpre[i], x, y);
     }
   };
-  float* const dh_in = (float*)mine + (threadIdx.x & 31) * N;
-  float* const db_in = dh_in + kWarp;
-  Ts* const h_in = (Ts*)(mine + 8 * kWarp) + (threadIdx.x & 31) * N;
-  T* const f_in = (T*)(mine + (8 + sizeof(Ts)) * kWarp) + (threadIdx.x & 31) * N;
-  T* const z_in = f_in + kWarp;
   // The copies of a row go in two groups: db and h, whose places are free after
   // the first sum's barrier, and dh, f, z, free after the second's.
   auto issue_pre = [&](int64_t row) {
@@ -418,9 +473,10 @@ __global__ void __launch_bounds__(512, UPT * N <= 8 ? 2 : 1) norm_residual_bwd_k
         const int64_t at = row * n + c0;
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
-          if (c0 + i * kStep < n) {
-            copy_ahead<float, N>(db_in + i * kStep, a.db + at + i * kStep);
-            copy_ahead<Ts, N>(h_in + i * kStep, (const Ts*)a.h + at + i * kStep);
+          if (is_here<RAGGED>(c0 + i * kStep, n)) {
+            const int64_t left = total_n - at - i * kStep;
+            copy_ahead<RAGGED>(db_in + i * kStep, a.db + at + i * kStep, left);
+            copy_ahead<RAGGED>(h_in + i * kStep, (const Ts*)a.h + at + i * kStep, left);
           }
         }
       }
@@ -433,10 +489,12 @@ __global__ void __launch_bounds__(512, UPT * N <= 8 ? 2 : 1) norm_residual_bwd_k
         const int64_t at = row * n + c0;
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
-          if (c0 + i * kStep < n) {
-            if (a.dh) copy_ahead<float, N>(dh_in + i * kStep, a.dh + at + i * kStep);
-            copy_ahead<T, N>(f_in + i * kStep, (const T*)a.f + at + i * kStep);
-            if (a.z) copy_ahead<T, N>(z_in + i * kStep, (const T*)a.z + at + i * kStep);
+          if (is_here<RAGGED>(c0 + i * kStep, n)) {
+            const int64_t left = total_n - at - i * kStep;
+            if (RAGGED && a.dh == a.dx) copy_own<RAGGED>(dh_in + i * kStep, a.dh + at + i * kStep, c0 + i * kStep, n);
+            else if (a.dh) copy_ahead<RAGGED>(dh_in + i * kStep, a.dh + at + i * kStep, left);
+            copy_ahead<RAGGED>(f_in + i * kStep, (const T*)a.f + at + i * kStep, left);
+            if (a.z) copy_ahead<RAGGED>(z_in + i * kStep, (const T*)a.z + at + i * kStep, left);
           }
         }
       }
@@ -456,120 +514,145 @@ __global__ void __launch_bounds__(512, UPT * N <= 8 ? 2 : 1) norm_residual_bwd_k
   load_rstd((int64_t)blockIdx.x * per + group);
   for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < a.rows; row0 += (int64_t)gridDim.x * per) {
     const int64_t row = row0 + group;
-    const int nrow = TPR == 0 || row < a.rows ? n : 0;   // (a group past the last row does nothing)
-    const int64_t at = row * n + c0;
+    const int nrow = TPR == 0 || row < a.rows ? n : -4;   // (a group past the last row does nothing)
+    const int64_t base = row * n;
     const float rf = rf_next, rh = rh_next;
     load_rstd(row + (int64_t)gridDim.x * per);
     if constexpr (AHEAD) copies_wait<1>();   // db and h are there
-    const float* dhp = AHEAD ? dh_in : a.dh + at;
-    const float* dbp = AHEAD ? db_in : a.db + at;
-    const Ts* hp = AHEAD ? h_in : (const Ts*)a.h + at;
-    const T* fp = AHEAD ? f_in : (const T*)a.f + at;
-    const T* zp = AHEAD ? z_in : (const T*)a.z + at;
-    float d[UPT][N];
-    float dot[N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) dot[e] = 0.f;
-    if (a.g_pre) {
-      float y[UPT][N], gd[UPT][N];
+    float d[UPT][4], y[UPT][4], dot[4];
+    // without copies ahead: f and z too are on their way before the first sum
+    float early_f[AHEAD ? 1 : UPT][4], early_z[AHEAD ? 1 : UPT][4];
+    zero4(dot);
+    if constexpr (!AHEAD) {
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
-        if (c0 + i * kStep < nrow) {
-          float g[N];
-          load_n<Ts, N>(hp + i * kStep, y[i]);
-          load_n<float, N>(dbp + i * kStep, gd[i]);
-          load_n<T, N>((const T*)a.g_pre + c0 + i * kStep, g);
-          mul_n<N>(y[i], rh);
-          add_to(i, false, gd[i], y[i]);
-          mul_n<N>(gd[i], g);
-          fma_n<N>(dot, gd[i], y[i]);
+        const int c = c0 + i * kStep;
+        zero4(d[i]);
+        if (is_here<RAGGED>(c, nrow)) {
+          if (a.dh) load_unit<RAGGED>(a.dh + base, c, n, d[i]);
+          load_unit<RAGGED>((const T*)a.f + base, c, n, early_f[i]);
+          if (a.z) load_unit<RAGGED>((const T*)a.z + base, c, n, early_z[i]);
         }
       }
-      const float mean = row_sum<TPR>(total<N>(dot), part[0]) * inv_n;
+    }
+    if (a.g_pre) {
+      float gd[UPT][4];
+#pragma unroll
+      for (int i = 0; i < UPT; ++i) {
+        const int c = c0 + i * kStep;
+        if (is_here<RAGGED>(c, nrow)) {
+          float g[4];
+          if constexpr (AHEAD) {
+            load_copied<RAGGED>(h_in + i * kStep, c, n, y[i]);
+            load_copied<RAGGED>(db_in + i * kStep, c, n, gd[i]);
+          } else {
+            load_unit<RAGGED>((const Ts*)a.h + base, c, n, y[i]);
+            load_unit<RAGGED>(a.db + base, c, n, gd[i]);
+          }
+          load_gain<RAGGED>((const T*)a.g_pre, c, n, g);
+          mul4(y[i], rh);
+          add_to(i, false, gd[i], y[i]);
+          mul4(gd[i], g);
+          fma4(dot, gd[i], y[i]);
+        }
+      }
+      const float mean = row_sum<TPR>(total(dot), part[0]) * inv_n;
       if constexpr (AHEAD) copies_wait<0>();   // dh, f and z too
       issue_pre(row + gridDim.x);
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) d[i][e] = 0.f;
-        if (c0 + i * kStep < nrow) {
-          if (a.dh) load_n<float, N>(dhp + i * kStep, d[i]);
-          fma_n<N>(gd[i], y[i], -mean);
-          fma_n<N>(d[i], gd[i], rh);
+        const int c = c0 + i * kStep;
+        if constexpr (AHEAD) zero4(d[i]);
+        if (is_here<RAGGED>(c, nrow)) {
+          if constexpr (AHEAD)
+            if (a.dh) load_copied<RAGGED>(dh_in + i * kStep, c, n, d[i]);
+          fma4(gd[i], y[i], -mean);
+          fma4(d[i], gd[i], rh);
         }
       }
-    } else {
-      if constexpr (AHEAD) copies_wait<0>();
+    } else if constexpr (AHEAD) {
+      copies_wait<0>();
       issue_pre(row + gridDim.x);   // (an empty group)
 #pragma unroll
       for (int i = 0; i < UPT; ++i)
-        if (c0 + i * kStep < nrow) load_n<float, N>(dhp + i * kStep, d[i]);
+        if (is_here<RAGGED>(c0 + i * kStep, nrow))
+          load_copied<RAGGED>(dh_in + i * kStep, c0 + i * kStep, n, d[i]);
     }
-    float y[UPT][N];
-#pragma unroll
-    for (int e = 0; e < N; ++e) dot[e] = 0.f;
-    float* dx = a.dx + at;
-    T* dz = (T*)a.dz + at;
+    zero4(dot);
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      if (c0 + i * kStep < nrow) {
-        store_n<float, N>(dx + i * kStep, d[i]);
-        load_n<T, N>(fp + i * kStep, y[i]);
-        mul_n<N>(y[i], rf);
-        mul_n<N>(d[i], a.s);
-        float g[N];
-        if (a.g_post) load_n<T, N>((const T*)a.g_post + c0 + i * kStep, g);
-        if (a.z) {
-          float open[N], slope[N];
-          load_n<T, N>(zp + i * kStep, open);
+      const int c = c0 + i * kStep;
+      if (is_here<RAGGED>(c, nrow)) {
+        store_unit<RAGGED>(a.dx + base, c, n, d[i]);
+        if constexpr (AHEAD) {
+          load_copied<RAGGED>(f_in + i * kStep, c, n, y[i]);
+        } else {
 #pragma unroll
-          for (int e = 0; e < N; ++e) open[e] = gate_of(open[e], &slope[e]);
-          mul_n<N>(slope, d[i]);
-          mul_n<N>(slope, y[i]);
-          if (a.g_post) mul_n<N>(slope, g);
-          store_n<T, N>(dz + i * kStep, slope);
-          mul_n<N>(d[i], open);
+          for (int e = 0; e < 4; ++e) y[i][e] = early_f[i][e];
+        }
+        mul4(y[i], rf);
+        mul4(d[i], a.s);
+        float g[4];
+        if (a.g_post) load_gain<RAGGED>((const T*)a.g_post, c, n, g);
+        if (a.z) {
+          float open[4], slope[4];
+          if constexpr (AHEAD) {
+            load_copied<RAGGED>(z_in + i * kStep, c, n, open);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) open[e] = early_z[i][e];
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) open[e] = gate_of(open[e], &slope[e]);
+          mul4(slope, d[i]);
+          mul4(slope, y[i]);
+          if (a.g_post) mul4(slope, g);
+          store_unit<RAGGED>((T*)a.dz + base, c, n, slope);
+          mul4(d[i], open);
         }
         if (a.g_post) {
           add_to(i, true, d[i], y[i]);
-          mul_n<N>(d[i], g);
-          fma_n<N>(dot, d[i], y[i]);
+          mul4(d[i], g);
+          fma4(dot, d[i], y[i]);
         }
       }
     }
-    T* df = (T*)a.df + at;
     if (a.g_post) {
-      const float mean = row_sum<TPR>(total<N>(dot), part[1]) * inv_n;
+      const float mean = row_sum<TPR>(total(dot), part[1]) * inv_n;
       issue_post(row + gridDim.x);
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
-        if (c0 + i * kStep < nrow) {
-          fma_n<N>(d[i], y[i], -mean);
-          mul_n<N>(d[i], rf);
+        if (is_here<RAGGED>(c0 + i * kStep, nrow)) {
+          fma4(d[i], y[i], -mean);
+          mul4(d[i], rf);
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < UPT; ++i)
-      if (c0 + i * kStep < nrow) store_n<T, N>(df + i * kStep, d[i]);
+      if (is_here<RAGGED>(c0 + i * kStep, nrow)) store_unit<RAGGED>((T*)a.df + base, c0 + i * kStep, n, d[i]);
     if (TPR == 0 && !(a.g_post && a.g_pre)) __syncthreads();
     if (!a.g_post) issue_post(row + gridDim.x);
   }
   if constexpr (TPR > 0) {
-    constexpr int kPlane = TPR * UPT * N;
-    float* sum = reinterpret_cast<float*>(ahead);   // [2][groups][kPlane]
+    float* sum = reinterpret_cast<float*>(ahead);   // [2][groups][n]
     const int groups = (int)per;
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      store_n<float, N>(sum + group * kPlane + c0 + i * kStep, dpost[i]);
-      store_n<float, N>(sum + (groups + group) * kPlane + c0 + i * kStep, dpre[i]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = c0 + i * kStep + e;
+        if (c < 0 || c >= n) continue;
+        sum[group * n + c] = dpost[i][e];
+        sum[(groups + group) * n + c] = dpre[i][e];
+      }
     }
     __syncthreads();
     for (int c = threadIdx.x; c < n; c += blockDim.x) {
       float p = 0.f, q = 0.f;
       for (int g = 0; g < groups; ++g) {
-        p += sum[g * kPlane + c];
-        q += sum[(groups + g) * kPlane + c];
+        p += sum[g * n + c];
+        q += sum[(groups + g) * n + c];
       }
       if (a.g_post) a.part_post[(int64_t)blockIdx.x * n + c] = p;
       if (a.g_pre) a.part_pre[(int64_t)blockIdx.x * n + c] = q;
@@ -577,14 +660,18 @@ __global__ void __launch_bounds__(512, UPT * N <= 8 ? 2 : 1) norm_residual_bwd_k
   } else {
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
-      if (c0 + i * kStep < n) {
-        const int64_t o = (int64_t)blockIdx.x * n + c0 + i * kStep;
-        if constexpr (AHEAD) {
-          load_n<float, N>(sum_in + kWarp + i * kStep, dpost[0]);
-          load_n<float, N>(sum_in + i * kStep, dpre[0]);
+      const int c = c0 + i * kStep;
+      if (is_here<RAGGED>(c, n)) {
+        if constexpr (kSums) {
+          load4(sum_in + kWarp + i * kStep, dpost[0]);
+          load4(sum_in + i * kStep, dpre[0]);
         }
-        if (a.g_post) store_n<float, N>(a.part_post + o, dpost[AHEAD ? 0 : i]);
-        if (a.g_pre) store_n<float, N>(a.part_pre + o, dpre[AHEAD ? 0 : i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (c + e < 0 || c + e >= n) continue;
+          if (a.g_post) a.part_post[(int64_t)blockIdx.x * n + c + e] = dpost[kSums ? 0 : i][e];
+          if (a.g_pre) a.part_pre[(int64_t)blockIdx.x * n + c + e] = dpre[kSums ? 0 : i][e];
+        }
       }
     }
   }
@@ -656,153 +743,152 @@ __global__ void __launch_bounds__(1024) norm_residual_bwd_wide_kernel(const __gr
   }
 }
 
-// dg[i] = the column sums of the CTAs' partials, in a fixed order: 32 columns a
-// CTA, 32 warps over the partials; blockIdx.y picks the gain.
-__global__ void __launch_bounds__(1024) norm_residual_gain_kernel(const float* __restrict__ p0,
-                                                                  float* __restrict__ o0,
-                                                                  const float* __restrict__ p1,
-                                                                  float* __restrict__ o1, int nb,
-                                                                  int n) {
-  __shared__ float acc[32][33];
+// dg[i] = the column sums of the CTAs' partials, in a fixed order: COLS columns a
+// CTA, 1024 / COLS partial rows at a time; blockIdx.y picks the gain.
+template <int COLS>
+__global__ void __launch_bounds__(1024) norm_residual_gain_kernel(const float* p0, float* __restrict__ o0,
+                                                                  const float* p1, float* __restrict__ o1,
+                                                                  int nb, int n) {
+  constexpr int R = 1024 / COLS;
+  __shared__ float acc[COLS][R + 1];
+  after_previous_kernel();
   const float* part = blockIdx.y ? p1 : p0;
   float* out = blockIdx.y ? o1 : o0;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int i = blockIdx.x * 32 + tx;
+  const int tx = threadIdx.x % COLS, ty = threadIdx.x / COLS;
+  const int i = blockIdx.x * COLS + tx;
   float s = 0.f;
   if (i < n) {
 #pragma unroll 4
-    for (int b = ty; b < nb; b += 32) s += part[(int64_t)b * n + i];
+    for (int b = ty; b < nb; b += R) s += part[(int64_t)b * n + i];
   }
-  acc[ty][tx] = s;
+  acc[tx][ty] = s;
   __syncthreads();
-  s = warp_sum(acc[tx][ty]);   // column ty of this CTA
-  if (tx == 0 && blockIdx.x * 32 + ty < n) out[blockIdx.x * 32 + ty] = s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp >= COLS) return;
+  s = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; r += 32) s += acc[warp][r + lane];
+  s = warp_sum(s);
+  if (lane == 0 && blockIdx.x * COLS + warp < n) out[blockIdx.x * COLS + warp] = s;
 }
 
-// How rows of n elements are laid on threads.
-struct Shape {
-  int N, upt;      // units of N elements, units a thread; upt == 0: the wide kernel
-  int tpr;         // threads a row below 32 or of one warp; 0: the CTA
-  int threads;     // of the CTA
-};
-Shape shape_of(int n, int max_threads) {
-  Shape s;
-  s.N = n % 4 == 0 ? 4 : 1;
-  const int units = n / s.N;
-  if (units <= 64) {              // up to two units a lane of one warp
-    s.upt = units <= 32 ? 1 : 2;
-    s.tpr = units <= 8 ? 8 : units <= 16 ? 16 : 32;
-    s.threads = 256;
-    return s;
-  }
-  s.tpr = 0;
-  s.upt = units <= 512 ? 1 : units <= 1024 ? 2 : 4;
-  if (s.N == 1 && units > 512) s.upt = units <= 2048 ? 4 : 8;
-  s.threads = ((units + s.upt - 1) / s.upt + 31) / 32 * 32;
-  if (s.threads > max_threads) s.upt = 0, s.threads = 1024;
-  return s;
-}
-// CTAs a multiprocessor: what 2048 threads and the copies' shared memory allow.
-// The GB300's 152 multiprocessors are a constant here because the backward's
-// workspace, sized without a device, holds a partial row a CTA.
-constexpr int kSms = 152, kSmemPerSm = 220 * 1024;
-
+// How rows of n elements are laid on threads, and the grid.
 struct Plan {
-  Shape s;
-  bool ahead;
+  int upt;         // units a thread; 0: the wide kernel
+  int tpr;         // threads a row, of one warp at most; 0: the CTA
+  int threads;     // of the CTA
+  bool ahead, ragged;
   int smem, grid;
 };
-Plan plan_of(int64_t rows, const Shape& s, int row_bytes_per_el, bool ahead, int threads_per_sm) {
-  Plan p;
-  p.s = s;
-  p.ahead = false;
-  p.smem = 0;
-  const int per = p.s.tpr > 0 ? p.s.threads / p.s.tpr : 1;
-  int per_sm = std::max(1, threads_per_sm / p.s.threads);
-  const int64_t items = (rows + per - 1) / per;
-  const int stage = p.s.threads * p.s.upt * p.s.N * row_bytes_per_el;
-  if (ahead && p.s.tpr == 0 && p.s.upt > 0 && stage <= kSmemPerSm) {
-    p.ahead = true;
-    p.smem = stage;
-    per_sm = std::max(1, std::min(per_sm, kSmemPerSm / (stage + 1024)));
+// The GB300's 152 multiprocessors are a constant here because the backward's
+// workspace, sized without a device, holds a partial row a CTA.  (A multiple of
+// four, as ragged rows need: a grid below it gives every CTA one row.)
+constexpr int kSms = 152, kSmemPerSm = 224 * 1024;
+
+void set_grid(Plan* p, int64_t rows, int per_sm) {
+  const int per = p->tpr > 0 ? p->threads / p->tpr : 1;
+  p->grid = (int)std::min<int64_t>((rows + per - 1) / per, (int64_t)kSms * std::max(1, per_sm));
+}
+// upt units a thread of a CTA, with the next row's `bytes` an element copied ahead
+// where they fit
+void set_cta(Plan* p, int64_t rows, int units, int upt, int bytes, int threads_per_sm) {
+  p->upt = upt;
+  p->tpr = 0;
+  p->threads = ((units + upt - 1) / upt + 31) / 32 * 32;
+  const int row = p->threads * upt * 4 * bytes;
+  int per_sm = std::min(32, threads_per_sm / p->threads);
+  p->ahead = row <= kSmemPerSm;
+  if (p->ahead) {
+    p->smem = row;
+    per_sm = std::min(per_sm, kSmemPerSm / (row + 1024));
   }
-  p.grid = (int)std::min<int64_t>(items, (int64_t)kSms * per_sm);
+  set_grid(p, rows, per_sm);
+}
+Plan start_plan(int n, int* units) {
+  Plan p = {};
+  p.ragged = n % 4 != 0;
+  *units = p.ragged ? (n + 6) / 4 : n / 4;   // (up to three elements before the row)
+  p.threads = 256;
+  p.tpr = *units <= 8 ? 8 : *units <= 16 ? 16 : 32;
+  p.upt = *units <= 32 ? 1 : 2;
   return p;
 }
 
 template <typename T, typename Ts>
 Plan fwd_plan(int64_t rows, int n) {
-  const Shape s = shape_of(n, 1024);
-  // 40 registers a thread up to 8 elements, 64 above
-  return plan_of(rows, s, 2 * sizeof(T) + sizeof(Ts), sizeof(T) * s.N >= 4,
-                 s.upt * s.N < 8 || s.upt == 2 ? 1536 : 1024);
+  int units;
+  Plan p = start_plan(n, &units);
+  if (units <= 64) {
+    set_grid(&p, rows, 6);
+  } else if (units <= 4 * 1024) {
+    // four units a thread: more rows at a time than with two or one (2048 bf16,
+    // fp32 stream: 91% of the copy rate against 69% with one)
+    set_cta(&p, rows, units, 4, 2 * sizeof(T) + sizeof(Ts), 1024);
+  } else {
+    p.upt = p.tpr = 0;
+    p.threads = 1024;
+    set_grid(&p, rows, 1);
+  }
+  return p;
 }
 template <typename T, typename Ts>
 Plan bwd_plan(int64_t rows, int n) {
-  const Shape s = shape_of(n, 512);   // 128 registers a thread: gain sums and a row
-  // (the inputs of a row, and two gain sums)
-  return plan_of(rows, s, 16 + sizeof(Ts) + 2 * sizeof(T), sizeof(T) * s.N >= 4, 1024);
+  int units;
+  Plan p = start_plan(n, &units);
+  if (units <= 64) {
+    p.smem = 2 * (p.threads / p.tpr) * n * 4;   // the groups' gain gradients
+    set_grid(&p, rows, 3);
+  } else if (units <= 4 * kMaxBwdThreads) {
+    const int upt = units <= 1024 ? 2 : 4;
+    set_cta(&p, rows, units, upt, (gain_sums_in_smem(upt, true) ? 16 : 8) + sizeof(Ts) + 2 * sizeof(T),
+            upt == 2 ? 1024 : kMaxBwdThreads);
+    // two rows a CTA at least: a CTA's partial gains cost about the traffic of one
+    if (p.grid > kSms) p.grid = (int)std::max<int64_t>(kSms, std::min<int64_t>(p.grid, rows / 8 * 4));
+  } else {
+    p.upt = p.tpr = 0;
+    p.threads = 1024;
+    set_grid(&p, rows, 1);
+  }
+  return p;
 }
 
 template <typename K, typename A>
 tsp_status launch(K kernel, const Plan& p, const A& a, cudaStream_t st) {
   if (p.smem > 47 * 1024)   // (the kernels' static shared memory counts too)
     TSP_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem));
-  kernel<<<p.grid, p.s.threads, p.smem, st>>>(a);
+  kernel<<<p.grid, p.threads, p.smem, st>>>(a);
   TSP_CUDA_TRY(cudaGetLastError());
   return TSP_OK;
 }
 
-template <typename T, typename Ts, int N, int UPT>
-tsp_status fwd_cta(const Plan& p, const FwdArgs& a, cudaStream_t st) {
-  if constexpr (sizeof(T) * N >= 4)
-    if (p.ahead) return launch(norm_residual_fwd_kernel<T, Ts, N, UPT, 0, true>, p, a, st);
-  return launch(norm_residual_fwd_kernel<T, Ts, N, UPT, 0, false>, p, a, st);
-}
-template <typename T, typename Ts, int N>
-tsp_status fwd_n(const Plan& p, const FwdArgs& a, cudaStream_t st) {
-  if (p.s.tpr == 8) return launch(norm_residual_fwd_kernel<T, Ts, N, 1, 8, false>, p, a, st);
-  if (p.s.tpr == 16) return launch(norm_residual_fwd_kernel<T, Ts, N, 1, 16, false>, p, a, st);
-  if (p.s.tpr == 32)
-    return p.s.upt == 1 ? launch(norm_residual_fwd_kernel<T, Ts, N, 1, 32, false>, p, a, st)
-                        : launch(norm_residual_fwd_kernel<T, Ts, N, 2, 32, false>, p, a, st);
-  if (p.s.upt == 1) return fwd_cta<T, Ts, N, 1>(p, a, st);
-  if constexpr (N == 4)
-    if (p.s.upt == 2) return fwd_cta<T, Ts, N, 2>(p, a, st);
-  if (p.s.upt == 4) return fwd_cta<T, Ts, N, 4>(p, a, st);
-  if constexpr (N == 1)
-    if (p.s.upt == 8) return fwd_cta<T, Ts, N, 8>(p, a, st);
-  return launch(norm_residual_fwd_wide_kernel<T, Ts>, p, a, st);
+template <typename T, typename Ts, bool RAGGED>
+tsp_status fwd_r(const Plan& p, const FwdArgs& a, cudaStream_t st) {
+#define TSP_NRF(upt, tpr, ahead) \
+  launch(norm_residual_fwd_kernel<T, Ts, upt, tpr, ahead, RAGGED>, p, a, st)
+  if (p.tpr == 8) return TSP_NRF(1, 8, false);
+  if (p.tpr == 16) return TSP_NRF(1, 16, false);
+  if (p.tpr == 32) return p.upt == 1 ? TSP_NRF(1, 32, false) : TSP_NRF(2, 32, false);
+  return TSP_NRF(4, 0, true);   // (8 or 12 bytes an element of 16384: always fits)
+#undef TSP_NRF
 }
 template <typename T, typename Ts>
 tsp_status fwd_t(const FwdArgs& a, cudaStream_t st) {
   const Plan p = fwd_plan<T, Ts>(a.rows, a.n);
   Prof prof("norm_residual_fwd", st);
-  return p.s.N == 4 ? fwd_n<T, Ts, 4>(p, a, st) : fwd_n<T, Ts, 1>(p, a, st);
+  if (p.upt == 0) return launch(norm_residual_fwd_wide_kernel<T, Ts>, p, a, st);
+  return p.ragged ? fwd_r<T, Ts, true>(p, a, st) : fwd_r<T, Ts, false>(p, a, st);
 }
 
-template <typename T, typename Ts, int N, int UPT>
-tsp_status bwd_cta(const Plan& p, const BwdArgs& a, cudaStream_t st) {
-  if constexpr (sizeof(T) * N >= 4)
-    if (p.ahead) return launch(norm_residual_bwd_kernel<T, Ts, N, UPT, 0, true>, p, a, st);
-  return launch(norm_residual_bwd_kernel<T, Ts, N, UPT, 0, false>, p, a, st);
-}
-template <typename T, typename Ts, int N>
-tsp_status bwd_n(Plan p, const BwdArgs& a, cudaStream_t st) {
-  if (p.s.tpr > 0) {
-    p.smem = 2 * p.s.threads * p.s.upt * p.s.N * 4;   // the groups' gain gradients
-    if (p.s.tpr == 8) return launch(norm_residual_bwd_kernel<T, Ts, N, 1, 8, false>, p, a, st);
-    if (p.s.tpr == 16) return launch(norm_residual_bwd_kernel<T, Ts, N, 1, 16, false>, p, a, st);
-    return p.s.upt == 1 ? launch(norm_residual_bwd_kernel<T, Ts, N, 1, 32, false>, p, a, st)
-                        : launch(norm_residual_bwd_kernel<T, Ts, N, 2, 32, false>, p, a, st);
-  }
-  if (p.s.upt == 1) return bwd_cta<T, Ts, N, 1>(p, a, st);
-  if constexpr (N == 4)
-    if (p.s.upt == 2) return bwd_cta<T, Ts, N, 2>(p, a, st);
-  if (p.s.upt == 4) return bwd_cta<T, Ts, N, 4>(p, a, st);
-  if constexpr (N == 1)
-    if (p.s.upt == 8) return bwd_cta<T, Ts, N, 8>(p, a, st);
-  return launch(norm_residual_bwd_wide_kernel<T, Ts>, p, a, st);
+template <typename T, typename Ts, bool RAGGED>
+tsp_status bwd_r(const Plan& p, const BwdArgs& a, cudaStream_t st) {
+#define TSP_NRB(upt, tpr, ahead) \
+  launch(norm_residual_bwd_kernel<T, Ts, upt, tpr, ahead, RAGGED>, p, a, st)
+  if (p.tpr == 8) return TSP_NRB(1, 8, false);
+  if (p.tpr == 16) return TSP_NRB(1, 16, false);
+  if (p.tpr == 32) return p.upt == 1 ? TSP_NRB(1, 32, false) : TSP_NRB(2, 32, false);
+  if (p.upt == 2) return TSP_NRB(2, 0, true);
+  return TSP_NRB(4, 0, true);   // (up to 20 bytes an element of 8192: always fits)
+#undef TSP_NRB
 }
 
 template <typename T, typename Ts>
@@ -812,15 +898,20 @@ tsp_status bwd_t(BwdArgs a, float* dg_post, float* dg_pre, void* ws, cudaStream_
   a.part_post = (float*)ws;
   a.part_pre = (float*)ws + (int64_t)p.grid * a.n;
   Prof prof("norm_residual_bwd", st, gains ? 2 : 1);
-  const tsp_status r = p.s.N == 4 ? bwd_n<T, Ts, 4>(p, a, st) : bwd_n<T, Ts, 1>(p, a, st);
+  const tsp_status r = p.upt == 0 ? launch(norm_residual_bwd_wide_kernel<T, Ts>, p, a, st)
+                       : p.ragged ? bwd_r<T, Ts, true>(p, a, st)
+                                  : bwd_r<T, Ts, false>(p, a, st);
   if (r != TSP_OK || !gains) return r;
   const bool both = a.g_post && a.g_pre;
   const float* p0 = a.g_post ? a.part_post : a.part_pre;
   float* o0 = a.g_post ? dg_post : dg_pre;
-  norm_residual_gain_kernel<<<dim3((a.n + 31) / 32, both ? 2 : 1), 1024, 0, st>>>(
-      p0, o0, a.part_pre, dg_pre, p.grid, a.n);
-  TSP_CUDA_TRY(cudaGetLastError());
-  return TSP_OK;
+  // short rows: few columns a CTA (a 32-byte sector of each partial row), so that
+  // there are CTAs enough (1001 columns, 1032 partial rows: 4 us of 31, 7 with 32
+  // columns; the other way round 4096 x 304 in 4 us less)
+  const int cols = a.n <= 2048 ? 8 : 32;
+  return launch_after(cols == 8 ? norm_residual_gain_kernel<8> : norm_residual_gain_kernel<32>,
+                      dim3((a.n + cols - 1) / cols, both ? 2 : 1), 1024, 0, st, p0, o0,
+                      (const float*)a.part_pre, dg_pre, p.grid, a.n);
 }
 
 }  // namespace
