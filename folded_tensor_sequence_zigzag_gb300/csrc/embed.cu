@@ -312,8 +312,8 @@ int run_of(int64_t S) {
 // Backward, step 2: rows summed along the sorted order
 // ---------------------------------------------------------------------------
 // A warp takes a chunk of the sorted positions and a slab of 256 columns (8 a
-// lane) and walks the chunk's rows, four loads ahead; places and tokens come 32
-// at a time.  A token whose positions lie inside the chunk is written (or added)
+// lane) and walks the chunk's rows, four or (16-bit) eight of them on their way at
+// a time; places and tokens come 32 at a time.  A token whose positions lie inside the chunk is written (or added)
 // to its table row at once; one that came in from the chunk before leaves its
 // part in slot 2*chunk, one that starts here and goes on in slot 2*chunk + 1.
 // Step 3 adds those up.  The first warps of the grid write the zero rows of absent
@@ -321,31 +321,39 @@ int run_of(int64_t S) {
 // next to the other warps' loads.
 constexpr int kSlab = 256, kZeroRows = 8, kLong = 12;
 
+// A lane's eight columns of a row: two groups of four next to each other (VEC), or
+// eight single ones 32 apart; as they are stored, until they are added up.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_cols(const T* row, int c0, int lane, int d, float (&v)[8]) {
-  if constexpr (VEC) {
+struct Cols {
+  T e[8];
+  __device__ __forceinline__ void load(const T* row, int c0, int lane, int d) {
+    if constexpr (VEC) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = c0 + h * 128 + lane * 4;
-      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c < d) {
-        if constexpr (sizeof(T) == 4) {
-          f = __ldcs(reinterpret_cast<const float4*>(row + c));
-        } else {
-          const uint2 u = __ldcs(reinterpret_cast<const uint2*>(row + c));
-          f = make_float4(lo2<T>(u.x), hi2<T>(u.x), lo2<T>(u.y), hi2<T>(u.y));
-        }
+      for (int h = 0; h < 2; ++h) {
+        const int c = c0 + h * 128 + lane * 4;
+        if constexpr (sizeof(T) == 4)
+          reinterpret_cast<float4*>(e)[h] = c < d ? __ldcs(reinterpret_cast<const float4*>(row + c)) : float4{};
+        else
+          reinterpret_cast<uint2*>(e)[h] = c < d ? __ldcs(reinterpret_cast<const uint2*>(row + c)) : uint2{};
       }
-      v[4 * h] = f.x; v[4 * h + 1] = f.y; v[4 * h + 2] = f.z; v[4 * h + 3] = f.w;
-    }
-  } else {
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = c0 + e * 32 + lane;
-      v[e] = c < d ? to_f<T>(row[c]) : 0.f;
+      for (int i = 0; i < 8; ++i) {
+        const int c = c0 + i * 32 + lane;
+        e[i] = c < d ? row[c] : from_f<T>(0.f);
+      }
     }
   }
-}
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = from_f<T>(0.f);
+  }
+  __device__ __forceinline__ void add_to(float (&acc)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] += to_f<T>(e[i]);
+  }
+} __attribute__((aligned(16)));
+
 // row = v * s, or row += v * s.  The addition is the memory's (nothing waits for the
 // old value); it is the only one the element gets in a call, so no order matters.
 template <bool VEC>
@@ -387,6 +395,7 @@ struct SumArgs {
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const T* __restrict__ dx,
                                                         const __grid_constant__ SumArgs a) {
+  constexpr int kAhead = VEC && sizeof(T) == 2 ? 8 : 4;
   const int lane = threadIdx.x & 31;
   int64_t task = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const bool add = a.zero_tasks == 0;
@@ -427,22 +436,20 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const T* __restrict__ dx
   for (int j = j0; j < j1; j += 32) {
     const bool in = j + lane < j1;
     const int2 mine = in ? a.pair[j + lane] : make_int2(a.vocab, 0);
-    for (int k = 0; k < 32 && j + k < j1; k += 4) {
-      float v[4][8];
-      int key[4];
+    for (int k = 0; k < 32 && j + k < j1; k += kAhead) {
+      Cols<T, VEC> v[kAhead];
+      int key[kAhead];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         key[u] = __shfl_sync(0xffffffffu, mine.x, k + u);
         const int r = __shfl_sync(0xffffffffu, mine.y, k + u);
-        if (key[u] < a.vocab && TSP_INB(r >= 0 && r < a.S, a.status)) {
-          load_cols<T, VEC>(dx + (int64_t)r * a.d, c0, lane, a.d, v[u]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
-        }
+        if (key[u] < a.vocab && TSP_INB(r >= 0 && r < a.S, a.status))
+          v[u].load(dx + (int64_t)r * a.d, c0, lane, a.d);
+        else
+          v[u].clear();
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
         if (j + k + u >= j1) break;
         if (key[u] != cur) {
           leave(false);
@@ -452,8 +459,7 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const T* __restrict__ dx
 #pragma unroll
           for (int e = 0; e < 8; ++e) acc[e] = 0.f;
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += v[u][e];
+        v[u].add_to(acc);
       }
     }
   }
@@ -470,12 +476,19 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const T* __restrict__ dx
 // listed the chunks where one starts): its parts added in chunk order, a warp a
 // token and slab.  The few tokens of more than kLong chunks get a CTA a slab, whose
 // warps add up every eighth part each, then the eight sums in order.
+// acc += the part of the token that starts in chunk ch and goes on
+template <bool VEC>
+__device__ __forceinline__ void first_part(const SumArgs& a, int ch, int c0, int lane, float (&acc)[8]) {
+  Cols<float, VEC> v;
+  v.load(a.part + ((int64_t)2 * ch + 1) * a.d, c0, lane, a.d);
+  v.add_to(acc);
+}
 // acc += the parts of token `tok` in chunks k, k + step, ...
 template <bool VEC>
 __device__ __forceinline__ void add_parts(const SumArgs& a, int tok, int k, int step, int c0, int lane,
                                           float (&acc)[8]) {
   for (; k < a.nchunks; k += 4 * step) {
-    float v[4][8];
+    Cols<float, VEC> v[4];
     bool in[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -484,13 +497,10 @@ __device__ __forceinline__ void add_parts(const SumArgs& a, int tok, int k, int 
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      if (in[u]) load_cols<float, VEC>(a.part + (int64_t)2 * (k + u * step) * a.d, c0, lane, a.d, v[u]);
+      if (in[u]) v[u].load(a.part + (int64_t)2 * (k + u * step) * a.d, c0, lane, a.d);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (!in[u]) continue;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += v[u][e];
-    }
+    for (int u = 0; u < 4; ++u)
+      if (in[u]) v[u].add_to(acc);
     if (!in[3]) return;
   }
 }
@@ -505,7 +515,7 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const __grid_constant__
     const int ch = a.start[a.nchunks + task / a.nslabs], c0 = (int)(task % a.nslabs) * kSlab;
     const int tok = a.pair[(ch + 1) * a.chunk].x;
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (warp == 0) load_cols<float, VEC>(a.part + ((int64_t)2 * ch + 1) * a.d, c0, lane, a.d, acc);
+    if (warp == 0) first_part<VEC>(a, ch, c0, lane, acc);
     add_parts<VEC>(a, tok, ch + 1 + warp, 8, c0, lane, acc);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sums[warp][e * 32 + lane] = acc[e];
@@ -522,8 +532,8 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const __grid_constant__
   for (int64_t task = (int64_t)blockIdx.x * 8 + warp; task < n_short; task += (int64_t)gridDim.x * 8) {
     const int ch = a.start[task / a.nslabs], c0 = (int)(task % a.nslabs) * kSlab;
     const int tok = a.pair[(ch + 1) * a.chunk].x;
-    float acc[8];
-    load_cols<float, VEC>(a.part + ((int64_t)2 * ch + 1) * a.d, c0, lane, a.d, acc);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    first_part<VEC>(a, ch, c0, lane, acc);
     add_parts<VEC>(a, tok, ch + 1, 1, c0, lane, acc);
     store_cols<VEC>(a.table + (int64_t)tok * a.d, c0, lane, a.d, acc, a.scale, a.zero_tasks == 0);
   }
