@@ -84,6 +84,36 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const void* __restrict__
   }
 }
 
+// Rows of at most 16 units: 2^lanes lanes a row, and four positions a thread, whose
+// ids and then rows are loaded together.
+template <typename T, typename V>
+__global__ void __launch_bounds__(256) embed_fwd_short_kernel(const void* __restrict__ ids, int id_bytes,
+                                                              const V* __restrict__ table,
+                                                              V* __restrict__ x, int S, int c, int D,
+                                                              int64_t vocab, int upr, int lanes,
+                                                              float scale, int* __restrict__ status) {
+  constexpr int K = 4;
+  const int unit = threadIdx.x & ((1 << lanes) - 1), rows = 256 >> lanes;
+  const int64_t p0 = (int64_t)blockIdx.x * K * rows + (threadIdx.x >> lanes);
+  int64_t id[K];
+  V v[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) id[k] = p0 + k * rows < S ? load_id(ids, id_bytes, p0 + k * rows) : -1;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    v[k] = V{};
+    if (id[k] >= vocab) report_status(status, (int)TSP_ERR_RANGE);
+    else if (id[k] >= 0 && unit < upr) v[k] = table[id[k] * upr + unit];
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (p0 + k * rows >= S || unit >= upr) continue;
+    const int row = row_of((int)(p0 + k * rows), c, D);
+    if (TSP_INB(row >= 0 && row < S, status))
+      x[(int64_t)row * upr + unit] = scale == 1.f ? v[k] : scale_unit<T, V>(v[k], scale);
+  }
+}
+
 template <typename T, typename V>
 tsp_status embed_fwd_t(const void* ids, int id_bytes, const void* table, void* x, int64_t S, int D,
                        int64_t vocab, int d, float scale, cudaStream_t st) {
@@ -91,7 +121,14 @@ tsp_status embed_fwd_t(const void* ids, int id_bytes, const void* table, void* x
   const unsigned gx = (unsigned)((S + 7) / 8);
   const int64_t full = (int64_t)num_sms() * 4;   // CTAs the GPU holds at 64 registers a thread
   Prof prof("embed_fwd", st);
-  if (gx < full) {   // few positions: short segments, on CTAs of their own
+  if (upr <= 16) {   // (131072 x 64 bf16: 5.3 us, 27 with a warp a row)
+    int lanes = 0;
+    while (1 << lanes < upr) ++lanes;
+    const int64_t rows = 4 * (256 >> lanes);
+    embed_fwd_short_kernel<T, V><<<(unsigned)((S + rows - 1) / rows), 256, 0, st>>>(
+        ids, id_bytes, (const V*)table, (V*)x, (int)S, (int)(S / (2 * D)), D, vocab, upr, lanes, scale,
+        status_word());
+  } else if (gx < full) {   // few positions: short segments, on CTAs of their own
     const int gy = (int)std::min<int64_t>((upr + 63) / 64, full / gx);
     embed_fwd_kernel<T, V, 2><<<dim3(gx, gy), 256, 0, st>>>(
         ids, id_bytes, (const V*)table, (V*)x, (int)S, (int)(S / (2 * D)), D, vocab, upr, scale,

@@ -57,7 +57,7 @@ def ref_fwd(f, x, gate, g_post, g_pre, s):
     return h, b, rf, rh
 
 
-SHAPES = [(1000, 1), (300, 2), (701, 5), (613, 27), (2003, 29), (650, 255), (1300, 513), (155, 8191),
+SHAPES = [(2600, 1000), (5003, 261), (640, 8192), (700, 5003), (1000, 1), (300, 2), (701, 5), (613, 27), (2003, 29), (650, 255), (1300, 513), (155, 8191),
           (153, 12290), (1, 1), (1, 8), (3, 7), (1, 4096), (2, 16384), (5, 64), (300, 256), (7, 1001), (4, 250),
           (9, 2057), (3, 8192), (2, 8200), (1000, 24), (3, 20000), (2, 40001), (700, 1000)]
 MODES = [(True, True, True), (False, True, True), (True, False, True), (False, True, False),
