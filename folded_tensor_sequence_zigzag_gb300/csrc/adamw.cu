@@ -184,6 +184,12 @@ struct Step {
   float lr, step_size, fix, gscale;
 };
 
+__device__ __forceinline__ float quick_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Where a lane's four elements of a group are (master, prep: or null), and the
 // group's scales.
 template <typename T>
@@ -231,11 +237,11 @@ __device__ __forceinline__ bool finish(const Args& a, const Place<T>& to, int o,
   for (int e = 0; e < 4; ++e) x[e] = root[e] = __fsqrt_rn(v[e]);
   mul4(x, s.fix, nz);
   add4(x, a.eps);
-  // With 8-bit states the quotient is the quick one, off by two half spacings: it
+  // With 8-bit states the quotient is the quick one, off by a few half spacings: it
   // enters w alone, and times lr is far below w's own spacing.  (Root and sums are
-  // what the codes are made of and stay exact.)
+  // what the codes are made of and stay exact; quick ones gain nothing.)
 #pragma unroll
-  for (int e = 0; e < 4; ++e) x[e] = BITS == 32 ? __fdiv_rn(m[e], x[e]) : __fdividef(m[e], x[e]);
+  for (int e = 0; e < 4; ++e) x[e] = BITS == 32 ? __fdiv_rn(m[e], x[e]) : m[e] * quick_rcp(x[e]);
   mul4(x, -s.step_size, nz);
   mul4(p, keep, nz);
   add4(p, x);
@@ -349,7 +355,8 @@ __device__ __forceinline__ Step step_of(const Args& a) {
   return s;
 }
 
-// 32-bit states: 28 to 32 bytes an element and little to compute.
+// 32-bit states: 28 to 32 bytes an element and little to compute; CTAs in order of
+// the elements (a 7B-shaped block: 922 us, 962 with 8 CTAs a multiprocessor walking).
 template <typename T>
 __global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ Args a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -385,8 +392,8 @@ struct Ahead {   // one warp's groups on their way
 };
 constexpr int kAheadSmem = 8 * sizeof(Ahead);
 
-template <typename T>
-__global__ void __launch_bounds__(256, 3) adamw_coded_kernel(const __grid_constant__ Args a) {
+template <typename T, int CTAS>   // CTAs a multiprocessor
+__global__ void __launch_bounds__(256, CTAS) adamw_coded_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Ahead& in = reinterpret_cast<Ahead*>(smem)[warp];
@@ -502,13 +509,21 @@ tsp_status launch_adamw(const tsp_adamw_tensor* ts, int count, const tsp_adamw_h
     if (a.count == 0) break;
     Prof prof("adamw", st);
     if (state_bits == 8) {
-      // runs of up to 8 chunks to copy ahead in, while the GPU's CTAs get two each;
-      // in order, so that what is written at a time lies together (a 7B-shaped
-      // block: 649 us, with resident CTAs walking all chunks 738)
-      a.run = (int)std::max<int64_t>(1, std::min<int64_t>(8, chunks / ((int64_t)num_sms() * 6)));
+      // Runs of up to 8 chunks to copy ahead in, while there are eight of them for
+      // every resident CTA; in order, so that what is written at a time lies together
+      // (a 7B-shaped block: 602 us, with resident CTAs walking all chunks 738).  Long
+      // runs take two CTAs a multiprocessor and no spills (602 us against 631 with
+      // three), single chunks three (10.4 M elements: 36 us against 43 with two).
+      a.run = (int)std::max<int64_t>(1, std::min<int64_t>(8, chunks / ((int64_t)num_sms() * 24)));
       const unsigned grid = (unsigned)((chunks + a.run - 1) / a.run);
-      if (dtype == TSP_BF16) adamw_coded_kernel<__nv_bfloat16><<<grid, 256, kAheadSmem, st>>>(a);
-      else adamw_coded_kernel<float><<<grid, 256, kAheadSmem, st>>>(a);
+      const bool bf = dtype == TSP_BF16;
+      if (a.run >= 4) {
+        if (bf) adamw_coded_kernel<__nv_bfloat16, 2><<<grid, 256, kAheadSmem, st>>>(a);
+        else adamw_coded_kernel<float, 2><<<grid, 256, kAheadSmem, st>>>(a);
+      } else {
+        if (bf) adamw_coded_kernel<__nv_bfloat16, 3><<<grid, 256, kAheadSmem, st>>>(a);
+        else adamw_coded_kernel<float, 3><<<grid, 256, kAheadSmem, st>>>(a);
+      }
     } else {
       const int grid = (int)std::min<int64_t>(chunks, (int64_t)num_sms() * 256);
       if (dtype == TSP_BF16) adamw_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
