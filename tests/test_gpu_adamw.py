@@ -161,6 +161,42 @@ def test_codes_are_within_half_a_step():
             assert bool((q[want > 0] > 0).all())
 
 
+@pytest.mark.parametrize("dt,total", [(BF, 66_000_000), (F32, 31_000_000)])
+def test_long_runs_of_chunks(dt, total):
+    """Tensors large enough that a CTA takes several chunks in a row (4 and 2 of
+    them), ragged and empty ones between: chunk ends inside tensors, runs that
+    cross from one to the next, on the GPU against elementary operations there."""
+    sizes = [total // 2 + 77, 0, 5, 4096 * 3 + 1, total // 4 + 2, 129, 4096, total // 4]
+    gen = torch.Generator("cuda").manual_seed(3)
+    r = lambda n: torch.randn(n, generator=gen, device="cuda")   # noqa: E731
+    params = [(0.02 * r(n)).to(dt) for n in sizes]
+    opt = tsp.AdamW(params, weight_decay=0.1, state_bits=8, betas=(B1, B2), eps=EPS)
+    state = [p.float().clone() for p in params]
+    ref = [(torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")) for n in sizes]
+    for k in (1, 2):
+        grads = [r(n) * 1e-3 for n in sizes]
+        opt.step(grads, lr=1e-3)
+        for i, n in enumerate(sizes):
+            m, root = ref[i]
+            w, m, v, root = reference(state[i], m, root * root, grads[i], 1e-3, 0.1, k)
+            got = opt.master[i] if dt == BF else opt.params[i]
+            # the quotients differ by 4 u (rcp 2, product 1, division 1) of an update of at
+            # most 1e-3 * sqrt(1 / 0.05); two numbers that far apart round to weights at
+            # most a spacing further apart, 2 u of the larger
+            tol = 2 * U * torch.maximum(w.abs(), got.abs()) + 4 * U * 5e-3
+            assert bool(((got - w).abs() <= tol).all()), (i, k)
+            assert torch.equal(opt.params[i], got.to(dt))
+            state[i] = got.clone()
+            if n == 0:
+                continue
+            qm, sm = quantise(m, False)
+            qr, sr = quantise(root, True)
+            assert torch.equal(opt.m_scale[i], sm) and torch.equal(opt.v_scale[i], sr), (i, k)
+            assert torch.equal(opt.m[i].view(torch.uint8), qm.view(torch.uint8)), (i, k)
+            assert torch.equal(opt.v[i].view(torch.uint8), qr.view(torch.uint8)), (i, k)
+            ref[i] = dequantise(qm, sm), dequantise(qr, sr)
+
+
 def test_many_tensors_take_every_launch():
     """More tensors than one launch holds, empty ones among them."""
     sizes = [(7 * i) % 300 for i in range(300)]

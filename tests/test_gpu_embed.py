@@ -194,6 +194,39 @@ def test_gradient_against_differences():
                 abs(diff) * 8 * U32
 
 
+def test_more_positions_than_tiles_of_the_sort():
+    """Over 512 * 1024 positions a CTA of the sort takes several tiles in a row."""
+    S, V, d = 600002, 3001, 4
+    gen = torch.Generator("cuda").manual_seed(1)
+    ids = torch.randint(-50, V, (S,), generator=gen, device="cuda")
+    ids[200000:260000] = 17
+    dx = torch.randn(S, d, generator=gen, device="cuda")
+    got = tsp.embed_bwd(ids, dx, V)
+    there = ids >= 0
+    z = lambda t, w: torch.zeros(V, w, dtype=torch.float64, device="cuda").index_add_(0, ids[there], t[there])   # noqa: E731
+    ref, mag = z(dx.double(), d), z(dx.double().abs(), d)
+    n = z(torch.ones(S, 1, dtype=torch.float64, device="cuda"), 1)
+    assert bool(((got.double() - ref).abs() <= mag * ((n + 3) * U32)).all())
+    assert torch.equal(got, tsp.embed_bwd(ids, dx, V))
+
+
+@pytest.mark.parametrize("S", [3, 1000, 9000])
+def test_huge_vocabulary(S):
+    """Tokens of 27 bits: too wide to be counted in one word with their position,
+    three passes of the sort; nearly all rows are absent."""
+    V, d = (1 << 26) + 5, 2
+    gen = torch.Generator().manual_seed(S)
+    ids = torch.randint(0, V, (S,), generator=gen)
+    ids[0], ids[-1] = V - 1, 0
+    ids[S // 2] = ids[S // 3]
+    dx = torch.randn(S, d, generator=gen)
+    got = tsp.embed_bwd(ids.cuda(), dx.cuda(), V)
+    at, back = ids.unique(return_inverse=True)
+    ref = torch.zeros(len(at), d, dtype=torch.float64).index_add_(0, back, dx.double())
+    assert bool(((got[at.cuda()].double().cpu() - ref).abs() <= 4 * U32 * (ref.abs() + 8)).all())
+    assert int((got != 0).any(1).sum()) == len(at)
+
+
 def test_row_offsets_past_32_bits():
     """A table of more than 2^31 elements: the last rows are read and written."""
     V, d = 530000, 4096                     # 2.17e9 elements
