@@ -18,6 +18,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <exception>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <string>
@@ -1026,7 +1027,8 @@ tsp_status tsp_embed_fwd(const void* ids, int32_t id_bytes, const void* table, v
                          void* stream) {
   const tsp_status r = check_embed(S, D, V, d);
   if (r != TSP_OK) return r;
-  if (!ids_ok(ids, id_bytes) || !al16(table) || !al16(x_z) || !std::isfinite(scale) ||
+  if (!ids_ok(ids, id_bytes) || !al16(table) || !al16(x_z) || x_z == table || x_z == ids ||
+      !std::isfinite(scale) ||
       (dtype != TSP_F32 && dtype != TSP_BF16))
     return TSP_ERR_INVALID_ARG;
   return launch_embed_fwd(ids, id_bytes, table, x_z, S, D, V, d, scale, dtype, S_(stream));
@@ -1041,12 +1043,24 @@ tsp_status tsp_embed_bwd(const void* ids, int32_t id_bytes, const void* dx_z, in
                          int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
   const tsp_status r = check_embed(S, D, V, d);
   if (r != TSP_OK) return r;
-  if (!ids_ok(ids, id_bytes) || !al16(dx_z) || !al16(dtable) || !al16(ws) ||
-      !std::isfinite(scale) || (dx_dtype != TSP_F32 && dx_dtype != TSP_BF16) ||
+  if (!ids_ok(ids, id_bytes) || !al16(dx_z) || !al16(dtable) || !al16(ws) || dtable == dx_z ||
+      ws == dx_z || ws == dtable || !std::isfinite(scale) || (dx_dtype != TSP_F32 && dx_dtype != TSP_BF16) ||
       ws_bytes < embed_bwd_ws_bytes(S, d))
     return TSP_ERR_INVALID_ARG;
   return launch_embed_bwd(ids, id_bytes, dx_z, dx_dtype, dtable, S, D, V, d, scale, accumulate != 0,
                           ws, S_(stream));
+}
+
+// true if no output is an input, or another output (NULLs aside)
+static bool apart(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+  for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
+    if (!*o) continue;
+    for (const void* i : ins)
+      if (i == *o) return false;
+    for (const void* const* q = outs.begin(); q != o; ++q)
+      if (*q == *o) return false;
+  }
+  return true;
 }
 
 // true if p is a 16-byte aligned pointer when `used`, and NULL when not
@@ -1070,7 +1084,8 @@ tsp_status tsp_norm_residual_fwd(const void* f, const void* x, const void* gate,
   if (r != TSP_OK) return r;
   if (!al16(f) || !al16(x) || !al16(h) || (gate && !al16(gate)) || (g_post && !al16(g_post)) ||
       (g_pre && !al16(g_pre)) || !used_or_null(b, g_pre != nullptr) || !(eps >= 0.f) ||
-      (rstd_f && !(g_post && al16(rstd_f))) || (rstd_h && !(g_pre && al16(rstd_h))))
+      (rstd_f && !(g_post && al16(rstd_f))) || (rstd_h && !(g_pre && al16(rstd_h))) ||
+      !apart({h == x ? nullptr : h, b, rstd_f, rstd_h}, {f, x, gate, g_post, g_pre}) || b == h)
     return TSP_ERR_INVALID_ARG;
   return launch_norm_residual_fwd(f, x, gate, g_post, g_pre, h, b, rstd_f, rstd_h, rows, n, scale,
                                   eps, dtype, stream_dtype, S_(stream));
@@ -1095,7 +1110,9 @@ tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f
       (pre && !al16(g_pre)) || (dh ? !al16(dh) : !pre) || !used_or_null(db, pre) ||
       !used_or_null(h, pre) || !used_or_null(rstd_h, pre) || !used_or_null(dg_pre, pre) ||
       !used_or_null(rstd_f, post) || !used_or_null(dg_post, post) ||
-      !used_or_null(dgate, gate != nullptr))
+      !used_or_null(dgate, gate != nullptr) ||
+      !apart({dx == dh ? nullptr : dx, df, dgate, dg_post, dg_pre},
+             {dh, db, f, gate, h, g_post, g_pre, rstd_f, rstd_h}))
     return TSP_ERR_INVALID_ARG;
   if ((post || pre) && (!al16(ws) || ws_bytes < norm_residual_bwd_ws_bytes(rows, n)))
     return TSP_ERR_INVALID_ARG;

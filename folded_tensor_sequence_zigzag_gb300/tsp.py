@@ -631,6 +631,13 @@ def _arg(name, t, shape, dtype, index):
     return t.data_ptr()
 
 
+def _ws_arg(ws, index):
+    """(address, bytes) of a workspace the caller keeps."""
+    if ws.dtype != torch.uint8 or ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous uint8 tensor on the device of the other tensors")
+    return ws.data_ptr(), ws.numel()
+
+
 _ENUM = {torch.bfloat16: TSP_BF16, torch.float32: TSP_F32}
 
 
@@ -692,9 +699,9 @@ def embed_bwd(ids, dx_z, V: int, D: int = 1, scale: float = 1.0, out=None,
         lib = load()
         if ws is None:
             ws = _ws(lib.tsp_embed_bwd_workspace_bytes(S, V, d), dev)
+        pw, nw = _ws_arg(ws, index)
         _check(lib.tsp_embed_bwd(pi, id_bytes, px, e, po, S, D, V, d, scale,
-                                 1 if accumulate else 0, ws.data_ptr(), ws.numel(), st),
-               "tsp_embed_bwd")
+                                 1 if accumulate else 0, pw, nw, st), "tsp_embed_bwd")
     return out
 
 
@@ -774,10 +781,10 @@ def norm_residual_bwd(dh, db, f, h, g_post=None, g_pre=None, rstd_f=None, rstd_h
             pdq = out["dg_pre"].data_ptr()
         if ws is None and (pp is not None or pq is not None):
             ws = _ws(lib.tsp_norm_residual_bwd_workspace_bytes(rows, n), dev)
+        pw, nw = (None, 0) if ws is None else _ws_arg(ws, index)
         _check(lib.tsp_norm_residual_bwd(pdh, pdb, pf, pz, ph, pp, pq, prf, prh, pdx,
                                          out["df"].data_ptr(), pdz, pdp, pdq, rows, n, scale, e, es,
-                                         None if ws is None else ws.data_ptr(),
-                                         0 if ws is None else ws.numel(), st),
+                                         pw, nw, st),
                "tsp_norm_residual_bwd")
     return out
 

@@ -509,7 +509,8 @@ tsp_status tsp_rank_attn_bwd_finish(const tsp_cfg* cfg, int32_t r, const void* x
  *   rows are left alone (a table tied to the output projection).  dx_z is
  *   what tsp_stack_bwd leaves (dx_dtype TSP_F32) or bf16 (TSP_BF16).  The
  *   positions are sorted by token first and each sum runs in the order of the
- *   positions, in fp32, so equal calls give equal bits.
+ *   positions, in fp32, so equal calls give equal bits.  (With accumulate
+ *   the memory adds, which may take a subnormal for zero.)
  *
  *   ids       [S] global token order, id_bytes 4 (int32) or 8 (int64); needs
  *             only its own alignment.  id < 0: padding -- a zero row of x_z,
@@ -520,6 +521,7 @@ tsp_status tsp_rank_attn_bwd_finish(const tsp_cfg* cfg, int32_t r, const void* x
  *             the global order and takes every S >= 1 (decoded tokens)
  *   ws        tsp_embed_bwd_workspace_bytes(S, V, d) bytes; nothing in it has
  *             to survive the call
+ * No output may overlap another argument.
  * Errors: TSP_ERR_INVALID_ARG (sizes, NULL or misaligned pointers, a scale
  *   that is not finite, a short workspace); TSP_ERR_UNSUPPORTED for S > 2^30
  *   or V > 2^31 - 2.  tsp_embed_bwd_workspace_bytes returns 0 for sizes that
@@ -553,7 +555,9 @@ tsp_status tsp_embed_bwd(const void* ids, int32_t id_bytes, const void* dx_z, in
  * dg_post, dg_pre [n] fp32, overwritten, summed over the rows in a fixed
  * order.  ws: tsp_norm_residual_bwd_workspace_bytes(rows, n) bytes (NULL
  * without gains).
- * A pointer that the NULLs above leave without a use has to be NULL too.
+ * A pointer that the NULLs above leave without a use has to be NULL too; an
+ * output may overlap no other argument but for h on x and dx on dh (the same
+ * address).  A row of zeros with eps == 0 has no norm (NaN).
  * Errors: TSP_ERR_INVALID_ARG; TSP_ERR_UNSUPPORTED for n > 2^24. */
 tsp_status tsp_norm_residual_fwd(const void* f, const void* x, const void* gate,
                                  const void* g_post, const void* g_pre, void* h, void* b,
@@ -575,7 +579,7 @@ tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f
  *   w = w (1 - lr weight_decay)
  *       - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  * in fp32, each elementary operation rounded by itself (with 8-bit states the
- * quotient by two half spacings at most).
+ * quotient m / (...) within four half spacings).
  *
  * tsp_adamw_tensor (a host array of `count`; the pointers are device pointers):
  *   n        elements, >= 0 (0: skipped, its pointers may be NULL)
@@ -586,8 +590,8 @@ tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f
  *   g        [n] fp32
  *   m, v     state_bits 32: [n] fp32.  state_bits 8: [n] e4m3 codes, v holding
  *            sqrt(v); m_scale, v_scale [ceil(n / TSP_ADAMW_BLOCK)] fp32 (NULL
- *            with 32; 4-byte aligned), a block's largest magnitude / 448: a code stands for
- *            code * scale.  A block below 2^-100 is held as zeros; a positive
+ *            with 32; 4-byte aligned), a block's largest magnitude / 448: a code
+ *            stands for code * scale.  A block below 2^-100 is held as zeros; a positive
  *            sqrt(v) takes at least the smallest code.  Zero bytes are the
  *            initial state of either.  (Nearest rounding: an 8-bit v that moves
  *            by less than half a spacing relative to its block stays.)
@@ -595,7 +599,7 @@ tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f
  *            operand copy tsp_block_weights_prepare would make of it (a weight
  *            fp16 cannot hold records TSP_ERR_RANGE)
  * tsp_adamw_hyper: lr, beta1, beta2 in [0, 1), eps >= 0, step t >= 1 (the first
- *   update is 1).  lr_dev, step_dev, gscale_dev (nullable DEVICE pointers to one
+ *   update is 1; behind step_dev it is not checked).  lr_dev, step_dev, gscale_dev (nullable DEVICE pointers to one
  *   value, read when the kernel runs): replace lr and step, and scale the
  *   gradients (clipping by a norm computed on the device).  A captured call
  *   keeps the host values it was captured with; a graph that is replayed over

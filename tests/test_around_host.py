@@ -24,11 +24,11 @@ def lib():
     (INV, dict(S=0)), (INV, dict(S=-4)), (INV, dict(D=0)), (INV, dict(D=65, S=130)),
     (INV, dict(S=18, D=4)), (INV, dict(V=0)), (INV, dict(d=0)), (INV, dict(ids=None)),
     (INV, dict(ids=0x10004)), (INV, dict(id_bytes=2)), (INV, dict(table=None)),
-    (INV, dict(table=MIS)), (INV, dict(x=MIS)), (INV, dict(scale=float("nan"))),
+    (INV, dict(table=MIS)), (INV, dict(x=MIS)), (INV, dict(x=2 * OK)), (INV, dict(x=OK)), (INV, dict(scale=float("nan"))),
     (INV, dict(scale=float("inf"))), (INV, dict(dtype=2)),
     (UNS, dict(S=(1 << 30) + 2, D=1)), (UNS, dict(V=(1 << 31) - 1))])
 def test_embed_fwd_refuses(lib, code, bad):
-    a = dict(ids=OK, id_bytes=8, table=OK, x=OK, S=16, D=4, V=100, d=8, scale=1.0, dtype=1)
+    a = dict(ids=OK, id_bytes=8, table=2 * OK, x=3 * OK, S=16, D=4, V=100, d=8, scale=1.0, dtype=1)
     a.update(bad)
     assert lib.tsp_embed_fwd(a["ids"], a["id_bytes"], a["table"], a["x"], a["S"], a["D"], a["V"],
                              a["d"], a["scale"], a["dtype"], None) == code
@@ -37,10 +37,10 @@ def test_embed_fwd_refuses(lib, code, bad):
 @pytest.mark.parametrize("bad", [
     dict(S=0), dict(S=18, D=4), dict(V=0), dict(ids=None), dict(id_bytes=16), dict(dx=MIS),
     dict(dtable=None), dict(ws=None), dict(ws=MIS), dict(short=1), dict(dtype=3),
-    dict(scale=float("nan"))])
+    dict(scale=float("nan")), dict(dtable=2 * OK), dict(ws=3 * OK)])
 def test_embed_bwd_refuses(lib, bad):
-    a = dict(ids=OK, id_bytes=4, dx=OK, dtype=0, dtable=OK, S=16, D=4, V=100, d=8, scale=1.0,
-             ws=OK, short=0)
+    a = dict(ids=OK, id_bytes=4, dx=2 * OK, dtype=0, dtable=3 * OK, S=16, D=4, V=100, d=8, scale=1.0,
+             ws=4 * OK, short=0)
     a.update(bad)
     nb = lib.tsp_embed_bwd_workspace_bytes(16, 100, 8) - a["short"]
     assert lib.tsp_embed_bwd(a["ids"], a["id_bytes"], a["dx"], a["dtype"], a["dtable"], a["S"],
@@ -65,11 +65,14 @@ def test_workspace_sizes(lib):
     (INV, dict(b=None)), (INV, dict(g_pre=None)), (INV, dict(gate=MIS)), (INV, dict(rows=0)),
     (INV, dict(n=0)), (INV, dict(eps=-1.0)), (INV, dict(eps=float("nan"))),
     (INV, dict(scale=float("inf"))), (INV, dict(dtype=2)), (INV, dict(dtype=0, sdt=1)),
-    (INV, dict(rstd_f=MIS)), (INV, dict(g_post=None)), (UNS, dict(n=(1 << 24) + 1))])
+    (INV, dict(rstd_f=MIS)), (INV, dict(g_post=None)), (UNS, dict(n=(1 << 24) + 1)),
+    (INV, dict(h="f")), (INV, dict(b="f")), (INV, dict(b="x")), (INV, dict(b="h")),
+    (INV, dict(h="x", b="x")), (INV, dict(rstd_f="rstd_h"))])
 def test_norm_residual_fwd_refuses(lib, code, bad):
-    a = dict(f=OK, x=OK, gate=None, g_post=OK, g_pre=OK, h=OK, b=OK, rstd_f=OK, rstd_h=OK, rows=4,
-             n=8, scale=1.0, eps=1e-6, dtype=1, sdt=0)
-    a.update(bad)
+    names = ("f", "x", "gate", "g_post", "g_pre", "h", "b", "rstd_f", "rstd_h")
+    a = {k: OK + 0x1000 * i for i, k in enumerate(names)}
+    a.update(gate=None, rows=4, n=8, scale=1.0, eps=1e-6, dtype=1, sdt=0)
+    a.update({k: a[v] if isinstance(v, str) else v for k, v in bad.items()})
     assert lib.tsp_norm_residual_fwd(*a.values(), None) == code
 
 
@@ -79,12 +82,15 @@ def test_norm_residual_fwd_refuses(lib, code, bad):
     (INV, dict(rstd_f=None)), (INV, dict(dg_post=None)), (INV, dict(dg_pre=None)),
     (INV, dict(g_post=None)), (INV, dict(g_pre=None)), (INV, dict(rows=-1)), (INV, dict(n=0)),
     (INV, dict(ws=None)), (INV, dict(short=1)), (INV, dict(dtype=0, sdt=1)),
-    (UNS, dict(n=(1 << 24) + 1))])
+    (UNS, dict(n=(1 << 24) + 1)), (INV, dict(df="f")), (INV, dict(dgate="gate")),
+    (INV, dict(dx="db")), (INV, dict(df="dx")), (INV, dict(dg_post="g_post")),
+    (INV, dict(dg_post="dg_pre"))])
 def test_norm_residual_bwd_refuses(lib, code, bad):
-    a = dict(dh=OK, db=OK, f=OK, gate=OK, h=OK, g_post=OK, g_pre=OK, rstd_f=OK, rstd_h=OK, dx=OK,
-             df=OK, dgate=OK, dg_post=OK, dg_pre=OK, rows=4, n=8, scale=1.0, dtype=1, sdt=0, ws=OK,
-             short=0)
-    a.update(bad)
+    names = ("dh", "db", "f", "gate", "h", "g_post", "g_pre", "rstd_f", "rstd_h", "dx", "df",
+             "dgate", "dg_post", "dg_pre")
+    a = {k: OK + 0x1000 * i for i, k in enumerate(names)}
+    a.update(rows=4, n=8, scale=1.0, dtype=1, sdt=0, ws=OK, short=0)
+    a.update({k: a[v] if isinstance(v, str) else v for k, v in bad.items()})
     nb = lib.tsp_norm_residual_bwd_workspace_bytes(4, 8) - a.pop("short")
     assert lib.tsp_norm_residual_bwd(*a.values(), nb, None) == code
 

@@ -242,6 +242,19 @@ def test_row_offsets_past_32_bits():
     assert float(grad.sum(dtype=torch.float64)) == 4.0 * d
 
 
+def test_workspaces_are_checked():
+    ids, dx = torch.zeros(4, dtype=torch.int64, device="cuda"), torch.ones(4, 8, device="cuda")
+    n = tsp.embed_bwd_workspace_bytes(4, 3, 8)
+    for ws in (torch.zeros(n, device="cuda"), torch.zeros(n, dtype=torch.uint8)):
+        with pytest.raises(ValueError):
+            tsp.embed_bwd(ids, dx, 3, ws=ws)
+    with pytest.raises(tsp.TspError) as e:
+        tsp.embed_bwd(ids, dx, 3, ws=torch.zeros(n - 1, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == tsp.TSP_ERR_INVALID_ARG
+    with pytest.raises(ValueError):
+        tsp.embed_fwd(ids.cpu(), torch.ones(3, 8, device="cuda"))
+
+
 def test_zigzag_forward_is_gather_then_permute():
     S, D, V, d = 512, 8, 100, 256
     ids = make_ids("uniform", S, V, 1).cuda()
