@@ -1015,9 +1015,29 @@ void tsp_debug_skip_stage(int32_t n) { g_debug_skip.store(n > 0 ? n : 0); }
 static tsp_status check_embed(int64_t S, int32_t D, int64_t V, int32_t d) {
   if (S <= 0 || D < 1 || D > 64 || V <= 0 || d <= 0) return TSP_ERR_INVALID_ARG;
   if (D > 1 && S % (2 * (int64_t)D) != 0) return TSP_ERR_INVALID_ARG;
-  if (S > (int64_t)1 << 30 || V > INT32_MAX - 1) return TSP_ERR_UNSUPPORTED;
+  if (S > (int64_t)1 << 30 || V > INT32_MAX - 1 || d > 1 << 24) return TSP_ERR_UNSUPPORTED;
   return TSP_OK;
 }
+// an argument's memory; p NULL: none
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+// true if no output shares memory with an input or another output
+static bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return a.p && b.p && (x < y ? y - x < a.bytes : x - y < b.bytes);
+  };
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (meet(*o, i)) return false;
+    for (const Span* q = outs.begin(); q != o; ++q)
+      if (meet(*o, *q)) return false;
+  }
+  return true;
+}
+
 static bool ids_ok(const void* ids, int32_t id_bytes) {
   return ids && (id_bytes == 4 || id_bytes == 8) && (uintptr_t)ids % (uintptr_t)id_bytes == 0;
 }
@@ -1027,9 +1047,10 @@ tsp_status tsp_embed_fwd(const void* ids, int32_t id_bytes, const void* table, v
                          void* stream) {
   const tsp_status r = check_embed(S, D, V, d);
   if (r != TSP_OK) return r;
-  if (!ids_ok(ids, id_bytes) || !al16(table) || !al16(x_z) || x_z == table || x_z == ids ||
-      !std::isfinite(scale) ||
-      (dtype != TSP_F32 && dtype != TSP_BF16))
+  const size_t e = dtype == TSP_F32 ? 4 : 2;
+  if (!ids_ok(ids, id_bytes) || !al16(table) || !al16(x_z) || !std::isfinite(scale) ||
+      (dtype != TSP_F32 && dtype != TSP_BF16) ||
+      !apart({{x_z, S * d * e}}, {{table, V * d * e}, {ids, (size_t)S * id_bytes}}))
     return TSP_ERR_INVALID_ARG;
   return launch_embed_fwd(ids, id_bytes, table, x_z, S, D, V, d, scale, dtype, S_(stream));
 }
@@ -1043,24 +1064,14 @@ tsp_status tsp_embed_bwd(const void* ids, int32_t id_bytes, const void* dx_z, in
                          int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
   const tsp_status r = check_embed(S, D, V, d);
   if (r != TSP_OK) return r;
-  if (!ids_ok(ids, id_bytes) || !al16(dx_z) || !al16(dtable) || !al16(ws) || dtable == dx_z ||
-      ws == dx_z || ws == dtable || !std::isfinite(scale) || (dx_dtype != TSP_F32 && dx_dtype != TSP_BF16) ||
-      ws_bytes < embed_bwd_ws_bytes(S, d))
+  const size_t e = dx_dtype == TSP_F32 ? 4 : 2, need = embed_bwd_ws_bytes(S, d);
+  if (!ids_ok(ids, id_bytes) || !al16(dx_z) || !al16(dtable) || !al16(ws) || ws_bytes < need ||
+      !std::isfinite(scale) || (dx_dtype != TSP_F32 && dx_dtype != TSP_BF16) ||
+      !apart({{dtable, V * d * sizeof(float)}, {ws, need}},
+             {{dx_z, S * d * e}, {ids, (size_t)S * id_bytes}}))
     return TSP_ERR_INVALID_ARG;
   return launch_embed_bwd(ids, id_bytes, dx_z, dx_dtype, dtable, S, D, V, d, scale, accumulate != 0,
                           ws, S_(stream));
-}
-
-// true if no output is an input, or another output (NULLs aside)
-static bool apart(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
-  for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
-    if (!*o) continue;
-    for (const void* i : ins)
-      if (i == *o) return false;
-    for (const void* const* q = outs.begin(); q != o; ++q)
-      if (*q == *o) return false;
-  }
-  return true;
 }
 
 // true if p is a 16-byte aligned pointer when `used`, and NULL when not
@@ -1072,7 +1083,7 @@ static tsp_status check_norm_residual(int64_t rows, int32_t n, float scale, int3
   if (dtype != TSP_F32 && dtype != TSP_BF16) return TSP_ERR_INVALID_ARG;
   if (stream_dtype != TSP_F32 && !(stream_dtype == TSP_BF16 && dtype == TSP_BF16))
     return TSP_ERR_INVALID_ARG;
-  return n > 1 << 24 ? TSP_ERR_UNSUPPORTED : TSP_OK;
+  return n > 1 << 24 || rows > INT32_MAX ? TSP_ERR_UNSUPPORTED : TSP_OK;
 }
 
 tsp_status tsp_norm_residual_fwd(const void* f, const void* x, const void* gate,
@@ -1084,8 +1095,11 @@ tsp_status tsp_norm_residual_fwd(const void* f, const void* x, const void* gate,
   if (r != TSP_OK) return r;
   if (!al16(f) || !al16(x) || !al16(h) || (gate && !al16(gate)) || (g_post && !al16(g_post)) ||
       (g_pre && !al16(g_pre)) || !used_or_null(b, g_pre != nullptr) || !(eps >= 0.f) ||
-      (rstd_f && !(g_post && al16(rstd_f))) || (rstd_h && !(g_pre && al16(rstd_h))) ||
-      !apart({h == x ? nullptr : h, b, rstd_f, rstd_h}, {f, x, gate, g_post, g_pre}) || b == h)
+      (rstd_f && !(g_post && al16(rstd_f))) || (rstd_h && !(g_pre && al16(rstd_h))))
+    return TSP_ERR_INVALID_ARG;
+  const size_t t = dtype == TSP_F32 ? 4 : 2, ts = stream_dtype == TSP_F32 ? 4 : 2, all = rows * n;
+  if (!apart({{h, all * ts}, {b, all * t}, {rstd_f, rows * sizeof(float)}, {rstd_h, rows * sizeof(float)}},
+             {{f, all * t}, {x == h ? nullptr : x, all * ts}, {gate, all * t}, {g_post, n * t}, {g_pre, n * t}}))
     return TSP_ERR_INVALID_ARG;
   return launch_norm_residual_fwd(f, x, gate, g_post, g_pre, h, b, rstd_f, rstd_h, rows, n, scale,
                                   eps, dtype, stream_dtype, S_(stream));
@@ -1110,11 +1124,15 @@ tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f
       (pre && !al16(g_pre)) || (dh ? !al16(dh) : !pre) || !used_or_null(db, pre) ||
       !used_or_null(h, pre) || !used_or_null(rstd_h, pre) || !used_or_null(dg_pre, pre) ||
       !used_or_null(rstd_f, post) || !used_or_null(dg_post, post) ||
-      !used_or_null(dgate, gate != nullptr) ||
-      !apart({dx == dh ? nullptr : dx, df, dgate, dg_post, dg_pre},
-             {dh, db, f, gate, h, g_post, g_pre, rstd_f, rstd_h}))
+      !used_or_null(dgate, gate != nullptr))
     return TSP_ERR_INVALID_ARG;
-  if ((post || pre) && (!al16(ws) || ws_bytes < norm_residual_bwd_ws_bytes(rows, n)))
+  const size_t need = post || pre ? norm_residual_bwd_ws_bytes(rows, n) : 0;
+  if (need && (!al16(ws) || ws_bytes < need)) return TSP_ERR_INVALID_ARG;
+  const size_t t = dtype == TSP_F32 ? 4 : 2, ts = stream_dtype == TSP_F32 ? 4 : 2, all = rows * n;
+  const size_t f4 = sizeof(float);
+  if (!apart({{dx, all * f4}, {df, all * t}, {dgate, all * t}, {dg_post, n * f4}, {dg_pre, n * f4}, {need ? ws : nullptr, need}},
+             {{dh == dx ? nullptr : dh, all * f4}, {db, all * f4}, {f, all * t}, {gate, all * t}, {h, all * ts},
+              {g_post, n * t}, {g_pre, n * t}, {rstd_f, rows * f4}, {rstd_h, rows * f4}}))
     return TSP_ERR_INVALID_ARG;
   return launch_norm_residual_bwd(dh, db, f, gate, h, g_post, g_pre, rstd_f, rstd_h, dx, df, dgate,
                                   dg_post, dg_pre, rows, n, scale, dtype, stream_dtype, ws,

@@ -54,7 +54,8 @@ __device__ __forceinline__ V scale_unit(V u, float s) {
 // A warp a position, a segment of 32 * LOADS units of sizeof(V) bytes at a time
 // (stride gridDim.y), LOADS loads in flight a lane.  Not a persistent grid: CTAs
 // started in order keep the rows written at a time next to each other (131072 x
-// 4096 bf16: 232 us with 4 resident CTAs a multiprocessor walking the positions).
+// 4096 bf16 out of 32000 rows: 207 us, 1.32 GB of DRAM traffic at 6.4 TB/s; 232 us
+// with 4 resident CTAs a multiprocessor walking the positions).
 template <typename T, typename V, int LOADS>
 __global__ void __launch_bounds__(256) embed_fwd_kernel(const void* __restrict__ ids, int id_bytes,
                                                         const V* __restrict__ table,
@@ -350,12 +351,15 @@ int run_of(int64_t S) {
 // ---------------------------------------------------------------------------
 // A warp takes a chunk of the sorted positions and a slab of 256 columns (8 a
 // lane) and walks the chunk's rows, four or (16-bit) eight of them on their way at
-// a time; places and tokens come 32 at a time.  A token whose positions lie inside the chunk is written (or added)
-// to its table row at once; one that came in from the chunk before leaves its
-// part in slot 2*chunk, one that starts here and goes on in slot 2*chunk + 1.
-// Step 3 adds those up.  The first warps of the grid write the zero rows of absent
-// tokens, eight rows each, which they look up in the sorted tokens: plain stores
-// next to the other warps' loads.
+// a time; places and tokens come 32 at a time.  A token whose positions lie inside
+// the chunk is written (or added) to its table row at once; one that came in from
+// the chunk before leaves its part in slot 2*chunk, one that starts here and goes on
+// in slot 2*chunk + 1.  Step 3 adds those up.  So a frequent token is split over as
+// many warps as it has chunks, and every sum has one order.  The first warps of the
+// grid write the zero rows of absent tokens, eight rows each, which they look up in
+// the sorted tokens: plain stores next to the other warps' loads.  HBM-bound where
+// rows are long (32768 x 4096 fp32 into 32000 rows: 1.01 GB in 162 us of the call's
+// 181), by the latency of a warp's few loads where they are short.
 constexpr int kSlab = 256, kZeroRows = 8, kLong = 12;
 
 // A lane's eight columns of a row: two groups of four next to each other (VEC), or
@@ -509,10 +513,6 @@ __global__ void __launch_bounds__(256) embed_sum_kernel(const T* __restrict__ dx
   }
 }
 
-// Step 3: a token that starts in one chunk and ends in a later one (step 2 has
-// listed the chunks where one starts): its parts added in chunk order, a warp a
-// token and slab.  The few tokens of more than kLong chunks get a CTA a slab, whose
-// warps add up every eighth part each, then the eight sums in order.
 // acc += the part of the token that starts in chunk ch and goes on
 template <bool VEC>
 __device__ __forceinline__ void first_part(const SumArgs& a, int ch, int c0, int lane, float (&acc)[8]) {
@@ -542,6 +542,11 @@ __device__ __forceinline__ void add_parts(const SumArgs& a, int tok, int k, int 
   }
 }
 
+// Step 3: a token that starts in one chunk and ends in a later one (step 2 has
+// listed the chunks where one starts): its parts added in chunk order, a warp a
+// token and slab.  The few tokens of more than kLong chunks get a CTA a slab, whose
+// warps add up every eighth part each, then the eight sums in order.  Bound by the
+// latency of its four dependent loads (7 us for 32768 x 4096).
 template <bool VEC>
 __global__ void __launch_bounds__(256) embed_join_kernel(const __grid_constant__ SumArgs a) {
   __shared__ float sums[8][kSlab];

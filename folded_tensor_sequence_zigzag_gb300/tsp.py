@@ -813,7 +813,8 @@ class AdamW:
     from them), None updates the tensors themselves, a list gives the masters.
     ``m``, ``v``, ``m_scale``, ``v_scale``: lists of existing states to go on
     with (default: zeros).  ``prep``: for each tensor the fp16 operand copy to
-    refresh (prep_views) or None.
+    refresh (prep_views) or None.  All of them are updated in place and stay
+    where they are: new values (a checkpoint's) are copied into them.
     """
 
     def __init__(self, params, weight_decay=0.0, state_bits: int = 32, master=True, m=None, v=None,
@@ -866,6 +867,17 @@ class AdamW:
             t.m_scale = _arg(f"m_scale[{i}]", self.m_scale[i], blocks[i], f32, index)
             t.v_scale = _arg(f"v_scale[{i}]", self.v_scale[i], blocks[i], f32, index)
             t.weight_decay = float(weight_decay[i])
+        # The array holds addresses: the memory behind them is kept here too, and a
+        # weight that has moved (step) or an exchanged state (a tuple) is refused.
+        self._held = [x.detach() for x in self.params + self.m + self.v + self.m_scale +
+                      self.v_scale + self.master + self.prep if x is not None]
+        spans = sorted((x.data_ptr(), x.data_ptr() + x.numel() * x.element_size())
+                       for x in self._held if x.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("two of the tensors, states, masters or operand copies share memory")
+        for name in ("params", "m", "v", "m_scale", "v_scale", "master", "prep"):
+            setattr(self, name, tuple(getattr(self, name)))
+        self._at = [p.data_ptr() for p in self.params]
         self._sizes = [p.numel() for p in self.params]
         # the gradients' addresses in the array, set by every step
         words = ctypes.sizeof(AdamwTensor) // 8
@@ -886,6 +898,8 @@ class AdamW:
                 any([i != index for i in map(tensor.get_device, grads)]):
             raise ValueError(f"gradients: {len(self._sizes)} contiguous fp32 tensors of the sizes "
                              "and on the device of the tensors they are for")
+        if list(map(tensor.data_ptr, self.params)) != self._at:
+            raise ValueError("a tensor's memory is not the one this object was made for")
         self._g[:] = list(map(tensor.data_ptr, grads))
         hy = AdamwHyper(0.0, self.betas[0], self.betas[1], self.eps, 1)
         if isinstance(lr, torch.Tensor):

@@ -523,9 +523,9 @@ tsp_status tsp_rank_attn_bwd_finish(const tsp_cfg* cfg, int32_t r, const void* x
  *             to survive the call
  * No output may overlap another argument.
  * Errors: TSP_ERR_INVALID_ARG (sizes, NULL or misaligned pointers, a scale
- *   that is not finite, a short workspace); TSP_ERR_UNSUPPORTED for S > 2^30
- *   or V > 2^31 - 2.  tsp_embed_bwd_workspace_bytes returns 0 for sizes that
- *   the call would refuse. */
+ *   that is not finite, a short workspace); TSP_ERR_UNSUPPORTED for S > 2^30,
+ *   V > 2^31 - 2 or d > 2^24.  tsp_embed_bwd_workspace_bytes returns 0 for
+ *   sizes that the call would refuse. */
 tsp_status tsp_embed_fwd(const void* ids, int32_t id_bytes, const void* table, void* x_z,
                          int64_t S, int32_t D, int64_t V, int32_t d, float scale, int32_t dtype,
                          void* stream);
@@ -558,7 +558,8 @@ tsp_status tsp_embed_bwd(const void* ids, int32_t id_bytes, const void* dx_z, in
  * A pointer that the NULLs above leave without a use has to be NULL too; an
  * output may overlap no other argument but for h on x and dx on dh (the same
  * address).  A row of zeros with eps == 0 has no norm (NaN).
- * Errors: TSP_ERR_INVALID_ARG; TSP_ERR_UNSUPPORTED for n > 2^24. */
+ * Errors: TSP_ERR_INVALID_ARG; TSP_ERR_UNSUPPORTED for n > 2^24 or
+ * rows > 2^31 - 1. */
 tsp_status tsp_norm_residual_fwd(const void* f, const void* x, const void* gate,
                                  const void* g_post, const void* g_pre, void* h, void* b,
                                  float* rstd_f, float* rstd_h, int64_t rows, int32_t n,
@@ -598,12 +599,14 @@ tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f
  *   prep     [n] fp16 or NULL (TSP_BF16 only): receives the new weight as the
  *            operand copy tsp_block_weights_prepare would make of it (a weight
  *            fp16 cannot hold records TSP_ERR_RANGE)
+ * No two of a call's arrays may share memory (gradients among themselves may).
  * tsp_adamw_hyper: lr, beta1, beta2 in [0, 1), eps >= 0, step t >= 1 (the first
- *   update is 1; behind step_dev it is not checked).  lr_dev, step_dev, gscale_dev (nullable DEVICE pointers to one
- *   value, read when the kernel runs): replace lr and step, and scale the
- *   gradients (clipping by a norm computed on the device).  A captured call
- *   keeps the host values it was captured with; a graph that is replayed over
- *   many steps passes step_dev and advances it.
+ *   update is 1; behind step_dev it is not checked).  lr_dev, step_dev,
+ *   gscale_dev (nullable DEVICE pointers to one value, read when the kernel
+ *   runs): replace lr and step, and scale the gradients (clipping by a norm
+ *   computed on the device).  A captured call keeps the host values it was
+ *   captured with; a graph that is replayed over many steps passes step_dev and
+ *   advances it.
  * One launch per 128 tensors.  Errors: TSP_ERR_INVALID_ARG (also for two
  *   tensors whose weights overlap: one call may update a weight once). */
 #define TSP_ADAMW_BLOCK 128

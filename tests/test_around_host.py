@@ -24,9 +24,12 @@ def lib():
     (INV, dict(S=0)), (INV, dict(S=-4)), (INV, dict(D=0)), (INV, dict(D=65, S=130)),
     (INV, dict(S=18, D=4)), (INV, dict(V=0)), (INV, dict(d=0)), (INV, dict(ids=None)),
     (INV, dict(ids=0x10004)), (INV, dict(id_bytes=2)), (INV, dict(table=None)),
-    (INV, dict(table=MIS)), (INV, dict(x=MIS)), (INV, dict(x=2 * OK)), (INV, dict(x=OK)), (INV, dict(scale=float("nan"))),
+    (INV, dict(table=MIS)), (INV, dict(x=MIS)), (INV, dict(x=2 * OK)), (INV, dict(x=OK)),
+    # the last 16 bytes of the table and of the ids, and the other way round
+    (INV, dict(x=2 * OK + 1584)), (INV, dict(x=OK + 112)), (INV, dict(x=2 * OK - 240)),
+    (INV, dict(x=OK - 240)), (INV, dict(scale=float("nan"))),
     (INV, dict(scale=float("inf"))), (INV, dict(dtype=2)),
-    (UNS, dict(S=(1 << 30) + 2, D=1)), (UNS, dict(V=(1 << 31) - 1))])
+    (UNS, dict(S=(1 << 30) + 2, D=1)), (UNS, dict(V=(1 << 31) - 1)), (UNS, dict(d=(1 << 24) + 1))])
 def test_embed_fwd_refuses(lib, code, bad):
     a = dict(ids=OK, id_bytes=8, table=2 * OK, x=3 * OK, S=16, D=4, V=100, d=8, scale=1.0, dtype=1)
     a.update(bad)
@@ -37,7 +40,9 @@ def test_embed_fwd_refuses(lib, code, bad):
 @pytest.mark.parametrize("bad", [
     dict(S=0), dict(S=18, D=4), dict(V=0), dict(ids=None), dict(id_bytes=16), dict(dx=MIS),
     dict(dtable=None), dict(ws=None), dict(ws=MIS), dict(short=1), dict(dtype=3),
-    dict(scale=float("nan")), dict(dtable=2 * OK), dict(ws=3 * OK)])
+    dict(scale=float("nan")), dict(dtable=2 * OK), dict(ws=3 * OK),
+    dict(dtable=2 * OK + 496), dict(ws=3 * OK + 3184), dict(ws=2 * OK + 496), dict(ws=OK),
+    dict(dtable=OK + 48)])
 def test_embed_bwd_refuses(lib, bad):
     a = dict(ids=OK, id_bytes=4, dx=2 * OK, dtype=0, dtable=3 * OK, S=16, D=4, V=100, d=8, scale=1.0,
              ws=4 * OK, short=0)
@@ -67,7 +72,10 @@ def test_workspace_sizes(lib):
     (INV, dict(scale=float("inf"))), (INV, dict(dtype=2)), (INV, dict(dtype=0, sdt=1)),
     (INV, dict(rstd_f=MIS)), (INV, dict(g_post=None)), (UNS, dict(n=(1 << 24) + 1)),
     (INV, dict(h="f")), (INV, dict(b="f")), (INV, dict(b="x")), (INV, dict(b="h")),
-    (INV, dict(h="x", b="x")), (INV, dict(rstd_f="rstd_h"))])
+    (INV, dict(h="x", b="x")), (INV, dict(rstd_f="rstd_h")), (INV, dict(f="x", h="x")),
+    (INV, dict(b=OK + 48)), (INV, dict(b=OK - 48)), (INV, dict(h=OK + 0x1000 + 16)),
+    (INV, dict(rstd_f=OK + 0x1000 + 112)), (INV, dict(b=OK + 0x3000)),
+    (UNS, dict(rows=1 << 31))])
 def test_norm_residual_fwd_refuses(lib, code, bad):
     names = ("f", "x", "gate", "g_post", "g_pre", "h", "b", "rstd_f", "rstd_h")
     a = {k: OK + 0x1000 * i for i, k in enumerate(names)}
@@ -84,12 +92,14 @@ def test_norm_residual_fwd_refuses(lib, code, bad):
     (INV, dict(ws=None)), (INV, dict(short=1)), (INV, dict(dtype=0, sdt=1)),
     (UNS, dict(n=(1 << 24) + 1)), (INV, dict(df="f")), (INV, dict(dgate="gate")),
     (INV, dict(dx="db")), (INV, dict(df="dx")), (INV, dict(dg_post="g_post")),
-    (INV, dict(dg_post="dg_pre"))])
+    (INV, dict(dg_post="dg_pre")), (INV, dict(dx=OK + 16)), (INV, dict(df=OK + 0x2000 + 48)),
+    (INV, dict(dg_pre=OK + 0x1000 + 112)), (INV, dict(ws=OK + 0x1000)), (INV, dict(ws="dg_pre")),
+    (INV, dict(ws="df")), (UNS, dict(rows=1 << 31))])
 def test_norm_residual_bwd_refuses(lib, code, bad):
     names = ("dh", "db", "f", "gate", "h", "g_post", "g_pre", "rstd_f", "rstd_h", "dx", "df",
              "dgate", "dg_post", "dg_pre")
     a = {k: OK + 0x1000 * i for i, k in enumerate(names)}
-    a.update(rows=4, n=8, scale=1.0, dtype=1, sdt=0, ws=OK, short=0)
+    a.update(rows=4, n=8, scale=1.0, dtype=1, sdt=0, ws=2 * OK, short=0)
     a.update({k: a[v] if isinstance(v, str) else v for k, v in bad.items()})
     nb = lib.tsp_norm_residual_bwd_workspace_bytes(4, 8) - a.pop("short")
     assert lib.tsp_norm_residual_bwd(*a.values(), nb, None) == code
@@ -189,6 +199,21 @@ def test_adamw_object_checks_its_tensors():
         with pytest.raises(ValueError):
             opt.step(grads, lr=1e-3)
     assert opt.t == 0
+    # states that are one another, a weight that is another's master, overlapping copies
+    m, w16 = torch.zeros(335), [torch.zeros(300).bfloat16(), torch.zeros(40).bfloat16()]
+    copies = torch.zeros(400).half()
+    for args, k in ((p, dict(m=[m[:300], m[:35]])), (p, dict(m=[m[:300], m[299:334]])),
+                    (p, dict(m=[m[:300], m[300:]], v=[torch.zeros(300), m[300:]])),
+                    ([p[0], p[0][:100]], {}), (w16, dict(prep=[copies[:300], copies[296:336]]))):
+        with pytest.raises(ValueError, match="share memory"):
+            tsp.AdamW(args, **k)
+    tsp.AdamW(p, m=[m[:300], m[300:]])
+    # it holds addresses: an exchanged state or moved weight does not pass unseen
+    with pytest.raises(TypeError):
+        opt.m[0] = torch.zeros(300)
+    p[0].data = torch.ones(300)
+    with pytest.raises(ValueError, match="memory"):
+        opt.step([torch.zeros(300), torch.zeros(35)], lr=1e-3)
 
 
 def test_prep_views_are_the_prepared_copies(lib):
