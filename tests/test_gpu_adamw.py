@@ -307,3 +307,62 @@ def test_a_weight_past_fp16_is_recorded():
     assert tsp.device_status() == tsp.TSP_ERR_RANGE
     assert prep[0] == 1.0 and torch.equal(w.cpu(), torch.tensor([1.0, 7e4, 2.0, 3.0], dtype=BF))
     assert tsp.device_status() == tsp.TSP_OK
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_element_offsets_past_32_bits(bits):
+    """A tensor of more than 2^31 elements: the same blocks become the same bits,
+    wherever they are."""
+    period, times, rest = 1 << 20, 2050, 5 * 128 + 3
+    gen = torch.Generator("cuda").manual_seed(2)
+    w = (0.02 * torch.randn(period, device="cuda", generator=gen)).to(BF)
+    g = 1e-3 * torch.randn(period, device="cuda", generator=gen)
+
+    def repeated(x):
+        return torch.cat([x.repeat(times), x[:rest]])
+    small = tsp.AdamW([w], weight_decay=0.1, state_bits=bits, master=None, betas=(B1, B2), eps=EPS)
+    big = tsp.AdamW([repeated(w)], weight_decay=0.1, state_bits=bits, master=None, betas=(B1, B2), eps=EPS)
+    grad = repeated(g)
+    for _ in range(2):
+        small.step([g], lr=1e-3)
+        big.step([grad], lr=1e-3)
+    for name in ("params", "m", "v", "m_scale", "v_scale"):
+        a, b = getattr(big, name)[0], getattr(small, name)[0]
+        if a is None:
+            continue
+        if a.dtype == E4:
+            a, b = a.view(torch.uint8), b.view(torch.uint8)
+        k = len(b)
+        assert bool((a[:times * k].view(times, k) == b).all()), name
+        tail = a[times * k:]
+        if "scale" in name:      # the last block is a part of the small tensor's sixth
+            tail = tail[:-1]
+        whole = 5 * 128 if bits == 8 and name in ("m", "v", "params") else len(tail)
+        assert torch.equal(tail[:whole], b[:whole] if "scale" not in name else b[:len(tail)]), name
+    # the block that ends with the tensor has scales of its own, of the elements that are there
+    q = bits == 8
+    if q:
+        assert bool((big.m_scale[0][-1] <= small.m_scale[0][5]) & (big.v_scale[0][-1] > 0))
+
+
+def test_two_objects_at_once():
+    """Steps on two streams, each with its own tensors."""
+    sizes = [100_000, 77, 4096 * 40]
+    ts = [make(sizes, F32, seed=s) for s in (1, 2)]
+
+    def new():
+        return [tsp.AdamW([x["w"].cuda() for x in t], state_bits=8, betas=(B1, B2), eps=EPS) for t in ts]
+    one, two = new(), new()
+    grads = [[x["g"].cuda() for x in t] for t in ts]
+    streams = [torch.cuda.Stream() for _ in ts]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for o, g, s in zip(two, grads, streams):
+            o.step(g, lr=1e-3, stream=s)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for o, g in zip(one, grads):
+            o.step(g, lr=1e-3)
+    for a, b in zip(one, two):
+        assert all(torch.equal(x, y) for x, y in zip(a.params, b.params))
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a.m, b.m))

@@ -292,3 +292,20 @@ def test_side_stream_and_captured_calls():
     for k, (_, x) in enumerate(graphs):
         assert torch.equal(x, tsp.embed_fwd(ids, table))
         assert torch.equal(outs[k], tsp.embed_bwd(ids, dx, V, scale=1.0 + k))
+
+
+def test_position_offsets_past_32_bits():
+    """x_z and dx_z of more than 2^31 elements, in the zigzag order: the sums of ones are
+    counts, exact in fp32."""
+    S, D, V, d = 530000, 8, 9, 4096
+    ids = make_ids("padded", S, V, 3).cuda()
+    table = (torch.arange(V).float()[:, None] + torch.arange(d) / 64).to(BF).cuda()
+    x = tsp.embed_fwd(ids, table, D=D)
+    back = tsp.zigzag_permute(x, D, inverse=True)
+    for v in range(V):
+        assert bool((back[ids == v] == table[v]).all())
+    assert not bool(back[ids < 0].any())
+    del back
+    grad = tsp.embed_bwd(ids, x.fill_(1.0), V, D=D)
+    count = torch.stack([(ids == v).sum() for v in range(V)]).float()
+    assert torch.equal(grad, count[:, None].expand(V, d))

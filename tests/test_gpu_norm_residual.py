@@ -249,3 +249,51 @@ def test_single_row_side_stream_and_capture():
     assert all(torch.equal(x, y) for x, y in zip(want, (h, b, rf, rh)))
     again = tsp.norm_residual_bwd(dh, db, t["f"], h, t["g_post"], t["g_pre"], rf, rh, t["gate"])
     assert all(torch.equal(grads[k], again[k]) for k in grads)
+
+
+def test_element_offsets_past_32_bits():
+    """2^31 elements and more, of ragged rows: rows that hold the same and start at the
+    same element of a unit give the same bits, wherever they are."""
+    n, period, times = 2049, 1024, 1024          # 2.15e9 elements; the period is whole units
+    t = inputs(period, n, BF, BF, True, True, True)
+    gen = torch.Generator("cuda").manual_seed(1)
+    dh, db = (torch.randn(period, n, device="cuda", generator=gen) for _ in range(2))
+    args = (t["g_post"], t["g_pre"])
+    want = tsp.norm_residual_fwd(t["f"], t["x"], *args, t["gate"], 0.5, with_rstd=True)
+    grad = tsp.norm_residual_bwd(dh, db, t["f"], want[0], *args, *want[2:], t["gate"], 0.5)
+
+    def all_equal(big, small):
+        return bool((big.view(times, *small.shape) == small).all())
+    f, gate, h = (t[k].repeat(times, 1) for k in ("f", "gate", "x"))
+    got = tsp.norm_residual_fwd(f, h, *args, gate, 0.5, h=h, with_rstd=True)
+    for a, b in zip(got, want):
+        assert all_equal(a, b)
+    out = tsp.norm_residual_bwd(dh.repeat(times, 1), db.repeat(times, 1), f, h, *args, *got[2:], gate, 0.5)
+    for k in ("dx", "df", "dgate"):
+        assert all_equal(out[k], grad[k])
+    # dg_pre: a CTA (152 of them at least) adds up at most 2^20 / 152 = 6899 rows, then come
+    # the sums of the CTAs' parts, 43 additions deep at most; a term is off by 4 u (the
+    # product, h times its inverse norm): below 7000 u of the terms' magnitudes.
+    hh = want[0].double() * want[3].double()[:, None]
+    terms = db.double() * hh
+    tol = 7000 * U * terms.abs().sum(0) * times
+    assert bool(((out["dg_pre"].double() - terms.sum(0) * times).abs() <= tol).all())
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with what is its own."""
+    ts = [inputs(3000 + i, 1024, BF, F32, True, True, True, seed=i) for i in range(2)]
+    grads = [torch.randn(3000 + i, 1024, generator=torch.Generator().manual_seed(i)).cuda() for i in range(2)]
+
+    def step(t, g, stream=None):
+        h, b, rf, rh = tsp.norm_residual_fwd(t["f"], t["x"], t["g_post"], t["g_pre"], t["gate"],
+                                             with_rstd=True, stream=stream)
+        out = tsp.norm_residual_bwd(g, g, t["f"], h, t["g_post"], t["g_pre"], rf, rh, t["gate"], stream=stream)
+        return [h, b, *out.values()]
+    want = [step(t, g) for t, g in zip(ts, grads)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ts]
+    for _ in range(5):
+        got = [step(t, g, s) for t, g, s in zip(ts, grads, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for x, y in zip(want, got) for a, b in zip(x, y))
