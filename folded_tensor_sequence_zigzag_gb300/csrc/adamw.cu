@@ -154,28 +154,27 @@ __device__ __forceinline__ uint32_t f_to_codes(const float (&v)[4]) {
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
 }
-// the larger of two; a NaN wins
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
+// The bits of the warp's largest magnitude: their order is that of non-negative
+// floats with NaN above infinity, so a NaN is the largest.
+__device__ __forceinline__ unsigned top_of(const float (&x)[4]) {
+  float mine;
+  asm("{\n\t.reg .f32 t;\n\t"
+      "max.NaN.abs.f32 t, %1, %2, %3;\n\t"
+      "max.NaN.f32 %0, t, %4;\n\t}"
+      : "=f"(mine)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(fabsf(x[3])));
+  return __reduce_max_sync(0xffffffffu, __float_as_uint(mine));
 }
-// The warp's 128 values as codes and a scale (written by lane 0).  The warp's
-// largest magnitude is found on the bits, whose order is that of non-negative
-// floats with NaN above infinity: one instruction, and a NaN reaches the scale.
+// Four values as codes of a block whose 448 / (largest magnitude) is inv.  ROOT: a
+// positive one takes at least the smallest code, 2^-9.  (It is 2^-75 or more, so no
+// block that is held as zeros has one.)
 template <bool ROOT>
-__device__ __forceinline__ uint32_t quantise(const float (&x)[4], float* scale, int lane) {
-  const float mine = max_nan(max_nan(fabsf(x[0]), fabsf(x[1])), max_nan(fabsf(x[2]), fabsf(x[3])));
-  const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mine)));
-  const bool live = !(top < kScaleFloor);
-  const float inv = live ? __fmul_rn(448.f, __frcp_rn(top)) : 0.f;
-  if (lane == 0) *scale = live ? __fmul_rn(top, 1.f / 448.f) : 0.f;
-  const float least = live ? 0.001953125f : 0.f;   // 2^-9: what would round to 0 or to it
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[4], float inv) {
   float q[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     q[e] = __fmul_rn(x[e], inv);
-    if (ROOT && x[e] > 0.f) q[e] = fmaxf(q[e], least);
+    if (ROOT && x[e] > 0.f) q[e] = fmaxf(q[e], 0.001953125f);
   }
   return f_to_codes(q);
 }
@@ -254,8 +253,14 @@ __device__ __forceinline__ bool finish(const Args& a, const Place<T>& to, int o,
       for (int e = 0; e < 4; ++e)
         if (e >= k) m[e] = root[e] = 0.f;
     }
-    store_codes<ALL>(to.mq + o * 128, k, quantise<false>(m, to.ms + o, lane));
-    store_codes<ALL>(to.vq + o * 128, k, quantise<true>(root, to.vs + o, lane));
+    // the two scales at once: even lanes for m, odd ones for the root
+    const unsigned top_m = top_of(m), top_v = top_of(root);
+    const float top = __uint_as_float(lane & 1 ? top_v : top_m);
+    const bool live = !(top < kScaleFloor);
+    const float inv = live ? __fmul_rn(448.f, __frcp_rn(top)) : 0.f;
+    if (lane < 2) (lane ? to.vs : to.ms)[o] = live ? __fmul_rn(top, 1.f / 448.f) : 0.f;
+    store_codes<ALL>(to.mq + o * 128, k, codes_of<false>(m, __shfl_sync(0xffffffffu, inv, 0)));
+    store_codes<ALL>(to.vq + o * 128, k, codes_of<true>(root, __shfl_sync(0xffffffffu, inv, 1)));
   }
   bool bad = false;
   if (to.master) store4<ALL>(to.master + o * 128, k, p);
@@ -408,18 +413,35 @@ __global__ void __launch_bounds__(256, CTAS) adamw_coded_kernel(const __grid_con
   int64_t next_first = 0;
   bool whole = false;
   float scale = 0.f;
-  const float* from_g = nullptr;
+  const float *from_g = nullptr, *from_s = nullptr;
   const uint8_t *from_p = nullptr, *from_m = nullptr, *from_v = nullptr;
   bool wide = true;   // p is fp32
+  // Long runs stay in a tensor for many chunks: the search is for its first alone (a
+  // bf16 block without masters, 202 M elements: 448 us, 482 with a search a chunk).
+  int64_t end_next = 0;
   auto look = [&](int64_t ch) {
     whole = false;
     if (ch >= chunks) return;
+    if (CTAS == 2 && ch < end_next) {
+      next_first += kChunk;
+      whole = next_first + 512 <= a.t[next].n;
+      if (!whole) return;
+      from_s += kChunk / 128;
+      if (lane < 8) scale = *from_s;
+      from_g += kChunk;
+      from_p += wide ? kChunk * 4 : kChunk * 2;
+      from_m += kChunk;
+      from_v += kChunk;
+      return;
+    }
     next = find(a, ch, warp, &next_first);
     const Tensor& t = a.t[next];
+    if (CTAS == 2) end_next = a.end[next];
     whole = next_first + 512 <= t.n;
     if (!whole) return;
     const int64_t at = next_first + lane * 4;
-    if (lane < 8) scale = (lane < 4 ? t.ms : t.vs)[(next_first >> 7) + (lane & 3)];
+    from_s = (lane < 4 ? t.ms : t.vs) + (next_first >> 7) + (lane & 3);
+    if (lane < 8) scale = *from_s;
     wide = sizeof(T) == 4 || t.master;
     from_g = t.g + at;
     from_p = t.master ? (const uint8_t*)(t.master + at) : (const uint8_t*)((T*)t.w + at);
