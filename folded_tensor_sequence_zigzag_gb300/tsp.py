@@ -7,6 +7,7 @@ no fallback: if the library is missing or no GPU is present the calls raise.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from dataclasses import dataclass
 
@@ -790,6 +791,7 @@ def norm_residual_bwd(dh, db, f, h, g_post=None, g_pre=None, rstd_f=None, rstd_h
 
 
 ADAMW_BLOCK = 128   # TSP_ADAMW_BLOCK
+_dtype = operator.attrgetter("dtype")
 
 
 def prep_views(cfg: Cfg, prep) -> list:
@@ -894,13 +896,13 @@ class AdamW:
         grads = list(grads)
         if list(map(tensor.numel, grads)) != self._sizes or \
                 not all(map(tensor.is_contiguous, grads)) or \
-                any([g.dtype is not f32 for g in grads]) or \
-                any([i != index for i in map(tensor.get_device, grads)]):
+                set(map(_dtype, grads)) != {f32} or \
+                set(map(tensor.get_device, grads)) != {index}:
             raise ValueError(f"gradients: {len(self._sizes)} contiguous fp32 tensors of the sizes "
                              "and on the device of the tensors they are for")
         if list(map(tensor.data_ptr, self.params)) != self._at:
             raise ValueError("a tensor's memory is not the one this object was made for")
-        self._g[:] = list(map(tensor.data_ptr, grads))
+        self._g[:] = np.fromiter(map(tensor.data_ptr, grads), np.uint64, len(grads))
         hy = AdamwHyper(0.0, self.betas[0], self.betas[1], self.eps, 1)
         if isinstance(lr, torch.Tensor):
             hy.lr_dev = _arg("lr", lr.view(-1), (1,), f32, index)
