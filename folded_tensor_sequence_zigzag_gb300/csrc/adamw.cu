@@ -531,15 +531,21 @@ tsp_status launch_adamw(const tsp_adamw_tensor* ts, int count, const tsp_adamw_h
     if (a.count == 0) break;
     Prof prof("adamw", st);
     if (state_bits == 8) {
-      // Runs of up to 8 chunks to copy ahead in, while there are eight of them for
-      // every resident CTA; in order, so that what is written at a time lies together
-      // (a 7B-shaped block: 602 us, with resident CTAs walking all chunks 738).  Long
-      // runs take two CTAs a multiprocessor and no spills (602 us against 631 with
-      // three), single chunks three (10.4 M elements: 36 us against 43 with two).
-      a.run = (int)std::max<int64_t>(1, std::min<int64_t>(8, chunks / ((int64_t)num_sms() * 24)));
+      // Runs of several chunks to copy ahead in, in order, so that what is written at a
+      // time lies together (a 7B-shaped block: 591 us, with resident CTAs walking all
+      // chunks 738).  With masters (20 bytes an element) memory is the bound: runs of 4
+      // (8: 600 us), shorter ones where that leaves less than three for every resident
+      // CTA (12.8 M elements: 46 us in twos, 50 in single chunks).  Without (12 to 16
+      // bytes) the warps' instructions are: runs of 8 (180 M bf16 elements: 404 us, 424
+      // with 4), six for every resident CTA (10.4 M: 35 us, 40 with three).  Runs take two CTAs a multiprocessor and no spills (a
+      // 7B-shaped block: 602 us against 631 with three), single chunks three (10.4 M
+      // elements: 36 us against 43 with two).
+      const bool masters = a.t[0].master != nullptr;
+      a.run = (int)std::max<int64_t>(
+          1, std::min<int64_t>(masters ? 4 : 8, chunks / ((int64_t)num_sms() * (masters ? 6 : 12))));
       const unsigned grid = (unsigned)((chunks + a.run - 1) / a.run);
       const bool bf = dtype == TSP_BF16;
-      if (a.run >= 4) {
+      if (a.run >= 2) {
         if (bf) adamw_coded_kernel<__nv_bfloat16, 2><<<grid, 256, kAheadSmem, st>>>(a);
         else adamw_coded_kernel<float, 2><<<grid, 256, kAheadSmem, st>>>(a);
       } else {

@@ -163,8 +163,8 @@ def test_codes_are_within_half_a_step():
 
 @pytest.mark.parametrize("dt,total", [(BF, 66_000_000), (F32, 31_000_000)])
 def test_long_runs_of_chunks(dt, total):
-    """Tensors large enough that a CTA takes several chunks in a row (4 and 2 of
-    them), ragged and empty ones between: chunk ends inside tensors, runs that
+    """Tensors large enough that a CTA takes several chunks in a row (4 of them),
+    ragged and empty ones between: chunk ends inside tensors, runs that
     cross from one to the next, on the GPU against elementary operations there."""
     sizes = [total // 2 + 77, 0, 5, 4096 * 3 + 1, total // 4 + 2, 129, 4096, total // 4]
     gen = torch.Generator("cuda").manual_seed(3)
