@@ -173,8 +173,10 @@ __device__ __forceinline__ int token_of(const SortArgs& a, int p, bool* past) {
 
 // Up to kRankMax positions: the place of each is the number of positions with a
 // smaller (token, position), both in one 32-bit word.  A CTA takes 32 positions, a
-// warp of it a sixteenth of the comparisons (8192 positions: 64 M of them, 5 us).
-constexpr int kRankMax = 8192;
+// warp of it a sixteenth of the comparisons.  As long as there is a multiprocessor for
+// every CTA this is quicker than two passes of the sort below (64 columns added up,
+// 32000 tokens: 14.5 us at 4800 positions, 17.7 sorted; 17.9 and 17.5 at 5200).
+constexpr int kRankMax = 152 * 32;
 
 __global__ void __launch_bounds__(kSortThreads) embed_rank_kernel(const __grid_constant__ SortArgs a,
                                                                   int pos_bits) {

@@ -110,7 +110,7 @@ def bwd_tol(a, n, scale):
 
 BWD = [(1, 1, 5, 1), (1, 1, 40, 64), (7, 1, 40, 4096), (31, 1, 9, 33), (64, 4, 700, 256),
        (96, 3, 50, 1000), (514, 1, 20, 257), (1000, 1, 100000, 12), (4096, 8, 1000, 512),
-       (4098, 1, 77, 130), (20000, 2, 513, 68), (33000, 1, 262145, 4), (70000, 1, 512, 36)]
+       (4098, 1, 77, 130), (4864, 4, 3000, 40), (4865, 1, 3000, 40), (20000, 2, 513, 68), (33000, 1, 262145, 4), (70000, 1, 512, 36)]
 
 
 @pytest.mark.parametrize("S,D,V,d", BWD)
