@@ -22,6 +22,7 @@
 // Bound by HBM: every element is read and written once.
 #include <cuda_fp8.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -58,8 +59,43 @@ struct Args {
   const float* lr_dev;
   const int64_t* step_dev;
   const float* gscale;
+  const int* held;   // the status word as the call found it
   int* status;
 };
+
+// While the status word holds an error the contraction kernels leave their outputs as
+// they are, gradients among them, so an update made of those must not reach weights and
+// states.  All CTAs of all of a call's launches have to decide alike, though an error
+// may be recorded while they run (by this call too: a weight past fp16), or half of the
+// tensors would be updated.  So the word is copied once, where the stream reaches the
+// call, and the kernels look at the copy.  A call's place among the copies comes round
+// again after kHeldPlaces calls, and captured calls, which keep theirs, have a set of
+// their own.  (The first kernel follows this one as a dependent launch: 1.4 us of the
+// host's time, 1 us in a graph; a copy of four bytes by the driver costs 4 us.)
+constexpr unsigned kHeldPlaces = 32768;
+__device__ int g_held[2][kHeldPlaces];
+
+__global__ void adamw_held_kernel(int* held, const int* status) { *held = *status; }
+
+tsp_status take_held(const int* status, cudaStream_t st, const int** held) {
+  if (!status) return TSP_ERR_CUDA;
+  static int* base[kMaxDevices] = {nullptr};
+  static std::atomic<unsigned> calls[2];
+  const int dev = current_device();
+  if (!base[dev]) {
+    void* p = nullptr;
+    TSP_CUDA_TRY(cudaGetSymbolAddress(&p, g_held));
+    base[dev] = (int*)p;
+  }
+  cudaStreamCaptureStatus capturing;
+  TSP_CUDA_TRY(cudaStreamIsCapturing(st, &capturing));
+  const int set = capturing != cudaStreamCaptureStatusNone;
+  int* at = base[dev] + set * kHeldPlaces + calls[set].fetch_add(1) % kHeldPlaces;
+  adamw_held_kernel<<<1, 1, 0, st>>>(at, status);
+  TSP_CUDA_TRY(cudaGetLastError());
+  *held = at;
+  return TSP_OK;
+}
 
 // x^n by squaring, n >= 1
 __device__ double power(double x, int64_t n) {
@@ -281,12 +317,13 @@ __device__ __forceinline__ bool finish(const Args& a, const Place<T>& to, int o,
 }
 
 // One warp's 512 elements of a tensor from `first` on, in groups of 128, kBatch
-// groups' loads ahead of their use.  ALL: none is past the end.
+// groups' loads ahead of their use.  ALL: none is past the end.  held: an error holds
+// the update back; it is loaded next to the elements, not waited for before them.
 constexpr int kGroups = 4, kBatch = 2;
 
 template <typename T, int BITS, bool ALL>
 __device__ __forceinline__ bool update(const Args& a, const Tensor& t, int64_t first, int lane,
-                                       const Step& s) {
+                                       const Step& s, int held) {
   const float keep = __fsub_rn(1.f, __fmul_rn(s.lr, t.wd));
   const int64_t at = first + lane * 4;
   const float* gp = t.g + at;
@@ -315,6 +352,7 @@ __device__ __forceinline__ bool update(const Args& a, const Tensor& t, int64_t f
       }
     }
     __syncwarp();   // every lane has read the old scales
+    if (held) return false;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int o = u0 + u;
@@ -365,14 +403,16 @@ __device__ __forceinline__ Step step_of(const Args& a) {
 template <typename T>
 __global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ Args a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  after_previous_kernel();
+  const int held = *a.held;
   const Step s = step_of(a);
   bool bad = false;
   const int64_t chunks = a.end[a.count - 1];
   for (int64_t ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
     int64_t first;
     const Tensor& t = a.t[find(a, ch, warp, &first)];
-    bad |= first + 512 <= t.n ? update<T, 32, true>(a, t, first, lane, s)
-                              : update<T, 32, false>(a, t, first, lane, s);
+    bad |= first + 512 <= t.n ? update<T, 32, true>(a, t, first, lane, s, held)
+                              : update<T, 32, false>(a, t, first, lane, s, held);
   }
   if (bad) report_status(a.status, (int)TSP_ERR_RANGE);
 }
@@ -404,6 +444,8 @@ __global__ void __launch_bounds__(256, CTAS) adamw_coded_kernel(const __grid_con
   Ahead& in = reinterpret_cast<Ahead*>(smem)[warp];
   float *const in_g = in.g[0] + lane * 4, *const in_p = in.p[0] + lane * 4;
   uint32_t *const in_m = in.m[0] + lane, *const in_v = in.v[0] + lane;
+  after_previous_kernel();
+  const int held = *a.held;
   const Step s = step_of(a);
   bool bad = false;
   const int64_t begin = (int64_t)blockIdx.x * a.run, chunks = min(a.end[a.count - 1], begin + a.run);
@@ -461,6 +503,10 @@ __global__ void __launch_bounds__(256, CTAS) adamw_coded_kernel(const __grid_con
   look(begin);
 #pragma unroll
   for (int u = 0; u < kGroups; ++u) issue(u);
+  if (held) {   // (what is on its way has to arrive before the shared memory goes)
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
   for (int64_t ch = begin; ch < chunks; ++ch) {
     const Tensor& t = a.t[next];
     const int64_t first = next_first;
@@ -468,7 +514,7 @@ __global__ void __launch_bounds__(256, CTAS) adamw_coded_kernel(const __grid_con
     const float old = scale;
     look(ch + 1);
     if (!ahead) {
-      bad |= update<T, 8, false>(a, t, first, lane, s);
+      bad |= update<T, 8, false>(a, t, first, lane, s, 0);
 #pragma unroll
       for (int u = 0; u < kGroups; ++u) issue(u);
       continue;
@@ -493,6 +539,25 @@ __global__ void __launch_bounds__(256, CTAS) adamw_coded_kernel(const __grid_con
   if (bad) report_status(a.status, (int)TSP_ERR_RANGE);
 }
 
+// A launch of 256 threads a CTA; dependent: behind adamw_held_kernel (see launch_after,
+// which would copy the arguments' 11 KB).
+tsp_status launch(void (*kernel)(Args), unsigned grid, size_t smem, bool dependent, cudaStream_t st,
+                  Args& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = dependent ? 1 : 0;
+  void* args[] = {&a};
+  TSP_CUDA_TRY(cudaLaunchKernelExC(&cfg, (const void*)kernel, args));
+  return TSP_OK;
+}
+
 }  // namespace
 
 tsp_status launch_adamw(const tsp_adamw_tensor* ts, int count, const tsp_adamw_hyper* h,
@@ -511,6 +576,7 @@ tsp_status launch_adamw(const tsp_adamw_tensor* ts, int count, const tsp_adamw_h
   a.step_dev = h->step_dev;
   a.gscale = h->gscale_dev;
   a.status = status_word();
+  a.held = nullptr;
   a.step_size = a.fix = 0.f;
   if (!h->step_dev) {
     a.step_size = (float)((h->lr_dev ? 1.0 : h->lr) / (1.0 - std::pow(h->beta1, (double)h->step)));
@@ -529,6 +595,10 @@ tsp_status launch_adamw(const tsp_adamw_tensor* ts, int count, const tsp_adamw_h
       a.end[a.count++] = chunks;
     }
     if (a.count == 0) break;
+    const bool first = !a.held;
+    tsp_status r = TSP_OK;
+    if (first) r = take_held(a.status, st, &a.held);   // (all of the call's launches use it)
+    if (r != TSP_OK) return r;
     Prof prof("adamw", st);
     if (state_bits == 8) {
       // Runs of several chunks to copy ahead in, in order, so that what is written at a
@@ -545,19 +615,18 @@ tsp_status launch_adamw(const tsp_adamw_tensor* ts, int count, const tsp_adamw_h
           1, std::min<int64_t>(masters ? 4 : 8, chunks / ((int64_t)num_sms() * (masters ? 6 : 12))));
       const unsigned grid = (unsigned)((chunks + a.run - 1) / a.run);
       const bool bf = dtype == TSP_BF16;
-      if (a.run >= 2) {
-        if (bf) adamw_coded_kernel<__nv_bfloat16, 2><<<grid, 256, kAheadSmem, st>>>(a);
-        else adamw_coded_kernel<float, 2><<<grid, 256, kAheadSmem, st>>>(a);
-      } else {
-        if (bf) adamw_coded_kernel<__nv_bfloat16, 3><<<grid, 256, kAheadSmem, st>>>(a);
-        else adamw_coded_kernel<float, 3><<<grid, 256, kAheadSmem, st>>>(a);
-      }
+      if (a.run >= 2)
+        r = launch(bf ? adamw_coded_kernel<__nv_bfloat16, 2> : adamw_coded_kernel<float, 2>, grid,
+                   kAheadSmem, first, st, a);
+      else
+        r = launch(bf ? adamw_coded_kernel<__nv_bfloat16, 3> : adamw_coded_kernel<float, 3>, grid,
+                   kAheadSmem, first, st, a);
     } else {
-      const int grid = (int)std::min<int64_t>(chunks, (int64_t)num_sms() * 256);
-      if (dtype == TSP_BF16) adamw_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
-      else adamw_kernel<float><<<grid, 256, 0, st>>>(a);
+      const unsigned grid = (unsigned)std::min<int64_t>(chunks, (int64_t)num_sms() * 256);
+      r = launch(dtype == TSP_BF16 ? adamw_kernel<__nv_bfloat16> : adamw_kernel<float>, grid, 0, first,
+                 st, a);
     }
-    TSP_CUDA_TRY(cudaGetLastError());
+    if (r != TSP_OK) return r;
   }
   return TSP_OK;
 }

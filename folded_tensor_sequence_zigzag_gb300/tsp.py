@@ -891,7 +891,12 @@ class AdamW:
         update's number (1 first; default: counted by this object), or a
         one-element int64 GPU tensor; ``gscale``: a one-element fp32 GPU tensor
         that the gradients are multiplied by.  Tensors are read when the kernel
-        runs, so a captured step can be replayed with new values in them."""
+        runs, so a captured step can be replayed with new values in them.
+
+        While the device status word holds an error (a token id past its table, a
+        value past fp16), the step changes nothing on the GPU; ``t``, which counts
+        here, is then ahead by the steps held back, for whoever finds the error
+        (device_status) to set."""
         f32, tensor, index = torch.float32, torch.Tensor, self.params[0].get_device()
         grads = list(grads)
         if list(map(tensor.numel, grads)) != self._sizes or \

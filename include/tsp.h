@@ -62,7 +62,8 @@
  *    skips an access that fails, recording TSP_ERR_BOUNDS; the normal build
  *    carries none of these tests.
  *    While the word holds an error, the tensor-core kernels return without
- *    doing their work, until tsp_device_status(stream, 1) clears it.
+ *    doing their work and tsp_adamw_step updates nothing, until
+ *    tsp_device_status(stream, 1) clears it.
  *  - All pointers must be 16-byte aligned; row strides are dense.
  */
 #ifndef TSP_H_
@@ -607,6 +608,13 @@ tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f
  *   computed on the device).  A captured call keeps the host values it was
  *   captured with; a graph that is replayed over many steps passes step_dev and
  *   advances it.
+ * If the status word holds an error when the stream reaches the call, the
+ *   gradients may be what a kernel that returned without its work left of
+ *   them: weights, masters, states and copies stay as they are, all of them
+ *   (replays of a captured call look at the word anew).  An error recorded
+ *   later, by this call too (a weight fp16 cannot hold), holds back the next
+ *   call, not a part of this one.  The caller's step number is its own: an
+ *   update held back was none, and its number is for the next one.
  * One launch per 128 tensors.  Errors: TSP_ERR_INVALID_ARG (also for two
  *   tensors whose weights overlap: one call may update a weight once). */
 #define TSP_ADAMW_BLOCK 128
@@ -650,7 +658,8 @@ int32_t tsp_num_sms(void);
  * "label<TAB>kernels<TAB>total_ms<NL>", into buf (host memory, `bytes` long,
  * NUL-terminated); returns the number of lines, or -1 if buf is too small or
  * an event failed.  tsp_launch_count: kernels launched by the library since
- * it was loaded. */
+ * it was loaded (without the one thread in front of tsp_adamw_step's that
+ * copies the status word). */
 void tsp_profile_enable(int32_t on);
 int32_t tsp_profile_report(char* buf, int64_t bytes);
 int64_t tsp_launch_count(void);
