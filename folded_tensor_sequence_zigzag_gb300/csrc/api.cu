@@ -19,6 +19,7 @@
 #include <cstring>
 #include <exception>
 #include <initializer_list>
+#include <iterator>
 #include <map>
 #include <mutex>
 #include <string>
@@ -1038,6 +1039,97 @@ static bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> 
   return true;
 }
 
+// Memory of tsp_adamw_step; `read`: it is not written.
+struct Array {
+  uintptr_t at, end;
+  bool read;
+};
+// True if none that is written meets another one.  Sorted by address: v is runs that
+// ascend, few of them (arrays of one kind mostly lie in order); those are put in the
+// order of their starts and, where they still interleave, merged.
+static bool arrays_apart(std::vector<Array>& v) {
+  auto before = [](const Array& a, const Array& b) { return a.at < b.at; };
+  std::vector<size_t> starts;   // of the runs, and the end
+  auto find_runs = [&] {
+    starts.clear();
+    for (size_t i = 0; i < v.size(); ++i)
+      if (i == 0 || before(v[i], v[i - 1])) starts.push_back(i);
+    starts.push_back(v.size());
+  };
+  std::vector<Array> w;
+  w.reserve(v.size());
+  find_runs();
+  if (starts.size() > 2) {
+    std::vector<std::pair<uintptr_t, size_t>> order;
+    for (size_t r = 0; r + 1 < starts.size(); ++r) order.emplace_back(v[starts[r]].at, r);
+    std::sort(order.begin(), order.end());
+    for (const auto& o : order)
+      w.insert(w.end(), v.begin() + starts[o.second], v.begin() + starts[o.second + 1]);
+    v.swap(w);
+    find_runs();
+  }
+  while (starts.size() > 2) {   // halves the runs
+    w.clear();
+    for (size_t r = 0; r + 1 < starts.size(); r += 2) {
+      const auto a = v.begin() + starts[r], b = v.begin() + starts[r + 1];
+      const auto c = r + 2 < starts.size() ? v.begin() + starts[r + 2] : b;
+      std::merge(a, b, b, c, std::back_inserter(w), before);
+    }
+    v.swap(w);
+    find_runs();
+  }
+  uintptr_t written = 0, any = 0;   // the furthest ends so far
+  for (const Array& a : v) {
+    if (a.at < (a.read ? written : any)) return false;
+    any = std::max(any, a.end);
+    if (!a.read) written = std::max(written, a.end);
+  }
+  return true;
+}
+
+// True if no array that an update writes meets another one or a value read from the
+// device.  e, se: bytes of an element of w and of a state.
+static bool adamw_apart(const tsp_adamw_tensor* ts, int32_t count, const tsp_adamw_hyper* h, int64_t e,
+                        int64_t se) {
+  constexpr int kKinds = 8;
+  std::vector<Array> every((size_t)kKinds * count + 3), few;
+  few.reserve(kKinds + 3);
+  // Mostly each kind lies in order in memory of its own, and the kinds' ranges are all
+  // there is to compare (109 tensors: 1 us, the sorted list of every array 7).
+  bool in_order = true;
+  Array range[kKinds] = {};
+  for (int32_t i = 0; i < count; ++i) {
+    const tsp_adamw_tensor& t = ts[i];
+    if (t.n == 0) continue;
+    const int64_t scales = (t.n + TSP_ADAMW_BLOCK - 1) / TSP_ADAMW_BLOCK * 4;
+    const void* p[kKinds] = {t.w, t.m, t.v, t.m_scale, t.v_scale, t.master, t.prep, t.g};
+    const int64_t bytes[kKinds] = {t.n * e, t.n * se, t.n * se, scales, scales, t.n * 4, t.n * 2, t.n * 4};
+    for (int k = 0; k < kKinds; ++k) {
+      if (!p[k]) continue;
+      const Array a = {(uintptr_t)p[k], (uintptr_t)p[k] + (uintptr_t)bytes[k], k == kKinds - 1};
+      every[(size_t)k * count + i] = a;
+      Array& r = range[k];
+      if (!r.at) r = a;
+      else in_order &= a.read || a.at >= r.end;
+      r.at = std::min(r.at, a.at);
+      r.end = std::max(r.end, a.end);
+    }
+  }
+  const std::pair<const void*, int> values[3] = {{h->lr_dev, 4}, {h->step_dev, 8}, {h->gscale_dev, 4}};
+  for (int k = 0; k < 3; ++k)
+    if (values[k].first)
+      every[(size_t)kKinds * count + k] = {(uintptr_t)values[k].first,
+                                           (uintptr_t)values[k].first + values[k].second, true};
+  auto none = [](const Array& a) { return a.at == 0; };
+  if (in_order) {
+    std::remove_copy_if(range, range + kKinds, std::back_inserter(few), none);
+    std::remove_copy_if(every.end() - 3, every.end(), std::back_inserter(few), none);
+    if (arrays_apart(few)) return true;
+  }
+  every.erase(std::remove_if(every.begin(), every.end(), none), every.end());
+  return arrays_apart(every);
+}
+
 static bool ids_ok(const void* ids, int32_t id_bytes) {
   return ids && (id_bytes == 4 || id_bytes == 8) && (uintptr_t)ids % (uintptr_t)id_bytes == 0;
 }
@@ -1162,17 +1254,8 @@ tsp_status tsp_adamw_step(const tsp_adamw_tensor* tensors, int32_t count,
         (uintptr_t)t.m_scale % 4 || (uintptr_t)t.v_scale % 4 || !std::isfinite(t.weight_decay))
       return TSP_ERR_INVALID_ARG;
   }
-  // one call updates a weight once: sorted by address, no weight reaches the next
   try {
-    std::vector<std::pair<uintptr_t, uintptr_t>> span;
-    span.reserve(count);
-    for (int32_t i = 0; i < count; ++i)
-      if (tensors[i].n > 0)
-        span.emplace_back((uintptr_t)tensors[i].w,
-                          (uintptr_t)tensors[i].w + (uintptr_t)(tensors[i].n * e));
-    std::sort(span.begin(), span.end());
-    for (size_t i = 1; i < span.size(); ++i)
-      if (span[i].first < span[i - 1].second) return TSP_ERR_INVALID_ARG;
+    if (!adamw_apart(tensors, count, hyper, e, coded ? 1 : 4)) return TSP_ERR_INVALID_ARG;
   } catch (const std::exception&) {   // no host memory for the list: nothing was launched
     return TSP_ERR_INVALID_ARG;
   }

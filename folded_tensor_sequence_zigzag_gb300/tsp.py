@@ -791,7 +791,20 @@ def norm_residual_bwd(dh, db, f, h, g_post=None, g_pre=None, rstd_f=None, rstd_h
 
 
 ADAMW_BLOCK = 128   # TSP_ADAMW_BLOCK
-_dtype = operator.attrgetter("dtype")
+_dtype, _shape = operator.attrgetter("dtype"), operator.attrgetter("shape")
+
+
+def _fits(x, shape):
+    """x has this shape, or is flat and has as many elements."""
+    return x.shape == shape or x.dim() == 1 and x.numel() == shape.numel()
+
+
+def _value(name, t, dtype, index):
+    """data_ptr of a tensor of one element."""
+    if t.dtype is not dtype or t.numel() != 1 or t.get_device() != index:
+        raise ValueError(f"{name}: expected one {dtype} on the device of the tensors, got {t.dtype} of "
+                         f"shape {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def prep_views(cfg: Cfg, prep) -> list:
@@ -815,7 +828,8 @@ class AdamW:
     from them), None updates the tensors themselves, a list gives the masters.
     ``m``, ``v``, ``m_scale``, ``v_scale``: lists of existing states to go on
     with (default: zeros).  ``prep``: for each tensor the fp16 operand copy to
-    refresh (prep_views) or None.  All of them are updated in place and stay
+    refresh (prep_views) or None.  Each has its tensor's shape or is flat (the
+    scales: one per block).  All of them are updated in place and stay
     where they are: new values (a checkpoint's) are copied into them.
     """
 
@@ -863,8 +877,8 @@ class AdamW:
             for name, x, dtype in (("m", self.m[i], code), ("v", self.v[i], code),
                                    ("master", self.master[i], f32),
                                    ("prep", self.prep[i], torch.float16)):
-                if x is not None and x.numel() != p.numel():
-                    raise ValueError(f"{name}[{i}] has {x.numel()} elements, its tensor {p.numel()}")
+                if x is not None and not _fits(x, p.shape):
+                    raise ValueError(f"{name}[{i}] is {tuple(x.shape)}, its tensor {tuple(p.shape)}")
                 setattr(t, name, _arg(f"{name}[{i}]", x, None if x is None else x.shape, dtype, index))
             t.m_scale = _arg(f"m_scale[{i}]", self.m_scale[i], blocks[i], f32, index)
             t.v_scale = _arg(f"v_scale[{i}]", self.v_scale[i], blocks[i], f32, index)
@@ -880,13 +894,16 @@ class AdamW:
         for name in ("params", "m", "v", "m_scale", "v_scale", "master", "prep"):
             setattr(self, name, tuple(getattr(self, name)))
         self._at = [p.data_ptr() for p in self.params]
-        self._sizes = [p.numel() for p in self.params]
+        self._shapes = shapes
+        # of flat tensors the sizes are enough, and are quicker to look at
+        self._sizes = [p.numel() for p in self.params] if all(p.dim() == 1 for p in self.params) else None
         # the gradients' addresses in the array, set by every step
         words = ctypes.sizeof(AdamwTensor) // 8
         self._g = np.frombuffer(self._arr, np.uint64).reshape(n_t, words)[:, AdamwTensor.g.offset // 8]
 
     def step(self, grads, lr, step=None, gscale=None, stream=None):
-        """One update from the fp32 ``grads`` (one for each tensor, same sizes).
+        """One update from the fp32 ``grads`` (one for each tensor: of its shape, or one of
+        the two flat).
         ``lr``: a number, or a one-element fp32 GPU tensor; ``step``: the
         update's number (1 first; default: counted by this object), or a
         one-element int64 GPU tensor; ``gscale``: a one-element fp32 GPU tensor
@@ -899,26 +916,32 @@ class AdamW:
         (device_status) to set."""
         f32, tensor, index = torch.float32, torch.Tensor, self.params[0].get_device()
         grads = list(grads)
-        if list(map(tensor.numel, grads)) != self._sizes or \
+        if self._sizes is not None:
+            fit = list(map(tensor.numel, grads)) == self._sizes
+        else:
+            shapes = list(map(_shape, grads))
+            fit = shapes == self._shapes or (len(shapes) == len(self._shapes) and
+                                             all(map(_fits, grads, self._shapes)))
+        if not fit or \
                 not all(map(tensor.is_contiguous, grads)) or \
                 set(map(_dtype, grads)) != {f32} or \
                 set(map(tensor.get_device, grads)) != {index}:
-            raise ValueError(f"gradients: {len(self._sizes)} contiguous fp32 tensors of the sizes "
-                             "and on the device of the tensors they are for")
+            raise ValueError(f"gradients: {len(self._shapes)} contiguous fp32 tensors of the shapes "
+                             "(or flat) and on the device of the tensors they are for")
         if list(map(tensor.data_ptr, self.params)) != self._at:
             raise ValueError("a tensor's memory is not the one this object was made for")
         self._g[:] = np.fromiter(map(tensor.data_ptr, grads), np.uint64, len(grads))
         hy = AdamwHyper(0.0, self.betas[0], self.betas[1], self.eps, 1)
         if isinstance(lr, torch.Tensor):
-            hy.lr_dev = _arg("lr", lr.view(-1), (1,), f32, index)
+            hy.lr_dev = _value("lr", lr, f32, index)
         else:
             hy.lr = lr
         if isinstance(step, torch.Tensor):
-            hy.step_dev = _arg("step", step.view(-1), (1,), torch.int64, index)
+            hy.step_dev = _value("step", step, torch.int64, index)
         else:
             hy.step = self.t + 1 if step is None else step
         if gscale is not None:
-            hy.gscale_dev = _arg("gscale", gscale.view(-1), (1,), f32, index)
+            hy.gscale_dev = _value("gscale", gscale, f32, index)
         with _On(index, stream) as st:
             _check(load().tsp_adamw_step(self._arr, len(self._arr), ctypes.byref(hy), self.state_bits,
                                          self.dtype, st), "tsp_adamw_step")

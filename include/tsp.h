@@ -600,7 +600,8 @@ tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f
  *   prep     [n] fp16 or NULL (TSP_BF16 only): receives the new weight as the
  *            operand copy tsp_block_weights_prepare would make of it (a weight
  *            fp16 cannot hold records TSP_ERR_RANGE)
- * No two of a call's arrays may share memory (gradients among themselves may).
+ * No array that is written may share memory with another of the call's arrays
+ * or with a value that is read from the device (what is only read may).
  * tsp_adamw_hyper: lr, beta1, beta2 in [0, 1), eps >= 0, step t >= 1 (the first
  *   update is 1; behind step_dev it is not checked).  lr_dev, step_dev,
  *   gscale_dev (nullable DEVICE pointers to one value, read when the kernel
@@ -615,8 +616,8 @@ tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f
  *   later, by this call too (a weight fp16 cannot hold), holds back the next
  *   call, not a part of this one.  The caller's step number is its own: an
  *   update held back was none, and its number is for the next one.
- * One launch per 128 tensors.  Errors: TSP_ERR_INVALID_ARG (also for two
- *   tensors whose weights overlap: one call may update a weight once). */
+ * One launch per 128 tensors.  Errors: TSP_ERR_INVALID_ARG (also for arrays
+ *   that overlap). */
 #define TSP_ADAMW_BLOCK 128
 typedef struct {
   int64_t n;
