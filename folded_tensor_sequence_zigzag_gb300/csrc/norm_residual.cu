@@ -15,6 +15,7 @@
 // is what tsp_rmsnorm_fwd gives for the h the caller sees, and the backward,
 // which reads that h, differentiates the same function.
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -820,6 +821,16 @@ Plan start_plan(int n, int* units) {
   return p;
 }
 
+// Shared memory for an element of a row that is copied ahead.
+template <typename T, typename Ts>
+constexpr int fwd_bytes() {
+  return 2 * sizeof(T) + sizeof(Ts);
+}
+template <typename T, typename Ts>
+constexpr int bwd_bytes(int upt) {
+  return (gain_sums_in_smem(upt, true) ? 16 : 8) + sizeof(Ts) + 2 * sizeof(T);
+}
+
 template <typename T, typename Ts>
 Plan fwd_plan(int64_t rows, int n) {
   int units;
@@ -834,7 +845,7 @@ Plan fwd_plan(int64_t rows, int n) {
   } else if (units <= 4 * 1024) {
     // four units a thread: more rows at a time than with two or one (2048 bf16,
     // fp32 stream: 91% of the copy rate against 69% with one)
-    set_cta(&p, rows, units, 4, 2 * sizeof(T) + sizeof(Ts), 1024);
+    set_cta(&p, rows, units, 4, fwd_bytes<T, Ts>(), 1024);
   } else {
     p.upt = p.tpr = 0;
     p.threads = 1024;
@@ -851,8 +862,7 @@ Plan bwd_plan(int64_t rows, int n) {
     set_grid(&p, rows, 3);
   } else if (units <= 4 * kMaxBwdThreads) {
     const int upt = units <= 1024 ? 2 : 4;
-    set_cta(&p, rows, units, upt, (gain_sums_in_smem(upt, true) ? 16 : 8) + sizeof(Ts) + 2 * sizeof(T),
-            upt == 2 ? 1024 : kMaxBwdThreads);
+    set_cta(&p, rows, units, upt, bwd_bytes<T, Ts>(upt), upt == 2 ? 1024 : kMaxBwdThreads);
     // two rows a CTA at least: a CTA's partial gains cost about the traffic of one
     if (p.grid > kSms) p.grid = (int)std::max<int64_t>(kSms, std::min<int64_t>(p.grid, rows / 8 * 4));
   } else {
@@ -863,43 +873,52 @@ Plan bwd_plan(int64_t rows, int n) {
   return p;
 }
 
-template <typename K, typename A>
-tsp_status launch(K kernel, const Plan& p, const A& a, cudaStream_t st) {
-  if (p.smem > 47 * 1024)   // (the kernels' static shared memory counts too)
-    TSP_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem));
-  kernel<<<p.grid, p.threads, p.smem, st>>>(a);
+// MOST: the dynamic shared memory of the kernel's widest row.  The limit is a property of
+// the kernel on a device, which calls of all widths and host threads share: it is set
+// once, to that.
+template <auto KERNEL, int MOST, typename A>
+tsp_status launch(const Plan& p, const A& a, cudaStream_t st) {
+  if constexpr (MOST > 47 * 1024) {   // (the kernels' static shared memory counts too)
+    static std::atomic<bool> set[kMaxDevices];
+    const int dev = current_device();
+    if (!set[dev]) {
+      TSP_CUDA_TRY(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, MOST));
+      set[dev] = true;
+    }
+  }
+  KERNEL<<<p.grid, p.threads, p.smem, st>>>(a);
   TSP_CUDA_TRY(cudaGetLastError());
   return TSP_OK;
 }
 
 template <typename T, typename Ts, bool RAGGED>
 tsp_status fwd_r(const Plan& p, const FwdArgs& a, cudaStream_t st) {
-#define TSP_NRF(upt, tpr, ahead) \
-  launch(norm_residual_fwd_kernel<T, Ts, upt, tpr, ahead, RAGGED>, p, a, st)
-  if (p.tpr == 8) return TSP_NRF(1, 8, false);
-  if (p.tpr == 16) return TSP_NRF(1, 16, false);
-  if (p.tpr == 32) return p.upt == 1 ? TSP_NRF(1, 32, false) : TSP_NRF(2, 32, false);
-  if (!p.ahead) return p.upt == 1 ? TSP_NRF(1, 0, false) : TSP_NRF(2, 0, false);
-  return TSP_NRF(4, 0, true);   // (8 or 12 bytes an element of 16384: always fits)
+#define TSP_NRF(upt, tpr, most) \
+  launch<norm_residual_fwd_kernel<T, Ts, upt, tpr, (most > 0), RAGGED>, most>(p, a, st)
+  if (p.tpr == 8) return TSP_NRF(1, 8, 0);
+  if (p.tpr == 16) return TSP_NRF(1, 16, 0);
+  if (p.tpr == 32) return p.upt == 1 ? TSP_NRF(1, 32, 0) : TSP_NRF(2, 32, 0);
+  if (!p.ahead) return p.upt == 1 ? TSP_NRF(1, 0, 0) : TSP_NRF(2, 0, 0);
+  return TSP_NRF(4, 0, (1024 * 16 * fwd_bytes<T, Ts>()));
 #undef TSP_NRF
 }
 template <typename T, typename Ts>
 tsp_status fwd_t(const FwdArgs& a, cudaStream_t st) {
   const Plan p = fwd_plan<T, Ts>(a.rows, a.n);
   Prof prof("norm_residual_fwd", st);
-  if (p.upt == 0) return launch(norm_residual_fwd_wide_kernel<T, Ts>, p, a, st);
+  if (p.upt == 0) return launch<norm_residual_fwd_wide_kernel<T, Ts>, 0>(p, a, st);
   return p.ragged ? fwd_r<T, Ts, true>(p, a, st) : fwd_r<T, Ts, false>(p, a, st);
 }
 
 template <typename T, typename Ts, bool RAGGED>
 tsp_status bwd_r(const Plan& p, const BwdArgs& a, cudaStream_t st) {
-#define TSP_NRB(upt, tpr, ahead) \
-  launch(norm_residual_bwd_kernel<T, Ts, upt, tpr, ahead, RAGGED>, p, a, st)
-  if (p.tpr == 8) return TSP_NRB(1, 8, false);
-  if (p.tpr == 16) return TSP_NRB(1, 16, false);
-  if (p.tpr == 32) return p.upt == 1 ? TSP_NRB(1, 32, false) : TSP_NRB(2, 32, false);
-  if (p.upt == 2) return TSP_NRB(2, 0, true);
-  return TSP_NRB(4, 0, true);   // (up to 20 bytes an element of 8192: always fits)
+#define TSP_NRB(upt, tpr, most) \
+  launch<norm_residual_bwd_kernel<T, Ts, upt, tpr, (tpr == 0), RAGGED>, most>(p, a, st)
+  if (p.tpr == 8) return TSP_NRB(1, 8, 0);
+  if (p.tpr == 16) return TSP_NRB(1, 16, 0);
+  if (p.tpr == 32) return p.upt == 1 ? TSP_NRB(1, 32, 0) : TSP_NRB(2, 32, 0);
+  if (p.upt == 2) return TSP_NRB(2, 0, (kMaxBwdThreads * 8 * bwd_bytes<T, Ts>(2)));
+  return TSP_NRB(4, 0, (kMaxBwdThreads * 16 * bwd_bytes<T, Ts>(4)));
 #undef TSP_NRB
 }
 
@@ -910,7 +929,7 @@ tsp_status bwd_t(BwdArgs a, float* dg_post, float* dg_pre, void* ws, cudaStream_
   a.part_post = (float*)ws;
   a.part_pre = (float*)ws + (int64_t)p.grid * a.n;
   Prof prof("norm_residual_bwd", st, gains ? 2 : 1);
-  const tsp_status r = p.upt == 0 ? launch(norm_residual_bwd_wide_kernel<T, Ts>, p, a, st)
+  const tsp_status r = p.upt == 0 ? launch<norm_residual_bwd_wide_kernel<T, Ts>, 0>(p, a, st)
                        : p.ragged ? bwd_r<T, Ts, true>(p, a, st)
                                   : bwd_r<T, Ts, false>(p, a, st);
   if (r != TSP_OK || !gains) return r;
