@@ -428,7 +428,7 @@ constexpr bool gain_sums_in_smem(int upt, bool ahead) { return ahead && upt <= 2
 // rows (4099 x 1001 fp32: 28 us, half the copy rate) wait for the barriers of short rows
 // and the element accesses at their ends.
 template <typename T, typename Ts, int UPT, int TPR, bool AHEAD, bool RAGGED>
-__global__ void __launch_bounds__(TPR > 0 ? 256 : UPT <= 2 ? 512 : kMaxBwdThreads,
+__global__ void __launch_bounds__(TPR > 0 ? 256 : kMaxBwdThreads,
                                   TPR > 0 ? 3 : UPT <= 2 ? 2 : 1)
     norm_residual_bwd_kernel(const __grid_constant__ BwdArgs a) {
   __shared__ float part[2][32];
@@ -797,19 +797,14 @@ void set_grid(Plan* p, int64_t rows, int per_sm) {
   p->grid = (int)std::min<int64_t>((rows + per - 1) / per, (int64_t)kSms * std::max(1, per_sm));
 }
 // upt units a thread of a CTA, with the next row's `bytes` an element copied ahead
-// where they fit
+// (0: nothing is).  What the widest rows take fits: launch() asserts it.
 void set_cta(Plan* p, int64_t rows, int units, int upt, int bytes, int threads_per_sm) {
   p->upt = upt;
   p->tpr = 0;
   p->threads = ((units + upt - 1) / upt + 31) / 32 * 32;
-  const int row = p->threads * upt * 4 * bytes;
-  int per_sm = std::min(32, threads_per_sm / p->threads);
-  p->ahead = row <= kSmemPerSm;
-  if (p->ahead) {
-    p->smem = row;
-    per_sm = std::min(per_sm, kSmemPerSm / (row + 1024));
-  }
-  set_grid(p, rows, per_sm);
+  p->ahead = bytes > 0;
+  p->smem = p->threads * upt * 4 * bytes;
+  set_grid(p, rows, std::min({32, threads_per_sm / p->threads, kSmemPerSm / (p->smem + 1024)}));
 }
 Plan start_plan(int n, int* units) {
   Plan p = {};
@@ -841,7 +836,6 @@ Plan fwd_plan(int64_t rows, int n) {
     // a row a CTA and nothing to copy ahead (decoded tokens): as many threads as
     // there are units, all loads at once (1 x 4096: 2.8 us, 4.6 with four units each)
     set_cta(&p, rows, units, units <= 1024 ? 1 : 2, 0, 1024);
-    p.ahead = false;
   } else if (units <= 4 * 1024) {
     // four units a thread: more rows at a time than with two or one (2048 bf16,
     // fp32 stream: 91% of the copy rate against 69% with one)
@@ -878,6 +872,7 @@ Plan bwd_plan(int64_t rows, int n) {
 // once, to that.
 template <auto KERNEL, int MOST, typename A>
 tsp_status launch(const Plan& p, const A& a, cudaStream_t st) {
+  static_assert(MOST <= kSmemPerSm, "a row's copies have to fit");
   if constexpr (MOST > 47 * 1024) {   // (the kernels' static shared memory counts too)
     static std::atomic<bool> set[kMaxDevices];
     const int dev = current_device();
