@@ -1245,6 +1245,11 @@ tsp_status tsp_adamw_step(const tsp_adamw_tensor* tensors, int32_t count,
       (uintptr_t)hyper->lr_dev % 4 || (uintptr_t)hyper->step_dev % 8 ||
       (uintptr_t)hyper->gscale_dev % 4)
     return TSP_ERR_INVALID_ARG;
+  // 8-bit states divide by a reciprocal that takes subnormals for zero and has none itself
+  // for a denominator past 2^126: root(v) is 0 or between 2^-75 and 2^64, its factor below
+  // 2^27, so eps decides
+  const float eps = (float)hyper->eps;
+  if (coded && eps != 0.f && !(eps >= 0x1p-126f && eps <= 0x1p100f)) return TSP_ERR_INVALID_ARG;
   for (int32_t i = 0; i < count; ++i) {
     const tsp_adamw_tensor& t = tensors[i];
     if (t.n == 0) continue;

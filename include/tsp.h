@@ -603,7 +603,10 @@ tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f
  * No array that is written may share memory with another of the call's arrays
  * or with a value that is read from the device (what is only read may).
  * tsp_adamw_hyper: lr, beta1, beta2 in [0, 1), eps >= 0, step t >= 1 (the first
- *   update is 1; behind step_dev it is not checked).  lr_dev, step_dev,
+ *   update is 1; behind step_dev it is not checked).  eps counts as it is in
+ *   fp32; with 8-bit states it is 0 or from 2^-126 to 2^100, where the
+ *   quotient keeps its bound.  (With eps 0 an element whose gradients were
+ *   all zero has no quotient: NaN.)  lr_dev, step_dev,
  *   gscale_dev (nullable DEVICE pointers to one value, read when the kernel
  *   runs): replace lr and step, and scale the gradients (clipping by a norm
  *   computed on the device).  A captured call keeps the host values it was

@@ -89,3 +89,18 @@ def test_shapes_are_compared():
             tsp.AdamW(p, **{name: [torch.zeros(4, 6, dtype=dt), torch.zeros(4, 6, dtype=dt)]})
         tsp.AdamW(p, **{name: [torch.zeros(24, dtype=dt), torch.zeros(4, 6, dtype=dt)]})
     assert opt.t == 0
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses")
+@pytest.mark.parametrize("eps,ok", [(0.0, True), (1e-8, True), (2.0 ** -126, True), (2.0 ** 100, True),
+                                    (1e-39, False), (2.0 ** -149, False), (1.01 * 2.0 ** 100, False),
+                                    (1e39, False), (1e-50, True)])   # (the last is 0 in fp32)
+def test_an_eps_whose_reciprocal_is_no_normal_number(lib, eps, ok):
+    """8-bit states divide by a reciprocal that takes subnormals for zero: 0 / 1e-39 would
+    be NaN.  Such an eps is refused; in 32 bits it is divided by."""
+    base = addresses("by tensor")
+    assert (step(lib, base, dict(eps=eps)) == tsp.TSP_ERR_INVALID_ARG) == (not ok)
+    arr = (tsp.AdamwTensor * 1)()
+    arr[0].n, arr[0].w, arr[0].g, arr[0].m, arr[0].v = 1000, AT, 2 * AT, 3 * AT, 4 * AT
+    hy = tsp.AdamwHyper(1e-3, 0.9, 0.95, eps, 1)
+    assert lib.tsp_adamw_step(arr, 1, ctypes.byref(hy), 32, 0, None) != tsp.TSP_ERR_INVALID_ARG
