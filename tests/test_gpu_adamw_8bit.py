@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from folded_tensor_sequence_zigzag_gb300 import tsp
+from tests.test_gpu_adamw import B1, B2, EPS, U, UBF, dequantise, quantise, reference
 
 pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
@@ -37,3 +38,51 @@ def test_zero_gradients_over_the_smallest_eps(bits, eps):
     # (a held root or m is off by at most 2^-4 of itself, for the second of the two moves of 0.25)
     want = (2.0 * 0.875 - 0.25) * 0.875 - 0.25
     assert abs(float(w[300]) - want) <= 0.25 * (3 * 2.0 ** -4 if bits == 8 else 2.0 ** -18)
+
+
+@pytest.mark.parametrize("masters", ["none", "all but every other", "every other"])
+def test_long_runs_with_and_without_masters(masters):
+    """bf16 tensors large enough that a CTA takes 8 chunks in a row (4 where the first
+    tensor has a master), ragged and empty ones between; tensors with a master next to
+    ones without, whose weights come in 16 and in 8 bytes a lane.  On the GPU against
+    elementary operations there."""
+    total = 62_000_000
+    sizes = [total // 2 + 77, 0, 5, 4096 * 3 + 1, 8192 + 512, 640, total // 4 + 2, 129, 4096, 8192, 3 * 4096,
+             total // 4]
+    gen = torch.Generator("cuda").manual_seed(7)
+    r = lambda n: torch.randn(n, generator=gen, device="cuda")   # noqa: E731
+    params = [(0.02 * r(n)).to(BF) for n in sizes]
+    has = [masters != "none" and i % 2 == (masters == "every other") for i in range(len(sizes))]
+    given = [p.float() if on else None for p, on in zip(params, has)]
+    prep = [torch.zeros(n, dtype=torch.float16, device="cuda") if i % 3 else None for i, n in enumerate(sizes)]
+    opt = tsp.AdamW(params, weight_decay=0.1, state_bits=8, master=given, prep=prep, betas=(B1, B2), eps=EPS)
+    state = [p.float() for p in params]
+    ref = [(torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")) for n in sizes]
+    for k in (1, 2):
+        grads = [r(n) * 1e-3 for n in sizes]
+        opt.step(grads, lr=1e-3)
+        for i, n in enumerate(sizes):
+            if n == 0:
+                continue
+            m, root = ref[i]
+            w, m, v, root = reference(state[i], m, root * root, grads[i], 1e-3, 0.1, k)
+            got = opt.master[i] if has[i] else opt.params[i].float()
+            # quotients 4 u apart (rcp 2, product 1, division 1) of an update of at most 1e-3 *
+            # sqrt(1 / 0.05): 4 u of that; numbers that far apart round to weights at most a
+            # spacing further apart, 2 u of the larger (u of bf16 for a bf16 weight)
+            u = U if has[i] else UBF
+            big = torch.maximum(w.abs(), got.abs())
+            want = w if has[i] else w.to(BF).float()
+            assert bool(((got - want).abs() <= 2 * u * big + 4 * U * 5e-3).all()), (i, k)
+            # all but the few that a rounding border separates are the same weight
+            assert has[i] or float((got != want).float().mean()) <= 1e-3 + 1 / n
+            assert torch.equal(opt.params[i], got.to(BF))
+            assert prep[i] is None or torch.equal(prep[i], opt.params[i].half())
+            state[i] = got.clone()
+            qm, sm = quantise(m, False)
+            qr, sr = quantise(root, True)
+            assert torch.equal(opt.m_scale[i], sm) and torch.equal(opt.v_scale[i], sr), (i, k)
+            assert torch.equal(opt.m[i].view(torch.uint8), qm.view(torch.uint8)), (i, k)
+            assert torch.equal(opt.v[i].view(torch.uint8), qr.view(torch.uint8)), (i, k)
+            ref[i] = dequantise(qm, sm), dequantise(qr, sr)
+    assert tsp.device_status() == tsp.TSP_OK
