@@ -126,19 +126,35 @@ __device__ __forceinline__ void zero4(float (&v)[4]) { v[0] = v[1] = v[2] = v[3]
 __device__ __forceinline__ float total(const float (&v)[4]) { return (v[0] + v[1]) + (v[2] + v[3]); }
 
 // sigmoid(z) and its derivative from e = exp(-|z|), which neither overflows nor
-// cancels: sigmoid(|z|) = 1 / (1 + e), sigmoid(-|z|) = e / (1 + e).  e is 2^x of
-// the rounded x = -|z| log2(e): off by |z| + 2 half spacings, which the sigmoid
-// has only where it is e itself, near a closed gate.
+// cancels: sigmoid(|z|) = 1 / (1 + e), sigmoid(-|z|) = e / (1 + e).  e is 2^x of the
+// rounded x = -|z| log2(e), off by |z| half spacings of fp32 and what ex2 adds (2 or
+// 3), which the sigmoid has only where it is e itself, near a closed gate: far below
+// what a gate held in bf16 is uncertain by.  For gates in fp32 the rounding y of x is
+// made up for, 2^(x + y) = 2^x (1 + y ln 2): against 64 bits, every z of 1e-30 <= |z|
+// <= 87, an open gate is then off by 3 half spacings at most, a closed one by 5.3, the
+// slope by 7.4 (16384 x 4096 fp32: 201 us with and without; bf16 would go from 115 to
+// 120).  Beyond 87.3 e is 0.
+template <typename T>
 __device__ __forceinline__ float gate_of(float z, float* slope) {
-  const float e = ex2_approx(-1.4426950408889634f * fabsf(z));
-  float r;   // 1 / (1 + e): 1 <= 1 + e <= 2, one half spacing off at most
+  constexpr float hi = 1.4426950408889634f, lo = (float)(1.4426950408889634074 - (double)hi);
+  float e;
+  if constexpr (sizeof(T) == 4) {
+    const float a = fabsf(z) > 128.f ? 128.f : fabsf(z);   // (infinity has no y; a NaN stays)
+    const float x = -hi * a, y = fmaf(-lo, a, fmaf(-hi, a, -x));
+    e = ex2_approx(x);
+    e = fmaf(e, 0.6931471805599453f * y, e);
+  } else {
+    e = ex2_approx(-hi * fabsf(z));
+  }
+  float r;   // 1 / (1 + e): 1 <= 1 + e <= 2, a spacing off at most
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   *slope = e * r * r;
   return z >= 0.f ? r : e * r;   // (a NaN gives NaN: e is one)
 }
+template <typename T>
 __device__ __forceinline__ float gate_of(float z) {
   float slope;
-  return gate_of(z, &slope);
+  return gate_of<T>(z, &slope);
 }
 
 // Sum over the TPR threads of a row (TPR <= 32: a part of a warp; 0: the CTA),
@@ -325,7 +341,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : 1024, TPR > 0 ? 6 : 1) norm_re
         if (a.z) {
           if constexpr (AHEAD) load_copied<RAGGED>(z_in + i * kStep, c, n, w);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = gate_of(AHEAD ? w[e] : early_z[AHEAD ? 0 : i][e]);
+          for (int e = 0; e < 4; ++e) w[e] = gate_of<T>(AHEAD ? w[e] : early_z[AHEAD ? 0 : i][e]);
           mul4(v[i], w);
         }
         if constexpr (AHEAD) {
@@ -382,13 +398,29 @@ __global__ void __launch_bounds__(1024) norm_residual_fwd_wide_kernel(const __gr
       if (threadIdx.x == 0 && a.rstd_f) a.rstd_f[row] = r;
     }
     ss = 0.f;
-    for (int c = threadIdx.x; c < n; c += blockDim.x) {
-      float u = to_f<T>(f[c]);
-      if (a.g_post) u = u * r * to_f<T>(((const T*)a.g_post)[c]);
-      if (z) u *= gate_of(to_f<T>(z[c]));
-      const Ts o = from_f<Ts>(fmaf(a.s, u, to_f<Ts>(x[c])));
-      h[c] = o;
-      ss = fmaf(to_f<Ts>(o), to_f<Ts>(o), ss);
+    // columns whose loads are ahead of the first one's store (2000 x 20000 fp32: 330 us, 500
+    // with one; bf16: 412 with four, 398 with one)
+    constexpr int K = sizeof(T) == 4 ? 4 : 1;
+    for (int c0 = threadIdx.x; c0 < n; c0 += K * blockDim.x) {
+      float u[K], gate[K], old[K], gain[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int c = c0 + k * blockDim.x;
+        u[k] = c < n ? to_f<T>(f[c]) : 0.f;
+        gate[k] = z && c < n ? to_f<T>(z[c]) : 0.f;
+        old[k] = c < n ? to_f<Ts>(x[c]) : 0.f;
+        gain[k] = a.g_post && c < n ? to_f<T>(((const T*)a.g_post)[c]) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int c = c0 + k * blockDim.x;
+        if (c >= n) continue;
+        if (a.g_post) u[k] = u[k] * r * gain[k];
+        if (z) u[k] *= gate_of<T>(gate[k]);
+        const Ts o = from_f<Ts>(fmaf(a.s, u[k], old[k]));
+        h[c] = o;
+        ss = fmaf(to_f<Ts>(o), to_f<Ts>(o), ss);
+      }
     }
     if (a.g_pre) {
       r = rsqrtf(row_sum<0>(ss, part[1]) * inv_n + a.eps);
@@ -610,7 +642,7 @@ __global__ void __launch_bounds__(TPR > 0 ? 256 : kMaxBwdThreads,
             for (int e = 0; e < 4; ++e) open[e] = early_z[i][e];
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) open[e] = gate_of(open[e], &slope[e]);
+          for (int e = 0; e < 4; ++e) open[e] = gate_of<T>(open[e], &slope[e]);
           mul4(slope, d[i]);
           mul4(slope, y[i]);
           if (a.g_post) mul4(slope, g);
@@ -726,7 +758,7 @@ __global__ void __launch_bounds__(1024) norm_residual_bwd_wide_kernel(const __gr
       if (a.z) {
         const float z = to_f<T>(((const T*)a.z)[base + c]);
         float slope;
-        const float open = gate_of(z, &slope);
+        const float open = gate_of<T>(z, &slope);
         ((T*)a.dz)[base + c] = from_f<T>(d * (y * g) * slope);
         d *= open;
       }
@@ -741,7 +773,7 @@ __global__ void __launch_bounds__(1024) norm_residual_bwd_wide_kernel(const __gr
       dot2 = row_sum<0>(dot2, part[1]) * inv_n;
       for (int c = threadIdx.x; c < n; c += blockDim.x) {
         float d = a.dx[base + c] * a.s;
-        if (a.z) d *= gate_of(to_f<T>(((const T*)a.z)[base + c]));
+        if (a.z) d *= gate_of<T>(to_f<T>(((const T*)a.z)[base + c]));
         const float y = to_f<T>(((const T*)a.f)[base + c]) * rf;
         ((T*)a.df)[base + c] = from_f<T>(rf * (d * to_f<T>(gpost[c]) - y * dot2));
       }
@@ -932,7 +964,7 @@ tsp_status bwd_t(BwdArgs a, float* dg_post, float* dg_pre, void* ws, cudaStream_
   const float* p0 = a.g_post ? a.part_post : a.part_pre;
   float* o0 = a.g_post ? dg_post : dg_pre;
   // short rows: few columns a CTA (a 32-byte sector of each partial row), so that
-  // there are CTAs enough (1001 columns, 1032 partial rows: 4 us of 31, 7 with 32
+  // there are CTAs enough (1001 columns, 1064 partial rows: 4 us of 31, 7 with 32
   // columns; the other way round 4096 x 304 in 4 us less)
   const int cols = a.n <= 2048 ? 8 : 32;
   return launch_after(cols == 8 ? norm_residual_gain_kernel<8> : norm_residual_gain_kernel<32>,
