@@ -1245,6 +1245,7 @@ tsp_status tsp_adamw_step(const tsp_adamw_tensor* tensors, int32_t count,
       (uintptr_t)hyper->lr_dev % 4 || (uintptr_t)hyper->step_dev % 8 ||
       (uintptr_t)hyper->gscale_dev % 4)
     return TSP_ERR_INVALID_ARG;
+  if (coded && hyper->beta2 > TSP_ADAMW_BETA2_MAX) return TSP_ERR_INVALID_ARG;
   // 8-bit states divide by a reciprocal that takes subnormals for zero and has none itself
   // for a denominator past 2^126: root(v) is 0 or between 2^-75 and 2^64, its factor below
   // 2^27, so eps decides

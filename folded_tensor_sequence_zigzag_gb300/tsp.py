@@ -790,7 +790,8 @@ def norm_residual_bwd(dh, db, f, h, g_post=None, g_pre=None, rstd_f=None, rstd_h
     return out
 
 
-ADAMW_BLOCK = 128   # TSP_ADAMW_BLOCK
+ADAMW_BLOCK = 128        # TSP_ADAMW_BLOCK
+ADAMW_BETA2_MAX = 0.97   # TSP_ADAMW_BETA2_MAX, with 8-bit states
 _dtype, _shape = operator.attrgetter("dtype"), operator.attrgetter("shape")
 
 
@@ -824,7 +825,9 @@ class AdamW:
 
     ``weight_decay``: a number, or one per tensor.  ``state_bits``: 32, or 8
     for e4m3 codes with an fp32 scale per 128 elements (``v`` then holds the
-    square root).  ``master``: True keeps fp32 masters of bf16 tensors (started
+    square root).  The codes are rounded to nearest, which follows gradients
+    that change up to beta2 = 0.97 (the default is 0.95); with a larger one a
+    root that should fall stays, so that is refused.  ``master``: True keeps fp32 masters of bf16 tensors (started
     from them), None updates the tensors themselves, a list gives the masters.
     ``m``, ``v``, ``m_scale``, ``v_scale``: lists of existing states to go on
     with (default: zeros).  ``prep``: for each tensor the fp16 operand copy to
@@ -844,6 +847,9 @@ class AdamW:
         index = self.params[0].get_device()
         self.dtype, self.device, self.state_bits = _enum("params", dt), dev, state_bits
         self.betas, self.eps, self.t = (float(betas[0]), float(betas[1])), float(eps), 0
+        if state_bits == 8 and self.betas[1] > ADAMW_BETA2_MAX:
+            raise ValueError(f"8-bit states follow their gradients up to beta2 = {ADAMW_BETA2_MAX}, got "
+                             f"{self.betas[1]}: 32-bit states take it")
         if isinstance(weight_decay, (int, float)):
             weight_decay = [weight_decay] * n_t
         coded, f32 = state_bits == 8, torch.float32

@@ -595,8 +595,18 @@ tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f
  *            with 32; 4-byte aligned), a block's largest magnitude / 448: a code
  *            stands for code * scale.  A block below 2^-100 is held as zeros; a positive
  *            sqrt(v) takes at least the smallest code.  Zero bytes are the
- *            initial state of either.  (Nearest rounding: an 8-bit v that moves
- *            by less than half a spacing relative to its block stays.)
+ *            initial state of either.  Rounding is to nearest: a root that moves
+ *            by less than half a spacing (3 to 6%) relative to its block's
+ *            largest stays.  Without gradients it falls by the factor
+ *            sqrt(beta2) an update, so it is the noise of the block's scale
+ *            that lets it follow.  That suffices up to beta2 = 0.97
+ *            (TSP_ADAMW_BETA2_MAX, more is refused): where half of a block's
+ *            gradients fall by 100, its roots are up to 2.3 times those of 32
+ *            bits on the way down at 0.95 (the same 300 updates after the
+ *            fall), up to 6 times at 0.97 (1.3 times 600 updates after).  At
+ *            0.98 they are twice as large 1500 updates later, at 0.99 65
+ *            times.  A block whose largest gradient hardly varies has no such
+ *            noise.
  *   prep     [n] fp16 or NULL (TSP_BF16 only): receives the new weight as the
  *            operand copy tsp_block_weights_prepare would make of it (a weight
  *            fp16 cannot hold records TSP_ERR_RANGE)
@@ -622,6 +632,7 @@ tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f
  * One launch per 128 tensors.  Errors: TSP_ERR_INVALID_ARG (also for arrays
  *   that overlap). */
 #define TSP_ADAMW_BLOCK 128
+#define TSP_ADAMW_BETA2_MAX 0.97   /* with 8-bit states */
 typedef struct {
   int64_t n;
   void* w;

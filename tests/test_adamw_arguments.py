@@ -104,3 +104,17 @@ def test_an_eps_whose_reciprocal_is_no_normal_number(lib, eps, ok):
     arr[0].n, arr[0].w, arr[0].g, arr[0].m, arr[0].v = 1000, AT, 2 * AT, 3 * AT, 4 * AT
     hy = tsp.AdamwHyper(1e-3, 0.9, 0.95, eps, 1)
     assert lib.tsp_adamw_step(arr, 1, ctypes.byref(hy), 32, 0, None) != tsp.TSP_ERR_INVALID_ARG
+
+
+def test_a_beta2_that_8_bit_states_do_not_follow(lib):
+    p = [torch.zeros(300)]
+    for beta2, ok in ((0.0, True), (0.95, True), (0.97, True), (0.98, False), (0.999, False)):
+        if ok:
+            tsp.AdamW(p, state_bits=8, betas=(0.9, beta2))
+        else:
+            with pytest.raises(ValueError, match="beta2"):
+                tsp.AdamW(p, state_bits=8, betas=(0.9, beta2))
+        tsp.AdamW(p, state_bits=32, betas=(0.9, beta2))
+        if not torch.cuda.is_available():                       # (made-up addresses)
+            base = addresses("by tensor")
+            assert (step(lib, base, dict(beta2=beta2)) == tsp.TSP_ERR_INVALID_ARG) == (not ok)

@@ -86,3 +86,30 @@ def test_long_runs_with_and_without_masters(masters):
             assert torch.equal(opt.v[i].view(torch.uint8), qr.view(torch.uint8)), (i, k)
             ref[i] = dequantise(qm, sm), dequantise(qr, sr)
     assert tsp.device_status() == tsp.TSP_OK
+
+
+@pytest.mark.parametrize("beta2", [0.9, B2, 0.97])
+def test_held_roots_follow_their_gradients(beta2):
+    """After 300 updates the gradients of every other element fall by 100, for which v
+    itself needs ln(10^4) / ln(1 / beta2) updates, 302 at 0.97.  Four times that later the
+    held roots are on average within half an e4m3 step, 2^-4, of the 32-bit ones, which is
+    what a rounding that is not held on to leaves; so are the squares of the updates,
+    whose factor is the root (twice that)."""
+    n = 128 * 500
+    gen = torch.Generator("cuda").manual_seed(1)
+    size = torch.exp(torch.randn(n, device="cuda", generator=gen)) * 1e-3
+    half = torch.arange(n, device="cuda") % 2 == 0
+    opt = {b: tsp.AdamW([torch.zeros(n, device="cuda")], state_bits=b, betas=(B1, beta2)) for b in (8, 32)}
+    for k in range(1500):
+        if k == 300:
+            size = torch.where(half, size * 0.01, size)
+        if k == 1499:
+            before = {b: o.params[0].clone() for b, o in opt.items()}
+        g = torch.randn(n, device="cuda", generator=gen) * size
+        for o in opt.values():
+            o.step([g], lr=1e-3)
+    ratio = dequantise(opt[8].v[0], opt[8].v_scale[0]) / opt[32].v[0].sqrt()
+    for part in (half, ~half):
+        assert abs(float(ratio[part].mean()) - 1) <= 2.0 ** -4
+        moves = [float((opt[b].params[0] - before[b])[part].square().mean().sqrt()) for b in (8, 32)]
+        assert abs(moves[0] / moves[1] - 1) <= 2.0 ** -3
