@@ -445,7 +445,9 @@ struct BwdArgs {
 };
 
 // The gain sums of a CTA-wide row are in shared memory where 64 registers a thread
-// let two CTAs of 512 run on a multiprocessor (two units a thread).
+// let two CTAs of 512 run on a multiprocessor (two units a thread).  (Of fp32 rows of
+// more than 3840 elements the copies and sums leave room for one: 16384 x 4096 with a
+// gate takes 388 us, 82% of the copy rate; bf16 with an fp32 stream 249 us, 95%.)
 // (Four units a thread need 128 registers: 512 threads, rows of up to 8192.)
 constexpr int kMaxBwdThreads = 512;
 constexpr bool gain_sums_in_smem(int upt, bool ahead) { return ahead && upt <= 2; }
@@ -838,6 +840,10 @@ void set_cta(Plan* p, int64_t rows, int units, int upt, int bytes, int threads_p
   p->smem = p->threads * upt * 4 * bytes;
   set_grid(p, rows, std::min({32, threads_per_sm / p->threads, kSmemPerSm / (p->smem + 1024)}));
 }
+// Rows of up to 256 elements lie in a part of a warp.  With two units a lane (132 to 256)
+// the backward spills 36 to 136 bytes a thread at three CTAs a multiprocessor, the
+// forward 8 to 48 at six: 131072 x 256 with a gate and both norms takes 112 us forward
+// and 181 backward in fp32 (88% of the copy rate), 64 and 158 in bf16 (78 and 69%).
 Plan start_plan(int n, int* units) {
   Plan p = {};
   p.ragged = n % 4 != 0;

@@ -870,7 +870,7 @@ class AdamW:
         self.m_scale = states(m_scale, f32, blocks, coded)
         self.v_scale = states(v_scale, f32, blocks, coded)
         if master is True:
-            master = [p.float() for p in self.params] if self.dtype == TSP_BF16 else None
+            master = [p.detach().float() for p in self.params] if self.dtype == TSP_BF16 else None
         self.master = list(master) if master is not None and master is not False else [None] * n_t
         self.prep = list(prep) if prep is not None else [None] * n_t
         every = (weight_decay, self.m, self.v, self.m_scale, self.v_scale, self.master, self.prep)
