@@ -70,8 +70,8 @@ struct Args {
 // tensors would be updated.  So the word is copied once, where the stream reaches the
 // call, and the kernels look at the copy.  A call's place among the copies comes round
 // again after kHeldPlaces calls, and captured calls, which keep theirs, have a set of
-// their own.  (The first kernel follows this one as a dependent launch: 1.4 us of the
-// host's time, 1 us in a graph; a copy of four bytes by the driver costs 4 us.)
+// their own.  (The first kernel follows this one as a dependent launch: 2.5 us of a
+// call, 1 us in a graph; a copy of four bytes by the driver costs 4 us of a call.)
 constexpr unsigned kHeldPlaces = 32768;
 __device__ int g_held[2][kHeldPlaces];
 
@@ -607,7 +607,7 @@ tsp_status launch_adamw(const tsp_adamw_tensor* ts, int count, const tsp_adamw_h
     Prof prof("adamw", st);
     if (state_bits == 8) {
       // Runs of several chunks to copy ahead in, in order, so that what is written at a
-      // time lies together (a 7B-shaped block: 591 us, with resident CTAs walking all
+      // time lies together (a 7B-shaped block: 594 us, with resident CTAs walking all
       // chunks 738).  With masters (20 bytes an element) memory is the bound: runs of 4
       // (8: 600 us), shorter ones where that leaves less than three for every resident
       // CTA (12.8 M elements: 46 us in twos, 50 in single chunks).  Without (12 to 16
