@@ -20,6 +20,7 @@
 // element next to a much larger one is not divided by eps alone.
 //
 // Bound by HBM: every element is read and written once.
+#include <cooperative_groups.h>
 #include <cuda_fp8.h>
 
 #include <atomic>
@@ -59,7 +60,7 @@ struct Args {
   const float* lr_dev;
   const int64_t* step_dev;
   const float* gscale;
-  const int* held;   // the status word as the call found it
+  const int* held;   // the status word as the call found it (not in the cluster forms)
   int* status;
 };
 
@@ -70,9 +71,13 @@ struct Args {
 // tensors would be updated.  So the word is copied once, where the stream reaches the
 // call, and the kernels look at the copy.  A call's place among the copies comes round
 // again after kHeldPlaces calls, and captured calls, which keep theirs, have a set of
-// their own.  (The first kernel follows this one as a dependent launch: 2.5 us of a
+// their own.  (The first kernel follows this one as a dependent launch: 3 us of a
 // call, 1 us in a graph; a copy of four bytes by the driver costs 4 us of a call.)
+// Up to kClusterChunks chunks the grid is one cluster, whose first CTA looks at the word
+// for all of them: nine tensors of the tiny block (12 chunks) take 13 us a call so, 16
+// with the copy; in a graph 4.5 either way.
 constexpr unsigned kHeldPlaces = 32768;
+constexpr int kClusterChunks = 16;
 __device__ int g_held[2][kHeldPlaces];
 
 __global__ void adamw_held_kernel(int* held, const int* status) { *held = *status; }
@@ -95,6 +100,17 @@ tsp_status take_held(const int* status, cudaStream_t st, const int** held) {
   TSP_CUDA_TRY(cudaGetLastError());
   *held = at;
   return TSP_OK;
+}
+
+// The status word as the first CTA of the cluster finds it, the same in all of its CTAs.
+__device__ __forceinline__ int held_in_cluster(const Args& a) {
+  __shared__ int word;
+  const auto cluster = cooperative_groups::this_cluster();
+  if (threadIdx.x == 0 && cluster.block_rank() == 0) word = *(const volatile int*)a.status;
+  cluster.sync();
+  const int held = *cluster.map_shared_rank(&word, 0);
+  cluster.sync();   // (read by all before the first one may end)
+  return held;
 }
 
 // x^n by squaring, n >= 1
@@ -400,11 +416,16 @@ __device__ __forceinline__ Step step_of(const Args& a) {
 
 // 32-bit states: 28 to 32 bytes an element and little to compute; CTAs in order of
 // the elements (a 7B-shaped block: 922 us, 962 with 8 CTAs a multiprocessor walking).
-template <typename T>
+template <typename T, bool CLUSTER>   // the grid is one cluster
 __global__ void __launch_bounds__(256, 3) adamw_kernel(const __grid_constant__ Args a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  after_previous_kernel();
-  const int held = *a.held;
+  int held;
+  if constexpr (CLUSTER) {
+    held = held_in_cluster(a);
+  } else {
+    after_previous_kernel();
+    held = *a.held;
+  }
   const Step s = step_of(a);
   bool bad = false;
   const int64_t chunks = a.end[a.count - 1];
@@ -437,18 +458,19 @@ struct Ahead {   // one warp's groups on their way
 };
 constexpr int kAheadSmem = 8 * sizeof(Ahead);
 
-template <typename T, int CTAS>   // CTAs a multiprocessor
+template <typename T, int CTAS>   // CTAs a multiprocessor; 1: the grid is one cluster
 __global__ void __launch_bounds__(256, CTAS) adamw_coded_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Ahead& in = reinterpret_cast<Ahead*>(smem)[warp];
   float *const in_g = in.g[0] + lane * 4, *const in_p = in.p[0] + lane * 4;
   uint32_t *const in_m = in.m[0] + lane, *const in_v = in.v[0] + lane;
-  after_previous_kernel();
+  if (CTAS != 1) after_previous_kernel();
   // Loaded and tested in the way that costs least: for runs here, and as any value (593.9
   // us of a 7B-shaped block, 593.6 without; 598 in the other way); for single chunks
   // behind the first one's scales, with a vote (34.1 us of 3.1 M elements, 36 otherwise).
   int held = 0;
+  if (CTAS == 1) held = held_in_cluster(a);
   if (CTAS == 2) held = *a.held;
   const Step s = step_of(a);
   bool bad = false;
@@ -505,10 +527,10 @@ __global__ void __launch_bounds__(256, CTAS) adamw_coded_kernel(const __grid_con
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   look(begin);
-  if (CTAS != 2) held = *a.held;
+  if (CTAS == 3) held = *a.held;
 #pragma unroll
   for (int u = 0; u < kGroups; ++u) issue(u);
-  if (CTAS == 2 ? held != 0 : __any_sync(0xffffffffu, held)) {   // the copies have to arrive before their places go
+  if (CTAS != 3 ? held != 0 : __any_sync(0xffffffffu, held)) {   // the copies have to arrive before their places go
     asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
@@ -544,23 +566,41 @@ __global__ void __launch_bounds__(256, CTAS) adamw_coded_kernel(const __grid_con
   if (bad) report_status(a.status, (int)TSP_ERR_RANGE);
 }
 
-// A launch of 256 threads a CTA; dependent: behind adamw_held_kernel (see launch_after,
-// which would copy the arguments' 11 KB).
-tsp_status launch(void (*kernel)(Args), unsigned grid, size_t smem, bool dependent, cudaStream_t st,
-                  Args& a) {
+// A launch of 256 threads a CTA: an ordinary one, behind adamw_held_kernel (see
+// launch_after, which would copy the arguments' 11 KB), or of one cluster.
+enum class How { ordinary, dependent, cluster };
+tsp_status launch(void (*kernel)(Args), unsigned grid, size_t smem, How how, cudaStream_t st, Args& a) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
+  if (how == How::cluster) {
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = grid;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  } else {
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = at;
-  cfg.numAttrs = dependent ? 1 : 0;
+  cfg.numAttrs = how == How::ordinary ? 0 : 1;
   void* args[] = {&a};
   TSP_CUDA_TRY(cudaLaunchKernelExC(&cfg, (const void*)kernel, args));
   return TSP_OK;
+}
+
+// The whole grid as one cluster, of up to 16 CTAs (more than 8 have to be allowed).
+template <auto KERNEL>
+tsp_status launch_cluster(unsigned grid, size_t smem, cudaStream_t st, Args& a) {
+  static std::atomic<bool> allowed[kMaxDevices];
+  const int dev = current_device();
+  if (!allowed[dev]) {
+    TSP_CUDA_TRY(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+    allowed[dev] = true;
+  }
+  return launch(KERNEL, grid, smem, How::cluster, st, a);
 }
 
 }  // namespace
@@ -601,9 +641,23 @@ tsp_status launch_adamw(const tsp_adamw_tensor* ts, int count, const tsp_adamw_h
     }
     if (a.count == 0) break;
     const bool first = !a.held;
+    const bool bf = dtype == TSP_BF16;
+    if (first && chunks <= kClusterChunks) {   // (so few hold all of the call's tensors)
+      if (!a.status) return TSP_ERR_CUDA;
+      unsigned grid = 1;
+      while (grid < chunks) grid *= 2;
+      a.run = 1;
+      Prof prof("adamw", st);
+      if (state_bits == 8)
+        return bf ? launch_cluster<adamw_coded_kernel<__nv_bfloat16, 1>>(grid, kAheadSmem, st, a)
+                  : launch_cluster<adamw_coded_kernel<float, 1>>(grid, kAheadSmem, st, a);
+      return bf ? launch_cluster<adamw_kernel<__nv_bfloat16, true>>(grid, 0, st, a)
+                : launch_cluster<adamw_kernel<float, true>>(grid, 0, st, a);
+    }
     tsp_status r = TSP_OK;
     if (first) r = take_held(a.status, st, &a.held);   // (all of the call's launches use it)
     if (r != TSP_OK) return r;
+    const How how = first ? How::dependent : How::ordinary;
     Prof prof("adamw", st);
     if (state_bits == 8) {
       // Runs of several chunks to copy ahead in, in order, so that what is written at a
@@ -619,17 +673,15 @@ tsp_status launch_adamw(const tsp_adamw_tensor* ts, int count, const tsp_adamw_h
       a.run = (int)std::max<int64_t>(
           1, std::min<int64_t>(masters ? 4 : 8, chunks / ((int64_t)num_sms() * (masters ? 6 : 12))));
       const unsigned grid = (unsigned)((chunks + a.run - 1) / a.run);
-      const bool bf = dtype == TSP_BF16;
       if (a.run >= 2)
         r = launch(bf ? adamw_coded_kernel<__nv_bfloat16, 2> : adamw_coded_kernel<float, 2>, grid,
-                   kAheadSmem, first, st, a);
+                   kAheadSmem, how, st, a);
       else
         r = launch(bf ? adamw_coded_kernel<__nv_bfloat16, 3> : adamw_coded_kernel<float, 3>, grid,
-                   kAheadSmem, first, st, a);
+                   kAheadSmem, how, st, a);
     } else {
       const unsigned grid = (unsigned)std::min<int64_t>(chunks, (int64_t)num_sms() * 256);
-      r = launch(dtype == TSP_BF16 ? adamw_kernel<__nv_bfloat16> : adamw_kernel<float>, grid, 0, first,
-                 st, a);
+      r = launch(bf ? adamw_kernel<__nv_bfloat16, false> : adamw_kernel<float, false>, grid, 0, how, st, a);
     }
     if (r != TSP_OK) return r;
   }

@@ -43,9 +43,9 @@ def make(sizes, dt, bits, master, prep, seed=0):
     return tsp.AdamW(ps, weight_decay=0.1, state_bits=bits, master=master, prep=copies), gs
 
 
-# single chunks, runs of chunks (8-bit states: from 152 * 12 chunks of 4096 on) and tails;
-# more tensors than one launch holds
-SIZES = {"few": [1, 129, 4097, 0, 33000], "large": [9_000_001, 77], "many": [(37 * i) % 900 for i in range(300)]}
+# one cluster (up to 16 chunks of 4096), single chunks, runs of chunks (8-bit states: from
+# 152 * 12 chunks on) and tails; more tensors than one launch holds
+SIZES = {"one": [5], "few": [1, 129, 4097, 0, 33000], "some": [4096 * 16, 3], "medium": [1_000_001, 77], "large": [9_000_001, 77], "many": [(37 * i) % 900 for i in range(300)]}
 
 
 @pytest.mark.parametrize("sizes", SIZES)
@@ -72,7 +72,7 @@ def test_an_error_holds_the_update_back(sizes, bits, dt, master, prep):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
-@pytest.mark.parametrize("sizes", [[9_000_001, 77, 5000], [300] * 300])
+@pytest.mark.parametrize("sizes", [[9_000_001, 77, 5000], [300] * 300, [300] * 10, [40_000, 77], [300_000]])
 def test_an_error_of_its_own_stops_no_part_of_an_update(bits, sizes):
     """The first weight does not fit fp16: every tensor is updated all the same, and
     the next step is held back."""
