@@ -827,8 +827,9 @@ class AdamW:
     for e4m3 codes with an fp32 scale per 128 elements (``v`` then holds the
     square root).  The codes are rounded to nearest, which follows gradients
     that change up to beta2 = 0.97 (the default is 0.95); with a larger one a
-    root that should fall stays, so that is refused.  ``master``: True keeps fp32 masters of bf16 tensors (started
-    from them), None updates the tensors themselves, a list gives the masters.
+    root that should fall stays, so that is refused.  ``master``: True keeps
+    fp32 masters of bf16 tensors (started from them), None updates the tensors
+    themselves, a list gives the masters (None for a tensor without one).
     ``m``, ``v``, ``m_scale``, ``v_scale``: lists of existing states to go on
     with (default: zeros).  ``prep``: for each tensor the fp16 operand copy to
     refresh (prep_views) or None.  Each has its tensor's shape or is flat (the
