@@ -1231,6 +1231,113 @@ tsp_status tsp_norm_residual_bwd(const float* dh, const float* db, const void* f
                                   S_(stream));
 }
 
+// ---- behind the stack: log probabilities and losses of tokens ----
+
+static bool aligned(const void* p, size_t to) { return (uintptr_t)p % to == 0; }
+static size_t element(int32_t dtype) { return dtype == TSP_F32 ? 4 : 2; }
+
+// The rows and the given tokens (ids may be NULL).
+static tsp_status check_logits(const tsp_logits* x, const void* ids, int32_t id_bytes) {
+  if (!x || !x->logits || x->S <= 0 || x->V <= 0 || x->ld < x->V || x->D < 1 || x->D > 64 ||
+      (x->D > 1 && x->S % (2 * (int64_t)x->D) != 0) ||
+      (x->dtype != TSP_F32 && x->dtype != TSP_BF16) || !aligned(x->logits, element(x->dtype)) ||
+      !(x->scale >= 0x1p-16f && x->scale <= 0x1p16f) || (ids && !ids_ok(ids, id_bytes)))
+    return TSP_ERR_INVALID_ARG;
+  const int64_t most = (int64_t)1 << 30;
+  return x->S > most || x->V > most || x->ld > (int64_t)1 << 32 ? TSP_ERR_UNSUPPORTED : TSP_OK;
+}
+// Rows ld elements apart, without what lies behind the last one.
+static Span rows_span(const tsp_logits* x, const void* p, int64_t ld) {
+  return {p, (size_t)((x->S - 1) * ld + x->V) * element(x->dtype)};
+}
+static bool check_dlogits(const tsp_logits* x, const void* d, int64_t ld_d) {
+  return d && aligned(d, element(x->dtype)) && ld_d >= x->V && ld_d <= (int64_t)1 << 32;
+}
+// The logits as an input: none where the gradient takes their place.
+static Span logits_span(const tsp_logits* x, const void* dlogits, int64_t ld_d) {
+  return dlogits == x->logits && (ld_d == x->ld || x->S == 1) ? Span{nullptr, 0}
+                                                              : rows_span(x, x->logits, x->ld);
+}
+static tsp_status check_teacher(const tsp_teacher* t, float w_ce, const void* ids) {
+  if (!std::isfinite(w_ce) || (w_ce != 0.f && !ids)) return TSP_ERR_INVALID_ARG;
+  if (!t) return TSP_OK;
+  return t->ids && aligned(t->ids, 4) && t->logits && t->K >= 1 && t->K <= TSP_TOP_MAX &&
+                 std::isfinite(t->weight) && t->scale >= 0x1p-16f && t->scale <= 0x1p16f &&
+                 (t->dtype == TSP_F32 || t->dtype == TSP_BF16) &&
+                 aligned(t->logits, element(t->dtype))
+             ? TSP_OK
+             : TSP_ERR_INVALID_ARG;
+}
+
+tsp_status tsp_logprobs_fwd(const tsp_logits* x, const void* ids, int32_t id_bytes, float* logp,
+                            float* entropy, float* stats, int32_t* top_ids, float* top_logp,
+                            int32_t top, void* stream) {
+  const tsp_status r = check_logits(x, ids, id_bytes);
+  if (r != TSP_OK) return r;
+  const size_t S = x->S;
+  if ((logp && !ids) || top < 0 || top > TSP_TOP_MAX || (top > 0) != (top_ids != nullptr) ||
+      (top > 0) != (top_logp != nullptr) || !(logp || entropy || stats || top) ||
+      !aligned(logp, 4) || !aligned(entropy, 4) || !aligned(stats, 4) || !aligned(top_ids, 4) ||
+      !aligned(top_logp, 4) ||
+      !apart({{logp, S * 4}, {entropy, S * 4}, {stats, S * 8}, {top_ids, S * top * 4}, {top_logp, S * top * 4}},
+             {rows_span(x, x->logits, x->ld), {ids, S * id_bytes}}))
+    return TSP_ERR_INVALID_ARG;
+  return launch_logprobs_fwd(*x, ids, id_bytes, logp, entropy, stats, top_ids, top_logp, top,
+                             S_(stream));
+}
+
+tsp_status tsp_logprobs_bwd(const tsp_logits* x, const void* ids, int32_t id_bytes,
+                            const float* stats, const float* entropy, const float* dlogp,
+                            const float* dentropy, void* dlogits, int64_t ld_d, void* stream) {
+  const tsp_status r = check_logits(x, ids, id_bytes);
+  if (r != TSP_OK) return r;
+  const size_t S = x->S;
+  if (!stats || !(dlogp || dentropy) || (dlogp && !ids) || (dentropy != nullptr) != (entropy != nullptr) ||
+      !check_dlogits(x, dlogits, ld_d) || !aligned(stats, 4) || !aligned(entropy, 4) ||
+      !aligned(dlogp, 4) || !aligned(dentropy, 4) ||
+      !apart({rows_span(x, dlogits, ld_d)},
+             {logits_span(x, dlogits, ld_d), {ids, S * id_bytes}, {stats, S * 8}, {entropy, S * 4},
+              {dlogp, S * 4}, {dentropy, S * 4}}))
+    return TSP_ERR_INVALID_ARG;
+  return launch_logprobs_bwd(*x, ids, id_bytes, stats, entropy, dlogp, dentropy, dlogits, ld_d,
+                             S_(stream));
+}
+
+tsp_status tsp_token_loss_fwd(const tsp_logits* x, const void* ids, int32_t id_bytes, float w_ce,
+                              const tsp_teacher* teacher, float* loss, float* stats,
+                              const float* dloss, void* dlogits, int64_t ld_d, void* stream) {
+  tsp_status r = check_logits(x, ids, id_bytes);
+  if (r == TSP_OK) r = check_teacher(teacher, w_ce, ids);
+  if (r != TSP_OK) return r;
+  const size_t S = x->S, SK = teacher ? S * teacher->K : 0;
+  if (!loss || !stats || !aligned(loss, 4) || !aligned(stats, 4) || !aligned(dloss, 4) ||
+      (dlogits ? !check_dlogits(x, dlogits, ld_d) : dloss != nullptr) ||
+      !apart({dlogits ? rows_span(x, dlogits, ld_d) : Span{nullptr, 0}, {loss, S * 4}, {stats, S * 8}},
+             {logits_span(x, dlogits, ld_d), {ids, S * id_bytes}, {dloss, S * 4},
+              {teacher ? teacher->ids : nullptr, SK * 4},
+              {teacher ? teacher->logits : nullptr, teacher ? SK * element(teacher->dtype) : 0}}))
+    return TSP_ERR_INVALID_ARG;
+  return launch_token_loss_fwd(*x, ids, id_bytes, w_ce, teacher, loss, stats, dloss, dlogits, ld_d,
+                               S_(stream));
+}
+
+tsp_status tsp_token_loss_bwd(const tsp_logits* x, const void* ids, int32_t id_bytes, float w_ce,
+                              const tsp_teacher* teacher, const float* stats, const float* dloss,
+                              void* dlogits, int64_t ld_d, void* stream) {
+  tsp_status r = check_logits(x, ids, id_bytes);
+  if (r == TSP_OK) r = check_teacher(teacher, w_ce, ids);
+  if (r != TSP_OK) return r;
+  const size_t S = x->S, SK = teacher ? S * teacher->K : 0;
+  if (!stats || !aligned(stats, 4) || !aligned(dloss, 4) || !check_dlogits(x, dlogits, ld_d) ||
+      !apart({rows_span(x, dlogits, ld_d)},
+             {logits_span(x, dlogits, ld_d), {ids, S * id_bytes}, {stats, S * 8}, {dloss, S * 4},
+              {teacher ? teacher->ids : nullptr, SK * 4},
+              {teacher ? teacher->logits : nullptr, teacher ? SK * element(teacher->dtype) : 0}}))
+    return TSP_ERR_INVALID_ARG;
+  return launch_token_loss_bwd(*x, ids, id_bytes, w_ce, teacher, stats, dloss, dlogits, ld_d,
+                               S_(stream));
+}
+
 tsp_status tsp_adamw_step(const tsp_adamw_tensor* tensors, int32_t count,
                           const tsp_adamw_hyper* hyper, int32_t state_bits, int32_t dtype,
                           void* stream) {

@@ -163,6 +163,20 @@ tsp_status launch_norm_residual_bwd(const float* dh, const float* db, const void
 tsp_status launch_adamw(const tsp_adamw_tensor* ts, int count, const tsp_adamw_hyper* h,
                         int state_bits, int dtype, cudaStream_t st);
 
+// logits.cu (arguments as checked by tsp_logprobs_fwd / _bwd and tsp_token_loss_fwd / _bwd)
+tsp_status launch_logprobs_fwd(const tsp_logits& x, const void* ids, int id_bytes, float* logp,
+                               float* entropy, float* stats, int* top_ids, float* top_logp, int top,
+                               cudaStream_t st);
+tsp_status launch_logprobs_bwd(const tsp_logits& x, const void* ids, int id_bytes, const float* stats,
+                               const float* entropy, const float* dlogp, const float* dentropy,
+                               void* dlogits, int64_t ld_d, cudaStream_t st);
+tsp_status launch_token_loss_fwd(const tsp_logits& x, const void* ids, int id_bytes, float w_ce,
+                                 const tsp_teacher* teacher, float* loss, float* stats,
+                                 const float* dloss, void* dlogits, int64_t ld_d, cudaStream_t st);
+tsp_status launch_token_loss_bwd(const tsp_logits& x, const void* ids, int id_bytes, float w_ce,
+                                 const tsp_teacher* teacher, const float* stats, const float* dloss,
+                                 void* dlogits, int64_t ld_d, cudaStream_t st);
+
 // api.cu: TSP_OK if the configuration is valid (the entry points' common check)
 tsp_status cfg_status(const tsp_cfg* cfg);
 

@@ -40,7 +40,8 @@ EXPORTED = ("tsp_zigzag_permute", "tsp_rmsnorm_fwd", "tsp_workspace_bytes", "tsp
             "tsp_rank_mlp_bwd_step", "tsp_rank_mlp_bwd_finish", "tsp_rank_attn_bwd_heads",
             "tsp_rank_attn_bwd_weights", "tsp_rank_attn_bwd_finish", "tsp_embed_fwd",
             "tsp_embed_bwd_workspace_bytes", "tsp_embed_bwd", "tsp_norm_residual_fwd",
-            "tsp_norm_residual_bwd_workspace_bytes", "tsp_norm_residual_bwd", "tsp_adamw_step")
+            "tsp_norm_residual_bwd_workspace_bytes", "tsp_norm_residual_bwd", "tsp_adamw_step",
+            "tsp_logprobs_fwd", "tsp_logprobs_bwd", "tsp_token_loss_fwd", "tsp_token_loss_bwd")
 DECODE_MAX_T = 8   # TSP_DECODE_MAX_T
 
 
@@ -78,6 +79,17 @@ class AdamwHyper(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("lr_dev", ctypes.c_void_p),
                 ("step_dev", ctypes.c_void_p), ("gscale_dev", ctypes.c_void_p)]
+
+
+class Logits(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("ld", ctypes.c_int64), ("S", ctypes.c_int64),
+                ("V", ctypes.c_int64), ("D", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("dtype", ctypes.c_int32)]
+
+
+class Teacher(ctypes.Structure):
+    _fields_ = [("ids", ctypes.c_void_p), ("logits", ctypes.c_void_p), ("K", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("weight", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -145,6 +157,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "tsp_norm_residual_bwd_workspace_bytes": (sz, [i64, i32]),
         "tsp_norm_residual_bwd": (i32, [vp] * 14 + [i64, i32, f32, i32, i32, vp, sz, vp]),
         "tsp_adamw_step": (i32, [P(AdamwTensor), i32, P(AdamwHyper), i32, i32, vp]),
+        "tsp_logprobs_fwd": (i32, [P(Logits), vp, i32] + [vp] * 5 + [i32, vp]),
+        "tsp_logprobs_bwd": (i32, [P(Logits), vp, i32] + [vp] * 5 + [i64, vp]),
+        "tsp_token_loss_fwd": (i32, [P(Logits), vp, i32, f32, P(Teacher)] + [vp] * 4 + [i64, vp]),
+        "tsp_token_loss_bwd": (i32, [P(Logits), vp, i32, f32, P(Teacher)] + [vp] * 3 + [i64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -954,6 +970,160 @@ class AdamW:
                                          self.dtype, st), "tsp_adamw_step")
         if not isinstance(step, torch.Tensor):
             self.t = int(hy.step)
+
+
+# ---- behind the stack: log probabilities and losses of tokens ----
+TOP_MAX = 256   # TSP_TOP_MAX
+
+
+def _rows_arg(name, t, shape, dtype, index):
+    """(address, row distance) of a matrix whose rows are dense."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} of shape {tuple(shape)}, got {t.dtype} of "
+                         f"shape {tuple(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on the device of the other tensors")
+    V = shape[1]
+    ld, one = t.stride()
+    if one != 1 and V > 1 or ld < V and shape[0] > 1:
+        raise ValueError(f"{name}: elements of a row must be dense and rows apart, got strides {t.stride()}")
+    return t.data_ptr(), max(ld, V)
+
+
+def _logits_arg(logits, ids, D, scale):
+    """(tsp_logits, address of ids, id_bytes, device index)."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [S, V]")
+    dt, index, shape = logits.dtype, logits.get_device(), logits.shape
+    e = _enum("logits", dt)
+    px, ld = _rows_arg("logits", logits, shape, dt, index)
+    pi, id_bytes = None, 0
+    if ids is not None:
+        id_bytes = _ids_arg(ids)
+        pi = _arg("ids", ids, shape[:1], ids.dtype, index)
+    return Logits(px, ld, shape[0], shape[1], D, scale, e), pi, id_bytes, index
+
+
+def _rows_like(logits):
+    """A gradient's memory: rows as far apart as the logits'."""
+    S, V = logits.shape
+    ld = max(logits.stride(0), V)
+    if ld == V:
+        return empty((S, V), logits.dtype, logits.device)
+    return empty((S * ld,), logits.dtype, logits.device).view(S, ld)[:, :V]
+
+
+def logprobs_fwd(logits, ids=None, D: int = 1, scale: float = 1.0, top: int = 0,
+                 entropy: bool = False, stats: bool = False, stream=None) -> dict:
+    """Log probabilities of the tokens ``ids`` [S] (int32 or int64, global order, < 0
+    for padding) under softmax(scale * logits): ``logp`` [S] (with ids) and, where
+    wanted, ``entropy`` [S], ``stats`` [S, 2] (for the gradients) and the ``top``
+    largest alternatives ``top_ids`` [S, top] int32 and ``top_logp`` [S, top].
+    ``logits`` [S, V] bf16 or fp32 in the zigzag order of D ranks (D = 1: global
+    order), rows dense, possibly further apart than V; the results are in global order."""
+    x, pi, id_bytes, index = _logits_arg(logits, ids, D, scale)
+    S, dev, f32 = x.S, logits.device, torch.float32
+    out = {}
+    p = [None] * 5
+    with _On(index, stream) as st:
+        if pi is not None:
+            t = out["logp"] = empty((S,), f32, dev)
+            p[0] = t.data_ptr()
+        if entropy:
+            t = out["entropy"] = empty((S,), f32, dev)
+            p[1] = t.data_ptr()
+        if stats:
+            t = out["stats"] = empty((S, 2), f32, dev)
+            p[2] = t.data_ptr()
+        if 0 < top <= TOP_MAX:
+            t = out["top_ids"] = empty((S, top), torch.int32, dev)
+            p[3] = t.data_ptr()
+            t = out["top_logp"] = empty((S, top), f32, dev)
+            p[4] = t.data_ptr()
+        _check(load().tsp_logprobs_fwd(ctypes.byref(x), pi, id_bytes, *p, top, st), "tsp_logprobs_fwd")
+    return out
+
+
+def logprobs_bwd(logits, ids, stats, dlogp=None, entropy=None, dentropy=None, D: int = 1,
+                 scale: float = 1.0, out=None, stream=None):
+    """The gradient of sum(dlogp * logp) + sum(dentropy * entropy) for the logits
+    (their type and order), from logprobs_fwd's ``stats`` and, with ``dentropy``,
+    ``entropy``.  ``out`` may be the logits."""
+    x, pi, id_bytes, index = _logits_arg(logits, ids, D, scale)
+    one, f32 = (x.S,), torch.float32
+    ps = _arg("stats", stats, (x.S, 2), f32, index)
+    pe, pl = _arg("entropy", entropy, one, f32, index), _arg("dlogp", dlogp, one, f32, index)
+    pd = _arg("dentropy", dentropy, one, f32, index)
+    with _On(index, stream) as st:
+        if out is None:
+            out = _rows_like(logits)
+        po, ld = _rows_arg("out", out, logits.shape, logits.dtype, index)
+        _check(load().tsp_logprobs_bwd(ctypes.byref(x), pi, id_bytes, ps, pe, pl, pd, po, ld, st),
+               "tsp_logprobs_bwd")
+    return out
+
+
+def _teacher_arg(t_ids, t_logits, w_kd, t_scale, S, index):
+    """byref of a tsp_teacher, None without one."""
+    if (t_ids is None) != (t_logits is None):
+        raise ValueError("t_ids and t_logits go together")
+    if t_ids is None:
+        return None
+    if t_ids.dim() != 2:
+        raise ValueError("t_ids must be [S, K]")
+    shape = (S, t_ids.shape[1])
+    e = _enum("t_logits", t_logits.dtype)
+    return ctypes.byref(Teacher(_arg("t_ids", t_ids, shape, torch.int32, index),
+                                _arg("t_logits", t_logits, shape, t_logits.dtype, index), shape[1],
+                                t_scale, w_kd, e))
+
+
+def token_loss_fwd(logits, ids=None, t_ids=None, t_logits=None, w_ce: float = 1.0,
+                   w_kd: float = 1.0, D: int = 1, scale: float = 1.0, t_scale: float = 1.0,
+                   stats: bool = False, grad: bool = False, dloss=None, dlogits=None,
+                   stream=None) -> dict:
+    """``loss`` [S] = w_ce * (-log p of ids) + w_kd * KL(q || p), p = softmax(scale *
+    logits) and q the softmax of a teacher's t_scale * t_logits over the tokens it
+    lists: ``t_ids`` [S, K] int32 (-1: no entry) and ``t_logits`` [S, K] bf16 or fp32,
+    as logprobs_fwd's top_ids and top_logp are.  Without ids w_ce is not used,
+    without a teacher w_kd is not.  ``grad``: also ``dlogits``, the gradient of
+    sum(dloss * loss) (dloss [S] fp32, default ones), in the same pass, into
+    ``dlogits`` if that is given (it may be the logits).  ``stats``: also the [S, 2]
+    that token_loss_bwd reads.  Orders and padding as for logprobs_fwd."""
+    x, pi, id_bytes, index = _logits_arg(logits, ids, D, scale)
+    S, f32 = x.S, torch.float32
+    teacher = _teacher_arg(t_ids, t_logits, w_kd, t_scale, S, index)
+    pu = _arg("dloss", dloss, (S,), f32, index)
+    with _On(index, stream) as st:
+        loss, sums = empty((S,), f32, logits.device), empty((S, 2), f32, logits.device)
+        out, pd, ld = {"loss": loss}, None, 0
+        if stats:
+            out["stats"] = sums
+        if grad or dlogits is not None:
+            d = out["dlogits"] = _rows_like(logits) if dlogits is None else dlogits
+            pd, ld = _rows_arg("dlogits", d, logits.shape, logits.dtype, index)
+        _check(load().tsp_token_loss_fwd(ctypes.byref(x), pi, id_bytes, 0.0 if pi is None else w_ce,
+                                         teacher, loss.data_ptr(), sums.data_ptr(), pu, pd, ld, st),
+               "tsp_token_loss_fwd")
+    return out
+
+
+def token_loss_bwd(logits, stats, ids=None, t_ids=None, t_logits=None, w_ce: float = 1.0,
+                   w_kd: float = 1.0, D: int = 1, scale: float = 1.0, t_scale: float = 1.0,
+                   dloss=None, out=None, stream=None):
+    """The gradient of sum(dloss * loss) of token_loss_fwd for the logits (their type
+    and order), from its ``stats``.  ``out`` may be the logits."""
+    x, pi, id_bytes, index = _logits_arg(logits, ids, D, scale)
+    S, f32 = x.S, torch.float32
+    teacher = _teacher_arg(t_ids, t_logits, w_kd, t_scale, S, index)
+    ps, pu = _arg("stats", stats, (S, 2), f32, index), _arg("dloss", dloss, (S,), f32, index)
+    with _On(index, stream) as st:
+        if out is None:
+            out = _rows_like(logits)
+        po, ld = _rows_arg("out", out, logits.shape, logits.dtype, index)
+        _check(load().tsp_token_loss_bwd(ctypes.byref(x), pi, id_bytes, 0.0 if pi is None else w_ce,
+                                         teacher, ps, pu, po, ld, st), "tsp_token_loss_bwd")
+    return out
 
 
 def device_status(reset: bool = True, stream=None) -> int:

@@ -83,7 +83,7 @@ typedef enum {
   TSP_ERR_CUDA = 3,          /* a CUDA runtime call or launch failed               */
   TSP_ERR_TIMEOUT = 4,       /* a device pipeline wait exceeded its time limit     */
   TSP_ERR_RANGE = 5,         /* a value the bf16 path holds in fp16 was out of fp16 range,
-                                or a token id was past the embedding table */
+                                or a token id was past the embedding table or the logits */
   TSP_ERR_BOUNDS = 6         /* checked build only: a computed index failed its bounds check */
 } tsp_status;
 
@@ -653,6 +653,86 @@ typedef struct {
 tsp_status tsp_adamw_step(const tsp_adamw_tensor* tensors, int32_t count,
                           const tsp_adamw_hyper* hyper, int32_t state_bits, int32_t dtype,
                           void* stream);
+
+/* ---- Behind the stack: log probabilities and losses of tokens -----------------
+ * (not on the pages, whose block ends with y_z: what a model does with the
+ * logits that the output projection makes of it.)
+ *
+ * tsp_logits: logits [S, V] of dtype, one row a position in the zigzag order of
+ *   D ranks (D == 1: the global order, any S), rows ld >= V elements apart, each
+ *   multiplied by scale (1 / temperature, 2^-16 to 2^16); logits needs only its
+ *   element's alignment.  Elements past V are neither read nor written.
+ * Everything else is in global order, one value (or list) a position:
+ *   ids      [S], id_bytes 4 (int32) or 8 (int64): the given tokens.  id < 0:
+ *            padding -- the row is not read, its results are 0 and its gradient
+ *            is zero (its alternatives: none).  id >= V: the same, and
+ *            TSP_ERR_RANGE is recorded in the device status word.  NULL: every
+ *            row counts and there are no given tokens.
+ * With log p_j = scale (x_j - m) - l, m the row's largest logit and
+ * l = log sum_j exp(scale (x_j - m)):
+ *   logp     [S]    log p of the given token (with ids)
+ *   entropy  [S]    -sum_j p_j log p_j
+ *   stats    [S, 2] m and l, which the gradients read (log of the row's sum:
+ *            scale m + l); 0 and -inf for padding
+ *   top_ids, top_logp [S, top]: the tokens of the `top` largest logits, the
+ *            lowest of equal ones first, and their log p; -1 and -inf past the
+ *            tokens there are.  top 0 (both NULL) to TSP_TOP_MAX.
+ * A logit of -inf is a token that is left out: its p is 0, it is no alternative
+ * and its gradient is 0.  A row of nothing else has stats 0 and -inf, logp -inf,
+ * entropy 0, no alternatives and a zero gradient.  A row with NaN or +inf has
+ * no distribution: its results and gradient are NaN, its alternatives -1.
+ *
+ * tsp_logprobs_fwd: any of the above (NULL: not wanted; one at least).
+ * tsp_logprobs_bwd: the gradient of sum(dlogp * logp) + sum(dentropy * entropy):
+ *   dlogits [S, V] of dtype in the logits' order, rows ld_d apart:
+ *   scale (dlogp (delta_jt - p_j) - dentropy p_j (log p_j + entropy)).
+ *   dlogp needs ids; dentropy needs the forward's entropy; one of both is
+ *   needed.
+ *
+ * tsp_token_loss_fwd: loss[p] = w_ce (-log p_t) + teacher.weight KL(q || p), where
+ *   q is the softmax of a teacher's logits over the tokens it lists:
+ *   tsp_teacher: ids [S, K] (what tsp_logprobs_fwd has written to top_ids; -1:
+ *   no entry, also where the logit is -inf; >= V: no entry, TSP_ERR_RANGE),
+ *   logits [S, K] of its dtype (any constant may be added to a row: top_logp
+ *   serves), times scale; 1 to TSP_TOP_MAX entries, in any order; a token
+ *   listed twice counts twice.  NULL: no teacher.  A position without entries
+ *   has no second term.  A term of weight 0 is left out; w_ce != 0 needs ids.
+ *   stats [S, 2] is always written.  With dlogits the gradient is computed in
+ *   the same pass: that of sum(dloss * loss), dloss [S] or NULL for ones.
+ * tsp_token_loss_bwd: the same gradient, later, from stats:
+ *   dloss scale ((w_ce + weight) p_j - w_ce delta_jt - weight q_j).
+ * dlogits may be logits (the same address and row distance); otherwise no
+ * output may overlap another argument.  All sums and statistics are in fp32, in
+ * a fixed order: equal calls give equal bits.  No workspace.
+ * Errors: TSP_ERR_INVALID_ARG; TSP_ERR_UNSUPPORTED for S or V > 2^30 or
+ * ld > 2^32. */
+#define TSP_TOP_MAX 256
+typedef struct {
+  const void* logits;
+  int64_t ld, S, V;
+  int32_t D;
+  float scale;
+  int32_t dtype;
+} tsp_logits;
+typedef struct {
+  const int32_t* ids;
+  const void* logits;
+  int32_t K;
+  float scale, weight;
+  int32_t dtype;
+} tsp_teacher;
+tsp_status tsp_logprobs_fwd(const tsp_logits* x, const void* ids, int32_t id_bytes, float* logp,
+                            float* entropy, float* stats, int32_t* top_ids, float* top_logp,
+                            int32_t top, void* stream);
+tsp_status tsp_logprobs_bwd(const tsp_logits* x, const void* ids, int32_t id_bytes,
+                            const float* stats, const float* entropy, const float* dlogp,
+                            const float* dentropy, void* dlogits, int64_t ld_d, void* stream);
+tsp_status tsp_token_loss_fwd(const tsp_logits* x, const void* ids, int32_t id_bytes, float w_ce,
+                              const tsp_teacher* teacher, float* loss, float* stats,
+                              const float* dloss, void* dlogits, int64_t ld_d, void* stream);
+tsp_status tsp_token_loss_bwd(const tsp_logits* x, const void* ids, int32_t id_bytes, float w_ce,
+                              const tsp_teacher* teacher, const float* stats, const float* dloss,
+                              void* dlogits, int64_t ld_d, void* stream);
 
 /* Reads (and with reset != 0 clears) the sticky device status word.  Waits
  * for `stream` to finish.  Returns TSP_OK or the first device error seen
