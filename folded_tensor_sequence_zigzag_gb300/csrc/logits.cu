@@ -11,7 +11,10 @@
 //
 // A row starts at any element: it is taken as 16-byte units, the few elements in
 // front of the first and behind the last one are read by themselves.
+#include <cooperative_groups.h>
+
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -142,15 +145,17 @@ struct Row {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 
+// The CTA's largest logit and its sums relative to that, in every thread; a fixed order.
 template <bool ENT>
-__device__ __forceinline__ Row join(const Sums<ENT>& t, float low, float c2, float (*part)[3]) {
+__device__ __forceinline__ void join_sums(const Sums<ENT>& t, float low, float c2, float (*part)[4],
+                                          float* m_out, float* s_out, float* a_out) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   auto onto = [&](float m, float from, float& s, float& a) {   // sums relative to `from`, now to m
     const float d = fmaxf((from - m) * c2, kLeast), f = ex2_approx(d);
     if (ENT) a = (a + d * s) * f;
     s *= f;
   };
-  float s = t.s.x + t.s.y, a = t.a.x + t.a.y;
+  float s = t.s.x + t.s.y, a = ENT ? t.a.x + t.a.y : 0.f;
   const float mw = fmaxf(warp_max(t.top), low);
   onto(mw, t.m, s, a);
   s = warp_sum(s);
@@ -170,6 +175,14 @@ __device__ __forceinline__ Row join(const Sums<ENT>& t, float low, float c2, flo
     s += sw;
     a += aw;
   }
+  *m_out = m;
+  *s_out = s;
+  if (ENT) *a_out = a;
+}
+template <bool ENT>
+__device__ __forceinline__ Row join(const Sums<ENT>& t, float low, float c2, float (*part)[4]) {
+  float m, s, a = 0.f;
+  join_sums<ENT>(t, low, c2, part, &m, &s, &a);
   Row r;
   const bool none = s == 0.f;
   r.m = none ? 0.f : m;
@@ -405,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 2) fwd_kernel(const __grid_constant_
       for (int e = 0; e < RowUnits<T>::E / 2; ++e) sums.add(pair<T>(v[k], e), c2);
   }
   const float target = id >= 0 && (a.logp || a.t.w_ce != 0.f) ? to_f<T>(row.row[id]) : 0.f;
-  const Row x = join<ENT>(sums, low, c2, reinterpret_cast<float(*)[3]>(part));
+  const Row x = join<ENT>(sums, low, c2, part);
   const float logp = x.l == -INFINITY ? -INFINITY : a.r.scale * (target - x.m) - x.l;
   if (t == 0) {
     if (a.logp) a.logp[p] = logp;
@@ -611,6 +624,220 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
   }
 }
 
+// ---------------------------------------------------------------------------
+// Loss and gradient in one pass
+// ---------------------------------------------------------------------------
+// A row stays in shared memory between its sum and its gradient, so that it is read
+// once and written once: a CTA a row, or a cluster whose CTAs hold a part each and
+// hand each other their sums through distributed shared memory.  A thread copies
+// the units ahead that it will itself read, so that the data need no barrier.
+constexpr int kOnePassPart = 68 * 1024;    // bytes of a row a CTA: three CTAs a multiprocessor
+constexpr int kOnePassMost = 200 * 1024;   // ... of the longest rows: one
+constexpr int kOnePassAhead = 4;           // groups of two units a thread on their way
+
+__device__ __forceinline__ void copy_unit(uint4* dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_left() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+struct OnePassArgs {
+  GradArgs g;
+  float *loss, *stats;
+};
+struct OnePassSmem {
+  float part[kWarps][4], teach[kWarps][2];
+  float2 share[8];               // (largest logit, sum) of each CTA of the cluster
+  Adds adds;
+  float y[TSP_TOP_MAX], z[TSP_TOP_MAX];   // the teacher's logits, and the model's at its tokens
+  int tok[TSP_TOP_MAX];          // the teacher's tokens, -1: no entry
+  float loose[16];
+};
+
+template <typename T, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, 3) one_pass_kernel(const __grid_constant__ OnePassArgs o) {
+  constexpr int E = 16 / sizeof(T);
+  extern __shared__ uint4 seg[];
+  __shared__ OnePassSmem sm;
+  const GradArgs& a = o.g;
+  const int t = threadIdx.x, threads = blockDim.x, lane = t & 31, warp = t >> 5;
+  const int rank = CLUSTER ? (int)cooperative_groups::this_cluster().block_rank() : 0;
+  const int parts = CLUSTER ? (int)cooperative_groups::this_cluster().num_blocks() : 1;
+  const int r = CLUSTER ? blockIdx.x / parts : blockIdx.x, p = pos_of(r, a.r.c, a.r.D);
+  const bool inside = TSP_INB(p >= 0 && p < a.r.S, a.r.status);   // (the same in all CTAs of a row)
+  if (!inside) return;
+  int64_t id = -1;
+  if (a.r.ids) id = load_id(a.r.ids, a.r.id_bytes, p);
+  if (id >= a.r.V) {
+    if (t == 0) report_status(a.r.status, (int)TSP_ERR_RANGE);
+    id = -1;
+  }
+  const RowUnits<T> row(a.r.logits, a.r.ld, r, a.r.V);
+  const int per = (row.units + parts - 1) / parts;
+  const int u_lo = min(row.units, rank * per), n_u = min(row.units, u_lo + per) - u_lo;
+  const int lo = rank == 0 ? 0 : row.head + u_lo * E;
+  const int hi = rank == parts - 1 ? a.r.V : row.head + (u_lo + n_u) * E;
+  const uint4* src = row.first() + u_lo;
+  T* out = reinterpret_cast<T*>(a.out) + (int64_t)r * a.ld_out;
+  uint4* dst = reinterpret_cast<uint4*>(out + row.head) + u_lo;
+  const int j0 = t < 2 * E ? row.loose(t) : -1;
+  const bool mine = j0 >= lo && j0 < hi;   // a loose element of this part
+  bool live = !(a.r.ids && id < 0);
+  float m = 0.f, l = -INFINITY;
+  const float c = a.r.scale, c2 = c * kLog2e;
+  int K = a.t.w_kd != 0.f ? a.t.K : 0;
+  float target = 0.f;
+  if (live) {
+    // (the CTAs of a cluster have started before one writes into another's memory)
+    if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    const int groups = (per + 2 * threads - 1) / (2 * threads);
+    auto send = [&](int g) {
+      const int i = t + 2 * g * threads;
+      if (i < n_u) copy_unit(seg + i, src + i);
+      if (i + threads < n_u) copy_unit(seg + i + threads, src + i + threads);
+      copies_sent();
+    };
+    for (int g = 0; g < kOnePassAhead; ++g) send(g);
+    float x0 = -INFINITY;
+    if (mine) {
+      x0 = to_f<T>(row.row[j0]);
+      sm.loose[t] = x0;
+    }
+    if (id >= 0 && a.t.w_ce != 0.f && rank == 0) target = to_f<T>(row.row[id]);
+    if (K > 0) {
+      float y = 0.f;
+      int kid = -1;
+      if (t < K) {
+        kid = teacher_entry(a.t, a.r, p, t, &y);
+        sm.tok[t] = kid;
+        sm.y[t] = y;
+        if (rank == 0 && kid >= 0) sm.z[t] = to_f<T>(row.row[kid]);
+      }
+      const float mw = warp_max(kid >= 0 ? y : -INFINITY);
+      const float sw = warp_sum(kid >= 0 ? expf(a.t.scale * (y - mw)) : 0.f);
+      if (lane == 0) {
+        sm.teach[warp][0] = mw;
+        sm.teach[warp][1] = sw;
+      }
+    }
+    const float low = lowest<T>(), slack = kSlack / c2;
+    Sums<false> sums(low);
+    sums.see(x0, c2, slack);
+    sums.add(make_float2(x0, -INFINITY), c2);
+    for (int g = 0; g < groups; ++g) {
+      copies_left<kOnePassAhead - 1>();
+      const int i = t + 2 * g * threads;
+      uint4 v[2] = {no_unit<T>(), no_unit<T>()};
+      if (i < n_u) v[0] = seg[i];
+      if (i + threads < n_u) v[1] = seg[i + threads];
+      send(g + kOnePassAhead);
+      sums.see(largest<T, 2>(v), c2, slack);
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) sums.add(pair<T>(v[k], e), c2);
+    }
+    float s;
+    join_sums<false>(sums, low, c2, sm.part, &m, &s, nullptr);
+    if (CLUSTER) {
+      auto cluster = cooperative_groups::this_cluster();
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      if (t < parts) cluster.map_shared_rank(&sm.share[0], t)[rank] = make_float2(m, s);
+      cluster.sync();   // (also: every part's logits are read before any is overwritten)
+      m = low;
+      for (int k = 0; k < parts; ++k) m = fmaxf(m, sm.share[k].x);
+      s = 0.f;
+      for (int k = 0; k < parts; ++k)
+        s += sm.share[k].y * ex2_approx(fmaxf((sm.share[k].x - m) * c2, kLeast));
+    }
+    if (s == 0.f) m = 0.f;
+    l = s == 0.f ? -INFINITY : logf(s);
+  }
+  const bool flat = !live || l == -INFINITY;   // a zero gradient
+  float A = 0.f;
+  int n = 0;
+  if (!flat) {
+    const float up = a.up ? c * a.up[p] : c;
+    float w = a.t.w_ce;
+    if (K > 0) {
+      float mt = -INFINITY, se = 0.f;
+      for (int k = 0; k < threads / 32; ++k) mt = fmaxf(mt, sm.teach[k][0]);
+      for (int k = 0; k < threads / 32; ++k)
+        if (sm.teach[k][1] != 0.f) se += sm.teach[k][1] * expf(a.t.scale * (sm.teach[k][0] - mt));
+      if (t < K) {
+        const int kid = sm.tok[t];
+        sm.adds.id[t] = kid >= lo && kid < hi ? kid : -1;
+        sm.adds.add[t] = kid >= 0 ? -up * a.t.w_kd * (expf(a.t.scale * (sm.y[t] - mt)) / se) : 0.f;
+      }
+      if (se != 0.f) w += a.t.w_kd;
+    }
+    A = up * w;
+    n = K + 1;
+    if (t == 0) {
+      sm.adds.id[K] = id >= lo && id < hi && a.t.w_ce != 0.f ? (int)id : -1;
+      sm.adds.add[K] = -up * a.t.w_ce;
+    }
+  }
+  const float l2 = l * kLog2e;
+  auto grad = [&](float2 v) {
+    const float2 u = ffma2(fadd2(v, make_float2(-m, -m)), make_float2(c2, c2), make_float2(-l2, -l2));
+    return fmul2(make_float2(ex2_approx(u.x), ex2_approx(u.y)), make_float2(A, A));
+  };
+  if (mine) out[j0] = from_f<T>(flat ? 0.f : grad(make_float2(sm.loose[t], 0.f)).x);
+  for (int i = t; i < n_u; i += threads) {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (!flat) {
+      const uint4 v = seg[i];
+      if constexpr (sizeof(T) == 2) {
+        const float2 g0 = grad(pair<T>(v, 0)), g1 = grad(pair<T>(v, 1));
+        const float2 g2 = grad(pair<T>(v, 2)), g3 = grad(pair<T>(v, 3));
+        w = make_uint4(pack2<T>(g0.x, g0.y), pack2<T>(g1.x, g1.y), pack2<T>(g2.x, g2.y), pack2<T>(g3.x, g3.y));
+      } else {
+        const float2 g0 = grad(pair<T>(v, 0)), g1 = grad(pair<T>(v, 1));
+        w = make_uint4(__float_as_uint(g0.x), __float_as_uint(g0.y), __float_as_uint(g1.x), __float_as_uint(g1.y));
+      }
+    }
+    __stcs(dst + i, w);
+  }
+  if (!flat) {
+    __syncthreads();   // the listed tokens' values go on top of what other threads wrote
+    for (int k = t; k < n; k += threads) {
+      const int j = sm.adds.id[k];
+      if (j < 0) continue;
+      float sum = 0.f;
+      bool first = true;
+      for (int q = 0; q < n; ++q)
+        if (sm.adds.id[q] == j) {
+          sum += sm.adds.add[q];
+          first &= q >= k;
+        }
+      if (!first) continue;
+      const float x = j < row.head       ? sm.loose[j]
+                      : j >= row.tail ? sm.loose[row.head + j - row.tail]
+                                      : to_f<T>(reinterpret_cast<const T*>(seg)[j - row.head - u_lo * E]);
+      out[j] = from_f<T>(grad(make_float2(x, 0.f)).x + sum);
+    }
+  }
+  if (rank != 0) return;
+  float loss = 0.f;
+  if (live) {
+    if (a.t.w_ce != 0.f) loss = -a.t.w_ce * (l == -INFINITY ? l : c * (target - m) - l);
+    if (K > 0) {
+      const int kid = t < K ? sm.tok[t] : -1;
+      const float logp = kid >= 0 && l != -INFINITY ? c * (sm.z[t] - m) - l : -INFINITY;
+      const float2 kd = divergence(kid >= 0, kid >= 0 ? sm.y[t] : 0.f, a.t.scale, logp, sm.part);
+      if (kd.y != 0.f) loss += a.t.w_kd * kd.x;
+    }
+  }
+  if (t == 0) {
+    o.loss[p] = loss;
+    o.stats[2 * (int64_t)p] = m;
+    o.stats[2 * (int64_t)p + 1] = l;
+  }
+}
+
 Rows rows_of(const tsp_logits& x, const void* ids, int id_bytes) {
   Rows r;
   r.logits = x.logits;
@@ -660,13 +887,16 @@ tsp_status launch_fwd(const FwdArgs& a, int dtype, const char* name, cudaStream_
   return TSP_OK;
 }
 
+template <typename T>
+bool alike(const GradArgs& a) {   // rows that lie alike on 16-byte units
+  return ((uintptr_t)a.r.logits - (uintptr_t)a.out) % 16 == 0 &&
+         (a.r.S == 1 || (a.r.ld - a.ld_out) * (int64_t)sizeof(T) % 16 == 0);
+}
+
 template <typename T, bool ENT>
 void grad_t(const GradArgs& a, dim3 grid, int threads, cudaStream_t st) {
   // rows that lie alike on 16-byte units are read and written in units, others by element
-  const int64_t e = sizeof(T);
-  const bool alike = ((uintptr_t)a.r.logits - (uintptr_t)a.out) % 16 == 0 &&
-                     (a.r.S == 1 || (a.r.ld - a.ld_out) * e % 16 == 0);
-  if (alike) grad_kernel<T, ENT, 16 / (int)sizeof(T)><<<grid, threads, 0, st>>>(a);
+  if (alike<T>(a)) grad_kernel<T, ENT, 16 / (int)sizeof(T)><<<grid, threads, 0, st>>>(a);
   else grad_kernel<T, ENT, 1><<<grid, threads, 0, st>>>(a);
 }
 tsp_status launch_grad(const GradArgs& a, int dtype, const char* name, cudaStream_t st) {
@@ -682,6 +912,55 @@ tsp_status launch_grad(const GradArgs& a, int dtype, const char* name, cudaStrea
     ent ? grad_t<float, true>(a, grid, threads, st) : grad_t<float, false>(a, grid, threads, st);
   TSP_CUDA_TRY(cudaGetLastError());
   return TSP_OK;
+}
+
+// The most dynamic shared memory a kernel may be launched with, set once.
+template <auto KERNEL>
+tsp_status allow_smem(int most) {
+  static std::atomic<bool> set[kMaxDevices];
+  const int dev = current_device();
+  if (!set[dev]) {
+    TSP_CUDA_TRY(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    set[dev] = true;
+  }
+  return TSP_OK;
+}
+
+template <typename T>
+tsp_status launch_one_pass_t(const OnePassArgs& o, int parts, cudaStream_t st) {
+  const int64_t units = (int64_t)o.g.r.V * sizeof(T) / 16, per = (units + parts - 1) / parts;
+  int threads = 128;
+  while (threads < kThreads && (threads < o.g.t.K || threads * 4 <= per)) threads *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(o.g.r.S * parts));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = (size_t)per * 16;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = parts;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = parts > 1 ? 1 : 0;
+  Prof prof("token_loss_one_pass", st);
+  tsp_status r;
+  if (parts > 1) {
+    if ((r = allow_smem<one_pass_kernel<T, true>>(kOnePassMost)) != TSP_OK) return r;
+    TSP_CUDA_TRY(cudaLaunchKernelEx(&cfg, one_pass_kernel<T, true>, o));
+  } else {
+    if ((r = allow_smem<one_pass_kernel<T, false>>(kOnePassMost)) != TSP_OK) return r;
+    TSP_CUDA_TRY(cudaLaunchKernelEx(&cfg, one_pass_kernel<T, false>, o));
+  }
+  return TSP_OK;
+}
+
+// CTAs a row for the loss with its gradient: parts of 68 KB at most, 200 KB in
+// clusters of eight; for few rows more, down to 4 KB.  0: the row is too long.
+int one_pass_parts(int64_t S, int64_t units) {
+  int64_t parts = std::max<int64_t>(1, (units * 16 + kOnePassPart - 1) / kOnePassPart);
+  if (parts > 8) parts = (units + 7) / 8 * 16 <= kOnePassMost ? 8 : 0;
+  while (parts > 0 && parts <= 4 && S * parts < num_sms() && units / (2 * parts) >= 256) parts *= 2;
+  return (int)parts;
 }
 
 }  // namespace
@@ -733,6 +1012,20 @@ tsp_status launch_token_loss_bwd(const tsp_logits& x, const void* ids, int id_by
 tsp_status launch_token_loss_fwd(const tsp_logits& x, const void* ids, int id_bytes, float w_ce,
                                  const tsp_teacher* teacher, float* loss, float* stats,
                                  const float* dloss, void* dlogits, int64_t ld_d, cudaStream_t st) {
+  if (dlogits) {
+    OnePassArgs o = {};
+    o.g.r = rows_of(x, ids, id_bytes);
+    o.g.t = teacher_of(teacher, w_ce);
+    o.g.out = dlogits;
+    o.g.ld_out = ld_d;
+    o.g.up = dloss;
+    o.loss = loss;
+    o.stats = stats;
+    const bool bf = x.dtype == TSP_BF16;
+    const int parts = one_pass_parts(x.S, x.V * (bf ? 2 : 4) / 16);
+    if (parts > 0 && x.S * parts <= INT32_MAX && (bf ? alike<__nv_bfloat16>(o.g) : alike<float>(o.g)))
+      return bf ? launch_one_pass_t<__nv_bfloat16>(o, parts, st) : launch_one_pass_t<float>(o, parts, st);
+  }
   FwdArgs a = {};
   a.r = rows_of(x, ids, id_bytes);
   a.t = teacher_of(teacher, w_ce);

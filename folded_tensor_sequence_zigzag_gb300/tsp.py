@@ -1005,12 +1005,13 @@ def _logits_arg(logits, ids, D, scale):
 
 
 def _rows_like(logits):
-    """A gradient's memory: rows as far apart as the logits'."""
+    """A gradient's memory: rows as far apart as the logits' and as far from a 16-byte
+    boundary, which is how the kernels read and write them at once."""
     S, V = logits.shape
-    ld = max(logits.stride(0), V)
-    if ld == V:
+    ld, at = max(logits.stride(0), V), logits.data_ptr() % 16 // logits.element_size()
+    if ld == V and at == 0:
         return empty((S, V), logits.dtype, logits.device)
-    return empty((S * ld,), logits.dtype, logits.device).view(S, ld)[:, :V]
+    return empty((at + S * ld,), logits.dtype, logits.device)[at:].view(S, ld)[:, :V]
 
 
 def logprobs_fwd(logits, ids=None, D: int = 1, scale: float = 1.0, top: int = 0,

@@ -503,7 +503,9 @@ def test_offsets_past_32_bits():
     x = torch.as_strided(buf, (4, V), (far, 1))
     gen = torch.Generator().manual_seed(6)
     x.copy_(torch.randn(4, V, generator=gen).to(BF))
-    dense, ids = x.contiguous(), torch.arange(4, device="cuda") + V - 4
+    # (rows that lie as far from 16-byte boundaries are added up in the same order)
+    dense, ids = torch.empty(4, V + 5, dtype=BF, device="cuda")[:, :V], torch.arange(4, device="cuda") + V - 4
+    dense.copy_(x)
     a, b = (tsp.logprobs_fwd(t, ids, top=9, entropy=True, stats=True) for t in (x, dense))
     assert all(torch.equal(a[k], b[k]) for k in a)
     up = torch.ones(4, device="cuda")
