@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -166,18 +167,15 @@ __device__ __forceinline__ void join_sums(const Sums<ENT>& t, float low, float c
     part[warp][2] = a;
   }
   __syncthreads();
-  float m = part[0][0];
-  for (int w = 1; w < warps; ++w) m = fmaxf(m, part[w][0]);
-  s = a = 0.f;
-  for (int w = 0; w < warps; ++w) {
-    float sw = part[w][1], aw = part[w][2];
-    onto(m, part[w][0], sw, aw);
-    s += sw;
-    a += aw;
-  }
+  const bool one = lane < warps;   // a lane a warp
+  const float from = one ? part[lane][0] : low;
+  const float m = warp_max(from);
+  s = one ? part[lane][1] : 0.f;
+  a = ENT && one ? part[lane][2] : 0.f;
+  onto(m, from, s, a);
   *m_out = m;
-  *s_out = s;
-  if (ENT) *a_out = a;
+  *s_out = warp_sum(s);
+  if (ENT) *a_out = warp_sum(a);
 }
 template <bool ENT>
 __device__ __forceinline__ Row join(const Sums<ENT>& t, float low, float c2, float (*part)[4]) {
@@ -476,9 +474,35 @@ struct GradArgs {
 
 // What the listed tokens add: entry k < K the teacher's, entry K the given token.
 struct Adds {
-  int id[TSP_TOP_MAX + 1];
+  alignas(16) int id[TSP_TOP_MAX + 4];   // (-1 up to the next multiple of four)
   float add[TSP_TOP_MAX + 1];
 };
+__device__ __forceinline__ void end_adds(Adds& adds, int n, int t) {
+  if (t < 3) adds.id[n + t] = -1;
+}
+// An entry's token (-1: none of this part's, or not the first entry of its token) and
+// what all entries of the token add, in the order of the list.
+__device__ __forceinline__ int added(const Adds& adds, int n, int k, float* sum) {
+  const int j = adds.id[k];
+  *sum = 0.f;
+  if (j < 0) return -1;
+  int same = 0;
+  for (int q = 0; q < n; q += 4) {
+    const int4 o = *reinterpret_cast<const int4*>(adds.id + q);
+    same += (o.x == j) + (o.y == j) + (o.z == j) + (o.w == j);
+  }
+  if (same == 1) {
+    *sum = adds.add[k];
+    return j;
+  }
+  bool first = true;
+  for (int q = 0; q < n; ++q)
+    if (adds.id[q] == j) {
+      *sum += adds.add[q];
+      first &= q >= k;
+    }
+  return first ? j : -1;
+}
 
 // A part of a row a CTA: dx_j = p_j (A + B log p_j), then the listed tokens' values
 // once more with what they add (the same token twice adds twice; the first of its
@@ -560,6 +584,7 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
       }
     }
     ++n;
+    end_adds(adds, n, t);
     __syncthreads();
     for (int k = t, i = 0; k < n; k += threads, ++i)
       if (adds.id[k] >= 0) at_list[i] = to_f<T>(x[adds.id[k]]);
@@ -611,16 +636,9 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
   if (!live) return;
   __syncthreads();
   for (int k = t, i = 0; k < n; k += threads, ++i) {
-    const int j = adds.id[k];
-    if (j < 0) continue;
-    float sum = 0.f;
-    bool first = true;
-    for (int o = 0; o < n; ++o)
-      if (adds.id[o] == j) {
-        sum += adds.add[o];
-        first &= o >= k;
-      }
-    if (first) out[j] = from_f<T>(grad(make_float2(at_list[i], 0.f)).x + sum);
+    float sum;
+    const int j = added(adds, n, k, &sum);
+    if (j >= 0) out[j] = from_f<T>(grad(make_float2(at_list[i], 0.f)).x + sum);
   }
 }
 
@@ -628,213 +646,272 @@ __global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant
 // Loss and gradient in one pass
 // ---------------------------------------------------------------------------
 // A row stays in shared memory between its sum and its gradient, so that it is read
-// once and written once: a CTA a row, or a cluster whose CTAs hold a part each and
-// hand each other their sums through distributed shared memory.  A thread copies
-// the units ahead that it will itself read, so that the data need no barrier.
-constexpr int kOnePassPart = 68 * 1024;    // bytes of a row a CTA: three CTAs a multiprocessor
+// once and written once.  A CTA, or for long rows a cluster whose CTAs hold a part
+// each, takes one row after the other; its threads copy the next row's units into the
+// places whose gradient they have just written, so that reading goes on while the
+// sums are joined.  A thread copies what it will itself read: the data need no barrier.
+// Between the CTAs of a cluster go, through distributed shared memory, their sums and
+// the logits of the listed tokens.
+constexpr int kOneThreads = 256, kOneCtas = 3;
+constexpr int kOnePassPart = 66 * 1024;    // bytes of a row a CTA: three CTAs a multiprocessor
 constexpr int kOnePassMost = 200 * 1024;   // ... of the longest rows: one
-constexpr int kOnePassAhead = 4;           // groups of two units a thread on their way
 
 __device__ __forceinline__ void copy_unit(uint4* dst, const uint4* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copies_left() {
+template <int N> __device__ __forceinline__ void copies_left_c() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// until at most n (or eight) of the groups sent last are on their way
+__device__ __forceinline__ void copies_left(int n) {
+  switch (n) {
+    case 0: copies_left_c<0>(); break;
+    case 1: copies_left_c<1>(); break;
+    case 2: copies_left_c<2>(); break;
+    case 3: copies_left_c<3>(); break;
+    case 4: copies_left_c<4>(); break;
+    case 5: copies_left_c<5>(); break;
+    case 6: copies_left_c<6>(); break;
+    case 7: copies_left_c<7>(); break;
+    default: copies_left_c<8>();
+  }
 }
 
 struct OnePassArgs {
   GradArgs g;
   float *loss, *stats;
 };
+// What the CTAs of a cluster write into each other: of two rows, since one of them may
+// be a row ahead.
+struct Exchange {
+  float2 share[8];               // (largest logit, sum) of each part
+  float target, z[TSP_TOP_MAX];  // (in the first CTA) logits of the given and the teacher's tokens
+};
 struct OnePassSmem {
-  float part[kWarps][4], teach[kWarps][2];
-  float2 share[8];               // (largest logit, sum) of each CTA of the cluster
-  Adds adds;
-  float y[TSP_TOP_MAX], z[TSP_TOP_MAX];   // the teacher's logits, and the model's at its tokens
-  int tok[TSP_TOP_MAX];          // the teacher's tokens, -1: no entry
+  float part[kOneThreads / 32][4], teach[kOneThreads / 32][2];
+  Exchange ex[2];
+  Adds adds;                     // of this part
+  float z[TSP_TOP_MAX + 1];      // the listed tokens' logits
+  float q[TSP_TOP_MAX], logq[TSP_TOP_MAX];
   float loose[16];
 };
 
 template <typename T, bool CLUSTER>
-__global__ void __launch_bounds__(kThreads, 3) one_pass_kernel(const __grid_constant__ OnePassArgs o) {
-  constexpr int E = 16 / sizeof(T);
+__global__ void __launch_bounds__(kOneThreads, kOneCtas) one_pass_kernel(const __grid_constant__ OnePassArgs o) {
+  constexpr int E = 16 / sizeof(T), U = 4;
   extern __shared__ uint4 seg[];
   __shared__ OnePassSmem sm;
   const GradArgs& a = o.g;
   const int t = threadIdx.x, threads = blockDim.x, lane = t & 31, warp = t >> 5;
-  const int rank = CLUSTER ? (int)cooperative_groups::this_cluster().block_rank() : 0;
-  const int parts = CLUSTER ? (int)cooperative_groups::this_cluster().num_blocks() : 1;
-  const int r = CLUSTER ? blockIdx.x / parts : blockIdx.x, p = pos_of(r, a.r.c, a.r.D);
-  const bool inside = TSP_INB(p >= 0 && p < a.r.S, a.r.status);   // (the same in all CTAs of a row)
-  if (!inside) return;
-  int64_t id = -1;
-  if (a.r.ids) id = load_id(a.r.ids, a.r.id_bytes, p);
-  if (id >= a.r.V) {
-    if (t == 0) report_status(a.r.status, (int)TSP_ERR_RANGE);
-    id = -1;
-  }
-  const RowUnits<T> row(a.r.logits, a.r.ld, r, a.r.V);
-  const int per = (row.units + parts - 1) / parts;
-  const int u_lo = min(row.units, rank * per), n_u = min(row.units, u_lo + per) - u_lo;
-  const int lo = rank == 0 ? 0 : row.head + u_lo * E;
-  const int hi = rank == parts - 1 ? a.r.V : row.head + (u_lo + n_u) * E;
-  const uint4* src = row.first() + u_lo;
-  T* out = reinterpret_cast<T*>(a.out) + (int64_t)r * a.ld_out;
-  uint4* dst = reinterpret_cast<uint4*>(out + row.head) + u_lo;
-  const int j0 = t < 2 * E ? row.loose(t) : -1;
-  const bool mine = j0 >= lo && j0 < hi;   // a loose element of this part
-  bool live = !(a.r.ids && id < 0);
-  float m = 0.f, l = -INFINITY;
-  const float c = a.r.scale, c2 = c * kLog2e;
-  int K = a.t.w_kd != 0.f ? a.t.K : 0;
-  float target = 0.f;
-  if (live) {
-    // (the CTAs of a cluster have started before one writes into another's memory)
-    if (CLUSTER) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    const int groups = (per + 2 * threads - 1) / (2 * threads);
-    auto send = [&](int g) {
-      const int i = t + 2 * g * threads;
-      if (i < n_u) copy_unit(seg + i, src + i);
-      if (i + threads < n_u) copy_unit(seg + i + threads, src + i + threads);
-      copies_sent();
-    };
-    for (int g = 0; g < kOnePassAhead; ++g) send(g);
-    float x0 = -INFINITY;
-    if (mine) {
-      x0 = to_f<T>(row.row[j0]);
-      sm.loose[t] = x0;
-    }
-    if (id >= 0 && a.t.w_ce != 0.f && rank == 0) target = to_f<T>(row.row[id]);
-    if (K > 0) {
+  const auto cluster = cooperative_groups::this_cluster();
+  const int rank = CLUSTER ? (int)cluster.block_rank() : 0;
+  const int parts = CLUSTER ? (int)cluster.num_blocks() : 1;
+  const int stride = gridDim.x / parts;
+  const float c = a.r.scale, c2 = c * kLog2e, low = lowest<T>(), slack = kSlack / c2;
+  const int K = a.t.w_kd != 0.f ? a.t.K : 0;
+  // the units of a row that are this part's
+  struct Part {
+    const uint4* src;
+    int u_lo, n;
+  };
+  auto part_of = [&](const RowUnits<T>& row) {
+    const int per = (row.units + parts - 1) / parts, u_lo = min(row.units, rank * per);
+    return Part{row.first() + u_lo, u_lo, min(row.units, u_lo + per) - u_lo};
+  };
+  auto given = [&](int r) {   // a row's token: -1 for padding, -2 without tokens
+    if (r >= a.r.S || !a.r.ids) return -2;
+    const int64_t id = load_id(a.r.ids, a.r.id_bytes, pos_of(r, a.r.c, a.r.D));
+    if (id >= a.r.V && t == 0) report_status(a.r.status, (int)TSP_ERR_RANGE);
+    return id >= 0 && id < a.r.V ? (int)id : -1;
+  };
+  // the copies of a row's units i + k * threads, k < U
+  auto send = [&](const Part& x, int i) {
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (i + k * threads < x.n) copy_unit(seg + i + k * threads, x.src + i + k * threads);
+    copies_sent();
+  };
+  const int most = (a.r.V / E + parts - 1) / parts;      // units of a part at most
+  const int groups = (most + U * threads - 1) / (U * threads);
+  int r = CLUSTER ? blockIdx.x / parts : blockIdx.x;
+  int id = given(r);
+  // (the CTAs of a cluster have started before one writes into another's memory)
+  if (CLUSTER) cluster.sync();
+  bool there = false;   // this row's copies have been sent
+  for (int turn = 0; r < a.r.S; r += stride) {
+    const int p = pos_of(r, a.r.c, a.r.D);
+    if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
+    const bool live = id != -1;
+    const RowUnits<T> row(a.r.logits, a.r.ld, r, a.r.V);
+    const Part x = part_of(row);
+    const int lo = rank == 0 ? 0 : row.head + x.u_lo * E;
+    const int hi = rank == parts - 1 ? a.r.V : row.head + (x.u_lo + x.n) * E;
+    T* out = reinterpret_cast<T*>(a.out) + (int64_t)r * a.ld_out;
+    uint4* dst = reinterpret_cast<uint4*>(out + row.head) + x.u_lo;
+    const int j0 = t < 2 * E ? row.loose(t) : -1;
+    const bool mine = j0 >= lo && j0 < hi;   // a loose element of this part
+    const int id_next = given(r + stride);
+    Exchange& ex = sm.ex[turn];
+    float m = 0.f, l = -INFINITY, A = 0.f, x0 = -INFINITY;
+    int n = 0;
+    if (live) {
+      if (!there)
+        for (int g = 0; g < groups; ++g) send(x, t + U * g * threads);
+      if (mine) x0 = to_f<T>(row.row[j0]);
       float y = 0.f;
       int kid = -1;
-      if (t < K) {
-        kid = teacher_entry(a.t, a.r, p, t, &y);
-        sm.tok[t] = kid;
-        sm.y[t] = y;
-        if (rank == 0 && kid >= 0) sm.z[t] = to_f<T>(row.row[kid]);
-      }
-      const float mw = warp_max(kid >= 0 ? y : -INFINITY);
-      const float sw = warp_sum(kid >= 0 ? expf(a.t.scale * (y - mw)) : 0.f);
-      if (lane == 0) {
-        sm.teach[warp][0] = mw;
-        sm.teach[warp][1] = sw;
-      }
-    }
-    const float low = lowest<T>(), slack = kSlack / c2;
-    Sums<false> sums(low);
-    sums.see(x0, c2, slack);
-    sums.add(make_float2(x0, -INFINITY), c2);
-    for (int g = 0; g < groups; ++g) {
-      copies_left<kOnePassAhead - 1>();
-      const int i = t + 2 * g * threads;
-      uint4 v[2] = {no_unit<T>(), no_unit<T>()};
-      if (i < n_u) v[0] = seg[i];
-      if (i + threads < n_u) v[1] = seg[i + threads];
-      send(g + kOnePassAhead);
-      sums.see(largest<T, 2>(v), c2, slack);
+      if (t < K) kid = teacher_entry(a.t, a.r, p, t, &y);
+      const float up = a.up ? a.up[p] : 1.f;
+      Sums<false> sums(low);
+      for (int g = 0; g < groups; ++g) {
+        copies_left(groups - 1 - g);
+        const int i = t + U * g * threads;
+        if (i + (U - 1) * threads < x.n) {
+          uint4 v[U];
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+          for (int k = 0; k < U; ++k) v[k] = seg[i + k * threads];
+          sums.see(largest<T, U>(v), c2, slack);
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) sums.add(pair<T>(v[k], e), c2);
-    }
-    float s;
-    join_sums<false>(sums, low, c2, sm.part, &m, &s, nullptr);
-    if (CLUSTER) {
-      auto cluster = cooperative_groups::this_cluster();
-      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-      if (t < parts) cluster.map_shared_rank(&sm.share[0], t)[rank] = make_float2(m, s);
-      cluster.sync();   // (also: every part's logits are read before any is overwritten)
-      m = low;
-      for (int k = 0; k < parts; ++k) m = fmaxf(m, sm.share[k].x);
-      s = 0.f;
-      for (int k = 0; k < parts; ++k)
-        s += sm.share[k].y * ex2_approx(fmaxf((sm.share[k].x - m) * c2, kLeast));
-    }
-    if (s == 0.f) m = 0.f;
-    l = s == 0.f ? -INFINITY : logf(s);
-  }
-  const bool flat = !live || l == -INFINITY;   // a zero gradient
-  float A = 0.f;
-  int n = 0;
-  if (!flat) {
-    const float up = a.up ? c * a.up[p] : c;
-    float w = a.t.w_ce;
-    if (K > 0) {
-      float mt = -INFINITY, se = 0.f;
-      for (int k = 0; k < threads / 32; ++k) mt = fmaxf(mt, sm.teach[k][0]);
-      for (int k = 0; k < threads / 32; ++k)
-        if (sm.teach[k][1] != 0.f) se += sm.teach[k][1] * expf(a.t.scale * (sm.teach[k][0] - mt));
-      if (t < K) {
-        const int kid = sm.tok[t];
-        sm.adds.id[t] = kid >= lo && kid < hi ? kid : -1;
-        sm.adds.add[t] = kid >= 0 ? -up * a.t.w_kd * (expf(a.t.scale * (sm.y[t] - mt)) / se) : 0.f;
-      }
-      if (se != 0.f) w += a.t.w_kd;
-    }
-    A = up * w;
-    n = K + 1;
-    if (t == 0) {
-      sm.adds.id[K] = id >= lo && id < hi && a.t.w_ce != 0.f ? (int)id : -1;
-      sm.adds.add[K] = -up * a.t.w_ce;
-    }
-  }
-  const float l2 = l * kLog2e;
-  auto grad = [&](float2 v) {
-    const float2 u = ffma2(fadd2(v, make_float2(-m, -m)), make_float2(c2, c2), make_float2(-l2, -l2));
-    return fmul2(make_float2(ex2_approx(u.x), ex2_approx(u.y)), make_float2(A, A));
-  };
-  if (mine) out[j0] = from_f<T>(flat ? 0.f : grad(make_float2(sm.loose[t], 0.f)).x);
-  for (int i = t; i < n_u; i += threads) {
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (!flat) {
-      const uint4 v = seg[i];
-      if constexpr (sizeof(T) == 2) {
-        const float2 g0 = grad(pair<T>(v, 0)), g1 = grad(pair<T>(v, 1));
-        const float2 g2 = grad(pair<T>(v, 2)), g3 = grad(pair<T>(v, 3));
-        w = make_uint4(pack2<T>(g0.x, g0.y), pack2<T>(g1.x, g1.y), pack2<T>(g2.x, g2.y), pack2<T>(g3.x, g3.y));
-      } else {
-        const float2 g0 = grad(pair<T>(v, 0)), g1 = grad(pair<T>(v, 1));
-        w = make_uint4(__float_as_uint(g0.x), __float_as_uint(g0.y), __float_as_uint(g1.x), __float_as_uint(g1.y));
-      }
-    }
-    __stcs(dst + i, w);
-  }
-  if (!flat) {
-    __syncthreads();   // the listed tokens' values go on top of what other threads wrote
-    for (int k = t; k < n; k += threads) {
-      const int j = sm.adds.id[k];
-      if (j < 0) continue;
-      float sum = 0.f;
-      bool first = true;
-      for (int q = 0; q < n; ++q)
-        if (sm.adds.id[q] == j) {
-          sum += sm.adds.add[q];
-          first &= q >= k;
+          for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) sums.add(pair<T>(v[k], e), c2);
+        } else {
+          for (int k = i; k < x.n; k += threads) {
+            const uint4 v[1] = {seg[k]};
+            sums.see(largest<T, 1>(v), c2, slack);
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) sums.add(pair<T>(v[0], e), c2);
+          }
         }
-      if (!first) continue;
-      const float x = j < row.head       ? sm.loose[j]
-                      : j >= row.tail ? sm.loose[row.head + j - row.tail]
-                                      : to_f<T>(reinterpret_cast<const T*>(seg)[j - row.head - u_lo * E]);
-      out[j] = from_f<T>(grad(make_float2(x, 0.f)).x + sum);
+      }
+      sums.see(x0, c2, slack);
+      sums.add(make_float2(x0, -INFINITY), c2);
+      if (mine) sm.loose[t] = x0;
+      if (K > 0) {
+        const float mw = warp_max(kid >= 0 ? y : -INFINITY);
+        const float sw = warp_sum(kid >= 0 ? expf(a.t.scale * (y - mw)) : 0.f);
+        if (lane == 0) {
+          sm.teach[warp][0] = mw;
+          sm.teach[warp][1] = sw;
+        }
+      }
+      float s;
+      join_sums<false>(sums, low, c2, sm.part, &m, &s, nullptr);
+      // every logit of this part is in shared memory: hand on the listed ones
+      auto logit = [&](int j) {
+        return j < row.head    ? sm.loose[j]
+               : j >= row.tail ? sm.loose[row.head + j - row.tail]
+                               : to_f<T>(reinterpret_cast<const T*>(seg)[j - row.head - x.u_lo * E]);
+      };
+      Exchange* first = CLUSTER ? cluster.map_shared_rank(&ex, 0) : &ex;
+      const bool here = kid >= lo && kid < hi, given_here = id >= lo && id < hi;
+      if (here) first->z[t] = sm.z[t] = logit(kid);
+      if (t == 0 && given_here) first->target = sm.z[K] = logit(id);
+      if (CLUSTER) {
+        if (t < parts) cluster.map_shared_rank(&ex, t)->share[rank] = make_float2(m, s);
+        cluster.sync();
+        m = low;
+        for (int k = 0; k < parts; ++k) m = fmaxf(m, ex.share[k].x);
+        s = 0.f;
+        for (int k = 0; k < parts; ++k)
+          s += ex.share[k].y * ex2_approx(fmaxf((ex.share[k].x - m) * c2, kLeast));
+      }
+      if (s == 0.f) m = 0.f;
+      l = s == 0.f ? -INFINITY : logf(s);
+      float w = a.t.w_ce;
+      if (K > 0) {
+        const float from = lane < threads / 32 ? sm.teach[lane][0] : -INFINITY, mt = warp_max(from);
+        float se = lane < threads / 32 ? sm.teach[lane][1] : 0.f;
+        if (se != 0.f) se *= expf(a.t.scale * (from - mt));
+        se = warp_sum(se);
+        if (t < K) {
+          const float logq = a.t.scale * (y - mt) - logf(se), q = kid >= 0 ? expf(a.t.scale * (y - mt)) / se : 0.f;
+          sm.q[t] = q;
+          sm.logq[t] = logq;
+          sm.adds.id[t] = here ? kid : -1;
+          sm.adds.add[t] = -up * c * a.t.w_kd * q;
+        }
+        if (se != 0.f) w += a.t.w_kd;
+      }
+      if (t == 0) {
+        sm.adds.id[K] = given_here && a.t.w_ce != 0.f ? id : -1;
+        sm.adds.add[K] = -up * c * a.t.w_ce;
+      }
+      end_adds(sm.adds, K + 1, t);
+      A = up * c * w;
+      n = l == -INFINITY ? 0 : K + 1;
+      if (!CLUSTER) __syncthreads();   // (the listed logits are read before the next row comes in)
     }
-  }
-  if (rank != 0) return;
-  float loss = 0.f;
-  if (live) {
-    if (a.t.w_ce != 0.f) loss = -a.t.w_ce * (l == -INFINITY ? l : c * (target - m) - l);
-    if (K > 0) {
-      const int kid = t < K ? sm.tok[t] : -1;
-      const float logp = kid >= 0 && l != -INFINITY ? c * (sm.z[t] - m) - l : -INFINITY;
-      const float2 kd = divergence(kid >= 0, kid >= 0 ? sm.y[t] : 0.f, a.t.scale, logp, sm.part);
-      if (kd.y != 0.f) loss += a.t.w_kd * kd.x;
+    const bool flat = !live || l == -INFINITY;   // a zero gradient
+    const float l2 = l * kLog2e;
+    auto grad = [&](float2 v) {
+      const float2 u = ffma2(fadd2(v, make_float2(-m, -m)), make_float2(c2, c2), make_float2(-l2, -l2));
+      return fmul2(make_float2(ex2_approx(u.x), ex2_approx(u.y)), make_float2(A, A));
+    };
+    if (mine) out[j0] = from_f<T>(flat ? 0.f : grad(make_float2(x0, 0.f)).x);
+    there = r + stride < a.r.S && id_next != -1;
+    Part next = {nullptr, 0, 0};
+    if (there) next = part_of(RowUnits<T>(a.r.logits, a.r.ld, r + stride, a.r.V));
+    auto put_unit = [&](int i) {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (!flat) {
+        const uint4 v = seg[i];
+        if constexpr (sizeof(T) == 2) {
+          const float2 g0 = grad(pair<T>(v, 0)), g1 = grad(pair<T>(v, 1));
+          const float2 g2 = grad(pair<T>(v, 2)), g3 = grad(pair<T>(v, 3));
+          w = make_uint4(pack2<T>(g0.x, g0.y), pack2<T>(g1.x, g1.y), pack2<T>(g2.x, g2.y),
+                         pack2<T>(g3.x, g3.y));
+        } else {
+          const float2 g0 = grad(pair<T>(v, 0)), g1 = grad(pair<T>(v, 1));
+          w = make_uint4(__float_as_uint(g0.x), __float_as_uint(g0.y), __float_as_uint(g1.x),
+                         __float_as_uint(g1.y));
+        }
+      }
+      __stcs(dst + i, w);
+    };
+    for (int g = 0; g < groups; ++g) {
+      const int i0 = t + U * g * threads;
+      if (i0 + (U - 1) * threads < x.n) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) put_unit(i0 + k * threads);
+      } else {
+        for (int i = i0; i < x.n; i += threads) put_unit(i);
+      }
+      if (there) send(next, i0);
     }
-  }
-  if (t == 0) {
-    o.loss[p] = loss;
-    o.stats[2 * (int64_t)p] = m;
-    o.stats[2 * (int64_t)p + 1] = l;
+    if (live) {
+      __syncthreads();   // the listed tokens' values go on top of what other threads wrote
+      auto put = [&](int k) {
+        float sum;
+        const int j = added(sm.adds, n, k, &sum);
+        if (j >= 0) out[j] = from_f<T>(grad(make_float2(sm.z[k], 0.f)).x + sum);
+      };
+      if (t < K && n > 0) put(t);
+      if (t == 0 && n > 0) put(K);
+    }
+    if (rank == 0 && warp == 0) {
+      float loss = 0.f;
+      if (live) {
+        if (a.t.w_ce != 0.f && id >= 0) loss = -a.t.w_ce * (l == -INFINITY ? l : c * (ex.target - m) - l);
+        float kd = 0.f;
+        bool any = false;
+        for (int k = lane; k < K; k += 32) {
+          const float q = sm.q[k];
+          any |= q != 0.f;
+          if (q != 0.f) kd += q * (sm.logq[k] - (l == -INFINITY ? l : c * (ex.z[k] - m) - l));
+        }
+        kd = warp_sum(kd);
+        if (__any_sync(0xffffffffu, any)) loss += a.t.w_kd * kd;
+      }
+      if (lane == 0) {
+        o.loss[p] = loss;
+        o.stats[2 * (int64_t)p] = m;
+        o.stats[2 * (int64_t)p + 1] = l;
+      }
+    }
+    if (live) turn ^= 1;
+    id = id_next;
   }
 }
 
@@ -926,13 +1003,41 @@ tsp_status allow_smem(int most) {
   return TSP_OK;
 }
 
-template <typename T>
-tsp_status launch_one_pass_t(const OnePassArgs& o, int parts, cudaStream_t st) {
-  const int64_t units = (int64_t)o.g.r.V * sizeof(T) / 16, per = (units + parts - 1) / parts;
+// How many clusters (CTAs, if those are alone) of a launch the GPU holds at once,
+// looked up once for each kind of launch: a persistent grid takes as many.
+int64_t resident(const void* kernel, const cudaLaunchConfig_t& cfg, int parts) {
+  struct Known {
+    const void* kernel;
+    size_t smem;
+    int dev, parts, threads, n;
+  };
+  static std::mutex mu;
+  static Known known[32];   // (the oldest gives way)
+  static unsigned at = 0;
+  const int dev = current_device(), threads = (int)cfg.blockDim.x;
+  std::lock_guard<std::mutex> lk(mu);
+  for (const Known& k : known)
+    if (k.kernel == kernel && k.smem == cfg.dynamicSmemBytes && k.dev == dev && k.parts == parts && k.threads == threads)
+      return k.n;
+  int n = 0;
+  if (parts > 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+  } else if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, cfg.dynamicSmemBytes) == cudaSuccess) {
+    n *= num_sms();
+  } else {
+    n = 0;
+  }
+  n = n > 0 ? n : std::max(1, num_sms() / parts);
+  known[at++ % 32] = {kernel, cfg.dynamicSmemBytes, dev, parts, threads, n};
+  return n;
+}
+
+template <typename T, bool CLUSTER>
+tsp_status launch_one_pass_c(const OnePassArgs& o, int parts, cudaStream_t st) {
+  const int64_t per = ((int64_t)o.g.r.V * sizeof(T) / 16 + parts - 1) / parts;
   int threads = 128;
-  while (threads < kThreads && (threads < o.g.t.K || threads * 4 <= per)) threads *= 2;
+  while (threads < kOneThreads && (threads < o.g.t.K || threads * 4 <= per)) threads *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(o.g.r.S * parts));
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = (size_t)per * 16;
   cfg.stream = st;
@@ -941,20 +1046,22 @@ tsp_status launch_one_pass_t(const OnePassArgs& o, int parts, cudaStream_t st) {
   at[0].val.clusterDim.x = parts;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = parts > 1 ? 1 : 0;
+  cfg.numAttrs = CLUSTER ? 1 : 0;
+  constexpr auto kernel = one_pass_kernel<T, CLUSTER>;
+  const tsp_status r = allow_smem<kernel>(kOnePassMost);
+  if (r != TSP_OK) return r;
+  cfg.gridDim = dim3((unsigned)parts);
+  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(o.g.r.S, resident((const void*)kernel, cfg, parts)) * parts));
   Prof prof("token_loss_one_pass", st);
-  tsp_status r;
-  if (parts > 1) {
-    if ((r = allow_smem<one_pass_kernel<T, true>>(kOnePassMost)) != TSP_OK) return r;
-    TSP_CUDA_TRY(cudaLaunchKernelEx(&cfg, one_pass_kernel<T, true>, o));
-  } else {
-    if ((r = allow_smem<one_pass_kernel<T, false>>(kOnePassMost)) != TSP_OK) return r;
-    TSP_CUDA_TRY(cudaLaunchKernelEx(&cfg, one_pass_kernel<T, false>, o));
-  }
+  TSP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, o));
   return TSP_OK;
 }
+template <typename T>
+tsp_status launch_one_pass_t(const OnePassArgs& o, int parts, cudaStream_t st) {
+  return parts > 1 ? launch_one_pass_c<T, true>(o, parts, st) : launch_one_pass_c<T, false>(o, parts, st);
+}
 
-// CTAs a row for the loss with its gradient: parts of 68 KB at most, 200 KB in
+// CTAs a row for the loss with its gradient: parts of 66 KB at most, 200 KB in
 // clusters of eight; for few rows more, down to 4 KB.  0: the row is too long.
 int one_pass_parts(int64_t S, int64_t units) {
   int64_t parts = std::max<int64_t>(1, (units * 16 + kOnePassPart - 1) / kOnePassPart);
@@ -1023,7 +1130,7 @@ tsp_status launch_token_loss_fwd(const tsp_logits& x, const void* ids, int id_by
     o.stats = stats;
     const bool bf = x.dtype == TSP_BF16;
     const int parts = one_pass_parts(x.S, x.V * (bf ? 2 : 4) / 16);
-    if (parts > 0 && x.S * parts <= INT32_MAX && (bf ? alike<__nv_bfloat16>(o.g) : alike<float>(o.g)))
+    if (parts > 0 && (bf ? alike<__nv_bfloat16>(o.g) : alike<float>(o.g)))
       return bf ? launch_one_pass_t<__nv_bfloat16>(o, parts, st) : launch_one_pass_t<float>(o, parts, st);
   }
   FwdArgs a = {};
