@@ -5,12 +5,22 @@
 //   l = log sum_j exp(c (x_j - m)),   log p_j = c (x_j - m) - l,
 //   H = -sum_j p_j log p_j = l - sum_j p_j c (x_j - m)
 //   loss = w_ce (-log p_t) + w_kd sum_k q_k (log q_k - log p_{id_k}),  q = softmax_k(t_scale * teacher)
-//   dx_j = p_j (A + B log p_j) + what the listed tokens add at j
-// (A, B and the additions in grad_kernel).  Everything is bound by HBM: the
-// forward reads the rows once, the gradient reads and writes them once.
+//   dx_j = p_j (A + B log2 p_j) + what the listed tokens add at j
+// (A, B and the additions in the gradients' kernels).  The work is bound by HBM: the
+// forward reads the rows once, the gradient reads and writes them once.  At its rate a
+// multiprocessor has about eleven issue slots for a bf16 logit that is read, 22 for
+// one that is read and written, so instructions are counted here.
+//
+// exp(c x) is taken as 2^(c2 x - R), c2 = c log2(e), with a whole number R near the
+// largest c2 x: one fused multiply-add, whose only rounding is that of the small
+// difference.  The differences of logits are then as exact as fp32 holds them however
+// large the logits are, and sums move from one R to another by powers of two.
 //
 // A row starts at any element: it is taken as 16-byte units, the few elements in
-// front of the first and behind the last one are read by themselves.
+// front of the first and behind the last one are read by themselves.  A CTA, or a
+// cluster whose CTAs hold a part each, takes one row after the other; a thread copies
+// the units that it will itself read ahead into shared memory, so that the data need
+// no barrier and reading goes on while the sums of a row are joined.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -30,54 +40,132 @@ constexpr float kLeast = -1024.f;
 // A running reference is renewed once a logit is this far (in powers of 2) above it:
 // sums then stay below V * 2^8, and renewals are rare.
 constexpr float kSlack = 8.f;
+// Whole numbers and half of their rounding fit fp32 below this: rows whose |c2 m| is not
+// are added up once more as 2^(c2 (x - m)).
+constexpr float kFar = 0x1p24f;
 
-__device__ __forceinline__ int64_t load_id(const void* ids, int id_bytes, int64_t p) {
-  return id_bytes == 8 ? (int64_t)reinterpret_cast<const long long*>(ids)[p]
-                       : (int64_t)reinterpret_cast<const int*>(ids)[p];
+constexpr int kMostThreads = 256;   // of a CTA; 128 for short rows
+constexpr int kGroup = 4;           // units of a thread that are sent for and worked on together
+
+// ---------------------------------------------------------------------------
+// Two values an instruction
+// ---------------------------------------------------------------------------
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 two(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 fma_two(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 add_two(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul_two(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 ex2_two(f2 u) {
+  const float2 v = both(u);
+  return two(ex2_approx(v.x), ex2_approx(v.y));
+}
+__device__ __forceinline__ f2 not_least(f2 u) {
+  const float2 v = both(u);
+  return two(fmaxf(v.x, kLeast), fmaxf(v.y, kLeast));
+}
+// The largest value of the warp's lanes (NaN does not count).
+__device__ __forceinline__ float lanes_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+template <int N>   // over N lanes that lie next to each other
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = N / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
-__device__ __forceinline__ int pos_of(int row, int c, int D) {
-  return D == 1 ? row : (int)zz_pos_of_row(row, c, D);
-}
-
-template <typename T> __device__ __forceinline__ float lowest();
-template <> __device__ __forceinline__ float lowest<float>() { return -3.4028234663852886e38f; }
-template <> __device__ __forceinline__ float lowest<__nv_bfloat16>() { return -3.3895313892515355e38f; }
-
-// A row as 16-byte units: `head` elements in front of the first, `units` of them,
-// and the elements from `tail` on behind the last.
-template <typename T>
-struct RowUnits {
-  static constexpr int E = 16 / sizeof(T);
-  const T* row;
-  int head, units, tail, V;
-  __device__ RowUnits(const void* base, int64_t ld, int64_t r, int v) {
-    row = reinterpret_cast<const T*>(base) + r * ld;
-    V = v;
-    head = min(v, (int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(T));
-    units = (v - head) / E;
-    tail = head + units * E;
-  }
-  __device__ const uint4* first() const { return reinterpret_cast<const uint4*>(row + head); }
-  // the n-th element outside the units, -1 behind the last of them
-  __device__ int loose(int n) const { return n < head ? n : (tail + n - head < V ? tail + n - head : -1); }
+// ---------------------------------------------------------------------------
+// Rows
+// ---------------------------------------------------------------------------
+struct Rows {
+  const void* logits;
+  int64_t ld;
+  const void* ids;     // may be NULL
+  int id_bytes, S, c, D, V;
+  float scale;
+  int* status;
 };
 
-template <typename T> __device__ __forceinline__ float2 pair(uint4 u, int i);
-template <> __device__ __forceinline__ float2 pair<__nv_bfloat16>(uint4 u, int i) {
+// Position of a row, 32-bit (S is at most 2^30).
+__device__ __forceinline__ int pos_of(const Rows& a, int row) {
+  if (a.D == 1) return row;
+  const int r = (unsigned)row / (2u * a.c), rest = row - r * 2 * a.c;
+  return rest < a.c ? r * a.c + rest : (2 * a.D - 1 - r) * a.c + rest - a.c;
+}
+// A row's given token: -1 for padding, -2 where there are no tokens or no such row.
+__device__ __forceinline__ int given(const Rows& a, int row) {
+  if (row >= a.S || !a.ids) return -2;
+  const int p = pos_of(a, row);
+  const int64_t id = a.id_bytes == 8 ? (int64_t)reinterpret_cast<const long long*>(a.ids)[p]
+                                     : (int64_t)reinterpret_cast<const int*>(a.ids)[p];
+  if (id >= a.V && threadIdx.x == 0) report_status(a.status, (int)TSP_ERR_RANGE);
+  return id >= 0 && id < a.V ? (int)id : -1;
+}
+
+// A row as 16-byte units: `head` elements in front of the first, `units` of them,
+// and the elements from `tail` on behind the last.  A part of it (one of `parts`) has
+// the n units from u_lo on and the elements [lo, hi).
+template <typename T>
+struct RowPart {
+  static constexpr int E = 16 / sizeof(T);
+  const T* row;
+  const uint4* src;
+  int head, units, tail, V, u_lo, n, lo, hi;
+  __device__ __forceinline__ RowPart(const Rows& a, int r, int rank, int parts) {
+    row = reinterpret_cast<const T*>(a.logits) + (int64_t)r * a.ld;
+    V = a.V;
+    head = min(V, (int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(T));
+    units = (V - head) / E;
+    tail = head + units * E;
+    const int per = parts == 1 ? units : (int)((unsigned)(units + parts - 1) / (unsigned)parts);
+    u_lo = min(units, rank * per);
+    n = min(units, u_lo + per) - u_lo;
+    lo = rank == 0 ? 0 : head + u_lo * E;
+    hi = rank == parts - 1 ? V : head + (u_lo + n) * E;
+    src = reinterpret_cast<const uint4*>(row + head) + u_lo;
+  }
+  // the k-th element outside the units if it is this part's, else -1
+  __device__ __forceinline__ int loose(int k) const {
+    const int j = k < head ? k : tail + k - head;
+    return k < 2 * E && j >= lo && j < hi ? j : -1;
+  }
+};
+
+template <typename T> __device__ __forceinline__ f2 pair(const uint4& u, int i);
+template <> __device__ __forceinline__ f2 pair<__nv_bfloat16>(const uint4& u, int i) {
   const uint32_t w = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
-  return make_float2(bf16_lo(w), bf16_hi(w));
+  return two(bf16_lo(w), bf16_hi(w));
 }
-template <> __device__ __forceinline__ float2 pair<float>(uint4 u, int i) {
-  return i == 0 ? make_float2(__uint_as_float(u.x), __uint_as_float(u.y))
-                : make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+template <> __device__ __forceinline__ f2 pair<float>(const uint4& u, int i) {
+  return i == 0 ? two(__uint_as_float(u.x), __uint_as_float(u.y))
+                : two(__uint_as_float(u.z), __uint_as_float(u.w));
 }
-template <typename T> __device__ __forceinline__ uint4 no_unit();   // -inf throughout
-template <> __device__ __forceinline__ uint4 no_unit<__nv_bfloat16>() {
-  return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-}
-template <> __device__ __forceinline__ uint4 no_unit<float>() {
-  return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+template <typename T> __device__ __forceinline__ uint4 no_unit() {   // -inf throughout
+  const uint32_t w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+  return make_uint4(w, w, w, w);
 }
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -87,9 +175,9 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
 // The largest of N units; NaN does not count.
 template <typename T, int N> __device__ __forceinline__ float largest(const uint4 (&u)[N]) {
   if constexpr (sizeof(T) == 2) {
-    uint32_t m = 0xff80ff80u;
+    uint32_t m = max_bf16x2(max_bf16x2(u[0].x, u[0].y), max_bf16x2(u[0].z, u[0].w));
 #pragma unroll
-    for (int k = 0; k < N; ++k)
+    for (int k = 1; k < N; ++k)
       m = max_bf16x2(m, max_bf16x2(max_bf16x2(u[k].x, u[k].y), max_bf16x2(u[k].z, u[k].w)));
     return fmaxf(bf16_lo(m), bf16_hi(m));
   } else {
@@ -101,117 +189,404 @@ template <typename T, int N> __device__ __forceinline__ float largest(const uint
     return m;
   }
 }
-__device__ __forceinline__ uint4 load_unit(const uint4* p) {
-  uint4 u;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-               : "l"(p)
-               : "memory");
-  return u;
+
+__device__ __forceinline__ void copy_unit(uint4* dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-
-// A thread's sums over its logits, relative to a reference m that is a logit it has
-// seen (the type's lowest value at first): s = sum 2^u and a = sum 2^u u with
-// u = c2 (x - m), c2 = c log2(e).  The difference is exact or rounded once, so that
-// large logits cost no accuracy.
-template <bool ENT>
-struct Sums {
-  float m, top;      // reference, largest logit so far
-  float2 s, a;
-  __device__ explicit Sums(float low)
-      : m(low), top(-INFINITY), s(make_float2(0.f, 0.f)), a(make_float2(0.f, 0.f)) {}
-
-  __device__ __forceinline__ void see(float largest, float c2, float slack) {
-    top = fmaxf(top, largest);
-    if (largest > m + slack) {
-      const float d = fmaxf((m - largest) * c2, kLeast), f = ex2_approx(d);
-      if (ENT) a = make_float2((a.x + d * s.x) * f, (a.y + d * s.y) * f);
-      s = make_float2(s.x * f, s.y * f);
-      m = largest;
+__device__ __forceinline__ void copies_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_left_c() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// until at most n (or six) of the groups sent last are on their way
+__device__ __forceinline__ void copies_left(int n) {
+  switch (n) {
+    case 0: copies_left_c<0>(); break;
+    case 1: copies_left_c<1>(); break;
+    case 2: copies_left_c<2>(); break;
+    case 3: copies_left_c<3>(); break;
+    case 4: copies_left_c<4>(); break;
+    case 5: copies_left_c<5>(); break;
+    default: copies_left_c<6>();
+  }
+}
+// Sends for group g of a part, of kGroup units a thread, into `dst`; places past the
+// part's units get -inf.  One commit each.
+template <typename T, int THREADS>
+__device__ __forceinline__ void send_group(uint4* dst, const RowPart<T>& x, int g) {
+  const int i = (int)threadIdx.x + kGroup * g * THREADS;
+  dst += threadIdx.x;
+  const uint4* src = x.src + i;
+  if (i + (kGroup - 1) * THREADS < x.n) {
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) copy_unit(dst + k * THREADS, src + k * THREADS);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) {
+      if (i + k * THREADS < x.n) copy_unit(dst + k * THREADS, src + k * THREADS);
+      else dst[k * THREADS] = no_unit<T>();
     }
   }
-  __device__ __forceinline__ void add(float2 x, float c2) {
-    const float2 u = fmul2(fadd2(x, make_float2(-m, -m)), make_float2(c2, c2));
-    const float2 e = make_float2(ex2_approx(u.x), ex2_approx(u.y));
-    s = fadd2(s, e);
-    if (ENT) a = ffma2(e, make_float2(fmaxf(u.x, kLeast), fmaxf(u.y, kLeast)), a);
-  }
-};
-
-// What the threads of a CTA have together.
-struct Row {
-  float m, l;        // largest logit, log of the sum: -inf where no logit is above -inf
-  float entropy;
-};
-
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-
-// The CTA's largest logit and its sums relative to that, in every thread; a fixed order.
-template <bool ENT>
-__device__ __forceinline__ void join_sums(const Sums<ENT>& t, float low, float c2, float (*part)[4],
-                                          float* m_out, float* s_out, float* a_out) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  auto onto = [&](float m, float from, float& s, float& a) {   // sums relative to `from`, now to m
-    const float d = fmaxf((from - m) * c2, kLeast), f = ex2_approx(d);
-    if (ENT) a = (a + d * s) * f;
-    s *= f;
-  };
-  float s = t.s.x + t.s.y, a = ENT ? t.a.x + t.a.y : 0.f;
-  const float mw = fmaxf(warp_max(t.top), low);
-  onto(mw, t.m, s, a);
-  s = warp_sum(s);
-  if (ENT) a = warp_sum(a);
-  if (lane == 0) {
-    part[warp][0] = mw;
-    part[warp][1] = s;
-    part[warp][2] = a;
-  }
-  __syncthreads();
-  const bool one = lane < warps;   // a lane a warp
-  const float from = one ? part[lane][0] : low;
-  const float m = warp_max(from);
-  s = one ? part[lane][1] : 0.f;
-  a = ENT && one ? part[lane][2] : 0.f;
-  onto(m, from, s, a);
-  *m_out = m;
-  *s_out = warp_sum(s);
-  if (ENT) *a_out = warp_sum(a);
+  copies_sent();
 }
+
+// ---------------------------------------------------------------------------
+// Sums
+// ---------------------------------------------------------------------------
+// A thread's sums over its logits, s = sum 2^u and a = sum 2^u u with u = c2 x - R.
 template <bool ENT>
-__device__ __forceinline__ Row join(const Sums<ENT>& t, float low, float c2, float (*part)[4]) {
-  float m, s, a = 0.f;
-  join_sums<ENT>(t, low, c2, part, &m, &s, &a);
-  Row r;
-  const bool none = s == 0.f;
-  r.m = none ? 0.f : m;
-  r.l = none ? -INFINITY : logf(s);
-  r.entropy = none ? 0.f : r.l - a / s * kLn2;
+struct Sums {
+  float R, limit, top;      // reference, c2 x that renews it, largest logit so far
+  f2 neg, s, a;
+  __device__ __forceinline__ Sums()
+      : R(-kFar), limit(-kFar), top(-INFINITY), neg(two(kFar, kFar)), s(0), a(0) {}
+
+  __device__ __forceinline__ void see(float largest, float c2) {
+    top = fmaxf(top, largest);
+    const float y = largest * c2;
+    if (y > limit) {
+      const float to = ceilf(y), d = fmaxf(R - to, kLeast), f = ex2_approx(d);
+      if (ENT) a = mul_two(fma_two(s, two(d, d), a), two(f, f));
+      s = mul_two(s, two(f, f));
+      R = to;
+      limit = to + kSlack;
+      neg = two(-to, -to);
+    }
+  }
+  __device__ __forceinline__ void add(f2 x, f2 c2) {
+    const f2 u = fma_two(x, c2, neg), e = ex2_two(u);
+    s = add_two(s, e);
+    if (ENT) a = fma_two(e, not_least(u), a);
+  }
+  template <typename T, int N> __device__ __forceinline__ void add_units(const uint4 (&v)[N], float c, f2 c2) {
+    see(largest<T, N>(v), c);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int e = 0; e < RowPart<T>::E / 2; ++e) add(pair<T>(v[k], e), c2);
+  }
+};
+
+// What the threads have together: largest logit, reference, sums.
+struct Joined {
+  float m, R, s, a;
+};
+__device__ __forceinline__ void onto(float R, float from, float& s, float& a) {
+  const float d = fmaxf(from - R, kLeast), f = ex2_approx(d);
+  a = (a + d * s) * f;
+  s *= f;
+}
+// Over the CTA, in every thread; a fixed order.  One barrier, behind which `part` may
+// be read until the CTA's next one.
+template <bool ENT, int THREADS>
+__device__ __forceinline__ Joined join(const Sums<ENT>& t, float4* part) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float2 s2 = both(t.s), a2 = both(t.a);
+  float s = s2.x + s2.y, a = ENT ? a2.x + a2.y : 0.f;
+  const float R = lanes_max(t.R), m = lanes_max(t.top);
+  onto(R, t.R, s, a);
+  s = lanes_sum<32>(s);
+  if (ENT) a = lanes_sum<32>(a);
+  if (lane == 0) part[warp] = make_float4(m, R, s, a);
+  __syncthreads();
+  const float4 w = part[lane & (THREADS / 32 - 1)];   // a lane a warp, over and over
+  Joined j;
+  j.m = lanes_max(w.x);
+  j.R = lanes_max(w.y);
+  s = w.z;
+  a = w.w;
+  onto(j.R, w.y, s, a);
+  j.s = lanes_sum<THREADS / 32>(s);
+  j.a = ENT ? lanes_sum<THREADS / 32>(a) : 0.f;
+  return j;
+}
+// The parts' sums into one, in the order of the parts.
+__device__ __forceinline__ Joined join_parts(const float4* share, int parts) {
+  Joined j = {-INFINITY, -kFar, 0.f, 0.f};
+  for (int k = 0; k < parts; ++k) {
+    j.m = fmaxf(j.m, share[k].x);
+    j.R = fmaxf(j.R, share[k].y);
+  }
+  for (int k = 0; k < parts; ++k) {
+    float s = share[k].z, a = share[k].w;
+    onto(j.R, share[k].y, s, a);
+    j.s += s;
+    j.a += a;
+  }
+  return j;
+}
+// True for a row whose sums have to be taken as 2^(c2 (x - m)).
+__device__ __forceinline__ bool is_far(float m, float c2) { return m != -INFINITY && !(fabsf(m) * c2 < kFar); }
+
+// A thread's sums of such a row, of its units src[t], src[t + THREADS] ...
+template <typename T, int THREADS>
+__device__ __noinline__ float2 far_sums(const uint4* src, int n, float loose, float m, float c2) {
+  float s = ex2_approx((loose - m) * c2), a = s * fmaxf((loose - m) * c2, kLeast);
+  for (int i = threadIdx.x; i < n; i += THREADS) {
+    const uint4 v = src[i];
+    for (int e = 0; e < RowPart<T>::E / 2; ++e) {
+      const float2 x = both(pair<T>(v, e));
+      const float u = (x.x - m) * c2, w = (x.y - m) * c2;
+      s += ex2_approx(u) + ex2_approx(w);
+      a += ex2_approx(u) * fmaxf(u, kLeast) + ex2_approx(w) * fmaxf(w, kLeast);
+    }
+  }
+  return make_float2(s, a);
+}
+template <int THREADS>
+__device__ __forceinline__ float2 cta_sum(float2 v, float4* part) {
+  v = make_float2(lanes_sum<32>(v.x), lanes_sum<32>(v.y));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float4(v.x, v.y, 0.f, 0.f);
+  __syncthreads();
+  const float4 w = part[threadIdx.x & (THREADS / 32 - 1)];
+  return make_float2(lanes_sum<THREADS / 32>(w.x), lanes_sum<THREADS / 32>(w.y));
+}
+
+// The row's statistics.
+struct Stats {
+  float m, l, entropy;   // 0, -inf, 0 where no logit is above -inf
+};
+__device__ __forceinline__ Stats stats_of(float m, float s, float a, float shift) {
+  // shift: c2 m - R, what the sums are above the largest logit
+  Stats r = {0.f, -INFINITY, 0.f};
+  if (s == 0.f) return r;
+  const float log_s = logf(s);
+  r.m = m;
+  r.l = log_s - kLn2 * shift;
+  r.entropy = log_s - kLn2 * (a / s);
   if (r.entropy < 0.f) r.entropy = 0.f;
   return r;
 }
 
-// ---------------------------------------------------------------------------
-// Forward
-// ---------------------------------------------------------------------------
-struct Rows {
-  const void* logits;
-  int64_t ld;
-  const void* ids;     // may be NULL
-  int id_bytes, S, c, D, V;
-  float scale;
-  int* status;
+// What the CTAs of a cluster write into each other, of two rows by turns, since one of
+// them may be a row ahead.
+struct Exchange {
+  float4 share[8];
+  float2 again[8];
+  float target, z[TSP_TOP_MAX];   // (in the first CTA) logits of the given and the teacher's tokens
 };
+
+// The statistics of a row from its threads' sums.  `units`: where a thread finds its
+// units again; `loose`: its element outside the units or -inf.  Every thread of the
+// CTA (of the cluster) takes part.
+template <typename T, bool ENT, bool CLUSTER, int THREADS>
+__device__ __forceinline__ Stats statistics(const Sums<ENT>& sums, const uint4* units, int n, float loose,
+                                            float c2, float4* part, Exchange* ex, int rank, int parts) {
+  const auto cluster = cooperative_groups::this_cluster();
+  Joined j = join<ENT, THREADS>(sums, part);
+  if (CLUSTER) {
+    if ((int)threadIdx.x < parts)
+      cluster.map_shared_rank(ex, threadIdx.x)->share[rank] = make_float4(j.m, j.R, j.s, j.a);
+    cluster.sync();
+    j = join_parts(ex->share, parts);
+  }
+  if (!is_far(j.m, c2)) return stats_of(j.m, j.s, j.a, fmaf(j.m, c2, -j.R));
+  float2 v = cta_sum<THREADS>(far_sums<T, THREADS>(units, n, loose, j.m, c2), part);
+  if (CLUSTER) {
+    if ((int)threadIdx.x < parts) cluster.map_shared_rank(ex, threadIdx.x)->again[rank] = v;
+    cluster.sync();
+    v = make_float2(0.f, 0.f);
+    for (int k = 0; k < parts; ++k) v = make_float2(v.x + ex->again[k].x, v.y + ex->again[k].y);
+  }
+  return stats_of(j.m, v.x, v.y, 0.f);
+}
+__device__ __forceinline__ float log_p(float x, const Stats& st, float c) {
+  return st.l == -INFINITY ? -INFINITY : c * (x - st.m) - st.l;
+}
+
+// ---------------------------------------------------------------------------
+// A teacher's list
+// ---------------------------------------------------------------------------
 struct Teacher {
   const int* ids;      // [S, K]
   const void* logits;  // [S, K]
   int f32, K;
   float scale, w_ce, w_kd;
 };
+// An entry as it stands (not yet looked at), and its token: -1 for none.
+struct Entry {
+  int id;
+  float y;
+};
+__device__ __forceinline__ Entry load_entry(const Teacher& t, int p, int k) {
+  const int64_t i = (int64_t)p * t.K + k;
+  return {t.ids[i], t.f32 ? reinterpret_cast<const float*>(t.logits)[i]
+                          : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(t.logits)[i])};
+}
+__device__ __forceinline__ int token_of(const Entry& e, const Rows& r) {
+  if (e.id >= r.V) report_status(r.status, (int)TSP_ERR_RANGE);
+  return e.id >= 0 && e.id < r.V && !(e.y == -INFINITY) ? e.id : -1;
+}
+// The list's softmax, entry k thread k's (there: it counts): warps' parts before the
+// CTA's next barrier, the whole behind it.
+__device__ __forceinline__ void teacher_part(bool there, float y, float scale, float2* teach) {
+  const float mw = lanes_max(there ? y : -INFINITY);
+  const float sw = lanes_sum<32>(there ? expf(scale * (y - mw)) : 0.f);
+  if ((threadIdx.x & 31) == 0) teach[threadIdx.x >> 5] = make_float2(mw, sw);
+}
+template <int THREADS>
+__device__ __forceinline__ float2 teacher_whole(float scale, const float2* teach) {   // (largest, sum)
+  const float2 w = teach[threadIdx.x & (THREADS / 32 - 1)];
+  const float m = lanes_max(w.x);
+  return make_float2(m, lanes_sum<THREADS / 32>(w.y == 0.f ? 0.f : w.y * expf(scale * (w.x - m))));
+}
+// Entry's q and log q.
+__device__ __forceinline__ float2 teacher_q(bool there, float y, float scale, float2 whole) {
+  const float v = scale * (y - whole.x);
+  return there ? make_float2(expf(v) / whole.y, v - logf(whole.y)) : make_float2(0.f, 0.f);
+}
+
+// What the listed tokens add: entry k < K the teacher's, entry K the given token.
+struct Adds {
+  alignas(16) int id[TSP_TOP_MAX + 4];   // (-1: none of this part's; up to a multiple of four)
+  float add[TSP_TOP_MAX + 1];
+  float z[TSP_TOP_MAX + 1];   // their logits, read before they may be overwritten
+};
+__device__ __forceinline__ void end_adds(Adds& adds, int n) {
+  if (threadIdx.x < 3) adds.id[n + threadIdx.x] = -1;
+}
+// put(k, token, what all its entries add in the order of the list) for the first entry
+// k of each token.  All threads of the CTA take part, a power of two of them an entry,
+// which look for its token in the list.
+template <int THREADS, typename F>
+__device__ __forceinline__ void for_added(const Adds& adds, int n, F put) {
+  const int t = threadIdx.x;
+  if (n == 1) {
+    if (t == 0 && adds.id[0] >= 0) put(0, adds.id[0], adds.add[0]);
+    return;
+  }
+  int log_g = 0;
+  while (log_g < 5 && (n << (log_g + 1)) <= THREADS) ++log_g;
+  const int g = 1 << log_g;
+  for (int k = t >> log_g; k - ((t & 31) >> log_g) < n; k += THREADS >> log_g) {   // (whole warps)
+    const int j = k < n ? adds.id[k] : -1;
+    int same = 0;
+    for (int q = 4 * (t & (g - 1)); q < n; q += 4 * g) {
+      const int4 o = *reinterpret_cast<const int4*>(adds.id + q);
+      same += (o.x == j) + (o.y == j) + (o.z == j) + (o.w == j);
+    }
+    for (int o = 1; o < g; o *= 2) same += __shfl_xor_sync(0xffffffffu, same, o);
+    if (j < 0 || (t & (g - 1)) != 0) continue;
+    float sum = adds.add[k];
+    bool first = true;
+    if (same > 1) {   // the same token more than once
+      sum = 0.f;
+      for (int q = 0; q < n; ++q)
+        if (adds.id[q] == j) {
+          sum += adds.add[q];
+          first &= q >= k;
+        }
+    }
+    if (first) put(k, j, sum);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradients of a row's logits: e 2^u with e = 2^-f (A + B (u - f)), u as in the sums
+// (far rows: c2 (x - m)), u - f = log2 p.
+// ---------------------------------------------------------------------------
+template <bool ENT>
+struct Slope {
+  float R, c2, A, B;
+  bool far;
+  __device__ __forceinline__ Slope(float m, float l, float scale_c2, float a, float b) : c2(scale_c2) {
+    far = is_far(m, c2);
+    R = far ? m : ceilf(m * c2);
+    const float f = far ? l * kLog2e : fmaf(m, c2, -R) + l * kLog2e, e = ex2_approx(-f);
+    A = ENT ? e * (a - b * f) : e * a;
+    B = ENT ? e * b : 0.f;
+  }
+  __device__ __forceinline__ f2 at(f2 u) const {
+    const f2 e = ex2_two(u);
+    return mul_two(e, ENT ? fma_two(not_least(u), two(B, B), two(A, A)) : two(A, A));
+  }
+  __device__ __forceinline__ f2 near(f2 x) const { return at(fma_two(x, two(c2, c2), two(-R, -R))); }
+  __device__ __forceinline__ float one(float x) const {
+    return both(at(two(far ? (x - R) * c2 : fmaf(x, c2, -R), 0.f))).x;
+  }
+};
+template <typename T> __device__ __forceinline__ uint32_t pack_two(f2 v) {
+  const float2 b = both(v);
+  return pack2<T>(b.x, b.y);
+}
+// The gradients of a unit (of one that is not in a far row).
+template <typename T, bool ENT>
+__device__ __forceinline__ uint4 unit_grad(const uint4& v, const Slope<ENT>& s) {
+  if constexpr (sizeof(T) == 2) {
+    return make_uint4(pack_two<T>(s.near(pair<T>(v, 0))), pack_two<T>(s.near(pair<T>(v, 1))),
+                      pack_two<T>(s.near(pair<T>(v, 2))), pack_two<T>(s.near(pair<T>(v, 3))));
+  } else {
+    const float2 g = both(s.near(pair<T>(v, 0))), h = both(s.near(pair<T>(v, 1)));
+    return make_uint4(__float_as_uint(g.x), __float_as_uint(g.y), __float_as_uint(h.x), __float_as_uint(h.y));
+  }
+}
+template <typename T, bool ENT>
+__device__ __noinline__ uint4 far_grad(uint4 v, const Slope<ENT>& s) {
+  T e[16 / sizeof(T)];
+  memcpy(e, &v, 16);
+  for (int i = 0; i < (int)(16 / sizeof(T)); ++i) e[i] = from_f<T>(s.one(to_f<T>(e[i])));
+  memcpy(&v, e, 16);
+  return v;
+}
+
+// The row's CTAs: of a cluster, or those that share rows without speaking to each other.
+struct Place {
+  int rank, parts, first, stride;
+  __device__ __forceinline__ explicit Place(int p) : parts(p) {
+    rank = p == 1 ? 0 : blockIdx.x % p;
+    first = p == 1 ? blockIdx.x : blockIdx.x / p;
+    stride = p == 1 ? gridDim.x : gridDim.x / p;
+  }
+};
+// Groups of a part at most.
+template <typename T, int THREADS>
+__device__ __forceinline__ int groups_of(int V, int parts) {
+  const int units = V / RowPart<T>::E, per = parts == 1 ? units : (units + parts - 1) / parts;
+  return max(1, (per + kGroup * THREADS - 1) / (kGroup * THREADS));
+}
+
+// Groups of rows that are not padding sent for ahead of their use, into the places of a
+// ring by turns: kStages commits are on their way at any time.
+constexpr int kStages = 4;
+template <typename T, int THREADS>
+struct Sender {
+  const Rows& a;
+  uint4* ring;
+  Place at;
+  int groups, row, g, ahead, slot;
+  RowPart<T> x;
+  __device__ __forceinline__ Sender(const Rows& rows, uint4* to, Place place, int n)
+      : a(rows), ring(to), at(place), groups(n), row(place.first - place.stride), g(n),
+        ahead(given(rows, place.first)), slot(0), x(rows, 0, 0, 1) {
+    for (int k = 0; k < kStages; ++k) send();
+  }
+  __device__ __forceinline__ uint4* place() const { return ring + slot * kGroup * THREADS; }
+  // into the place that is next in turn
+  __device__ __forceinline__ void send() {
+    if (g == groups) {
+      int id;
+      do {
+        row += at.stride;
+        id = ahead;
+        ahead = given(a, row + at.stride);
+      } while (row < a.S && id == -1);
+      g = 0;
+      if (row < a.S) x = RowPart<T>(a, row, at.rank, at.parts);
+    }
+    if (row < a.S) send_group<T, THREADS>(place(), x, g++);
+    else copies_sent();
+    slot = (slot + 1) % kStages;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Forward
+// ---------------------------------------------------------------------------
 struct FwdArgs {
   Rows r;
   float *logp, *entropy, *stats, *top_logp;
   int* top_ids;
-  int top;
+  int top, parts;
   Teacher t;
   float* loss;
 };
@@ -231,12 +606,17 @@ __device__ __forceinline__ uint64_t key_of(float x, int j) {
 constexpr uint32_t kOrderNone = 0x007fffffu;   // order_of(-inf)
 
 constexpr int kCandidates = 1024;
-struct TopSmem {
-  float best[kThreads];        // largest logit of each group of threads
-  int sel[kThreads];
+template <int THREADS> struct TopSmem {
+  float best[THREADS];        // largest logit of each group of threads
+  int sel[THREADS];
   uint64_t key[kCandidates], above;
   int n, n_sel;
 };
+struct TopLists {             // of a cluster's parts, in the first CTA
+  uint64_t key[8][TSP_TOP_MAX];
+  int n[8];
+};
+struct Nothing {};
 
 // The number of keys above mine among the n.
 __device__ __forceinline__ int rank_in(const uint64_t* key, int n, uint64_t mine) {
@@ -244,19 +624,30 @@ __device__ __forceinline__ int rank_in(const uint64_t* key, int n, uint64_t mine
   for (int i = 0; i < n; ++i) r += key[i] > mine;
   return r;
 }
+// ... in a list from the largest down.
+__device__ __forceinline__ int rank_in_sorted(const uint64_t* key, int n, uint64_t mine) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (key[mid] > mine) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
 
-// The largest `top` of the row's logits, in order, into smem keys: a bound from the
-// threads' own largest values (top of them are logits of the row, so the smallest of
-// the best `top` is one), then the logits of the threads that reach it once more,
-// out of L2.  Returns how many keys there are (sorted ranks are found by the caller).
-template <typename T>
-__device__ int candidates(const RowUnits<T>& row, int top, float mine, TopSmem& sm) {
-  const int t = threadIdx.x, threads = blockDim.x;
-  int g = 1;   // threads a group: some four groups for each alternative
-  while (g < 32 && threads / (2 * g) >= 4 * top) g *= 2;
+// Keys of a part's logits, the `top` largest among them, into sm.key; their number.
+// A bound first: each thread's largest logit (`mine`, of its units) is a logit of the
+// part, so the top-th largest of them (of groups of threads, four for each alternative
+// where there are as many) is not above the top-th of all.  Then the logits of the
+// threads that reach it once more, out of L2: top / groups of the part.
+template <typename T, int THREADS>
+__device__ __noinline__ int candidates(const RowPart<T>& x, int top, float mine, TopSmem<THREADS>& sm) {
+  const int t = threadIdx.x;
+  int g = 1;   // threads a group
+  while (g < 32 && THREADS / (2 * g) >= 4 * top) g *= 2;
   float b = mine;
   for (int o = 1; o < g; o *= 2) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
-  const int groups = threads / g, i = t / g;
+  const int groups = THREADS / g, i = t / g;
   if (t % g == 0) sm.best[i] = b;
   if (t == 0) {
     sm.n = sm.n_sel = 0;
@@ -271,30 +662,28 @@ __device__ int candidates(const RowUnits<T>& row, int top, float mine, TopSmem& 
   if (t % g == 0 && b > -INFINITY && order_of(b) >= (uint32_t)(sm.above >> 32))
     sm.sel[atomicAdd(&sm.n_sel, 1)] = i;
   __syncthreads();
-  const int n_sel = sm.n_sel, rounds = (row.units + threads - 1) / threads;
-  const int per = n_sel * g;
+  const int per = sm.n_sel * g, rounds = (x.n + THREADS - 1) / THREADS;
   for (;;) {
     const uint64_t above = sm.above;
-    auto take = [&](float x, int j) {
-      const uint64_t k = key_of(x, j);
+    auto take = [&](float v, int j) {
+      const uint64_t k = key_of(v, j);
       if (k < above) return;
       const int n = atomicAdd(&sm.n, 1);
       if (n < kCandidates) sm.key[n] = k;
     };
-    const int j0 = row.loose(t);
-    if (t < 2 * RowUnits<T>::E && j0 >= 0) take(to_f<T>(row.row[j0]), j0);
-    for (int w = t; w < per * rounds; w += threads) {
+    const int j0 = x.loose(t);
+    if (j0 >= 0) take(to_f<T>(x.row[j0]), j0);
+    for (int w = t; w < per * rounds; w += THREADS) {
       const int round = w / per, in = w - round * per;
-      const int u = sm.sel[in / g] * g + in % g + round * threads;
-      if (u >= row.units) continue;
-      const uint4 v = load_unit(row.first() + u);
-      uint4 one[1] = {v};
-      if (order_of(largest<T, 1>(one)) < (uint32_t)(above >> 32)) continue;
+      const int u = sm.sel[in / g] * g + in % g + round * THREADS;
+      if (u >= x.n) continue;
+      const uint4 v[1] = {x.src[u]};
+      if (order_of(largest<T, 1>(v)) < (uint32_t)(above >> 32)) continue;
 #pragma unroll
-      for (int e = 0; e < RowUnits<T>::E / 2; ++e) {
-        const float2 x = pair<T>(v, e);
-        take(x.x, row.head + u * RowUnits<T>::E + 2 * e);
-        take(x.y, row.head + u * RowUnits<T>::E + 2 * e + 1);
+      for (int e = 0; e < RowPart<T>::E / 2; ++e) {
+        const float2 y = both(pair<T>(v[0], e));
+        take(y.x, x.head + (x.u_lo + u) * RowPart<T>::E + 2 * e);
+        take(y.y, x.head + (x.u_lo + u) * RowPart<T>::E + 2 * e + 1);
       }
     }
     __syncthreads();
@@ -303,165 +692,158 @@ __device__ int candidates(const RowUnits<T>& row, int top, float mine, TopSmem& 
     // More than there is room for (many equal logits, or a few threads hold most of the
     // large ones): the top-th of those stored is a better bound, since as many reach it.
     __syncthreads();
-    for (int k = t; k < kCandidates; k += threads)
+    for (int k = t; k < kCandidates; k += THREADS)
       if (rank_in(sm.key, kCandidates, sm.key[k]) == top - 1) sm.above = sm.key[k];
     if (t == 0) sm.n = 0;
     __syncthreads();
   }
 }
 
-// The teacher's and the given token's part of a row's loss.
-__device__ __forceinline__ float teacher_value(const Teacher& t, int64_t i) {
-  return t.f32 ? reinterpret_cast<const float*>(t.logits)[i]
-               : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(t.logits)[i]);
-}
-// An entry of the teacher's list: its token (-1: none) and logit.
-__device__ __forceinline__ int teacher_entry(const Teacher& t, const Rows& r, int p, int k, float* y) {
-  const int64_t i = (int64_t)p * t.K + k;
-  const int id = t.ids[i];
-  *y = teacher_value(t, i);
-  if (id >= r.V) report_status(r.status, (int)TSP_ERR_RANGE);
-  return id >= 0 && id < r.V && !(*y == -INFINITY) ? id : -1;
-}
-
-// sum_k q_k (log q_k - log p_k) and whether there is an entry, for all threads: entry
-// k is thread k's, y the teacher's logit, c its scale, logp the model's.
-__device__ __forceinline__ float2 divergence(bool there, float y, float c, float logp,
-                                             float (*part)[4]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const bool nan = there && !(y < INFINITY);
-  const float mw = warp_max(there && !nan ? y : -INFINITY);
-  float e = 0.f, x = 0.f;
-  if (there) {
-    e = nan ? NAN : expf(c * (y - mw));
-    if (!(e == 0.f)) x = e * (c * (y - mw) - logp);
-  }
-  e = warp_sum(e);
-  x = warp_sum(x);
-  __syncthreads();
-  if (lane == 0) {
-    part[warp][0] = mw;
-    part[warp][1] = e;
-    part[warp][2] = x;
-  }
-  __syncthreads();
-  float m = -INFINITY, se = 0.f, sx = 0.f;
-  for (int w = 0; w < warps; ++w) m = fmaxf(m, part[w][0]);
-  for (int w = 0; w < warps; ++w) {
-    if (part[w][1] == 0.f) continue;
-    const float d = c * (part[w][0] - m), f = expf(d);
-    if (f == 0.f) continue;
-    se += part[w][1] * f;
-    sx += (part[w][2] + d * part[w][1]) * f;
-  }
-  return make_float2(sx / se - logf(se), se == 0.f ? 0.f : 1.f);
-}
-
-template <typename T, bool ENT>
-__global__ void __launch_bounds__(kThreads, 2) fwd_kernel(const __grid_constant__ FwdArgs a) {
-  constexpr int U = 4;
-  __shared__ float part[kWarps][4];
-  __shared__ TopSmem sm;
-  const int t = threadIdx.x, threads = blockDim.x, r = blockIdx.x;
-  const int p = pos_of(r, a.r.c, a.r.D);
-  if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
-  int64_t id = -1;
-  bool live = true;
-  if (a.r.ids) {
-    id = load_id(a.r.ids, a.r.id_bytes, p);
-    if (id >= a.r.V) {
-      if (t == 0) report_status(a.r.status, (int)TSP_ERR_RANGE);
-      id = -1;
+template <typename T, bool ENT, bool CLUSTER, int THREADS>
+__global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __grid_constant__ FwdArgs a) {
+  extern __shared__ uint4 ring[];
+  __shared__ struct {
+    float4 part[2][THREADS / 32];
+    float2 teach[THREADS / 32];
+    float kd[THREADS / 32];
+    typename std::conditional<CLUSTER, Exchange, Nothing>::type ex[2];
+    typename std::conditional<CLUSTER, TopLists, Nothing>::type lists;
+    TopSmem<THREADS> top;
+  } sm;
+  const auto cluster = cooperative_groups::this_cluster();
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const Place at(CLUSTER ? a.parts : 1);
+  const float c = a.r.scale, c2 = c * kLog2e;
+  const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
+  const int K = a.loss && a.t.w_kd != 0.f ? a.t.K : 0;
+  Sender<T, THREADS> sender(a.r, ring, at, groups);
+  // (the CTAs of a cluster have started before one writes into another's memory)
+  if (CLUSTER) cluster.sync();
+  int id = given(a.r, at.first), turn = 0;
+  for (int r = at.first; r < a.r.S; r += at.stride) {
+    const int p = pos_of(a.r, r), id_now = id;
+    if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
+    id = given(a.r, r + at.stride);
+    if (id_now == -1) {   // padding: the row is not looked at
+      if (at.rank != 0) continue;
+      if (t == 0) {
+        if (a.logp) a.logp[p] = 0.f;
+        if (a.entropy) a.entropy[p] = 0.f;
+        if (a.loss) a.loss[p] = 0.f;
+        if (a.stats) {
+          a.stats[2 * (int64_t)p] = 0.f;
+          a.stats[2 * (int64_t)p + 1] = -INFINITY;
+        }
+      }
+      for (int k = t; k < a.top; k += THREADS) {
+        a.top_ids[(int64_t)p * a.top + k] = -1;
+        a.top_logp[(int64_t)p * a.top + k] = -INFINITY;
+      }
+      continue;
     }
-    live = id >= 0;
-  }
-  if (!live) {   // padding: the row is not looked at
-    if (t == 0) {
-      if (a.logp) a.logp[p] = 0.f;
-      if (a.entropy) a.entropy[p] = 0.f;
-      if (a.loss) a.loss[p] = 0.f;
+    const RowPart<T> x(a.r, r, at.rank, at.parts);
+    const int j0 = x.loose(t);
+    const float x0 = j0 >= 0 ? to_f<T>(x.row[j0]) : -INFINITY;
+    float target = 0.f, z = 0.f;
+    if (t == 0 && id_now >= 0) target = to_f<T>(x.row[id_now]);
+    Entry e = {-1, -INFINITY};
+    int kid = -1;
+    if (t < K && at.rank == 0) e = load_entry(a.t, p, t);
+    Sums<ENT> sums;
+    for (int g = 0; g < groups; ++g) {
+      copies_left_c<kStages - 1>();
+      uint4 v[kGroup];
+      const uint4* from = sender.place() + t;
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k) v[k] = from[k * THREADS];
+      sender.send();
+      sums.template add_units<T, kGroup>(v, c2, two(c2, c2));
+      if (g == 0 && t < K) {   // the entry is there by now: its logit is sent for
+        kid = token_of(e, a.r);
+        if (kid >= 0) z = to_f<T>(x.row[kid]);
+      }
+    }
+    const float mine = sums.top;   // of the units
+    sums.see(x0, c2);
+    sums.add(two(x0, -INFINITY), two(c2, c2));
+    if (K > 0) teacher_part(kid >= 0, e.y, a.t.scale, sm.teach);
+    Exchange* ex = nullptr;
+    if constexpr (CLUSTER) ex = &sm.ex[turn];
+    const Stats st = statistics<T, ENT, CLUSTER, THREADS>(sums, x.src, x.n, x0, c2, sm.part[turn], ex, at.rank,
+                                                          at.parts);
+    turn ^= 1;
+    if (t == 0 && at.rank == 0) {
+      if (a.logp) a.logp[p] = log_p(target, st, c);
+      if (a.entropy) a.entropy[p] = st.entropy;
       if (a.stats) {
-        a.stats[2 * (int64_t)p] = 0.f;
-        a.stats[2 * (int64_t)p + 1] = -INFINITY;
+        a.stats[2 * (int64_t)p] = st.m;
+        a.stats[2 * (int64_t)p + 1] = st.l;
       }
     }
-    for (int k = t; k < a.top; k += threads) {
-      a.top_ids[(int64_t)p * a.top + k] = -1;
-      a.top_logp[(int64_t)p * a.top + k] = -INFINITY;
-    }
-    return;
-  }
-  const RowUnits<T> row(a.r.logits, a.r.ld, r, a.r.V);
-  const float c2 = a.r.scale * kLog2e, slack = kSlack / c2, low = lowest<T>();
-  Sums<ENT> sums(low);
-  const int j0 = t < 2 * RowUnits<T>::E ? row.loose(t) : -1;
-  if (j0 >= 0) {
-    const float x = to_f<T>(row.row[j0]);
-    sums.see(x, c2, slack);
-    sums.add(make_float2(x, -INFINITY), c2);
-    sums.top = fmaxf(sums.top, x);
-  }
-  float mine = -INFINITY;   // of the units
-  for (int u0 = t; u0 < row.units; u0 += U * threads) {
-    uint4 v[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k)
-      v[k] = u0 + k * threads < row.units ? load_unit(row.first() + u0 + k * threads) : no_unit<T>();
-    const float b = largest<T, U>(v);
-    mine = fmaxf(mine, b);
-    sums.see(b, c2, slack);
-#pragma unroll
-    for (int k = 0; k < U; ++k)
-#pragma unroll
-      for (int e = 0; e < RowUnits<T>::E / 2; ++e) sums.add(pair<T>(v[k], e), c2);
-  }
-  const float target = id >= 0 && (a.logp || a.t.w_ce != 0.f) ? to_f<T>(row.row[id]) : 0.f;
-  const Row x = join<ENT>(sums, low, c2, part);
-  const float logp = x.l == -INFINITY ? -INFINITY : a.r.scale * (target - x.m) - x.l;
-  if (t == 0) {
-    if (a.logp) a.logp[p] = logp;
-    if (a.entropy) a.entropy[p] = x.entropy;
-    if (a.stats) {
-      a.stats[2 * (int64_t)p] = x.m;
-      a.stats[2 * (int64_t)p + 1] = x.l;
-    }
-  }
-  if (a.loss) {
-    float loss = a.t.w_ce != 0.f ? -a.t.w_ce * logp : 0.f;
-    if (a.t.K > 0 && a.t.w_kd != 0.f) {
-      float y = 0.f, lp = 0.f;
-      int kid = -1;
-      if (t < a.t.K) {
-        kid = teacher_entry(a.t, a.r, p, t, &y);
-        if (kid >= 0)
-          lp = x.l == -INFINITY ? -INFINITY : a.r.scale * (to_f<T>(row.row[kid]) - x.m) - x.l;
+    if (a.loss) {
+      float kd = 0.f;
+      if (K > 0) {
+        const float2 whole = teacher_whole<THREADS>(a.t.scale, sm.teach);
+        const float2 q = teacher_q(kid >= 0, e.y, a.t.scale, whole);
+        kd = lanes_sum<32>(q.x != 0.f ? q.x * (q.y - log_p(z, st, c)) : 0.f);
+        if (lane == 0) sm.kd[warp] = kd;
+        __syncthreads();
+        kd = 0.f;
+        for (int k = 0; k < THREADS / 32; ++k) kd += sm.kd[k];
+        kd = whole.y != 0.f ? a.t.w_kd * kd : 0.f;
       }
-      const float2 kd = divergence(kid >= 0, y, a.t.scale, lp, part);
-      if (kd.y != 0.f) loss += a.t.w_kd * kd.x;
+      if (t == 0 && at.rank == 0)
+        a.loss[p] = (a.t.w_ce != 0.f ? -a.t.w_ce * log_p(target, st, c) : 0.f) + kd;
     }
-    if (t == 0) a.loss[p] = loss;
-  }
-  if (a.top > 0) {
-    const int64_t at = (int64_t)p * a.top;
-    int n = 0;
-    if (!isnan(x.l)) n = candidates<T>(row, a.top, mine, sm);
-    for (int k = t; k < n; k += threads) {
-      const uint64_t key = sm.key[k];
-      const int rank = rank_in(sm.key, n, key);
-      if (rank < a.top) {
-        a.top_ids[at + rank] = (int)~(uint32_t)key;
-        a.top_logp[at + rank] = a.r.scale * (logit_of((uint32_t)(key >> 32)) - x.m) - x.l;
+    if (a.top > 0) {
+      const int64_t to = (int64_t)p * a.top;
+      int n = 0;
+      auto put = [&](int rank, uint64_t key) {
+        if (rank >= a.top) return;
+        a.top_ids[to + rank] = (int)~(uint32_t)key;
+        a.top_logp[to + rank] = log_p(logit_of((uint32_t)(key >> 32)), st, c);
+      };
+      if (!isnan(st.l)) {
+        n = candidates<T, THREADS>(x, a.top, mine, sm.top);
+        if constexpr (!CLUSTER) {
+          for (int k = t; k < n; k += THREADS) put(rank_in(sm.top.key, n, sm.top.key[k]), sm.top.key[k]);
+        } else {
+          TopLists* first = cluster.map_shared_rank(&sm.lists, 0);
+          for (int k = t; k < n; k += THREADS) {
+            const int rank = rank_in(sm.top.key, n, sm.top.key[k]);
+            if (rank < a.top) first->key[at.rank][rank] = sm.top.key[k];
+          }
+          if (t == 0) first->n[at.rank] = min(n, a.top);
+          cluster.sync();
+          if (at.rank == 0) {
+            n = 0;
+            for (int q = 0; q < at.parts; ++q) {
+              const int nq = sm.lists.n[q];
+              n += nq;
+              for (int k = t; k < nq; k += THREADS) {
+                const uint64_t key = sm.lists.key[q][k];
+                int rank = k;
+                for (int o = 0; o < at.parts; ++o)
+                  if (o != q) rank += rank_in_sorted(sm.lists.key[o], sm.lists.n[o], key);
+                put(rank, key);
+              }
+            }
+          }
+          cluster.sync();   // the lists are read before the next row's come in
+        }
       }
-    }
-    for (int k = n + t; k < a.top; k += threads) {
-      a.top_ids[at + k] = -1;
-      a.top_logp[at + k] = isnan(x.l) ? x.l : -INFINITY;
+      if (at.rank == 0) {
+        for (int k = min(n, a.top) + t; k < a.top; k += THREADS) {
+          a.top_ids[to + k] = -1;
+          a.top_logp[to + k] = isnan(st.l) ? st.l : -INFINITY;
+        }
+      }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Gradient
+// Gradient from the forward's statistics
 // ---------------------------------------------------------------------------
 struct GradArgs {
   Rows r;
@@ -470,451 +852,385 @@ struct GradArgs {
   const float *stats, *entropy, *up, *up_entropy;   // up: dlogp, or dloss (NULL: 1)
   Teacher t;
   bool loss;
+  int parts;
 };
-
-// What the listed tokens add: entry k < K the teacher's, entry K the given token.
-struct Adds {
-  alignas(16) int id[TSP_TOP_MAX + 4];   // (-1 up to the next multiple of four)
-  float add[TSP_TOP_MAX + 1];
+// What a row's position holds.
+struct Upstream {
+  float m, l, up, up_entropy, entropy;
 };
-__device__ __forceinline__ void end_adds(Adds& adds, int n, int t) {
-  if (t < 3) adds.id[n + t] = -1;
+template <bool ENT>
+__device__ __forceinline__ Upstream upstream(const GradArgs& a, int r) {
+  Upstream u = {0.f, -INFINITY, 0.f, 0.f, 0.f};
+  if (r >= a.r.S) return u;
+  const int64_t p = pos_of(a.r, r);
+  u.m = a.stats[2 * p];
+  u.l = a.stats[2 * p + 1];
+  u.up = a.up ? a.up[p] : a.loss ? 1.f : 0.f;
+  if (ENT) {
+    u.up_entropy = a.up_entropy[p];
+    u.entropy = a.entropy[p];
+  }
+  return u;
 }
-// An entry's token (-1: none of this part's, or not the first entry of its token) and
-// what all entries of the token add, in the order of the list.
-__device__ __forceinline__ int added(const Adds& adds, int n, int k, float* sum) {
-  const int j = adds.id[k];
-  *sum = 0.f;
-  if (j < 0) return -1;
-  int same = 0;
-  for (int q = 0; q < n; q += 4) {
-    const int4 o = *reinterpret_cast<const int4*>(adds.id + q);
-    same += (o.x == j) + (o.y == j) + (o.z == j) + (o.w == j);
-  }
-  if (same == 1) {
-    *sum = adds.add[k];
-    return j;
-  }
-  bool first = true;
-  for (int q = 0; q < n; ++q)
-    if (adds.id[q] == j) {
-      *sum += adds.add[q];
-      first &= q >= k;
+// A and B of a row, and what the given token adds; `teacher`: there are entries.
+struct Factors {
+  float A, B, given;
+};
+__device__ __forceinline__ Factors factors(const GradArgs& a, const Upstream& u, bool teacher) {
+  const float c = a.r.scale;
+  if (a.loss) return {u.up * c * (a.t.w_ce + (teacher ? a.t.w_kd : 0.f)), 0.f, -u.up * c * a.t.w_ce};
+  return {-c * (u.up + u.up_entropy * u.entropy), -c * kLn2 * u.up_entropy, c * u.up};
+}
+// The group of a thread's that has the token, if it is one of the thread's units.
+template <typename T, int THREADS>
+__device__ __forceinline__ int group_with(const RowPart<T>& x, int id) {
+  const int u = (id - x.head) / RowPart<T>::E - x.u_lo;
+  return id >= x.head && id < x.tail && u >= 0 && u < x.n && u % THREADS == (int)threadIdx.x
+             ? u / (kGroup * THREADS)
+             : -1;
+}
+// Its logit, in a group that lies at `place` in shared memory.
+template <typename T, int THREADS>
+__device__ __forceinline__ float logit_in(const uint4* place, const RowPart<T>& x, int id) {
+  const int u = ((id - x.head) / RowPart<T>::E - x.u_lo) % (kGroup * THREADS);
+  return to_f<T>(reinterpret_cast<const T*>(place + u)[(id - x.head) % RowPart<T>::E]);
+}
+
+// Without a teacher a row needs no barrier: the given token's value is written by the
+// thread that has its unit.  With one, the listed tokens' logits are read first and
+// their values written once more at the end.
+template <typename T, bool ENT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __grid_constant__ GradArgs a) {
+  extern __shared__ uint4 ring[];
+  __shared__ struct {
+    float2 teach[THREADS / 32];
+    Adds adds;
+  } sm;
+  const int t = threadIdx.x;
+  const Place at(a.parts);
+  const float c2 = a.r.scale * kLog2e;
+  const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
+  const int K = a.loss && a.t.w_kd != 0.f ? a.t.K : 0;
+  Sender<T, THREADS> sender(a.r, ring, at, groups);
+  int id = given(a.r, at.first);
+  Upstream up = upstream<ENT>(a, at.first);
+  Entry e = {-1, -INFINITY};
+  if (t < K && at.first < a.r.S) e = load_entry(a.t, pos_of(a.r, at.first), t);
+  for (int r = at.first; r < a.r.S; r += at.stride) {
+    const int id_now = id;
+    const Upstream u = up;
+    const Entry entry = e;
+    const int p = pos_of(a.r, r);
+    if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
+    id = given(a.r, r + at.stride);
+    up = upstream<ENT>(a, r + at.stride);
+    if (t < K && r + at.stride < a.r.S) e = load_entry(a.t, pos_of(a.r, r + at.stride), t);
+    const RowPart<T> x(a.r, r, at.rank, at.parts);
+    T* out = reinterpret_cast<T*>(a.out) + (int64_t)r * a.ld_out;
+    uint4* dst = reinterpret_cast<uint4*>(out + x.head) + x.u_lo + t;
+    const int j0 = x.loose(t);
+    const bool flat = id_now == -1 || u.l == -INFINITY;
+    if (flat) {   // padding's groups have not been sent, an empty row's have
+      if (j0 >= 0) out[j0] = from_f<T>(0.f);
+      for (int i = t; i < x.n; i += THREADS) __stcs(dst + i - t, make_uint4(0, 0, 0, 0));
+      if (id_now != -1)
+        for (int g = 0; g < groups; ++g) {
+          copies_left_c<kStages - 1>();
+          sender.send();
+        }
+      continue;
     }
-  return first ? j : -1;
+    const float x0 = j0 >= 0 ? to_f<T>(x.row[j0]) : -INFINITY;
+    bool teacher = false;
+    int kid = -1;
+    if (K > 0) {
+      if (t < K) kid = token_of(entry, a.r);
+      teacher_part(kid >= 0, entry.y, a.t.scale, sm.teach);
+      __syncthreads();
+      const float2 whole = teacher_whole<THREADS>(a.t.scale, sm.teach);
+      teacher = whole.y != 0.f;
+      if (t < K) {
+        const bool here = kid >= x.lo && kid < x.hi;
+        sm.adds.id[t] = here ? kid : -1;
+        sm.adds.add[t] = -u.up * a.r.scale * a.t.w_kd * teacher_q(kid >= 0, entry.y, a.t.scale, whole).x;
+        if (here) sm.adds.z[t] = to_f<T>(x.row[kid]);
+      }
+    }
+    const Factors f = factors(a, u, teacher);
+    const Slope<ENT> slope(u.m, u.l, c2, f.A, f.B);
+    const bool adds_given = id_now >= 0 && (a.loss ? a.t.w_ce != 0.f : a.up != nullptr);
+    int own = -1;   // the group with the given token
+    if (K > 0) {
+      if (t == 0) {
+        const bool here = adds_given && id_now >= x.lo && id_now < x.hi;
+        sm.adds.id[K] = here ? id_now : -1;
+        sm.adds.add[K] = f.given;
+        if (here) sm.adds.z[K] = to_f<T>(x.row[id_now]);
+      }
+      end_adds(sm.adds, K + 1);
+      __syncthreads();   // the listed logits are read before any is overwritten
+    } else if (adds_given) {
+      own = group_with<T, THREADS>(x, id_now);
+    }
+    if (j0 >= 0) out[j0] = from_f<T>(slope.one(x0) + (K == 0 && adds_given && j0 == id_now ? f.given : 0.f));
+    for (int g = 0; g < groups; ++g, dst += kGroup * THREADS) {
+      copies_left_c<kStages - 1>();
+      uint4 v[kGroup];
+      const uint4* from = sender.place() + t;
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k) v[k] = from[k * THREADS];
+      const float z = g == own ? logit_in<T, THREADS>(sender.place(), x, id_now) : 0.f;
+      sender.send();
+      const int i = t + kGroup * g * THREADS;
+#pragma unroll
+      for (int k = 0; k < kGroup; ++k)
+        if (i + k * THREADS < x.n)
+          __stcs(dst + k * THREADS, slope.far ? far_grad<T, ENT>(v[k], slope) : unit_grad<T, ENT>(v[k], slope));
+      if (g == own) out[id_now] = from_f<T>(slope.one(z) + f.given);
+    }
+    if (K > 0) {
+      __syncthreads();   // the listed tokens' values go on top of what other threads wrote
+      for_added<THREADS>(sm.adds, K + 1, [&](int k, int j, float sum) {
+        out[j] = from_f<T>(slope.one(sm.adds.z[k]) + sum);
+      });
+    }
+  }
 }
 
-// A part of a row a CTA: dx_j = p_j (A + B log p_j), then the listed tokens' values
-// once more with what they add (the same token twice adds twice; the first of its
-// entries writes the value).
-template <typename T, bool ENT, int E>
-__global__ void __launch_bounds__(kThreads, 2) grad_kernel(const __grid_constant__ GradArgs a) {
-  constexpr int U = 4;
-  typedef typename std::conditional<E == 1, T, uint4>::type Unit;
-  __shared__ float part[kWarps][4];
-  __shared__ Adds adds;
-  const int t = threadIdx.x, threads = blockDim.x, r = blockIdx.x;
-  const int p = pos_of(r, a.r.c, a.r.D);
+// Rows and gradients that do not lie alike on 16-byte units: a part of a row a CTA,
+// element by element (8192 x 50257 bf16 at rows 50258 apart: see the table of figures).
+template <typename T, bool ENT>
+__global__ void __launch_bounds__(kMostThreads) grad_elements_kernel(const __grid_constant__ GradArgs a) {
+  constexpr int THREADS = kMostThreads, U = 8;
+  __shared__ struct {
+    float2 teach[THREADS / 32];
+    Adds adds;
+  } sm;
+  const int t = threadIdx.x, r = blockIdx.x, p = pos_of(a.r, r);
   if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
-  int64_t id = -1;
-  if (a.r.ids) id = load_id(a.r.ids, a.r.id_bytes, p);
-  if (id >= a.r.V) {
-    if (t == 0) report_status(a.r.status, (int)TSP_ERR_RANGE);
-    id = -1;
-  }
-  const float m = a.stats[2 * (int64_t)p], l = a.stats[2 * (int64_t)p + 1];
-  const bool live = !(a.r.ids && id < 0) && l != -INFINITY;
+  const int id = given(a.r, r), K = a.loss && a.t.w_kd != 0.f ? a.t.K : 0;
+  const int per = (a.r.V + gridDim.y - 1) / gridDim.y, lo = min(a.r.V, (int)blockIdx.y * per), hi = min(a.r.V, lo + per);
   const T* x = reinterpret_cast<const T*>(a.r.logits) + (int64_t)r * a.r.ld;
   T* out = reinterpret_cast<T*>(a.out) + (int64_t)r * a.ld_out;
-  const int head = E == 1 ? 0 : min(a.r.V, (int)((16 - ((uintptr_t)x & 15)) & 15) / (int)sizeof(T));
-  const int units = (a.r.V - head) / E, tail = head + units * E;
-  const Unit* xu = reinterpret_cast<const Unit*>(x + head);
-  Unit* ou = reinterpret_cast<Unit*>(out + head);
-  // the part of this CTA: units [u_lo, u_hi), and the loose elements with the first part
-  const int per = (units + gridDim.y - 1) / gridDim.y;
-  const int u_lo = min(units, (int)blockIdx.y * per), u_hi = min(units, u_lo + per);
-  const int lo = blockIdx.y == 0 ? 0 : head + u_lo * E;
-  const int hi = blockIdx.y == gridDim.y - 1 ? a.r.V : head + u_hi * E;
-  float A = 0.f, B = 0.f;
-  int n = 0;
-  const float c = a.r.scale, c2 = c * kLog2e, l2 = l * kLog2e;
-  float at_list[2] = {0.f, 0.f};   // logits of the listed tokens, read before they may be overwritten
-  if (live) {
-    const float up = a.up ? a.up[p] : 1.f;
-    if (a.loss) {
-      float w = a.t.w_ce;
-      if (a.t.K > 0 && a.t.w_kd != 0.f) {
-        float y = 0.f;
-        int kid = -1;
-        if (t < a.t.K) kid = teacher_entry(a.t, a.r, p, t, &y);
-        const int lane = t & 31, warp = t >> 5;
-        const float mw = warp_max(kid >= 0 ? y : -INFINITY);
-        if (lane == 0) part[warp][0] = mw;
-        __syncthreads();
-        float mt = -INFINITY;
-        for (int k = 0; k < threads / 32; ++k) mt = fmaxf(mt, part[k][0]);
-        const float e = kid >= 0 ? expf(a.t.scale * (y - mt)) : 0.f;
-        const float sw = warp_sum(e);
-        if (lane == 0) part[warp][1] = sw;
-        __syncthreads();
-        float se = 0.f;
-        for (int k = 0; k < threads / 32; ++k) se += part[k][1];
-        if (t < a.t.K) {
-          adds.id[t] = kid >= lo && kid < hi ? kid : -1;
-          adds.add[t] = -up * c * a.t.w_kd * (e / se);
-        }
-        n = a.t.K;
-        if (se != 0.f) w += a.t.w_kd;
-      }
-      A = up * c * w;
-      if (t == 0) {
-        adds.id[n] = id >= lo && id < hi && a.t.w_ce != 0.f ? (int)id : -1;
-        adds.add[n] = -up * c * a.t.w_ce;
-      }
-    } else {
-      const float de = ENT ? a.up_entropy[p] : 0.f;
-      A = a.up ? -c * up : 0.f;
-      if (ENT) {
-        A -= c * de * a.entropy[p];
-        B = -c * de * kLn2;
-      }
-      if (t == 0) {
-        adds.id[0] = a.up && id >= lo && id < hi ? (int)id : -1;
-        adds.add[0] = c * up;
-      }
+  const Upstream u = upstream<ENT>(a, r);
+  if (id == -1 || u.l == -INFINITY) {
+    for (int j = lo + t; j < hi; j += THREADS) out[j] = from_f<T>(0.f);
+    return;
+  }
+  bool teacher = false;
+  if (K > 0) {
+    Entry e = {-1, -INFINITY};
+    if (t < K) e = load_entry(a.t, p, t);
+    const int kid = t < K ? token_of(e, a.r) : -1;
+    teacher_part(kid >= 0, e.y, a.t.scale, sm.teach);
+    __syncthreads();
+    const float2 whole = teacher_whole<THREADS>(a.t.scale, sm.teach);
+    teacher = whole.y != 0.f;
+    if (t < K) {
+      const bool here = kid >= lo && kid < hi;
+      sm.adds.id[t] = here ? kid : -1;
+      sm.adds.add[t] = -u.up * a.r.scale * a.t.w_kd * teacher_q(kid >= 0, e.y, a.t.scale, whole).x;
+      if (here) sm.adds.z[t] = to_f<T>(x[kid]);
     }
-    ++n;
-    end_adds(adds, n, t);
-    __syncthreads();
-    for (int k = t, i = 0; k < n; k += threads, ++i)
-      if (adds.id[k] >= 0) at_list[i] = to_f<T>(x[adds.id[k]]);
-    __syncthreads();
   }
-  auto grad = [&](float2 v) {
-    if (!live) return make_float2(0.f, 0.f);
-    const float2 u = ffma2(fadd2(v, make_float2(-m, -m)), make_float2(c2, c2), make_float2(-l2, -l2));
-    const float2 q = make_float2(ex2_approx(u.x), ex2_approx(u.y));
-    float2 w = make_float2(A, A);
-    if (ENT) w = ffma2(make_float2(fmaxf(u.x, kLeast), fmaxf(u.y, kLeast)), make_float2(B, B), w);
-    return fmul2(q, w);
-  };
-  if (E > 1 && t < 2 * E) {
-    const int j = t < head ? t : tail + t - head;
-    if (j < a.r.V && (j < head ? blockIdx.y == 0 : blockIdx.y == gridDim.y - 1))
-      out[j] = from_f<T>(grad(make_float2(live ? to_f<T>(x[j]) : 0.f, 0.f)).x);
+  const Factors f = factors(a, u, teacher);
+  const Slope<ENT> slope(u.m, u.l, a.r.scale * kLog2e, f.A, f.B);
+  if (t == 0) {
+    const bool here = id >= lo && id < hi && (a.loss ? a.t.w_ce != 0.f : a.up != nullptr);
+    sm.adds.id[K] = here ? id : -1;
+    sm.adds.add[K] = f.given;
+    if (here) sm.adds.z[K] = to_f<T>(x[id]);
   }
-  for (int u0 = u_lo + t; u0 < u_hi; u0 += U * threads) {
-    Unit v[U];
+  end_adds(sm.adds, K + 1);
+  __syncthreads();
+  for (int j = lo + t; j < hi; j += U * THREADS) {
+    T v[U];
 #pragma unroll
     for (int k = 0; k < U; ++k)
-      if (live && u0 + k * threads < u_hi) {
-        if constexpr (E == 1) v[k] = xu[u0 + k * threads];
-        else v[k] = load_unit(xu + u0 + k * threads);
-      }
+      if (j + k * THREADS < hi) v[k] = x[j + k * THREADS];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (u0 + k * threads >= u_hi) continue;
-      if constexpr (E == 1) {
-        ou[u0 + k * threads] = from_f<T>(grad(make_float2(live ? to_f<T>(v[k]) : 0.f, 0.f)).x);
-      } else if (!live) {
-        ou[u0 + k * threads] = make_uint4(0, 0, 0, 0);
-      } else if constexpr (sizeof(T) == 2) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 g = grad(pair<T>(v[k], e));
-          w[e] = pack2<T>(g.x, g.y);
-        }
-        __stcs(ou + u0 + k * threads, make_uint4(w[0], w[1], w[2], w[3]));
-      } else {
-        const float2 g = grad(pair<T>(v[k], 0)), h = grad(pair<T>(v[k], 1));
-        __stcs(ou + u0 + k * threads, make_uint4(__float_as_uint(g.x), __float_as_uint(g.y),
-                                                 __float_as_uint(h.x), __float_as_uint(h.y)));
-      }
-    }
+    for (int k = 0; k < U; ++k)
+      if (j + k * THREADS < hi) out[j + k * THREADS] = from_f<T>(slope.one(to_f<T>(v[k])));
   }
-  if (!live) return;
   __syncthreads();
-  for (int k = t, i = 0; k < n; k += threads, ++i) {
-    float sum;
-    const int j = added(adds, n, k, &sum);
-    if (j >= 0) out[j] = from_f<T>(grad(make_float2(at_list[i], 0.f)).x + sum);
-  }
+  for_added<THREADS>(sm.adds, K + 1, [&](int k, int j, float sum) {
+    out[j] = from_f<T>(slope.one(sm.adds.z[k]) + sum);
+  });
 }
 
 // ---------------------------------------------------------------------------
 // Loss and gradient in one pass
 // ---------------------------------------------------------------------------
 // A row stays in shared memory between its sum and its gradient, so that it is read
-// once and written once.  A CTA, or for long rows a cluster whose CTAs hold a part
-// each, takes one row after the other; its threads copy the next row's units into the
-// places whose gradient they have just written, so that reading goes on while the
-// sums are joined.  A thread copies what it will itself read: the data need no barrier.
-// Between the CTAs of a cluster go, through distributed shared memory, their sums and
-// the logits of the listed tokens.
-constexpr int kOneThreads = 256, kOneCtas = 3;
-constexpr int kOnePassPart = 66 * 1024;    // bytes of a row a CTA: three CTAs a multiprocessor
-constexpr int kOnePassMost = 200 * 1024;   // ... of the longest rows: one
-
-__device__ __forceinline__ void copy_unit(uint4* dst, const uint4* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copies_left_c() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-// until at most n (or eight) of the groups sent last are on their way
-__device__ __forceinline__ void copies_left(int n) {
-  switch (n) {
-    case 0: copies_left_c<0>(); break;
-    case 1: copies_left_c<1>(); break;
-    case 2: copies_left_c<2>(); break;
-    case 3: copies_left_c<3>(); break;
-    case 4: copies_left_c<4>(); break;
-    case 5: copies_left_c<5>(); break;
-    case 6: copies_left_c<6>(); break;
-    case 7: copies_left_c<7>(); break;
-    default: copies_left_c<8>();
-  }
-}
-
+// once and written once.  The next row's units are sent for into the places whose
+// gradient has just been written.  Between the CTAs of a cluster go, through distributed
+// shared memory, their sums and the logits of the listed tokens.
 struct OnePassArgs {
   GradArgs g;
   float *loss, *stats;
 };
-// What the CTAs of a cluster write into each other: of two rows, since one of them may
-// be a row ahead.
-struct Exchange {
-  float2 share[8];               // (largest logit, sum) of each part
-  float target, z[TSP_TOP_MAX];  // (in the first CTA) logits of the given and the teacher's tokens
-};
-struct OnePassSmem {
-  float part[kOneThreads / 32][4], teach[kOneThreads / 32][2];
-  Exchange ex[2];
-  Adds adds;                     // of this part
-  float z[TSP_TOP_MAX + 1];      // the listed tokens' logits
-  float q[TSP_TOP_MAX], logq[TSP_TOP_MAX];
-  float loose[16];
-};
 
-template <typename T, bool CLUSTER>
-__global__ void __launch_bounds__(kOneThreads, kOneCtas) one_pass_kernel(const __grid_constant__ OnePassArgs o) {
-  constexpr int E = 16 / sizeof(T), U = 4;
+template <typename T, bool CLUSTER, int THREADS>
+__global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const __grid_constant__ OnePassArgs o) {
   extern __shared__ uint4 seg[];
-  __shared__ OnePassSmem sm;
+  __shared__ struct {
+    float4 part[2][THREADS / 32];
+    float2 teach[THREADS / 32];
+    Exchange ex[2];
+    Adds adds;                     // of this part
+    float q[TSP_TOP_MAX], logq[TSP_TOP_MAX];
+    float loose[16];
+  } sm;
   const GradArgs& a = o.g;
-  const int t = threadIdx.x, threads = blockDim.x, lane = t & 31, warp = t >> 5;
   const auto cluster = cooperative_groups::this_cluster();
-  const int rank = CLUSTER ? (int)cluster.block_rank() : 0;
-  const int parts = CLUSTER ? (int)cluster.num_blocks() : 1;
-  const int stride = gridDim.x / parts;
-  const float c = a.r.scale, c2 = c * kLog2e, low = lowest<T>(), slack = kSlack / c2;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const Place at(CLUSTER ? a.parts : 1);
+  const float c = a.r.scale, c2 = c * kLog2e;
+  const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
   const int K = a.t.w_kd != 0.f ? a.t.K : 0;
-  // the units of a row that are this part's
-  struct Part {
-    const uint4* src;
-    int u_lo, n;
-  };
-  auto part_of = [&](const RowUnits<T>& row) {
-    const int per = (row.units + parts - 1) / parts, u_lo = min(row.units, rank * per);
-    return Part{row.first() + u_lo, u_lo, min(row.units, u_lo + per) - u_lo};
-  };
-  auto given = [&](int r) {   // a row's token: -1 for padding, -2 without tokens
-    if (r >= a.r.S || !a.r.ids) return -2;
-    const int64_t id = load_id(a.r.ids, a.r.id_bytes, pos_of(r, a.r.c, a.r.D));
-    if (id >= a.r.V && t == 0) report_status(a.r.status, (int)TSP_ERR_RANGE);
-    return id >= 0 && id < a.r.V ? (int)id : -1;
-  };
-  // the copies of a row's units i + k * threads, k < U
-  auto send = [&](const Part& x, int i) {
-#pragma unroll
-    for (int k = 0; k < U; ++k)
-      if (i + k * threads < x.n) copy_unit(seg + i + k * threads, x.src + i + k * threads);
-    copies_sent();
-  };
-  const int most = (a.r.V / E + parts - 1) / parts;      // units of a part at most
-  const int groups = (most + U * threads - 1) / (U * threads);
-  int r = CLUSTER ? blockIdx.x / parts : blockIdx.x;
-  int id = given(r);
+  int id = given(a.r, at.first);
   // (the CTAs of a cluster have started before one writes into another's memory)
   if (CLUSTER) cluster.sync();
   bool there = false;   // this row's copies have been sent
-  for (int turn = 0; r < a.r.S; r += stride) {
-    const int p = pos_of(r, a.r.c, a.r.D);
+  int turn = 0;
+  for (int r = at.first; r < a.r.S; r += at.stride) {
+    const int p = pos_of(a.r, r), id_now = id;
     if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
-    const bool live = id != -1;
-    const RowUnits<T> row(a.r.logits, a.r.ld, r, a.r.V);
-    const Part x = part_of(row);
-    const int lo = rank == 0 ? 0 : row.head + x.u_lo * E;
-    const int hi = rank == parts - 1 ? a.r.V : row.head + (x.u_lo + x.n) * E;
+    id = given(a.r, r + at.stride);
+    const RowPart<T> x(a.r, r, at.rank, at.parts);
     T* out = reinterpret_cast<T*>(a.out) + (int64_t)r * a.ld_out;
-    uint4* dst = reinterpret_cast<uint4*>(out + row.head) + x.u_lo;
-    const int j0 = t < 2 * E ? row.loose(t) : -1;
-    const bool mine = j0 >= lo && j0 < hi;   // a loose element of this part
-    const int id_next = given(r + stride);
-    Exchange& ex = sm.ex[turn];
-    float m = 0.f, l = -INFINITY, A = 0.f, x0 = -INFINITY;
-    int n = 0;
-    if (live) {
-      if (!there)
-        for (int g = 0; g < groups; ++g) send(x, t + U * g * threads);
-      if (mine) x0 = to_f<T>(row.row[j0]);
-      float y = 0.f;
-      int kid = -1;
-      if (t < K) kid = teacher_entry(a.t, a.r, p, t, &y);
-      const float up = a.up ? a.up[p] : 1.f;
-      Sums<false> sums(low);
+    uint4* dst = reinterpret_cast<uint4*>(out + x.head) + x.u_lo + t;
+    const int j0 = x.loose(t);
+    const bool sent = there;
+    there = r + at.stride < a.r.S && id != -1;
+    RowPart<T> next(a.r, there ? r + at.stride : r, at.rank, at.parts);
+    Stats st = {0.f, -INFINITY, 0.f};
+    float x0 = -INFINITY, up = 1.f, target = 0.f;
+    bool teacher = false;
+    if (id_now != -1) {
+      if (!sent)
+        for (int g = 0; g < groups; ++g) send_group<T, THREADS>(seg + kGroup * g * THREADS, x, g);
+      if (j0 >= 0) x0 = to_f<T>(x.row[j0]);
+      if (t == 0 && id_now >= 0) target = to_f<T>(x.row[id_now]);
+      if (a.up) up = a.up[p];
+      Entry e = {-1, -INFINITY};
+      if (t < K) e = load_entry(a.t, p, t);
+      Sums<false> sums;
       for (int g = 0; g < groups; ++g) {
         copies_left(groups - 1 - g);
-        const int i = t + U * g * threads;
-        if (i + (U - 1) * threads < x.n) {
-          uint4 v[U];
+        uint4 v[kGroup];
+        const uint4* from = seg + t + kGroup * g * THREADS;
 #pragma unroll
-          for (int k = 0; k < U; ++k) v[k] = seg[i + k * threads];
-          sums.see(largest<T, U>(v), c2, slack);
-#pragma unroll
-          for (int k = 0; k < U; ++k)
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) sums.add(pair<T>(v[k], e), c2);
-        } else {
-          for (int k = i; k < x.n; k += threads) {
-            const uint4 v[1] = {seg[k]};
-            sums.see(largest<T, 1>(v), c2, slack);
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) sums.add(pair<T>(v[0], e), c2);
-          }
-        }
+        for (int k = 0; k < kGroup; ++k) v[k] = from[k * THREADS];
+        sums.template add_units<T, kGroup>(v, c2, two(c2, c2));
       }
-      sums.see(x0, c2, slack);
-      sums.add(make_float2(x0, -INFINITY), c2);
-      if (mine) sm.loose[t] = x0;
+      sums.see(x0, c2);
+      sums.add(two(x0, -INFINITY), two(c2, c2));
+      int kid = -1;
       if (K > 0) {
-        const float mw = warp_max(kid >= 0 ? y : -INFINITY);
-        const float sw = warp_sum(kid >= 0 ? expf(a.t.scale * (y - mw)) : 0.f);
-        if (lane == 0) {
-          sm.teach[warp][0] = mw;
-          sm.teach[warp][1] = sw;
-        }
+        if (t < K) kid = token_of(e, a.r);
+        if (j0 >= 0) sm.loose[t] = x0;
+        teacher_part(kid >= 0, e.y, a.t.scale, sm.teach);
       }
-      float s;
-      join_sums<false>(sums, low, c2, sm.part, &m, &s, nullptr);
-      // every logit of this part is in shared memory: hand on the listed ones
-      auto logit = [&](int j) {
-        return j < row.head    ? sm.loose[j]
-               : j >= row.tail ? sm.loose[row.head + j - row.tail]
-                               : to_f<T>(reinterpret_cast<const T*>(seg)[j - row.head - x.u_lo * E]);
+      if constexpr (CLUSTER) {
+        // (the listed logits go with the sums: every thread's units are there behind this)
+        if (K > 0) __syncthreads();
+      }
+      auto hand_on = [&] {   // the logits of the listed tokens that are in this part
+        auto logit = [&](int j) {
+          return j < x.head    ? sm.loose[j]
+                 : j >= x.tail ? sm.loose[x.head + j - x.tail]
+                               : to_f<T>(reinterpret_cast<const T*>(seg)[j - x.head - x.u_lo * RowPart<T>::E]);
+        };
+        Exchange* first = CLUSTER ? cluster.map_shared_rank(&sm.ex[turn], 0) : &sm.ex[turn];
+        const bool here = kid >= x.lo && kid < x.hi;
+        if (t < K) sm.adds.id[t] = here ? kid : -1;
+        if (here) first->z[t] = sm.adds.z[t] = logit(kid);
+        if (t == 0) {
+          const bool given_here = id_now >= x.lo && id_now < x.hi && a.t.w_ce != 0.f;
+          sm.adds.id[K] = given_here ? id_now : -1;
+          if (given_here) sm.adds.z[K] = logit(id_now);
+        }
+        end_adds(sm.adds, K + 1);
       };
-      Exchange* first = CLUSTER ? cluster.map_shared_rank(&ex, 0) : &ex;
-      const bool here = kid >= lo && kid < hi, given_here = id >= lo && id < hi;
-      if (here) first->z[t] = sm.z[t] = logit(kid);
-      if (t == 0 && given_here) first->target = sm.z[K] = logit(id);
-      if (CLUSTER) {
-        if (t < parts) cluster.map_shared_rank(&ex, t)->share[rank] = make_float2(m, s);
-        cluster.sync();
-        m = low;
-        for (int k = 0; k < parts; ++k) m = fmaxf(m, ex.share[k].x);
-        s = 0.f;
-        for (int k = 0; k < parts; ++k)
-          s += ex.share[k].y * ex2_approx(fmaxf((ex.share[k].x - m) * c2, kLeast));
-      }
-      if (s == 0.f) m = 0.f;
-      l = s == 0.f ? -INFINITY : logf(s);
-      float w = a.t.w_ce;
+      if (CLUSTER && K > 0) hand_on();
+      st = statistics<T, false, CLUSTER, THREADS>(sums, seg, x.n, x0, c2, sm.part[turn], &sm.ex[turn], at.rank,
+                                                  at.parts);
       if (K > 0) {
-        const float from = lane < threads / 32 ? sm.teach[lane][0] : -INFINITY, mt = warp_max(from);
-        float se = lane < threads / 32 ? sm.teach[lane][1] : 0.f;
-        if (se != 0.f) se *= expf(a.t.scale * (from - mt));
-        se = warp_sum(se);
+        if (!CLUSTER) hand_on();
+        const float2 whole = teacher_whole<THREADS>(a.t.scale, sm.teach);
+        teacher = whole.y != 0.f;
         if (t < K) {
-          const float logq = a.t.scale * (y - mt) - logf(se), q = kid >= 0 ? expf(a.t.scale * (y - mt)) / se : 0.f;
-          sm.q[t] = q;
-          sm.logq[t] = logq;
-          sm.adds.id[t] = here ? kid : -1;
-          sm.adds.add[t] = -up * c * a.t.w_kd * q;
+          const float2 q = teacher_q(kid >= 0, e.y, a.t.scale, whole);
+          sm.q[t] = q.x;
+          sm.logq[t] = q.y;
+          sm.adds.add[t] = -up * c * a.t.w_kd * q.x;
         }
-        if (se != 0.f) w += a.t.w_kd;
+        if (t == 0) sm.adds.add[K] = -up * c * a.t.w_ce;
+        __syncthreads();   // the listed logits are read before the next row comes in
       }
-      if (t == 0) {
-        sm.adds.id[K] = given_here && a.t.w_ce != 0.f ? id : -1;
-        sm.adds.add[K] = -up * c * a.t.w_ce;
-      }
-      end_adds(sm.adds, K + 1, t);
-      A = up * c * w;
-      n = l == -INFINITY ? 0 : K + 1;
-      if (!CLUSTER) __syncthreads();   // (the listed logits are read before the next row comes in)
     }
-    const bool flat = !live || l == -INFINITY;   // a zero gradient
-    const float l2 = l * kLog2e;
-    auto grad = [&](float2 v) {
-      const float2 u = ffma2(fadd2(v, make_float2(-m, -m)), make_float2(c2, c2), make_float2(-l2, -l2));
-      return fmul2(make_float2(ex2_approx(u.x), ex2_approx(u.y)), make_float2(A, A));
-    };
-    if (mine) out[j0] = from_f<T>(flat ? 0.f : grad(make_float2(x0, 0.f)).x);
-    there = r + stride < a.r.S && id_next != -1;
-    Part next = {nullptr, 0, 0};
-    if (there) next = part_of(RowUnits<T>(a.r.logits, a.r.ld, r + stride, a.r.V));
-    auto put_unit = [&](int i) {
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (!flat) {
-        const uint4 v = seg[i];
-        if constexpr (sizeof(T) == 2) {
-          const float2 g0 = grad(pair<T>(v, 0)), g1 = grad(pair<T>(v, 1));
-          const float2 g2 = grad(pair<T>(v, 2)), g3 = grad(pair<T>(v, 3));
-          w = make_uint4(pack2<T>(g0.x, g0.y), pack2<T>(g1.x, g1.y), pack2<T>(g2.x, g2.y),
-                         pack2<T>(g3.x, g3.y));
-        } else {
-          const float2 g0 = grad(pair<T>(v, 0)), g1 = grad(pair<T>(v, 1));
-          w = make_uint4(__float_as_uint(g0.x), __float_as_uint(g0.y), __float_as_uint(g1.x),
-                         __float_as_uint(g1.y));
-        }
+    const bool flat = id_now == -1 || st.l == -INFINITY;   // a zero gradient
+    const float by_given = -up * c * a.t.w_ce;
+    const Slope<false> slope(st.m, st.l, c2, up * c * (a.t.w_ce + (teacher ? a.t.w_kd : 0.f)), 0.f);
+    const bool adds_given = K == 0 && !flat && id_now >= 0 && a.t.w_ce != 0.f;
+    if (j0 >= 0) out[j0] = from_f<T>(flat ? 0.f : slope.one(x0) + (adds_given && j0 == id_now ? by_given : 0.f));
+    if (flat || slope.far) {
+      for (int g = 0; g < groups; ++g) {
+        for (int k = 0, i = t + kGroup * g * THREADS; k < kGroup && i < x.n; ++k, i += THREADS)
+          __stcs(dst + i - t, flat ? make_uint4(0, 0, 0, 0) : far_grad<T, false>(seg[i], slope));
+        if (adds_given && group_with<T, THREADS>(x, id_now) == g)
+          out[id_now] = from_f<T>(slope.one(logit_in<T, THREADS>(seg + kGroup * g * THREADS, x, id_now)) + by_given);
+        if (there) send_group<T, THREADS>(seg + kGroup * g * THREADS, next, g);
       }
-      __stcs(dst + i, w);
-    };
-    for (int g = 0; g < groups; ++g) {
-      const int i0 = t + U * g * threads;
-      if (i0 + (U - 1) * threads < x.n) {
+    } else {
+      const int own = adds_given ? group_with<T, THREADS>(x, id_now) : -1;   // the group with the given token
+      for (int g = 0; g < groups; ++g, dst += kGroup * THREADS) {
+        uint4* place = seg + kGroup * g * THREADS;
+        const int i = t + kGroup * g * THREADS;
 #pragma unroll
-        for (int k = 0; k < U; ++k) put_unit(i0 + k * threads);
-      } else {
-        for (int i = i0; i < x.n; i += threads) put_unit(i);
-      }
-      if (there) send(next, i0);
-    }
-    if (live) {
-      __syncthreads();   // the listed tokens' values go on top of what other threads wrote
-      auto put = [&](int k) {
-        float sum;
-        const int j = added(sm.adds, n, k, &sum);
-        if (j >= 0) out[j] = from_f<T>(grad(make_float2(sm.z[k], 0.f)).x + sum);
-      };
-      if (t < K && n > 0) put(t);
-      if (t == 0 && n > 0) put(K);
-    }
-    if (rank == 0 && warp == 0) {
-      float loss = 0.f;
-      if (live) {
-        if (a.t.w_ce != 0.f && id >= 0) loss = -a.t.w_ce * (l == -INFINITY ? l : c * (ex.target - m) - l);
-        float kd = 0.f;
-        bool any = false;
-        for (int k = lane; k < K; k += 32) {
-          const float q = sm.q[k];
-          any |= q != 0.f;
-          if (q != 0.f) kd += q * (sm.logq[k] - (l == -INFINITY ? l : c * (ex.z[k] - m) - l));
+        for (int k = 0; k < kGroup; ++k) {
+          const uint4 v = unit_grad<T, false>(place[t + k * THREADS], slope);
+          if (i + k * THREADS < x.n) __stcs(dst + k * THREADS, v);
         }
-        kd = warp_sum(kd);
-        if (__any_sync(0xffffffffu, any)) loss += a.t.w_kd * kd;
+        if (g == own) out[id_now] = from_f<T>(slope.one(logit_in<T, THREADS>(place, x, id_now)) + by_given);
+        if (there) send_group<T, THREADS>(place, next, g);
+      }
+    }
+    if (id_now != -1 && K > 0) {
+      __syncthreads();   // the listed tokens' values go on top of what other threads wrote
+      if (!flat)
+        for_added<THREADS>(sm.adds, K + 1, [&](int k, int j, float sum) {
+          out[j] = from_f<T>(slope.one(sm.adds.z[k]) + sum);
+        });
+    }
+    if (at.rank == 0 && warp == 0) {
+      float loss = 0.f;
+      if (id_now != -1) {
+        if (id_now >= 0 && a.t.w_ce != 0.f) loss = -a.t.w_ce * log_p(target, st, c);
+        if (K > 0) {
+          float kd = 0.f;
+          for (int k = lane; k < K; k += 32) {
+            const float q = sm.q[k];
+            if (q != 0.f) kd += q * (sm.logq[k] - log_p(sm.ex[turn].z[k], st, c));
+          }
+          kd = lanes_sum<32>(kd);
+          if (teacher) loss += a.t.w_kd * kd;
+        }
       }
       if (lane == 0) {
         o.loss[p] = loss;
-        o.stats[2 * (int64_t)p] = m;
-        o.stats[2 * (int64_t)p + 1] = l;
+        o.stats[2 * (int64_t)p] = st.m;
+        o.stats[2 * (int64_t)p + 1] = st.l;
       }
     }
-    if (live) turn ^= 1;
-    id = id_next;
+    if (id_now != -1) turn ^= 1;
   }
 }
 
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
 Rows rows_of(const tsp_logits& x, const void* ids, int id_bytes) {
   Rows r;
   r.logits = x.logits;
@@ -942,69 +1258,8 @@ Teacher teacher_of(const tsp_teacher* t, float w_ce) {
   return k;
 }
 
-// Threads of a CTA for rows of V elements and lists of n: one for each unit up to 512.
-int threads_for(int64_t V, int dtype, int n) {
-  const int64_t units = V * (dtype == TSP_F32 ? 4 : 2) / 16;
-  int t = 128;
-  while (t < kThreads && (t < n || t * 4 <= units)) t *= 2;
-  return t;
-}
-
-tsp_status launch_fwd(const FwdArgs& a, int dtype, const char* name, cudaStream_t st) {
-  Prof prof(name, st);
-  const int threads = threads_for(a.r.V, dtype, std::max(a.top, a.t.K));
-  const bool ent = a.entropy != nullptr;
-  if (dtype == TSP_BF16)
-    ent ? fwd_kernel<__nv_bfloat16, true><<<a.r.S, threads, 0, st>>>(a)
-        : fwd_kernel<__nv_bfloat16, false><<<a.r.S, threads, 0, st>>>(a);
-  else
-    ent ? fwd_kernel<float, true><<<a.r.S, threads, 0, st>>>(a)
-        : fwd_kernel<float, false><<<a.r.S, threads, 0, st>>>(a);
-  TSP_CUDA_TRY(cudaGetLastError());
-  return TSP_OK;
-}
-
-template <typename T>
-bool alike(const GradArgs& a) {   // rows that lie alike on 16-byte units
-  return ((uintptr_t)a.r.logits - (uintptr_t)a.out) % 16 == 0 &&
-         (a.r.S == 1 || (a.r.ld - a.ld_out) * (int64_t)sizeof(T) % 16 == 0);
-}
-
-template <typename T, bool ENT>
-void grad_t(const GradArgs& a, dim3 grid, int threads, cudaStream_t st) {
-  // rows that lie alike on 16-byte units are read and written in units, others by element
-  if (alike<T>(a)) grad_kernel<T, ENT, 16 / (int)sizeof(T)><<<grid, threads, 0, st>>>(a);
-  else grad_kernel<T, ENT, 1><<<grid, threads, 0, st>>>(a);
-}
-tsp_status launch_grad(const GradArgs& a, int dtype, const char* name, cudaStream_t st) {
-  Prof prof(name, st);
-  const int threads = threads_for(a.r.V, dtype, a.t.K);
-  const int64_t units = (int64_t)a.r.V * (dtype == TSP_F32 ? 4 : 2) / 16;
-  const dim3 grid(a.r.S, (unsigned)std::min<int64_t>(1024, std::max<int64_t>(1, units / (16 * threads))));
-  const bool ent = a.up_entropy != nullptr;
-  if (dtype == TSP_BF16)
-    ent ? grad_t<__nv_bfloat16, true>(a, grid, threads, st)
-        : grad_t<__nv_bfloat16, false>(a, grid, threads, st);
-  else
-    ent ? grad_t<float, true>(a, grid, threads, st) : grad_t<float, false>(a, grid, threads, st);
-  TSP_CUDA_TRY(cudaGetLastError());
-  return TSP_OK;
-}
-
-// The most dynamic shared memory a kernel may be launched with, set once.
-template <auto KERNEL>
-tsp_status allow_smem(int most) {
-  static std::atomic<bool> set[kMaxDevices];
-  const int dev = current_device();
-  if (!set[dev]) {
-    TSP_CUDA_TRY(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
-    set[dev] = true;
-  }
-  return TSP_OK;
-}
-
-// How many clusters (CTAs, if those are alone) of a launch the GPU holds at once,
-// looked up once for each kind of launch: a persistent grid takes as many.
+// How many clusters of `parts` CTAs (CTAs, if parts is 1) of a kernel the GPU holds at
+// once, looked up once for each kind of launch: a grid takes as many.
 int64_t resident(const void* kernel, const cudaLaunchConfig_t& cfg, int parts) {
   struct Known {
     const void* kernel;
@@ -1020,26 +1275,42 @@ int64_t resident(const void* kernel, const cudaLaunchConfig_t& cfg, int parts) {
     if (k.kernel == kernel && k.smem == cfg.dynamicSmemBytes && k.dev == dev && k.parts == parts && k.threads == threads)
       return k.n;
   int n = 0;
+  cudaError_t e;
   if (parts > 1) {
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
-  } else if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, cfg.dynamicSmemBytes) == cudaSuccess) {
-    n *= num_sms();
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
   } else {
-    n = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, cfg.dynamicSmemBytes);
+    n *= num_sms();
   }
-  n = n > 0 ? n : std::max(1, num_sms() / parts);
+  if (e != cudaSuccess || n < 1) n = std::max(1, num_sms() / parts);
   known[at++ % 32] = {kernel, cfg.dynamicSmemBytes, dev, parts, threads, n};
   return n;
 }
 
-template <typename T, bool CLUSTER>
-tsp_status launch_one_pass_c(const OnePassArgs& o, int parts, cudaStream_t st) {
-  const int64_t per = ((int64_t)o.g.r.V * sizeof(T) / 16 + parts - 1) / parts;
-  int threads = 128;
-  while (threads < kOneThreads && (threads < o.g.t.K || threads * 4 <= per)) threads *= 2;
+// The most dynamic shared memory a kernel may be launched with, set once.
+template <auto KERNEL>
+tsp_status allow_smem(int most) {
+  static std::atomic<bool> set[kMaxDevices];
+  const int dev = current_device();
+  if (!set[dev]) {
+    TSP_CUDA_TRY(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    set[dev] = true;
+  }
+  return TSP_OK;
+}
+
+constexpr int kOnePassMost = 200 * 1024;   // bytes of a part of the longest rows
+constexpr int kRingMost = kStages * kGroup * kMostThreads * 16;
+// S rows on as many CTAs (clusters of `parts` with CLUSTER, groups of `parts` without)
+// as fit at once.  MOST: dynamic shared memory at most.
+template <auto KERNEL, bool CLUSTER, int MOST, typename A>
+tsp_status launch_rows(const A& a, int S, int threads, int parts, size_t smem, const char* name, cudaStream_t st) {
+  tsp_status r = allow_smem<KERNEL>(MOST);
+  if (r != TSP_OK) return r;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = (size_t)per * 16;
+  cfg.gridDim = dim3(parts);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -1047,27 +1318,95 @@ tsp_status launch_one_pass_c(const OnePassArgs& o, int parts, cudaStream_t st) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = CLUSTER ? 1 : 0;
-  constexpr auto kernel = one_pass_kernel<T, CLUSTER>;
-  const tsp_status r = allow_smem<kernel>(kOnePassMost);
-  if (r != TSP_OK) return r;
-  cfg.gridDim = dim3((unsigned)parts);
-  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(o.g.r.S, resident((const void*)kernel, cfg, parts)) * parts));
-  Prof prof("token_loss_one_pass", st);
-  TSP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, o));
+  const int64_t fit = CLUSTER ? resident((const void*)KERNEL, cfg, parts)
+                              : std::max<int64_t>(1, resident((const void*)KERNEL, cfg, 1) / parts);
+  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(S, fit) * parts));
+  Prof prof(name, st);
+  TSP_CUDA_TRY(cudaLaunchKernelEx(&cfg, KERNEL, a));
   return TSP_OK;
 }
+
+// Threads of a CTA for parts of `per` units and lists of n.
+int threads_for(int64_t per, int n) { return per <= 3 * kGroup * 128 && n <= 128 ? 128 : kMostThreads; }
+// CTAs a row where there are few rows: until the GPU is full, of 4 KB at least.
+int parts_for(int64_t S, int64_t units, int parts) {
+  while (parts <= 4 && S * parts * 2 <= num_sms() * 2 && units / (2 * parts) >= 256) parts *= 2;
+  return parts;
+}
+size_t ring_bytes(int threads) { return (size_t)kStages * kGroup * threads * 16; }
+
+template <typename T, bool ENT, bool CLUSTER>
+tsp_status launch_fwd_c(const FwdArgs& a, int threads, const char* name, cudaStream_t st) {
+  if (threads == 128)
+    return launch_rows<fwd_kernel<T, ENT, CLUSTER, 128>, CLUSTER, kRingMost>(a, a.r.S, 128, a.parts, ring_bytes(128), name, st);
+  return launch_rows<fwd_kernel<T, ENT, CLUSTER, 256>, CLUSTER, kRingMost>(a, a.r.S, 256, a.parts, ring_bytes(256), name, st);
+}
 template <typename T>
-tsp_status launch_one_pass_t(const OnePassArgs& o, int parts, cudaStream_t st) {
-  return parts > 1 ? launch_one_pass_c<T, true>(o, parts, st) : launch_one_pass_c<T, false>(o, parts, st);
+tsp_status launch_fwd_t(FwdArgs a, const char* name, cudaStream_t st) {
+  const int64_t units = (int64_t)a.r.V * sizeof(T) / 16;
+  a.parts = parts_for(a.r.S, units, 1);
+  const int threads = threads_for((units + a.parts - 1) / a.parts, std::max(a.top, a.t.K));
+  if (a.entropy)
+    return a.parts > 1 ? launch_fwd_c<T, true, true>(a, threads, name, st)
+                       : launch_fwd_c<T, true, false>(a, threads, name, st);
+  return a.parts > 1 ? launch_fwd_c<T, false, true>(a, threads, name, st)
+                     : launch_fwd_c<T, false, false>(a, threads, name, st);
+}
+tsp_status launch_fwd(const FwdArgs& a, int dtype, const char* name, cudaStream_t st) {
+  return dtype == TSP_BF16 ? launch_fwd_t<__nv_bfloat16>(a, name, st) : launch_fwd_t<float>(a, name, st);
 }
 
-// CTAs a row for the loss with its gradient: parts of 66 KB at most, 200 KB in
-// clusters of eight; for few rows more, down to 4 KB.  0: the row is too long.
+// Rows and gradients that lie alike on 16-byte units.
+template <typename T>
+bool alike(const GradArgs& a) {
+  return ((uintptr_t)a.r.logits - (uintptr_t)a.out) % 16 == 0 &&
+         (a.r.S == 1 || (a.r.ld - a.ld_out) * (int64_t)sizeof(T) % 16 == 0);
+}
+
+template <typename T, bool ENT>
+tsp_status launch_grad_t(GradArgs a, const char* name, cudaStream_t st) {
+  const int64_t units = (int64_t)a.r.V * sizeof(T) / 16;
+  if (!alike<T>(a)) {
+    const int64_t parts = std::min<int64_t>(1024, std::max<int64_t>(1, a.r.V / (32 * kMostThreads)));
+    Prof prof(name, st);
+    grad_elements_kernel<T, ENT><<<dim3(a.r.S, (unsigned)parts), kMostThreads, 0, st>>>(a);
+    TSP_CUDA_TRY(cudaGetLastError());
+    return TSP_OK;
+  }
+  a.parts = parts_for(a.r.S, units, 1);
+  const int threads = threads_for((units + a.parts - 1) / a.parts, a.t.K);
+  if (threads == 128)
+    return launch_rows<grad_kernel<T, ENT, 128>, false, kRingMost>(a, a.r.S, 128, a.parts, ring_bytes(128), name, st);
+  return launch_rows<grad_kernel<T, ENT, 256>, false, kRingMost>(a, a.r.S, 256, a.parts, ring_bytes(256), name, st);
+}
+tsp_status launch_grad(const GradArgs& a, int dtype, const char* name, cudaStream_t st) {
+  const bool ent = a.up_entropy != nullptr;
+  if (dtype == TSP_BF16)
+    return ent ? launch_grad_t<__nv_bfloat16, true>(a, name, st) : launch_grad_t<__nv_bfloat16, false>(a, name, st);
+  return ent ? launch_grad_t<float, true>(a, name, st) : launch_grad_t<float, false>(a, name, st);
+}
+
+// CTAs a row for the loss with its gradient: parts of four groups at most (64 KB: three
+// CTAs a multiprocessor), longer ones in clusters of eight.  0: the row is too long.
+constexpr int kOnePassUnits = 4 * kGroup * kMostThreads;
+size_t part_bytes(int64_t per, int threads) {
+  const int64_t group = kGroup * threads;
+  return (size_t)std::max<int64_t>(1, (per + group - 1) / group) * group * 16;
+}
 int one_pass_parts(int64_t S, int64_t units) {
-  int64_t parts = std::max<int64_t>(1, (units * 16 + kOnePassPart - 1) / kOnePassPart);
-  if (parts > 8) parts = (units + 7) / 8 * 16 <= kOnePassMost ? 8 : 0;
-  while (parts > 0 && parts <= 4 && S * parts < num_sms() && units / (2 * parts) >= 256) parts *= 2;
-  return (int)parts;
+  const int64_t parts = std::max<int64_t>(1, (units + kOnePassUnits - 1) / kOnePassUnits);
+  if (parts > 8) return part_bytes((units + 7) / 8, kMostThreads) <= kOnePassMost ? 8 : 0;
+  return parts_for(S, units, (int)parts);
+}
+template <typename T, bool CLUSTER>
+tsp_status launch_one_pass_c(const OnePassArgs& o, cudaStream_t st) {
+  const int parts = o.g.parts;
+  const int64_t per = ((int64_t)o.g.r.V * sizeof(T) / 16 + parts - 1) / parts;
+  const int threads = threads_for(per, o.g.t.K);
+  const size_t smem = part_bytes(per, threads);
+  if (threads == 128)
+    return launch_rows<one_pass_kernel<T, CLUSTER, 128>, CLUSTER, kOnePassMost>(o, o.g.r.S, 128, parts, smem, "token_loss_one_pass", st);
+  return launch_rows<one_pass_kernel<T, CLUSTER, 256>, CLUSTER, kOnePassMost>(o, o.g.r.S, 256, parts, smem, "token_loss_one_pass", st);
 }
 
 }  // namespace
@@ -1126,12 +1465,17 @@ tsp_status launch_token_loss_fwd(const tsp_logits& x, const void* ids, int id_by
     o.g.out = dlogits;
     o.g.ld_out = ld_d;
     o.g.up = dloss;
+    o.g.loss = true;
     o.loss = loss;
     o.stats = stats;
     const bool bf = x.dtype == TSP_BF16;
-    const int parts = one_pass_parts(x.S, x.V * (bf ? 2 : 4) / 16);
-    if (parts > 0 && (bf ? alike<__nv_bfloat16>(o.g) : alike<float>(o.g)))
-      return bf ? launch_one_pass_t<__nv_bfloat16>(o, parts, st) : launch_one_pass_t<float>(o, parts, st);
+    o.g.parts = one_pass_parts(x.S, x.V * (bf ? 2 : 4) / 16);
+    if (o.g.parts > 0 && (bf ? alike<__nv_bfloat16>(o.g) : alike<float>(o.g))) {
+      if (bf)
+        return o.g.parts > 1 ? launch_one_pass_c<__nv_bfloat16, true>(o, st)
+                             : launch_one_pass_c<__nv_bfloat16, false>(o, st);
+      return o.g.parts > 1 ? launch_one_pass_c<float, true>(o, st) : launch_one_pass_c<float, false>(o, st);
+    }
   }
   FwdArgs a = {};
   a.r = rows_of(x, ids, id_bytes);
