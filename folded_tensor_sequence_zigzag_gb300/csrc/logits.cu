@@ -190,9 +190,6 @@ template <typename T, int N> __device__ __forceinline__ float largest(const uint
   }
 }
 
-__device__ __forceinline__ void copy_unit(uint4* dst, const uint4* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
 __device__ __forceinline__ void copies_sent() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copies_left_c() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -209,25 +206,75 @@ __device__ __forceinline__ void copies_left(int n) {
     default: copies_left_c<6>();
   }
 }
-// Sends for group g of a part, of kGroup units a thread, into `dst`; places past the
-// part's units get -inf.  One commit each.
+// Sends for kGroup units of a thread, THREADS apart from src and place on; of those past
+// `left`, counted from src, the places get -inf.  One commit.
 template <typename T, int THREADS>
-__device__ __forceinline__ void send_group(uint4* dst, const RowPart<T>& x, int g) {
-  const int i = (int)threadIdx.x + kGroup * g * THREADS;
-  dst += threadIdx.x;
-  const uint4* src = x.src + i;
-  if (i + (kGroup - 1) * THREADS < x.n) {
+__device__ __forceinline__ void send_units(uint32_t place, const uint4* src, int left) {
+  if (left > (kGroup - 1) * THREADS) {
 #pragma unroll
-    for (int k = 0; k < kGroup; ++k) copy_unit(dst + k * THREADS, src + k * THREADS);
+    for (int k = 0; k < kGroup; ++k)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(place + 16 * k * THREADS), "l"(src + k * THREADS)
+                   : "memory");
   } else {
+    const uint4 none = no_unit<T>();
 #pragma unroll
     for (int k = 0; k < kGroup; ++k) {
-      if (i + k * THREADS < x.n) copy_unit(dst + k * THREADS, src + k * THREADS);
-      else dst[k * THREADS] = no_unit<T>();
+      if (left > k * THREADS)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(place + 16 * k * THREADS), "l"(src + k * THREADS)
+                     : "memory");
+      else
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(place + 16 * k * THREADS), "r"(none.x),
+                     "r"(none.y), "r"(none.z), "r"(none.w)
+                     : "memory");
     }
   }
   copies_sent();
 }
+
+// ---------------------------------------------------------------------------
+// Between the CTAs of a cluster
+// ---------------------------------------------------------------------------
+// Values go by st.async, which counts their bytes on a barrier of the CTA that they
+// are for.  (A cluster barrier for each row would first wait for the gradients that the
+// CTA has on their way to memory: 4096 x 128000 bf16, 372 us with one.)
+struct Wait {   // limits of a wait, and where it says that it gave up
+  int* status;
+  uint64_t limit_ns;
+};
+__device__ __noinline__ void wait_long(uint32_t bar, uint32_t parity, Wait w) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer() - t0 > w.limit_ns) {
+      report_timeout(w.status);
+      return;
+    }
+}
+__device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, const Wait& w) {
+  if (!mbar_try_wait(bar, parity)) wait_long(bar, parity, w);
+}
+// The address that one in this CTA's shared memory has in the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void give(uint32_t to, float4 v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+               "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void give(uint32_t to, float v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(to), "f"(v), "r"(bar)
+               : "memory");
+}
+// What a CTA gets of two rows by turns, since another one may be a row ahead (not two:
+// that one would need this CTA's sums of the row between).
+struct Exchange {
+  float4 share[8];                // each part's largest logit, reference and sums
+  float2 again[8];
+  float z[TSP_TOP_MAX];           // (in the first CTA) the model's logits of the teacher's tokens
+  uint64_t bar_share, bar_z;
+};
 
 // ---------------------------------------------------------------------------
 // Sums
@@ -358,31 +405,27 @@ __device__ __forceinline__ Stats stats_of(float m, float s, float a, float shift
   return r;
 }
 
-// What the CTAs of a cluster write into each other, of two rows by turns, since one of
-// them may be a row ahead.
-struct Exchange {
-  float4 share[8];
-  float2 again[8];
-  float target, z[TSP_TOP_MAX];   // (in the first CTA) logits of the given and the teacher's tokens
-};
-
 // The statistics of a row from its threads' sums.  `units`: where a thread finds its
-// units again; `loose`: its element outside the units or -inf.  Every thread of the
-// CTA (of the cluster) takes part.
+// units again; `loose`: its element outside the units or -inf; `parity`: of the row's
+// exchange.  Every thread of the CTA (of the cluster) takes part.
 template <typename T, bool ENT, bool CLUSTER, int THREADS>
 __device__ __forceinline__ Stats statistics(const Sums<ENT>& sums, const uint4* units, int n, float loose,
-                                            float c2, float4* part, Exchange* ex, int rank, int parts) {
-  const auto cluster = cooperative_groups::this_cluster();
+                                            float c2, float4* part, Exchange* ex, uint32_t parity, int rank,
+                                            int parts, const Wait& wait) {
   Joined j = join<ENT, THREADS>(sums, part);
   if (CLUSTER) {
-    if ((int)threadIdx.x < parts)
-      cluster.map_shared_rank(ex, threadIdx.x)->share[rank] = make_float4(j.m, j.R, j.s, j.a);
-    cluster.sync();
+    const int t = threadIdx.x;
+    const uint32_t bar = smem_u32(&ex->bar_share);
+    if (t == 0) mbar_arrive_expect_tx(bar, 16 * parts);
+    if (t < parts)
+      give(in_cta(smem_u32(&ex->share[rank]), t), make_float4(j.m, j.R, j.s, j.a), in_cta(bar, t));
+    wait_for(bar, parity, wait);
     j = join_parts(ex->share, parts);
   }
   if (!is_far(j.m, c2)) return stats_of(j.m, j.s, j.a, fmaf(j.m, c2, -j.R));
   float2 v = cta_sum<THREADS>(far_sums<T, THREADS>(units, n, loose, j.m, c2), part);
   if (CLUSTER) {
+    const auto cluster = cooperative_groups::this_cluster();
     if ((int)threadIdx.x < parts) cluster.map_shared_rank(ex, threadIdx.x)->again[rank] = v;
     cluster.sync();
     v = make_float2(0.f, 0.f);
@@ -529,6 +572,18 @@ __device__ __noinline__ uint4 far_grad(uint4 v, const Slope<ENT>& s) {
   return v;
 }
 
+// Before the first row: the barriers, and the cluster's other CTAs are there.
+__device__ __forceinline__ void start_exchange(Exchange* ex) {
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(smem_u32(&ex[k].bar_share), 1);
+      mbar_init(smem_u32(&ex[k].bar_z), 1);
+    }
+    fence_barrier_init();
+  }
+  cooperative_groups::this_cluster().sync();
+}
+
 // The row's CTAs: of a cluster, or those that share rows without speaking to each other.
 struct Place {
   int rank, parts, first, stride;
@@ -551,31 +606,47 @@ constexpr int kStages = 4;
 template <typename T, int THREADS>
 struct Sender {
   const Rows& a;
-  uint4* ring;
+  const uint4* mine;     // the thread's first place
+  uint32_t to;           // ... as an address in shared memory
   Place at;
-  int groups, row, g, ahead, slot;
-  RowPart<T> x;
-  __device__ __forceinline__ Sender(const Rows& rows, uint4* to, Place place, int n)
-      : a(rows), ring(to), at(place), groups(n), row(place.first - place.stride), g(n),
-        ahead(given(rows, place.first)), slot(0), x(rows, 0, 0, 1) {
+  int groups, row, ahead, slot;
+  int g, left;           // groups left of the row, units left from the thread's next one
+  const uint4* src;
+  __device__ __forceinline__ Sender(const Rows& rows, const uint4* ring, Place place, int n)
+      : a(rows), mine(ring + threadIdx.x), to(smem_u32(ring + threadIdx.x)), at(place), groups(n),
+        row(place.first - place.stride), ahead(given(rows, place.first)), slot(0), g(0), left(0), src(nullptr) {
     for (int k = 0; k < kStages; ++k) send();
   }
-  __device__ __forceinline__ uint4* place() const { return ring + slot * kGroup * THREADS; }
-  // into the place that is next in turn
+  // The thread's units of the group that is next in turn, THREADS apart.
+  __device__ __forceinline__ const uint4* next() const {
+    copies_left_c<kStages - 1>();
+    return mine + slot * (kGroup * THREADS);
+  }
+  // ... have been read: another group into their places
   __device__ __forceinline__ void send() {
-    if (g == groups) {
+    if (g == 0 && row < a.S) {   // (and no further than one stride past the end)
       int id;
       do {
         row += at.stride;
         id = ahead;
-        ahead = given(a, row + at.stride);
+        if (row < a.S) ahead = given(a, row + at.stride);
       } while (row < a.S && id == -1);
-      g = 0;
-      if (row < a.S) x = RowPart<T>(a, row, at.rank, at.parts);
+      if (row < a.S) {
+        const RowPart<T> x(a, row, at.rank, at.parts);
+        src = x.src + threadIdx.x;
+        left = x.n - (int)threadIdx.x;
+        g = groups;
+      }
     }
-    if (row < a.S) send_group<T, THREADS>(place(), x, g++);
-    else copies_sent();
-    slot = (slot + 1) % kStages;
+    if (g > 0) {
+      send_units<T, THREADS>(to + slot * (16 * kGroup * THREADS), src, left);
+      src += kGroup * THREADS;
+      left -= kGroup * THREADS;
+      --g;
+    } else {
+      copies_sent();
+    }
+    slot = slot + 1 == kStages ? 0 : slot + 1;
   }
 };
 
@@ -589,6 +660,7 @@ struct FwdArgs {
   int top, parts;
   Teacher t;
   float* loss;
+  Wait wait;
 };
 
 // A logit and its token as one key: the larger logit first, the lower token of equal
@@ -717,9 +789,9 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
   const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
   const int K = a.loss && a.t.w_kd != 0.f ? a.t.K : 0;
   Sender<T, THREADS> sender(a.r, ring, at, groups);
-  // (the CTAs of a cluster have started before one writes into another's memory)
-  if (CLUSTER) cluster.sync();
-  int id = given(a.r, at.first), turn = 0;
+  if constexpr (CLUSTER) start_exchange(sm.ex);
+  int id = given(a.r, at.first);
+  uint32_t live = 0;   // rows so far that are not padding
   for (int r = at.first; r < a.r.S; r += at.stride) {
     const int p = pos_of(a.r, r), id_now = id;
     if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
@@ -751,9 +823,8 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
     if (t < K && at.rank == 0) e = load_entry(a.t, p, t);
     Sums<ENT> sums;
     for (int g = 0; g < groups; ++g) {
-      copies_left_c<kStages - 1>();
       uint4 v[kGroup];
-      const uint4* from = sender.place() + t;
+      const uint4* from = sender.next();
 #pragma unroll
       for (int k = 0; k < kGroup; ++k) v[k] = from[k * THREADS];
       sender.send();
@@ -768,10 +839,10 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
     sums.add(two(x0, -INFINITY), two(c2, c2));
     if (K > 0) teacher_part(kid >= 0, e.y, a.t.scale, sm.teach);
     Exchange* ex = nullptr;
-    if constexpr (CLUSTER) ex = &sm.ex[turn];
-    const Stats st = statistics<T, ENT, CLUSTER, THREADS>(sums, x.src, x.n, x0, c2, sm.part[turn], ex, at.rank,
-                                                          at.parts);
-    turn ^= 1;
+    if constexpr (CLUSTER) ex = &sm.ex[live & 1];
+    const Stats st = statistics<T, ENT, CLUSTER, THREADS>(sums, x.src, x.n, x0, c2, sm.part[live & 1], ex, live >> 1 & 1,
+                                                          at.rank, at.parts, a.wait);
+    ++live;
     if (t == 0 && at.rank == 0) {
       if (a.logp) a.logp[p] = log_p(target, st, c);
       if (a.entropy) a.entropy[p] = st.entropy;
@@ -853,6 +924,7 @@ struct GradArgs {
   Teacher t;
   bool loss;
   int parts;
+  Wait wait;
 };
 // What a row's position holds.
 struct Upstream {
@@ -935,7 +1007,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __gr
       for (int i = t; i < x.n; i += THREADS) __stcs(dst + i - t, make_uint4(0, 0, 0, 0));
       if (id_now != -1)
         for (int g = 0; g < groups; ++g) {
-          copies_left_c<kStages - 1>();
+          sender.next();
           sender.send();
         }
       continue;
@@ -973,19 +1045,23 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __gr
       own = group_with<T, THREADS>(x, id_now);
     }
     if (j0 >= 0) out[j0] = from_f<T>(slope.one(x0) + (K == 0 && adds_given && j0 == id_now ? f.given : 0.f));
-    for (int g = 0; g < groups; ++g, dst += kGroup * THREADS) {
-      copies_left_c<kStages - 1>();
+    for (int g = 0, left = x.n - t; g < groups; ++g, left -= kGroup * THREADS, dst += kGroup * THREADS) {
+      const uint4* place = sender.next();
       uint4 v[kGroup];
-      const uint4* from = sender.place() + t;
 #pragma unroll
-      for (int k = 0; k < kGroup; ++k) v[k] = from[k * THREADS];
-      const float z = g == own ? logit_in<T, THREADS>(sender.place(), x, id_now) : 0.f;
+      for (int k = 0; k < kGroup; ++k) v[k] = place[k * THREADS];
+      const float z = g == own ? logit_in<T, THREADS>(place - t, x, id_now) : 0.f;
       sender.send();
-      const int i = t + kGroup * g * THREADS;
+      if (slope.far) {
+        for (int k = 0; k < kGroup; ++k)
+          if (left > k * THREADS) __stcs(dst + k * THREADS, far_grad<T, ENT>(v[k], slope));
+      } else {
 #pragma unroll
-      for (int k = 0; k < kGroup; ++k)
-        if (i + k * THREADS < x.n)
-          __stcs(dst + k * THREADS, slope.far ? far_grad<T, ENT>(v[k], slope) : unit_grad<T, ENT>(v[k], slope));
+        for (int k = 0; k < kGroup; ++k) {
+          const uint4 w = unit_grad<T, ENT>(v[k], slope);
+          if (left > k * THREADS) __stcs(dst + k * THREADS, w);
+        }
+      }
       if (g == own) out[id_now] = from_f<T>(slope.one(z) + f.given);
     }
     if (K > 0) {
@@ -1082,17 +1158,16 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
     float loose[16];
   } sm;
   const GradArgs& a = o.g;
-  const auto cluster = cooperative_groups::this_cluster();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const Place at(CLUSTER ? a.parts : 1);
   const float c = a.r.scale, c2 = c * kLog2e;
   const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
   const int K = a.t.w_kd != 0.f ? a.t.K : 0;
+  const uint32_t to = smem_u32(seg + t);
   int id = given(a.r, at.first);
-  // (the CTAs of a cluster have started before one writes into another's memory)
-  if (CLUSTER) cluster.sync();
+  if (CLUSTER) start_exchange(sm.ex);
   bool there = false;   // this row's copies have been sent
-  int turn = 0;
+  uint32_t live = 0;    // rows so far that are not padding
   for (int r = at.first; r < a.r.S; r += at.stride) {
     const int p = pos_of(a.r, r), id_now = id;
     if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
@@ -1104,12 +1179,15 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
     const bool sent = there;
     there = r + at.stride < a.r.S && id != -1;
     RowPart<T> next(a.r, there ? r + at.stride : r, at.rank, at.parts);
+    Exchange& ex = sm.ex[live & 1];
     Stats st = {0.f, -INFINITY, 0.f};
     float x0 = -INFINITY, up = 1.f, target = 0.f;
     bool teacher = false;
     if (id_now != -1) {
       if (!sent)
-        for (int g = 0; g < groups; ++g) send_group<T, THREADS>(seg + kGroup * g * THREADS, x, g);
+        for (int g = 0; g < groups; ++g)
+          send_units<T, THREADS>(to + 16 * kGroup * THREADS * g, x.src + t + kGroup * THREADS * g,
+                                 x.n - t - kGroup * THREADS * g);
       if (j0 >= 0) x0 = to_f<T>(x.row[j0]);
       if (t == 0 && id_now >= 0) target = to_f<T>(x.row[id_now]);
       if (a.up) up = a.up[p];
@@ -1132,32 +1210,31 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
         if (j0 >= 0) sm.loose[t] = x0;
         teacher_part(kid >= 0, e.y, a.t.scale, sm.teach);
       }
-      if constexpr (CLUSTER) {
-        // (the listed logits go with the sums: every thread's units are there behind this)
-        if (K > 0) __syncthreads();
-      }
-      auto hand_on = [&] {   // the logits of the listed tokens that are in this part
+      st = statistics<T, false, CLUSTER, THREADS>(sums, seg, x.n, x0, c2, sm.part[live & 1], &ex, live >> 1 & 1, at.rank,
+                                                  at.parts, a.wait);
+      if (K > 0) {
+        // the logits of the listed tokens that are in this part (every thread's units are
+        // there since the sums were joined)
         auto logit = [&](int j) {
           return j < x.head    ? sm.loose[j]
                  : j >= x.tail ? sm.loose[x.head + j - x.tail]
                                : to_f<T>(reinterpret_cast<const T*>(seg)[j - x.head - x.u_lo * RowPart<T>::E]);
         };
-        Exchange* first = CLUSTER ? cluster.map_shared_rank(&sm.ex[turn], 0) : &sm.ex[turn];
         const bool here = kid >= x.lo && kid < x.hi;
         if (t < K) sm.adds.id[t] = here ? kid : -1;
-        if (here) first->z[t] = sm.adds.z[t] = logit(kid);
+        if (here) sm.adds.z[t] = logit(kid);
+        if (CLUSTER) {   // each entry's comes from one CTA
+          const uint32_t bar = smem_u32(&ex.bar_z);
+          if (at.rank == 0 && t == 0) mbar_arrive_expect_tx(bar, 4 * K);
+          if (here || (at.rank == 0 && t < K && kid < 0))
+            give(in_cta(smem_u32(&ex.z[t]), 0), here ? sm.adds.z[t] : 0.f, in_cta(bar, 0));
+        }
         if (t == 0) {
           const bool given_here = id_now >= x.lo && id_now < x.hi && a.t.w_ce != 0.f;
           sm.adds.id[K] = given_here ? id_now : -1;
           if (given_here) sm.adds.z[K] = logit(id_now);
         }
         end_adds(sm.adds, K + 1);
-      };
-      if (CLUSTER && K > 0) hand_on();
-      st = statistics<T, false, CLUSTER, THREADS>(sums, seg, x.n, x0, c2, sm.part[turn], &sm.ex[turn], at.rank,
-                                                  at.parts);
-      if (K > 0) {
-        if (!CLUSTER) hand_on();
         const float2 whole = teacher_whole<THREADS>(a.t.scale, sm.teach);
         teacher = whole.y != 0.f;
         if (t < K) {
@@ -1175,27 +1252,30 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
     const Slope<false> slope(st.m, st.l, c2, up * c * (a.t.w_ce + (teacher ? a.t.w_kd : 0.f)), 0.f);
     const bool adds_given = K == 0 && !flat && id_now >= 0 && a.t.w_ce != 0.f;
     if (j0 >= 0) out[j0] = from_f<T>(flat ? 0.f : slope.one(x0) + (adds_given && j0 == id_now ? by_given : 0.f));
-    if (flat || slope.far) {
-      for (int g = 0; g < groups; ++g) {
-        for (int k = 0, i = t + kGroup * g * THREADS; k < kGroup && i < x.n; ++k, i += THREADS)
-          __stcs(dst + i - t, flat ? make_uint4(0, 0, 0, 0) : far_grad<T, false>(seg[i], slope));
-        if (adds_given && group_with<T, THREADS>(x, id_now) == g)
-          out[id_now] = from_f<T>(slope.one(logit_in<T, THREADS>(seg + kGroup * g * THREADS, x, id_now)) + by_given);
-        if (there) send_group<T, THREADS>(seg + kGroup * g * THREADS, next, g);
-      }
-    } else {
-      const int own = adds_given ? group_with<T, THREADS>(x, id_now) : -1;   // the group with the given token
-      for (int g = 0; g < groups; ++g, dst += kGroup * THREADS) {
-        uint4* place = seg + kGroup * g * THREADS;
-        const int i = t + kGroup * g * THREADS;
+    const int own = adds_given ? group_with<T, THREADS>(x, id_now) : -1;   // the group with the given token
+    const uint4 *place = seg + t, *src = next.src + t;
+    uint32_t from = to;
+    int left = x.n - t, left_next = next.n - t;
+    for (int g = 0; g < groups; ++g) {
+      if (flat || slope.far) {
+        for (int k = 0; k < kGroup; ++k)
+          if (left > k * THREADS)
+            __stcs(dst + k * THREADS, flat ? make_uint4(0, 0, 0, 0) : far_grad<T, false>(place[k * THREADS], slope));
+      } else {
 #pragma unroll
         for (int k = 0; k < kGroup; ++k) {
-          const uint4 v = unit_grad<T, false>(place[t + k * THREADS], slope);
-          if (i + k * THREADS < x.n) __stcs(dst + k * THREADS, v);
+          const uint4 v = unit_grad<T, false>(place[k * THREADS], slope);
+          if (left > k * THREADS) __stcs(dst + k * THREADS, v);
         }
-        if (g == own) out[id_now] = from_f<T>(slope.one(logit_in<T, THREADS>(place, x, id_now)) + by_given);
-        if (there) send_group<T, THREADS>(place, next, g);
       }
+      if (g == own) out[id_now] = from_f<T>(slope.one(logit_in<T, THREADS>(place - t, x, id_now)) + by_given);
+      if (there) send_units<T, THREADS>(from, src, left_next);
+      place += kGroup * THREADS;
+      src += kGroup * THREADS;
+      dst += kGroup * THREADS;
+      from += 16 * kGroup * THREADS;
+      left -= kGroup * THREADS;
+      left_next -= kGroup * THREADS;
     }
     if (id_now != -1 && K > 0) {
       __syncthreads();   // the listed tokens' values go on top of what other threads wrote
@@ -1210,9 +1290,11 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
         if (id_now >= 0 && a.t.w_ce != 0.f) loss = -a.t.w_ce * log_p(target, st, c);
         if (K > 0) {
           float kd = 0.f;
+          if (CLUSTER) wait_for(smem_u32(&ex.bar_z), live >> 1 & 1, a.wait);
+          const float* z = CLUSTER ? ex.z : sm.adds.z;
           for (int k = lane; k < K; k += 32) {
             const float q = sm.q[k];
-            if (q != 0.f) kd += q * (sm.logq[k] - log_p(sm.ex[turn].z[k], st, c));
+            if (q != 0.f) kd += q * (sm.logq[k] - log_p(z[k], st, c));
           }
           kd = lanes_sum<32>(kd);
           if (teacher) loss += a.t.w_kd * kd;
@@ -1224,7 +1306,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
         o.stats[2 * (int64_t)p + 1] = st.l;
       }
     }
-    if (id_now != -1) turn ^= 1;
+    if (id_now != -1) ++live;
   }
 }
 
@@ -1257,6 +1339,8 @@ Teacher teacher_of(const tsp_teacher* t, float w_ce) {
   }
   return k;
 }
+
+Wait wait_limits() { return {status_word(), wait_limit_ns()}; }
 
 // How many clusters of `parts` CTAs (CTAs, if parts is 1) of a kernel the GPU holds at
 // once, looked up once for each kind of launch: a grid takes as many.
@@ -1301,6 +1385,7 @@ tsp_status allow_smem(int most) {
 
 constexpr int kOnePassMost = 200 * 1024;   // bytes of a part of the longest rows
 constexpr int kRingMost = kStages * kGroup * kMostThreads * 16;
+constexpr int64_t kRowsACta = 2;
 // S rows on as many CTAs (clusters of `parts` with CLUSTER, groups of `parts` without)
 // as fit at once.  MOST: dynamic shared memory at most.
 template <auto KERNEL, bool CLUSTER, int MOST, typename A>
@@ -1320,7 +1405,7 @@ tsp_status launch_rows(const A& a, int S, int threads, int parts, size_t smem, c
   cfg.numAttrs = CLUSTER ? 1 : 0;
   const int64_t fit = CLUSTER ? resident((const void*)KERNEL, cfg, parts)
                               : std::max<int64_t>(1, resident((const void*)KERNEL, cfg, 1) / parts);
-  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(S, fit) * parts));
+  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(S, std::max<int64_t>(fit, (S + kRowsACta - 1) / kRowsACta)) * parts));
   Prof prof(name, st);
   TSP_CUDA_TRY(cudaLaunchKernelEx(&cfg, KERNEL, a));
   return TSP_OK;
@@ -1416,6 +1501,7 @@ tsp_status launch_logprobs_fwd(const tsp_logits& x, const void* ids, int id_byte
                                cudaStream_t st) {
   FwdArgs a = {};
   a.r = rows_of(x, ids, id_bytes);
+  a.wait = wait_limits();
   a.t = teacher_of(nullptr, 0.f);
   a.logp = logp;
   a.entropy = entropy;
@@ -1461,6 +1547,7 @@ tsp_status launch_token_loss_fwd(const tsp_logits& x, const void* ids, int id_by
   if (dlogits) {
     OnePassArgs o = {};
     o.g.r = rows_of(x, ids, id_bytes);
+    o.g.wait = wait_limits();
     o.g.t = teacher_of(teacher, w_ce);
     o.g.out = dlogits;
     o.g.ld_out = ld_d;
@@ -1479,6 +1566,7 @@ tsp_status launch_token_loss_fwd(const tsp_logits& x, const void* ids, int id_by
   }
   FwdArgs a = {};
   a.r = rows_of(x, ids, id_bytes);
+  a.wait = wait_limits();
   a.t = teacher_of(teacher, w_ce);
   a.loss = loss;
   a.stats = stats;
