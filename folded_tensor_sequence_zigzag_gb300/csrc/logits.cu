@@ -304,12 +304,15 @@ struct Sums {
     s = add_two(s, e);
     if (ENT) a = fma_two(e, not_least(u), a);
   }
-  template <typename T, int N> __device__ __forceinline__ void add_units(const uint4 (&v)[N], float c, f2 c2) {
-    see(largest<T, N>(v), c);
+  // Their largest logit.
+  template <typename T, int N> __device__ __forceinline__ float add_units(const uint4 (&v)[N], float c, f2 c2) {
+    const float b = largest<T, N>(v);
+    see(b, c);
 #pragma unroll
     for (int k = 0; k < N; ++k)
 #pragma unroll
       for (int e = 0; e < RowPart<T>::E / 2; ++e) add(pair<T>(v[k], e), c2);
+    return b;
   }
 };
 
@@ -460,18 +463,21 @@ __device__ __forceinline__ int token_of(const Entry& e, const Rows& r) {
   if (e.id >= r.V) report_status(r.status, (int)TSP_ERR_RANGE);
   return e.id >= 0 && e.id < r.V && !(e.y == -INFINITY) ? e.id : -1;
 }
-// The list's softmax, entry k thread k's (there: it counts): warps' parts before the
-// CTA's next barrier, the whole behind it.
-__device__ __forceinline__ void teacher_part(bool there, float y, float scale, float2* teach) {
+// The list's softmax, entry k thread k's (there: it counts): the warps' parts before the
+// CTA's next barrier, the whole behind it, in the warps that have entries; in the others
+// only whether there is an entry.
+__device__ __forceinline__ void teacher_part(int K, bool there, float y, float scale, float2* teach) {
+  if ((int)(threadIdx.x & ~31) >= K) return;
   const float mw = lanes_max(there ? y : -INFINITY);
   const float sw = lanes_sum<32>(there ? expf(scale * (y - mw)) : 0.f);
   if ((threadIdx.x & 31) == 0) teach[threadIdx.x >> 5] = make_float2(mw, sw);
 }
-template <int THREADS>
-__device__ __forceinline__ float2 teacher_whole(float scale, const float2* teach) {   // (largest, sum)
-  const float2 w = teach[threadIdx.x & (THREADS / 32 - 1)];
+__device__ __forceinline__ float2 teacher_whole(int K, float scale, const float2* teach) {   // (largest, sum)
+  const int warps = (K + 31) / 32, lane = threadIdx.x & 31;
+  const float2 w = lane < warps ? teach[lane] : make_float2(-INFINITY, 0.f);
+  if ((int)(threadIdx.x & ~31) >= K) return make_float2(0.f, __any_sync(0xffffffffu, w.y != 0.f) ? 1.f : 0.f);
   const float m = lanes_max(w.x);
-  return make_float2(m, lanes_sum<THREADS / 32>(w.y == 0.f ? 0.f : w.y * expf(scale * (w.x - m))));
+  return make_float2(m, lanes_sum<32>(w.y == 0.f ? 0.f : w.y * expf(scale * (w.x - m))));
 }
 // Entry's q and log q.
 __device__ __forceinline__ float2 teacher_q(bool there, float y, float scale, float2 whole) {
@@ -600,10 +606,13 @@ __device__ __forceinline__ int groups_of(int V, int parts) {
   return max(1, (per + kGroup * THREADS - 1) / (kGroup * THREADS));
 }
 
+// Stages of the rings: 32 KB for 128 threads, six CTAs a multiprocessor; with room for the
+// alternatives' search a quarter less.
+__host__ __device__ constexpr int stages_of(bool top) { return top ? 3 : 4; }
+
 // Groups of rows that are not padding sent for ahead of their use, into the places of a
-// ring by turns: kStages commits are on their way at any time.
-constexpr int kStages = 4;
-template <typename T, int THREADS>
+// ring by turns: STAGES commits are on their way at any time.
+template <typename T, int THREADS, int STAGES>
 struct Sender {
   const Rows& a;
   const uint4* mine;     // the thread's first place
@@ -615,11 +624,11 @@ struct Sender {
   __device__ __forceinline__ Sender(const Rows& rows, const uint4* ring, Place place, int n)
       : a(rows), mine(ring + threadIdx.x), to(smem_u32(ring + threadIdx.x)), at(place), groups(n),
         row(place.first - place.stride), ahead(given(rows, place.first)), slot(0), g(0), left(0), src(nullptr) {
-    for (int k = 0; k < kStages; ++k) send();
+    for (int k = 0; k < STAGES; ++k) send();
   }
   // The thread's units of the group that is next in turn, THREADS apart.
   __device__ __forceinline__ const uint4* next() const {
-    copies_left_c<kStages - 1>();
+    copies_left_c<STAGES - 1>();
     return mine + slot * (kGroup * THREADS);
   }
   // ... have been read: another group into their places
@@ -646,7 +655,7 @@ struct Sender {
     } else {
       copies_sent();
     }
-    slot = slot + 1 == kStages ? 0 : slot + 1;
+    slot = slot + 1 == STAGES ? 0 : slot + 1;
   }
 };
 
@@ -677,12 +686,16 @@ __device__ __forceinline__ uint64_t key_of(float x, int j) {
 }
 constexpr uint32_t kOrderNone = 0x007fffffu;   // order_of(-inf)
 
-constexpr int kCandidates = 1024;
+// Where alternatives are wanted, a thread leaves the largest logit (rounded up to 16 bits)
+// of each of up to kSlots runs of its groups.
+constexpr int kSlots = 16, kListed = 512;
 template <int THREADS> struct TopSmem {
-  float best[THREADS];        // largest logit of each group of threads
-  int sel[THREADS];
+  static constexpr int kCandidates = 4 * THREADS;
   uint64_t key[kCandidates], above;
-  int n, n_sel;
+  alignas(16) float best[THREADS];      // largest logit of each set of threads
+  __nv_bfloat16 slot[kSlots][THREADS];
+  uint16_t listed[kListed];             // slots to be looked at once more
+  int n, n_listed;
 };
 struct TopLists {             // of a cluster's parts, in the first CTA
   uint64_t key[8][TSP_TOP_MAX];
@@ -706,72 +719,125 @@ __device__ __forceinline__ int rank_in_sorted(const uint64_t* key, int n, uint64
   }
   return lo;
 }
+// put(rank, key) for each of the n keys, by a power of two of the threads each.
+template <int THREADS, typename F>
+__device__ __forceinline__ void for_ranked(const uint64_t* key, int n, F put) {
+  const int t = threadIdx.x;
+  int log_g = 0;
+  while (log_g < 5 && (n << (log_g + 1)) <= THREADS) ++log_g;
+  const int g = 1 << log_g;
+  for (int k = t >> log_g; k - ((t & 31) >> log_g) < n; k += THREADS >> log_g) {   // (whole warps)
+    const uint64_t mine = k < n ? key[k] : 0;
+    int rank = 0;
+    for (int q = t & (g - 1); q < n; q += g) rank += key[q] > mine;
+    for (int o = 1; o < g; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (k < n && (t & (g - 1)) == 0) put(rank, mine);
+  }
+}
 
 // Keys of a part's logits, the `top` largest among them, into sm.key; their number.
 // A bound first: each thread's largest logit (`mine`, of its units) is a logit of the
-// part, so the top-th largest of them (of groups of threads, four for each alternative
-// where there are as many) is not above the top-th of all.  Then the logits of the
-// threads that reach it once more, out of L2: top / groups of the part.
+// part, so the top-th largest of them (of sets of threads, two for each alternative
+// where there are as many) is not above the top-th of all.  Then the units of the slots
+// that reach it once more, out of L2: about as many slots as there are alternatives.
+// A slot is 2^shift groups of a thread.
 template <typename T, int THREADS>
-__device__ __noinline__ int candidates(const RowPart<T>& x, int top, float mine, TopSmem<THREADS>& sm) {
+__device__ __noinline__ int candidates(const RowPart<T>& x, int top, float mine, int groups, int shift,
+                                       TopSmem<THREADS>& sm) {
   const int t = threadIdx.x;
-  int g = 1;   // threads a group
-  while (g < 32 && THREADS / (2 * g) >= 4 * top) g *= 2;
+  int g = 1;   // threads a set
+  while (g < 32 && THREADS / (2 * g) >= 2 * top) g *= 2;
   float b = mine;
   for (int o = 1; o < g; o *= 2) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
-  const int groups = THREADS / g, i = t / g;
+  const int sets = THREADS / g, i = t / g;
   if (t % g == 0) sm.best[i] = b;
   if (t == 0) {
-    sm.n = sm.n_sel = 0;
+    sm.n = sm.n_listed = 0;
     sm.above = (uint64_t)(kOrderNone + 1) << 32;
   }
   __syncthreads();
   int rank = 0;
-  for (int j = t % g; j < groups; j += g) rank += sm.best[j] > b || (sm.best[j] == b && j < i);
+  for (int j = 4 * (t % g); j < sets; j += 4 * g) {   // (sets: a multiple of 4)
+    const float4 o = *reinterpret_cast<const float4*>(sm.best + j);
+    rank += (o.x > b || (o.x == b && j < i)) + (o.y > b || (o.y == b && j + 1 < i)) +
+            (o.z > b || (o.z == b && j + 2 < i)) + (o.w > b || (o.w == b && j + 3 < i));
+  }
   for (int o = 1; o < g; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
   if (rank == top - 1 && t % g == 0 && b > -INFINITY) sm.above = (uint64_t)order_of(b) << 32;
   __syncthreads();
-  if (t % g == 0 && b > -INFINITY && order_of(b) >= (uint32_t)(sm.above >> 32))
-    sm.sel[atomicAdd(&sm.n_sel, 1)] = i;
-  __syncthreads();
-  const int per = sm.n_sel * g, rounds = (x.n + THREADS - 1) / THREADS;
+  const int slots = (groups + (1 << shift) - 1) >> shift, log_per = 2 + shift;   // units of a slot
+  static_assert(kGroup == 4, "log_per");
   for (;;) {
     const uint64_t above = sm.above;
+    const uint32_t bound = (uint32_t)(above >> 32);
+    auto reaches = [&](int s, int who) { return order_of(__bfloat162float(sm.slot[s][who])) >= bound; };
+    for (int s = 0; order_of(mine) >= bound && s < slots; ++s)
+      if (reaches(s, t)) {
+        const int n = atomicAdd(&sm.n_listed, 1);
+        if (n < kListed) sm.listed[n] = (uint16_t)(s * THREADS + t);
+      }
     auto take = [&](float v, int j) {
       const uint64_t k = key_of(v, j);
       if (k < above) return;
       const int n = atomicAdd(&sm.n, 1);
-      if (n < kCandidates) sm.key[n] = k;
+      if (n < TopSmem<THREADS>::kCandidates) sm.key[n] = k;
+    };
+    auto look = [&](const uint4& v, int u) {
+      const uint4 one[1] = {v};
+      if (order_of(largest<T, 1>(one)) < bound) return;
+#pragma unroll
+      for (int e = 0; e < RowPart<T>::E / 2; ++e) {
+        const float2 y = both(pair<T>(v, e));
+        take(y.x, x.head + (x.u_lo + u) * RowPart<T>::E + 2 * e);
+        take(y.y, x.head + (x.u_lo + u) * RowPart<T>::E + 2 * e + 1);
+      }
     };
     const int j0 = x.loose(t);
     if (j0 >= 0) take(to_f<T>(x.row[j0]), j0);
-    for (int w = t; w < per * rounds; w += THREADS) {
-      const int round = w / per, in = w - round * per;
-      const int u = sm.sel[in / g] * g + in % g + round * THREADS;
-      if (u >= x.n) continue;
-      const uint4 v[1] = {x.src[u]};
-      if (order_of(largest<T, 1>(v)) < (uint32_t)(above >> 32)) continue;
+    __syncthreads();
+    const int listed = sm.n_listed;
+    if (listed <= kListed) {
+      constexpr int U = 4;   // loads on their way
+      for (int w0 = t; w0 < listed << log_per; w0 += U * THREADS) {
+        uint4 v[U];
+        int u[U];
 #pragma unroll
-      for (int e = 0; e < RowPart<T>::E / 2; ++e) {
-        const float2 y = both(pair<T>(v[0], e));
-        take(y.x, x.head + (x.u_lo + u) * RowPart<T>::E + 2 * e);
-        take(y.y, x.head + (x.u_lo + u) * RowPart<T>::E + 2 * e + 1);
+        for (int k = 0; k < U; ++k) {
+          const int w = w0 + k * THREADS;
+          u[k] = x.n;
+          if (w < listed << log_per) {
+            const int which = sm.listed[w >> log_per];
+            u[k] = (((which / THREADS) << log_per) + (w & ((1 << log_per) - 1))) * THREADS + which % THREADS;
+          }
+          v[k] = u[k] < x.n ? x.src[u[k]] : no_unit<T>();
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+          if (u[k] < x.n) look(v[k], u[k]);
+      }
+    } else {   // many equal logits: every thread its own
+      for (int s = 0; s < slots; ++s) {
+        if (!reaches(s, t)) continue;
+        for (int k = s << log_per; k < (s + 1) << log_per; ++k) {
+          const int u = k * THREADS + t;
+          if (u < x.n) look(x.src[u], u);
+        }
       }
     }
     __syncthreads();
     const int n = sm.n;
-    if (n <= kCandidates) return n;
+    if (n <= TopSmem<THREADS>::kCandidates) return n;
     // More than there is room for (many equal logits, or a few threads hold most of the
     // large ones): the top-th of those stored is a better bound, since as many reach it.
     __syncthreads();
-    for (int k = t; k < kCandidates; k += THREADS)
-      if (rank_in(sm.key, kCandidates, sm.key[k]) == top - 1) sm.above = sm.key[k];
-    if (t == 0) sm.n = 0;
+    for (int k = t; k < TopSmem<THREADS>::kCandidates; k += THREADS)
+      if (rank_in(sm.key, TopSmem<THREADS>::kCandidates, sm.key[k]) == top - 1) sm.above = sm.key[k];
+    if (t == 0) sm.n = sm.n_listed = 0;
     __syncthreads();
   }
 }
 
-template <typename T, bool ENT, bool CLUSTER, int THREADS>
+template <typename T, bool ENT, bool TOP, bool CLUSTER, int THREADS>
 __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __grid_constant__ FwdArgs a) {
   extern __shared__ uint4 ring[];
   __shared__ struct {
@@ -780,7 +846,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
     float kd[THREADS / 32];
     typename std::conditional<CLUSTER, Exchange, Nothing>::type ex[2];
     typename std::conditional<CLUSTER, TopLists, Nothing>::type lists;
-    TopSmem<THREADS> top;
+    typename std::conditional<TOP, TopSmem<THREADS>, Nothing>::type top;
   } sm;
   const auto cluster = cooperative_groups::this_cluster();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -788,7 +854,9 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
   const float c = a.r.scale, c2 = c * kLog2e;
   const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
   const int K = a.loss && a.t.w_kd != 0.f ? a.t.K : 0;
-  Sender<T, THREADS> sender(a.r, ring, at, groups);
+  Sender<T, THREADS, stages_of(TOP)> sender(a.r, ring, at, groups);
+  int shift = 0;   // groups a slot
+  while (TOP && (groups - 1) >> shift >= kSlots) ++shift;
   if constexpr (CLUSTER) start_exchange(sm.ex);
   int id = given(a.r, at.first);
   uint32_t live = 0;   // rows so far that are not padding
@@ -822,13 +890,21 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
     int kid = -1;
     if (t < K && at.rank == 0) e = load_entry(a.t, p, t);
     Sums<ENT> sums;
+    float in_slot = -INFINITY;
     for (int g = 0; g < groups; ++g) {
       uint4 v[kGroup];
       const uint4* from = sender.next();
 #pragma unroll
       for (int k = 0; k < kGroup; ++k) v[k] = from[k * THREADS];
       sender.send();
-      sums.template add_units<T, kGroup>(v, c2, two(c2, c2));
+      const float b = sums.template add_units<T, kGroup>(v, c2, two(c2, c2));
+      if constexpr (TOP) {
+        in_slot = fmaxf(in_slot, b);
+        if (((g + 1) & ((1 << shift) - 1)) == 0 || g + 1 == groups) {
+          sm.top.slot[g >> shift][t] = __float2bfloat16_ru(in_slot);
+          in_slot = -INFINITY;
+        }
+      }
       if (g == 0 && t < K) {   // the entry is there by now: its logit is sent for
         kid = token_of(e, a.r);
         if (kid >= 0) z = to_f<T>(x.row[kid]);
@@ -837,7 +913,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
     const float mine = sums.top;   // of the units
     sums.see(x0, c2);
     sums.add(two(x0, -INFINITY), two(c2, c2));
-    if (K > 0) teacher_part(kid >= 0, e.y, a.t.scale, sm.teach);
+    if (K > 0) teacher_part(K, kid >= 0, e.y, a.t.scale, sm.teach);
     Exchange* ex = nullptr;
     if constexpr (CLUSTER) ex = &sm.ex[live & 1];
     const Stats st = statistics<T, ENT, CLUSTER, THREADS>(sums, x.src, x.n, x0, c2, sm.part[live & 1], ex, live >> 1 & 1,
@@ -854,19 +930,21 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
     if (a.loss) {
       float kd = 0.f;
       if (K > 0) {
-        const float2 whole = teacher_whole<THREADS>(a.t.scale, sm.teach);
-        const float2 q = teacher_q(kid >= 0, e.y, a.t.scale, whole);
-        kd = lanes_sum<32>(q.x != 0.f ? q.x * (q.y - log_p(z, st, c)) : 0.f);
-        if (lane == 0) sm.kd[warp] = kd;
+        const float2 whole = teacher_whole(K, a.t.scale, sm.teach);
+        const float2 q = t < K ? teacher_q(kid >= 0, e.y, a.t.scale, whole) : make_float2(0.f, 0.f);
+        if (warp * 32 < K) {
+          kd = lanes_sum<32>(q.x != 0.f ? q.x * (q.y - log_p(z, st, c)) : 0.f);
+          if (lane == 0) sm.kd[warp] = kd;
+        }
         __syncthreads();
         kd = 0.f;
-        for (int k = 0; k < THREADS / 32; ++k) kd += sm.kd[k];
+        for (int k = 0; 32 * k < K; ++k) kd += sm.kd[k];
         kd = whole.y != 0.f ? a.t.w_kd * kd : 0.f;
       }
       if (t == 0 && at.rank == 0)
         a.loss[p] = (a.t.w_ce != 0.f ? -a.t.w_ce * log_p(target, st, c) : 0.f) + kd;
     }
-    if (a.top > 0) {
+    if constexpr (TOP) {
       const int64_t to = (int64_t)p * a.top;
       int n = 0;
       auto put = [&](int rank, uint64_t key) {
@@ -874,33 +952,31 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
         a.top_ids[to + rank] = (int)~(uint32_t)key;
         a.top_logp[to + rank] = log_p(logit_of((uint32_t)(key >> 32)), st, c);
       };
-      if (!isnan(st.l)) {
-        n = candidates<T, THREADS>(x, a.top, mine, sm.top);
+      if (a.top > 0 && !isnan(st.l)) {
+        n = candidates<T, THREADS>(x, a.top, mine, groups, shift, sm.top);
         if constexpr (!CLUSTER) {
-          for (int k = t; k < n; k += THREADS) put(rank_in(sm.top.key, n, sm.top.key[k]), sm.top.key[k]);
+          for_ranked<THREADS>(sm.top.key, n, put);
         } else {
           TopLists* first = cluster.map_shared_rank(&sm.lists, 0);
-          for (int k = t; k < n; k += THREADS) {
-            const int rank = rank_in(sm.top.key, n, sm.top.key[k]);
-            if (rank < a.top) first->key[at.rank][rank] = sm.top.key[k];
-          }
+          for_ranked<THREADS>(sm.top.key, n, [&](int rank, uint64_t key) {
+            if (rank < a.top) first->key[at.rank][rank] = key;
+          });
           if (t == 0) first->n[at.rank] = min(n, a.top);
           cluster.sync();
           if (at.rank == 0) {
+            // a lane an entry and another list, eight lanes an entry
             n = 0;
-            for (int q = 0; q < at.parts; ++q) {
-              const int nq = sm.lists.n[q];
-              n += nq;
-              for (int k = t; k < nq; k += THREADS) {
-                const uint64_t key = sm.lists.key[q][k];
-                int rank = k;
-                for (int o = 0; o < at.parts; ++o)
-                  if (o != q) rank += rank_in_sorted(sm.lists.key[o], sm.lists.n[o], key);
-                put(rank, key);
-              }
+            for (int q = 0; q < at.parts; ++q) n += sm.lists.n[q];
+            for (int e = t >> 3; e - ((t & 31) >> 3) < at.parts * a.top; e += THREADS >> 3) {   // (whole warps)
+              const int q = min(e / a.top, at.parts - 1), k = e - q * a.top, o = t & 7;
+              const bool there = k < sm.lists.n[q];
+              const uint64_t key = there ? sm.lists.key[q][k] : 0;
+              int rank = o == q ? k : there && o < at.parts ? rank_in_sorted(sm.lists.key[o], sm.lists.n[o], key) : 0;
+              for (int i = 1; i < 8; i *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, i);
+              if (there && o == 0) put(rank, key);
             }
           }
-          cluster.sync();   // the lists are read before the next row's come in
+          if (r + at.stride < a.r.S) cluster.sync();   // the lists are read before the next row's come in
         }
       }
       if (at.rank == 0) {
@@ -983,7 +1059,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __gr
   const float c2 = a.r.scale * kLog2e;
   const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
   const int K = a.loss && a.t.w_kd != 0.f ? a.t.K : 0;
-  Sender<T, THREADS> sender(a.r, ring, at, groups);
+  Sender<T, THREADS, stages_of(false)> sender(a.r, ring, at, groups);
   int id = given(a.r, at.first);
   Upstream up = upstream<ENT>(a, at.first);
   Entry e = {-1, -INFINITY};
@@ -1017,9 +1093,9 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __gr
     int kid = -1;
     if (K > 0) {
       if (t < K) kid = token_of(entry, a.r);
-      teacher_part(kid >= 0, entry.y, a.t.scale, sm.teach);
+      teacher_part(K, kid >= 0, entry.y, a.t.scale, sm.teach);
       __syncthreads();
-      const float2 whole = teacher_whole<THREADS>(a.t.scale, sm.teach);
+      const float2 whole = teacher_whole(K, a.t.scale, sm.teach);
       teacher = whole.y != 0.f;
       if (t < K) {
         const bool here = kid >= x.lo && kid < x.hi;
@@ -1098,9 +1174,9 @@ __global__ void __launch_bounds__(kMostThreads) grad_elements_kernel(const __gri
     Entry e = {-1, -INFINITY};
     if (t < K) e = load_entry(a.t, p, t);
     const int kid = t < K ? token_of(e, a.r) : -1;
-    teacher_part(kid >= 0, e.y, a.t.scale, sm.teach);
+    teacher_part(K, kid >= 0, e.y, a.t.scale, sm.teach);
     __syncthreads();
-    const float2 whole = teacher_whole<THREADS>(a.t.scale, sm.teach);
+    const float2 whole = teacher_whole(K, a.t.scale, sm.teach);
     teacher = whole.y != 0.f;
     if (t < K) {
       const bool here = kid >= lo && kid < hi;
@@ -1208,7 +1284,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
       if (K > 0) {
         if (t < K) kid = token_of(e, a.r);
         if (j0 >= 0) sm.loose[t] = x0;
-        teacher_part(kid >= 0, e.y, a.t.scale, sm.teach);
+        teacher_part(K, kid >= 0, e.y, a.t.scale, sm.teach);
       }
       st = statistics<T, false, CLUSTER, THREADS>(sums, seg, x.n, x0, c2, sm.part[live & 1], &ex, live >> 1 & 1, at.rank,
                                                   at.parts, a.wait);
@@ -1235,7 +1311,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
           if (given_here) sm.adds.z[K] = logit(id_now);
         }
         end_adds(sm.adds, K + 1);
-        const float2 whole = teacher_whole<THREADS>(a.t.scale, sm.teach);
+        const float2 whole = teacher_whole(K, a.t.scale, sm.teach);
         teacher = whole.y != 0.f;
         if (t < K) {
           const float2 q = teacher_q(kid >= 0, e.y, a.t.scale, whole);
@@ -1384,12 +1460,12 @@ tsp_status allow_smem(int most) {
 }
 
 constexpr int kOnePassMost = 200 * 1024;   // bytes of a part of the longest rows
-constexpr int kRingMost = kStages * kGroup * kMostThreads * 16;
-constexpr int64_t kRowsACta = 2;
-// S rows on as many CTAs (clusters of `parts` with CLUSTER, groups of `parts` without)
-// as fit at once.  MOST: dynamic shared memory at most.
+constexpr int kRingMost = 4 * kGroup * kMostThreads * 16;
+// S rows, `rows` of them a CTA (a cluster of `parts` with CLUSTER, a group of `parts`
+// without), or more where they would not fill the GPU.  MOST: dynamic shared memory at most.
 template <auto KERNEL, bool CLUSTER, int MOST, typename A>
-tsp_status launch_rows(const A& a, int S, int threads, int parts, size_t smem, const char* name, cudaStream_t st) {
+tsp_status launch_rows(const A& a, int S, int threads, int parts, size_t smem, int64_t rows, const char* name,
+                       cudaStream_t st) {
   tsp_status r = allow_smem<KERNEL>(MOST);
   if (r != TSP_OK) return r;
   cudaLaunchConfig_t cfg = {};
@@ -1405,7 +1481,7 @@ tsp_status launch_rows(const A& a, int S, int threads, int parts, size_t smem, c
   cfg.numAttrs = CLUSTER ? 1 : 0;
   const int64_t fit = CLUSTER ? resident((const void*)KERNEL, cfg, parts)
                               : std::max<int64_t>(1, resident((const void*)KERNEL, cfg, 1) / parts);
-  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(S, std::max<int64_t>(fit, (S + kRowsACta - 1) / kRowsACta)) * parts));
+  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(S, std::max<int64_t>(fit, (S + rows - 1) / rows)) * parts));
   Prof prof(name, st);
   TSP_CUDA_TRY(cudaLaunchKernelEx(&cfg, KERNEL, a));
   return TSP_OK;
@@ -1418,24 +1494,38 @@ int parts_for(int64_t S, int64_t units, int parts) {
   while (parts <= 4 && S * parts * 2 <= num_sms() * 2 && units / (2 * parts) >= 256) parts *= 2;
   return parts;
 }
-size_t ring_bytes(int threads) { return (size_t)kStages * kGroup * threads * 16; }
-
-template <typename T, bool ENT, bool CLUSTER>
-tsp_status launch_fwd_c(const FwdArgs& a, int threads, const char* name, cudaStream_t st) {
-  if (threads == 128)
-    return launch_rows<fwd_kernel<T, ENT, CLUSTER, 128>, CLUSTER, kRingMost>(a, a.r.S, 128, a.parts, ring_bytes(128), name, st);
-  return launch_rows<fwd_kernel<T, ENT, CLUSTER, 256>, CLUSTER, kRingMost>(a, a.r.S, 256, a.parts, ring_bytes(256), name, st);
+// Rows a CTA: 64 KB, three times that with a teacher.  The GPU hands CTAs out as others end,
+// which evens out what multiprocessors get of the memory (8192 x 32000 bf16, loss with
+// gradient: 152 us, 180 where each resident CTA walks as many rows).
+template <typename T>
+int64_t rows_a_cta(int64_t V, int parts, bool teacher) {
+  const int64_t bytes = std::max<int64_t>(1, V * (int64_t)sizeof(T) / parts);
+  return std::max<int64_t>(1, 65536 / bytes) * (teacher ? 3 : 1);
 }
+constexpr int ring_bytes(int threads, bool top = false) { return stages_of(top) * kGroup * threads * 16; }
+
+template <typename T, bool ENT, bool TOP, bool CLUSTER, int THREADS>
+tsp_status launch_fwd_c(const FwdArgs& a, const char* name, cudaStream_t st) {
+  return launch_rows<fwd_kernel<T, ENT, TOP, CLUSTER, THREADS>, CLUSTER, ring_bytes(THREADS, TOP)>(
+      a, a.r.S, THREADS, a.parts, ring_bytes(THREADS, TOP), rows_a_cta<T>(a.r.V, a.parts, a.t.K > 0), name, st);
+}
+// The fewer threads a CTA has, the less a row costs that is not its logits: 128, as many
+// as keep the pipelines full (8192 x 32000 bf16: 82 us, 101 with 256); 64 for rows of two
+// groups of these (65536 x 4000: 118, 193 with 128); 256 for long lists.
 template <typename T>
 tsp_status launch_fwd_t(FwdArgs a, const char* name, cudaStream_t st) {
   const int64_t units = (int64_t)a.r.V * sizeof(T) / 16;
   a.parts = parts_for(a.r.S, units, 1);
-  const int threads = threads_for((units + a.parts - 1) / a.parts, std::max(a.top, a.t.K));
-  if (a.entropy)
-    return a.parts > 1 ? launch_fwd_c<T, true, true>(a, threads, name, st)
-                       : launch_fwd_c<T, true, false>(a, threads, name, st);
-  return a.parts > 1 ? launch_fwd_c<T, false, true>(a, threads, name, st)
-                     : launch_fwd_c<T, false, false>(a, threads, name, st);
+  const bool ent = a.entropy != nullptr;
+  if (a.parts > 1) return launch_fwd_c<T, true, true, true, 256>(a, name, st);
+  if (a.top > 64) return launch_fwd_c<T, true, true, false, 256>(a, name, st);
+  if (a.top > 0) return launch_fwd_c<T, true, true, false, 128>(a, name, st);
+  if (a.t.K > 128) return launch_fwd_c<T, false, false, false, 256>(a, name, st);
+  if (a.t.K > 64 || units > 2 * kGroup * 128)
+    return ent ? launch_fwd_c<T, true, false, false, 128>(a, name, st)
+               : launch_fwd_c<T, false, false, false, 128>(a, name, st);
+  return ent ? launch_fwd_c<T, true, false, false, 64>(a, name, st)
+             : launch_fwd_c<T, false, false, false, 64>(a, name, st);
 }
 tsp_status launch_fwd(const FwdArgs& a, int dtype, const char* name, cudaStream_t st) {
   return dtype == TSP_BF16 ? launch_fwd_t<__nv_bfloat16>(a, name, st) : launch_fwd_t<float>(a, name, st);
@@ -1460,9 +1550,10 @@ tsp_status launch_grad_t(GradArgs a, const char* name, cudaStream_t st) {
   }
   a.parts = parts_for(a.r.S, units, 1);
   const int threads = threads_for((units + a.parts - 1) / a.parts, a.t.K);
+  const int64_t rows = rows_a_cta<T>(a.r.V, a.parts, a.t.K > 0);
   if (threads == 128)
-    return launch_rows<grad_kernel<T, ENT, 128>, false, kRingMost>(a, a.r.S, 128, a.parts, ring_bytes(128), name, st);
-  return launch_rows<grad_kernel<T, ENT, 256>, false, kRingMost>(a, a.r.S, 256, a.parts, ring_bytes(256), name, st);
+    return launch_rows<grad_kernel<T, ENT, 128>, false, kRingMost>(a, a.r.S, 128, a.parts, ring_bytes(128), rows, name, st);
+  return launch_rows<grad_kernel<T, ENT, 256>, false, kRingMost>(a, a.r.S, 256, a.parts, ring_bytes(256), rows, name, st);
 }
 tsp_status launch_grad(const GradArgs& a, int dtype, const char* name, cudaStream_t st) {
   const bool ent = a.up_entropy != nullptr;
@@ -1489,9 +1580,10 @@ tsp_status launch_one_pass_c(const OnePassArgs& o, cudaStream_t st) {
   const int64_t per = ((int64_t)o.g.r.V * sizeof(T) / 16 + parts - 1) / parts;
   const int threads = threads_for(per, o.g.t.K);
   const size_t smem = part_bytes(per, threads);
+  const int64_t rows = CLUSTER ? o.g.r.S : rows_a_cta<T>(o.g.r.V, parts, o.g.t.K > 0);
   if (threads == 128)
-    return launch_rows<one_pass_kernel<T, CLUSTER, 128>, CLUSTER, kOnePassMost>(o, o.g.r.S, 128, parts, smem, "token_loss_one_pass", st);
-  return launch_rows<one_pass_kernel<T, CLUSTER, 256>, CLUSTER, kOnePassMost>(o, o.g.r.S, 256, parts, smem, "token_loss_one_pass", st);
+    return launch_rows<one_pass_kernel<T, CLUSTER, 128>, CLUSTER, kOnePassMost>(o, o.g.r.S, 128, parts, smem, rows, "token_loss_one_pass", st);
+  return launch_rows<one_pass_kernel<T, CLUSTER, 256>, CLUSTER, kOnePassMost>(o, o.g.r.S, 256, parts, smem, rows, "token_loss_one_pass", st);
 }
 
 }  // namespace

@@ -136,11 +136,18 @@ def test_logprobs_fwd(S, V, D, wide, at, dt):
     i, logp, tol = r.order(top)
     assert torch.equal(got["top_ids"].cpu().long(), i)
     near(got["top_logp"], logp, tol, "top_logp")
-    # each result by itself, int32 ids, and once more: the same bits
-    for k, kw in (("logp", {}), ("entropy", dict(entropy=True)), ("stats", dict(stats=True)),
-                  ("top_ids", dict(top=top))):
-        some = tsp.logprobs_fwd(x, ids.int().cuda() if k == "logp" else None, D=D, scale=scale, **kw)
-        assert torch.equal(some[k], got[k]), k
+    # each result by itself, int32 ids (other kernels, which add up in other orders): held to
+    # the definition in the same way
+    some = tsp.logprobs_fwd(x, ids.int().cuda(), D=D, scale=scale)
+    near(some["logp"], r.logp[one, ids], r.d_logp[one, ids], "logp alone")
+    some = tsp.logprobs_fwd(x, D=D, scale=scale, entropy=True)
+    near(some["entropy"], r.entropy, r.d_entropy, "entropy alone")
+    some = tsp.logprobs_fwd(x, D=D, scale=scale, stats=True)
+    near(some["stats"][:, 1], r.l[:, 0], r.dl + 2 * U * r.l[:, 0].abs(), "l alone")
+    some = tsp.logprobs_fwd(x, D=D, scale=scale, top=top)
+    assert torch.equal(some["top_ids"].cpu().long(), i)
+    near(some["top_logp"], logp, tol, "top_logp alone")
+    # once more: the same bits
     again = tsp.logprobs_fwd(x, ids.cuda(), D=D, scale=scale, top=top, entropy=True, stats=True)
     assert all(torch.equal(again[k], got[k]) for k in got)
 
