@@ -172,6 +172,11 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t not_below(uint32_t a, uint32_t b) {   // (NaN stays)
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // The largest of N units; NaN does not count.
 template <typename T, int N> __device__ __forceinline__ float largest(const uint4 (&u)[N]) {
   if constexpr (sizeof(T) == 2) {
@@ -280,38 +285,63 @@ struct Exchange {
 // Sums
 // ---------------------------------------------------------------------------
 // A thread's sums over its logits, s = sum 2^u and a = sum 2^u u with u = c2 x - R.
-template <bool ENT>
+// What lies so far below R that 2^u is 0 must not be infinite in a's products: bf16
+// logits are kept at `floor`, two in an instruction, fp32 exponents at kLeast.
+template <typename T, bool ENT>
 struct Sums {
   float R, limit, top;      // reference, c2 x that renews it, largest logit so far
-  f2 neg, s, a;
-  __device__ __forceinline__ Sums()
-      : R(-kFar), limit(-kFar), top(-INFINITY), neg(two(kFar, kFar)), s(0), a(0) {}
-
-  __device__ __forceinline__ void see(float largest, float c2) {
+  float c2;
+  f2 c, neg, s, a;
+  uint32_t floor;
+  __device__ __forceinline__ explicit Sums(float scale) : top(-INFINITY), c2(scale), c(two(scale, scale)), s(0), a(0) {
+    refer_to(-kFar);
+    limit = -kFar;
+  }
+  __device__ __forceinline__ void refer_to(float to) {
+    R = to;
+    limit = to + kSlack;
+    neg = two(-to, -to);
+    if constexpr (ENT && sizeof(T) == 2) {   // (192: more than any rounding here, and 2^-127 is 0)
+      const uint32_t f = __bfloat16_as_ushort(__float2bfloat16_rd((to - 192.f) / c2));
+      floor = f << 16 | f;
+    }
+  }
+  __device__ __forceinline__ void see(float largest) {
     top = fmaxf(top, largest);
     const float y = largest * c2;
     if (y > limit) {
       const float to = ceilf(y), d = fmaxf(R - to, kLeast), f = ex2_approx(d);
       if (ENT) a = mul_two(fma_two(s, two(d, d), a), two(f, f));
       s = mul_two(s, two(f, f));
-      R = to;
-      limit = to + kSlack;
-      neg = two(-to, -to);
+      refer_to(to);
     }
   }
-  __device__ __forceinline__ void add(f2 x, f2 c2) {
-    const f2 u = fma_two(x, c2, neg), e = ex2_two(u);
+  template <bool HIGH>   // HIGH: nothing is below `floor`
+  __device__ __forceinline__ void add(f2 x) {
+    const f2 u = fma_two(x, c, neg), e = ex2_two(u);
     s = add_two(s, e);
-    if (ENT) a = fma_two(e, not_least(u), a);
+    if (ENT) a = fma_two(e, HIGH ? u : not_least(u), a);
+  }
+  __device__ __forceinline__ void add_one(float x) {
+    see(x);
+    add<false>(two(x, -INFINITY));
   }
   // Their largest logit.
-  template <typename T, int N> __device__ __forceinline__ float add_units(const uint4 (&v)[N], float c, f2 c2) {
+  template <int N> __device__ __forceinline__ float add_units(const uint4 (&v)[N]) {
     const float b = largest<T, N>(v);
-    see(b, c);
+    see(b);
 #pragma unroll
-    for (int k = 0; k < N; ++k)
+    for (int k = 0; k < N; ++k) {
+      if constexpr (ENT && sizeof(T) == 2) {
+        const uint4 w = make_uint4(not_below(v[k].x, floor), not_below(v[k].y, floor), not_below(v[k].z, floor),
+                                   not_below(v[k].w, floor));
 #pragma unroll
-      for (int e = 0; e < RowPart<T>::E / 2; ++e) add(pair<T>(v[k], e), c2);
+        for (int e = 0; e < RowPart<T>::E / 2; ++e) add<true>(pair<T>(w, e));
+      } else {
+#pragma unroll
+        for (int e = 0; e < RowPart<T>::E / 2; ++e) add<false>(pair<T>(v[k], e));
+      }
+    }
     return b;
   }
 };
@@ -327,8 +357,8 @@ __device__ __forceinline__ void onto(float R, float from, float& s, float& a) {
 }
 // Over the CTA, in every thread; a fixed order.  One barrier, behind which `part` may
 // be read until the CTA's next one.
-template <bool ENT, int THREADS>
-__device__ __forceinline__ Joined join(const Sums<ENT>& t, float4* part) {
+template <typename T, bool ENT, int THREADS>
+__device__ __forceinline__ Joined join(const Sums<T, ENT>& t, float4* part) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float2 s2 = both(t.s), a2 = both(t.a);
   float s = s2.x + s2.y, a = ENT ? a2.x + a2.y : 0.f;
@@ -412,10 +442,10 @@ __device__ __forceinline__ Stats stats_of(float m, float s, float a, float shift
 // units again; `loose`: its element outside the units or -inf; `parity`: of the row's
 // exchange.  Every thread of the CTA (of the cluster) takes part.
 template <typename T, bool ENT, bool CLUSTER, int THREADS>
-__device__ __forceinline__ Stats statistics(const Sums<ENT>& sums, const uint4* units, int n, float loose,
+__device__ __forceinline__ Stats statistics(const Sums<T, ENT>& sums, const uint4* units, int n, float loose,
                                             float c2, float4* part, Exchange* ex, uint32_t parity, int rank,
                                             int parts, const Wait& wait) {
-  Joined j = join<ENT, THREADS>(sums, part);
+  Joined j = join<T, ENT, THREADS>(sums, part);
   if (CLUSTER) {
     const int t = threadIdx.x;
     const uint32_t bar = smem_u32(&ex->bar_share);
@@ -609,6 +639,7 @@ __device__ __forceinline__ int groups_of(int V, int parts) {
 // Stages of the rings: 32 KB for 128 threads, six CTAs a multiprocessor; with room for the
 // alternatives' search a quarter less.
 __host__ __device__ constexpr int stages_of(bool top) { return top ? 3 : 4; }
+__host__ __device__ constexpr int ring_bytes(int threads, bool top = false) { return stages_of(top) * kGroup * threads * 16; }
 
 // Groups of rows that are not padding sent for ahead of their use, into the places of a
 // ring by turns: STAGES commits are on their way at any time.
@@ -686,17 +717,28 @@ __device__ __forceinline__ uint64_t key_of(float x, int j) {
 }
 constexpr uint32_t kOrderNone = 0x007fffffu;   // order_of(-inf)
 
-// Where alternatives are wanted, a thread leaves the largest logit (rounded up to 16 bits)
-// of each of up to kSlots runs of its groups.
-constexpr int kSlots = 16, kListed = 512;
+// Where alternatives are wanted, a thread leaves the upper half of the order of the largest
+// logit of each of up to kSlots runs of its groups, behind the ring.
+constexpr int kSlots = 32, kListed = 512;
 template <int THREADS> struct TopSmem {
   static constexpr int kCandidates = 4 * THREADS;
   uint64_t key[kCandidates], above;
-  alignas(16) float best[THREADS];      // largest logit of each set of threads
-  __nv_bfloat16 slot[kSlots][THREADS];
+  alignas(16) uint16_t best[THREADS];   // largest logit of each thread, the upper half of its order
   uint16_t listed[kListed];             // slots to be looked at once more
   int n, n_listed;
 };
+// The first of `count` places of the calling lane's out of a counter; the whole warp calls.
+__device__ __forceinline__ int places(int count, int* counter) {
+  int upto = count;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+    if ((threadIdx.x & 31) >= o) upto += v;
+  }
+  int base = 0;
+  if ((threadIdx.x & 31) == 31 && upto > 0) base = atomicAdd(counter, upto);
+  return __shfl_sync(0xffffffffu, base, 31) + upto - count;
+}
 struct TopLists {             // of a cluster's parts, in the first CTA
   uint64_t key[8][TSP_TOP_MAX];
   int n[8];
@@ -729,6 +771,7 @@ __device__ __forceinline__ void for_ranked(const uint64_t* key, int n, F put) {
   for (int k = t >> log_g; k - ((t & 31) >> log_g) < n; k += THREADS >> log_g) {   // (whole warps)
     const uint64_t mine = k < n ? key[k] : 0;
     int rank = 0;
+#pragma unroll 8
     for (int q = t & (g - 1); q < n; q += g) rank += key[q] > mine;
     for (int o = 1; o < g; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
     if (k < n && (t & (g - 1)) == 0) put(rank, mine);
@@ -743,62 +786,79 @@ __device__ __forceinline__ void for_ranked(const uint64_t* key, int n, F put) {
 // A slot is 2^shift groups of a thread.
 template <typename T, int THREADS>
 __device__ __noinline__ int candidates(const RowPart<T>& x, int top, float mine, int groups, int shift,
-                                       TopSmem<THREADS>& sm) {
+                                       const uint16_t* slot, TopSmem<THREADS>& sm) {
   const int t = threadIdx.x;
-  int g = 1;   // threads a set
-  while (g < 32 && THREADS / (2 * g) >= 2 * top) g *= 2;
-  float b = mine;
-  for (int o = 1; o < g; o *= 2) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
-  const int sets = THREADS / g, i = t / g;
-  if (t % g == 0) sm.best[i] = b;
-  if (t == 0) {
-    sm.n = sm.n_listed = 0;
-    sm.above = (uint64_t)(kOrderNone + 1) << 32;
-  }
+  sm.best[t] = (uint16_t)(order_of(mine) >> 16);
+  if (t == 0) sm.n = sm.n_listed = 0;
   __syncthreads();
-  int rank = 0;
-  for (int j = 4 * (t % g); j < sets; j += 4 * g) {   // (sets: a multiple of 4)
-    const float4 o = *reinterpret_cast<const float4*>(sm.best + j);
-    rank += (o.x > b || (o.x == b && j < i)) + (o.y > b || (o.y == b && j + 1 < i)) +
-            (o.z > b || (o.z == b && j + 2 < i)) + (o.w > b || (o.w == b && j + 3 < i));
+  // the largest 16 bits that `top` threads reach, bit by bit, in every warp
+  constexpr int OWN = THREADS / 32;
+  uint16_t own[OWN];
+  memcpy(own, sm.best + OWN * (t & 31), sizeof(own));
+  uint32_t reached = 0;
+#pragma unroll
+  for (int bit = 15; bit >= 0; --bit) {
+    const uint32_t v = reached | 1u << bit;
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < OWN; ++k) n += own[k] >= v;
+    if (__reduce_add_sync(0xffffffffu, n) >= top) reached = v;
   }
-  for (int o = 1; o < g; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-  if (rank == top - 1 && t % g == 0 && b > -INFINITY) sm.above = (uint64_t)order_of(b) << 32;
-  __syncthreads();
+  uint64_t above = (uint64_t)max(reached << 16, kOrderNone + 1) << 32;
   const int slots = (groups + (1 << shift) - 1) >> shift, log_per = 2 + shift;   // units of a slot
   static_assert(kGroup == 4, "log_per");
   for (;;) {
-    const uint64_t above = sm.above;
     const uint32_t bound = (uint32_t)(above >> 32);
-    auto reaches = [&](int s, int who) { return order_of(__bfloat162float(sm.slot[s][who])) >= bound; };
-    for (int s = 0; order_of(mine) >= bound && s < slots; ++s)
-      if (reaches(s, t)) {
-        const int n = atomicAdd(&sm.n_listed, 1);
-        if (n < kListed) sm.listed[n] = (uint16_t)(s * THREADS + t);
-      }
-    auto take = [&](float v, int j) {
-      const uint64_t k = key_of(v, j);
-      if (k < above) return;
-      const int n = atomicAdd(&sm.n, 1);
-      if (n < TopSmem<THREADS>::kCandidates) sm.key[n] = k;
+    // the slots of this thread that reach the bound, a bit each
+    uint32_t mask = 0;
+    if (order_of(mine) >= bound)
+      for (int s = 0; s < slots; ++s) mask |= (slot[s * THREADS + t] >= bound >> 16) << s;
+    int at = places(__popc(mask), &sm.n_listed);
+    for (uint32_t m = mask; m; m &= m - 1, ++at)
+      if (at < kListed) sm.listed[at] = (uint16_t)((__ffs(m) - 1) * THREADS + t);
+    // the elements of a unit that reach it, a bit each
+    const float least = logit_of(bound);
+    auto element = [&](const uint4& v, int e) {
+      T el[RowPart<T>::E], y;
+      memcpy(el, &v, 16);
+      y = el[0];
+#pragma unroll
+      for (int q = 1; q < RowPart<T>::E; ++q)
+        if (q == e) y = el[q];
+      return to_f<T>(y);
     };
-    auto look = [&](const uint4& v, int u) {
-      const uint4 one[1] = {v};
-      if (order_of(largest<T, 1>(one)) < bound) return;
+    auto token = [&](int u, int e) { return x.head + (x.u_lo + u) * RowPart<T>::E + e; };
+    auto reaching = [&](const uint4& v, int u) {
+      uint32_t r = 0;
 #pragma unroll
       for (int e = 0; e < RowPart<T>::E / 2; ++e) {
         const float2 y = both(pair<T>(v, e));
-        take(y.x, x.head + (x.u_lo + u) * RowPart<T>::E + 2 * e);
-        take(y.y, x.head + (x.u_lo + u) * RowPart<T>::E + 2 * e + 1);
+        r |= (y.x >= least) << (2 * e) | (y.y >= least) << (2 * e + 1);
       }
+      if ((uint32_t)above != 0)   // a bound with a token: equal logits of later ones do not
+        for (uint32_t m = r; m; m &= m - 1) {
+          const int e = __ffs(m) - 1;
+          if (key_of(element(v, e), token(u, e)) < above) r &= ~(1u << e);
+        }
+      return r;
     };
-    const int j0 = x.loose(t);
-    if (j0 >= 0) take(to_f<T>(x.row[j0]), j0);
+    auto keep = [&](uint64_t key, int place) {
+      if (place < TopSmem<THREADS>::kCandidates) sm.key[place] = key;
+    };
+    auto keep_unit = [&](const uint4& v, int u, uint32_t r, int& place) {
+      for (; r; r &= r - 1, ++place) keep(key_of(element(v, __ffs(r) - 1), token(u, __ffs(r) - 1)), place);
+    };
+    if (t < 32) {   // the elements outside the units (RowPart::loose: of the first lanes)
+      const int j = x.loose(t);
+      const uint64_t key = j >= 0 ? key_of(to_f<T>(x.row[j]), j) : 0;
+      const int place = places(key >= above ? 1 : 0, &sm.n);
+      if (key >= above) keep(key, place);
+    }
     __syncthreads();
     const int listed = sm.n_listed;
     if (listed <= kListed) {
-      constexpr int U = 4;   // loads on their way
-      for (int w0 = t; w0 < listed << log_per; w0 += U * THREADS) {
+      constexpr int U = 2;   // loads on their way
+      for (int w0 = t; w0 - (t & 31) < listed << log_per; w0 += U * THREADS) {   // (whole warps)
         uint4 v[U];
         int u[U];
 #pragma unroll
@@ -811,16 +871,26 @@ __device__ __noinline__ int candidates(const RowPart<T>& x, int top, float mine,
           }
           v[k] = u[k] < x.n ? x.src[u[k]] : no_unit<T>();
         }
+        uint32_t r[U];
+        int count = 0;
 #pragma unroll
-        for (int k = 0; k < U; ++k)
-          if (u[k] < x.n) look(v[k], u[k]);
+        for (int k = 0; k < U; ++k) {
+          r[k] = reaching(v[k], u[k]);
+          count += __popc(r[k]);
+        }
+        int place = places(count, &sm.n);
+#pragma unroll
+        for (int k = 0; k < U; ++k) keep_unit(v[k], u[k], r[k], place);
       }
     } else {   // many equal logits: every thread its own
-      for (int s = 0; s < slots; ++s) {
-        if (!reaches(s, t)) continue;
+      for (uint32_t m = mask; m; m &= m - 1) {
+        const int s = __ffs(m) - 1;
         for (int k = s << log_per; k < (s + 1) << log_per; ++k) {
           const int u = k * THREADS + t;
-          if (u < x.n) look(x.src[u], u);
+          if (u >= x.n) continue;
+          const uint32_t r = reaching(x.src[u], u);
+          int place = r ? atomicAdd(&sm.n, __popc(r)) : 0;
+          keep_unit(x.src[u], u, r, place);
         }
       }
     }
@@ -834,6 +904,7 @@ __device__ __noinline__ int candidates(const RowPart<T>& x, int top, float mine,
       if (rank_in(sm.key, TopSmem<THREADS>::kCandidates, sm.key[k]) == top - 1) sm.above = sm.key[k];
     if (t == 0) sm.n = sm.n_listed = 0;
     __syncthreads();
+    above = sm.above;
   }
 }
 
@@ -855,6 +926,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
   const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
   const int K = a.loss && a.t.w_kd != 0.f ? a.t.K : 0;
   Sender<T, THREADS, stages_of(TOP)> sender(a.r, ring, at, groups);
+  uint16_t* slot = reinterpret_cast<uint16_t*>(ring + ring_bytes(THREADS, TOP) / 16);
   int shift = 0;   // groups a slot
   while (TOP && (groups - 1) >> shift >= kSlots) ++shift;
   if constexpr (CLUSTER) start_exchange(sm.ex);
@@ -889,7 +961,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
     Entry e = {-1, -INFINITY};
     int kid = -1;
     if (t < K && at.rank == 0) e = load_entry(a.t, p, t);
-    Sums<ENT> sums;
+    Sums<T, ENT> sums(c2);
     float in_slot = -INFINITY;
     for (int g = 0; g < groups; ++g) {
       uint4 v[kGroup];
@@ -897,11 +969,11 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
 #pragma unroll
       for (int k = 0; k < kGroup; ++k) v[k] = from[k * THREADS];
       sender.send();
-      const float b = sums.template add_units<T, kGroup>(v, c2, two(c2, c2));
+      const float b = sums.template add_units<kGroup>(v);
       if constexpr (TOP) {
         in_slot = fmaxf(in_slot, b);
         if (((g + 1) & ((1 << shift) - 1)) == 0 || g + 1 == groups) {
-          sm.top.slot[g >> shift][t] = __float2bfloat16_ru(in_slot);
+          slot[(g >> shift) * THREADS + t] = (uint16_t)(order_of(in_slot) >> 16);
           in_slot = -INFINITY;
         }
       }
@@ -911,8 +983,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
       }
     }
     const float mine = sums.top;   // of the units
-    sums.see(x0, c2);
-    sums.add(two(x0, -INFINITY), two(c2, c2));
+    sums.add_one(x0);
     if (K > 0) teacher_part(K, kid >= 0, e.y, a.t.scale, sm.teach);
     Exchange* ex = nullptr;
     if constexpr (CLUSTER) ex = &sm.ex[live & 1];
@@ -953,7 +1024,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
         a.top_logp[to + rank] = log_p(logit_of((uint32_t)(key >> 32)), st, c);
       };
       if (a.top > 0 && !isnan(st.l)) {
-        n = candidates<T, THREADS>(x, a.top, mine, groups, shift, sm.top);
+        n = candidates<T, THREADS>(x, a.top, mine, groups, shift, slot, sm.top);
         if constexpr (!CLUSTER) {
           for_ranked<THREADS>(sm.top.key, n, put);
         } else {
@@ -1269,17 +1340,16 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
       if (a.up) up = a.up[p];
       Entry e = {-1, -INFINITY};
       if (t < K) e = load_entry(a.t, p, t);
-      Sums<false> sums;
+      Sums<T, false> sums(c2);
       for (int g = 0; g < groups; ++g) {
         copies_left(groups - 1 - g);
         uint4 v[kGroup];
         const uint4* from = seg + t + kGroup * g * THREADS;
 #pragma unroll
         for (int k = 0; k < kGroup; ++k) v[k] = from[k * THREADS];
-        sums.template add_units<T, kGroup>(v, c2, two(c2, c2));
+        sums.template add_units<kGroup>(v);
       }
-      sums.see(x0, c2);
-      sums.add(two(x0, -INFINITY), two(c2, c2));
+      sums.add_one(x0);
       int kid = -1;
       if (K > 0) {
         if (t < K) kid = token_of(e, a.r);
@@ -1502,12 +1572,15 @@ int64_t rows_a_cta(int64_t V, int parts, bool teacher) {
   const int64_t bytes = std::max<int64_t>(1, V * (int64_t)sizeof(T) / parts);
   return std::max<int64_t>(1, 65536 / bytes) * (teacher ? 3 : 1);
 }
-constexpr int ring_bytes(int threads, bool top = false) { return stages_of(top) * kGroup * threads * 16; }
 
 template <typename T, bool ENT, bool TOP, bool CLUSTER, int THREADS>
 tsp_status launch_fwd_c(const FwdArgs& a, const char* name, cudaStream_t st) {
-  return launch_rows<fwd_kernel<T, ENT, TOP, CLUSTER, THREADS>, CLUSTER, ring_bytes(THREADS, TOP)>(
-      a, a.r.S, THREADS, a.parts, ring_bytes(THREADS, TOP), rows_a_cta<T>(a.r.V, a.parts, a.t.K > 0), name, st);
+  constexpr int ring = ring_bytes(THREADS, TOP), most = ring + (TOP ? kSlots * THREADS * 2 : 0);
+  const int64_t per = (a.r.V * (int64_t)sizeof(T) / 16 + a.parts - 1) / a.parts;
+  const int64_t groups = std::max<int64_t>(1, (per + kGroup * THREADS - 1) / (kGroup * THREADS));
+  const size_t smem = ring + (TOP ? std::min<int64_t>(kSlots, groups) * THREADS * 2 : 0);
+  return launch_rows<fwd_kernel<T, ENT, TOP, CLUSTER, THREADS>, CLUSTER, most>(
+      a, a.r.S, THREADS, a.parts, smem, rows_a_cta<T>(a.r.V, a.parts, a.t.K > 0), name, st);
 }
 // The fewer threads a CTA has, the less a row costs that is not its logits: 128, as many
 // as keep the pipelines full (8192 x 32000 bf16: 82 us, 101 with 256); 64 for rows of two
@@ -1519,7 +1592,9 @@ tsp_status launch_fwd_t(FwdArgs a, const char* name, cudaStream_t st) {
   const bool ent = a.entropy != nullptr;
   if (a.parts > 1) return launch_fwd_c<T, true, true, true, 256>(a, name, st);
   if (a.top > 64) return launch_fwd_c<T, true, true, false, 256>(a, name, st);
-  if (a.top > 0) return launch_fwd_c<T, true, true, false, 128>(a, name, st);
+  if (a.top > 0)
+    return ent ? launch_fwd_c<T, true, true, false, 128>(a, name, st)
+               : launch_fwd_c<T, false, true, false, 128>(a, name, st);
   if (a.t.K > 128) return launch_fwd_c<T, false, false, false, 256>(a, name, st);
   if (a.t.K > 64 || units > 2 * kGroup * 128)
     return ent ? launch_fwd_c<T, true, false, false, 128>(a, name, st)
