@@ -493,9 +493,8 @@ __device__ __forceinline__ int token_of(const Entry& e, const Rows& r) {
   if (e.id >= r.V) report_status(r.status, (int)TSP_ERR_RANGE);
   return e.id >= 0 && e.id < r.V && !(e.y == -INFINITY) ? e.id : -1;
 }
-// The list's softmax, entry k thread k's (there: it counts): the warps' parts before the
-// CTA's next barrier, the whole behind it, in the warps that have entries; in the others
-// only whether there is an entry.
+// The list's softmax, entry k thread k's (there: it counts): the warps' parts before a
+// barrier of the CTA, the whole behind it, in the warps that have entries.
 __device__ __forceinline__ void teacher_part(int K, bool there, float y, float scale, float2* teach) {
   if ((int)(threadIdx.x & ~31) >= K) return;
   const float mw = lanes_max(there ? y : -INFINITY);
@@ -503,9 +502,8 @@ __device__ __forceinline__ void teacher_part(int K, bool there, float y, float s
   if ((threadIdx.x & 31) == 0) teach[threadIdx.x >> 5] = make_float2(mw, sw);
 }
 __device__ __forceinline__ float2 teacher_whole(int K, float scale, const float2* teach) {   // (largest, sum)
-  const int warps = (K + 31) / 32, lane = threadIdx.x & 31;
-  const float2 w = lane < warps ? teach[lane] : make_float2(-INFINITY, 0.f);
-  if ((int)(threadIdx.x & ~31) >= K) return make_float2(0.f, __any_sync(0xffffffffu, w.y != 0.f) ? 1.f : 0.f);
+  const int lane = threadIdx.x & 31;
+  const float2 w = lane < (K + 31) / 32 ? teach[lane] : make_float2(-INFINITY, 0.f);
   const float m = lanes_max(w.x);
   return make_float2(m, lanes_sum<32>(w.y == 0.f ? 0.f : w.y * expf(scale * (w.x - m))));
 }
@@ -523,6 +521,19 @@ struct Adds {
 };
 __device__ __forceinline__ void end_adds(Adds& adds, int n) {
   if (threadIdx.x < 3) adds.id[n + threadIdx.x] = -1;
+}
+// A list in which a token may occur more than once; two barriers around it.
+template <int THREADS>
+__device__ __forceinline__ void put_adds(Adds& adds, int K, int token, float add, float z) {
+  const int t = threadIdx.x;
+  __syncthreads();
+  if (t < K) {
+    adds.id[t] = token;
+    adds.add[t] = add;
+    adds.z[t] = z;
+  }
+  end_adds(adds, K);
+  __syncthreads();
 }
 // put(k, token, what all its entries add in the order of the list) for the first entry
 // k of each token.  All threads of the CTA take part, a power of two of them an entry,
@@ -558,6 +569,31 @@ __device__ __forceinline__ void for_added(const Adds& adds, int n, F put) {
     }
     if (first) put(k, j, sum);
   }
+}
+
+// What a thread keeps of its entry while it writes gradients, in shared memory to leave
+// the registers to them.
+struct Kept {
+  int token[TSP_TOP_MAX], claimed[TSP_TOP_MAX];   // token: -1 for none of the row's
+  float y[TSP_TOP_MAX], z[TSP_TOP_MAX];
+};
+// Tokens that a row lists, so that one listed twice shows: a place of the table for each,
+// -1 where it has one already (and *twice is set).
+constexpr int kTable = 512;
+static_assert(kTable >= 2 * TSP_TOP_MAX, "the search for a free place is short");
+__device__ __forceinline__ int claim(int* table, int token, int* twice) {
+  for (uint32_t h = (uint32_t)token * 2654435761u >> 23;; h = (h + 1) % kTable) {
+    const int old = atomicCAS(table + h, -1, token);
+    if (old == -1) return (int)h;
+    if (old == token) {
+      *twice = 1;
+      return -1;
+    }
+  }
+}
+__device__ __forceinline__ bool any_entry(int K, const float2* teach) {
+  const int lane = threadIdx.x & 31;
+  return __any_sync(0xffffffffu, lane < (K + 31) / 32 && teach[lane].y != 0.f);
 }
 
 // ---------------------------------------------------------------------------
@@ -924,7 +960,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
   const Place at(CLUSTER ? a.parts : 1);
   const float c = a.r.scale, c2 = c * kLog2e;
   const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
-  const int K = a.loss && a.t.w_kd != 0.f ? a.t.K : 0;
+  const int K = a.loss ? a.t.K : 0;
   Sender<T, THREADS, stages_of(TOP)> sender(a.r, ring, at, groups);
   uint16_t* slot = reinterpret_cast<uint16_t*>(ring + ring_bytes(THREADS, TOP) / 16);
   int shift = 0;   // groups a slot
@@ -1001,16 +1037,16 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
     if (a.loss) {
       float kd = 0.f;
       if (K > 0) {
-        const float2 whole = teacher_whole(K, a.t.scale, sm.teach);
-        const float2 q = t < K ? teacher_q(kid >= 0, e.y, a.t.scale, whole) : make_float2(0.f, 0.f);
         if (warp * 32 < K) {
+          const float2 whole = teacher_whole(K, a.t.scale, sm.teach);
+          const float2 q = teacher_q(kid >= 0, e.y, a.t.scale, whole);
           kd = lanes_sum<32>(q.x != 0.f ? q.x * (q.y - log_p(z, st, c)) : 0.f);
           if (lane == 0) sm.kd[warp] = kd;
         }
         __syncthreads();
         kd = 0.f;
         for (int k = 0; 32 * k < K; ++k) kd += sm.kd[k];
-        kd = whole.y != 0.f ? a.t.w_kd * kd : 0.f;
+        kd = any_entry(K, sm.teach) ? a.t.w_kd * kd : 0.f;
       }
       if (t == 0 && at.rank == 0)
         a.loss[p] = (a.t.w_ce != 0.f ? -a.t.w_ce * log_p(target, st, c) : 0.f) + kd;
@@ -1115,26 +1151,37 @@ __device__ __forceinline__ float logit_in(const uint4* place, const RowPart<T>& 
   return to_f<T>(reinterpret_cast<const T*>(place + u)[(id - x.head) % RowPart<T>::E]);
 }
 
-// Without a teacher a row needs no barrier: the given token's value is written by the
-// thread that has its unit.  With one, the listed tokens' logits are read first and
-// their values written once more at the end.
-template <typename T, bool ENT, int THREADS>
+// The given token's value is written by the thread that has its unit, so that a row
+// without a teacher needs no barrier.  The tokens a teacher lists are written once more
+// at the end, each by the thread that has the entry.
+template <typename T, bool ENT, bool LIST, int THREADS>   // LIST: with a teacher
 __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __grid_constant__ GradArgs a) {
   extern __shared__ uint4 ring[];
-  __shared__ struct {
-    float2 teach[THREADS / 32];
-    Adds adds;
-  } sm;
+  struct Shared {
+    float2 teach[2][THREADS / 32];   // (of two rows by turns)
+    int table[2][kTable], twice[2];
+    union {
+      Kept kept;
+      Adds adds;   // (once kept has been read)
+    };
+  };
+  __shared__ typename std::conditional<LIST, Shared, Nothing>::type sm;
   const int t = threadIdx.x;
   const Place at(a.parts);
   const float c2 = a.r.scale * kLog2e;
   const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
-  const int K = a.loss && a.t.w_kd != 0.f ? a.t.K : 0;
+  const int K = LIST ? a.t.K : 0;
   Sender<T, THREADS, stages_of(false)> sender(a.r, ring, at, groups);
   int id = given(a.r, at.first);
   Upstream up = upstream<ENT>(a, at.first);
   Entry e = {-1, -INFINITY};
-  if (t < K && at.first < a.r.S) e = load_entry(a.t, pos_of(a.r, at.first), t);
+  if constexpr (LIST) {
+    if (t < K && at.first < a.r.S) e = load_entry(a.t, pos_of(a.r, at.first), t);
+    for (int k = t; k < 2 * kTable; k += THREADS) sm.table[k / kTable][k % kTable] = -1;
+    if (t < 2) sm.twice[t] = 0;
+    __syncthreads();
+  }
+  int turn = 0;
   for (int r = at.first; r < a.r.S; r += at.stride) {
     const int id_now = id;
     const Upstream u = up;
@@ -1143,7 +1190,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __gr
     if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
     id = given(a.r, r + at.stride);
     up = upstream<ENT>(a, r + at.stride);
-    if (t < K && r + at.stride < a.r.S) e = load_entry(a.t, pos_of(a.r, r + at.stride), t);
+    if (LIST && t < K && r + at.stride < a.r.S) e = load_entry(a.t, pos_of(a.r, r + at.stride), t);
     const RowPart<T> x(a.r, r, at.rank, at.parts);
     T* out = reinterpret_cast<T*>(a.out) + (int64_t)r * a.ld_out;
     uint4* dst = reinterpret_cast<uint4*>(out + x.head) + x.u_lo + t;
@@ -1161,43 +1208,31 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __gr
     }
     const float x0 = j0 >= 0 ? to_f<T>(x.row[j0]) : -INFINITY;
     bool teacher = false;
-    int kid = -1;
-    if (K > 0) {
-      if (t < K) kid = token_of(entry, a.r);
-      teacher_part(K, kid >= 0, entry.y, a.t.scale, sm.teach);
-      __syncthreads();
-      const float2 whole = teacher_whole(K, a.t.scale, sm.teach);
-      teacher = whole.y != 0.f;
+    if constexpr (LIST) {
+      const int token = t < K ? token_of(entry, a.r) : -1;
+      teacher_part(K, token >= 0, entry.y, a.t.scale, sm.teach[turn]);
       if (t < K) {
-        const bool here = kid >= x.lo && kid < x.hi;
-        sm.adds.id[t] = here ? kid : -1;
-        sm.adds.add[t] = -u.up * a.r.scale * a.t.w_kd * teacher_q(kid >= 0, entry.y, a.t.scale, whole).x;
-        if (here) sm.adds.z[t] = to_f<T>(x.row[kid]);
+        const bool here = token >= x.lo && token < x.hi;
+        sm.kept.token[t] = token;
+        sm.kept.y[t] = entry.y;
+        sm.kept.claimed[t] = here ? claim(sm.table[turn], token, &sm.twice[turn]) : -1;
+        if (here) sm.kept.z[t] = to_f<T>(x.row[token]);
       }
+      __syncthreads();   // (also: the listed logits are read before any is overwritten)
+      teacher = any_entry(K, sm.teach[turn]);
+      if (t == 0) sm.twice[turn ^ 1] = 0;
     }
     const Factors f = factors(a, u, teacher);
     const Slope<ENT> slope(u.m, u.l, c2, f.A, f.B);
     const bool adds_given = id_now >= 0 && (a.loss ? a.t.w_ce != 0.f : a.up != nullptr);
-    int own = -1;   // the group with the given token
-    if (K > 0) {
-      if (t == 0) {
-        const bool here = adds_given && id_now >= x.lo && id_now < x.hi;
-        sm.adds.id[K] = here ? id_now : -1;
-        sm.adds.add[K] = f.given;
-        if (here) sm.adds.z[K] = to_f<T>(x.row[id_now]);
-      }
-      end_adds(sm.adds, K + 1);
-      __syncthreads();   // the listed logits are read before any is overwritten
-    } else if (adds_given) {
-      own = group_with<T, THREADS>(x, id_now);
-    }
-    if (j0 >= 0) out[j0] = from_f<T>(slope.one(x0) + (K == 0 && adds_given && j0 == id_now ? f.given : 0.f));
+    const int own = adds_given ? group_with<T, THREADS>(x, id_now) : -1;   // the group with the given token
+    if (j0 >= 0) out[j0] = from_f<T>(slope.one(x0) + (adds_given && j0 == id_now ? f.given : 0.f));
     for (int g = 0, left = x.n - t; g < groups; ++g, left -= kGroup * THREADS, dst += kGroup * THREADS) {
       const uint4* place = sender.next();
       uint4 v[kGroup];
 #pragma unroll
       for (int k = 0; k < kGroup; ++k) v[k] = place[k * THREADS];
-      const float z = g == own ? logit_in<T, THREADS>(place - t, x, id_now) : 0.f;
+      const float x_given = g == own ? logit_in<T, THREADS>(place - t, x, id_now) : 0.f;
       sender.send();
       if (slope.far) {
         for (int k = 0; k < kGroup; ++k)
@@ -1209,13 +1244,34 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __gr
           if (left > k * THREADS) __stcs(dst + k * THREADS, w);
         }
       }
-      if (g == own) out[id_now] = from_f<T>(slope.one(z) + f.given);
+      if (g == own) out[id_now] = from_f<T>(slope.one(x_given) + f.given);
     }
-    if (K > 0) {
+    if constexpr (LIST) {
       __syncthreads();   // the listed tokens' values go on top of what other threads wrote
-      for_added<THREADS>(sm.adds, K + 1, [&](int k, int j, float sum) {
-        out[j] = from_f<T>(slope.one(sm.adds.z[k]) + sum);
-      });
+      const bool twice = sm.twice[turn] != 0;
+      int token = -1;
+      float add = 0.f, z = 0.f;
+      if ((t & ~31) < K) {
+        const float2 whole = teacher_whole(K, a.t.scale, sm.teach[turn]);
+        if (t < K) {
+          token = sm.kept.token[t];
+          add = -u.up * a.r.scale * a.t.w_kd * teacher_q(token >= 0, sm.kept.y[t], a.t.scale, whole).x;
+          const bool here = token >= x.lo && token < x.hi;
+          if (here) z = sm.kept.z[t];
+          if (here && !twice)
+            out[token] = from_f<T>(slope.one(z) + (add + (adds_given && token == id_now ? f.given : 0.f)));
+          if (!here) token = -1;
+          if (sm.kept.claimed[t] >= 0) sm.table[turn][sm.kept.claimed[t]] = -1;
+        }
+      }
+      if (twice) {
+        put_adds<THREADS>(sm.adds, K, token, add, z);
+        for_added<THREADS>(sm.adds, K, [&](int k, int j, float sum) {
+          out[j] = from_f<T>(slope.one(sm.adds.z[k]) + (sum + (adds_given && j == id_now ? f.given : 0.f)));
+        });
+        __syncthreads();   // (the next row's entries lie where these did)
+      }
+      turn ^= 1;
     }
   }
 }
@@ -1293,26 +1349,38 @@ struct OnePassArgs {
   float *loss, *stats;
 };
 
-template <typename T, bool CLUSTER, int THREADS>
+template <typename T, bool LIST, bool CLUSTER, int THREADS>   // LIST: with a teacher
 __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const __grid_constant__ OnePassArgs o) {
   extern __shared__ uint4 seg[];
+  struct Listed {
+    float2 teach[2][THREADS / 32];
+    int table[kTable], twice;
+    union {
+      Kept kept;
+      Adds adds;   // (once kept has been read)
+    };
+    float kd[THREADS / 32], loose[16];
+  };
   __shared__ struct {
     float4 part[2][THREADS / 32];
-    float2 teach[THREADS / 32];
-    Exchange ex[2];
-    Adds adds;                     // of this part
-    float q[TSP_TOP_MAX], logq[TSP_TOP_MAX];
-    float loose[16];
+    typename std::conditional<CLUSTER, Exchange, Nothing>::type ex[2];
+    typename std::conditional<LIST, Listed, Nothing>::type list;
   } sm;
   const GradArgs& a = o.g;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const Place at(CLUSTER ? a.parts : 1);
   const float c = a.r.scale, c2 = c * kLog2e;
   const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
-  const int K = a.t.w_kd != 0.f ? a.t.K : 0;
+  const int K = LIST ? a.t.K : 0;
   const uint32_t to = smem_u32(seg + t);
   int id = given(a.r, at.first);
-  if (CLUSTER) start_exchange(sm.ex);
+  Entry e = {-1, -INFINITY};
+  if constexpr (LIST) {
+    if (t < K && at.first < a.r.S) e = load_entry(a.t, pos_of(a.r, at.first), t);
+    for (int k = t; k < kTable; k += THREADS) sm.list.table[k] = -1;
+    if (t == 0) sm.list.twice = 0;
+  }
+  if constexpr (CLUSTER) start_exchange(sm.ex);
   bool there = false;   // this row's copies have been sent
   uint32_t live = 0;    // rows so far that are not padding
   for (int r = at.first; r < a.r.S; r += at.stride) {
@@ -1326,10 +1394,13 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
     const bool sent = there;
     there = r + at.stride < a.r.S && id != -1;
     RowPart<T> next(a.r, there ? r + at.stride : r, at.rank, at.parts);
-    Exchange& ex = sm.ex[live & 1];
+    Exchange* ex = nullptr;
+    if constexpr (CLUSTER) ex = &sm.ex[live & 1];
     Stats st = {0.f, -INFINITY, 0.f};
     float x0 = -INFINITY, up = 1.f, target = 0.f;
     bool teacher = false;
+    const Entry entry = e;
+    if (LIST && t < K && r + at.stride < a.r.S) e = load_entry(a.t, pos_of(a.r, r + at.stride), t);
     if (id_now != -1) {
       if (!sent)
         for (int g = 0; g < groups; ++g)
@@ -1338,8 +1409,6 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
       if (j0 >= 0) x0 = to_f<T>(x.row[j0]);
       if (t == 0 && id_now >= 0) target = to_f<T>(x.row[id_now]);
       if (a.up) up = a.up[p];
-      Entry e = {-1, -INFINITY};
-      if (t < K) e = load_entry(a.t, p, t);
       Sums<T, false> sums(c2);
       for (int g = 0; g < groups; ++g) {
         copies_left(groups - 1 - g);
@@ -1350,53 +1419,40 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
         sums.template add_units<kGroup>(v);
       }
       sums.add_one(x0);
-      int kid = -1;
-      if (K > 0) {
-        if (t < K) kid = token_of(e, a.r);
-        if (j0 >= 0) sm.loose[t] = x0;
-        teacher_part(K, kid >= 0, e.y, a.t.scale, sm.teach);
+      int token = -1;
+      if constexpr (LIST) {
+        if (t < K) token = token_of(entry, a.r);
+        if (j0 >= 0) sm.list.loose[t] = x0;
+        teacher_part(K, token >= 0, entry.y, a.t.scale, sm.list.teach[live & 1]);
       }
-      st = statistics<T, false, CLUSTER, THREADS>(sums, seg, x.n, x0, c2, sm.part[live & 1], &ex, live >> 1 & 1, at.rank,
+      st = statistics<T, false, CLUSTER, THREADS>(sums, seg, x.n, x0, c2, sm.part[live & 1], ex, live >> 1 & 1, at.rank,
                                                   at.parts, a.wait);
-      if (K > 0) {
-        // the logits of the listed tokens that are in this part (every thread's units are
-        // there since the sums were joined)
-        auto logit = [&](int j) {
-          return j < x.head    ? sm.loose[j]
-                 : j >= x.tail ? sm.loose[x.head + j - x.tail]
-                               : to_f<T>(reinterpret_cast<const T*>(seg)[j - x.head - x.u_lo * RowPart<T>::E]);
-        };
-        const bool here = kid >= x.lo && kid < x.hi;
-        if (t < K) sm.adds.id[t] = here ? kid : -1;
-        if (here) sm.adds.z[t] = logit(kid);
-        if (CLUSTER) {   // each entry's comes from one CTA
-          const uint32_t bar = smem_u32(&ex.bar_z);
-          if (at.rank == 0 && t == 0) mbar_arrive_expect_tx(bar, 4 * K);
-          if (here || (at.rank == 0 && t < K && kid < 0))
-            give(in_cta(smem_u32(&ex.z[t]), 0), here ? sm.adds.z[t] : 0.f, in_cta(bar, 0));
-        }
-        if (t == 0) {
-          const bool given_here = id_now >= x.lo && id_now < x.hi && a.t.w_ce != 0.f;
-          sm.adds.id[K] = given_here ? id_now : -1;
-          if (given_here) sm.adds.z[K] = logit(id_now);
-        }
-        end_adds(sm.adds, K + 1);
-        const float2 whole = teacher_whole(K, a.t.scale, sm.teach);
-        teacher = whole.y != 0.f;
+      if constexpr (LIST) {
+        // the listed logits of this part (every thread's units are there since the sums
+        // were joined); in a cluster each goes to the first CTA from the one that has it
         if (t < K) {
-          const float2 q = teacher_q(kid >= 0, e.y, a.t.scale, whole);
-          sm.q[t] = q.x;
-          sm.logq[t] = q.y;
-          sm.adds.add[t] = -up * c * a.t.w_kd * q.x;
+          const bool here = token >= x.lo && token < x.hi;
+          float z = 0.f;
+          if (here)
+            z = token < x.head    ? sm.list.loose[token]
+                : token >= x.tail ? sm.list.loose[x.head + token - x.tail]
+                                  : to_f<T>(reinterpret_cast<const T*>(seg)[token - x.head - x.u_lo * RowPart<T>::E]);
+          sm.list.kept.token[t] = token;
+          sm.list.kept.y[t] = entry.y;
+          sm.list.kept.z[t] = z;
+          sm.list.kept.claimed[t] = here ? claim(sm.list.table, token, &sm.list.twice) : -1;
+          if (CLUSTER && (here || (at.rank == 0 && token < 0)))
+            give(in_cta(smem_u32(&ex->z[t]), 0), z, in_cta(smem_u32(&ex->bar_z), 0));
         }
-        if (t == 0) sm.adds.add[K] = -up * c * a.t.w_ce;
-        __syncthreads();   // the listed logits are read before the next row comes in
+        if (CLUSTER && at.rank == 0 && t == 0) mbar_arrive_expect_tx(smem_u32(&ex->bar_z), 4 * K);
+        teacher = any_entry(K, sm.list.teach[live & 1]);
+        if (there) __syncthreads();   // the listed logits are read before the next row comes in
       }
     }
     const bool flat = id_now == -1 || st.l == -INFINITY;   // a zero gradient
     const float by_given = -up * c * a.t.w_ce;
     const Slope<false> slope(st.m, st.l, c2, up * c * (a.t.w_ce + (teacher ? a.t.w_kd : 0.f)), 0.f);
-    const bool adds_given = K == 0 && !flat && id_now >= 0 && a.t.w_ce != 0.f;
+    const bool adds_given = !flat && id_now >= 0 && a.t.w_ce != 0.f;
     if (j0 >= 0) out[j0] = from_f<T>(flat ? 0.f : slope.one(x0) + (adds_given && j0 == id_now ? by_given : 0.f));
     const int own = adds_given ? group_with<T, THREADS>(x, id_now) : -1;   // the group with the given token
     const uint4 *place = seg + t, *src = next.src + t;
@@ -1423,34 +1479,55 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
       left -= kGroup * THREADS;
       left_next -= kGroup * THREADS;
     }
-    if (id_now != -1 && K > 0) {
-      __syncthreads();   // the listed tokens' values go on top of what other threads wrote
-      if (!flat)
-        for_added<THREADS>(sm.adds, K + 1, [&](int k, int j, float sum) {
-          out[j] = from_f<T>(slope.one(sm.adds.z[k]) + sum);
-        });
-    }
-    if (at.rank == 0 && warp == 0) {
-      float loss = 0.f;
+    float kd = 0.f;
+    if constexpr (LIST) {
       if (id_now != -1) {
-        if (id_now >= 0 && a.t.w_ce != 0.f) loss = -a.t.w_ce * log_p(target, st, c);
-        if (K > 0) {
-          float kd = 0.f;
-          if (CLUSTER) wait_for(smem_u32(&ex.bar_z), live >> 1 & 1, a.wait);
-          const float* z = CLUSTER ? ex.z : sm.adds.z;
-          for (int k = lane; k < K; k += 32) {
-            const float q = sm.q[k];
-            if (q != 0.f) kd += q * (sm.logq[k] - log_p(z[k], st, c));
+        __syncthreads();   // the listed tokens' values go on top of what other threads wrote
+        const bool twice = sm.list.twice != 0;
+        int token = -1;
+        float add = 0.f, z = 0.f;
+        if (warp * 32 < K) {
+          const float2 whole = teacher_whole(K, a.t.scale, sm.list.teach[live & 1]);
+          if (CLUSTER && at.rank == 0) wait_for(smem_u32(&ex->bar_z), live >> 1 & 1, a.wait);
+          if (t < K) {
+            token = sm.list.kept.token[t];
+            z = sm.list.kept.z[t];
+            const float2 q = teacher_q(token >= 0, sm.list.kept.y[t], a.t.scale, whole);
+            add = -up * c * a.t.w_kd * q.x;
+            const bool here = token >= x.lo && token < x.hi;
+            if (here && !flat && !twice)
+              out[token] = from_f<T>(slope.one(z) + (add + (adds_given && token == id_now ? by_given : 0.f)));
+            if (sm.list.kept.claimed[t] >= 0) sm.list.table[sm.list.kept.claimed[t]] = -1;
+            if (q.x != 0.f) kd = q.x * (q.y - log_p(CLUSTER && at.rank == 0 ? ex->z[t] : z, st, c));
+            if (!here) token = -1;
           }
-          kd = lanes_sum<32>(kd);
-          if (teacher) loss += a.t.w_kd * kd;
+          if (at.rank == 0) {
+            kd = lanes_sum<32>(kd);
+            if (K > 32) {   // over the warps that have entries
+              if (lane == 0) sm.list.kd[warp] = kd;
+              asm volatile("bar.sync 1, %0;" ::"r"((K + 31) / 32 * 32) : "memory");
+              kd = 0.f;
+              for (int k = 0; 32 * k < K; ++k) kd += sm.list.kd[k];
+            }
+          }
+        }
+        if (twice) {
+          put_adds<THREADS>(sm.list.adds, K, token, add, z);
+          if (t == 0) sm.list.twice = 0;
+          if (!flat)
+            for_added<THREADS>(sm.list.adds, K, [&](int k, int j, float sum) {
+              out[j] = from_f<T>(slope.one(sm.list.adds.z[k]) + (sum + (adds_given && j == id_now ? by_given : 0.f)));
+            });
         }
       }
-      if (lane == 0) {
-        o.loss[p] = loss;
-        o.stats[2 * (int64_t)p] = st.m;
-        o.stats[2 * (int64_t)p + 1] = st.l;
-      }
+    }
+    if (t == 0 && at.rank == 0) {
+      float loss = 0.f;
+      if (id_now >= 0 && a.t.w_ce != 0.f) loss = -a.t.w_ce * log_p(target, st, c);
+      if (teacher) loss += a.t.w_kd * kd;
+      o.loss[p] = loss;
+      o.stats[2 * (int64_t)p] = st.m;
+      o.stats[2 * (int64_t)p + 1] = st.l;
     }
     if (id_now != -1) ++live;
   }
@@ -1475,7 +1552,7 @@ Rows rows_of(const tsp_logits& x, const void* ids, int id_bytes) {
 }
 Teacher teacher_of(const tsp_teacher* t, float w_ce) {
   Teacher k = {nullptr, nullptr, 0, 0, 1.f, w_ce, 0.f};
-  if (t) {
+  if (t && t->weight != 0.f) {   // (without weight it is not looked at)
     k.ids = t->ids;
     k.logits = t->logits;
     k.f32 = t->dtype == TSP_F32;
@@ -1559,6 +1636,14 @@ tsp_status launch_rows(const A& a, int S, int threads, int parts, size_t smem, i
 
 // Threads of a CTA for parts of `per` units and lists of n.
 int threads_for(int64_t per, int n) { return per <= 3 * kGroup * 128 && n <= 128 ? 128 : kMostThreads; }
+// CTAs a row of the forward where there are few: parts of 16 KB at least, as the cluster's
+// meeting has a price (8 x 50257 fp32: 5.7 us with eight, 8.8 with one; 8 x 32000 bf16 with
+// 20 alternatives: 11.8 and 9.3).
+int fwd_parts(int64_t S, int64_t units) {
+  int parts = 1;
+  while (units >= 8192 && parts <= 4 && S * parts * 4 <= num_sms() && units / (2 * parts) >= 1024) parts *= 2;
+  return parts;
+}
 // CTAs a row where there are few rows: until the GPU is full, of 4 KB at least.
 int parts_for(int64_t S, int64_t units, int parts) {
   while (parts <= 4 && S * parts * 2 <= num_sms() * 2 && units / (2 * parts) >= 256) parts *= 2;
@@ -1588,7 +1673,7 @@ tsp_status launch_fwd_c(const FwdArgs& a, const char* name, cudaStream_t st) {
 template <typename T>
 tsp_status launch_fwd_t(FwdArgs a, const char* name, cudaStream_t st) {
   const int64_t units = (int64_t)a.r.V * sizeof(T) / 16;
-  a.parts = parts_for(a.r.S, units, 1);
+  a.parts = fwd_parts(a.r.S, units);
   const bool ent = a.entropy != nullptr;
   if (a.parts > 1) return launch_fwd_c<T, true, true, true, 256>(a, name, st);
   if (a.top > 64) return launch_fwd_c<T, true, true, false, 256>(a, name, st);
@@ -1613,7 +1698,7 @@ bool alike(const GradArgs& a) {
          (a.r.S == 1 || (a.r.ld - a.ld_out) * (int64_t)sizeof(T) % 16 == 0);
 }
 
-template <typename T, bool ENT>
+template <typename T, bool ENT, bool LIST>
 tsp_status launch_grad_t(GradArgs a, const char* name, cudaStream_t st) {
   const int64_t units = (int64_t)a.r.V * sizeof(T) / 16;
   if (!alike<T>(a)) {
@@ -1627,14 +1712,16 @@ tsp_status launch_grad_t(GradArgs a, const char* name, cudaStream_t st) {
   const int threads = threads_for((units + a.parts - 1) / a.parts, a.t.K);
   const int64_t rows = rows_a_cta<T>(a.r.V, a.parts, a.t.K > 0);
   if (threads == 128)
-    return launch_rows<grad_kernel<T, ENT, 128>, false, kRingMost>(a, a.r.S, 128, a.parts, ring_bytes(128), rows, name, st);
-  return launch_rows<grad_kernel<T, ENT, 256>, false, kRingMost>(a, a.r.S, 256, a.parts, ring_bytes(256), rows, name, st);
+    return launch_rows<grad_kernel<T, ENT, LIST, 128>, false, kRingMost>(a, a.r.S, 128, a.parts, ring_bytes(128), rows, name, st);
+  return launch_rows<grad_kernel<T, ENT, LIST, 256>, false, kRingMost>(a, a.r.S, 256, a.parts, ring_bytes(256), rows, name, st);
+}
+template <typename T>
+tsp_status launch_grad_d(const GradArgs& a, const char* name, cudaStream_t st) {
+  if (a.up_entropy) return launch_grad_t<T, true, false>(a, name, st);
+  return a.t.K > 0 ? launch_grad_t<T, false, true>(a, name, st) : launch_grad_t<T, false, false>(a, name, st);
 }
 tsp_status launch_grad(const GradArgs& a, int dtype, const char* name, cudaStream_t st) {
-  const bool ent = a.up_entropy != nullptr;
-  if (dtype == TSP_BF16)
-    return ent ? launch_grad_t<__nv_bfloat16, true>(a, name, st) : launch_grad_t<__nv_bfloat16, false>(a, name, st);
-  return ent ? launch_grad_t<float, true>(a, name, st) : launch_grad_t<float, false>(a, name, st);
+  return dtype == TSP_BF16 ? launch_grad_d<__nv_bfloat16>(a, name, st) : launch_grad_d<float>(a, name, st);
 }
 
 // CTAs a row for the loss with its gradient: parts of four groups at most (64 KB: three
@@ -1649,7 +1736,7 @@ int one_pass_parts(int64_t S, int64_t units) {
   if (parts > 8) return part_bytes((units + 7) / 8, kMostThreads) <= kOnePassMost ? 8 : 0;
   return parts_for(S, units, (int)parts);
 }
-template <typename T, bool CLUSTER>
+template <typename T, bool LIST, bool CLUSTER>
 tsp_status launch_one_pass_c(const OnePassArgs& o, cudaStream_t st) {
   const int parts = o.g.parts;
   const int64_t per = ((int64_t)o.g.r.V * sizeof(T) / 16 + parts - 1) / parts;
@@ -1657,8 +1744,15 @@ tsp_status launch_one_pass_c(const OnePassArgs& o, cudaStream_t st) {
   const size_t smem = part_bytes(per, threads);
   const int64_t rows = CLUSTER ? o.g.r.S : rows_a_cta<T>(o.g.r.V, parts, o.g.t.K > 0);
   if (threads == 128)
-    return launch_rows<one_pass_kernel<T, CLUSTER, 128>, CLUSTER, kOnePassMost>(o, o.g.r.S, 128, parts, smem, rows, "token_loss_one_pass", st);
-  return launch_rows<one_pass_kernel<T, CLUSTER, 256>, CLUSTER, kOnePassMost>(o, o.g.r.S, 256, parts, smem, rows, "token_loss_one_pass", st);
+    return launch_rows<one_pass_kernel<T, LIST, CLUSTER, 128>, CLUSTER, kOnePassMost>(o, o.g.r.S, 128, parts, smem, rows, "token_loss_one_pass", st);
+  return launch_rows<one_pass_kernel<T, LIST, CLUSTER, 256>, CLUSTER, kOnePassMost>(o, o.g.r.S, 256, parts, smem, rows, "token_loss_one_pass", st);
+}
+
+template <typename T>
+tsp_status launch_one_pass(const OnePassArgs& o, cudaStream_t st) {
+  if (o.g.t.K > 0)
+    return o.g.parts > 1 ? launch_one_pass_c<T, true, true>(o, st) : launch_one_pass_c<T, true, false>(o, st);
+  return o.g.parts > 1 ? launch_one_pass_c<T, false, true>(o, st) : launch_one_pass_c<T, false, false>(o, st);
 }
 
 }  // namespace
@@ -1725,10 +1819,7 @@ tsp_status launch_token_loss_fwd(const tsp_logits& x, const void* ids, int id_by
     const bool bf = x.dtype == TSP_BF16;
     o.g.parts = one_pass_parts(x.S, x.V * (bf ? 2 : 4) / 16);
     if (o.g.parts > 0 && (bf ? alike<__nv_bfloat16>(o.g) : alike<float>(o.g))) {
-      if (bf)
-        return o.g.parts > 1 ? launch_one_pass_c<__nv_bfloat16, true>(o, st)
-                             : launch_one_pass_c<__nv_bfloat16, false>(o, st);
-      return o.g.parts > 1 ? launch_one_pass_c<float, true>(o, st) : launch_one_pass_c<float, false>(o, st);
+      return bf ? launch_one_pass<__nv_bfloat16>(o, st) : launch_one_pass<float>(o, st);
     }
   }
   FwdArgs a = {};
