@@ -125,19 +125,24 @@ __device__ __forceinline__ int given(const Rows& a, int row) {
   return id >= 0 && id < a.V ? (int)id : -1;
 }
 
-// A row as 16-byte units: `head` elements in front of the first, `units` of them,
-// and the elements from `tail` on behind the last.  A part of it (one of `parts`) has
-// the n units from u_lo on and the elements [lo, hi).
-template <typename T>
+// A row as 16-byte units: `head` elements in front of the first, which starts a line,
+// `units` of them, and the elements from `tail` on behind the last.  A part of it (one of
+// `parts`) has the n units from u_lo on and the elements [lo, hi).  Copies that keep to the
+// lines of both memories are quicker (shared memory off by 48 bytes: 4096 x 128000 bf16, 371
+// us and not 325).
+template <typename T, int THREADS>
 struct RowPart {
   static constexpr int E = 16 / sizeof(T);
+  // bytes of a line; each element outside the units has a thread
+  static constexpr int kLine = THREADS >= 128 ? 128 : 64, kLoose = kLine / sizeof(T) - 1 + E - 1;
+  static_assert(kLoose <= THREADS, "");
   const T* row;
   const uint4* src;
   int head, units, tail, V, u_lo, n, lo, hi;
   __device__ __forceinline__ RowPart(const Rows& a, int r, int rank, int parts) {
     row = reinterpret_cast<const T*>(a.logits) + (int64_t)r * a.ld;
     V = a.V;
-    head = min(V, (int)((16 - ((uintptr_t)row & 15)) & 15) / (int)sizeof(T));
+    head = min(V, (int)((kLine - ((uintptr_t)row & (kLine - 1))) & (kLine - 1)) / (int)sizeof(T));
     units = (V - head) / E;
     tail = head + units * E;
     const int per = parts == 1 ? units : (int)((unsigned)(units + parts - 1) / (unsigned)parts);
@@ -150,7 +155,7 @@ struct RowPart {
   // the k-th element outside the units if it is this part's, else -1
   __device__ __forceinline__ int loose(int k) const {
     const int j = k < head ? k : tail + k - head;
-    return k < 2 * E && j >= lo && j < hi ? j : -1;
+    return k < kLoose && j >= lo && j < hi ? j : -1;
   }
 };
 
@@ -212,9 +217,9 @@ __device__ __forceinline__ void copies_left(int n) {
   }
 }
 // Sends for kGroup units of a thread, THREADS apart from src and place on; of those past
-// `left`, counted from src, the places get -inf.  One commit.
+// `left`, counted from src, the places get -inf with `fill`.  One commit.
 template <typename T, int THREADS>
-__device__ __forceinline__ void send_units(uint32_t place, const uint4* src, int left) {
+__device__ __forceinline__ void send_units(uint32_t place, const uint4* src, int left, bool fill) {
   if (left > (kGroup - 1) * THREADS) {
 #pragma unroll
     for (int k = 0; k < kGroup; ++k)
@@ -227,7 +232,7 @@ __device__ __forceinline__ void send_units(uint32_t place, const uint4* src, int
       if (left > k * THREADS)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(place + 16 * k * THREADS), "l"(src + k * THREADS)
                      : "memory");
-      else
+      else if (fill)
         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(place + 16 * k * THREADS), "r"(none.x),
                      "r"(none.y), "r"(none.z), "r"(none.w)
                      : "memory");
@@ -336,10 +341,10 @@ struct Sums {
         const uint4 w = make_uint4(not_below(v[k].x, floor), not_below(v[k].y, floor), not_below(v[k].z, floor),
                                    not_below(v[k].w, floor));
 #pragma unroll
-        for (int e = 0; e < RowPart<T>::E / 2; ++e) add<true>(pair<T>(w, e));
+        for (int e = 0; e < (16 / (int)sizeof(T)) / 2; ++e) add<true>(pair<T>(w, e));
       } else {
 #pragma unroll
-        for (int e = 0; e < RowPart<T>::E / 2; ++e) add<false>(pair<T>(v[k], e));
+        for (int e = 0; e < (16 / (int)sizeof(T)) / 2; ++e) add<false>(pair<T>(v[k], e));
       }
     }
     return b;
@@ -403,7 +408,7 @@ __device__ __noinline__ float2 far_sums(const uint4* src, int n, float loose, fl
   float s = ex2_approx((loose - m) * c2), a = s * fmaxf((loose - m) * c2, kLeast);
   for (int i = threadIdx.x; i < n; i += THREADS) {
     const uint4 v = src[i];
-    for (int e = 0; e < RowPart<T>::E / 2; ++e) {
+    for (int e = 0; e < (16 / (int)sizeof(T)) / 2; ++e) {
       const float2 x = both(pair<T>(v, e));
       const float u = (x.x - m) * c2, w = (x.y - m) * c2;
       s += ex2_approx(u) + ex2_approx(w);
@@ -668,7 +673,7 @@ struct Place {
 // Groups of a part at most.
 template <typename T, int THREADS>
 __device__ __forceinline__ int groups_of(int V, int parts) {
-  const int units = V / RowPart<T>::E, per = parts == 1 ? units : (units + parts - 1) / parts;
+  const int units = V / (16 / (int)sizeof(T)), per = parts == 1 ? units : (units + parts - 1) / parts;
   return max(1, (per + kGroup * THREADS - 1) / (kGroup * THREADS));
 }
 
@@ -708,14 +713,14 @@ struct Sender {
         if (row < a.S) ahead = given(a, row + at.stride);
       } while (row < a.S && id == -1);
       if (row < a.S) {
-        const RowPart<T> x(a, row, at.rank, at.parts);
+        const RowPart<T, THREADS> x(a, row, at.rank, at.parts);
         src = x.src + threadIdx.x;
         left = x.n - (int)threadIdx.x;
         g = groups;
       }
     }
     if (g > 0) {
-      send_units<T, THREADS>(to + slot * (16 * kGroup * THREADS), src, left);
+      send_units<T, THREADS>(to + slot * (16 * kGroup * THREADS), src, left, true);
       src += kGroup * THREADS;
       left -= kGroup * THREADS;
       --g;
@@ -821,7 +826,7 @@ __device__ __forceinline__ void for_ranked(const uint64_t* key, int n, F put) {
 // that reach it once more, out of L2: about as many slots as there are alternatives.
 // A slot is 2^shift groups of a thread.
 template <typename T, int THREADS>
-__device__ __noinline__ int candidates(const RowPart<T>& x, int top, float mine, int groups, int shift,
+__device__ __noinline__ int candidates(const RowPart<T, THREADS>& x, int top, float mine, int groups, int shift,
                                        const uint16_t* slot, TopSmem<THREADS>& sm) {
   const int t = threadIdx.x;
   sm.best[t] = (uint16_t)(order_of(mine) >> 16);
@@ -855,19 +860,19 @@ __device__ __noinline__ int candidates(const RowPart<T>& x, int top, float mine,
     // the elements of a unit that reach it, a bit each
     const float least = logit_of(bound);
     auto element = [&](const uint4& v, int e) {
-      T el[RowPart<T>::E], y;
+      T el[(16 / (int)sizeof(T))], y;
       memcpy(el, &v, 16);
       y = el[0];
 #pragma unroll
-      for (int q = 1; q < RowPart<T>::E; ++q)
+      for (int q = 1; q < (16 / (int)sizeof(T)); ++q)
         if (q == e) y = el[q];
       return to_f<T>(y);
     };
-    auto token = [&](int u, int e) { return x.head + (x.u_lo + u) * RowPart<T>::E + e; };
+    auto token = [&](int u, int e) { return x.head + (x.u_lo + u) * (16 / (int)sizeof(T)) + e; };
     auto reaching = [&](const uint4& v, int u) {
       uint32_t r = 0;
 #pragma unroll
-      for (int e = 0; e < RowPart<T>::E / 2; ++e) {
+      for (int e = 0; e < (16 / (int)sizeof(T)) / 2; ++e) {
         const float2 y = both(pair<T>(v, e));
         r |= (y.x >= least) << (2 * e) | (y.y >= least) << (2 * e + 1);
       }
@@ -884,7 +889,7 @@ __device__ __noinline__ int candidates(const RowPart<T>& x, int top, float mine,
     auto keep_unit = [&](const uint4& v, int u, uint32_t r, int& place) {
       for (; r; r &= r - 1, ++place) keep(key_of(element(v, __ffs(r) - 1), token(u, __ffs(r) - 1)), place);
     };
-    if (t < 32) {   // the elements outside the units (RowPart::loose: of the first lanes)
+    if (t < (RowPart<T, THREADS>::kLoose + 31) / 32 * 32) {   // the elements outside the units (whole warps)
       const int j = x.loose(t);
       const uint64_t key = j >= 0 ? key_of(to_f<T>(x.row[j]), j) : 0;
       const int place = places(key >= above ? 1 : 0, &sm.n);
@@ -946,7 +951,7 @@ __device__ __noinline__ int candidates(const RowPart<T>& x, int top, float mine,
 
 template <typename T, bool ENT, bool TOP, bool CLUSTER, int THREADS>
 __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __grid_constant__ FwdArgs a) {
-  extern __shared__ uint4 ring[];
+  extern __shared__ __align__(128) uint4 ring[];
   __shared__ struct {
     float4 part[2][THREADS / 32];
     float2 teach[THREADS / 32];
@@ -989,7 +994,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
       }
       continue;
     }
-    const RowPart<T> x(a.r, r, at.rank, at.parts);
+    const RowPart<T, THREADS> x(a.r, r, at.rank, at.parts);
     const int j0 = x.loose(t);
     const float x0 = j0 >= 0 ? to_f<T>(x.row[j0]) : -INFINITY;
     float target = 0.f, z = 0.f;
@@ -1138,17 +1143,17 @@ __device__ __forceinline__ Factors factors(const GradArgs& a, const Upstream& u,
 }
 // The group of a thread's that has the token, if it is one of the thread's units.
 template <typename T, int THREADS>
-__device__ __forceinline__ int group_with(const RowPart<T>& x, int id) {
-  const int u = (id - x.head) / RowPart<T>::E - x.u_lo;
+__device__ __forceinline__ int group_with(const RowPart<T, THREADS>& x, int id) {
+  const int u = (id - x.head) / (16 / (int)sizeof(T)) - x.u_lo;
   return id >= x.head && id < x.tail && u >= 0 && u < x.n && u % THREADS == (int)threadIdx.x
              ? u / (kGroup * THREADS)
              : -1;
 }
 // Its logit, in a group that lies at `place` in shared memory.
 template <typename T, int THREADS>
-__device__ __forceinline__ float logit_in(const uint4* place, const RowPart<T>& x, int id) {
-  const int u = ((id - x.head) / RowPart<T>::E - x.u_lo) % (kGroup * THREADS);
-  return to_f<T>(reinterpret_cast<const T*>(place + u)[(id - x.head) % RowPart<T>::E]);
+__device__ __forceinline__ float logit_in(const uint4* place, const RowPart<T, THREADS>& x, int id) {
+  const int u = ((id - x.head) / (16 / (int)sizeof(T)) - x.u_lo) % (kGroup * THREADS);
+  return to_f<T>(reinterpret_cast<const T*>(place + u)[(id - x.head) % (16 / (int)sizeof(T))]);
 }
 
 // The given token's value is written by the thread that has its unit, so that a row
@@ -1156,7 +1161,7 @@ __device__ __forceinline__ float logit_in(const uint4* place, const RowPart<T>& 
 // at the end, each by the thread that has the entry.
 template <typename T, bool ENT, bool LIST, int THREADS>   // LIST: with a teacher
 __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __grid_constant__ GradArgs a) {
-  extern __shared__ uint4 ring[];
+  extern __shared__ __align__(128) uint4 ring[];
   struct Shared {
     float2 teach[2][THREADS / 32];   // (of two rows by turns)
     int table[2][kTable], twice[2];
@@ -1191,7 +1196,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __gr
     id = given(a.r, r + at.stride);
     up = upstream<ENT>(a, r + at.stride);
     if (LIST && t < K && r + at.stride < a.r.S) e = load_entry(a.t, pos_of(a.r, r + at.stride), t);
-    const RowPart<T> x(a.r, r, at.rank, at.parts);
+    const RowPart<T, THREADS> x(a.r, r, at.rank, at.parts);
     T* out = reinterpret_cast<T*>(a.out) + (int64_t)r * a.ld_out;
     uint4* dst = reinterpret_cast<uint4*>(out + x.head) + x.u_lo + t;
     const int j0 = x.loose(t);
@@ -1347,11 +1352,12 @@ __global__ void __launch_bounds__(kMostThreads) grad_elements_kernel(const __gri
 struct OnePassArgs {
   GradArgs g;
   float *loss, *stats;
+  bool fill;   // there is room for whole groups: what lies past a part is -inf
 };
 
 template <typename T, bool LIST, bool CLUSTER, int THREADS>   // LIST: with a teacher
 __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const __grid_constant__ OnePassArgs o) {
-  extern __shared__ uint4 seg[];
+  extern __shared__ __align__(128) uint4 seg[];
   struct Listed {
     float2 teach[2][THREADS / 32];
     int table[kTable], twice;
@@ -1359,7 +1365,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
       Kept kept;
       Adds adds;   // (once kept has been read)
     };
-    float kd[THREADS / 32], loose[16];
+    float kd[THREADS / 32], loose[RowPart<T, THREADS>::kLoose];
   };
   __shared__ struct {
     float4 part[2][THREADS / 32];
@@ -1387,13 +1393,13 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
     const int p = pos_of(a.r, r), id_now = id;
     if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
     id = given(a.r, r + at.stride);
-    const RowPart<T> x(a.r, r, at.rank, at.parts);
+    const RowPart<T, THREADS> x(a.r, r, at.rank, at.parts);
     T* out = reinterpret_cast<T*>(a.out) + (int64_t)r * a.ld_out;
     uint4* dst = reinterpret_cast<uint4*>(out + x.head) + x.u_lo + t;
     const int j0 = x.loose(t);
     const bool sent = there;
     there = r + at.stride < a.r.S && id != -1;
-    RowPart<T> next(a.r, there ? r + at.stride : r, at.rank, at.parts);
+    RowPart<T, THREADS> next(a.r, there ? r + at.stride : r, at.rank, at.parts);
     Exchange* ex = nullptr;
     if constexpr (CLUSTER) ex = &sm.ex[live & 1];
     Stats st = {0.f, -INFINITY, 0.f};
@@ -1405,17 +1411,23 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
       if (!sent)
         for (int g = 0; g < groups; ++g)
           send_units<T, THREADS>(to + 16 * kGroup * THREADS * g, x.src + t + kGroup * THREADS * g,
-                                 x.n - t - kGroup * THREADS * g);
+                                 x.n - t - kGroup * THREADS * g, o.fill);
       if (j0 >= 0) x0 = to_f<T>(x.row[j0]);
       if (t == 0 && id_now >= 0) target = to_f<T>(x.row[id_now]);
       if (a.up) up = a.up[p];
       Sums<T, false> sums(c2);
       for (int g = 0; g < groups; ++g) {
         copies_left(groups - 1 - g);
-        uint4 v[kGroup];
         const uint4* from = seg + t + kGroup * g * THREADS;
+        const int left = x.n - t - kGroup * g * THREADS;
+        uint4 v[kGroup];
+        if (o.fill || left > (kGroup - 1) * THREADS) {
 #pragma unroll
-        for (int k = 0; k < kGroup; ++k) v[k] = from[k * THREADS];
+          for (int k = 0; k < kGroup; ++k) v[k] = from[k * THREADS];
+        } else {
+#pragma unroll
+          for (int k = 0; k < kGroup; ++k) v[k] = left > k * THREADS ? from[k * THREADS] : no_unit<T>();
+        }
         sums.template add_units<kGroup>(v);
       }
       sums.add_one(x0);
@@ -1436,7 +1448,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
           if (here)
             z = token < x.head    ? sm.list.loose[token]
                 : token >= x.tail ? sm.list.loose[x.head + token - x.tail]
-                                  : to_f<T>(reinterpret_cast<const T*>(seg)[token - x.head - x.u_lo * RowPart<T>::E]);
+                                  : to_f<T>(reinterpret_cast<const T*>(seg)[token - x.head - x.u_lo * (16 / (int)sizeof(T))]);
           sm.list.kept.token[t] = token;
           sm.list.kept.y[t] = entry.y;
           sm.list.kept.z[t] = z;
@@ -1463,15 +1475,18 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
         for (int k = 0; k < kGroup; ++k)
           if (left > k * THREADS)
             __stcs(dst + k * THREADS, flat ? make_uint4(0, 0, 0, 0) : far_grad<T, false>(place[k * THREADS], slope));
-      } else {
+      } else if (o.fill || left > (kGroup - 1) * THREADS) {
 #pragma unroll
         for (int k = 0; k < kGroup; ++k) {
           const uint4 v = unit_grad<T, false>(place[k * THREADS], slope);
           if (left > k * THREADS) __stcs(dst + k * THREADS, v);
         }
+      } else {
+        for (int k = 0; k < kGroup; ++k)
+          if (left > k * THREADS) __stcs(dst + k * THREADS, unit_grad<T, false>(place[k * THREADS], slope));
       }
       if (g == own) out[id_now] = from_f<T>(slope.one(logit_in<T, THREADS>(place - t, x, id_now)) + by_given);
-      if (there) send_units<T, THREADS>(from, src, left_next);
+      if (there) send_units<T, THREADS>(from, src, left_next, o.fill);
       place += kGroup * THREADS;
       src += kGroup * THREADS;
       dst += kGroup * THREADS;
@@ -1724,25 +1739,32 @@ tsp_status launch_grad(const GradArgs& a, int dtype, const char* name, cudaStrea
   return dtype == TSP_BF16 ? launch_grad_d<__nv_bfloat16>(a, name, st) : launch_grad_d<float>(a, name, st);
 }
 
-// CTAs a row for the loss with its gradient: parts of four groups at most (64 KB: three
-// CTAs a multiprocessor), longer ones in clusters of eight.  0: the row is too long.
-constexpr int kOnePassUnits = 4 * kGroup * kMostThreads;
-size_t part_bytes(int64_t per, int threads) {
-  const int64_t group = kGroup * threads;
-  return (size_t)std::max<int64_t>(1, (per + group - 1) / group) * group * 16;
+// CTAs a row for the loss with its gradient: one or two up to 104 KB each (two CTAs a
+// multiprocessor; 4096 x 40000 bf16: 104 us, 123 in two parts; 4096 x 50257 fp32: 252 us in
+// two, 272 in four), for longer rows parts of 68 KB at most (three a multiprocessor; 4096 x
+// 128000 bf16: 316 us in four, 384 in three of 84 KB), the longest in clusters of eight.
+// 0: the row is too long.
+constexpr int kOnePassAlone = 26 * kMostThreads, kOnePassUnits = 17 * kMostThreads;
+// Bytes of a part of `per` units, in multiples of `rows` for each thread.
+size_t part_bytes(int64_t per, int threads, int rows) {
+  const int64_t n = (int64_t)threads * rows;
+  return (size_t)std::max<int64_t>(1, (per + n - 1) / n) * n * 16;
 }
 int one_pass_parts(int64_t S, int64_t units) {
-  const int64_t parts = std::max<int64_t>(1, (units + kOnePassUnits - 1) / kOnePassUnits);
-  if (parts > 8) return part_bytes((units + 7) / 8, kMostThreads) <= kOnePassMost ? 8 : 0;
+  int64_t parts = (units + kOnePassUnits - 1) / kOnePassUnits;
+  if (units <= 2 * kOnePassAlone) parts = std::max<int64_t>(1, (units + kOnePassAlone - 1) / kOnePassAlone);
+  if (parts > 8) return part_bytes((units + 7) / 8, kMostThreads, 1) <= kOnePassMost ? 8 : 0;
   return parts_for(S, units, (int)parts);
 }
 template <typename T, bool LIST, bool CLUSTER>
-tsp_status launch_one_pass_c(const OnePassArgs& o, cudaStream_t st) {
+tsp_status launch_one_pass_c(OnePassArgs o, cudaStream_t st) {
   const int parts = o.g.parts;
   const int64_t per = ((int64_t)o.g.r.V * sizeof(T) / 16 + parts - 1) / parts;
   const int threads = threads_for(per, o.g.t.K);
-  const size_t smem = part_bytes(per, threads);
-  const int64_t rows = CLUSTER ? o.g.r.S : rows_a_cta<T>(o.g.r.V, parts, o.g.t.K > 0);
+  // whole groups up to three CTAs' share of a multiprocessor (quicker: no case is apart)
+  o.fill = per <= 16 * kMostThreads;
+  const size_t smem = part_bytes(per, threads, o.fill ? kGroup : 1);
+  const int64_t rows = CLUSTER ? 4 : rows_a_cta<T>(o.g.r.V, parts, o.g.t.K > 0);
   if (threads == 128)
     return launch_rows<one_pass_kernel<T, LIST, CLUSTER, 128>, CLUSTER, kOnePassMost>(o, o.g.r.S, 128, parts, smem, rows, "token_loss_one_pass", st);
   return launch_rows<one_pass_kernel<T, LIST, CLUSTER, 256>, CLUSTER, kOnePassMost>(o, o.g.r.S, 256, parts, smem, rows, "token_loss_one_pass", st);
