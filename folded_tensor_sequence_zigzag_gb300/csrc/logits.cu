@@ -760,13 +760,13 @@ constexpr uint32_t kOrderNone = 0x007fffffu;   // order_of(-inf)
 
 // Where alternatives are wanted, a thread leaves the upper half of the order of the largest
 // logit of each of up to kSlots runs of its groups, behind the ring.
-constexpr int kSlots = 32, kListed = 512;
+constexpr int kSlots = 32, kListed = 128;
 template <int THREADS> struct TopSmem {
   static constexpr int kCandidates = 4 * THREADS;
   uint64_t key[kCandidates], above;
   alignas(16) uint16_t best[THREADS];   // largest logit of each thread, the upper half of its order
-  uint16_t listed[kListed];             // slots to be looked at once more
-  int n, n_listed;
+  uint16_t listed[THREADS / 32][kListed];   // of each warp: slots to be looked at once more
+  int n;
 };
 // The first of `count` places of the calling lane's out of a counter; the whole warp calls.
 __device__ __forceinline__ int places(int count, int* counter) {
@@ -826,11 +826,11 @@ __device__ __forceinline__ void for_ranked(const uint64_t* key, int n, F put) {
 // that reach it once more, out of L2: about as many slots as there are alternatives.
 // A slot is 2^shift groups of a thread.
 template <typename T, int THREADS>
-__device__ __noinline__ int candidates(const RowPart<T, THREADS>& x, int top, float mine, int groups, int shift,
-                                       const uint16_t* slot, TopSmem<THREADS>& sm) {
-  const int t = threadIdx.x;
+__device__ __noinline__ int candidates(const RowPart<T, THREADS>& x, int top, float mine, float loose, int groups,
+                                       int shift, const uint16_t* slot, TopSmem<THREADS>& sm) {
+  const int t = threadIdx.x, lane = t & 31;
   sm.best[t] = (uint16_t)(order_of(mine) >> 16);
-  if (t == 0) sm.n = sm.n_listed = 0;
+  if (t == 0) sm.n = 0;
   __syncthreads();
   // the largest 16 bits that `top` threads reach, bit by bit, in every warp
   constexpr int OWN = THREADS / 32;
@@ -850,23 +850,26 @@ __device__ __noinline__ int candidates(const RowPart<T, THREADS>& x, int top, fl
   static_assert(kGroup == 4, "log_per");
   for (;;) {
     const uint32_t bound = (uint32_t)(above >> 32);
-    // the slots of this thread that reach the bound, a bit each
+    // the slots of this warp that reach the bound
     uint32_t mask = 0;
-    if (order_of(mine) >= bound)
+    if (order_of(mine) >= bound) {
+#pragma unroll 8
       for (int s = 0; s < slots; ++s) mask |= (slot[s * THREADS + t] >= bound >> 16) << s;
-    int at = places(__popc(mask), &sm.n_listed);
-    for (uint32_t m = mask; m; m &= m - 1, ++at)
-      if (at < kListed) sm.listed[at] = (uint16_t)((__ffs(m) - 1) * THREADS + t);
+    }
+    uint16_t* list = sm.listed[t >> 5];
+    int listed = 0;
+    for (uint32_t m = mask, any; (any = __ballot_sync(0xffffffffu, m != 0)) != 0; m &= m - 1) {
+      const int place = listed + __popc(any & ((1u << lane) - 1));
+      if (m != 0 && place < kListed) list[place] = (uint16_t)((__ffs(m) - 1) * THREADS + t);
+      listed += __popc(any);
+    }
+    __syncwarp();
     // the elements of a unit that reach it, a bit each
     const float least = logit_of(bound);
     auto element = [&](const uint4& v, int e) {
-      T el[(16 / (int)sizeof(T))], y;
-      memcpy(el, &v, 16);
-      y = el[0];
-#pragma unroll
-      for (int q = 1; q < (16 / (int)sizeof(T)); ++q)
-        if (q == e) y = el[q];
-      return to_f<T>(y);
+      const int k = sizeof(T) == 2 ? e >> 1 : e;
+      const uint32_t w = k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
+      return sizeof(T) == 2 ? __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16) : __uint_as_float(w);
     };
     auto token = [&](int u, int e) { return x.head + (x.u_lo + u) * (16 / (int)sizeof(T)) + e; };
     auto reaching = [&](const uint4& v, int u) {
@@ -889,25 +892,23 @@ __device__ __noinline__ int candidates(const RowPart<T, THREADS>& x, int top, fl
     auto keep_unit = [&](const uint4& v, int u, uint32_t r, int& place) {
       for (; r; r &= r - 1, ++place) keep(key_of(element(v, __ffs(r) - 1), token(u, __ffs(r) - 1)), place);
     };
-    if (t < (RowPart<T, THREADS>::kLoose + 31) / 32 * 32) {   // the elements outside the units (whole warps)
-      const int j = x.loose(t);
-      const uint64_t key = j >= 0 ? key_of(to_f<T>(x.row[j]), j) : 0;
+    if (x.units * (16 / (int)sizeof(T)) != x.V && t < (RowPart<T, THREADS>::kLoose + 31) / 32 * 32) {
+      const int j = x.loose(t);   // the elements outside the units (whole warps)
+      const uint64_t key = j >= 0 ? key_of(loose, j) : 0;
       const int place = places(key >= above ? 1 : 0, &sm.n);
       if (key >= above) keep(key, place);
     }
-    __syncthreads();
-    const int listed = sm.n_listed;
     if (listed <= kListed) {
       constexpr int U = 2;   // loads on their way
-      for (int w0 = t; w0 - (t & 31) < listed << log_per; w0 += U * THREADS) {   // (whole warps)
+      for (int w0 = lane; w0 - lane < listed << log_per; w0 += U * 32) {   // (all lanes)
         uint4 v[U];
         int u[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-          const int w = w0 + k * THREADS;
+          const int w = w0 + k * 32;
           u[k] = x.n;
           if (w < listed << log_per) {
-            const int which = sm.listed[w >> log_per];
+            const int which = list[w >> log_per];
             u[k] = (((which / THREADS) << log_per) + (w & ((1 << log_per) - 1))) * THREADS + which % THREADS;
           }
           v[k] = u[k] < x.n ? x.src[u[k]] : no_unit<T>();
@@ -943,7 +944,7 @@ __device__ __noinline__ int candidates(const RowPart<T, THREADS>& x, int top, fl
     __syncthreads();
     for (int k = t; k < TopSmem<THREADS>::kCandidates; k += THREADS)
       if (rank_in(sm.key, TopSmem<THREADS>::kCandidates, sm.key[k]) == top - 1) sm.above = sm.key[k];
-    if (t == 0) sm.n = sm.n_listed = 0;
+    if (t == 0) sm.n = 0;
     __syncthreads();
     above = sm.above;
   }
@@ -1065,7 +1066,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
         a.top_logp[to + rank] = log_p(logit_of((uint32_t)(key >> 32)), st, c);
       };
       if (a.top > 0 && !isnan(st.l)) {
-        n = candidates<T, THREADS>(x, a.top, mine, groups, shift, slot, sm.top);
+        n = candidates<T, THREADS>(x, a.top, mine, x0, groups, shift, slot, sm.top);
         if constexpr (!CLUSTER) {
           for_ranked<THREADS>(sm.top.key, n, put);
         } else {
