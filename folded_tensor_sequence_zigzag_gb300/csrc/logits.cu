@@ -832,20 +832,34 @@ __device__ __noinline__ int candidates(const RowPart<T, THREADS>& x, int top, fl
   sm.best[t] = (uint16_t)(order_of(mine) >> 16);
   if (t == 0) sm.n = 0;
   __syncthreads();
-  // the largest 16 bits that `top` threads reach, bit by bit, in every warp
-  constexpr int OWN = THREADS / 32;
-  uint16_t own[OWN];
-  memcpy(own, sm.best + OWN * (t & 31), sizeof(own));
-  uint32_t reached = 0;
+  // the largest 16 bits that `top` threads reach, bit by bit from the first one in which the
+  // threads differ
+  if (t < 32) {
+    constexpr int OWN = THREADS / 32;
+    uint16_t own[OWN];
+    memcpy(own, sm.best + OWN * t, sizeof(own));
+    uint32_t low = 0xffffu, high = 0;
 #pragma unroll
-  for (int bit = 15; bit >= 0; --bit) {
-    const uint32_t v = reached | 1u << bit;
-    int n = 0;
+    for (int k = 0; k < OWN; ++k) {
+      low = min(low, (uint32_t)own[k]);
+      high = max(high, (uint32_t)own[k]);
+    }
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
+    const int same = 32 - __clz(low ^ high);
+    uint32_t reached = high >> same << same;
+    for (int bit = same - 1; bit >= 0; --bit) {
+      const uint32_t v = reached | 1u << bit;
+      int n = 0;
 #pragma unroll
-    for (int k = 0; k < OWN; ++k) n += own[k] >= v;
-    if (__reduce_add_sync(0xffffffffu, n) >= top) reached = v;
+      for (int k = 0; k < OWN; ++k) n += own[k] >= v;
+      if (__reduce_add_sync(0xffffffffu, n) >= top) reached = v;
+    }
+    if (top > THREADS) reached = 0;   // (as many threads there are not)
+    if (t == 0) sm.above = (uint64_t)max(reached << 16, kOrderNone + 1) << 32;
   }
-  uint64_t above = (uint64_t)max(reached << 16, kOrderNone + 1) << 32;
+  __syncthreads();
+  uint64_t above = sm.above;
   const int slots = (groups + (1 << shift) - 1) >> shift, log_per = 2 + shift;   // units of a slot
   static_assert(kGroup == 4, "log_per");
   for (;;) {
