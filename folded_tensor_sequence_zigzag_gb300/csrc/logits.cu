@@ -18,9 +18,11 @@
 //
 // A row starts at any element: it is taken as 16-byte units, the few elements in
 // front of the first and behind the last one are read by themselves.  A CTA, or a
-// cluster whose CTAs hold a part each, takes one row after the other; a thread copies
-// the units that it will itself read ahead into shared memory, so that the data need
-// no barrier and reading goes on while the sums of a row are joined.
+// cluster whose CTAs hold a part each, takes a few rows one after the other; a thread
+// copies the units that it will itself read ahead into shared memory, so that the data
+// need no barrier and reading goes on while the sums of a row are joined.  What lies
+// between two rows (joining, search, lists) is what the kernels lose against the copy
+// rate: several small CTAs a multiprocessor take turns at it.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -44,8 +46,9 @@ constexpr float kSlack = 8.f;
 // are added up once more as 2^(c2 (x - m)).
 constexpr float kFar = 0x1p24f;
 
-constexpr int kMostThreads = 256;   // of a CTA; 128 for short rows
+constexpr int kMostThreads = 256;   // of a CTA
 constexpr int kGroup = 4;           // units of a thread that are sent for and worked on together
+template <typename T> constexpr int kElems = 16 / sizeof(T);   // of a unit
 
 // ---------------------------------------------------------------------------
 // Two values an instruction
@@ -132,10 +135,9 @@ __device__ __forceinline__ int given(const Rows& a, int row) {
 // us and not 325).
 template <typename T, int THREADS>
 struct RowPart {
-  static constexpr int E = 16 / sizeof(T);
   // bytes of a line; each element outside the units has a thread
-  static constexpr int kLine = THREADS >= 128 ? 128 : 64, kLoose = kLine / sizeof(T) - 1 + E - 1;
-  static_assert(kLoose <= THREADS, "");
+  static constexpr int kLine = THREADS >= 128 ? 128 : 64, kLoose = kLine / sizeof(T) - 1 + kElems<T> - 1;
+  static_assert(kLoose <= THREADS, "a thread for each element outside the units");
   const T* row;
   const uint4* src;
   int head, units, tail, V, u_lo, n, lo, hi;
@@ -143,13 +145,13 @@ struct RowPart {
     row = reinterpret_cast<const T*>(a.logits) + (int64_t)r * a.ld;
     V = a.V;
     head = min(V, (int)((kLine - ((uintptr_t)row & (kLine - 1))) & (kLine - 1)) / (int)sizeof(T));
-    units = (V - head) / E;
-    tail = head + units * E;
+    units = (V - head) / kElems<T>;
+    tail = head + units * kElems<T>;
     const int per = parts == 1 ? units : (int)((unsigned)(units + parts - 1) / (unsigned)parts);
     u_lo = min(units, rank * per);
     n = min(units, u_lo + per) - u_lo;
-    lo = rank == 0 ? 0 : head + u_lo * E;
-    hi = rank == parts - 1 ? V : head + (u_lo + n) * E;
+    lo = rank == 0 ? 0 : head + u_lo * kElems<T>;
+    hi = rank == parts - 1 ? V : head + (u_lo + n) * kElems<T>;
     src = reinterpret_cast<const uint4*>(row + head) + u_lo;
   }
   // the k-th element outside the units if it is this part's, else -1
@@ -246,7 +248,7 @@ __device__ __forceinline__ void send_units(uint32_t place, const uint4* src, int
 // ---------------------------------------------------------------------------
 // Values go by st.async, which counts their bytes on a barrier of the CTA that they
 // are for.  (A cluster barrier for each row would first wait for the gradients that the
-// CTA has on their way to memory: 4096 x 128000 bf16, 372 us with one.)
+// CTA has on their way to memory: 4096 x 128000 bf16, 372 us with one and 334 without.)
 struct Wait {   // limits of a wait, and where it says that it gave up
   int* status;
   uint64_t limit_ns;
@@ -341,10 +343,10 @@ struct Sums {
         const uint4 w = make_uint4(not_below(v[k].x, floor), not_below(v[k].y, floor), not_below(v[k].z, floor),
                                    not_below(v[k].w, floor));
 #pragma unroll
-        for (int e = 0; e < (16 / (int)sizeof(T)) / 2; ++e) add<true>(pair<T>(w, e));
+        for (int e = 0; e < kElems<T> / 2; ++e) add<true>(pair<T>(w, e));
       } else {
 #pragma unroll
-        for (int e = 0; e < (16 / (int)sizeof(T)) / 2; ++e) add<false>(pair<T>(v[k], e));
+        for (int e = 0; e < kElems<T> / 2; ++e) add<false>(pair<T>(v[k], e));
       }
     }
     return b;
@@ -408,7 +410,7 @@ __device__ __noinline__ float2 far_sums(const uint4* src, int n, float loose, fl
   float s = ex2_approx((loose - m) * c2), a = s * fmaxf((loose - m) * c2, kLeast);
   for (int i = threadIdx.x; i < n; i += THREADS) {
     const uint4 v = src[i];
-    for (int e = 0; e < (16 / (int)sizeof(T)) / 2; ++e) {
+    for (int e = 0; e < kElems<T> / 2; ++e) {
       const float2 x = both(pair<T>(v, e));
       const float u = (x.x - m) * c2, w = (x.y - m) * c2;
       s += ex2_approx(u) + ex2_approx(w);
@@ -518,7 +520,7 @@ __device__ __forceinline__ float2 teacher_q(bool there, float y, float scale, fl
   return there ? make_float2(expf(v) / whole.y, v - logf(whole.y)) : make_float2(0.f, 0.f);
 }
 
-// What the listed tokens add: entry k < K the teacher's, entry K the given token.
+// What the tokens of a list add (behind a teacher's entries there may be the given token).
 struct Adds {
   alignas(16) int id[TSP_TOP_MAX + 4];   // (-1: none of this part's; up to a multiple of four)
   float add[TSP_TOP_MAX + 1];
@@ -661,6 +663,11 @@ __device__ __forceinline__ void start_exchange(Exchange* ex) {
   cooperative_groups::this_cluster().sync();
 }
 
+// No CTA ends while another one, whose wait may have run out, can still write to it.
+__device__ __forceinline__ void leave_cluster() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // The row's CTAs: of a cluster, or those that share rows without speaking to each other.
 struct Place {
   int rank, parts, first, stride;
@@ -673,7 +680,7 @@ struct Place {
 // Groups of a part at most.
 template <typename T, int THREADS>
 __device__ __forceinline__ int groups_of(int V, int parts) {
-  const int units = V / (16 / (int)sizeof(T)), per = parts == 1 ? units : (units + parts - 1) / parts;
+  const int units = V / kElems<T>, per = parts == 1 ? units : (units + parts - 1) / parts;
   return max(1, (per + kGroup * THREADS - 1) / (kGroup * THREADS));
 }
 
@@ -885,11 +892,11 @@ __device__ __noinline__ int candidates(const RowPart<T, THREADS>& x, int top, fl
       const uint32_t w = k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
       return sizeof(T) == 2 ? __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16) : __uint_as_float(w);
     };
-    auto token = [&](int u, int e) { return x.head + (x.u_lo + u) * (16 / (int)sizeof(T)) + e; };
+    auto token = [&](int u, int e) { return x.head + (x.u_lo + u) * kElems<T> + e; };
     auto reaching = [&](const uint4& v, int u) {
       uint32_t r = 0;
 #pragma unroll
-      for (int e = 0; e < (16 / (int)sizeof(T)) / 2; ++e) {
+      for (int e = 0; e < kElems<T> / 2; ++e) {
         const float2 y = both(pair<T>(v, e));
         r |= (y.x >= least) << (2 * e) | (y.y >= least) << (2 * e + 1);
       }
@@ -906,7 +913,7 @@ __device__ __noinline__ int candidates(const RowPart<T, THREADS>& x, int top, fl
     auto keep_unit = [&](const uint4& v, int u, uint32_t r, int& place) {
       for (; r; r &= r - 1, ++place) keep(key_of(element(v, __ffs(r) - 1), token(u, __ffs(r) - 1)), place);
     };
-    if (x.units * (16 / (int)sizeof(T)) != x.V && t < (RowPart<T, THREADS>::kLoose + 31) / 32 * 32) {
+    if (x.units * kElems<T> != x.V && t < (RowPart<T, THREADS>::kLoose + 31) / 32 * 32) {
       const int j = x.loose(t);   // the elements outside the units (whole warps)
       const uint64_t key = j >= 0 ? key_of(loose, j) : 0;
       const int place = places(key >= above ? 1 : 0, &sm.n);
@@ -1063,10 +1070,11 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
           kd = lanes_sum<32>(q.x != 0.f ? q.x * (q.y - log_p(z, st, c)) : 0.f);
           if (lane == 0) sm.kd[warp] = kd;
         }
+        const bool teacher = any_entry(K, sm.teach);   // (the next row's entries come in behind the barrier)
         __syncthreads();
         kd = 0.f;
         for (int k = 0; 32 * k < K; ++k) kd += sm.kd[k];
-        kd = any_entry(K, sm.teach) ? a.t.w_kd * kd : 0.f;
+        kd = teacher ? a.t.w_kd * kd : 0.f;
       }
       if (t == 0 && at.rank == 0)
         a.loss[p] = (a.t.w_ce != 0.f ? -a.t.w_ce * log_p(target, st, c) : 0.f) + kd;
@@ -1114,6 +1122,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
       }
     }
   }
+  if constexpr (CLUSTER) leave_cluster();
 }
 
 // ---------------------------------------------------------------------------
@@ -1159,7 +1168,7 @@ __device__ __forceinline__ Factors factors(const GradArgs& a, const Upstream& u,
 // The group of a thread's that has the token, if it is one of the thread's units.
 template <typename T, int THREADS>
 __device__ __forceinline__ int group_with(const RowPart<T, THREADS>& x, int id) {
-  const int u = (id - x.head) / (16 / (int)sizeof(T)) - x.u_lo;
+  const int u = (id - x.head) / kElems<T> - x.u_lo;
   return id >= x.head && id < x.tail && u >= 0 && u < x.n && u % THREADS == (int)threadIdx.x
              ? u / (kGroup * THREADS)
              : -1;
@@ -1167,8 +1176,8 @@ __device__ __forceinline__ int group_with(const RowPart<T, THREADS>& x, int id) 
 // Its logit, in a group that lies at `place` in shared memory.
 template <typename T, int THREADS>
 __device__ __forceinline__ float logit_in(const uint4* place, const RowPart<T, THREADS>& x, int id) {
-  const int u = ((id - x.head) / (16 / (int)sizeof(T)) - x.u_lo) % (kGroup * THREADS);
-  return to_f<T>(reinterpret_cast<const T*>(place + u)[(id - x.head) % (16 / (int)sizeof(T))]);
+  const int u = ((id - x.head) / kElems<T> - x.u_lo) % (kGroup * THREADS);
+  return to_f<T>(reinterpret_cast<const T*>(place + u)[(id - x.head) % kElems<T>]);
 }
 
 // The given token's value is written by the thread that has its unit, so that a row
@@ -1297,7 +1306,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __gr
 }
 
 // Rows and gradients that do not lie alike on 16-byte units: a part of a row a CTA,
-// element by element (8192 x 50257 bf16 at rows 50258 apart: see the table of figures).
+// element by element.
 template <typename T, bool ENT>
 __global__ void __launch_bounds__(kMostThreads) grad_elements_kernel(const __grid_constant__ GradArgs a) {
   constexpr int THREADS = kMostThreads, U = 8;
@@ -1386,6 +1395,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
     float4 part[2][THREADS / 32];
     typename std::conditional<CLUSTER, Exchange, Nothing>::type ex[2];
     typename std::conditional<LIST, Listed, Nothing>::type list;
+    float target;   // the given token's logit
   } sm;
   const GradArgs& a = o.g;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -1418,7 +1428,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
     Exchange* ex = nullptr;
     if constexpr (CLUSTER) ex = &sm.ex[live & 1];
     Stats st = {0.f, -INFINITY, 0.f};
-    float x0 = -INFINITY, up = 1.f, target = 0.f;
+    float x0 = -INFINITY, up = 1.f;
     bool teacher = false;
     const Entry entry = e;
     if (LIST && t < K && r + at.stride < a.r.S) e = load_entry(a.t, pos_of(a.r, r + at.stride), t);
@@ -1428,6 +1438,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
           send_units<T, THREADS>(to + 16 * kGroup * THREADS * g, x.src + t + kGroup * THREADS * g,
                                  x.n - t - kGroup * THREADS * g, o.fill);
       if (j0 >= 0) x0 = to_f<T>(x.row[j0]);
+      float target = 0.f;
       if (t == 0 && id_now >= 0) target = to_f<T>(x.row[id_now]);
       if (a.up) up = a.up[p];
       Sums<T, false> sums(c2);
@@ -1446,6 +1457,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
         sums.template add_units<kGroup>(v);
       }
       sums.add_one(x0);
+      if (t == 0) sm.target = target;   // (it has come before any CTA may write on it)
       int token = -1;
       if constexpr (LIST) {
         if (t < K) token = token_of(entry, a.r);
@@ -1463,7 +1475,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
           if (here)
             z = token < x.head    ? sm.list.loose[token]
                 : token >= x.tail ? sm.list.loose[x.head + token - x.tail]
-                                  : to_f<T>(reinterpret_cast<const T*>(seg)[token - x.head - x.u_lo * (16 / (int)sizeof(T))]);
+                                  : to_f<T>(reinterpret_cast<const T*>(seg)[token - x.head - x.u_lo * kElems<T>]);
           sm.list.kept.token[t] = token;
           sm.list.kept.y[t] = entry.y;
           sm.list.kept.z[t] = z;
@@ -1553,7 +1565,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
     }
     if (t == 0 && at.rank == 0) {
       float loss = 0.f;
-      if (id_now >= 0 && a.t.w_ce != 0.f) loss = -a.t.w_ce * log_p(target, st, c);
+      if (id_now >= 0 && a.t.w_ce != 0.f) loss = -a.t.w_ce * log_p(sm.target, st, c);
       if (teacher) loss += a.t.w_kd * kd;
       o.loss[p] = loss;
       o.stats[2 * (int64_t)p] = st.m;
@@ -1561,6 +1573,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
     }
     if (id_now != -1) ++live;
   }
+  if constexpr (CLUSTER) leave_cluster();
 }
 
 // ---------------------------------------------------------------------------

@@ -1005,10 +1005,12 @@ def _logits_arg(logits, ids, D, scale):
 
 
 def _rows_like(logits):
-    """A gradient's memory: rows as far apart as the logits' and as far from a 16-byte
-    boundary, which is how the kernels read and write them at once."""
+    """A gradient's memory: its rows lie on 128-byte lines as the logits' do, which is
+    how the kernels read and write them at once."""
     S, V = logits.shape
-    ld, at = max(logits.stride(0), V), logits.data_ptr() % 16 // logits.element_size()
+    line = 128 // logits.element_size()
+    at = logits.data_ptr() % 128 // logits.element_size()
+    ld = V + (max(logits.stride(0), V) - V) % line if S > 1 else V
     if ld == V and at == 0:
         return empty((S, V), logits.dtype, logits.device)
     return empty((at + S * ld,), logits.dtype, logits.device)[at:].view(S, ld)[:, :V]

@@ -602,3 +602,60 @@ def test_a_model_is_its_own_teacher():
     i, logp, _ = r.order(7)
     want = -logp.exp().sum(1).log()                  # KL(p restricted to the list || p)
     assert ((o["loss"].cpu().double() - want).abs() <= 2 * r.dl + 700 * U).all()
+
+
+@pytest.mark.parametrize("K", [40, 256])
+@pytest.mark.parametrize("V", [64, 320])
+def test_positions_with_and_without_entries_by_turns(V, K):
+    """Many short rows one after the other: none takes the neighbour's list.  The rows are
+    whole lines, so that every position comes out as it does alone with its own kind."""
+    S = 20000
+    x = torch.randn(S, V, device="cuda", generator=torch.Generator("cuda").manual_seed(V)).bfloat16()
+    gen = torch.Generator().manual_seed(K)
+    t_ids, t_y = torch.randint(0, V, (S, K), generator=gen).int(), torch.randn(S, K, generator=gen)
+    t_ids[::2] = -1
+    t_ids, t_y = t_ids.cuda(), t_y.cuda()
+    for grad in (False, True):
+        got = tsp.token_loss_fwd(x, None, t_ids, t_y, grad=grad)
+        assert not got["loss"][::2].any() and got["loss"][1::2].all()
+        alone = tsp.token_loss_fwd(x[1::2].contiguous(), None, t_ids[1::2].contiguous(), t_y[1::2].contiguous(), grad=grad)
+        assert torch.equal(got["loss"][1::2], alone["loss"])
+        if grad:
+            assert not got["dlogits"][::2].any() and torch.equal(got["dlogits"][1::2], alone["dlogits"])
+
+
+@pytest.mark.parametrize("S,V,dt", [(600, 130000, BF), (600, 70000, F32), (3, 40000, BF)])
+def test_in_place_over_parts_of_a_row(S, V, dt):
+    """A gradient that takes the logits' place: the given token's logit is read by one CTA
+    and written over by another."""
+    gen = torch.Generator("cuda").manual_seed(S)
+    x = torch.randn(S, V, device="cuda", generator=gen).to(dt)
+    t_ids = torch.randint(0, V, (S, 16), generator=gen, device="cuda").int()
+    t_y = torch.randn(S, 16, generator=gen, device="cuda")
+    for kw in (dict(), dict(t_ids=t_ids, t_logits=t_y)):
+        for k in range(4):
+            ids = torch.randint(0, V, (S,), generator=gen, device="cuda")
+            want = tsp.token_loss_fwd(x, ids, grad=True, **kw)
+            y = x.clone()
+            got = tsp.token_loss_fwd(y, ids, dlogits=y, **kw)
+            assert torch.equal(got["loss"], want["loss"]) and torch.equal(y, want["dlogits"])
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_last_positions_of_a_batch(dt):
+    """Rows a whole sequence apart: the gradient takes their own room, not the batch's."""
+    gen = torch.Generator().manual_seed(3)
+    B, L, V = 5, 300, 1003
+    x = (torch.randn(B, L, V, generator=gen) * 2).to(dt).cuda()[:, -1]
+    ids = torch.randint(0, V, (B,), generator=gen).cuda()
+    got = tsp.token_loss_fwd(x, ids, grad=True, stats=True)
+    assert got["dlogits"]._base is None or got["dlogits"]._base.numel() < (B + 1) * (V + 64)
+    r = Ref(x)
+    loss, tol, adds, weight = loss_reference(r, ids.cpu(), 1.0, None, None, 0.0, 1.0)
+    near(got["loss"], loss, tol, "loss")
+    size = torch.ones_like(r.p)
+    gtol = grad_tolerance(r, size, adds.abs(), dt) + 1.01 * r.p * r.dl[:, None]
+    near(got["dlogits"], r.p + adds, gtol, "gradient (one pass)")
+    near(tsp.token_loss_bwd(x, got["stats"], ids), r.p + adds, gtol, "gradient")
+    one = tsp.token_loss_fwd(x[:1], ids[:1], grad=True)
+    assert one["dlogits"].is_contiguous()
