@@ -520,6 +520,16 @@ __device__ __forceinline__ float2 teacher_q(bool there, float y, float scale, fl
   return there ? make_float2(expf(v) / whole.y, v - logf(whole.y)) : make_float2(0.f, 0.f);
 }
 
+// The sum of the values of the warps that have entries; all of these take part.
+__device__ __forceinline__ float warps_sum(float v, int K, float* part) {
+  if (K <= 32) return v;
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  asm volatile("bar.sync 1, %0;" ::"r"((K + 31) / 32 * 32) : "memory");
+  v = 0.f;
+  for (int k = 0; 32 * k < K; ++k) v += part[k];
+  return v;
+}
+
 // What the tokens of a list add (behind a teacher's entries there may be the given token).
 struct Adds {
   alignas(16) int id[TSP_TOP_MAX + 4];   // (-1: none of this part's; up to a multiple of four)
@@ -983,7 +993,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
     typename std::conditional<TOP, TopSmem<THREADS>, Nothing>::type top;
   } sm;
   const auto cluster = cooperative_groups::this_cluster();
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int t = threadIdx.x, warp = t >> 5;
   const Place at(CLUSTER ? a.parts : 1);
   const float c = a.r.scale, c2 = c * kLog2e;
   const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
@@ -994,11 +1004,15 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
   while (TOP && (groups - 1) >> shift >= kSlots) ++shift;
   if constexpr (CLUSTER) start_exchange(sm.ex);
   int id = given(a.r, at.first);
+  Entry e = {-1, -INFINITY};
+  if (t < K && at.first < a.r.S) e = load_entry(a.t, pos_of(a.r, at.first), t);
   uint32_t live = 0;   // rows so far that are not padding
   for (int r = at.first; r < a.r.S; r += at.stride) {
     const int p = pos_of(a.r, r), id_now = id;
     if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
     id = given(a.r, r + at.stride);
+    const Entry entry = e;
+    if (t < K && r + at.stride < a.r.S) e = load_entry(a.t, pos_of(a.r, r + at.stride), t);
     if (id_now == -1) {   // padding: the row is not looked at
       if (at.rank != 0) continue;
       if (t == 0) {
@@ -1021,9 +1035,8 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
     const float x0 = j0 >= 0 ? to_f<T>(x.row[j0]) : -INFINITY;
     float target = 0.f, z = 0.f;
     if (t == 0 && id_now >= 0) target = to_f<T>(x.row[id_now]);
-    Entry e = {-1, -INFINITY};
-    int kid = -1;
-    if (t < K && at.rank == 0) e = load_entry(a.t, p, t);
+    const int kid = t < K && at.rank == 0 ? token_of(entry, a.r) : -1;
+    if (kid >= 0) z = to_f<T>(x.row[kid]);
     Sums<T, ENT> sums(c2);
     float in_slot = -INFINITY;
     for (int g = 0; g < groups; ++g) {
@@ -1040,14 +1053,10 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
           in_slot = -INFINITY;
         }
       }
-      if (g == 0 && t < K) {   // the entry is there by now: its logit is sent for
-        kid = token_of(e, a.r);
-        if (kid >= 0) z = to_f<T>(x.row[kid]);
-      }
     }
     const float mine = sums.top;   // of the units
     sums.add_one(x0);
-    if (K > 0) teacher_part(K, kid >= 0, e.y, a.t.scale, sm.teach);
+    if (K > 0) teacher_part(K, kid >= 0, entry.y, a.t.scale, sm.teach);
     Exchange* ex = nullptr;
     if constexpr (CLUSTER) ex = &sm.ex[live & 1];
     const Stats st = statistics<T, ENT, CLUSTER, THREADS>(sums, x.src, x.n, x0, c2, sm.part[live & 1], ex, live >> 1 & 1,
@@ -1063,18 +1072,12 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
     }
     if (a.loss) {
       float kd = 0.f;
-      if (K > 0) {
-        if (warp * 32 < K) {
-          const float2 whole = teacher_whole(K, a.t.scale, sm.teach);
-          const float2 q = teacher_q(kid >= 0, e.y, a.t.scale, whole);
-          kd = lanes_sum<32>(q.x != 0.f ? q.x * (q.y - log_p(z, st, c)) : 0.f);
-          if (lane == 0) sm.kd[warp] = kd;
-        }
-        const bool teacher = any_entry(K, sm.teach);   // (the next row's entries come in behind the barrier)
-        __syncthreads();
-        kd = 0.f;
-        for (int k = 0; 32 * k < K; ++k) kd += sm.kd[k];
-        kd = teacher ? a.t.w_kd * kd : 0.f;
+      if (warp * 32 < K) {
+        const float2 whole = teacher_whole(K, a.t.scale, sm.teach);
+        const float2 q = teacher_q(kid >= 0, entry.y, a.t.scale, whole);
+        kd = lanes_sum<32>(q.x != 0.f ? q.x * (q.y - log_p(z, st, c)) : 0.f);
+        kd = warps_sum(kd, K, sm.kd);   // (behind its barrier the next row's entries come in)
+        kd = whole.y != 0.f ? a.t.w_kd * kd : 0.f;
       }
       if (t == 0 && at.rank == 0)
         a.loss[p] = (a.t.w_ce != 0.f ? -a.t.w_ce * log_p(target, st, c) : 0.f) + kd;
@@ -1398,7 +1401,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
     float target;   // the given token's logit
   } sm;
   const GradArgs& a = o.g;
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int t = threadIdx.x, warp = t >> 5;
   const Place at(CLUSTER ? a.parts : 1);
   const float c = a.r.scale, c2 = c * kLog2e;
   const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
@@ -1543,15 +1546,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
             if (q.x != 0.f) kd = q.x * (q.y - log_p(CLUSTER && at.rank == 0 ? ex->z[t] : z, st, c));
             if (!here) token = -1;
           }
-          if (at.rank == 0) {
-            kd = lanes_sum<32>(kd);
-            if (K > 32) {   // over the warps that have entries
-              if (lane == 0) sm.list.kd[warp] = kd;
-              asm volatile("bar.sync 1, %0;" ::"r"((K + 31) / 32 * 32) : "memory");
-              kd = 0.f;
-              for (int k = 0; 32 * k < K; ++k) kd += sm.list.kd[k];
-            }
-          }
+          if (at.rank == 0) kd = warps_sum(lanes_sum<32>(kd), K, sm.list.kd);
         }
         if (twice) {
           put_adds<THREADS>(sm.list.adds, K, token, add, z);
