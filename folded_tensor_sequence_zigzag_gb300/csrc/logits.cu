@@ -520,6 +520,31 @@ __device__ __forceinline__ float2 teacher_q(bool there, float y, float scale, fl
   return there ? make_float2(expf(v) / whole.y, v - logf(whole.y)) : make_float2(0.f, 0.f);
 }
 
+// KL(q || p) without a second look at the entries when l is known: a warp's largest entry
+// and listed logit (y0, z0), sum e^(scale (y - y0)) and the sum of its terms times scale
+// (y - y0) - c (z - z0).  One thread puts the warps together; what is added for y0 and z0
+// has the sign of the differences from them, so that nothing cancels.
+__device__ __forceinline__ float4 list_sums(bool there, float y, float z, float scale, float c) {
+  const float y0 = lanes_max(there ? y : -INFINITY);
+  float z0 = lanes_max(there ? z : -INFINITY);
+  if (z0 == -INFINITY) z0 = 0.f;
+  const float v = scale * (y - y0), e = there ? expf(v) : 0.f;
+  return make_float4(y0, lanes_sum<32>(e), lanes_sum<32>(e != 0.f ? e * (v - c * (z - z0)) : 0.f), z0);
+}
+__device__ __forceinline__ float divergence(const float4* listed, int K, float scale, const Stats& st, float c) {
+  const int n = (K + 31) / 32;
+  float y0 = -INFINITY, s = 0.f, b = 0.f;
+  for (int k = 0; k < n; ++k) y0 = fmaxf(y0, listed[k].x);
+  for (int k = 0; k < n; ++k) {
+    const float4 w = listed[k];
+    const float v = scale * (w.x - y0), f = w.y == 0.f ? 0.f : expf(v);
+    if (f == 0.f) continue;
+    s += f * w.y;
+    b += f * (w.z + w.y * (v - c * (w.w - st.m)));
+  }
+  if (s == 0.f) return 0.f;   // no entry
+  return st.l == -INFINITY ? INFINITY : b / s - logf(s) + st.l;
+}
 // The sum of the values of the warps that have entries; all of these take part.
 __device__ __forceinline__ float warps_sum(float v, int K, float* part) {
   if (K <= 32) return v;
@@ -985,27 +1010,25 @@ template <typename T, bool ENT, bool TOP, bool CLUSTER, int THREADS>
 __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __grid_constant__ FwdArgs a) {
   extern __shared__ __align__(128) uint4 ring[];
   __shared__ struct {
-    float4 part[2][THREADS / 32];
-    float2 teach[THREADS / 32];
-    float kd[THREADS / 32];
+    float4 part[2][THREADS / 32], listed[2][THREADS / 32];
     typename std::conditional<CLUSTER, Exchange, Nothing>::type ex[2];
     typename std::conditional<CLUSTER, TopLists, Nothing>::type lists;
     typename std::conditional<TOP, TopSmem<THREADS>, Nothing>::type top;
   } sm;
   const auto cluster = cooperative_groups::this_cluster();
-  const int t = threadIdx.x, warp = t >> 5;
+  const int t = threadIdx.x;
   const Place at(CLUSTER ? a.parts : 1);
   const float c = a.r.scale, c2 = c * kLog2e;
   const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
   const int K = a.loss ? a.t.K : 0;
+  Entry e = {-1, -INFINITY};
+  if (t < K && at.first < a.r.S) e = load_entry(a.t, pos_of(a.r, at.first), t);
   Sender<T, THREADS, stages_of(TOP)> sender(a.r, ring, at, groups);
   uint16_t* slot = reinterpret_cast<uint16_t*>(ring + ring_bytes(THREADS, TOP) / 16);
   int shift = 0;   // groups a slot
   while (TOP && (groups - 1) >> shift >= kSlots) ++shift;
   if constexpr (CLUSTER) start_exchange(sm.ex);
   int id = given(a.r, at.first);
-  Entry e = {-1, -INFINITY};
-  if (t < K && at.first < a.r.S) e = load_entry(a.t, pos_of(a.r, at.first), t);
   uint32_t live = 0;   // rows so far that are not padding
   for (int r = at.first; r < a.r.S; r += at.stride) {
     const int p = pos_of(a.r, r), id_now = id;
@@ -1046,6 +1069,10 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
       for (int k = 0; k < kGroup; ++k) v[k] = from[k * THREADS];
       sender.send();
       const float b = sums.template add_units<kGroup>(v);
+      if (g == 0 && (t & ~31) < K && at.rank == 0) {   // the listed logits are there by now
+        const float4 w = list_sums(kid >= 0, entry.y, z, a.t.scale, c);
+        if ((t & 31) == 0) sm.listed[live & 1][t >> 5] = w;
+      }
       if constexpr (TOP) {
         in_slot = fmaxf(in_slot, b);
         if (((g + 1) & ((1 << shift) - 1)) == 0 || g + 1 == groups) {
@@ -1056,12 +1083,10 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
     }
     const float mine = sums.top;   // of the units
     sums.add_one(x0);
-    if (K > 0) teacher_part(K, kid >= 0, entry.y, a.t.scale, sm.teach);
     Exchange* ex = nullptr;
     if constexpr (CLUSTER) ex = &sm.ex[live & 1];
     const Stats st = statistics<T, ENT, CLUSTER, THREADS>(sums, x.src, x.n, x0, c2, sm.part[live & 1], ex, live >> 1 & 1,
                                                           at.rank, at.parts, a.wait);
-    ++live;
     if (t == 0 && at.rank == 0) {
       if (a.logp) a.logp[p] = log_p(target, st, c);
       if (a.entropy) a.entropy[p] = st.entropy;
@@ -1069,19 +1094,11 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
         a.stats[2 * (int64_t)p] = st.m;
         a.stats[2 * (int64_t)p + 1] = st.l;
       }
+      if (a.loss)
+        a.loss[p] = (a.t.w_ce != 0.f ? -a.t.w_ce * log_p(target, st, c) : 0.f) +
+                    (K > 0 ? a.t.w_kd * divergence(sm.listed[live & 1], K, a.t.scale, st, c) : 0.f);
     }
-    if (a.loss) {
-      float kd = 0.f;
-      if (warp * 32 < K) {
-        const float2 whole = teacher_whole(K, a.t.scale, sm.teach);
-        const float2 q = teacher_q(kid >= 0, entry.y, a.t.scale, whole);
-        kd = lanes_sum<32>(q.x != 0.f ? q.x * (q.y - log_p(z, st, c)) : 0.f);
-        kd = warps_sum(kd, K, sm.kd);   // (behind its barrier the next row's entries come in)
-        kd = whole.y != 0.f ? a.t.w_kd * kd : 0.f;
-      }
-      if (t == 0 && at.rank == 0)
-        a.loss[p] = (a.t.w_ce != 0.f ? -a.t.w_ce * log_p(target, st, c) : 0.f) + kd;
-    }
+    ++live;
     if constexpr (TOP) {
       const int64_t to = (int64_t)p * a.top;
       int n = 0;
@@ -1203,12 +1220,12 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __gr
   const float c2 = a.r.scale * kLog2e;
   const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
   const int K = LIST ? a.t.K : 0;
-  Sender<T, THREADS, stages_of(false)> sender(a.r, ring, at, groups);
-  int id = given(a.r, at.first);
-  Upstream up = upstream<ENT>(a, at.first);
   Entry e = {-1, -INFINITY};
+  if (LIST && t < K && at.first < a.r.S) e = load_entry(a.t, pos_of(a.r, at.first), t);
+  Upstream up = upstream<ENT>(a, at.first);
+  int id = given(a.r, at.first);
+  Sender<T, THREADS, stages_of(false)> sender(a.r, ring, at, groups);
   if constexpr (LIST) {
-    if (t < K && at.first < a.r.S) e = load_entry(a.t, pos_of(a.r, at.first), t);
     for (int k = t; k < 2 * kTable; k += THREADS) sm.table[k / kTable][k % kTable] = -1;
     if (t < 2) sm.twice[t] = 0;
     __syncthreads();
@@ -1687,13 +1704,13 @@ int parts_for(int64_t S, int64_t units, int parts) {
   while (parts <= 4 && S * parts * 2 <= num_sms() * 2 && units / (2 * parts) >= 256) parts *= 2;
   return parts;
 }
-// Rows a CTA: 64 KB, three times that with a teacher.  The GPU hands CTAs out as others end,
-// which evens out what multiprocessors get of the memory (8192 x 32000 bf16, loss with
-// gradient: 152 us, 180 where each resident CTA walks as many rows).
+// Rows a CTA: 64 KB.  The GPU hands CTAs out as others end, which evens out what
+// multiprocessors get of the memory (8192 x 32000 bf16, loss with gradient: 152 us, 180
+// where each resident CTA walks as many rows).
 template <typename T>
-int64_t rows_a_cta(int64_t V, int parts, bool teacher) {
+int64_t rows_a_cta(int64_t V, int parts) {
   const int64_t bytes = std::max<int64_t>(1, V * (int64_t)sizeof(T) / parts);
-  return std::max<int64_t>(1, 65536 / bytes) * (teacher ? 3 : 1);
+  return std::max<int64_t>(1, 65536 / bytes);
 }
 
 template <typename T, bool ENT, bool TOP, bool CLUSTER, int THREADS>
@@ -1703,7 +1720,7 @@ tsp_status launch_fwd_c(const FwdArgs& a, const char* name, cudaStream_t st) {
   const int64_t groups = std::max<int64_t>(1, (per + kGroup * THREADS - 1) / (kGroup * THREADS));
   const size_t smem = ring + (TOP ? std::min<int64_t>(kSlots, groups) * THREADS * 2 : 0);
   return launch_rows<fwd_kernel<T, ENT, TOP, CLUSTER, THREADS>, CLUSTER, most>(
-      a, a.r.S, THREADS, a.parts, smem, rows_a_cta<T>(a.r.V, a.parts, a.t.K > 0), name, st);
+      a, a.r.S, THREADS, a.parts, smem, rows_a_cta<T>(a.r.V, a.parts) * (a.t.K > 128 ? 3 : 1), name, st);
 }
 // The fewer threads a CTA has, the less a row costs that is not its logits: 128, as many
 // as keep the pipelines full (8192 x 32000 bf16: 82 us, 101 with 256); 64 for rows of two
@@ -1748,7 +1765,7 @@ tsp_status launch_grad_t(GradArgs a, const char* name, cudaStream_t st) {
   }
   a.parts = parts_for(a.r.S, units, 1);
   const int threads = threads_for((units + a.parts - 1) / a.parts, a.t.K);
-  const int64_t rows = rows_a_cta<T>(a.r.V, a.parts, a.t.K > 0);
+  const int64_t rows = rows_a_cta<T>(a.r.V, a.parts);
   if (threads == 128)
     return launch_rows<grad_kernel<T, ENT, LIST, 128>, false, kRingMost>(a, a.r.S, 128, a.parts, ring_bytes(128), rows, name, st);
   return launch_rows<grad_kernel<T, ENT, LIST, 256>, false, kRingMost>(a, a.r.S, 256, a.parts, ring_bytes(256), rows, name, st);
@@ -1787,7 +1804,7 @@ tsp_status launch_one_pass_c(OnePassArgs o, cudaStream_t st) {
   // whole groups up to three CTAs' share of a multiprocessor (quicker: no case is apart)
   o.fill = per <= 16 * kMostThreads;
   const size_t smem = part_bytes(per, threads, o.fill ? kGroup : 1);
-  const int64_t rows = CLUSTER ? 4 : rows_a_cta<T>(o.g.r.V, parts, o.g.t.K > 0);
+  const int64_t rows = CLUSTER ? 4 : rows_a_cta<T>(o.g.r.V, parts) * (LIST ? 2 : 1);
   if (threads == 128)
     return launch_rows<one_pass_kernel<T, LIST, CLUSTER, 128>, CLUSTER, kOnePassMost>(o, o.g.r.S, 128, parts, smem, rows, "token_loss_one_pass", st);
   return launch_rows<one_pass_kernel<T, LIST, CLUSTER, 256>, CLUSTER, kOnePassMost>(o, o.g.r.S, 256, parts, smem, rows, "token_loss_one_pass", st);
