@@ -118,12 +118,33 @@ __device__ __forceinline__ int pos_of(const Rows& a, int row) {
   const int r = (unsigned)row / (2u * a.c), rest = row - r * 2 * a.c;
   return rest < a.c ? r * a.c + rest : (2 * a.D - 1 - r) * a.c + rest - a.c;
 }
+// What is read ahead of its use stays as it was read: to convert it would be to wait for
+// it.  (The asm keeps the conversion from being moved up to the read.)
+template <typename T> using Bits = typename std::conditional<sizeof(T) == 2, unsigned short, unsigned>::type;
+template <typename T> __device__ __forceinline__ Bits<T> bits_at(const T* p) { return *reinterpret_cast<const Bits<T>*>(p); }
+template <typename T> __device__ __forceinline__ Bits<T> no_logit() { return sizeof(T) == 2 ? 0xff80u : 0xff800000u; }   // -inf
+__device__ __forceinline__ float value_of(unsigned short b) {
+  asm volatile("" : "+h"(b));
+  return __uint_as_float((unsigned)b << 16);
+}
+__device__ __forceinline__ float value_of(unsigned b) { return __uint_as_float(b); }
+
 // A row's given token: -1 for padding, -2 where there are no tokens or no such row.
-__device__ __forceinline__ int given(const Rows& a, int row) {
+__device__ __forceinline__ int2 ask_given(const Rows& a, int row) {
+  int2 id = make_int2(0, 0);
+  if (row < a.S && a.ids) {
+    const int p = pos_of(a, row);
+    if (a.id_bytes == 8)
+      id = reinterpret_cast<const int2*>(a.ids)[p];
+    else
+      id.x = reinterpret_cast<const int*>(a.ids)[p];
+  }
+  return id;
+}
+__device__ __forceinline__ int given(const Rows& a, int row, int2 asked) {
+  asm volatile("" : "+r"(asked.x), "+r"(asked.y));
   if (row >= a.S || !a.ids) return -2;
-  const int p = pos_of(a, row);
-  const int64_t id = a.id_bytes == 8 ? (int64_t)reinterpret_cast<const long long*>(a.ids)[p]
-                                     : (int64_t)reinterpret_cast<const int*>(a.ids)[p];
+  const int64_t id = a.id_bytes == 8 ? (int64_t)((uint64_t)(uint32_t)asked.y << 32 | (uint32_t)asked.x) : (int64_t)asked.x;
   if (id >= a.V && threadIdx.x == 0) report_status(a.status, (int)TSP_ERR_RANGE);
   return id >= 0 && id < a.V ? (int)id : -1;
 }
@@ -486,15 +507,28 @@ struct Teacher {
   int f32, K;
   float scale, w_ce, w_kd;
 };
-// An entry as it stands (not yet looked at), and its token: -1 for none.
+// An entry as it was read, and its values.
+struct Asked {
+  int id;
+  unsigned y;
+};
 struct Entry {
   int id;
   float y;
 };
-__device__ __forceinline__ Entry load_entry(const Teacher& t, int p, int k) {
+__device__ __forceinline__ Asked ask_entry(const Teacher& t, int p, int k) {
   const int64_t i = (int64_t)p * t.K + k;
-  return {t.ids[i], t.f32 ? reinterpret_cast<const float*>(t.logits)[i]
-                          : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(t.logits)[i])};
+  Asked e;
+  e.id = t.ids[i];
+  if (t.f32)
+    e.y = reinterpret_cast<const unsigned*>(t.logits)[i];
+  else
+    e.y = reinterpret_cast<const unsigned short*>(t.logits)[i];
+  return e;
+}
+__device__ __forceinline__ Entry entry_of(const Teacher& t, Asked e) {
+  asm volatile("" : "+r"(e.y));
+  return {e.id, __uint_as_float(t.f32 ? e.y : e.y << 16)};
 }
 __device__ __forceinline__ int token_of(const Entry& e, const Rows& r) {
   if (e.id >= r.V) report_status(r.status, (int)TSP_ERR_RANGE);
@@ -732,12 +766,13 @@ struct Sender {
   const uint4* mine;     // the thread's first place
   uint32_t to;           // ... as an address in shared memory
   Place at;
-  int groups, row, ahead, slot;
+  int groups, row, slot;
+  int2 ahead;            // the next row's given token
   int g, left;           // groups left of the row, units left from the thread's next one
   const uint4* src;
   __device__ __forceinline__ Sender(const Rows& rows, const uint4* ring, Place place, int n)
       : a(rows), mine(ring + threadIdx.x), to(smem_u32(ring + threadIdx.x)), at(place), groups(n),
-        row(place.first - place.stride), ahead(given(rows, place.first)), slot(0), g(0), left(0), src(nullptr) {
+        row(place.first - place.stride), slot(0), ahead(ask_given(rows, place.first)), g(0), left(0), src(nullptr) {
     for (int k = 0; k < STAGES; ++k) send();
   }
   // The thread's units of the group that is next in turn, THREADS apart.
@@ -751,8 +786,8 @@ struct Sender {
       int id;
       do {
         row += at.stride;
-        id = ahead;
-        if (row < a.S) ahead = given(a, row + at.stride);
+        id = row < a.S ? given(a, row, ahead) : -2;
+        if (row < a.S) ahead = ask_given(a, row + at.stride);
       } while (row < a.S && id == -1);
       if (row < a.S) {
         const RowPart<T, THREADS> x(a, row, at.rank, at.parts);
@@ -1020,28 +1055,29 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
   const Place at(CLUSTER ? a.parts : 1);
   const float c = a.r.scale, c2 = c * kLog2e;
   const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
-  const int K = a.loss ? a.t.K : 0;
-  Entry e = {-1, -INFINITY};
-  if (t < K && at.first < a.r.S) e = load_entry(a.t, pos_of(a.r, at.first), t);
+  constexpr bool LOSS = CLUSTER || !(ENT || TOP);   // (a loss asks for neither)
+  const int K = LOSS ? a.t.K : 0;
+  Asked e = {-1, 0};
+  if (t < K && at.first < a.r.S) e = ask_entry(a.t, pos_of(a.r, at.first), t);
   Sender<T, THREADS, stages_of(TOP)> sender(a.r, ring, at, groups);
   uint16_t* slot = reinterpret_cast<uint16_t*>(ring + ring_bytes(THREADS, TOP) / 16);
   int shift = 0;   // groups a slot
   while (TOP && (groups - 1) >> shift >= kSlots) ++shift;
   if constexpr (CLUSTER) start_exchange(sm.ex);
-  int id = given(a.r, at.first);
+  int2 asked = ask_given(a.r, at.first);
   uint32_t live = 0;   // rows so far that are not padding
   for (int r = at.first; r < a.r.S; r += at.stride) {
-    const int p = pos_of(a.r, r), id_now = id;
+    const int p = pos_of(a.r, r), id_now = given(a.r, r, asked);
     if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
-    id = given(a.r, r + at.stride);
-    const Entry entry = e;
-    if (t < K && r + at.stride < a.r.S) e = load_entry(a.t, pos_of(a.r, r + at.stride), t);
+    asked = ask_given(a.r, r + at.stride);
+    const Entry entry = entry_of(a.t, e);
+    if (t < K && r + at.stride < a.r.S) e = ask_entry(a.t, pos_of(a.r, r + at.stride), t);
     if (id_now == -1) {   // padding: the row is not looked at
       if (at.rank != 0) continue;
       if (t == 0) {
         if (a.logp) a.logp[p] = 0.f;
         if (a.entropy) a.entropy[p] = 0.f;
-        if (a.loss) a.loss[p] = 0.f;
+        if (LOSS && a.loss) a.loss[p] = 0.f;
         if (a.stats) {
           a.stats[2 * (int64_t)p] = 0.f;
           a.stats[2 * (int64_t)p + 1] = -INFINITY;
@@ -1055,11 +1091,11 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
     }
     const RowPart<T, THREADS> x(a.r, r, at.rank, at.parts);
     const int j0 = x.loose(t);
-    const float x0 = j0 >= 0 ? to_f<T>(x.row[j0]) : -INFINITY;
-    float target = 0.f, z = 0.f;
-    if (t == 0 && id_now >= 0) target = to_f<T>(x.row[id_now]);
+    Bits<T> loose = no_logit<T>(), target = 0, z = 0;
+    if (j0 >= 0) loose = bits_at(x.row + j0);
+    if (t == 0 && id_now >= 0) target = bits_at(x.row + id_now);
     const int kid = t < K && at.rank == 0 ? token_of(entry, a.r) : -1;
-    if (kid >= 0) z = to_f<T>(x.row[kid]);
+    if (kid >= 0) z = bits_at(x.row + kid);
     Sums<T, ENT> sums(c2);
     float in_slot = -INFINITY;
     for (int g = 0; g < groups; ++g) {
@@ -1070,7 +1106,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
       sender.send();
       const float b = sums.template add_units<kGroup>(v);
       if (g == 0 && (t & ~31) < K && at.rank == 0) {   // the listed logits are there by now
-        const float4 w = list_sums(kid >= 0, entry.y, z, a.t.scale, c);
+        const float4 w = list_sums(kid >= 0, entry.y, value_of(z), a.t.scale, c);
         if ((t & 31) == 0) sm.listed[live & 1][t >> 5] = w;
       }
       if constexpr (TOP) {
@@ -1081,21 +1117,21 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) fwd_kernel(const __gri
         }
       }
     }
-    const float mine = sums.top;   // of the units
+    const float mine = sums.top, x0 = value_of(loose);   // (mine: of the units)
     sums.add_one(x0);
     Exchange* ex = nullptr;
     if constexpr (CLUSTER) ex = &sm.ex[live & 1];
     const Stats st = statistics<T, ENT, CLUSTER, THREADS>(sums, x.src, x.n, x0, c2, sm.part[live & 1], ex, live >> 1 & 1,
                                                           at.rank, at.parts, a.wait);
     if (t == 0 && at.rank == 0) {
-      if (a.logp) a.logp[p] = log_p(target, st, c);
+      if (a.logp) a.logp[p] = log_p(value_of(target), st, c);
       if (a.entropy) a.entropy[p] = st.entropy;
       if (a.stats) {
         a.stats[2 * (int64_t)p] = st.m;
         a.stats[2 * (int64_t)p + 1] = st.l;
       }
-      if (a.loss)
-        a.loss[p] = (a.t.w_ce != 0.f ? -a.t.w_ce * log_p(target, st, c) : 0.f) +
+      if (LOSS && a.loss)
+        a.loss[p] = (a.t.w_ce != 0.f ? -a.t.w_ce * log_p(value_of(target), st, c) : 0.f) +
                     (K > 0 ? a.t.w_kd * divergence(sm.listed[live & 1], K, a.t.scale, st, c) : 0.f);
     }
     ++live;
@@ -1220,10 +1256,10 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __gr
   const float c2 = a.r.scale * kLog2e;
   const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
   const int K = LIST ? a.t.K : 0;
-  Entry e = {-1, -INFINITY};
-  if (LIST && t < K && at.first < a.r.S) e = load_entry(a.t, pos_of(a.r, at.first), t);
+  Asked e = {-1, 0};
+  if (LIST && t < K && at.first < a.r.S) e = ask_entry(a.t, pos_of(a.r, at.first), t);
   Upstream up = upstream<ENT>(a, at.first);
-  int id = given(a.r, at.first);
+  int2 asked = ask_given(a.r, at.first);
   Sender<T, THREADS, stages_of(false)> sender(a.r, ring, at, groups);
   if constexpr (LIST) {
     for (int k = t; k < 2 * kTable; k += THREADS) sm.table[k / kTable][k % kTable] = -1;
@@ -1232,14 +1268,14 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __gr
   }
   int turn = 0;
   for (int r = at.first; r < a.r.S; r += at.stride) {
-    const int id_now = id;
+    const int id_now = given(a.r, r, asked);
     const Upstream u = up;
-    const Entry entry = e;
+    const Entry entry = entry_of(a.t, e);
     const int p = pos_of(a.r, r);
     if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
-    id = given(a.r, r + at.stride);
+    asked = ask_given(a.r, r + at.stride);
     up = upstream<ENT>(a, r + at.stride);
-    if (LIST && t < K && r + at.stride < a.r.S) e = load_entry(a.t, pos_of(a.r, r + at.stride), t);
+    if (LIST && t < K && r + at.stride < a.r.S) e = ask_entry(a.t, pos_of(a.r, r + at.stride), t);
     const RowPart<T, THREADS> x(a.r, r, at.rank, at.parts);
     T* out = reinterpret_cast<T*>(a.out) + (int64_t)r * a.ld_out;
     uint4* dst = reinterpret_cast<uint4*>(out + x.head) + x.u_lo + t;
@@ -1255,7 +1291,8 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __gr
         }
       continue;
     }
-    const float x0 = j0 >= 0 ? to_f<T>(x.row[j0]) : -INFINITY;
+    Bits<T> loose = no_logit<T>();
+    if (j0 >= 0) loose = bits_at(x.row + j0);
     bool teacher = false;
     if constexpr (LIST) {
       const int token = t < K ? token_of(entry, a.r) : -1;
@@ -1275,7 +1312,6 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __gr
     const Slope<ENT> slope(u.m, u.l, c2, f.A, f.B);
     const bool adds_given = id_now >= 0 && (a.loss ? a.t.w_ce != 0.f : a.up != nullptr);
     const int own = adds_given ? group_with<T, THREADS>(x, id_now) : -1;   // the group with the given token
-    if (j0 >= 0) out[j0] = from_f<T>(slope.one(x0) + (adds_given && j0 == id_now ? f.given : 0.f));
     for (int g = 0, left = x.n - t; g < groups; ++g, left -= kGroup * THREADS, dst += kGroup * THREADS) {
       const uint4* place = sender.next();
       uint4 v[kGroup];
@@ -1295,6 +1331,7 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) grad_kernel(const __gr
       }
       if (g == own) out[id_now] = from_f<T>(slope.one(x_given) + f.given);
     }
+    if (j0 >= 0) out[j0] = from_f<T>(slope.one(value_of(loose)) + (adds_given && j0 == id_now ? f.given : 0.f));
     if constexpr (LIST) {
       __syncthreads();   // the listed tokens' values go on top of what other threads wrote
       const bool twice = sm.twice[turn] != 0;
@@ -1336,7 +1373,7 @@ __global__ void __launch_bounds__(kMostThreads) grad_elements_kernel(const __gri
   } sm;
   const int t = threadIdx.x, r = blockIdx.x, p = pos_of(a.r, r);
   if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
-  const int id = given(a.r, r), K = a.loss && a.t.w_kd != 0.f ? a.t.K : 0;
+  const int id = given(a.r, r, ask_given(a.r, r)), K = a.loss && a.t.w_kd != 0.f ? a.t.K : 0;
   const int per = (a.r.V + gridDim.y - 1) / gridDim.y, lo = min(a.r.V, (int)blockIdx.y * per), hi = min(a.r.V, lo + per);
   const T* x = reinterpret_cast<const T*>(a.r.logits) + (int64_t)r * a.r.ld;
   T* out = reinterpret_cast<T*>(a.out) + (int64_t)r * a.ld_out;
@@ -1348,7 +1385,7 @@ __global__ void __launch_bounds__(kMostThreads) grad_elements_kernel(const __gri
   bool teacher = false;
   if (K > 0) {
     Entry e = {-1, -INFINITY};
-    if (t < K) e = load_entry(a.t, p, t);
+    if (t < K) e = entry_of(a.t, ask_entry(a.t, p, t));
     const int kid = t < K ? token_of(e, a.r) : -1;
     teacher_part(K, kid >= 0, e.y, a.t.scale, sm.teach);
     __syncthreads();
@@ -1424,10 +1461,11 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
   const int groups = groups_of<T, THREADS>(a.r.V, at.parts);
   const int K = LIST ? a.t.K : 0;
   const uint32_t to = smem_u32(seg + t);
-  int id = given(a.r, at.first);
-  Entry e = {-1, -INFINITY};
+  int id = given(a.r, at.first, ask_given(a.r, at.first));
+  int2 asked = ask_given(a.r, at.first + at.stride);
+  Asked e = {-1, 0};
   if constexpr (LIST) {
-    if (t < K && at.first < a.r.S) e = load_entry(a.t, pos_of(a.r, at.first), t);
+    if (t < K && at.first < a.r.S) e = ask_entry(a.t, pos_of(a.r, at.first), t);
     for (int k = t; k < kTable; k += THREADS) sm.list.table[k] = -1;
     if (t == 0) sm.list.twice = 0;
   }
@@ -1437,7 +1475,8 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
   for (int r = at.first; r < a.r.S; r += at.stride) {
     const int p = pos_of(a.r, r), id_now = id;
     if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
-    id = given(a.r, r + at.stride);
+    id = given(a.r, r + at.stride, asked);
+    asked = ask_given(a.r, r + at.stride < a.r.S ? r + 2 * at.stride : a.r.S);
     const RowPart<T, THREADS> x(a.r, r, at.rank, at.parts);
     T* out = reinterpret_cast<T*>(a.out) + (int64_t)r * a.ld_out;
     uint4* dst = reinterpret_cast<uint4*>(out + x.head) + x.u_lo + t;
@@ -1450,16 +1489,16 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
     Stats st = {0.f, -INFINITY, 0.f};
     float x0 = -INFINITY, up = 1.f;
     bool teacher = false;
-    const Entry entry = e;
-    if (LIST && t < K && r + at.stride < a.r.S) e = load_entry(a.t, pos_of(a.r, r + at.stride), t);
+    const Entry entry = entry_of(a.t, e);
+    if (LIST && t < K && r + at.stride < a.r.S) e = ask_entry(a.t, pos_of(a.r, r + at.stride), t);
     if (id_now != -1) {
       if (!sent)
         for (int g = 0; g < groups; ++g)
           send_units<T, THREADS>(to + 16 * kGroup * THREADS * g, x.src + t + kGroup * THREADS * g,
                                  x.n - t - kGroup * THREADS * g, o.fill);
-      if (j0 >= 0) x0 = to_f<T>(x.row[j0]);
-      float target = 0.f;
-      if (t == 0 && id_now >= 0) target = to_f<T>(x.row[id_now]);
+      Bits<T> loose = no_logit<T>(), target = 0;
+      if (j0 >= 0) loose = bits_at(x.row + j0);
+      if (t == 0 && id_now >= 0) target = bits_at(x.row + id_now);
       if (a.up) up = a.up[p];
       Sums<T, false> sums(c2);
       for (int g = 0; g < groups; ++g) {
@@ -1476,8 +1515,9 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
         }
         sums.template add_units<kGroup>(v);
       }
+      x0 = value_of(loose);
       sums.add_one(x0);
-      if (t == 0) sm.target = target;   // (it has come before any CTA may write on it)
+      if (t == 0) sm.target = value_of(target);   // (it has come before any CTA may write on it)
       int token = -1;
       if constexpr (LIST) {
         if (t < K) token = token_of(entry, a.r);
