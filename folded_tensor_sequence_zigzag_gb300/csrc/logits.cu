@@ -1462,7 +1462,6 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
   const int K = LIST ? a.t.K : 0;
   const uint32_t to = smem_u32(seg + t);
   int id = given(a.r, at.first, ask_given(a.r, at.first));
-  int2 asked = ask_given(a.r, at.first + at.stride);
   Asked e = {-1, 0};
   if constexpr (LIST) {
     if (t < K && at.first < a.r.S) e = ask_entry(a.t, pos_of(a.r, at.first), t);
@@ -1475,20 +1474,18 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
   for (int r = at.first; r < a.r.S; r += at.stride) {
     const int p = pos_of(a.r, r), id_now = id;
     if (!TSP_INB(p >= 0 && p < a.r.S, a.r.status)) return;
-    id = given(a.r, r + at.stride, asked);
-    asked = ask_given(a.r, r + at.stride < a.r.S ? r + 2 * at.stride : a.r.S);
+    const int2 asked = ask_given(a.r, r + at.stride);
     const RowPart<T, THREADS> x(a.r, r, at.rank, at.parts);
     T* out = reinterpret_cast<T*>(a.out) + (int64_t)r * a.ld_out;
     uint4* dst = reinterpret_cast<uint4*>(out + x.head) + x.u_lo + t;
     const int j0 = x.loose(t);
     const bool sent = there;
-    there = r + at.stride < a.r.S && id != -1;
-    RowPart<T, THREADS> next(a.r, there ? r + at.stride : r, at.rank, at.parts);
     Exchange* ex = nullptr;
     if constexpr (CLUSTER) ex = &sm.ex[live & 1];
     Stats st = {0.f, -INFINITY, 0.f};
     float x0 = -INFINITY, up = 1.f;
     bool teacher = false;
+    int token = -1;
     const Entry entry = entry_of(a.t, e);
     if (LIST && t < K && r + at.stride < a.r.S) e = ask_entry(a.t, pos_of(a.r, r + at.stride), t);
     if (id_now != -1) {
@@ -1518,7 +1515,6 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
       x0 = value_of(loose);
       sums.add_one(x0);
       if (t == 0) sm.target = value_of(target);   // (it has come before any CTA may write on it)
-      int token = -1;
       if constexpr (LIST) {
         if (t < K) token = token_of(entry, a.r);
         if (j0 >= 0) sm.list.loose[t] = x0;
@@ -1526,7 +1522,12 @@ __global__ void __launch_bounds__(THREADS, 768 / THREADS) one_pass_kernel(const 
       }
       st = statistics<T, false, CLUSTER, THREADS>(sums, seg, x.n, x0, c2, sm.part[live & 1], ex, live >> 1 & 1, at.rank,
                                                   at.parts, a.wait);
-      if constexpr (LIST) {
+    }
+    id = given(a.r, r + at.stride, asked);
+    there = r + at.stride < a.r.S && id != -1;
+    RowPart<T, THREADS> next(a.r, there ? r + at.stride : r, at.rank, at.parts);
+    if constexpr (LIST) {
+      if (id_now != -1) {
         // the listed logits of this part (every thread's units are there since the sums
         // were joined); in a cluster each goes to the first CTA from the one that has it
         if (t < K) {
