@@ -157,7 +157,7 @@ __device__ __forceinline__ int given(const Rows& a, int row, int2 asked) {
 template <typename T, int THREADS>
 struct RowPart {
   // bytes of a line; each element outside the units has a thread
-  static constexpr int kLine = THREADS >= 128 ? 128 : 64, kLoose = kLine / sizeof(T) - 1 + kElems<T> - 1;
+  static constexpr int kLine = THREADS >= 128 ? 128 : THREADS >= 64 ? 64 : 32, kLoose = kLine / sizeof(T) - 1 + kElems<T> - 1;
   static_assert(kLoose <= THREADS, "a thread for each element outside the units");
   const T* row;
   const uint4* src;
@@ -1730,8 +1730,25 @@ tsp_status launch_rows(const A& a, int S, int threads, int parts, size_t smem, i
   return TSP_OK;
 }
 
-// Threads of a CTA for parts of `per` units and lists of n.
-int threads_for(int64_t per, int n) { return per <= 3 * kGroup * 128 && n <= 128 ? 128 : kMostThreads; }
+// Threads of a CTA of the gradients' kernels for parts of `per` units and lists of n.  The
+// shorter a row, the more of its time is the CTA's meeting, which a single warp has not (a
+// list has more of these): 65536 x 2000 bf16, loss with gradient: 99 us with a warp a row,
+// 175 with four; 65536 x 4000: 162 with two, 171 with one, 187 with four, with 8 listed
+// tokens 200 and 267 with two and four.  Only where there are rows to fill the GPU.
+bool fills(int64_t S, int threads) { return S * threads >= (int64_t)768 * num_sms(); }
+int threads_for(int64_t S, int64_t per, int n) {
+  const int64_t row = n > 0 ? per / 2 : per;
+  if (row <= 2 * kGroup * 32 && n <= 32 && fills(S, 32)) return 32;
+  if (row <= 2 * kGroup * 64 && n <= 64 && fills(S, 64)) return 64;
+  return per <= 3 * kGroup * 128 && n <= 128 ? 128 : kMostThreads;
+}
+template <typename F>
+tsp_status with_threads(int threads, F launch) {
+  return threads == 32    ? launch(std::integral_constant<int, 32>())
+         : threads == 64  ? launch(std::integral_constant<int, 64>())
+         : threads == 128 ? launch(std::integral_constant<int, 128>())
+                          : launch(std::integral_constant<int, 256>());
+}
 // CTAs a row of the forward where there are few: parts of 16 KB at least, as the cluster's
 // meeting has a price (8 x 50257 fp32: 5.7 us with eight, 8.8 with one; 8 x 32000 bf16 with
 // 20 alternatives: 11.8 and 9.3).
@@ -1751,7 +1768,7 @@ int parts_for(int64_t S, int64_t units, int parts) {
 template <typename T>
 int64_t rows_a_cta(int64_t V, int parts) {
   const int64_t bytes = std::max<int64_t>(1, V * (int64_t)sizeof(T) / parts);
-  return std::max<int64_t>(1, 65536 / bytes);
+  return std::max<int64_t>(1, (65536 + bytes / 2) / bytes);
 }
 
 template <typename T, bool ENT, bool TOP, bool CLUSTER, int THREADS>
@@ -1763,9 +1780,13 @@ tsp_status launch_fwd_c(const FwdArgs& a, const char* name, cudaStream_t st) {
   return launch_rows<fwd_kernel<T, ENT, TOP, CLUSTER, THREADS>, CLUSTER, most>(
       a, a.r.S, THREADS, a.parts, smem, rows_a_cta<T>(a.r.V, a.parts) * (a.t.K > 128 ? 3 : 1), name, st);
 }
-// The fewer threads a CTA has, the less a row costs that is not its logits: 128, as many
-// as keep the pipelines full (8192 x 32000 bf16: 82 us, 101 with 256); 64 for rows of two
-// groups of these (65536 x 4000: 118, 193 with 128); 256 for long lists.
+// The fewer threads a CTA has, the less a row costs that is not its logits, and the more
+// rows are between their sums and their end at a time: 128, as many as keep the pipelines
+// full (8192 x 32000 bf16: 77 us, 101 with 256), 64 for rows up to 40 KB, a warp for those
+// up to 16 KB (65536 x 4000 bf16: 87 us, 110 with 64 and 193 with 128), where there are rows
+// to fill the GPU; 256 for long lists.  Alternatives are looked for from the threads' largest
+// logits, three threads for one at least: 16384 x 20000 bf16 with 10: 124 us with 64 threads,
+// 156 with 128.
 template <typename T>
 tsp_status launch_fwd_t(FwdArgs a, const char* name, cudaStream_t st) {
   const int64_t units = (int64_t)a.r.V * sizeof(T) / 16;
@@ -1773,15 +1794,21 @@ tsp_status launch_fwd_t(FwdArgs a, const char* name, cudaStream_t st) {
   const bool ent = a.entropy != nullptr;
   if (a.parts > 1) return launch_fwd_c<T, true, true, true, 256>(a, name, st);
   if (a.top > 64) return launch_fwd_c<T, true, true, false, 256>(a, name, st);
+  if (a.top > 0 && 3 * a.top <= 64 && units <= 16 * kGroup * 64 && fills(a.r.S, 64))
+    return ent ? launch_fwd_c<T, true, true, false, 64>(a, name, st)
+               : launch_fwd_c<T, false, true, false, 64>(a, name, st);
   if (a.top > 0)
     return ent ? launch_fwd_c<T, true, true, false, 128>(a, name, st)
                : launch_fwd_c<T, false, true, false, 128>(a, name, st);
   if (a.t.K > 128) return launch_fwd_c<T, false, false, false, 256>(a, name, st);
-  if (a.t.K > 64 || units > 2 * kGroup * 128)
-    return ent ? launch_fwd_c<T, true, false, false, 128>(a, name, st)
-               : launch_fwd_c<T, false, false, false, 128>(a, name, st);
-  return ent ? launch_fwd_c<T, true, false, false, 64>(a, name, st)
-             : launch_fwd_c<T, false, false, false, 64>(a, name, st);
+  if (units <= 8 * kGroup * 32 && a.t.K <= 32 && fills(a.r.S, 32))
+    return ent ? launch_fwd_c<T, true, false, false, 32>(a, name, st)
+               : launch_fwd_c<T, false, false, false, 32>(a, name, st);
+  if (units <= 10 * kGroup * 64 && a.t.K <= 64 && fills(a.r.S, 64))
+    return ent ? launch_fwd_c<T, true, false, false, 64>(a, name, st)
+               : launch_fwd_c<T, false, false, false, 64>(a, name, st);
+  return ent ? launch_fwd_c<T, true, false, false, 128>(a, name, st)
+             : launch_fwd_c<T, false, false, false, 128>(a, name, st);
 }
 tsp_status launch_fwd(const FwdArgs& a, int dtype, const char* name, cudaStream_t st) {
   return dtype == TSP_BF16 ? launch_fwd_t<__nv_bfloat16>(a, name, st) : launch_fwd_t<float>(a, name, st);
@@ -1805,11 +1832,13 @@ tsp_status launch_grad_t(GradArgs a, const char* name, cudaStream_t st) {
     return TSP_OK;
   }
   a.parts = parts_for(a.r.S, units, 1);
-  const int threads = threads_for((units + a.parts - 1) / a.parts, a.t.K);
+  const int threads = threads_for(a.r.S, (units + a.parts - 1) / a.parts, a.t.K);
   const int64_t rows = rows_a_cta<T>(a.r.V, a.parts);
-  if (threads == 128)
-    return launch_rows<grad_kernel<T, ENT, LIST, 128>, false, kRingMost>(a, a.r.S, 128, a.parts, ring_bytes(128), rows, name, st);
-  return launch_rows<grad_kernel<T, ENT, LIST, 256>, false, kRingMost>(a, a.r.S, 256, a.parts, ring_bytes(256), rows, name, st);
+  auto launch = [&](auto n) {
+    constexpr int THREADS = decltype(n)::value;
+    return launch_rows<grad_kernel<T, ENT, LIST, THREADS>, false, kRingMost>(a, a.r.S, THREADS, a.parts, ring_bytes(THREADS), rows, name, st);
+  };
+  return with_threads(threads, launch);
 }
 template <typename T>
 tsp_status launch_grad_d(const GradArgs& a, const char* name, cudaStream_t st) {
@@ -1841,14 +1870,19 @@ template <typename T, bool LIST, bool CLUSTER>
 tsp_status launch_one_pass_c(OnePassArgs o, cudaStream_t st) {
   const int parts = o.g.parts;
   const int64_t per = ((int64_t)o.g.r.V * sizeof(T) / 16 + parts - 1) / parts;
-  const int threads = threads_for(per, o.g.t.K);
+  const int threads = threads_for(CLUSTER ? 0 : o.g.r.S, per, o.g.t.K);
   // whole groups up to three CTAs' share of a multiprocessor (quicker: no case is apart)
   o.fill = per <= 16 * kMostThreads;
   const size_t smem = part_bytes(per, threads, o.fill ? kGroup : 1);
   const int64_t rows = CLUSTER ? 4 : rows_a_cta<T>(o.g.r.V, parts) * (LIST ? 2 : 1);
-  if (threads == 128)
-    return launch_rows<one_pass_kernel<T, LIST, CLUSTER, 128>, CLUSTER, kOnePassMost>(o, o.g.r.S, 128, parts, smem, rows, "token_loss_one_pass", st);
-  return launch_rows<one_pass_kernel<T, LIST, CLUSTER, 256>, CLUSTER, kOnePassMost>(o, o.g.r.S, 256, parts, smem, rows, "token_loss_one_pass", st);
+  auto launch = [&](auto n) {
+    constexpr int THREADS = decltype(n)::value;
+    return launch_rows<one_pass_kernel<T, LIST, CLUSTER, THREADS>, CLUSTER, kOnePassMost>(o, o.g.r.S, THREADS, parts, smem, rows, "token_loss_one_pass", st);
+  };
+  if constexpr (CLUSTER)   // (few rows, or long ones)
+    return threads == 128 ? launch(std::integral_constant<int, 128>()) : launch(std::integral_constant<int, 256>());
+  else
+    return with_threads(threads, launch);
 }
 
 template <typename T>
