@@ -1750,11 +1750,11 @@ tsp_status with_threads(int threads, F launch) {
                           : launch(std::integral_constant<int, 256>());
 }
 // CTAs a row of the forward where there are few: parts of 16 KB at least, as the cluster's
-// meeting has a price (8 x 50257 fp32: 5.7 us with eight, 8.8 with one; 8 x 32000 bf16 with
-// 20 alternatives: 11.8 and 9.3).
+// meeting has a price (8 x 50257 fp32: 5.7 us with eight, 8.8 with one; 70 x 100000 fp32: 9.9
+// with two, 12.9 with one; 8 x 32000 bf16 with 20 alternatives: 11.8 and 9.3).
 int fwd_parts(int64_t S, int64_t units) {
   int parts = 1;
-  while (units >= 8192 && parts <= 4 && S * parts * 4 <= num_sms() && units / (2 * parts) >= 1024) parts *= 2;
+  while (units >= 8192 && parts <= 4 && S * parts * 2 <= num_sms() && units / (2 * parts) >= 1024) parts *= 2;
   return parts;
 }
 // CTAs a row where there are few rows: until the GPU is full, of 4 KB at least.
@@ -1782,7 +1782,8 @@ tsp_status launch_fwd_c(const FwdArgs& a, const char* name, cudaStream_t st) {
 }
 // The fewer threads a CTA has, the less a row costs that is not its logits, and the more
 // rows are between their sums and their end at a time: 128, as many as keep the pipelines
-// full (8192 x 32000 bf16: 77 us, 101 with 256), 64 for rows up to 40 KB, a warp for those
+// full (8192 x 32000 bf16: 77 us, 101 with 256), 64 for rows up to 40 KB or where the rows
+// are a few more than the GPU holds of 128 (1072 x 116416: 41 us, 48), a warp for those
 // up to 16 KB (65536 x 4000 bf16: 87 us, 110 with 64 and 193 with 128), where there are rows
 // to fill the GPU; 256 for long lists.  Alternatives are looked for from the threads' largest
 // logits, three threads for one at least: 16384 x 20000 bf16 with 10: 124 us with 64 threads,
@@ -1804,7 +1805,7 @@ tsp_status launch_fwd_t(FwdArgs a, const char* name, cudaStream_t st) {
   if (units <= 8 * kGroup * 32 && a.t.K <= 32 && fills(a.r.S, 32))
     return ent ? launch_fwd_c<T, true, false, false, 32>(a, name, st)
                : launch_fwd_c<T, false, false, false, 32>(a, name, st);
-  if (units <= 10 * kGroup * 64 && a.t.K <= 64 && fills(a.r.S, 64))
+  if (a.t.K <= 64 && (units <= 10 * kGroup * 64 ? fills(a.r.S, 64) : a.r.S > 6 * num_sms() && a.r.S <= 8 * num_sms()))
     return ent ? launch_fwd_c<T, true, false, false, 64>(a, name, st)
                : launch_fwd_c<T, false, false, false, 64>(a, name, st);
   return ent ? launch_fwd_c<T, true, false, false, 128>(a, name, st)

@@ -1013,7 +1013,7 @@ def _rows_like(logits):
     ld = V + (max(logits.stride(0), V) - V) % line if S > 1 else V
     if ld == V and at == 0:
         return empty((S, V), logits.dtype, logits.device)
-    return empty((at + S * ld,), logits.dtype, logits.device)[at:].view(S, ld)[:, :V]
+    return empty((at + S * ld,), logits.dtype, logits.device).as_strided((S, V), (ld, 1), at)
 
 
 def logprobs_fwd(logits, ids=None, D: int = 1, scale: float = 1.0, top: int = 0,
