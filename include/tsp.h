@@ -702,10 +702,14 @@ tsp_status tsp_adamw_step(const tsp_adamw_tensor* tensors, int32_t count,
  * tsp_token_loss_bwd: the same gradient, later, from stats:
  *   dloss scale ((w_ce + weight) p_j - w_ce delta_jt - weight q_j).
  * dlogits may be logits (the same address and row distance); otherwise no
- * output may overlap another argument.  All sums and statistics are in fp32, in
- * a fixed order: equal calls give equal bits.  No workspace.
+ * output may overlap another argument.  Gradients are quickest where they lie as
+ * the logits do: addresses and row distances that differ by multiples of 16
+ * bytes.  All sums and statistics are in fp32, in a fixed order: equal calls on
+ * memory of equal alignment (to 128 bytes) give equal bits.  No workspace.
+ * A teacher of weight 0 is not looked at, nor are its tokens.
  * Errors: TSP_ERR_INVALID_ARG; TSP_ERR_UNSUPPORTED for S or V > 2^30 or
- * ld > 2^32. */
+ * ld > 2^32; where CTAs share a row their waits for one another are bounded
+ * (TSP_ERR_TIMEOUT in the device status word). */
 #define TSP_TOP_MAX 256
 typedef struct {
   const void* logits;
