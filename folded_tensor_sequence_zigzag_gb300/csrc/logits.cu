@@ -583,7 +583,7 @@ __device__ __forceinline__ float divergence(const float4* listed, int K, float s
 __device__ __forceinline__ float warps_sum(float v, int K, float* part) {
   if (K <= 32) return v;
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  asm volatile("bar.sync 1, %0;" ::"r"((K + 31) / 32 * 32) : "memory");
+  asm volatile("barrier.sync 1, %0;" ::"r"((K + 31) / 32 * 32) : "memory");
   v = 0.f;
   for (int k = 0; 32 * k < K; ++k) v += part[k];
   return v;
@@ -734,7 +734,7 @@ __device__ __forceinline__ void start_exchange(Exchange* ex) {
 
 // No CTA ends while another one, whose wait may have run out, can still write to it.
 __device__ __forceinline__ void leave_cluster() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.relaxed;\n\tbarrier.cluster.wait;" ::: "memory");
 }
 
 // The row's CTAs: of a cluster, or those that share rows without speaking to each other.
