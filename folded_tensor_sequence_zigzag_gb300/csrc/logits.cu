@@ -840,7 +840,8 @@ constexpr uint32_t kOrderNone = 0x007fffffu;   // order_of(-inf)
 constexpr int kSlots = 32, kListed = 128;
 template <int THREADS> struct TopSmem {
   static constexpr int kCandidates = 4 * THREADS;
-  uint64_t key[kCandidates], above;
+  alignas(16) uint64_t key[kCandidates];
+  uint64_t above;
   alignas(16) uint16_t best[THREADS];   // largest logit of each thread, the upper half of its order
   uint16_t listed[THREADS / 32][kListed];   // of each warp: slots to be looked at once more
   int n;
@@ -889,8 +890,12 @@ __device__ __forceinline__ void for_ranked(const uint64_t* key, int n, F put) {
   for (int k = t >> log_g; k - ((t & 31) >> log_g) < n; k += THREADS >> log_g) {   // (whole warps)
     const uint64_t mine = k < n ? key[k] : 0;
     int rank = 0;
-#pragma unroll 8
-    for (int q = t & (g - 1); q < n; q += g) rank += key[q] > mine;
+#pragma unroll 4
+    for (int q = 2 * (t & (g - 1)); q + 1 < n; q += 2 * g) {
+      const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(key + q);
+      rank += (o.x > mine) + (o.y > mine);
+    }
+    if ((n & 1) && (t & (g - 1)) == 0) rank += key[n - 1] > mine;
     for (int o = 1; o < g; o *= 2) rank += __shfl_xor_sync(0xffffffffu, rank, o);
     if (k < n && (t & (g - 1)) == 0) put(rank, mine);
   }
@@ -1788,15 +1793,16 @@ tsp_status launch_fwd_c(const FwdArgs& a, const char* name, cudaStream_t st) {
 // are a few more than the GPU holds of 128 (1072 x 116416: 41 us, 48), a warp for those
 // up to 16 KB (65536 x 4000 bf16: 87 us, 110 with 64 and 193 with 128), where there are rows
 // to fill the GPU; 256 for long lists.  Alternatives are looked for from the threads' largest
-// logits, three threads for one at least: 16384 x 20000 bf16 with 10: 124 us with 64 threads,
-// 156 with 128.
+// logits, so 64 threads serve up to 21 (16384 x 20000 bf16 with 10: 124 us, 156 with 128), 128
+// up to 85, of fp32 64 (80 of 8192 x 32000 bf16: 141 us, 181 with 256; of 4096 x 50257 fp32:
+// 181 and 163).
 template <typename T>
 tsp_status launch_fwd_t(FwdArgs a, const char* name, cudaStream_t st) {
   const int64_t units = (int64_t)a.r.V * sizeof(T) / 16;
   a.parts = fwd_parts(a.r.S, units);
   const bool ent = a.entropy != nullptr;
   if (a.parts > 1) return launch_fwd_c<T, true, true, true, 256>(a, name, st);
-  if (a.top > 64) return launch_fwd_c<T, true, true, false, 256>(a, name, st);
+  if (a.top > (sizeof(T) == 2 ? 85 : 64)) return launch_fwd_c<T, true, true, false, 256>(a, name, st);
   if (a.top > 0 && 3 * a.top <= 64 && units <= 16 * kGroup * 64 && fills(a.r.S, 64))
     return ent ? launch_fwd_c<T, true, true, false, 64>(a, name, st)
                : launch_fwd_c<T, false, true, false, 64>(a, name, st);

@@ -659,3 +659,48 @@ def test_last_positions_of_a_batch(dt):
     near(tsp.token_loss_bwd(x, got["stats"], ids), r.p + adds, gtol, "gradient")
     one = tsp.token_loss_fwd(x[:1], ids[:1], grad=True)
     assert one["dlogits"].is_contiguous()
+
+
+# as many rows as there are CTAs of one or two warps on the GPU, which take short rows then
+MANY = [(3700, 1, 1, 0, 0), (4000, 9, 4, 0, 3), (3800, 257, 1, 5, 1), (4096, 1000, 8, 0, 0), (3700, 2047, 1, 1, 7), (1900, 5003, 1, 0, 0), (1840, 8192, 2, 8, 0)]
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("S,V,D,wide,at", MANY)
+def test_many_short_rows(S, V, D, wide, at, dt):
+    test_logprobs_fwd(S, V, D, wide, at, dt)
+    test_logprobs_bwd(S, V, D, wide, at, "both" if S % 3 else "logp", dt)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("K,w_ce,w_kd", [(0, 1.0, 0.0), (3, 0.3, 0.7), (32, 0.0, 2.0), (33, 0.5, 1.0), (64, 0.5, -0.25), (65, 1.0, 1.0)])
+@pytest.mark.parametrize("S,V,D,wide,at", [s for s in MANY if s[1] in (1, 9, 257, 1000, 5003)])
+def test_losses_of_many_short_rows(S, V, D, wide, at, K, w_ce, w_kd, dt):
+    test_token_loss(S, V, D, wide, at, K, w_ce, w_kd, dt)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("V,top", [(9, 3), (700, 1), (1003, 21), (1000, 22), (2500, 5), (2501, 64), (5003, 85), (5003, 86)])
+def test_many_special_rows(V, top, dt):
+    named = special(V, dt)
+    one = torch.stack(list(named.values()))
+    n = one.shape[0]
+    R = -(-3700 // n)
+    x = one.cuda().repeat(R, 1)
+    ids = torch.full((n * R,), V - 1, device="cuda")
+    r = Ref(one)
+    dead = (r.x == -INF).all(1)
+    none = lambda v, to: torch.where(dead, torch.tensor(to, dtype=torch.float64), v).repeat(R)
+    got = tsp.logprobs_fwd(x, ids, top=top, entropy=True, stats=True)
+    near(got["stats"][:, 0], none(r.m[:, 0], 0.0), torch.tensor(0.0), "m")
+    near(got["stats"][:, 1], none(r.l[:, 0], -INF), (r.dl.nan_to_num(0.0) + 2 * U * r.l[:, 0].abs().nan_to_num(0.0)).repeat(R), "l")
+    near(got["logp"], none(r.logp[:, V - 1], -INF), r.d_logp[:, V - 1].nan_to_num(0.0, posinf=0.0).repeat(R), "logp")
+    near(got["entropy"], none(r.entropy, 0.0), r.d_entropy.nan_to_num(0.0).repeat(R), "entropy")
+    r.logp[dead] = -INF
+    i, logp, tol = r.order(top)
+    off = (got["top_ids"].cpu().long().view(R, n, top) != i).any(2).any(0)
+    assert not off.any(), [name for name, o in zip(named, off) if o]
+    near(got["top_logp"], logp.repeat(R, 1), tol.nan_to_num(0.0, posinf=0.0).repeat(R, 1), "top_logp")
+    loss = tsp.token_loss_fwd(x, ids, grad=True)
+    near(loss["loss"], none(-r.logp[:, V - 1], INF), r.d_logp[:, V - 1].nan_to_num(0.0, posinf=0.0).repeat(R) * 1.01, "loss")
+    assert loss["dlogits"].isfinite().all() and not loss["dlogits"].view(R, n, V)[:, dead.cuda()].any()
