@@ -5,11 +5,14 @@ Tolerances.  U = 2^-24 is half an fp32 step, E2 = 2^-22 the stated error of the
 hardware's 2^x.  With u_j = scale (x_j - m) and l = log sum exp(u_j):
   * a summand exp(u_j) is off by E2 and 4 U |u_j|, the few renewals of a running
     reference add as much each (8 E2 in all), and a thread's sum, the warps' and the
-    CTAs' add V / 1024 + 64 roundings; so l is off by
+    CTAs' add V / 1024 + 64 roundings (a thread has two sums of n <= V / 64 terms each, up
+    to 128 in one warp and 500 in four; roundings have either sign and are the smaller the
+    smaller the sum still is: five standard deviations, 5 U sqrt(n / 9), are 37 U at most,
+    before the warps' ten and the CTAs'); so l is off by
       dl = 8 E2 + (V / 1024 + 64) U + 8 U (E|u| + 8),     E|u| = sum_j p_j |u_j|;
   * log p_j by dl + 4 U (|u_j| + |l|);
   * the entropy, l + sum p |u|, by (1 + E|u| + 8) times that without the last term;
-  * p_j in a gradient relatively by E2 + 8 U (|u_j| + |l| + 2); rounding to bf16 adds 2^-9
+  * p_j in a gradient relatively by E2 + 8 U (|u_j| + |l| + 2); rounding to bf16 adds 2^-8
     of the value, a step of the smallest bf16 numbers 2^-126 (flushed results).
 """
 import math
