@@ -1007,12 +1007,14 @@ def _logits_arg(logits, ids, D, scale):
 def _rows_like(logits):
     """A gradient's memory: its rows lie on 128-byte lines as the logits' do, which is
     how the kernels read and write them at once."""
+    if logits.data_ptr() % 128 == 0 and logits.is_contiguous():
+        return empty(logits.shape, logits.dtype, logits.device)
     S, V = logits.shape
     line = 128 // logits.element_size()
     at = logits.data_ptr() % 128 // logits.element_size()
     ld = V + (max(logits.stride(0), V) - V) % line if S > 1 else V
-    if ld == V and at == 0:
-        return empty((S, V), logits.dtype, logits.device)
+    if at == 0 and not POISON:
+        return torch.empty_strided((S, V), (ld, 1), dtype=logits.dtype, device=logits.device)
     return empty((at + S * ld,), logits.dtype, logits.device).as_strided((S, V), (ld, 1), at)
 
 
